@@ -121,6 +121,7 @@ typedef enum {
 #define WC_EF_BAD_SEEK 16u       /* seek entries out of order, misaligned or past payload_bytes */
 #define WC_EF_CAPACITY 32u       /* encode: the payload did not fit payload_bytes */
 #define WC_EF_BAD_CRC 64u        /* decode with WC_OPT_CRC32: a chunk's payload does not match crc[k] */
+#define WC_EF_BAD_INDEX 128u     /* a token or adapter number out of range (the operators beside the weights) */
 
 #define WC_CHUNK 65536u
 
@@ -341,6 +342,75 @@ wc_status wc_encode_noalloc(wc_format format, const void *d_in, uint64_t n, cons
 /* The most chunks wc_encode_noalloc takes under `format` (0 for a bad
  * format word).  Pure host function. */
 uint64_t wc_noalloc_max_chunks(wc_format format);
+
+/* ---------------------------------------------------------------------
+ * Operators beside the weights: what a model's step computes next to the
+ * products with its (compressed) weights.  The conventions above hold for
+ * them too: device pointers owned by the caller, nothing allocated, nothing
+ * synchronised, enqueued on `stream`.  Sums, softmax statistics and
+ * intermediate products are held in 32 bits. */
+
+/* Element types of activations, logits and uncompressed weights. */
+#define WC_T_BF16 0u
+#define WC_T_FP16 1u
+#define WC_T_FP32 2u
+
+/* Log probabilities of given tokens.  Row r of `logits` (m rows of vocab
+ * elements of `type`, `stride` elements apart, at any element's alignment)
+ * gives lse = log sum_j exp z_j, logprob = z_t - lse for t = tokens[r],
+ * entropy = -sum_j p_j log p_j, and its `top` largest logits: their log
+ * probabilities and indices, largest first, equal logits (-0 = 0) by index,
+ * NaN after everything else.  Token -1: logprob 0; another token outside
+ * [0, vocab): logprob NaN and WC_EF_BAD_INDEX.  -inf is a logit whose
+ * probability is 0; a row of nothing but -inf has lse -inf, log
+ * probabilities -inf and entropy 0.  NaN or +inf anywhere in a row makes its
+ * statistics and log probabilities NaN. */
+typedef struct {
+    const void *logits;
+    uint64_t stride;
+    const int64_t *tokens;   /* m */
+    uint64_t m;
+    uint32_t vocab;          /* 1 .. 2^22 */
+    uint32_t top;            /* 0 .. 64, at most vocab */
+    uint32_t type;           /* WC_T_* */
+    uint32_t reserved;
+    float *logprob;          /* m each */
+    float *entropy;
+    float *lse;
+    float *top_logprobs;     /* m x top, if top > 0 */
+    int64_t *top_ids;        /* m x top, if top > 0 */
+} wc_logprobs;
+
+/* Bytes of scratch that wc_token_logprobs needs (0 for sizes that it
+ * rejects).  Pure host function. */
+uint64_t wc_token_logprobs_scratch(uint64_t m, uint32_t vocab, uint32_t top);
+
+/* d_scratch: 16-byte aligned; its contents need no preparation. */
+wc_status wc_token_logprobs(const wc_logprobs *a, void *d_scratch, uint64_t scratch_bytes, uint32_t *d_err,
+                            hipStream_t stream);
+
+/* The gradient of the logits from the gradients of logprob and entropy:
+ * out_j = grad_logprob [j = t] - p_j (grad_logprob + grad_entropy
+ * (log p_j + entropy)) with p_j = exp(z_j - lse), rounded once to `type`.
+ * Either gradient may be NULL (zero).  Rows whose token is -1 or out of
+ * range have no part of grad_logprob; rows with lse -inf have a zero
+ * gradient.  `out` may be `logits` itself (with the same stride). */
+typedef struct {
+    const void *logits;
+    uint64_t stride;
+    void *out;
+    uint64_t out_stride;
+    const int64_t *tokens;      /* m each */
+    const float *lse;
+    const float *entropy;       /* may be NULL without grad_entropy */
+    const float *grad_logprob;  /* may be NULL */
+    const float *grad_entropy;  /* may be NULL */
+    uint64_t m;
+    uint32_t vocab;
+    uint32_t type;
+} wc_logprobs_grad;
+
+wc_status wc_token_logprobs_backward(const wc_logprobs_grad *a, uint32_t *d_err, hipStream_t stream);
 
 #ifdef __cplusplus
 }

@@ -29,9 +29,13 @@ EF_BAD_TAIL = 8
 EF_BAD_SEEK = 16
 EF_CAPACITY = 32
 EF_BAD_CRC = 64
+EF_BAD_INDEX = 128
 EF_NAMES = {EF_BAD_TABLE: "bad table", EF_WORD_OVERRUN: "word overrun",
             EF_BAD_FINAL_STATE: "bad final state", EF_BAD_TAIL: "bad tail",
-            EF_BAD_SEEK: "bad seek", EF_CAPACITY: "payload capacity", EF_BAD_CRC: "CRC mismatch"}
+            EF_BAD_SEEK: "bad seek", EF_CAPACITY: "payload capacity", EF_BAD_CRC: "CRC mismatch",
+            EF_BAD_INDEX: "index out of range"}
+
+WC_T_BF16, WC_T_FP16, WC_T_FP32 = 0, 1, 2  # element types of the operators beside the weights
 
 CHUNK = 65536
 WC_NOALLOC_SCRATCH_BYTES = 128 << 20  # the fixed device array of wc_encode_noalloc
@@ -39,7 +43,8 @@ WC_NOALLOC_SCRATCH_BYTES = 128 << 20  # the fixed device array of wc_encode_noal
 EXPORTS = ["wc_version", "wc_status_string", "wc_query_layout", "wc_plan_batch", "wc_encode",
            "wc_decode", "wc_encode_batch", "wc_decode_batch", "wc_check_division", "wc_tile_order",
            "wc_decode_gemm_batch", "wc_decode_variant", "wc_encode_noalloc", "wc_noalloc_max_chunks",
-           "wc_set_encoder_words", "wc_encode_variant"]
+           "wc_set_encoder_words", "wc_encode_variant", "wc_token_logprobs_scratch", "wc_token_logprobs",
+           "wc_token_logprobs_backward"]
 # encoder word-store forms (wc_set_encoder_words)
 ENC_WORDS_AUTO, ENC_WORDS_DIRECT, ENC_WORDS_STAGED = 0, 1, 2
 
@@ -71,6 +76,21 @@ class wc_segment(ctypes.Structure):
 class wc_gemm(ctypes.Structure):
     _fields_ = [("x", ctypes.c_uint64), ("y", ctypes.c_uint64), ("rows", ctypes.c_uint32),
                 ("cols", ctypes.c_uint32)]
+
+
+class wc_logprobs(ctypes.Structure):
+    _fields_ = [("logits", ctypes.c_void_p), ("stride", ctypes.c_uint64), ("tokens", ctypes.c_void_p),
+                ("m", ctypes.c_uint64), ("vocab", ctypes.c_uint32), ("top", ctypes.c_uint32),
+                ("type", ctypes.c_uint32), ("reserved", ctypes.c_uint32), ("logprob", ctypes.c_void_p),
+                ("entropy", ctypes.c_void_p), ("lse", ctypes.c_void_p), ("top_logprobs", ctypes.c_void_p),
+                ("top_ids", ctypes.c_void_p)]
+
+
+class wc_logprobs_grad(ctypes.Structure):
+    _fields_ = [("logits", ctypes.c_void_p), ("stride", ctypes.c_uint64), ("out", ctypes.c_void_p),
+                ("out_stride", ctypes.c_uint64), ("tokens", ctypes.c_void_p), ("lse", ctypes.c_void_p),
+                ("entropy", ctypes.c_void_p), ("grad_logprob", ctypes.c_void_p), ("grad_entropy", ctypes.c_void_p),
+                ("m", ctypes.c_uint64), ("vocab", ctypes.c_uint32), ("type", ctypes.c_uint32)]
 
 
 _lib = None
@@ -106,9 +126,13 @@ def lib() -> ctypes.CDLL:
     L.wc_encode_variant.argtypes = [I, U64, P, ctypes.POINTER(I)]
     L.wc_noalloc_max_chunks.argtypes = [I]
     L.wc_noalloc_max_chunks.restype = U64
+    L.wc_token_logprobs_scratch.argtypes = [U64, U32, U32]
+    L.wc_token_logprobs_scratch.restype = U64
+    L.wc_token_logprobs.argtypes = [ctypes.POINTER(wc_logprobs), P, U64, P, P]
+    L.wc_token_logprobs_backward.argtypes = [ctypes.POINTER(wc_logprobs_grad), P, P]
     for name in ("wc_query_layout", "wc_plan_batch", "wc_encode", "wc_decode", "wc_encode_batch",
                  "wc_decode_batch", "wc_tile_order", "wc_decode_gemm_batch", "wc_decode_variant",
-                 "wc_encode_noalloc", "wc_encode_variant"):
+                 "wc_encode_noalloc", "wc_encode_variant", "wc_token_logprobs", "wc_token_logprobs_backward"):
         getattr(L, name).restype = I
     _lib = L
     return L
@@ -263,6 +287,19 @@ def wc_encode_variant(dtype, num_chunks: int, stream=None) -> bool:
     rc = lib().wc_encode_variant(_code(dtype), int(num_chunks), _stream(stream), ctypes.byref(a))
     _check(rc, "wc_encode_variant")
     return bool(a.value)
+
+
+def wc_token_logprobs_scratch(m: int, vocab: int, top: int) -> int:
+    return lib().wc_token_logprobs_scratch(m, vocab, top)
+
+
+def wc_token_logprobs(args: wc_logprobs, d_scratch, scratch_bytes: int, d_err=None, stream=None):
+    rc = lib().wc_token_logprobs(args, _ptr(d_scratch), scratch_bytes, _ptr(d_err), _stream(stream))
+    _check(rc, "wc_token_logprobs")
+
+
+def wc_token_logprobs_backward(args: wc_logprobs_grad, d_err=None, stream=None):
+    _check(lib().wc_token_logprobs_backward(args, _ptr(d_err), _stream(stream)), "wc_token_logprobs_backward")
 
 
 def wc_check_division(samples_per_divisor: int = 256) -> int:

@@ -11,7 +11,8 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libwc.so")
-SOURCES = [os.path.join(CSRC, "wc_lib.hip"), os.path.join(CSRC, "wc_noalloc.hip")]
+SOURCES = [os.path.join(CSRC, "wc_lib.hip"), os.path.join(CSRC, "wc_noalloc.hip"),
+           os.path.join(CSRC, "ops", "wc_ops.hip")]
 
 ARCH = "gfx950"
 
@@ -35,6 +36,7 @@ def flags() -> list:
         "-Wall",
         f"-I{INCLUDE}",
         f"-I{CSRC}",
+        f"-I{os.path.join(CSRC, 'ops')}",
     ]
 
 

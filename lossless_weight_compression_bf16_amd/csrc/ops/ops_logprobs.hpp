@@ -1,0 +1,560 @@
+// ops_logprobs.hpp -- log probabilities of given tokens, with the entropy and
+// the most likely alternatives of every row, and their gradient.
+//
+//   lse = log sum_j exp z_j,  logprob = z_t - lse,  p_j = exp(z_j - lse)
+//   H = -sum_j p_j log p_j = lse - sum_j p_j z_j
+//   d logprob / d z_j = [j = t] - p_j,   d H / d z_j = -p_j (log p_j + H)
+//
+// One pass over the logits.  Every thread keeps the largest logit m it has
+// seen, S = sum 2^d and W = sum 2^d d with d = (z - m) log2 e, and corrects S
+// and W when a batch of 32 logits raises m:
+//   S' = c S,  W' = c (W + delta S),  delta = (m - m') log2 e,  c = 2^delta.
+// With the row's M, S, W: lse = M + ln S, H = ln S - ln 2 W / S.
+//
+// The alternatives need no sort of the row.  Let T be the n-th largest of
+// the 256 threads' maxima: at least n logits are >= T, so every logit among
+// the n largest is >= T.  The largest logit of every batch is kept in LDS, so
+// the logits >= T are found by looking again at the batches whose maximum is
+// >= T only (about n of V / 32), and ranked by counting.  Rows with so many
+// equal logits that the lists overflow take the scan of top_slow.
+//
+// Order of the alternatives: larger logits first, equal ones (-0 = 0) by
+// their index, NaN after everything else.
+#pragma once
+
+#include "ops_common.hpp"
+
+namespace wc {
+namespace ops {
+
+constexpr uint32_t kRowThreads = 256;
+constexpr uint32_t kBatch = 32;                          // logits a thread takes per round
+constexpr uint32_t kSweep = kRowThreads * kBatch;        // logits of a round of the block
+constexpr uint32_t kMaxSlice = 131072;                   // logits of one block
+constexpr uint32_t kMaxSlices = 64;                      // blocks of one row
+constexpr uint32_t kMinSlice = 2048;
+constexpr uint32_t kMaxTop = 64;
+constexpr uint32_t kMaxVocab = kMaxSlice * kMaxSlices / 2;
+constexpr uint32_t kListCap = 1024;                      // candidates ranked by counting
+constexpr float kFloor = -1e30f;                         // a thread's maximum before its first logit
+
+// Whole numbers in the order of the alternatives: 0 for no logit, 1 for NaN.
+__device__ __forceinline__ uint32_t key_of(float f)
+{
+    if (f != f) return 1u;
+    const uint32_t b = __builtin_bit_cast(uint32_t, f + 0.0f);  // -0 + 0 = 0
+    return (b & 0x80000000u) ? ~b : b | 0x80000000u;
+}
+__device__ __forceinline__ float key_value(uint32_t k)
+{
+    if (k <= 1u) return nan32();
+    return __builtin_bit_cast(float, (k & 0x80000000u) ? k & 0x7FFFFFFFu : ~k);
+}
+
+// Softmax statistics in base 2: see the file's comment.
+struct Stat {
+    float m, s, w;
+};
+__device__ __forceinline__ void raise(Stat &a, float m)  // m >= a.m
+{
+    const float delta = fmaxf((a.m - m) * kLog2e, kFloor);  // finite, so that a zero S stays zero
+    const float c = exp2_fast(delta);
+    a.w = c * (a.w + delta * a.s);
+    a.s = c * a.s;
+    a.m = m;
+}
+__device__ __forceinline__ Stat merge(Stat a, Stat b)
+{
+    const float m = fmaxf(a.m, b.m);
+    raise(a, m);
+    raise(b, m);
+    return Stat{m, a.s + b.s, a.w + b.w};
+}
+
+template <bool kTop, bool kSlice>
+struct RowShared {
+    uint64_t list[kTop ? kListCap : 1];                               // candidates: key << 32 | ~index
+    uint32_t batch_max[kTop && kSlice ? kMaxSlice / kBatch : 1];      // bits of the largest logit of batch 256 i + thread
+    uint32_t hits[kTop && kSlice ? kListCap : 1];                     // batches to look at again
+    uint32_t keys[kTop && kSlice ? kRowThreads : 4];
+    float part[3 * (kRowThreads / 64)];
+    uint64_t thresh64;
+    uint32_t thresh, n_list, n_hits, wave_count[kRowThreads / 64];
+};
+
+__device__ __forceinline__ uint64_t entry(uint32_t key, uint32_t index) { return ((uint64_t)key << 32) | (uint32_t)~index; }
+
+// The block's statistics, in every thread.
+template <class Sh>
+__device__ inline Stat block_stat(Stat a, Sh &sh)
+{
+    for (int o = 32; o; o >>= 1) {
+        const Stat b{__shfl_xor(a.m, o, 64), __shfl_xor(a.s, o, 64), __shfl_xor(a.w, o, 64)};
+        a = merge(a, b);
+    }
+    const uint32_t wave = threadIdx.x >> 6;
+    if ((threadIdx.x & 63) == 0) {
+        sh.part[3 * wave] = a.m;
+        sh.part[3 * wave + 1] = a.s;
+        sh.part[3 * wave + 2] = a.w;
+    }
+    __syncthreads();
+    a = Stat{sh.part[0], sh.part[1], sh.part[2]};
+    for (uint32_t i = 1; i < kRowThreads / 64; i++)
+        a = merge(a, Stat{sh.part[3 * i], sh.part[3 * i + 1], sh.part[3 * i + 2]});
+    return a;
+}
+
+// The n-th largest of the keys that every thread gives one of (the smallest
+// if fewer than n are not 0), in every thread.
+template <class Sh>
+__device__ inline uint32_t nth_key(uint32_t key, uint32_t n, Sh &sh)
+{
+    sh.keys[threadIdx.x] = key;
+    if (threadIdx.x == 0) sh.thresh = ~0u;
+    __syncthreads();
+    uint32_t above = 0;
+    for (uint32_t i = 0; i < kRowThreads; i += 4) {
+        const u32x4 k = *reinterpret_cast<const u32x4 *>(&sh.keys[i]);
+        above += (k[0] > key) + (k[1] > key) + (k[2] > key) + (k[3] > key);
+    }
+    if (above < n) atomicMin(&sh.thresh, key);
+    __syncthreads();
+    return lds_uniform(sh.thresh);
+}
+
+// Writes the n largest entries of the list, in order; fewer entries than n
+// leave zeros.
+template <class Sh, class Put>
+__device__ inline void rank_list(uint32_t count, uint32_t n, const Sh &sh, Put put)
+{
+    for (uint32_t i = threadIdx.x; i < count; i += kRowThreads) {
+        const uint64_t mine = sh.list[i];
+        uint32_t above = 0;
+        for (uint32_t j = 0; j < count; j++) above += sh.list[j] > mine;
+        if (above < n) put(above, mine);
+    }
+    for (uint32_t i = count + threadIdx.x; i < n; i += kRowThreads) put(i, 0ull);
+}
+
+// Adds to the list, in the order of the index, the first elements of
+// [lo, hi) whose key is `key` until it holds n entries; the new count.
+template <int T, class Sh>
+__device__ inline uint32_t fill_equal(const typename Type<T>::elem *row, uint32_t lo, uint32_t hi, uint32_t n,
+                                      uint32_t count, uint32_t key, Sh &sh)
+{
+    const uint32_t wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+    for (uint32_t j0 = lo; count < n && j0 < hi; j0 += kRowThreads) {
+        const uint32_t j = j0 + threadIdx.x;
+        const bool eq = j < hi && key_of(Type<T>::to_f32(row[j])) == key;
+        const uint64_t votes = __ballot(eq);
+        if (lane == 0) sh.wave_count[wave] = (uint32_t)__popcll(votes);
+        __syncthreads();
+        uint32_t at = count + (uint32_t)__popcll(votes & ((1ull << lane) - 1)), total = 0;
+        for (uint32_t i = 0; i < kRowThreads / 64; i++) {
+            if (i < wave) at += sh.wave_count[i];
+            total += sh.wave_count[i];
+        }
+        if (eq && at < n) sh.list[at] = entry(key, j);
+        count = min(count + total, n);
+        __syncthreads();
+    }
+    return count;
+}
+
+// The candidates where more elements than the list holds are above `thresh`,
+// a key that at least n elements reach: the n-th largest of those in the
+// list is a higher key that n elements reach, and the scan starts again from
+// there.  The key grows every time, so this ends; it takes rows in which few
+// threads hold more than a thousand of the largest logits.
+template <int T, class Sh>
+__device__ __noinline__ uint32_t top_slow(const typename Type<T>::elem *row, uint32_t lo, uint32_t hi, uint32_t n,
+                                          uint32_t thresh, Sh &sh)
+{
+    for (;;) {
+        __syncthreads();
+        if (threadIdx.x == 0) {
+            sh.n_list = 0;
+            sh.thresh = ~0u;
+        }
+        __syncthreads();
+        for (uint32_t j = lo + threadIdx.x; j < hi; j += kRowThreads) {
+            const uint32_t key = key_of(Type<T>::to_f32(row[j]));
+            if (key > thresh) {
+                const uint32_t at = atomicAdd(&sh.n_list, 1u);
+                if (at < kListCap) sh.list[at] = entry(key, j);
+            }
+        }
+        __syncthreads();
+        const uint32_t count = lds_uniform(sh.n_list);
+        if (count <= kListCap) return fill_equal<T>(row, lo, hi, n, count, thresh, sh);
+        for (uint32_t i = threadIdx.x; i < kListCap; i += kRowThreads) {
+            const uint32_t key = (uint32_t)(sh.list[i] >> 32);
+            uint32_t above = 0;
+            for (uint32_t j = 0; j < kListCap; j++) above += (uint32_t)(sh.list[j] >> 32) > key;
+            if (above < n) atomicMin(&sh.thresh, key);
+        }
+        __syncthreads();
+        thresh = lds_uniform(sh.thresh);
+    }
+}
+
+// Collects the elements of [lo, hi) whose key is at least `limit` from the
+// batches that have one.  False if they are too many for the lists.
+template <int T, class Sh>
+__device__ inline bool collect(const typename Type<T>::elem *row, uint32_t lo, uint32_t hi, uint32_t rounds,
+                               uint32_t limit, Sh &sh)
+{
+    using Ty = Type<T>;
+    constexpr uint32_t kPer = Ty::kPer16, kVecs = kBatch / kPer;
+    const uint32_t tid = threadIdx.x;
+    __syncthreads();
+    if (tid == 0) sh.n_list = sh.n_hits = 0;
+    __syncthreads();
+    for (uint32_t i = 0; i < rounds; i++) {
+        if (key_of(__builtin_bit_cast(float, sh.batch_max[kRowThreads * i + tid])) >= limit) {
+            const uint32_t at = atomicAdd(&sh.n_hits, 1u);
+            if (at < kListCap) sh.hits[at] = kRowThreads * i + tid;
+        }
+    }
+    __syncthreads();
+    const uint32_t hits = lds_uniform(sh.n_hits);
+    if (hits > kListCap) return false;
+    for (uint32_t i = tid; i < hits * kVecs; i += kRowThreads) {
+        const uint32_t b = sh.hits[i / kVecs];
+        const uint32_t j = lo + (b / kRowThreads) * kSweep + (kRowThreads * (i % kVecs) + b % kRowThreads) * kPer;
+        for (uint32_t q = 0; q < kPer; q++) {
+            const uint32_t key = j + q < hi ? key_of(Ty::to_f32(row[j + q])) : 0u;
+            if (key >= limit) {
+                const uint32_t at = atomicAdd(&sh.n_list, 1u);
+                if (at < kListCap) sh.list[at] = entry(key, j + q);
+            }
+        }
+    }
+    __syncthreads();
+    return lds_uniform(sh.n_list) <= kListCap;
+}
+
+// The candidates of a slice in sh.list: their number.  best: the key of the
+// thread's largest logit (0: it had none).
+template <int T, class Sh>
+__device__ inline uint32_t candidates(const typename Type<T>::elem *row, uint32_t lo, uint32_t hi, uint32_t rounds,
+                                      uint32_t best, uint32_t n, Sh &sh)
+{
+    const uint32_t none = key_of(-kInf);
+    const uint32_t thresh = max(nth_key(best, n, sh), none);
+    if (thresh > none && collect<T>(row, lo, hi, rounds, thresh, sh)) return lds_uniform(sh.n_list);
+    // Many logits equal the threshold (a masked row), or fewer than n are
+    // above -inf: those above it (in fewer than n threads' batches, so at
+    // most 63 x 16 of them), then the first that equal it, then NaN.
+    if (!collect<T>(row, lo, hi, rounds, thresh + 1, sh)) return top_slow<T>(row, lo, hi, n, thresh, sh);
+    uint32_t count = fill_equal<T>(row, lo, hi, n, lds_uniform(sh.n_list), thresh, sh);
+    if (thresh == none) count = fill_equal<T>(row, lo, hi, n, count, 1u, sh);
+    return count;
+}
+
+// Statistics of elements [lo, hi) of a row, in every thread, and with kTop
+// the number of candidates in sh.list.
+template <int T, bool kTop, class Sh>
+__device__ inline Stat slice_pass(const typename Type<T>::elem *row, uint32_t lo, uint32_t hi, uint32_t n, Sh &sh,
+                                  uint32_t *count)
+{
+    using Ty = Type<T>;
+    constexpr int kPer = Ty::kPer16, kVecs = kBatch / kPer;
+    const uint32_t tid = threadIdx.x;
+    Stat a{kFloor, 0.f, 0.f};
+    float best = -kInf;   // the largest of the thread's batches
+    bool any = false;     // the thread had a logit
+    uint32_t round = 0;
+    u32x4 cur[kVecs], nxt[kVecs];
+    // a round's vector u of a thread: elements base + (256 u + tid) kPer ..
+    auto fetch = [&](u32x4 *v, uint32_t base) {
+#pragma unroll
+        for (int u = 0; u < kVecs; u++) v[u] = load16<Ty::kBytes>(row + base + (kRowThreads * u + tid) * kPer);
+    };
+    auto take = [&](const float *f, float bmax) {
+        if (bmax > a.m) raise(a, bmax);
+        const float ml = a.m * kLog2e;
+#pragma unroll
+        for (int i = 0; i < (int)kBatch; i++) {
+            const float d = __builtin_fmaf(f[i], kLog2e, -ml);
+            const float e = exp2_fast(d);
+            a.s += e;
+            a.w = __builtin_fmaf(e, fmaxf(d, -1000.f), a.w);  // a masked logit adds 0 * -1000, not 0 * -inf
+        }
+    };
+    uint32_t base = lo;
+    if (hi - lo >= kSweep) fetch(cur, base);
+    for (; hi - base >= kSweep; base += kSweep, round++) {
+        if (hi - base >= 2 * kSweep) fetch(nxt, base + kSweep);
+        float f[kBatch];
+#pragma unroll
+        for (int u = 0; u < kVecs; u++) Ty::unpack(cur[u], f + kPer * u);
+        float bmax = f[0];
+#pragma unroll
+        for (int i = 1; i < (int)kBatch; i++) bmax = fmaxf(bmax, f[i]);
+        take(f, bmax);
+        if constexpr (kTop) {
+            // a batch of nothing but NaN counts as -inf: its elements are looked at if the threshold is that low
+            sh.batch_max[kRowThreads * round + tid] = __builtin_bit_cast(uint32_t, fmaxf(bmax, -kInf));
+            best = fmaxf(best, bmax);
+            any = true;
+        }
+#pragma unroll
+        for (int u = 0; u < kVecs; u++) cur[u] = nxt[u];
+    }
+    if (base < hi) {  // the last, partial round: absent elements as -inf
+        float f[kBatch];
+        bool had = false;
+#pragma unroll
+        for (int u = 0; u < kVecs; u++) {
+            const uint32_t j = base + (kRowThreads * u + tid) * kPer;
+            if (j + kPer <= hi) {
+                Ty::unpack(load16<Ty::kBytes>(row + j), f + kPer * u);
+            } else {
+#pragma unroll
+                for (int i = 0; i < kPer; i++) f[kPer * u + i] = j + i < hi ? Ty::to_f32(row[j + i]) : -kInf;
+            }
+            had = had || j < hi;
+        }
+        float bmax = f[0];
+#pragma unroll
+        for (int i = 1; i < (int)kBatch; i++) bmax = fmaxf(bmax, f[i]);
+        if (had) {
+            take(f, bmax);
+            any = true;
+        }
+        if constexpr (kTop) {
+            sh.batch_max[kRowThreads * round + tid] = __builtin_bit_cast(uint32_t, fmaxf(bmax, -kInf));
+            best = fmaxf(best, bmax);
+        }
+        round++;
+    }
+    if constexpr (kTop) *count = candidates<T>(row, lo, hi, round, any ? key_of(best) : 0u, n, sh);
+    return block_stat(a, sh);
+}
+
+// A row's statistics with its true maximum and exact differences, by the
+// whole block: for rows whose logits are too large for slice_pass.
+template <int T, class Sh>
+__device__ __noinline__ Stat exact_stat(const typename Type<T>::elem *row, uint32_t vocab, Sh &sh)
+{
+    __syncthreads();
+    float m = -kInf;
+    for (uint32_t j = threadIdx.x; j < vocab; j += kRowThreads) m = fmaxf(m, Type<T>::to_f32(row[j]));
+    m = block_stat(Stat{m, 0.f, 0.f}, sh).m;
+    Stat b{0.f, 0.f, 0.f};
+    for (uint32_t j = threadIdx.x; j < vocab; j += kRowThreads) {
+        const float d = (Type<T>::to_f32(row[j]) - m) * kLog2e;
+        const float e = m == -kInf ? 0.f : exp2_fast(d);
+        b.s += e;
+        b.w += e > 0.f ? e * d : 0.f;
+    }
+    __syncthreads();
+    b = block_stat(b, sh);
+    return Stat{m, b.s, b.w};
+}
+
+struct LogprobArgs {
+    const void *logits;
+    uint64_t stride;
+    const int64_t *tokens;
+    uint32_t vocab, top, slices, slice;  // slice: logits per block, a multiple of 8
+    float *logprob, *entropy, *lse, *top_logprobs;
+    int64_t *top_ids;
+    float *part;        // (row, slice): M, S, W and a spare, when slices > 1
+    uint64_t *part_top; // (row, slice): the slice's top entries in order
+    uint32_t *err;
+};
+
+// Writes a row's statistics; returns its lse for the alternatives.  Called
+// by the whole block.  S is 0 where every logit is below kFloor or the
+// largest above 2^127 / log2 e (masks of the type's lowest value in a whole
+// row, infinities, -inf in a whole row): such a row is computed again with
+// its true maximum and exact differences.
+template <int T, class Sh>
+__device__ inline float write_row(const LogprobArgs &g, uint64_t r, Stat a, Sh &sh)
+{
+    using Ty = Type<T>;
+    const typename Ty::elem *row = static_cast<const typename Ty::elem *>(g.logits) + r * g.stride;
+    float lse, entropy;
+    if (a.s == 0.f) a = exact_stat<T>(row, g.vocab, sh);
+    if (a.s == 0.f) {  // nothing but -inf: no token is possible
+        lse = -kInf;
+        entropy = 0.f;
+    } else if (!(a.s < kInf)) {  // a NaN or +inf among the logits
+        lse = entropy = nan32();
+    } else {
+        const float ln_s = __logf(a.s);
+        lse = a.m + ln_s;
+        entropy = fmaxf(ln_s - kLn2 * (a.w / a.s), 0.f);
+    }
+    if (threadIdx.x == 0) {
+        const int64_t t = g.tokens[r];
+        float lp = 0.f;
+        if (t >= 0 && t < (int64_t)g.vocab) {
+            const float z = Ty::to_f32(row[t]);
+            lp = z == -kInf && lse == lse ? -kInf : z - lse;
+        } else if (t != -1) {
+            lp = nan32();
+            report(g.err, WC_EF_BAD_INDEX);
+        }
+        g.logprob[r] = lp;
+        g.entropy[r] = entropy;
+        g.lse[r] = lse;
+    }
+    return lse;
+}
+
+__device__ __forceinline__ void put_top(const LogprobArgs &g, uint64_t r, uint32_t at, uint64_t e, float lse)
+{
+    const float z = key_value((uint32_t)(e >> 32));
+    g.top_logprobs[r * g.top + at] = z == -kInf && lse == lse ? -kInf : z - lse;
+    g.top_ids[r * g.top + at] = (int64_t)(uint32_t)~(uint32_t)e;
+}
+
+// One block per slice of a row; with one slice it writes the row.
+template <int T, bool kTop>
+__global__ __launch_bounds__(kRowThreads) void k_logprobs(LogprobArgs g)
+{
+    __shared__ RowShared<kTop, true> sh;
+    const uint64_t r = blockIdx.x / g.slices;
+    const uint32_t s = blockIdx.x % g.slices;
+    const typename Type<T>::elem *row = static_cast<const typename Type<T>::elem *>(g.logits) + r * g.stride;
+    const uint32_t lo = s * g.slice, hi = min(g.vocab, lo + g.slice);
+    uint32_t count = 0;
+    const Stat a = slice_pass<T, kTop>(row, lo, hi, g.top, sh, &count);
+    if (g.slices == 1) {
+        const float lse = write_row<T>(g, r, a, sh);
+        if constexpr (kTop) rank_list(count, g.top, sh, [&](uint32_t at, uint64_t e) { put_top(g, r, at, e, lse); });
+        return;
+    }
+    if (threadIdx.x == 0) *reinterpret_cast<f32x4 *>(g.part + 4 * (uint64_t)blockIdx.x) = f32x4{a.m, a.s, a.w, 0.f};
+    if constexpr (kTop)
+        rank_list(count, g.top, sh, [&](uint32_t at, uint64_t e) { g.part_top[(uint64_t)blockIdx.x * g.top + at] = e; });
+}
+
+// Joins the slices of a row: one block per row.  The n largest of the
+// slices' lists are found as in a slice, T being the n-th largest of the
+// threads' largest entries.  No two entries are equal, so exactly n threads
+// hold entries >= T, and a thread holds at most 16 (64 slices x 64 / 256).
+template <int T, bool kTop>
+__global__ __launch_bounds__(kRowThreads) void k_logprobs_join(LogprobArgs g)
+{
+    __shared__ RowShared<kTop, false> sh;
+    static_assert(kMaxSlices * kMaxTop / kRowThreads * kMaxTop <= kListCap, "the join's list");
+    const uint32_t tid = threadIdx.x;
+    const uint64_t r = blockIdx.x;
+    Stat a{kFloor, 0.f, 0.f};
+    if (tid < g.slices) {
+        const f32x4 p = *reinterpret_cast<const f32x4 *>(g.part + 4 * (r * g.slices + tid));
+        a = Stat{p[0], p[1], p[2]};
+    }
+    a = block_stat(a, sh);
+    const float lse = write_row<T>(g, r, a, sh);
+    if constexpr (kTop) {
+        const uint64_t *tops = g.part_top + r * g.slices * g.top;
+        const uint32_t total = g.slices * g.top;
+        uint64_t best = 0;
+        for (uint32_t i = tid; i < total; i += kRowThreads) best = max(best, tops[i]);
+        sh.list[tid] = best;
+        if (tid == 0) {
+            sh.thresh64 = ~0ull;
+            sh.n_list = 0;
+        }
+        __syncthreads();
+        uint32_t above = 0;
+        for (uint32_t i = 0; i < kRowThreads; i++) above += sh.list[i] > best;
+        if (above < g.top) atomicMin(reinterpret_cast<unsigned long long *>(&sh.thresh64), (unsigned long long)best);
+        __syncthreads();
+        const uint64_t thresh = sh.thresh64;
+        for (uint32_t i = tid; i < total; i += kRowThreads) {
+            const uint64_t e = tops[i];
+            if (e && e >= thresh) sh.list[atomicAdd(&sh.n_list, 1u)] = e;
+        }
+        __syncthreads();
+        rank_list(lds_uniform(sh.n_list), g.top, sh, [&](uint32_t at, uint64_t e) { put_top(g, r, at, e, lse); });
+    }
+}
+
+// The gradient: with g and h the gradients of a row's log probability and
+// entropy, dz_j = g [j = t] - p_j (g + h (log p_j + H)), one pass that reads
+// and writes every logit once; a thread takes 32 of them per round.  Every
+// element is read and written by one thread, the read first, so dz may be
+// the logits' own memory.
+//
+// log p_j = z_j - lse; an lse of 2^16 or more (a row of nothing but the
+// type's lowest value, say) has no bits left for the probabilities in 32
+// bits, so such a row's maximum and log of the sum are computed again.  That
+// reads the whole row: in the logits' own memory a row has only one block.
+struct LogprobGradArgs {
+    const void *logits;
+    void *out;
+    uint64_t stride, out_stride;
+    const int64_t *tokens;
+    const float *lse, *entropy, *grad_logprob, *grad_entropy;  // the gradients may be null: zero
+    uint32_t vocab, blocks;                                    // blocks per row
+    uint32_t *err;
+};
+
+template <int T>
+__global__ __launch_bounds__(kRowThreads) void k_logprobs_grad(LogprobGradArgs a)
+{
+    using Ty = Type<T>;
+    using E = typename Ty::elem;
+    constexpr int kPer = Ty::kPer16, kVecs = kBatch / kPer;
+    const uint64_t r = blockIdx.x / a.blocks;
+    const uint32_t first = (blockIdx.x % a.blocks) * kSweep, tid = threadIdx.x;
+    const E *row = static_cast<const E *>(a.logits) + r * a.stride;
+    __shared__ RowShared<false, true> sh;
+    E *out = static_cast<E *>(a.out) + r * a.out_stride;
+    const int64_t t64 = a.tokens[r];
+    const bool given = t64 >= 0 && t64 < (int64_t)a.vocab;
+    if (!given && t64 != -1 && first == 0 && tid == 0) report(a.err, WC_EF_BAD_INDEX);
+    const uint32_t t = given ? (uint32_t)t64 : ~0u;
+    float g = given && a.grad_logprob ? a.grad_logprob[r] : 0.f;
+    float h = a.grad_entropy ? a.grad_entropy[r] : 0.f;
+    float lse = a.lse[r];
+    if (lse == -kInf) {  // nothing but -inf: constant outputs, no gradient
+        g = h = 0.f;
+        lse = kInf;  // every p becomes exp(-inf) = 0
+    }
+    float shift = 0.f;
+    if (fabsf(lse) >= 65536.f && fabsf(lse) < kInf) {
+        const Stat st = exact_stat<T>(row, a.vocab, sh);
+        lse = st.m;
+        shift = __logf(st.s);
+    }
+    const float gh = __builtin_fmaf(h, h != 0.f ? a.entropy[r] : 0.f, g);
+    auto grad = [&](float z, uint32_t j) {
+        const float lp = (z - lse) - shift;
+        const float p = exp2_fast(lp * kLog2e);
+        const float d = -p * __builtin_fmaf(h, fmaxf(lp, -1e30f), gh);  // p = 0: 0 times a finite number
+        return j == t ? d + g : d;
+    };
+    for (uint32_t base = first; base < a.vocab; base += a.blocks * kSweep) {
+        uint32_t at[kVecs];
+        u32x4 v[kVecs];
+#pragma unroll
+        for (int u = 0; u < kVecs; u++) {
+            at[u] = base + (kRowThreads * u + tid) * kPer;
+            if (at[u] + kPer <= a.vocab) v[u] = load16<Ty::kBytes>(row + at[u]);
+        }
+#pragma unroll
+        for (int u = 0; u < kVecs; u++) {
+            if (at[u] + kPer <= a.vocab) {
+                float f[kPer];
+                Ty::unpack(v[u], f);
+#pragma unroll
+                for (int i = 0; i < kPer; i++) f[i] = grad(f[i], at[u] + i);
+                store16<Ty::kBytes>(out + at[u], Ty::pack(f));
+            } else {
+                for (int i = 0; i < kPer; i++)
+                    if (at[u] + i < a.vocab) out[at[u] + i] = Ty::from_f32(grad(Ty::to_f32(row[at[u] + i]), at[u] + i));
+            }
+        }
+    }
+}
+
+}  // namespace ops
+}  // namespace wc

@@ -412,6 +412,38 @@ typedef struct {
 
 wc_status wc_token_logprobs_backward(const wc_logprobs_grad *a, uint32_t *d_err, hipStream_t stream);
 
+/* Low-rank adapters of many requests beside a shared projection (for
+ * instance wc_decode_gemm_batch, which adds X W^T into the same Y):
+ * y_t += scales[i] B_i (A_i x_t) with i = ids[t].  ids[t] = -1: no adapter,
+ * y_t stays; another number outside [0, n): y_t stays and WC_EF_BAD_INDEX.
+ * Tokens may have adapters in any order; tokens side by side with the same
+ * one share its reading.  Adapters of smaller ranks are padded with zeros. */
+typedef struct {
+    const void *x;         /* m x cols, rows x_stride elements apart, 16-byte aligned rows */
+    uint64_t x_stride;     /* a multiple of 8 */
+    void *y;               /* m x rows, rows y_stride elements apart, any alignment */
+    uint64_t y_stride;
+    const void *a;         /* n x rank x cols, 16-byte aligned */
+    const void *b;         /* n x rows x rank */
+    const int64_t *ids;    /* m */
+    const float *scales;   /* n, or NULL: 1 */
+    uint64_t m;
+    uint32_t n;
+    uint32_t rank;         /* 1 .. 256 */
+    uint32_t cols;         /* a multiple of 8 */
+    uint32_t rows;
+    uint32_t type;         /* of x, a and b: WC_T_BF16 or WC_T_FP16 */
+    uint32_t y_type;       /* `type` or WC_T_FP32 */
+} wc_adapters;
+
+/* Bytes of scratch that wc_add_adapters needs (0 for sizes that it rejects).
+ * Pure host function. */
+uint64_t wc_add_adapters_scratch(uint64_t m, uint32_t rank, uint32_t cols, uint32_t rows);
+
+/* d_scratch: 16-byte aligned; its contents need no preparation. */
+wc_status wc_add_adapters(const wc_adapters *a, void *d_scratch, uint64_t scratch_bytes, uint32_t *d_err,
+                          hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -44,7 +44,7 @@ EXPORTS = ["wc_version", "wc_status_string", "wc_query_layout", "wc_plan_batch",
            "wc_decode", "wc_encode_batch", "wc_decode_batch", "wc_check_division", "wc_tile_order",
            "wc_decode_gemm_batch", "wc_decode_variant", "wc_encode_noalloc", "wc_noalloc_max_chunks",
            "wc_set_encoder_words", "wc_encode_variant", "wc_token_logprobs_scratch", "wc_token_logprobs",
-           "wc_token_logprobs_backward"]
+           "wc_token_logprobs_backward", "wc_add_adapters_scratch", "wc_add_adapters"]
 # encoder word-store forms (wc_set_encoder_words)
 ENC_WORDS_AUTO, ENC_WORDS_DIRECT, ENC_WORDS_STAGED = 0, 1, 2
 
@@ -93,6 +93,14 @@ class wc_logprobs_grad(ctypes.Structure):
                 ("m", ctypes.c_uint64), ("vocab", ctypes.c_uint32), ("type", ctypes.c_uint32)]
 
 
+class wc_adapters(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_void_p), ("x_stride", ctypes.c_uint64), ("y", ctypes.c_void_p),
+                ("y_stride", ctypes.c_uint64), ("a", ctypes.c_void_p), ("b", ctypes.c_void_p),
+                ("ids", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("m", ctypes.c_uint64),
+                ("n", ctypes.c_uint32), ("rank", ctypes.c_uint32), ("cols", ctypes.c_uint32),
+                ("rows", ctypes.c_uint32), ("type", ctypes.c_uint32), ("y_type", ctypes.c_uint32)]
+
+
 _lib = None
 
 
@@ -129,10 +137,14 @@ def lib() -> ctypes.CDLL:
     L.wc_token_logprobs_scratch.argtypes = [U64, U32, U32]
     L.wc_token_logprobs_scratch.restype = U64
     L.wc_token_logprobs.argtypes = [ctypes.POINTER(wc_logprobs), P, U64, P, P]
+    L.wc_add_adapters_scratch.argtypes = [U64, U32, U32, U32]
+    L.wc_add_adapters_scratch.restype = U64
+    L.wc_add_adapters.argtypes = [ctypes.POINTER(wc_adapters), P, U64, P, P]
     L.wc_token_logprobs_backward.argtypes = [ctypes.POINTER(wc_logprobs_grad), P, P]
     for name in ("wc_query_layout", "wc_plan_batch", "wc_encode", "wc_decode", "wc_encode_batch",
                  "wc_decode_batch", "wc_tile_order", "wc_decode_gemm_batch", "wc_decode_variant",
-                 "wc_encode_noalloc", "wc_encode_variant", "wc_token_logprobs", "wc_token_logprobs_backward"):
+                 "wc_encode_noalloc", "wc_encode_variant", "wc_token_logprobs", "wc_token_logprobs_backward",
+                 "wc_add_adapters"):
         getattr(L, name).restype = I
     _lib = L
     return L
@@ -300,6 +312,15 @@ def wc_token_logprobs(args: wc_logprobs, d_scratch, scratch_bytes: int, d_err=No
 
 def wc_token_logprobs_backward(args: wc_logprobs_grad, d_err=None, stream=None):
     _check(lib().wc_token_logprobs_backward(args, _ptr(d_err), _stream(stream)), "wc_token_logprobs_backward")
+
+
+def wc_add_adapters_scratch(m: int, rank: int, cols: int, rows: int) -> int:
+    return lib().wc_add_adapters_scratch(m, rank, cols, rows)
+
+
+def wc_add_adapters(args: wc_adapters, d_scratch, scratch_bytes: int, d_err=None, stream=None):
+    rc = lib().wc_add_adapters(args, _ptr(d_scratch), scratch_bytes, _ptr(d_err), _stream(stream))
+    _check(rc, "wc_add_adapters")
 
 
 def wc_check_division(samples_per_divisor: int = 256) -> int:

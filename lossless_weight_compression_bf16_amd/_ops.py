@@ -24,6 +24,13 @@ def rows_of(t: torch.Tensor) -> torch.Tensor:
     return t.contiguous()
 
 
+def rows16(t: torch.Tensor) -> torch.Tensor:
+    """t (2-D, 16-bit) with 16-byte aligned rows of unit column stride: itself, or a copy."""
+    if t.stride(1) == 1 and t.stride(0) % 8 == 0 and t.stride(0) >= t.shape[1] and t.data_ptr() % 16 == 0:
+        return t
+    return t.clone(memory_format=torch.contiguous_format)
+
+
 def on_stream(device: torch.device, stream, call):
     """call(raw stream) with the device and stream of the call current, so
     that what it allocates belongs to that stream.  stream: None (the

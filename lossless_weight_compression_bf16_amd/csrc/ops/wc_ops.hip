@@ -6,6 +6,7 @@
 #include <stdint.h>
 
 #include "wc.h"
+#include "ops_adapters.hpp"
 #include "ops_common.hpp"
 #include "ops_logprobs.hpp"
 
@@ -54,6 +55,82 @@ wc_status launch_logprobs(const LogprobArgs &g, uint64_t m, hipStream_t stream)
         if (g.top) hipLaunchKernelGGL((k_logprobs_join<T, true>), dim3((uint32_t)m), block, 0, stream, g);
         else hipLaunchKernelGGL((k_logprobs_join<T, false>), dim3((uint32_t)m), block, 0, stream, g);
     }
+    return launched();
+}
+
+// Launch shapes of the adapters: tiles of 16 tokens where the tokens are
+// few, each turn of a tile (an adapter) its own block, so that as many blocks
+// as possible share the reading; tiles of 64 tokens where prompts repeat
+// their adapter over many tokens, so that it is read once per tile.
+struct AdapterPlan {
+    uint32_t rank_pad, rank_blocks, tile, turns, splits, steps;  // k_adapters_down
+    uint32_t up_tile, row_blocks, row_block;                     // k_adapters_up
+    uint64_t tiles, up_tiles, scratch;
+};
+
+AdapterPlan adapter_plan(uint64_t m, uint32_t rank, uint32_t cols, uint32_t rows)
+{
+    AdapterPlan p{};
+    const bool many = m > 512;
+    p.rank_pad = (rank + 15) / 16 * 16;
+    p.rank_blocks = (uint32_t)ceil_div(rank, 64);
+    p.tile = many ? 64 : 16;
+    p.turns = many ? 1 : (uint32_t)(m < 16 ? m : 16);
+    p.tiles = ceil_div(m, p.tile);
+    const uint64_t steps = ceil_div(cols, 32), blocks = p.tiles * p.turns * p.rank_blocks;
+    uint64_t splits = blocks < 2 * kCus ? 2 * kCus / blocks : 1;
+    const uint64_t most = ceil_div(steps, 8);  // two steps for each of a block's waves
+    if (splits > most) splits = most;
+    if (splits > 16) splits = 16;
+    p.steps = (uint32_t)(ceil_div(ceil_div(steps, splits), 4) * 4);
+    p.splits = (uint32_t)ceil_div(steps, p.steps);
+    p.up_tile = many ? (rank <= 64 ? 64 : rank <= 128 ? 32 : 16) : 16;
+    p.up_tiles = ceil_div(m, p.up_tile);
+    uint64_t rb = ceil_div(4 * kCus, p.up_tiles * p.turns);
+    const uint64_t rmost = ceil_div(rows, 256);
+    if (rb > rmost) rb = rmost;
+    p.row_block = (uint32_t)(ceil_div(ceil_div(rows, rb), 256) * 256);
+    p.row_blocks = (uint32_t)ceil_div(rows, p.row_block);
+    p.scratch = (uint64_t)p.splits * m * p.rank_pad * 4;
+    return p;
+}
+
+bool valid_adapters(uint64_t m, uint32_t rank, uint32_t cols, uint32_t rows)
+{
+    return m <= (1ull << 31) && rank >= 1 && rank <= kAdapterMaxRank && cols >= 8 && cols % 8 == 0 && rows >= 1 &&
+           rows <= (1u << 30) && cols <= (1u << 30);
+}
+
+template <int T, int TT>
+void launch_down(const AdapterArgs &g, const AdapterPlan &p, hipStream_t stream)
+{
+    const dim3 grid((uint32_t)(p.tiles * p.splits), p.rank_blocks, p.turns), block(256);
+    if (g.rank <= 16) hipLaunchKernelGGL((k_adapters_down<T, TT, 1>), grid, block, 0, stream, g);
+    else if (g.rank <= 32) hipLaunchKernelGGL((k_adapters_down<T, TT, 2>), grid, block, 0, stream, g);
+    else hipLaunchKernelGGL((k_adapters_down<T, TT, 4>), grid, block, 0, stream, g);
+}
+
+template <int T, int YT>
+void launch_up(const AdapterArgs &g, const AdapterPlan &p, hipStream_t stream)
+{
+    const dim3 grid((uint32_t)(p.up_tiles * p.row_blocks), 1, p.turns), block(256);
+    const uint32_t tt = p.up_tile / 16;
+    if (tt == 4 && g.rank <= 32) hipLaunchKernelGGL((k_adapters_up<T, YT, 4, 1>), grid, block, 0, stream, g);
+    else if (tt == 4) hipLaunchKernelGGL((k_adapters_up<T, YT, 4, 2>), grid, block, 0, stream, g);
+    else if (tt == 2) hipLaunchKernelGGL((k_adapters_up<T, YT, 2, 4>), grid, block, 0, stream, g);
+    else if (g.rank <= 32) hipLaunchKernelGGL((k_adapters_up<T, YT, 1, 1>), grid, block, 0, stream, g);
+    else if (g.rank <= 64) hipLaunchKernelGGL((k_adapters_up<T, YT, 1, 2>), grid, block, 0, stream, g);
+    else if (g.rank <= 128) hipLaunchKernelGGL((k_adapters_up<T, YT, 1, 4>), grid, block, 0, stream, g);
+    else hipLaunchKernelGGL((k_adapters_up<T, YT, 1, 8>), grid, block, 0, stream, g);
+}
+
+template <int T>
+wc_status launch_adapters(const AdapterArgs &g, const AdapterPlan &p, uint32_t y_type, hipStream_t stream)
+{
+    if (p.tile == 64) launch_down<T, 4>(g, p, stream);
+    else launch_down<T, 1>(g, p, stream);
+    if (y_type == WC_T_FP32) launch_up<T, WC_T_FP32>(g, p, stream);
+    else launch_up<T, T>(g, p, stream);
     return launched();
 }
 
@@ -141,6 +218,52 @@ wc_status wc_token_logprobs_backward(const wc_logprobs_grad *a, uint32_t *d_err,
     default: hipLaunchKernelGGL(k_logprobs_grad<WC_T_FP32>, grid, block, 0, stream, g); break;
     }
     return launched();
+}
+
+uint64_t wc_add_adapters_scratch(uint64_t m, uint32_t rank, uint32_t cols, uint32_t rows)
+{
+    if (m == 0 || !valid_adapters(m, rank, cols, rows)) return 0;
+    return adapter_plan(m, rank, cols, rows).scratch;
+}
+
+wc_status wc_add_adapters(const wc_adapters *a, void *d_scratch, uint64_t scratch_bytes, uint32_t *d_err,
+                          hipStream_t stream)
+{
+    if (!a || (a->type != WC_T_BF16 && a->type != WC_T_FP16) || (a->y_type != a->type && a->y_type != WC_T_FP32))
+        return WC_ERR_ARG;
+    if (!valid_adapters(a->m, a->rank, a->cols, a->rows) || a->n > 0x7FFFFFFFu) return WC_ERR_ARG;
+    if (d_err && !aligned(d_err, 4)) return WC_ERR_ARG;
+    if (a->m == 0) return WC_OK;
+    if (a->n && (!a->a || !aligned(a->a, 16) || !a->b || !aligned(a->b, 2))) return WC_ERR_ARG;
+    if (!a->x || !aligned(a->x, 16) || (a->m > 1 && (a->x_stride < a->cols || a->x_stride % 8))) return WC_ERR_ARG;
+    if (!a->y || !aligned(a->y, type_bytes(a->y_type)) || (a->m > 1 && a->y_stride < a->rows)) return WC_ERR_ARG;
+    if (!a->ids || !aligned(a->ids, 8) || !aligned(a->scales, 4)) return WC_ERR_ARG;
+    const AdapterPlan p = adapter_plan(a->m, a->rank, a->cols, a->rows);
+    if (p.tiles * p.splits > kMaxGrid || p.up_tiles * p.row_blocks > kMaxGrid) return WC_ERR_ARG;
+    if (scratch_bytes < p.scratch) return WC_ERR_CAPACITY;
+    if (!d_scratch || !aligned(d_scratch, 16)) return WC_ERR_ARG;
+    AdapterArgs g{};
+    g.x = static_cast<const uint16_t *>(a->x);
+    g.x_stride = a->x_stride;
+    g.y = a->y;
+    g.y_stride = a->y_stride;
+    g.a = static_cast<const uint16_t *>(a->a);
+    g.b = static_cast<const uint16_t *>(a->b);
+    g.ids = a->ids;
+    g.scales = a->scales;
+    g.m = a->m;
+    g.n = a->n;
+    g.rank = a->rank;
+    g.cols = a->cols;
+    g.rows = a->rows;
+    g.u = static_cast<float *>(d_scratch);
+    g.rank_pad = p.rank_pad;
+    g.splits = p.splits;
+    g.steps = p.steps;
+    g.row_block = p.row_block;
+    g.err = d_err;
+    return a->type == WC_T_BF16 ? launch_adapters<WC_T_BF16>(g, p, a->y_type, stream)
+                                : launch_adapters<WC_T_FP16>(g, p, a->y_type, stream);
 }
 
 }  // extern "C"

@@ -444,6 +444,43 @@ uint64_t wc_add_adapters_scratch(uint64_t m, uint32_t rank, uint32_t cols, uint3
 wc_status wc_add_adapters(const wc_adapters *a, void *d_scratch, uint64_t scratch_bytes, uint32_t *d_err,
                           hipStream_t stream);
 
+/* A whole mixture-of-experts layer for few tokens, on uncompressed experts
+ * (for instance what wc_decode_batch wrote).  For each of the m tokens:
+ * logits l = R x over the experts, p = softmax(l), the top_k experts with the
+ * largest logits (equal ones by their number, NaN last), their weights p, or
+ * with `renormalize` p divided by the sum of the chosen ones, and
+ * out = sum_e weight_e W2_e (silu(W1_e x) * (W3_e x)), rounded once to
+ * `type`.  Experts without tokens are not read. */
+typedef struct {
+    const void *x;          /* m x cols, rows x_stride elements apart, 16-byte aligned rows */
+    uint64_t x_stride;      /* a multiple of 8 */
+    const void *router;     /* experts x cols, 16-byte aligned */
+    const void *w1;         /* experts x inner x cols (gate); 16-byte aligned, as w3 and w2 */
+    const void *w3;         /* the same (up) */
+    const void *w2;         /* experts x cols x inner (down) */
+    uint64_t up_expert;     /* elements from one expert, and one row, of w1 and w3 to the next: */
+    uint64_t up_row;        /*   multiples of 8 */
+    uint64_t down_expert;   /* of w2 */
+    uint64_t down_row;
+    void *out;              /* m x cols, rows out_stride elements apart, any alignment */
+    uint64_t out_stride;
+    uint64_t m;             /* 0 .. 64 */
+    uint32_t experts;       /* 1 .. 1024 */
+    uint32_t top_k;         /* 1 .. 16, at most experts */
+    uint32_t cols;          /* a multiple of 8, at most 2^20 */
+    uint32_t inner;         /* a multiple of 8, at most 2^20 */
+    uint32_t type;          /* WC_T_BF16 or WC_T_FP16: of everything above */
+    uint32_t renormalize;
+} wc_moe;
+
+/* Bytes of scratch that wc_moe_layer needs (0 for sizes that it rejects).
+ * Pure host function. */
+uint64_t wc_moe_layer_scratch(uint64_t m, uint32_t experts, uint32_t top_k, uint32_t cols, uint32_t inner);
+
+/* d_scratch: 256-byte aligned; its contents need no preparation.  `out` must
+ * not overlap x. */
+wc_status wc_moe_layer(const wc_moe *a, void *d_scratch, uint64_t scratch_bytes, hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

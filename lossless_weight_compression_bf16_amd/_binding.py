@@ -44,7 +44,8 @@ EXPORTS = ["wc_version", "wc_status_string", "wc_query_layout", "wc_plan_batch",
            "wc_decode", "wc_encode_batch", "wc_decode_batch", "wc_check_division", "wc_tile_order",
            "wc_decode_gemm_batch", "wc_decode_variant", "wc_encode_noalloc", "wc_noalloc_max_chunks",
            "wc_set_encoder_words", "wc_encode_variant", "wc_token_logprobs_scratch", "wc_token_logprobs",
-           "wc_token_logprobs_backward", "wc_add_adapters_scratch", "wc_add_adapters"]
+           "wc_token_logprobs_backward", "wc_add_adapters_scratch", "wc_add_adapters",
+           "wc_moe_layer_scratch", "wc_moe_layer"]
 # encoder word-store forms (wc_set_encoder_words)
 ENC_WORDS_AUTO, ENC_WORDS_DIRECT, ENC_WORDS_STAGED = 0, 1, 2
 
@@ -101,6 +102,16 @@ class wc_adapters(ctypes.Structure):
                 ("rows", ctypes.c_uint32), ("type", ctypes.c_uint32), ("y_type", ctypes.c_uint32)]
 
 
+class wc_moe(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_void_p), ("x_stride", ctypes.c_uint64), ("router", ctypes.c_void_p),
+                ("w1", ctypes.c_void_p), ("w3", ctypes.c_void_p), ("w2", ctypes.c_void_p),
+                ("up_expert", ctypes.c_uint64), ("up_row", ctypes.c_uint64), ("down_expert", ctypes.c_uint64),
+                ("down_row", ctypes.c_uint64), ("out", ctypes.c_void_p), ("out_stride", ctypes.c_uint64),
+                ("m", ctypes.c_uint64), ("experts", ctypes.c_uint32), ("top_k", ctypes.c_uint32),
+                ("cols", ctypes.c_uint32), ("inner", ctypes.c_uint32), ("type", ctypes.c_uint32),
+                ("renormalize", ctypes.c_uint32)]
+
+
 _lib = None
 
 
@@ -140,11 +151,14 @@ def lib() -> ctypes.CDLL:
     L.wc_add_adapters_scratch.argtypes = [U64, U32, U32, U32]
     L.wc_add_adapters_scratch.restype = U64
     L.wc_add_adapters.argtypes = [ctypes.POINTER(wc_adapters), P, U64, P, P]
+    L.wc_moe_layer_scratch.argtypes = [U64, U32, U32, U32, U32]
+    L.wc_moe_layer_scratch.restype = U64
+    L.wc_moe_layer.argtypes = [ctypes.POINTER(wc_moe), P, U64, P]
     L.wc_token_logprobs_backward.argtypes = [ctypes.POINTER(wc_logprobs_grad), P, P]
     for name in ("wc_query_layout", "wc_plan_batch", "wc_encode", "wc_decode", "wc_encode_batch",
                  "wc_decode_batch", "wc_tile_order", "wc_decode_gemm_batch", "wc_decode_variant",
                  "wc_encode_noalloc", "wc_encode_variant", "wc_token_logprobs", "wc_token_logprobs_backward",
-                 "wc_add_adapters"):
+                 "wc_add_adapters", "wc_moe_layer"):
         getattr(L, name).restype = I
     _lib = L
     return L
@@ -321,6 +335,14 @@ def wc_add_adapters_scratch(m: int, rank: int, cols: int, rows: int) -> int:
 def wc_add_adapters(args: wc_adapters, d_scratch, scratch_bytes: int, d_err=None, stream=None):
     rc = lib().wc_add_adapters(args, _ptr(d_scratch), scratch_bytes, _ptr(d_err), _stream(stream))
     _check(rc, "wc_add_adapters")
+
+
+def wc_moe_layer_scratch(m: int, experts: int, top_k: int, cols: int, inner: int) -> int:
+    return lib().wc_moe_layer_scratch(m, experts, top_k, cols, inner)
+
+
+def wc_moe_layer(args: wc_moe, d_scratch, scratch_bytes: int, stream=None):
+    _check(lib().wc_moe_layer(args, _ptr(d_scratch), scratch_bytes, _stream(stream)), "wc_moe_layer")
 
 
 def wc_check_division(samples_per_divisor: int = 256) -> int:

@@ -131,6 +131,19 @@ __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_ex
 __device__ __forceinline__ float nan32() { return __builtin_bit_cast(float, 0x7FC00000u); }
 constexpr float kInf = __builtin_inff();
 
+// Whole numbers in the order of floats (-0 = 0), 1 for NaN, 0 for nothing.
+__device__ __forceinline__ uint32_t key_of(float f)
+{
+    if (f != f) return 1u;
+    const uint32_t b = __builtin_bit_cast(uint32_t, f + 0.0f);  // -0 + 0 = 0
+    return (b & 0x80000000u) ? ~b : b | 0x80000000u;
+}
+__device__ __forceinline__ float key_value(uint32_t k)
+{
+    if (k <= 1u) return nan32();
+    return __builtin_bit_cast(float, (k & 0x80000000u) ? k & 0x7FFFFFFFu : ~k);
+}
+
 // A word of LDS that is the same for the whole block, read to the end: a
 // plain read may still be under way when its wave reaches the next barrier,
 // after which another wave may write the word again.

@@ -38,19 +38,6 @@ constexpr uint32_t kMaxVocab = kMaxSlice * kMaxSlices / 2;
 constexpr uint32_t kListCap = 1024;                      // candidates ranked by counting
 constexpr float kFloor = -1e30f;                         // a thread's maximum before its first logit
 
-// Whole numbers in the order of the alternatives: 0 for no logit, 1 for NaN.
-__device__ __forceinline__ uint32_t key_of(float f)
-{
-    if (f != f) return 1u;
-    const uint32_t b = __builtin_bit_cast(uint32_t, f + 0.0f);  // -0 + 0 = 0
-    return (b & 0x80000000u) ? ~b : b | 0x80000000u;
-}
-__device__ __forceinline__ float key_value(uint32_t k)
-{
-    if (k <= 1u) return nan32();
-    return __builtin_bit_cast(float, (k & 0x80000000u) ? k & 0x7FFFFFFFu : ~k);
-}
-
 // Softmax statistics in base 2: see the file's comment.
 struct Stat {
     float m, s, w;

@@ -9,6 +9,7 @@
 #include "ops_adapters.hpp"
 #include "ops_common.hpp"
 #include "ops_logprobs.hpp"
+#include "ops_moe.hpp"
 
 using namespace wc::ops;
 
@@ -132,6 +133,75 @@ wc_status launch_adapters(const AdapterArgs &g, const AdapterPlan &p, uint32_t y
     if (y_type == WC_T_FP32) launch_up<T, WC_T_FP32>(g, p, stream);
     else launch_up<T, T>(g, p, stream);
     return launched();
+}
+
+// Launch shapes and scratch of the mixture-of-experts layer.
+struct MoePlan {
+    uint32_t route_tiles, route_splits, route_steps, experts_pad, slots, up_tiles, down_tiles, parts;
+    uint64_t logits, ids, weights, h, part, bytes;  // offsets in the scratch
+};
+
+MoePlan moe_plan(uint32_t m, uint32_t experts, uint32_t top_k, uint32_t cols, uint32_t inner)
+{
+    MoePlan p{};
+    p.route_tiles = (experts + 15) / 16;
+    p.experts_pad = 16 * p.route_tiles;
+    const uint32_t steps = (cols + 31) / 32;
+    uint32_t splits = 128 / p.route_tiles;
+    const uint32_t most = (steps + 7) / 8;  // two steps for each of a block's waves
+    if (splits > most) splits = most;
+    if (splits > 16) splits = 16;
+    if (splits < 1) splits = 1;
+    p.route_steps = (uint32_t)(ceil_div(ceil_div(steps, splits), 4) * 4);
+    p.route_splits = (uint32_t)ceil_div(steps, p.route_steps);
+    p.slots = m * top_k < experts ? m * top_k : experts;
+    p.up_tiles = (inner + 15) / 16;
+    p.down_tiles = (cols + 15) / 16;
+    p.parts = 1;
+    while (p.parts < 16 && p.down_tiles * p.parts < kCus) p.parts *= 2;
+    uint64_t at = 0;
+    auto take = [&](uint64_t bytes) {
+        const uint64_t here = at;
+        at = ceil_div(at + bytes, 256) * 256;
+        return here;
+    };
+    p.logits = take(4ull * p.route_splits * m * p.experts_pad);
+    p.ids = take(4ull * m * top_k);
+    p.weights = take(4ull * m * top_k);
+    p.h = take(4ull * m * top_k * inner);
+    p.part = take(p.parts > 1 ? 4ull * p.parts * m * cols : 0);
+    p.bytes = at;
+    return p;
+}
+
+bool valid_moe(uint64_t m, uint32_t experts, uint32_t top_k, uint32_t cols, uint32_t inner)
+{
+    return m <= kMoeMaxTokens && experts >= 1 && experts <= kMoeMaxExperts && top_k >= 1 && top_k <= kMoeMaxTop &&
+           top_k <= experts && cols >= 8 && cols % 8 == 0 && cols <= (1u << 20) && inner >= 8 && inner % 8 == 0 &&
+           inner <= (1u << 20);
+}
+
+template <int T, int TT>
+wc_status launch_moe(const MoeArgs &g, const MoePlan &p, hipStream_t stream)
+{
+    hipLaunchKernelGGL((k_moe_route<T, TT>), dim3(p.route_tiles * p.route_splits), dim3(256), 0, stream, g);
+    const dim3 tokens(g.m), wave(64);
+    if (g.experts <= 64) hipLaunchKernelGGL(k_moe_select<1>, tokens, wave, 0, stream, g);
+    else if (g.experts <= 256) hipLaunchKernelGGL(k_moe_select<4>, tokens, wave, 0, stream, g);
+    else hipLaunchKernelGGL(k_moe_select<16>, tokens, wave, 0, stream, g);
+    hipLaunchKernelGGL((k_moe_up<T, TT>), dim3(p.slots * p.up_tiles), dim3(256), 0, stream, g);
+    hipLaunchKernelGGL((k_moe_down<T, TT>), dim3(p.down_tiles * p.parts), dim3(64 * kMoeDownWaves), 0, stream, g);
+    if (p.parts > 1)
+        hipLaunchKernelGGL(k_moe_join<T>, dim3((g.m * (g.cols / 4) + 255) / 256), dim3(256), 0, stream, g);
+    return launched();
+}
+
+template <int T>
+wc_status launch_moe_tiles(const MoeArgs &g, const MoePlan &p, hipStream_t stream)
+{
+    if (g.m <= 16) return launch_moe<T, 1>(g, p, stream);
+    if (g.m <= 32) return launch_moe<T, 2>(g, p, stream);
+    return launch_moe<T, 4>(g, p, stream);
 }
 
 }  // namespace
@@ -264,6 +334,63 @@ wc_status wc_add_adapters(const wc_adapters *a, void *d_scratch, uint64_t scratc
     g.err = d_err;
     return a->type == WC_T_BF16 ? launch_adapters<WC_T_BF16>(g, p, a->y_type, stream)
                                 : launch_adapters<WC_T_FP16>(g, p, a->y_type, stream);
+}
+
+uint64_t wc_moe_layer_scratch(uint64_t m, uint32_t experts, uint32_t top_k, uint32_t cols, uint32_t inner)
+{
+    if (m == 0 || !valid_moe(m, experts, top_k, cols, inner)) return 0;
+    return moe_plan((uint32_t)m, experts, top_k, cols, inner).bytes;
+}
+
+wc_status wc_moe_layer(const wc_moe *a, void *d_scratch, uint64_t scratch_bytes, hipStream_t stream)
+{
+    if (!a || (a->type != WC_T_BF16 && a->type != WC_T_FP16)) return WC_ERR_ARG;
+    if (!valid_moe(a->m, a->experts, a->top_k, a->cols, a->inner)) return WC_ERR_ARG;
+    if (a->m == 0) return WC_OK;
+    if (!a->x || !aligned(a->x, 16) || (a->m > 1 && (a->x_stride < a->cols || a->x_stride % 8))) return WC_ERR_ARG;
+    if (!a->router || !aligned(a->router, 16)) return WC_ERR_ARG;
+    if (!a->w1 || !a->w3 || !a->w2 || !aligned(a->w1, 16) || !aligned(a->w3, 16) || !aligned(a->w2, 16))
+        return WC_ERR_ARG;
+    if (a->up_row < a->cols || a->up_row % 8 || a->up_expert % 8 || a->down_row < a->inner || a->down_row % 8 ||
+        a->down_expert % 8)
+        return WC_ERR_ARG;
+    if (!a->out || !aligned(a->out, 2) || (a->m > 1 && a->out_stride < a->cols)) return WC_ERR_ARG;
+    const MoePlan p = moe_plan((uint32_t)a->m, a->experts, a->top_k, a->cols, a->inner);
+    if ((uint64_t)p.slots * p.up_tiles > kMaxGrid) return WC_ERR_ARG;
+    if (scratch_bytes < p.bytes) return WC_ERR_CAPACITY;
+    if (!d_scratch || !aligned(d_scratch, 256)) return WC_ERR_ARG;
+    char *s = static_cast<char *>(d_scratch);
+    MoeArgs g{};
+    g.x = static_cast<const uint16_t *>(a->x);
+    g.router = static_cast<const uint16_t *>(a->router);
+    g.w1 = static_cast<const uint16_t *>(a->w1);
+    g.w3 = static_cast<const uint16_t *>(a->w3);
+    g.w2 = static_cast<const uint16_t *>(a->w2);
+    g.x_stride = a->x_stride;
+    g.up_expert = a->up_expert;
+    g.up_row = a->up_row;
+    g.down_expert = a->down_expert;
+    g.down_row = a->down_row;
+    g.out = static_cast<uint16_t *>(a->out);
+    g.out_stride = a->out_stride;
+    g.m = (uint32_t)a->m;
+    g.experts = a->experts;
+    g.top_k = a->top_k;
+    g.cols = a->cols;
+    g.inner = a->inner;
+    g.renormalize = a->renormalize;
+    g.logits = reinterpret_cast<float *>(s + p.logits);
+    g.ids = reinterpret_cast<int32_t *>(s + p.ids);
+    g.weights = reinterpret_cast<float *>(s + p.weights);
+    g.h = reinterpret_cast<uint16_t *>(s + p.h);
+    g.part = reinterpret_cast<float *>(s + p.part);
+    g.experts_pad = p.experts_pad;
+    g.route_splits = p.route_splits;
+    g.route_steps = p.route_steps;
+    g.slots = p.slots;
+    g.parts = p.parts;
+    return a->type == WC_T_BF16 ? launch_moe_tiles<WC_T_BF16>(g, p, stream)
+                                : launch_moe_tiles<WC_T_FP16>(g, p, stream);
 }
 
 }  // extern "C"

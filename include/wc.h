@@ -431,13 +431,13 @@ typedef struct {
     uint32_t n;
     uint32_t rank;         /* 1 .. 256 */
     uint32_t cols;         /* a multiple of 8 */
-    uint32_t rows;
+    uint32_t rows;         /* rows * rank below 2^31 */
     uint32_t type;         /* of x, a and b: WC_T_BF16 or WC_T_FP16 */
     uint32_t y_type;       /* `type` or WC_T_FP32 */
 } wc_adapters;
 
-/* Bytes of scratch that wc_add_adapters needs (0 for sizes that it rejects).
- * Pure host function. */
+/* Bytes of scratch that wc_add_adapters needs (0 for few tokens, and for
+ * sizes that it rejects).  Pure host function. */
 uint64_t wc_add_adapters_scratch(uint64_t m, uint32_t rank, uint32_t cols, uint32_t rows);
 
 /* d_scratch: 16-byte aligned; its contents need no preparation. */

@@ -55,7 +55,7 @@ def add_adapters(x: torch.Tensor, y: torch.Tensor, a: torch.Tensor, b: torch.Ten
 
     def call(raw):
         nbytes = B.wc_add_adapters_scratch(m, rank, cols, rows)
-        scratch = torch.empty(nbytes, dtype=torch.uint8, device=x.device)
+        scratch = torch.empty(nbytes, dtype=torch.uint8, device=x.device) if nbytes else None
         err = torch.zeros(1, dtype=torch.int32, device=x.device) if check else None
         g = B.wc_adapters(x.data_ptr(), x.stride(0), y.data_ptr(), y.stride(0), a.data_ptr(), b.data_ptr(),
                           ids.data_ptr(), scales.data_ptr() if scales is not None else 0, m, n, rank, cols, rows,

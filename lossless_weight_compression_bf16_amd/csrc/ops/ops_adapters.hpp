@@ -2,20 +2,19 @@
 // projection:  y_t += s_i B_i (A_i x_t)  with i = ids[t], A_i of rank x cols,
 // B_i of rows x rank.
 //
-// Two launches on the matrix cores, both over tiles of 16 (few tokens) or 64
-// consecutive tokens and, within a tile, one adapter after the other: the
-// tokens of a prompt lie side by side and share their adapter, the tokens of
-// a batch of single requests differ and take one turn each, spread over the
-// grid's z.
-//   k_adapters_down  u_t = s_i A_i x_t (fp32), the columns split over the
-//                    waves of a block and, for few tokens, over blocks
-//   k_adapters_up    y_t += B_i u_t
+// On the matrix cores, over tiles of 16 (few tokens) or 64 consecutive tokens
+// and, within a tile, one adapter after the other: the tokens of a prompt lie
+// side by side and share their adapter, the tokens of a batch of single
+// requests differ and take one turn each, spread over the grid's z.
+//   k_adapters_few   few tokens: both products in one launch
+//   k_adapters_down  u_t = s_i A_i x_t, the columns split over the waves of a
+//                    block
+//   k_adapters_up    y_t += B_i u_t, or, for many tokens, k_adapters_up_many
 // What bounds it: x read once, y read and written once.  u stays in 32 bits:
-// it enters the matrix cores as a sum of 16-bit numbers, three of BF16 (8
-// significant bits each), or two of FP16 (11 each) after a scaling by a power
-// of two per token that brings its largest value to 2^14..2^15; products with
-// the 16-bit B are exact and summed in fp32, so y is rounded once, to its own
-// type.
+// it enters the matrix cores as a sum of 16-bit numbers, of BF16 or, after a
+// scaling by a power of two per token that brings its largest value to
+// 2^14..2^15, of FP16; products with the 16-bit B are exact and summed in
+// fp32, so y is rounded once, to its own type.
 //
 // MFMA 16x16x32 (lane l = 16 g + i): A operand row i, k = 8 g .. 8 g + 7;
 // B operand column i, the same k; D column i, rows 4 g .. 4 g + 3.  Here A is
@@ -23,11 +22,13 @@
 #pragma once
 
 #include "ops_common.hpp"
+#include "wc_common.hpp"
 
 namespace wc {
 namespace ops {
 
 constexpr uint32_t kAdapterMaxRank = 256;
+constexpr int kDownWaves = 8;
 
 struct AdapterArgs {
     const uint16_t *x;
@@ -39,9 +40,10 @@ struct AdapterArgs {
     const float *scales;    // n, or null: 1
     uint64_t m;
     uint32_t n, rank, cols, rows;
-    float *u;               // splits x m x padded rank
-    uint32_t rank_pad, splits, steps;  // steps: of 32 columns, per split
-    uint32_t row_block;                // rows of y per block of k_adapters_up
+    uint16_t *u;            // terms x m x rank_pad: k_adapters_down's result
+    float *unscale;         // m x rank blocks: what k_adapters_up multiplies its products by
+    uint32_t rank_pad;      // the rank rounded up to 32
+    uint32_t row_block;     // rows of y per block of k_adapters_up and k_adapters_few
     uint32_t *err;
 };
 
@@ -67,24 +69,84 @@ struct TileIds {
     {
         if (!pending) return false;
         adapter = (uint32_t)__builtin_amdgcn_readlane(id, __builtin_ctzll(pending));
+        take(adapter, mask);
+        return true;
+    }
+    // the tokens of an adapter
+    __device__ void take(uint32_t adapter, uint64_t &mask)
+    {
         mask = __ballot(id == (int32_t)adapter);
         pending &= ~mask;
-        return true;
     }
 };
 
-// u = s A x.  Grid: x = tiles x splits, y = blocks of 16 RT ranks, z = turns.
-template <int T, int TT, int RT>
-__global__ __launch_bounds__(256) void k_adapters_down(AdapterArgs g)
+// 32-bit numbers as sums of 16-bit ones.  BF16 (8 significant bits each):
+// three terms leave out less than 2^-24 of a number; for a 16-bit y, which
+// keeps 8 bits itself, two, which leave out 2^-16.  FP16 (11 each): two.
+template <int T, int YT>
+struct Terms;
+template <int YT>
+struct Terms<WC_T_BF16, YT> {
+    static constexpr int kCount = YT == WC_T_FP32 ? 3 : 2;
+    __device__ static void split(const float *f, bf16x8 *out)
+    {
+#pragma unroll
+        for (int e = 0; e < 8; e++) {
+            float v = f[e];
+#pragma unroll
+            for (int c = 0; c < kCount; c++) {
+                const __bf16 a = (__bf16)v;
+                out[c][e] = a;
+                v = fabsf((float)a) < kInf ? v - (float)a : 0.f;  // an infinity is its own first term
+            }
+        }
+    }
+};
+template <int YT>
+struct Terms<WC_T_FP16, YT> {
+    static constexpr int kCount = 2;
+    __device__ static void split(const float *f, f16x8 *out)
+    {
+#pragma unroll
+        for (int e = 0; e < 8; e++) {
+            const _Float16 a = (_Float16)f[e];
+            out[0][e] = a;
+            out[1][e] = (_Float16)(fabsf((float)a) < kInf ? f[e] - (float)a : 0.f);
+        }
+    }
+};
+
+// What FP16 values are multiplied by before they are split: the power of two
+// that brings `most`, the largest of them, to 2^14..2^15; its inverse in
+// `unscale`.  1 for BF16, whose range is that of FP32.
+template <int T>
+__device__ __forceinline__ float term_scale(float most, float &unscale)
 {
+    unscale = 1.f;
+    if (T != WC_T_FP16 || !(most > 0.f && most < kInf)) return 1.f;
+    const int ex = max(-100, min(100, 15 - __builtin_amdgcn_frexp_expf(most)));
+    unscale = __builtin_ldexpf(1.f, -ex);
+    return __builtin_ldexpf(1.f, ex);
+}
+
+// u = s A x, as terms.  Grid: x = tiles, y = blocks of 64 ranks (RT tiles of
+// 16), z = turns.  The columns go round the waves of the block.  Each XCD
+// takes a contiguous range of the tiles (xcd_block), so that the tiles of a
+// prompt find their A in one L2 cache; dealt out one by one, all eight caches
+// fetched every A, and that cost more than x (8192 tokens of 16 adapters,
+// 4096 columns, rank 64: 77 us).
+template <int T, int YT, int TT, int RT>
+__global__ __launch_bounds__(64 * kDownWaves, 2) void k_adapters_down(AdapterArgs g)
+{
+    constexpr int Q = 4;
     using Ty = Type<T>;
     using X8 = typename Ty::x8;
-    __shared__ f32x4 part[4][RT * TT][64];
+    constexpr int W = kDownWaves, kTerms = Terms<T, YT>::kCount, kPad = 16 * RT + 4;  // + 4: tokens in different banks
+    __shared__ f32x4 part[W][RT * TT][64];
+    __shared__ float su[16 * TT][kPad];
     const uint32_t wave = threadIdx.x >> 6, lane = threadIdx.x & 63, i = lane & 15, gr = lane >> 4;
-    const uint64_t tile = (uint64_t)(blockIdx.x / g.splits) * (16 * TT);
-    const uint32_t split = blockIdx.x % g.splits;
-    const uint32_t r0 = blockIdx.y * (16 * RT);
-    const uint32_t s0 = split * g.steps, s1 = min((g.cols + 31) / 32, s0 + g.steps), full = min(g.cols / 32, s1);
+    const uint64_t tile = (uint64_t)xcd_block() * (16 * TT);
+    const uint32_t r0 = blockIdx.y * 64, steps = (g.cols + 31) / 32;
     TileIds ids(g, tile, 16 * TT);
     const uint16_t *xr[TT];
 #pragma unroll
@@ -102,197 +164,479 @@ __global__ __launch_bounds__(256) void k_adapters_down(AdapterArgs g)
         for (int r = 0; r < RT; r++)
 #pragma unroll
             for (int t = 0; t < TT; t++) acc[r][t] = f32x4{0.f, 0.f, 0.f, 0.f};
-        auto step = [&](uint32_t st, bool in) {  // 32 columns; a lane's 8 are all there or all not
-            X8 av[RT], xv[TT];
-            const uint32_t k = 32 * st + 8 * gr;
+        // A step is 32 columns, of which a lane has 8: all there, or none.
+        // Four steps are on their way at once: x comes from memory, and a
+        // block per compute unit has registers to wait with.
+        for (uint32_t j = 0; wave_step<W>(wave, j) < steps; j += Q) {
+            X8 av[Q][RT], xv[Q][TT];
 #pragma unroll
-            for (int r = 0; r < RT; r++)
-                av[r] = __builtin_bit_cast(X8, in ? load16<16>(ar[r] + k) : u32x4{0u, 0u, 0u, 0u});
+            for (int q = 0; q < Q; q++) {
+                const uint32_t k = 32 * wave_step<W>(wave, j + q) + 8 * gr;
+                const bool in = k < g.cols;
 #pragma unroll
-            for (int t = 0; t < TT; t++)
-                xv[t] = __builtin_bit_cast(X8, in ? load16<16>(xr[t] + k) : u32x4{0u, 0u, 0u, 0u});
+                for (int t = 0; t < TT; t++)
+                    xv[q][t] = __builtin_bit_cast(X8, in ? load16<16>(xr[t] + k) : u32x4{0u, 0u, 0u, 0u});
 #pragma unroll
-            for (int r = 0; r < RT; r++)
+                for (int r = 0; r < RT; r++)
+                    av[q][r] = __builtin_bit_cast(X8, in ? load16<16>(ar[r] + k) : u32x4{0u, 0u, 0u, 0u});
+            }
 #pragma unroll
-                for (int t = 0; t < TT; t++) acc[r][t] = Ty::mfma(av[r], xv[t], acc[r][t]);
-        };
-        uint32_t st = s0 + wave;
-#pragma unroll 4
-        for (; st < full; st += 4) step(st, true);
-        if (st < s1) step(st, 32 * st + 8 * gr < g.cols);  // the columns' end is a multiple of 8, not of 32
+            for (int q = 0; q < Q; q++)
+#pragma unroll
+                for (int r = 0; r < RT; r++)
+#pragma unroll
+                    for (int t = 0; t < TT; t++) acc[r][t] = Ty::mfma(av[q][r], xv[q][t], acc[r][t]);
+        }
 #pragma unroll
         for (int r = 0; r < RT; r++)
 #pragma unroll
             for (int t = 0; t < TT; t++) part[wave][r * TT + t][lane] = acc[r][t];
         __syncthreads();
-        const float s = g.scales ? g.scales[adapter] : 1.f;
+        const float scale = g.scales ? g.scales[adapter] : 1.f;
+        for (uint32_t q = threadIdx.x; q < 64 * RT * TT; q += 64 * W) {  // four ranks of a token
+            const uint32_t c = q >> 6, l = q & 63, t = c % TT, r = 16 * (c / TT) + 4 * (l >> 4);
+            f32x4 v = part[0][c][l];
 #pragma unroll
-        for (int q = 0; q < (RT * TT + 3) / 4; q++) {
-            const uint32_t c = 4 * q + wave;
-            if (c < RT * TT) {
-                const uint32_t t = c % TT, row = r0 + 16 * (c / TT) + 4 * gr;
-                f32x4 v = (part[0][c][lane] + part[1][c][lane]) + (part[2][c][lane] + part[3][c][lane]);
+            for (int w = 1; w < W; w++) v += part[w][c][l];
 #pragma unroll
-                for (int e = 0; e < 4; e++) v[e] = row + e < g.rank ? s * v[e] : 0.f;
-                if (((mask >> (16 * t + i)) & 1) && row < g.rank_pad)
-                    *reinterpret_cast<f32x4 *>(g.u + ((uint64_t)split * g.m + tile + 16 * t + i) * g.rank_pad + row) = v;
-            }
+            for (int e = 0; e < 4; e++) su[16 * t + (l & 15)][r + e] = r0 + r + e < g.rank ? scale * v[e] : 0.f;
+        }
+        __syncthreads();
+        for (uint32_t q = threadIdx.x; q < 16 * TT * 2 * RT; q += 64 * W) {  // eight ranks of a token
+            const uint32_t t = q / (2 * RT), r = 8 * (q % (2 * RT));
+            if (!((mask >> t) & 1) || r0 + r >= g.rank_pad) continue;
+            float most = 0.f, unscale;
+            if constexpr (T == WC_T_FP16)
+                for (uint32_t e = 0; e < 16 * RT; e++) most = fmaxf(most, fabsf(su[t][e]));
+            const float sc = term_scale<T>(most, unscale);
+            float f[8];
+#pragma unroll
+            for (int e = 0; e < 8; e++) f[e] = sc * su[t][r + e];
+            X8 u[kTerms];
+            Terms<T, YT>::split(f, u);
+            const uint64_t at = (tile + t) * g.rank_pad + r0 + r;
+#pragma unroll
+            for (int c = 0; c < kTerms; c++)
+                *reinterpret_cast<u32x4 *>(g.u + c * g.m * g.rank_pad + at) = __builtin_bit_cast(u32x4, u[c]);
+            if (RT == 1)  // the rank's padding to 32
+                for (int c = 0; c < kTerms; c++)
+                    *reinterpret_cast<u32x4 *>(g.u + c * g.m * g.rank_pad + at + 16) = u32x4{0u, 0u, 0u, 0u};
+            if (r == 0) g.unscale[(tile + t) * gridDim.y + blockIdx.y] = unscale;
         }
         __syncthreads();
     }
 }
 
-// A 16-bit operand's 32-bit numbers as sums of 16-bit ones.
-template <int T>
-struct Terms;
-template <>
-struct Terms<WC_T_BF16> {
-    static constexpr int kCount = 3;
-    __device__ static void split(const float *f, bf16x8 *out)
-    {
+// The same within a wave: u of one token (32 KS values, those of the lane; the
+// lanes of a token are 16 apart) as terms.
+template <int T, int YT, int KS, int C>
+__device__ __forceinline__ float adapter_terms(float (&f)[KS][8], typename Type<T>::x8 (&u)[KS][C])
+{
+    float most = 0.f, unscale;
+    if constexpr (T == WC_T_FP16) {
 #pragma unroll
-        for (int e = 0; e < 8; e++) {
-            const __bf16 a = (__bf16)f[e];
-            const float r1 = fabsf((float)a) < kInf ? f[e] - (float)a : 0.f;  // an infinity is its own first term
-            const __bf16 b = (__bf16)r1;
-            out[0][e] = a;
-            out[1][e] = b;
-            out[2][e] = (__bf16)(r1 - (float)b);
+        for (int s = 0; s < KS; s++)
+#pragma unroll
+            for (int e = 0; e < 8; e++) most = fmaxf(most, fabsf(f[s][e]));
+        most = fmaxf(most, __shfl_xor(most, 16, 64));
+        most = fmaxf(most, __shfl_xor(most, 32, 64));
+    }
+    const float sc = term_scale<T>(most, unscale);
+#pragma unroll
+    for (int s = 0; s < KS; s++) {
+        if constexpr (T == WC_T_FP16)
+#pragma unroll
+            for (int e = 0; e < 8; e++) f[s][e] *= sc;
+        Terms<T, YT>::split(f[s], u[s]);
+    }
+    return unscale;
+}
+
+// 64 rows of B from nb as four operand tiles whose rows are dealt out so that
+// the four lanes of a token hold 64 bytes of its y side by side, 16 each: for
+// a 32-bit y, row i of tile p is row 16 p + i of the 64; for a 16-bit y, row
+// 32 (p / 2) + 8 (i / 4) + 4 (p % 2) + i % 4, and two tiles make 16 bytes.
+template <int YT>
+__device__ __forceinline__ uint32_t adapter_row(int p, uint32_t i)
+{
+    if constexpr (Type<YT>::kPer16 == 4) return 16 * p + i;
+    else return 32 * (p >> 1) + 8 * (i >> 2) + 4 * (p & 1) + (i & 3);
+}
+
+// Eight elements of B from `at`, as far as B goes and at most `have`.
+__device__ __noinline__ u32x4 b_end(const uint16_t *b, uint64_t at, uint64_t total, uint32_t have)
+{
+    u32x4 w{0u, 0u, 0u, 0u};
+#pragma unroll
+    for (uint32_t e = 0; e < 8; e++)
+        if (e < have && at + e < total) w[e >> 1] |= (uint32_t)b[at + e] << (16 * (e & 1));
+    return w;
+}
+
+// The rows of B of one adapter as operands.  A lane reads 16 bytes whatever
+// the rank, so that all loads of a wave are on their way at once, and clears
+// what is past the rank (it belongs to the rows behind); only where that
+// would run past the end of B are elements read one by one.
+template <int T, int YT, int KS>
+struct BRows {
+    const uint16_t *b;
+    uint64_t left;      // elements from b to the end of B
+    uint32_t keep[KS][4];
+    uint32_t off[KS];   // the lane's first rank, 0 where it is past the rank
+
+    __device__ __forceinline__ BRows(const AdapterArgs &g, uint32_t adapter, uint32_t k0)
+    {
+        b = g.b + (uint64_t)adapter * g.rows * g.rank;
+        left = (uint64_t)(g.n - adapter) * g.rows * g.rank;
+        const uint32_t gr = (threadIdx.x & 63) >> 4;
+#pragma unroll
+        for (int s = 0; s < KS; s++) {
+            const uint32_t k = k0 + 32 * s + 8 * gr, have = k < g.rank ? g.rank - k : 0u;
+            off[s] = have ? k : 0u;
+#pragma unroll
+            for (uint32_t e = 0; e < 4; e++) keep[s][e] = 2 * e + 1 < have ? ~0u : 2 * e < have ? 0xFFFFu : 0u;
         }
     }
-};
-template <>
-struct Terms<WC_T_FP16> {
-    static constexpr int kCount = 2;
-    __device__ static void split(const float *f, f16x8 *out)
+    // tile p of the 64 rows from nb
+    __device__ __forceinline__ void load(const AdapterArgs &g, uint32_t nb, int p, u32x4 (&v)[KS]) const
+    {
+        const bool end = left < (uint64_t)(min(nb + 64, g.rows) - 1) * g.rank + g.rank + 8;  // the same in all lanes
+        const uint32_t row = min(nb + adapter_row<YT>(p, threadIdx.x & 15), g.rows - 1) * g.rank;  // below 2^31
+#pragma unroll
+        for (int s = 0; s < KS; s++) v[s] = end ? b_end(b, row + off[s], left, 8) : load16<2>(b + (row + off[s]));
+    }
+    __device__ __forceinline__ u32x4 kept(u32x4 v, int s) const
     {
 #pragma unroll
-        for (int e = 0; e < 8; e++) {
-            const _Float16 a = (_Float16)f[e];
-            out[0][e] = a;
-            out[1][e] = (_Float16)(fabsf((float)a) < kInf ? f[e] - (float)a : 0.f);
+        for (int e = 0; e < 4; e++) v[e] &= keep[s][e];
+        return v;
+    }
+    __device__ __forceinline__ void load(const AdapterArgs &g, uint32_t nb, typename Type<T>::x8 (&bv)[4][KS]) const
+    {
+        u32x4 v[4][KS];
+#pragma unroll
+        for (int p = 0; p < 4; p++) load(g, nb, p, v[p]);
+#pragma unroll
+        for (int p = 0; p < 4; p++)
+#pragma unroll
+            for (int s = 0; s < KS; s++) bv[p][s] = __builtin_bit_cast(typename Type<T>::x8, kept(v[p][s], s));
+    }
+};
+
+// The lane's sixteen elements of 64 of a row of y from column n0: vectors of
+// 16 bytes, 64 bytes apart.
+template <int YT>
+struct YRow {
+    using Y = Type<YT>;
+    using E = typename Y::elem;
+    static constexpr int kPer = Y::kPer16, kVecs = 16 / kPer;
+    u32x4 v[kVecs];
+    __device__ __forceinline__ static uint32_t column(int q, uint32_t gr) { return (4 * q + gr) * kPer; }
+    __device__ __forceinline__ void load(const E *p, uint32_t gr)
+    {
+#pragma unroll
+        for (int q = 0; q < kVecs; q++) v[q] = load16<Y::kBytes>(p + column(q, gr));
+    }
+    __device__ __forceinline__ void add(E *p, uint32_t gr, const f32x4 (&acc)[4], float scale) const
+    {
+#pragma unroll
+        for (int q = 0; q < kVecs; q++) {
+            float f[kPer];
+            Y::unpack(v[q], f);
+#pragma unroll
+            for (int e = 0; e < kPer; e++) f[e] += acc[q * kPer / 4 + e / 4][e & 3] * scale;
+            store16<Y::kBytes>(p + column(q, gr), Y::pack(f));
         }
     }
 };
 
+// The same where the row ends within the 64, after `count`.
+template <int YT>
+__device__ __noinline__ void y_add_some(typename Type<YT>::elem *p, uint32_t gr, uint32_t count, f32x4 a0, f32x4 a1,
+                                        f32x4 a2, f32x4 a3, float scale)
+{
+    using Y = Type<YT>;
+    const f32x4 acc[4] = {a0, a1, a2, a3};
+#pragma unroll
+    for (int q = 0; q < YRow<YT>::kVecs; q++)
+#pragma unroll
+        for (int e = 0; e < Y::kPer16; e++) {
+            const uint32_t n = YRow<YT>::column(q, gr) + e;
+            if (n < count) p[n] = Y::from_f32(Y::to_f32(p[n]) + acc[q * Y::kPer16 / 4 + e / 4][e & 3] * scale);
+        }
+}
+
 // y += B u.  Grid: x = tiles x row blocks, z = turns.  A wave takes 64 rows
-// at a time as four tiles whose rows are dealt out so that a lane ends with
-// 16 consecutive elements of its token's y: row i of tile p is row
-// 16 (i / 4) + 4 p + i % 4 of the 64.
-template <int T, int YT, int TT, int KS>
+// of B at a time; u stays in its registers, or, with kBlocks blocks of 64
+// ranks (each with its own scaling), is read again for every 64 rows.
+template <int T, int YT, int KS, bool kBlocks>
 __global__ __launch_bounds__(256) void k_adapters_up(AdapterArgs g)
 {
+    constexpr int TT = 1;
     using Ty = Type<T>;
-    using Y = Type<YT>;
-    using YE = typename Y::elem;
+    using YE = typename Type<YT>::elem;
     using X8 = typename Ty::x8;
-    constexpr int kTerms = Terms<T>::kCount, kYVecs = 16 / Y::kPer16;
+    constexpr int kTerms = Terms<T, YT>::kCount;
     const uint32_t wave = threadIdx.x >> 6, lane = threadIdx.x & 63, i = lane & 15, gr = lane >> 4;
-    const uint32_t row_blocks = (g.rows + g.row_block - 1) / g.row_block;
+    const uint32_t row_blocks = (g.rows + g.row_block - 1) / g.row_block, rank_blocks = kBlocks ? (g.rank_pad + 63) / 64 : 1;
     const uint64_t tile = (uint64_t)(blockIdx.x / row_blocks) * (16 * TT);
     const uint32_t n0 = (blockIdx.x % row_blocks) * g.row_block, n1 = min(g.rows, n0 + g.row_block);
     TileIds ids(g, tile, 16 * TT);
+    uint64_t token[TT];
+    YE *yr[TT];
+#pragma unroll
+    for (int t = 0; t < TT; t++) {
+        token[t] = min(tile + 16 * t + i, g.m - 1);
+        yr[t] = static_cast<YE *>(g.y) + token[t] * g.y_stride;
+    }
     uint32_t adapter, turn = 0;
     uint64_t mask;
     while (ids.next(adapter, mask)) {
         if (turn++ % gridDim.z != blockIdx.z) continue;
         X8 u[TT][KS][kTerms];
         float unscale[TT];
-#pragma unroll
-        for (int t = 0; t < TT; t++) {
-            const uint64_t token = min(tile + 16 * t + i, g.m - 1);
-            float f[KS][8];
-            float most = 0.f;
-#pragma unroll
-            for (int s = 0; s < KS; s++) {
-                const uint32_t k = 32 * s + 8 * gr;
-#pragma unroll
-                for (int e = 0; e < 8; e++) f[s][e] = 0.f;
-                if (k < g.rank_pad && ((mask >> (16 * t + i)) & 1)) {
-                    for (uint32_t sp = 0; sp < g.splits; sp++) {
-                        const float *p = g.u + ((uint64_t)sp * g.m + token) * g.rank_pad + k;
-                        const f32x4 v = *reinterpret_cast<const f32x4 *>(p), w = *reinterpret_cast<const f32x4 *>(p + 4);
-#pragma unroll
-                        for (int e = 0; e < 4; e++) {
-                            f[s][e] += v[e];
-                            f[s][4 + e] += w[e];
-                        }
-                    }
-                }
-#pragma unroll
-                for (int e = 0; e < 8; e++) most = fmaxf(most, fabsf(f[s][e]));
-            }
-            unscale[t] = 1.f;
-            if constexpr (T == WC_T_FP16) {
-                most = fmaxf(most, __shfl_xor(most, 16, 64));
-                most = fmaxf(most, __shfl_xor(most, 32, 64));
-                if (most > 0.f && most < kInf) {
-                    const int ex = max(-100, min(100, 15 - __builtin_amdgcn_frexp_expf(most)));
-                    unscale[t] = __builtin_ldexpf(1.f, -ex);
-#pragma unroll
-                    for (int s = 0; s < KS; s++)
-#pragma unroll
-                        for (int e = 0; e < 8; e++) f[s][e] = __builtin_ldexpf(f[s][e], ex);
-                }
-            }
-#pragma unroll
-            for (int s = 0; s < KS; s++) Terms<T>::split(f[s], u[t][s]);
-        }
-        const uint16_t *b = g.b + (uint64_t)adapter * g.rows * g.rank;
-        for (uint32_t nb = n0 + 64 * wave; nb < n1; nb += 256) {
-            X8 bv[4][KS];
-#pragma unroll
-            for (int p = 0; p < 4; p++) {
-                const uint32_t row = min(nb + 16 * (i >> 2) + 4 * p + (i & 3), g.rows - 1);
-                const uint16_t *br = b + (uint64_t)row * g.rank;
-#pragma unroll
-                for (int s = 0; s < KS; s++) {
-                    const uint32_t k = 32 * s + 8 * gr;
-                    u32x4 v{0u, 0u, 0u, 0u};
-                    if (k + 8 <= g.rank) {
-                        v = load16<2>(br + k);
-                    } else {
-                        for (uint32_t e = 0; e < 8; e++)
-                            if (k + e < g.rank) v[e >> 1] |= (uint32_t)br[k + e] << (16 * (e & 1));
-                    }
-                    bv[p][s] = __builtin_bit_cast(X8, v);
-                }
-            }
-            const uint32_t n = nb + 16 * gr;
+        // every lane reads its column's u, also of a token that is another adapter's (then it is dropped)
+        auto fetch_u = [&](uint32_t rb) {
 #pragma unroll
             for (int t = 0; t < TT; t++) {
-                if (!((mask >> (16 * t)) & 0xFFFFu)) continue;
-                const bool mine = (mask >> (16 * t + i)) & 1;
-                YE *yp = static_cast<YE *>(g.y) + (tile + 16 * t + i) * g.y_stride + n;
-                float f[16];
-                const bool whole = mine && n + 16 <= n1;
-                if (whole) {
 #pragma unroll
-                    for (int v = 0; v < kYVecs; v++)
-                        Y::unpack(load16<Y::kBytes>(yp + v * Y::kPer16), f + v * Y::kPer16);
+                for (int s = 0; s < KS; s++)
+#pragma unroll
+                    for (int c = 0; c < kTerms; c++) {
+                        const uint32_t k = min(64 * rb + 32 * s, g.rank_pad - 32) + 8 * gr;  // past it B is zero
+                        u[t][s][c] = __builtin_bit_cast(X8, load16<16>(g.u + (c * g.m + token[t]) * g.rank_pad + k));
+                    }
+                unscale[t] = T == WC_T_FP16 ? g.unscale[token[t] * rank_blocks + rb] : 1.f;
+            }
+        };
+        fetch_u(0);
+        const BRows<T, YT, KS> rows(g, adapter, 0);
+        for (uint32_t nb = n0 + 64 * wave; nb < n1; nb += 256) {
+            X8 bv[4][KS];
+            YRow<YT> y[TT];
+            const bool whole = nb + 64 <= n1;
+            // all of the tile's y is on its way before the first store, which the compiler may not move loads past
+            if (whole) {
+#pragma unroll
+                for (int t = 0; t < TT; t++) y[t].load(yr[t] + nb, gr);
+            }
+            rows.load(g, nb, bv);
+#pragma unroll
+            for (int t = 0; t < TT; t++) {
+                f32x4 sum[4];
+                for (uint32_t rb = 0; rb < rank_blocks; rb++) {
+                    if (kBlocks && rb) BRows<T, YT, KS>(g, adapter, 64 * rb).load(g, nb, bv);
+                    if (kBlocks) fetch_u(rb);
+#pragma unroll
+                    for (int p = 0; p < 4; p++) {
+                        f32x4 acc{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                        for (int s = 0; s < KS; s++)
+#pragma unroll
+                            for (int c = kTerms - 1; c >= 0; c--) acc = Ty::mfma(bv[p][s], u[t][s][c], acc);
+                        if (!kBlocks) sum[p] = acc;
+                        else sum[p] = rb ? sum[p] + unscale[t] * acc : unscale[t] * acc;
+                    }
                 }
-                f32x4 acc[4];
-#pragma unroll
-                for (int p = 0; p < 4; p++) {
-                    acc[p] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                    for (int s = 0; s < KS; s++)
-#pragma unroll
-                        for (int c = kTerms - 1; c >= 0; c--) acc[p] = Ty::mfma(bv[p][s], u[t][s][c], acc[p]);
-                }
-                if (whole) {
-#pragma unroll
-                    for (int e = 0; e < 16; e++) f[e] += acc[e >> 2][e & 3] * unscale[t];
-#pragma unroll
-                    for (int v = 0; v < kYVecs; v++)
-                        store16<Y::kBytes>(yp + v * Y::kPer16, Y::pack(f + v * Y::kPer16));
-                } else if (mine) {
-#pragma unroll
-                    for (int e = 0; e < 16; e++)
-                        if (n + e < n1) yp[e] = Y::from_f32(Y::to_f32(yp[e]) + acc[e >> 2][e & 3] * unscale[t]);
-                }
+                if (!((mask >> (16 * t + i)) & 1)) continue;
+                if (whole) y[t].add(yr[t] + nb, gr, sum, kBlocks ? 1.f : unscale[t]);
+                else y_add_some<YT>(yr[t] + nb, gr, n1 - nb, sum[0], sum[1], sum[2], sum[3], kBlocks ? 1.f : unscale[t]);
             }
         }
+    }
+}
+
+// y += B u for many tokens and ranks up to 64.  Grid: x = tiles of 128 tokens
+// x row blocks.  The four waves of a block take 32 tokens each and the same
+// 64 rows of B, which reach them through LDS in operand order: B would
+// otherwise pass through the L1 cache once per 32 tokens, twice as many bytes
+// as y, and how much can be on its way into that cache is what bounds a
+// kernel that only streams.
+template <int T, int YT, int KS>
+__global__ __launch_bounds__(256, 4) void k_adapters_up_many(AdapterArgs g)
+{
+    using Ty = Type<T>;
+    using YE = typename Type<YT>::elem;
+    using X8 = typename Ty::x8;
+    constexpr int kTerms = Terms<T, YT>::kCount, TT = 2;
+    __shared__ u32x4 sb[2][4][KS][64];
+    const uint32_t wave = threadIdx.x >> 6, lane = threadIdx.x & 63, i = lane & 15, gr = lane >> 4;
+    const uint32_t row_blocks = (g.rows + g.row_block - 1) / g.row_block;
+    const uint32_t block = xcd_block();
+    const uint64_t tile = (uint64_t)(block / row_blocks) * 128;
+    const uint32_t n0 = (block % row_blocks) * g.row_block, n1 = min(g.rows, n0 + g.row_block);
+    TileIds low(g, tile, 64), high(g, tile + 64, 64);
+    uint64_t token[TT];
+    YE *yr[TT];
+#pragma unroll
+    for (int t = 0; t < TT; t++) {
+        token[t] = min(tile + 32 * wave + 16 * t + i, g.m - 1);
+        yr[t] = static_cast<YE *>(g.y) + token[t] * g.y_stride;
+    }
+    uint64_t mlow, mhigh;
+    uint32_t adapter;
+    while (low.pending | high.pending) {
+        if (low.next(adapter, mlow)) {
+            high.take(adapter, mhigh);
+        } else {
+            mlow = 0;
+            high.next(adapter, mhigh);
+        }
+        const uint32_t mask = (uint32_t)((wave & 2 ? mhigh : mlow) >> (32 * (wave & 1)));
+        X8 u[TT][KS][kTerms];
+        float unscale[TT];
+        bool mine[TT];
+#pragma unroll
+        for (int t = 0; t < TT; t++) {
+            mine[t] = (mask >> (16 * t + i)) & 1;
+#pragma unroll
+            for (int s = 0; s < KS; s++)
+#pragma unroll
+                for (int c = 0; c < kTerms; c++)
+                    u[t][s][c] = __builtin_bit_cast(X8, load16<16>(g.u + (c * g.m + token[t]) * g.rank_pad + 32 * s + 8 * gr));
+            unscale[t] = T == WC_T_FP16 ? g.unscale[token[t]] : 1.f;
+        }
+        const BRows<T, YT, KS> rows(g, adapter, 0);
+        u32x4 nextb[KS];
+        rows.load(g, n0, (int)wave, nextb);
+        uint32_t turn = 0;
+        for (uint32_t nb = n0; nb < n1; nb += 64, turn ^= 1) {
+            YRow<YT> y[TT];
+            if (mask && nb + 64 <= n1) {
+#pragma unroll
+                for (int t = 0; t < TT; t++) y[t].load(yr[t] + nb, gr);
+            }
+#pragma unroll
+            for (int s = 0; s < KS; s++) sb[turn][wave][s][lane] = rows.kept(nextb[s], s);
+            __syncthreads();  // the other buffer's last readers passed the barrier before this one
+            if (nb + 64 < n1) rows.load(g, nb + 64, (int)wave, nextb);
+            if (!mask) continue;
+#pragma unroll
+            for (int t = 0; t < TT; t++) {
+                f32x4 sum[4];
+#pragma unroll
+                for (int p = 0; p < 4; p++) {
+                    sum[p] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                    for (int s = 0; s < KS; s++) {
+                        const X8 bv = __builtin_bit_cast(X8, sb[turn][p][s][lane]);
+#pragma unroll
+                        for (int c = kTerms - 1; c >= 0; c--) sum[p] = Ty::mfma(bv, u[t][s][c], sum[p]);
+                    }
+                }
+                if (mine[t]) {
+                    if (nb + 64 <= n1) y[t].add(yr[t] + nb, gr, sum, unscale[t]);
+                    else y_add_some<YT>(yr[t] + nb, gr, n1 - nb, sum[0], sum[1], sum[2], sum[3], unscale[t]);
+                }
+                __builtin_amdgcn_sched_barrier(0);  // one tile's sums at a time: registers for four waves
+            }
+        }
+        __syncthreads();
+    }
+}
+
+// Both products in one launch, for few tokens: every block of 1,024 rows (or
+// a few times that) works out u for itself, its sixteen waves sharing the
+// columns, while its first rows of B and y are on their way.  The row blocks
+// of a tile's turn are on one XCD (blocks are dealt to the XCDs in the order
+// of their number), where A comes from the L2 cache after the first of them.
+// Grid: turns x tiles of 16 tokens, rounded up to 8, x row blocks.
+template <int T, int YT, int RT>
+__global__ __launch_bounds__(1024) void k_adapters_few(AdapterArgs g)
+{
+    using Ty = Type<T>;
+    using YE = typename Type<YT>::elem;
+    using X8 = typename Ty::x8;
+    constexpr int kTerms = Terms<T, YT>::kCount, KS = (RT + 1) / 2, Q = RT == 4 ? 1 : 4;
+    constexpr int kPad = 32 * KS + 4;  // + 4: tokens in different banks
+    __shared__ f32x4 part[16][RT][64];
+    __shared__ float su[16][kPad];
+    const uint32_t wave = threadIdx.x >> 6, lane = threadIdx.x & 63, i = lane & 15, gr = lane >> 4;
+    const uint32_t row_blocks = (g.rows + g.row_block - 1) / g.row_block;
+    const uint32_t tiles = (uint32_t)((g.m + 15) / 16), slot = blockIdx.x / 8;
+    const uint32_t pair = slot / row_blocks * 8 + blockIdx.x % 8;  // of a turn and a tile
+    const uint64_t tile = (uint64_t)(pair % tiles) * 16;
+    const uint32_t n0 = (slot % row_blocks) * g.row_block, n1 = min(g.rows, n0 + g.row_block);
+    TileIds ids(g, tile, 16);
+    uint32_t adapter;
+    uint64_t mask;
+    for (uint32_t turn = 0;; turn++) {
+        if (!ids.next(adapter, mask)) return;
+        if (turn == pair / tiles) break;
+    }
+    const bool mine = (mask >> i) & 1;
+    // lanes of other tokens repeat the first one's loads
+    const uint64_t token = tile + (mine ? i : (uint32_t)__builtin_ctzll(mask));
+    YE *yr = static_cast<YE *>(g.y) + token * g.y_stride;
+    uint32_t nb = n0 + 64 * wave;
+    YRow<YT> y;
+    X8 bv[4][KS];
+    const BRows<T, YT, KS> rows(g, adapter, 0);
+    auto fetch = [&]() {
+        if (mine && nb + 64 <= n1) y.load(yr + nb, gr);
+        rows.load(g, nb, bv);
+    };
+    if (nb < n1) fetch();
+    const uint16_t *xr = g.x + token * g.x_stride;
+    const uint16_t *ar[RT];
+    f32x4 acc[RT];
+#pragma unroll
+    for (int r = 0; r < RT; r++) {
+        ar[r] = g.a + ((uint64_t)adapter * g.rank + min(16 * r + i, g.rank - 1)) * g.cols;
+        acc[r] = f32x4{0.f, 0.f, 0.f, 0.f};
+    }
+    for (uint32_t j = 0; 32 * wave_step<16>(wave, j) < g.cols; j += Q) {
+        X8 av[Q][RT], xv[Q];
+#pragma unroll
+        for (int q = 0; q < Q; q++) {
+            const uint32_t k = 32 * wave_step<16>(wave, j + q) + 8 * gr;
+            const bool in = k < g.cols;
+            xv[q] = __builtin_bit_cast(X8, in ? load16<16>(xr + k) : u32x4{0u, 0u, 0u, 0u});
+#pragma unroll
+            for (int r = 0; r < RT; r++)
+                av[q][r] = __builtin_bit_cast(X8, in ? load16<16>(ar[r] + k) : u32x4{0u, 0u, 0u, 0u});
+        }
+#pragma unroll
+        for (int q = 0; q < Q; q++)
+#pragma unroll
+            for (int r = 0; r < RT; r++) acc[r] = Ty::mfma(av[q][r], xv[q], acc[r]);
+    }
+#pragma unroll
+    for (int r = 0; r < RT; r++) part[wave][r][lane] = acc[r];
+    __syncthreads();
+    if (threadIdx.x < 256 * RT) {  // a thread per token and rank: element e of lane l of tile r
+        const uint32_t r = threadIdx.x >> 8, l = (threadIdx.x >> 2) & 63, e = threadIdx.x & 3;
+        const uint32_t rank = 16 * r + 4 * (l >> 4) + e;
+        float v = 0.f;
+#pragma unroll
+        for (int w = 0; w < 16; w++) v += part[w][r][l][e];
+        su[l & 15][rank] = rank < g.rank ? v * (g.scales ? g.scales[adapter] : 1.f) : 0.f;
+    }
+    __syncthreads();
+    float f[KS][8];
+#pragma unroll
+    for (int s = 0; s < KS; s++)
+#pragma unroll
+        for (int e = 0; e < 8; e++) {
+            const uint32_t k = 32 * s + 8 * gr + e;
+            f[s][e] = mine && k < 16 * RT ? su[i][k] : 0.f;
+        }
+    X8 u[KS][kTerms];
+    const float unscale = adapter_terms<T, YT, KS>(f, u);
+    while (nb < n1) {
+        f32x4 d[4];
+#pragma unroll
+        for (int p = 0; p < 4; p++) {
+            d[p] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int s = 0; s < KS; s++)
+#pragma unroll
+                for (int c = kTerms - 1; c >= 0; c--) d[p] = Ty::mfma(bv[p][s], u[s][c], d[p]);
+        }
+        if (mine && nb + 64 <= n1) y.add(yr + nb, gr, d, unscale);
+        else if (mine) y_add_some<YT>(yr + nb, gr, n1 - nb, d[0], d[1], d[2], d[3], unscale);
+        nb += 1024;
+        if (nb < n1) fetch();
     }
 }
 

@@ -12,8 +12,9 @@
 // With the row's M, S, W: lse = M + ln S, H = ln S - ln 2 W / S.
 //
 // The alternatives need no sort of the row.  Let T be the n-th largest of
-// the 256 threads' maxima: at least n logits are >= T, so every logit among
-// the n largest is >= T.  The largest logit of every batch is kept in LDS, so
+// the maxima of 256 classes of threads: at least n logits are >= T, so every
+// logit among the n largest is >= T (so a T a little lower does as well).
+// The largest logit of every batch is kept in LDS, so
 // the logits >= T are found by looking again at the batches whose maximum is
 // >= T only (about n of V / 32), and ranked by counting.  Rows with so many
 // equal logits that the lists overflow take the scan of top_slow.
@@ -27,12 +28,11 @@
 namespace wc {
 namespace ops {
 
-constexpr uint32_t kRowThreads = 256;
+constexpr uint32_t kJoinThreads = 256;
 constexpr uint32_t kBatch = 32;                          // logits a thread takes per round
-constexpr uint32_t kSweep = kRowThreads * kBatch;        // logits of a round of the block
 constexpr uint32_t kMaxSlice = 131072;                   // logits of one block
 constexpr uint32_t kMaxSlices = 64;                      // blocks of one row
-constexpr uint32_t kMinSlice = 2048;
+constexpr uint32_t kClasses = 256;                       // groups of threads whose maxima give the threshold
 constexpr uint32_t kMaxTop = 64;
 constexpr uint32_t kMaxVocab = kMaxSlice * kMaxSlices / 2;
 constexpr uint32_t kListCap = 1024;                      // candidates ranked by counting
@@ -58,56 +58,81 @@ __device__ __forceinline__ Stat merge(Stat a, Stat b)
     return Stat{m, a.s + b.s, a.w + b.w};
 }
 
-template <bool kTop, bool kSlice>
+template <bool kTop, bool kSlice, int NT_>
 struct RowShared {
+    static constexpr uint32_t NT = NT_;  // threads of the block
     uint64_t list[kTop ? kListCap : 1];                               // candidates: key << 32 | ~index
-    uint32_t batch_max[kTop && kSlice ? kMaxSlice / kBatch : 1];      // bits of the largest logit of batch 256 i + thread
+    uint32_t batch_max[kTop && kSlice ? kMaxSlice / kBatch : 1];      // bits of the largest logit of batch NT i + thread
     uint32_t hits[kTop && kSlice ? kListCap : 1];                     // batches to look at again
-    uint32_t keys[kTop && kSlice ? kRowThreads : 4];
-    float part[3 * (kRowThreads / 64)];
+    uint32_t keys[kTop && kSlice ? kClasses : 4];
+    float part[3 * (NT / 64)];
     uint64_t thresh64;
-    uint32_t thresh, n_list, n_hits, wave_count[kRowThreads / 64];
+    uint32_t thresh, n_list, n_hits, wave_count[NT / 64];
 };
 
 __device__ __forceinline__ uint64_t entry(uint32_t key, uint32_t index) { return ((uint64_t)key << 32) | (uint32_t)~index; }
+
+// The wave's statistics, in every lane.
+__device__ __forceinline__ Stat wave_stat(Stat a)
+{
+    raise(a, wave_max(a.m));
+    return Stat{a.m, wave_sum(a.s), wave_sum(a.w)};
+}
 
 // The block's statistics, in every thread.
 template <class Sh>
 __device__ inline Stat block_stat(Stat a, Sh &sh)
 {
-    for (int o = 32; o; o >>= 1) {
-        const Stat b{__shfl_xor(a.m, o, 64), __shfl_xor(a.s, o, 64), __shfl_xor(a.w, o, 64)};
-        a = merge(a, b);
-    }
-    const uint32_t wave = threadIdx.x >> 6;
-    if ((threadIdx.x & 63) == 0) {
+    const uint32_t wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+    a = wave_stat(a);
+    if (lane == 0) {
         sh.part[3 * wave] = a.m;
         sh.part[3 * wave + 1] = a.s;
         sh.part[3 * wave + 2] = a.w;
     }
     __syncthreads();
-    a = Stat{sh.part[0], sh.part[1], sh.part[2]};
-    for (uint32_t i = 1; i < kRowThreads / 64; i++)
-        a = merge(a, Stat{sh.part[3 * i], sh.part[3 * i + 1], sh.part[3 * i + 2]});
-    return a;
+    a = Stat{-kInf, 0.f, 0.f};
+    if (lane < Sh::NT / 64) a = Stat{sh.part[3 * lane], sh.part[3 * lane + 1], sh.part[3 * lane + 2]};
+    return wave_stat(a);
 }
 
-// The n-th largest of the keys that every thread gives one of (the smallest
-// if fewer than n are not 0), in every thread.
+// A key that at least n of the 256 classes of threads reach (0 if fewer than
+// n have one), and hardly more: the n-th largest, or a lower one if at most
+// 64 and n + 8 classes reach it.  A class is a thread, or four threads side by
+// side, and its key the largest of theirs.  Found by bisection between the
+// smallest and the largest, every wave counting all classes by itself.
 template <class Sh>
 __device__ inline uint32_t nth_key(uint32_t key, uint32_t n, Sh &sh)
 {
-    sh.keys[threadIdx.x] = key;
-    if (threadIdx.x == 0) sh.thresh = ~0u;
-    __syncthreads();
-    uint32_t above = 0;
-    for (uint32_t i = 0; i < kRowThreads; i += 4) {
-        const u32x4 k = *reinterpret_cast<const u32x4 *>(&sh.keys[i]);
-        above += (k[0] > key) + (k[1] > key) + (k[2] > key) + (k[3] > key);
+    constexpr uint32_t kPer = Sh::NT / kClasses;
+    if constexpr (kPer == 4) {
+        key = max(key, lanes_moved<0xB1, 0xF>(key, 0u));  // lanes 1 0 3 2 of each four
+        key = max(key, lanes_moved<0x4E, 0xF>(key, 0u));  // lanes 2 3 0 1
     }
-    if (above < n) atomicMin(&sh.thresh, key);
+    static_assert(kPer == 1 || kPer == 4, "classes");
+    if (threadIdx.x % kPer == 0) sh.keys[threadIdx.x / kPer] = key;
     __syncthreads();
-    return lds_uniform(sh.thresh);
+    const u32x4 k = *reinterpret_cast<const u32x4 *>(&sh.keys[4 * (threadIdx.x & 63)]);
+    auto reach = [&](uint32_t c) {
+        return (uint32_t)(__popcll(__ballot(k[0] >= c)) + __popcll(__ballot(k[1] >= c)) +
+                          __popcll(__ballot(k[2] >= c)) + __popcll(__ballot(k[3] >= c)));
+    };
+    const uint32_t few = min(n + 8, 64u);
+    uint32_t count = reach(1u);
+    if (count < n) return 0;
+    // none of the keys is below lo but 0; count classes reach lo, fewer than n reach hi + 1
+    uint32_t lo = wave_min(min(min(k[0] - 1, k[1] - 1), min(k[2] - 1, k[3] - 1))) + 1;
+    uint32_t hi = ~wave_min(min(min(~k[0], ~k[1]), min(~k[2], ~k[3])));
+    while (count > few && lo < hi) {
+        const uint32_t mid = lo + (hi - lo + 1) / 2, c = reach(mid);
+        if (c >= n) {
+            lo = mid;
+            count = c;
+        } else {
+            hi = mid - 1;
+        }
+    }
+    return lo;
 }
 
 // Writes the n largest entries of the list, in order; fewer entries than n
@@ -115,13 +140,14 @@ __device__ inline uint32_t nth_key(uint32_t key, uint32_t n, Sh &sh)
 template <class Sh, class Put>
 __device__ inline void rank_list(uint32_t count, uint32_t n, const Sh &sh, Put put)
 {
-    for (uint32_t i = threadIdx.x; i < count; i += kRowThreads) {
+    for (uint32_t i = threadIdx.x; i < count; i += Sh::NT) {
         const uint64_t mine = sh.list[i];
         uint32_t above = 0;
+#pragma unroll 4
         for (uint32_t j = 0; j < count; j++) above += sh.list[j] > mine;
         if (above < n) put(above, mine);
     }
-    for (uint32_t i = count + threadIdx.x; i < n; i += kRowThreads) put(i, 0ull);
+    for (uint32_t i = count + threadIdx.x; i < n; i += Sh::NT) put(i, 0ull);
 }
 
 // Adds to the list, in the order of the index, the first elements of
@@ -131,14 +157,14 @@ __device__ inline uint32_t fill_equal(const typename Type<T>::elem *row, uint32_
                                       uint32_t count, uint32_t key, Sh &sh)
 {
     const uint32_t wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-    for (uint32_t j0 = lo; count < n && j0 < hi; j0 += kRowThreads) {
+    for (uint32_t j0 = lo; count < n && j0 < hi; j0 += Sh::NT) {
         const uint32_t j = j0 + threadIdx.x;
         const bool eq = j < hi && key_of(Type<T>::to_f32(row[j])) == key;
         const uint64_t votes = __ballot(eq);
         if (lane == 0) sh.wave_count[wave] = (uint32_t)__popcll(votes);
         __syncthreads();
         uint32_t at = count + (uint32_t)__popcll(votes & ((1ull << lane) - 1)), total = 0;
-        for (uint32_t i = 0; i < kRowThreads / 64; i++) {
+        for (uint32_t i = 0; i < Sh::NT / 64; i++) {
             if (i < wave) at += sh.wave_count[i];
             total += sh.wave_count[i];
         }
@@ -165,7 +191,7 @@ __device__ __noinline__ uint32_t top_slow(const typename Type<T>::elem *row, uin
             sh.thresh = ~0u;
         }
         __syncthreads();
-        for (uint32_t j = lo + threadIdx.x; j < hi; j += kRowThreads) {
+        for (uint32_t j = lo + threadIdx.x; j < hi; j += Sh::NT) {
             const uint32_t key = key_of(Type<T>::to_f32(row[j]));
             if (key > thresh) {
                 const uint32_t at = atomicAdd(&sh.n_list, 1u);
@@ -175,7 +201,7 @@ __device__ __noinline__ uint32_t top_slow(const typename Type<T>::elem *row, uin
         __syncthreads();
         const uint32_t count = lds_uniform(sh.n_list);
         if (count <= kListCap) return fill_equal<T>(row, lo, hi, n, count, thresh, sh);
-        for (uint32_t i = threadIdx.x; i < kListCap; i += kRowThreads) {
+        for (uint32_t i = threadIdx.x; i < kListCap; i += Sh::NT) {
             const uint32_t key = (uint32_t)(sh.list[i] >> 32);
             uint32_t above = 0;
             for (uint32_t j = 0; j < kListCap; j++) above += (uint32_t)(sh.list[j] >> 32) > key;
@@ -193,33 +219,61 @@ __device__ inline bool collect(const typename Type<T>::elem *row, uint32_t lo, u
                                uint32_t limit, Sh &sh)
 {
     using Ty = Type<T>;
-    constexpr uint32_t kPer = Ty::kPer16, kVecs = kBatch / kPer;
+    constexpr uint32_t kPer = Ty::kPer16, kVecs = kBatch / kPer, kSweep = Sh::NT * kBatch;
     const uint32_t tid = threadIdx.x;
     __syncthreads();
     if (tid == 0) sh.n_list = sh.n_hits = 0;
     __syncthreads();
+#pragma unroll 4
     for (uint32_t i = 0; i < rounds; i++) {
-        if (key_of(__builtin_bit_cast(float, sh.batch_max[kRowThreads * i + tid])) >= limit) {
+        if (key_of(__builtin_bit_cast(float, sh.batch_max[Sh::NT * i + tid])) >= limit) {
             const uint32_t at = atomicAdd(&sh.n_hits, 1u);
-            if (at < kListCap) sh.hits[at] = kRowThreads * i + tid;
+            if (at < kListCap) sh.hits[at] = Sh::NT * i + tid;
         }
     }
     __syncthreads();
     const uint32_t hits = lds_uniform(sh.n_hits);
     if (hits > kListCap) return false;
-    for (uint32_t i = tid; i < hits * kVecs; i += kRowThreads) {
+    for (uint32_t i = tid; i < hits * kVecs; i += Sh::NT) {
         const uint32_t b = sh.hits[i / kVecs];
-        const uint32_t j = lo + (b / kRowThreads) * kSweep + (kRowThreads * (i % kVecs) + b % kRowThreads) * kPer;
-        for (uint32_t q = 0; q < kPer; q++) {
-            const uint32_t key = j + q < hi ? key_of(Ty::to_f32(row[j + q])) : 0u;
-            if (key >= limit) {
-                const uint32_t at = atomicAdd(&sh.n_list, 1u);
-                if (at < kListCap) sh.list[at] = entry(key, j + q);
-            }
+        const uint32_t j = lo + (b / Sh::NT) * kSweep + (Sh::NT * (i % kVecs) + b % Sh::NT) * kPer;
+        float f[kPer];
+        if (j + kPer <= hi) {
+            Ty::unpack(load16<Ty::kBytes>(row + j), f);
+        } else {
+#pragma unroll
+            for (uint32_t q = 0; q < kPer; q++) f[q] = j + q < hi ? Ty::to_f32(row[j + q]) : 0.f;
+        }
+        uint32_t has = 0;
+#pragma unroll
+        for (uint32_t q = 0; q < kPer; q++) has |= (j + q < hi && key_of(f[q]) >= limit) ? 1u << q : 0u;
+        if (has) {
+            uint32_t at = atomicAdd(&sh.n_list, (uint32_t)__popc(has));
+#pragma unroll
+            for (uint32_t q = 0; q < kPer; q++)
+                if ((has >> q) & 1) {
+                    if (at < kListCap) sh.list[at] = entry(key_of(f[q]), j + q);
+                    at++;
+                }
         }
     }
     __syncthreads();
     return lds_uniform(sh.n_list) <= kListCap;
+}
+
+// The candidates of a slice where many logits equal the threshold (a masked
+// row), or fewer than n are above -inf: those above it (in the batches of at
+// most 64 classes, 16 of each), then the first that equal it, then NaN.
+template <int T, class Sh>
+__device__ __noinline__ uint32_t candidates_many(const typename Type<T>::elem *row, uint32_t lo, uint32_t hi,
+                                                 uint32_t rounds, uint32_t thresh, uint32_t n, Sh &sh)
+{
+    if (!collect<T>(row, lo, hi, rounds, thresh + 1, sh)) return top_slow<T>(row, lo, hi, n, thresh, sh);
+    uint32_t count = lds_uniform(sh.n_list);
+    for (uint32_t key = thresh;; key = 1u) {
+        count = fill_equal<T>(row, lo, hi, n, count, key, sh);
+        if (key != key_of(-kInf)) return count;
+    }
 }
 
 // The candidates of a slice in sh.list: their number.  best: the key of the
@@ -231,93 +285,74 @@ __device__ inline uint32_t candidates(const typename Type<T>::elem *row, uint32_
     const uint32_t none = key_of(-kInf);
     const uint32_t thresh = max(nth_key(best, n, sh), none);
     if (thresh > none && collect<T>(row, lo, hi, rounds, thresh, sh)) return lds_uniform(sh.n_list);
-    // Many logits equal the threshold (a masked row), or fewer than n are
-    // above -inf: those above it (in fewer than n threads' batches, so at
-    // most 63 x 16 of them), then the first that equal it, then NaN.
-    if (!collect<T>(row, lo, hi, rounds, thresh + 1, sh)) return top_slow<T>(row, lo, hi, n, thresh, sh);
-    uint32_t count = fill_equal<T>(row, lo, hi, n, lds_uniform(sh.n_list), thresh, sh);
-    if (thresh == none) count = fill_equal<T>(row, lo, hi, n, count, 1u, sh);
-    return count;
+    return candidates_many<T>(row, lo, hi, rounds, thresh, n, sh);
 }
 
 // Statistics of elements [lo, hi) of a row, in every thread, and with kTop
-// the number of candidates in sh.list.
+// the number of candidates in sh.list.  All rounds run the same code (a
+// second copy for the last, partial one costs a short row more in fetching
+// instructions than it saves): a vector that crosses the end is read ending
+// there, and what is not its own counts as -inf.
 template <int T, bool kTop, class Sh>
 __device__ inline Stat slice_pass(const typename Type<T>::elem *row, uint32_t lo, uint32_t hi, uint32_t n, Sh &sh,
                                   uint32_t *count)
 {
     using Ty = Type<T>;
-    constexpr int kPer = Ty::kPer16, kVecs = kBatch / kPer;
+    constexpr uint32_t kPer = Ty::kPer16, kVecs = kBatch / kPer;
+    constexpr uint32_t kSweep = Sh::NT * kBatch;  // logits of a round of the block
     const uint32_t tid = threadIdx.x;
     Stat a{kFloor, 0.f, 0.f};
     float best = -kInf;   // the largest of the thread's batches
-    bool any = false;     // the thread had a logit
     uint32_t round = 0;
     u32x4 cur[kVecs], nxt[kVecs];
-    // a round's vector u of a thread: elements base + (256 u + tid) kPer ..
+    // a round's vector u of a thread: elements base + (NT u + tid) kPer ..
     auto fetch = [&](u32x4 *v, uint32_t base) {
 #pragma unroll
-        for (int u = 0; u < kVecs; u++) v[u] = load16<Ty::kBytes>(row + base + (kRowThreads * u + tid) * kPer);
+        for (uint32_t u = 0; u < kVecs; u++)
+            v[u] = read16<Ty::kBytes, Sh::NT == 256>(row + min(base + (Sh::NT * u + tid) * kPer, hi - kPer));
     };
-    auto take = [&](const float *f, float bmax) {
+    const bool tiny = hi < kPer;  // a row shorter than a vector
+    if (!tiny) fetch(cur, lo);
+    for (uint32_t base = lo; base < hi; base += kSweep, round++) {
+        if (hi - base > kSweep) fetch(nxt, base + kSweep);
+        float f[kBatch];
+        if (!tiny) {
+#pragma unroll
+            for (uint32_t u = 0; u < kVecs; u++) Ty::unpack(cur[u], f + kPer * u);
+            if (hi - base < kSweep) {
+#pragma unroll
+                for (uint32_t u = 0; u < kVecs; u++) {
+                    const uint32_t j = base + (Sh::NT * u + tid) * kPer, at = min(j, hi - kPer);
+#pragma unroll
+                    for (uint32_t i = 0; i < kPer; i++) f[kPer * u + i] = at + i >= j ? f[kPer * u + i] : -kInf;
+                }
+            }
+        } else {
+#pragma unroll
+            for (uint32_t i = 0; i < kBatch; i++) f[i] = i < kPer && tid == 0 && i < hi ? Ty::to_f32(row[i]) : -kInf;
+        }
+        float bmax = f[0];
+#pragma unroll
+        for (uint32_t i = 1; i < kBatch; i++) bmax = fmaxf(bmax, f[i]);
         if (bmax > a.m) raise(a, bmax);
         const float ml = a.m * kLog2e;
 #pragma unroll
-        for (int i = 0; i < (int)kBatch; i++) {
+        for (uint32_t i = 0; i < kBatch; i++) {
             const float d = __builtin_fmaf(f[i], kLog2e, -ml);
             const float e = exp2_fast(d);
             a.s += e;
             a.w = __builtin_fmaf(e, fmaxf(d, -1000.f), a.w);  // a masked logit adds 0 * -1000, not 0 * -inf
         }
-    };
-    uint32_t base = lo;
-    if (hi - lo >= kSweep) fetch(cur, base);
-    for (; hi - base >= kSweep; base += kSweep, round++) {
-        if (hi - base >= 2 * kSweep) fetch(nxt, base + kSweep);
-        float f[kBatch];
-#pragma unroll
-        for (int u = 0; u < kVecs; u++) Ty::unpack(cur[u], f + kPer * u);
-        float bmax = f[0];
-#pragma unroll
-        for (int i = 1; i < (int)kBatch; i++) bmax = fmaxf(bmax, f[i]);
-        take(f, bmax);
         if constexpr (kTop) {
             // a batch of nothing but NaN counts as -inf: its elements are looked at if the threshold is that low
-            sh.batch_max[kRowThreads * round + tid] = __builtin_bit_cast(uint32_t, fmaxf(bmax, -kInf));
-            best = fmaxf(best, bmax);
-            any = true;
-        }
-#pragma unroll
-        for (int u = 0; u < kVecs; u++) cur[u] = nxt[u];
-    }
-    if (base < hi) {  // the last, partial round: absent elements as -inf
-        float f[kBatch];
-        bool had = false;
-#pragma unroll
-        for (int u = 0; u < kVecs; u++) {
-            const uint32_t j = base + (kRowThreads * u + tid) * kPer;
-            if (j + kPer <= hi) {
-                Ty::unpack(load16<Ty::kBytes>(row + j), f + kPer * u);
-            } else {
-#pragma unroll
-                for (int i = 0; i < kPer; i++) f[kPer * u + i] = j + i < hi ? Ty::to_f32(row[j + i]) : -kInf;
-            }
-            had = had || j < hi;
-        }
-        float bmax = f[0];
-#pragma unroll
-        for (int i = 1; i < (int)kBatch; i++) bmax = fmaxf(bmax, f[i]);
-        if (had) {
-            take(f, bmax);
-            any = true;
-        }
-        if constexpr (kTop) {
-            sh.batch_max[kRowThreads * round + tid] = __builtin_bit_cast(uint32_t, fmaxf(bmax, -kInf));
+            bmax = fmaxf(bmax, -kInf);
+            sh.batch_max[Sh::NT * round + tid] = __builtin_bit_cast(uint32_t, bmax);
             best = fmaxf(best, bmax);
         }
-        round++;
+#pragma unroll
+        for (uint32_t u = 0; u < kVecs; u++) cur[u] = nxt[u];
     }
-    if constexpr (kTop) *count = candidates<T>(row, lo, hi, round, any ? key_of(best) : 0u, n, sh);
+    if constexpr (kTop) *count = candidates<T>(row, lo, hi, round, lo + tid * kPer < hi ? key_of(best) : 0u, n, sh);
     return block_stat(a, sh);
 }
 
@@ -328,10 +363,10 @@ __device__ __noinline__ Stat exact_stat(const typename Type<T>::elem *row, uint3
 {
     __syncthreads();
     float m = -kInf;
-    for (uint32_t j = threadIdx.x; j < vocab; j += kRowThreads) m = fmaxf(m, Type<T>::to_f32(row[j]));
+    for (uint32_t j = threadIdx.x; j < vocab; j += Sh::NT) m = fmaxf(m, Type<T>::to_f32(row[j]));
     m = block_stat(Stat{m, 0.f, 0.f}, sh).m;
     Stat b{0.f, 0.f, 0.f};
-    for (uint32_t j = threadIdx.x; j < vocab; j += kRowThreads) {
+    for (uint32_t j = threadIdx.x; j < vocab; j += Sh::NT) {
         const float d = (Type<T>::to_f32(row[j]) - m) * kLog2e;
         const float e = m == -kInf ? 0.f : exp2_fast(d);
         b.s += e;
@@ -355,12 +390,12 @@ struct LogprobArgs {
 };
 
 // Writes a row's statistics; returns its lse for the alternatives.  Called
-// by the whole block.  S is 0 where every logit is below kFloor or the
+// by the whole block; z is the logit of the row's token t.  S is 0 where every logit is below kFloor or the
 // largest above 2^127 / log2 e (masks of the type's lowest value in a whole
 // row, infinities, -inf in a whole row): such a row is computed again with
 // its true maximum and exact differences.
 template <int T, class Sh>
-__device__ inline float write_row(const LogprobArgs &g, uint64_t r, Stat a, Sh &sh)
+__device__ inline float write_row(const LogprobArgs &g, uint64_t r, Stat a, int64_t t, float z, Sh &sh)
 {
     using Ty = Type<T>;
     const typename Ty::elem *row = static_cast<const typename Ty::elem *>(g.logits) + r * g.stride;
@@ -377,10 +412,8 @@ __device__ inline float write_row(const LogprobArgs &g, uint64_t r, Stat a, Sh &
         entropy = fmaxf(ln_s - kLn2 * (a.w / a.s), 0.f);
     }
     if (threadIdx.x == 0) {
-        const int64_t t = g.tokens[r];
         float lp = 0.f;
         if (t >= 0 && t < (int64_t)g.vocab) {
-            const float z = Ty::to_f32(row[t]);
             lp = z == -kInf && lse == lse ? -kInf : z - lse;
         } else if (t != -1) {
             lp = nan32();
@@ -400,19 +433,30 @@ __device__ __forceinline__ void put_top(const LogprobArgs &g, uint64_t r, uint32
     g.top_ids[r * g.top + at] = (int64_t)(uint32_t)~(uint32_t)e;
 }
 
-// One block per slice of a row; with one slice it writes the row.
-template <int T, bool kTop>
-__global__ __launch_bounds__(kRowThreads) void k_logprobs(LogprobArgs g)
+// A row's token and its logit (0 for none), read before anything else.
+template <int T>
+__device__ __forceinline__ float given_logit(const LogprobArgs &g, uint64_t r, int64_t &t)
 {
-    __shared__ RowShared<kTop, true> sh;
+    t = g.tokens[r];
+    if (t < 0 || t >= (int64_t)g.vocab) return 0.f;
+    return Type<T>::to_f32(static_cast<const typename Type<T>::elem *>(g.logits)[r * g.stride + t]);
+}
+
+// One block per slice of a row; with one slice it writes the row.
+template <int T, bool kTop, int NT>
+__global__ __launch_bounds__(NT) void k_logprobs(LogprobArgs g)
+{
+    __shared__ RowShared<kTop, true, NT> sh;
     const uint64_t r = blockIdx.x / g.slices;
     const uint32_t s = blockIdx.x % g.slices;
     const typename Type<T>::elem *row = static_cast<const typename Type<T>::elem *>(g.logits) + r * g.stride;
     const uint32_t lo = s * g.slice, hi = min(g.vocab, lo + g.slice);
     uint32_t count = 0;
+    int64_t token;
+    const float z = given_logit<T>(g, r, token);
     const Stat a = slice_pass<T, kTop>(row, lo, hi, g.top, sh, &count);
     if (g.slices == 1) {
-        const float lse = write_row<T>(g, r, a, sh);
+        const float lse = write_row<T>(g, r, a, token, z, sh);
         if constexpr (kTop) rank_list(count, g.top, sh, [&](uint32_t at, uint64_t e) { put_top(g, r, at, e, lse); });
         return;
     }
@@ -426,10 +470,10 @@ __global__ __launch_bounds__(kRowThreads) void k_logprobs(LogprobArgs g)
 // threads' largest entries.  No two entries are equal, so exactly n threads
 // hold entries >= T, and a thread holds at most 16 (64 slices x 64 / 256).
 template <int T, bool kTop>
-__global__ __launch_bounds__(kRowThreads) void k_logprobs_join(LogprobArgs g)
+__global__ __launch_bounds__(kJoinThreads) void k_logprobs_join(LogprobArgs g)
 {
-    __shared__ RowShared<kTop, false> sh;
-    static_assert(kMaxSlices * kMaxTop / kRowThreads * kMaxTop <= kListCap, "the join's list");
+    __shared__ RowShared<kTop, false, kJoinThreads> sh;
+    static_assert(kMaxSlices * kMaxTop / kJoinThreads * kMaxTop <= kListCap, "the join's list");
     const uint32_t tid = threadIdx.x;
     const uint64_t r = blockIdx.x;
     Stat a{kFloor, 0.f, 0.f};
@@ -437,13 +481,15 @@ __global__ __launch_bounds__(kRowThreads) void k_logprobs_join(LogprobArgs g)
         const f32x4 p = *reinterpret_cast<const f32x4 *>(g.part + 4 * (r * g.slices + tid));
         a = Stat{p[0], p[1], p[2]};
     }
+    int64_t token;
+    const float z = given_logit<T>(g, r, token);
     a = block_stat(a, sh);
-    const float lse = write_row<T>(g, r, a, sh);
+    const float lse = write_row<T>(g, r, a, token, z, sh);
     if constexpr (kTop) {
         const uint64_t *tops = g.part_top + r * g.slices * g.top;
         const uint32_t total = g.slices * g.top;
         uint64_t best = 0;
-        for (uint32_t i = tid; i < total; i += kRowThreads) best = max(best, tops[i]);
+        for (uint32_t i = tid; i < total; i += kJoinThreads) best = max(best, tops[i]);
         sh.list[tid] = best;
         if (tid == 0) {
             sh.thresh64 = ~0ull;
@@ -451,11 +497,11 @@ __global__ __launch_bounds__(kRowThreads) void k_logprobs_join(LogprobArgs g)
         }
         __syncthreads();
         uint32_t above = 0;
-        for (uint32_t i = 0; i < kRowThreads; i++) above += sh.list[i] > best;
+        for (uint32_t i = 0; i < kJoinThreads; i++) above += sh.list[i] > best;
         if (above < g.top) atomicMin(reinterpret_cast<unsigned long long *>(&sh.thresh64), (unsigned long long)best);
         __syncthreads();
         const uint64_t thresh = sh.thresh64;
-        for (uint32_t i = tid; i < total; i += kRowThreads) {
+        for (uint32_t i = tid; i < total; i += kJoinThreads) {
             const uint64_t e = tops[i];
             if (e && e >= thresh) sh.list[atomicAdd(&sh.n_list, 1u)] = e;
         }
@@ -474,6 +520,8 @@ __global__ __launch_bounds__(kRowThreads) void k_logprobs_join(LogprobArgs g)
 // type's lowest value, say) has no bits left for the probabilities in 32
 // bits, so such a row's maximum and log of the sum are computed again.  That
 // reads the whole row: in the logits' own memory a row has only one block.
+constexpr uint32_t kGradThreads = 256;
+
 struct LogprobGradArgs {
     const void *logits;
     void *out;
@@ -484,16 +532,17 @@ struct LogprobGradArgs {
     uint32_t *err;
 };
 
-template <int T>
-__global__ __launch_bounds__(kRowThreads) void k_logprobs_grad(LogprobGradArgs a)
+template <int T, bool kStream>
+__global__ __launch_bounds__(kGradThreads) void k_logprobs_grad(LogprobGradArgs a)
 {
     using Ty = Type<T>;
     using E = typename Ty::elem;
     constexpr int kPer = Ty::kPer16, kVecs = kBatch / kPer;
+    constexpr uint32_t kSweep = kGradThreads * kBatch;
     const uint64_t r = blockIdx.x / a.blocks;
     const uint32_t first = (blockIdx.x % a.blocks) * kSweep, tid = threadIdx.x;
     const E *row = static_cast<const E *>(a.logits) + r * a.stride;
-    __shared__ RowShared<false, true> sh;
+    __shared__ RowShared<false, true, kGradThreads> sh;
     E *out = static_cast<E *>(a.out) + r * a.out_stride;
     const int64_t t64 = a.tokens[r];
     const bool given = t64 >= 0 && t64 < (int64_t)a.vocab;
@@ -524,8 +573,8 @@ __global__ __launch_bounds__(kRowThreads) void k_logprobs_grad(LogprobGradArgs a
         u32x4 v[kVecs];
 #pragma unroll
         for (int u = 0; u < kVecs; u++) {
-            at[u] = base + (kRowThreads * u + tid) * kPer;
-            if (at[u] + kPer <= a.vocab) v[u] = load16<Ty::kBytes>(row + at[u]);
+            at[u] = base + (kGradThreads * u + tid) * kPer;
+            if (at[u] + kPer <= a.vocab) v[u] = read16<Ty::kBytes, kStream>(row + at[u]);
         }
 #pragma unroll
         for (int u = 0; u < kVecs; u++) {
@@ -534,7 +583,7 @@ __global__ __launch_bounds__(kRowThreads) void k_logprobs_grad(LogprobGradArgs a
                 Ty::unpack(v[u], f);
 #pragma unroll
                 for (int i = 0; i < kPer; i++) f[i] = grad(f[i], at[u] + i);
-                store16<Ty::kBytes>(out + at[u], Ty::pack(f));
+                write16<Ty::kBytes, kStream>(out + at[u], Ty::pack(f));
             } else {
                 for (int i = 0; i < kPer; i++)
                     if (at[u] + i < a.vocab) out[at[u] + i] = Ty::from_f32(grad(Ty::to_f32(row[at[u] + i]), at[u] + i));

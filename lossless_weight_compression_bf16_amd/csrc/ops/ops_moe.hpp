@@ -5,6 +5,7 @@
 //
 //   k_moe_route   router logits, split over blocks along the columns
 //   k_moe_select  softmax and the top_k of each token: one wave per token
+//   k_moe_route_one  both, where the router is small: one block per token
 //   k_moe_up      h = silu(W1 x) * (W3 x), for every expert with tokens
 //   k_moe_down    y = sum p W2 h, in the order of the experts
 //   k_moe_join    where few rows of y make k_moe_down split the experts
@@ -31,7 +32,7 @@ namespace wc {
 namespace ops {
 
 constexpr uint32_t kMoeMaxTokens = 64, kMoeMaxTop = 16, kMoeMaxExperts = 1024;
-constexpr uint32_t kMoeDownWaves = 8;
+constexpr uint32_t kMoeRouteSplits = 16;
 
 struct MoeArgs {
     const uint16_t *x, *router, *w1, *w3, *w2;
@@ -73,6 +74,12 @@ struct MoeTerms<WC_T_FP16> {
 };
 
 __device__ __forceinline__ u32x4 zero4() { return u32x4{0u, 0u, 0u, 0u}; }
+__device__ __forceinline__ u32x4 only(bool in, u32x4 v)  // all lanes load, some drop what they got
+{
+#pragma unroll
+    for (int e = 0; e < 4; e++) v[e] = in ? v[e] : 0u;
+    return v;
+}
 
 // logits[split][t][e]: 16 experts per block, the columns of a split over its
 // four waves.
@@ -93,8 +100,8 @@ __global__ __launch_bounds__(256) void k_moe_route(MoeArgs g)
         acc[t] = f32x4{0.f, 0.f, 0.f, 0.f};
     }
     const uint32_t s0 = split * g.route_steps, s1 = min((g.cols + 31) / 32, s0 + g.route_steps);
-    for (uint32_t st = s0 + wave; st < s1; st += 4) {
-        const uint32_t k = 32 * st + 8 * gr;
+    for (uint32_t j = 0; s0 + wave_step<4>(wave, j) < s1; j++) {
+        const uint32_t k = 32 * (s0 + wave_step<4>(wave, j)) + 8 * gr;
         const bool in = k < g.cols;
         const X8 rv = __builtin_bit_cast(X8, in ? load16<16>(rr + k) : zero4());
 #pragma unroll
@@ -111,64 +118,103 @@ __global__ __launch_bounds__(256) void k_moe_route(MoeArgs g)
     }
 }
 
-__device__ __forceinline__ uint64_t wave_max64(uint64_t v)
+// The experts of one token by one wave, largest logit first, equal ones by
+// their number, NaN last: always top_k different ones.  logit(e): expert e's.
+template <int PER, class F>
+__device__ __forceinline__ void moe_choose(const MoeArgs &g, uint32_t t, F logit)
 {
-    for (int o = 32; o; o >>= 1) {
-        const uint32_t lo = __shfl_xor((uint32_t)v, o, 64), hi = __shfl_xor((uint32_t)(v >> 32), o, 64);
-        v = max(v, ((uint64_t)hi << 32) | lo);
-    }
-    return v;
-}
-
-// The experts of one token, largest logit first, equal ones by their number,
-// NaN last: always top_k different ones.
-template <int PER>
-__global__ __launch_bounds__(64) void k_moe_select(MoeArgs g)
-{
-    const uint32_t t = blockIdx.x, lane = threadIdx.x;
-    uint64_t key[PER];
-    float most = -kInf;
-    float l[PER];
+    const uint32_t lane = threadIdx.x & 63;
+    uint32_t key[PER];  // lane's expert 64 q + lane; 0: none, or taken
+    float l[PER], most = -kInf, sum = 0.f;
 #pragma unroll
     for (int q = 0; q < PER; q++) {
         const uint32_t e = 64 * q + lane;
-        key[q] = 0;
-        l[q] = -kInf;
-        if (e < g.experts) {
-            float v = 0.f;
-            for (uint32_t s = 0; s < g.route_splits; s++) v += g.logits[((uint64_t)s * g.m + t) * g.experts_pad + e];
-            l[q] = v;
-            key[q] = ((uint64_t)key_of(v) << 32) | (uint32_t)~e;
-            most = fmaxf(most, v);
-        }
+        l[q] = e < g.experts ? logit(e) : -kInf;
+        key[q] = e < g.experts ? key_of(l[q]) : 0u;
+        most = fmaxf(most, l[q]);
     }
-    for (int o = 32; o; o >>= 1) most = fmaxf(most, __shfl_xor(most, o, 64));
-    float sum = 0.f;
+    most = wave_max(most);
 #pragma unroll
     for (int q = 0; q < PER; q++)
         if (64 * q + lane < g.experts) sum += exp2_fast((l[q] - most) * kLog2e);  // NaN or +inf: NaN
-    for (int o = 32; o; o >>= 1) sum += __shfl_xor(sum, o, 64);
+    sum = wave_sum(sum);
     float chosen = 0.f, mine = 0.f;
     uint32_t id = 0;
     for (uint32_t s = 0; s < g.top_k; s++) {
-        uint64_t best = 0;
+        uint32_t best = 0;
 #pragma unroll
         for (int q = 0; q < PER; q++) best = max(best, key[q]);
-        best = wave_max64(best);
+        best = ~wave_min(~best);
+        uint32_t e = ~0u;
+#pragma unroll
+        for (int q = PER - 1; q >= 0; q--)
+            if (key[q] == best) e = 64 * q + lane;
+        e = wave_min(e);
 #pragma unroll
         for (int q = 0; q < PER; q++)
-            if (key[q] == best) key[q] = 0;
-        const float p = exp2_fast((key_value((uint32_t)(best >> 32)) - most) * kLog2e);
+            if (64 * q + lane == e) key[q] = 0;
+        const float p = exp2_fast((key_value(best) - most) * kLog2e);
         chosen += p;
         if (lane == s) {
             mine = p;
-            id = ~(uint32_t)best;
+            id = e;
         }
     }
     if (lane < g.top_k) {
         g.ids[t * g.top_k + lane] = (int32_t)id;
         g.weights[t * g.top_k + lane] = mine / (g.renormalize ? chosen : sum);
     }
+}
+
+template <int PER>
+__global__ __launch_bounds__(64) void k_moe_select(MoeArgs g)
+{
+    moe_choose<PER>(g, blockIdx.x, [&](uint32_t e) {
+        const float *p = g.logits + (uint64_t)blockIdx.x * g.experts_pad + e;
+        const uint64_t step = (uint64_t)g.m * g.experts_pad;
+        float v[kMoeRouteSplits];  // all loads before the first sum
+#pragma unroll
+        for (uint32_t s = 0; s < kMoeRouteSplits; s++) v[s] = p[min(s, g.route_splits - 1) * step];
+        float sum = v[0];
+#pragma unroll
+        for (uint32_t s = 1; s < kMoeRouteSplits; s++) sum += s < g.route_splits ? v[s] : 0.f;
+        return sum;
+    });
+}
+
+// Both for one token in one block, where the router is small: tiles of 16
+// experts and, if they are fewer than the waves, pieces of the columns go
+// round the waves; the token is the only column.
+template <int T, int PER>
+__global__ __launch_bounds__(1024) void k_moe_route_one(MoeArgs g)
+{
+    using Ty = Type<T>;
+    using X8 = typename Ty::x8;
+    constexpr uint32_t W = 16;
+    __shared__ float logits[W][64 * PER];
+    const uint32_t wave = threadIdx.x >> 6, lane = threadIdx.x & 63, i = lane & 15, gr = lane >> 4;
+    const uint32_t tiles = g.experts_pad / 16, steps = (g.cols + 31) / 32;
+    const uint32_t pieces = tiles < W ? W / tiles : 1u, piece = (steps + pieces - 1) / pieces;
+    const uint16_t *xr = g.x + blockIdx.x * g.x_stride;
+    for (uint32_t it = wave; it < tiles * pieces; it += W) {
+        const uint32_t e0 = 16 * (it / pieces), pc = it % pieces, s1 = min(steps, (pc + 1) * piece);
+        const uint16_t *rr = g.router + (uint64_t)min(e0 + i, g.experts - 1) * g.cols;
+        f32x4 acc{0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+        for (uint32_t st = pc * piece; st < s1; st++) {
+            const uint32_t c = 32 * st + 8 * gr, k = min(c, g.cols - 8);
+            const X8 rv = __builtin_bit_cast(X8, only(c < g.cols, load16<16>(rr + k)));
+            acc = Ty::mfma(rv, __builtin_bit_cast(X8, only(c < g.cols, load16<16>(xr + k))), acc);
+        }
+        if (i == 0) *reinterpret_cast<f32x4 *>(&logits[pc][e0 + 4 * gr]) = acc;
+    }
+    __syncthreads();
+    if (wave == 0)
+        moe_choose<PER>(g, blockIdx.x, [&](uint32_t e) {
+            float v = logits[0][e];
+            for (uint32_t pc = 1; pc < pieces; pc++) v += logits[pc][e];
+            return v;
+        });
 }
 
 // The experts that have tokens, as a set in LDS.
@@ -219,14 +265,55 @@ struct MoeSet {
     }
 };
 
+// A wave's share of the columns for 16 rows (the lane's at `row`) of W1 and W3
+// of one expert against its tokens, up to 16 NT of them, into part.
+template <int T, int NT, int TT>
+__device__ __forceinline__ void moe_up_rows(const MoeArgs &g, uint64_t row, const int32_t *place, uint32_t count,
+                                            f32x4 (&part)[4][2 * TT][64])
+{
+    using Ty = Type<T>;
+    using X8 = typename Ty::x8;
+    constexpr int U = NT == 4 ? 2 : 4;  // steps on their way at once
+    const uint32_t wave = threadIdx.x >> 6, lane = threadIdx.x & 63, i = lane & 15, gr = lane >> 4;
+    const uint16_t *w1 = g.w1 + row, *w3 = g.w3 + row, *xr[NT];
+    f32x4 acc[2][NT];
+#pragma unroll
+    for (int t = 0; t < NT; t++) {
+        xr[t] = g.x + (uint64_t)((uint32_t)place[min(16 * t + i, count - 1)] / g.top_k) * g.x_stride;
+        acc[0][t] = acc[1][t] = f32x4{0.f, 0.f, 0.f, 0.f};
+    }
+    for (uint32_t j = 0; 32 * wave_step<4>(wave, j) < g.cols; j += U) {
+        X8 a[U], b[U], xv[U][NT];
+#pragma unroll
+        for (int u = 0; u < U; u++) {
+            // past the rows' end the loads repeat their last numbers, and the operands are zero
+            const uint32_t c = 32 * wave_step<4>(wave, j + u) + 8 * gr, k = min(c, g.cols - 8);
+            const bool in = c < g.cols;
+            a[u] = __builtin_bit_cast(X8, only(in, load16<16>(w1 + k)));
+            b[u] = __builtin_bit_cast(X8, only(in, load16<16>(w3 + k)));
+#pragma unroll
+            for (int t = 0; t < NT; t++) xv[u][t] = __builtin_bit_cast(X8, only(in, load16<16>(xr[t] + k)));
+        }
+#pragma unroll
+        for (int u = 0; u < U; u++)
+#pragma unroll
+            for (int t = 0; t < NT; t++) {
+                acc[0][t] = Ty::mfma(a[u], xv[u][t], acc[0][t]);
+                acc[1][t] = Ty::mfma(b[u], xv[u][t], acc[1][t]);
+            }
+    }
+#pragma unroll
+    for (int t = 0; t < NT; t++) {
+        part[wave][t][lane] = acc[0][t];
+        part[wave][TT + t][lane] = acc[1][t];
+    }
+}
+
 // h of 16 inner rows of one expert.  Grid: slots x inner / 16; a slot is the
 // p-th expert that has tokens.  Columns over the four waves.
 template <int T, int TT>
 __global__ __launch_bounds__(256) void k_moe_up(MoeArgs g)
 {
-    using Ty = Type<T>;
-    using X8 = typename Ty::x8;
-    constexpr int U = TT == 1 ? 4 : 2;
     __shared__ MoeSet set;
     __shared__ f32x4 part[4][2 * TT][64];
     __shared__ int32_t place[64];  // token top_k + choice of column c
@@ -241,54 +328,9 @@ __global__ __launch_bounds__(256) void k_moe_up(MoeArgs g)
     if (mine >= 0) place[__popcll(mask & ((1ull << lane) - 1))] = mine;  // the same from every wave
     __syncthreads();
     const uint64_t row = (uint64_t)expert * g.up_expert + (uint64_t)min(n0 + i, g.inner - 1) * g.up_row;
-    const uint16_t *w1 = g.w1 + row, *w3 = g.w3 + row;
-    const uint16_t *xr[TT];
-    f32x4 acc[2][TT];
-#pragma unroll
-    for (int t = 0; t < TT; t++) {
-        const uint32_t c = min(16 * t + i, count - 1);
-        xr[t] = g.x + (uint64_t)((uint32_t)place[c] / g.top_k) * g.x_stride;
-        acc[0][t] = acc[1][t] = f32x4{0.f, 0.f, 0.f, 0.f};
-    }
-    const uint32_t full = g.cols / 32, tiles = (count + 15) / 16;
-    uint32_t st = wave;
-    for (; st + 4 * (U - 1) < full; st += 4 * U) {
-        X8 a[U], b[U], xv[U][TT];
-#pragma unroll
-        for (int u = 0; u < U; u++) {
-            const uint32_t k = 32 * (st + 4 * u) + 8 * gr;
-            a[u] = __builtin_bit_cast(X8, load16<16>(w1 + k));
-            b[u] = __builtin_bit_cast(X8, load16<16>(w3 + k));
-#pragma unroll
-            for (int t = 0; t < TT; t++)
-                if (t < (int)tiles) xv[u][t] = __builtin_bit_cast(X8, load16<16>(xr[t] + k));
-        }
-#pragma unroll
-        for (int u = 0; u < U; u++)
-#pragma unroll
-            for (int t = 0; t < TT; t++)
-                if (t < (int)tiles) {
-                    acc[0][t] = Ty::mfma(a[u], xv[u][t], acc[0][t]);
-                    acc[1][t] = Ty::mfma(b[u], xv[u][t], acc[1][t]);
-                }
-    }
-    for (; 32 * st < g.cols; st += 4) {
-        const uint32_t k = 32 * st + 8 * gr;
-        const bool in = k < g.cols;
-        const X8 a = __builtin_bit_cast(X8, in ? load16<16>(w1 + k) : zero4());
-        const X8 b = __builtin_bit_cast(X8, in ? load16<16>(w3 + k) : zero4());
-#pragma unroll
-        for (int t = 0; t < TT; t++) {
-            const X8 xv = __builtin_bit_cast(X8, in ? load16<16>(xr[t] + k) : zero4());
-            acc[0][t] = Ty::mfma(a, xv, acc[0][t]);
-            acc[1][t] = Ty::mfma(b, xv, acc[1][t]);
-        }
-    }
-#pragma unroll
-    for (int t = 0; t < TT; t++) {
-        part[wave][t][lane] = acc[0][t];
-        part[wave][TT + t][lane] = acc[1][t];
-    }
+    if (TT == 1 || count <= 16) moe_up_rows<T, 1, TT>(g, row, place, count, part);
+    else if (TT == 2 || count <= 32) moe_up_rows<T, 2, TT>(g, row, place, count, part);
+    else moe_up_rows<T, 4, TT>(g, row, place, count, part);
     __syncthreads();
     const uint32_t n = n0 + 4 * gr, c = 16 * wave + i;
     if (wave < TT && c < count && n < g.inner) {
@@ -309,21 +351,72 @@ __global__ __launch_bounds__(256) void k_moe_up(MoeArgs g)
     }
 }
 
-// 16 columns of y (rows of W2).  Grid: columns / 16 x parts.  The experts
-// with tokens, each cut into pieces along the inner rows where they are few,
-// go round the waves of all parts; a wave adds its tokens' products, times
-// their weights, into a slice of LDS of its own, and at the end the slices
-// are added in the order of the waves.
-template <int T, int TT>
-__global__ __launch_bounds__(64 * kMoeDownWaves) void k_moe_down(MoeArgs g)
+// One piece of one expert in k_moe_down: steps s0 .. s1 of W2's 16 rows (the
+// lane's at w2) against the expert's tokens, up to 16 NT of them, added into
+// sums.
+template <int T, int NT>
+__device__ __forceinline__ void moe_down_piece(const MoeArgs &g, const uint16_t *w2, const int32_t *place, uint32_t count,
+                                               uint32_t s0, uint32_t s1, f32x4 (*sums)[4])
 {
     using Ty = Type<T>;
     using X8 = typename Ty::x8;
-    constexpr int U = TT == 1 ? 4 : 2, W = kMoeDownWaves;
+    constexpr int U = NT == 1 ? 4 : NT == 2 ? 2 : 1;  // steps on their way at once: NT U x 2 KiB of h
+    const uint32_t lane = threadIdx.x & 63, i = lane & 15, gr = lane >> 4;
+    const uint64_t plane = (uint64_t)g.m * g.top_k * g.inner;
+    const uint16_t *hr[NT];
+    int32_t at[NT];
+    f32x4 acc[2][NT];
+#pragma unroll
+    for (int t = 0; t < NT; t++) {
+        at[t] = place[min(16 * t + i, count - 1)];
+        hr[t] = g.h + (uint64_t)at[t] * g.inner;
+        acc[0][t] = acc[1][t] = f32x4{0.f, 0.f, 0.f, 0.f};
+    }
+    for (uint32_t st = s0; st < s1; st += U) {
+        X8 a[U], h0[U][NT], h1[U][NT];
+#pragma unroll
+        for (int u = 0; u < U; u++) {
+            // past the piece, or the rows' end, the operands are zero
+            const uint32_t c = 32 * (st + u) + 8 * gr, k = min(c, g.inner - 8);
+            const bool in = st + u < s1 && c < g.inner;
+            a[u] = __builtin_bit_cast(X8, only(in, load16<16>(w2 + k)));
+#pragma unroll
+            for (int t = 0; t < NT; t++) {
+                h0[u][t] = __builtin_bit_cast(X8, only(in, load16<16>(hr[t] + k)));
+                h1[u][t] = __builtin_bit_cast(X8, only(in, load16<16>(hr[t] + plane + k)));
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < U; u++)
+#pragma unroll
+            for (int t = 0; t < NT; t++) {
+                acc[0][t] = Ty::mfma(a[u], h0[u][t], acc[0][t]);
+                acc[1][t] = Ty::mfma(a[u], h1[u][t], acc[1][t]);
+            }
+    }
+#pragma unroll
+    for (int t = 0; t < NT; t++) {
+        if (16 * t + i < count) {
+            const float p = g.weights[at[t]];
+            f32x4 &s = sums[(uint32_t)at[t] / g.top_k][gr];
+            s += p * (MoeTerms<T>::kScale[0] * acc[0][t] + MoeTerms<T>::kScale[1] * acc[1][t]);
+        }
+    }
+}
+
+// 16 columns of y (rows of W2).  Grid: columns / 16 x parts.  The experts
+// with tokens, each cut into pieces along the inner rows where they are few,
+// go round the W waves of all parts; a wave adds its tokens' products, times
+// their weights, into a slice of LDS of its own, and at the end the slices
+// are added in the order of the waves.
+template <int T, int TT, int W>
+__global__ __launch_bounds__(64 * W, 4) void k_moe_down(MoeArgs g)
+{
+    using Ty = Type<T>;
     __shared__ MoeSet set;
     __shared__ f32x4 sums[W][16 * TT][4];   // [wave][token][column / 4]
     __shared__ int32_t place[W][64];
-    const uint32_t wave = threadIdx.x >> 6, lane = threadIdx.x & 63, i = lane & 15, gr = lane >> 4;
+    const uint32_t wave = threadIdx.x >> 6, lane = threadIdx.x & 63, i = lane & 15;
     const uint32_t part = blockIdx.x % g.parts, n0 = 16 * (blockIdx.x / g.parts);
     for (uint32_t q = lane; q < 64 * TT; q += 64) sums[wave][q >> 2][q & 3] = f32x4{0.f, 0.f, 0.f, 0.f};
     set.fill(g);
@@ -334,68 +427,20 @@ __global__ __launch_bounds__(64 * kMoeDownWaves) void k_moe_down(MoeArgs g)
     uint32_t pieces = active >= 8 * waves ? 1u : min((4 * waves + active - 1) / active, max(steps / 8, 1u));
     const uint32_t piece = (steps + pieces - 1) / pieces;
     pieces = (steps + piece - 1) / piece;
-    const uint64_t plane = (uint64_t)g.m * g.top_k * g.inner;
     const uint64_t row = (uint64_t)min(n0 + i, g.cols - 1) * g.down_row;
     for (uint32_t it = wave + W * part; it < active * pieces; it += waves) {
         set.find(it / pieces, expert);
         const int32_t mine = set.choice(g, expert);
         const uint64_t mask = __ballot(mine >= 0);
-        const uint32_t count = (uint32_t)__popcll(mask), tiles = (count + 15) / 16;
+        const uint32_t count = (uint32_t)__popcll(mask);
         __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "wavefront");  // a wave's own LDS: in order
         if (mine >= 0) place[wave][__popcll(mask & ((1ull << lane) - 1))] = mine;
         __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "wavefront");
         const uint16_t *w2 = g.w2 + (uint64_t)expert * g.down_expert + row;
-        const uint16_t *hr[TT];
-        int32_t at[TT];
-        f32x4 acc[2][TT];
-#pragma unroll
-        for (int t = 0; t < TT; t++) {
-            at[t] = place[wave][min(16 * t + i, count - 1)];
-            hr[t] = g.h + (uint64_t)at[t] * g.inner;
-            acc[0][t] = acc[1][t] = f32x4{0.f, 0.f, 0.f, 0.f};
-        }
-        const uint32_t s0 = (it % pieces) * piece, s1 = min(steps, s0 + piece), full = min(s1, g.inner / 32);
-        uint32_t st = s0;
-        for (; st + U <= full; st += U) {
-            X8 a[U], h0[U][TT], h1[U][TT];
-#pragma unroll
-            for (int u = 0; u < U; u++) {
-                const uint32_t k = 32 * (st + u) + 8 * gr;
-                a[u] = __builtin_bit_cast(X8, load16<16>(w2 + k));
-#pragma unroll
-                for (int t = 0; t < TT; t++)
-                    if (t < (int)tiles) {
-                        h0[u][t] = __builtin_bit_cast(X8, load16<16>(hr[t] + k));
-                        h1[u][t] = __builtin_bit_cast(X8, load16<16>(hr[t] + plane + k));
-                    }
-            }
-#pragma unroll
-            for (int u = 0; u < U; u++)
-#pragma unroll
-                for (int t = 0; t < TT; t++)
-                    if (t < (int)tiles) {
-                        acc[0][t] = Ty::mfma(a[u], h0[u][t], acc[0][t]);
-                        acc[1][t] = Ty::mfma(a[u], h1[u][t], acc[1][t]);
-                    }
-        }
-        for (; st < s1; st++) {
-            const uint32_t k = 32 * st + 8 * gr;
-            const bool in = k < g.inner;
-            const X8 a = __builtin_bit_cast(X8, in ? load16<16>(w2 + k) : zero4());
-#pragma unroll
-            for (int t = 0; t < TT; t++) {
-                acc[0][t] = Ty::mfma(a, __builtin_bit_cast(X8, in ? load16<16>(hr[t] + k) : zero4()), acc[0][t]);
-                acc[1][t] = Ty::mfma(a, __builtin_bit_cast(X8, in ? load16<16>(hr[t] + plane + k) : zero4()), acc[1][t]);
-            }
-        }
-#pragma unroll
-        for (int t = 0; t < TT; t++) {
-            if (16 * t + i < count) {
-                const float p = g.weights[at[t]];
-                f32x4 &s = sums[wave][(uint32_t)at[t] / g.top_k][gr];
-                s += p * (MoeTerms<T>::kScale[0] * acc[0][t] + MoeTerms<T>::kScale[1] * acc[1][t]);
-            }
-        }
+        const uint32_t s0 = (it % pieces) * piece, s1 = min(steps, s0 + piece);
+        if (TT == 1 || count <= 16) moe_down_piece<T, 1>(g, w2, place[wave], count, s0, s1, sums[wave]);
+        else if (TT == 2 || count <= 32) moe_down_piece<T, 2>(g, w2, place[wave], count, s0, s1, sums[wave]);
+        else moe_down_piece<T, 4>(g, w2, place[wave], count, s0, s1, sums[wave]);
     }
     __syncthreads();
     for (uint32_t q = threadIdx.x; q < 4 * g.m; q += 64 * W) {

@@ -24,17 +24,13 @@ uintptr_t type_bytes(uint32_t t) { return t == WC_T_FP32 ? 4 : 2; }
 
 wc_status launched() { return hipGetLastError() == hipSuccess ? WC_OK : WC_ERR_HIP; }
 
-// Blocks of a row of the log probabilities.  A block's first round is 8,192
-// logits, but with few rows more, smaller blocks fill the GPU better: 4 per
-// compute unit, at least 2,048 logits each.
-void logprob_slices(uint64_t m, uint32_t vocab, uint32_t *slices, uint32_t *slice)
+// Blocks of a row of the log probabilities: one, up to the batches that its
+// LDS has room for; more only for larger vocabularies, and then a second
+// launch joins them.  (Four blocks a row for 64 rows of 128,256 logits took
+// 12 us and 6 us for the join, against 16 us in one block and one launch.)
+void logprob_slices(uint32_t vocab, uint32_t *slices, uint32_t *slice)
 {
-    uint64_t s = ceil_div(4 * kCus, m);
-    const uint64_t most = ceil_div(vocab, kMinSlice);
-    if (s > most) s = most;
-    if (s > kMaxSlices) s = kMaxSlices;
-    const uint64_t least = ceil_div(vocab, kMaxSlice);
-    if (s < least) s = least;
+    const uint64_t s = ceil_div(vocab, kMaxSlice);
     *slice = (uint32_t)((ceil_div(vocab, s) + 7) / 8 * 8);
     *slices = (uint32_t)ceil_div(vocab, *slice);
 }
@@ -42,21 +38,33 @@ void logprob_slices(uint64_t m, uint32_t vocab, uint32_t *slices, uint32_t *slic
 uint64_t logprob_scratch(uint64_t m, uint32_t vocab, uint32_t top)
 {
     uint32_t slices, slice;
-    logprob_slices(m, vocab, &slices, &slice);
+    logprob_slices(vocab, &slices, &slice);
     return slices == 1 ? 0 : m * slices * (16 + 8ull * top);
+}
+
+template <int T, bool kTop, int NT>
+void launch_rows(const LogprobArgs &g, uint64_t m, hipStream_t stream)
+{
+    hipLaunchKernelGGL((k_logprobs<T, kTop, NT>), dim3((uint32_t)(m * g.slices)), dim3(NT), 0, stream, g);
+    if (g.slices > 1)
+        hipLaunchKernelGGL((k_logprobs_join<T, kTop>), dim3((uint32_t)m), dim3(kJoinThreads), 0, stream, g);
 }
 
 template <int T>
 wc_status launch_logprobs(const LogprobArgs &g, uint64_t m, hipStream_t stream)
 {
-    const dim3 grid((uint32_t)(m * g.slices)), block(kRowThreads);
-    if (g.top) hipLaunchKernelGGL((k_logprobs<T, true>), grid, block, 0, stream, g);
-    else hipLaunchKernelGGL((k_logprobs<T, false>), grid, block, 0, stream, g);
-    if (g.slices > 1) {
-        if (g.top) hipLaunchKernelGGL((k_logprobs_join<T, true>), dim3((uint32_t)m), block, 0, stream, g);
-        else hipLaunchKernelGGL((k_logprobs_join<T, false>), dim3((uint32_t)m), block, 0, stream, g);
-    }
+    // few rows: more threads for each, and logits that may still be in the caches
+    const bool few = m * g.slices < 2 * kCus;
+    if (g.top) few ? launch_rows<T, true, 1024>(g, m, stream) : launch_rows<T, true, 256>(g, m, stream);
+    else few ? launch_rows<T, false, 1024>(g, m, stream) : launch_rows<T, false, 256>(g, m, stream);
     return launched();
+}
+
+template <int T>
+void launch_grad(const LogprobGradArgs &g, dim3 grid, bool large, hipStream_t stream)
+{
+    if (large) hipLaunchKernelGGL((k_logprobs_grad<T, true>), grid, dim3(kGradThreads), 0, stream, g);
+    else hipLaunchKernelGGL((k_logprobs_grad<T, false>), grid, dim3(kGradThreads), 0, stream, g);
 }
 
 // Launch shapes of the adapters: tiles of 16 tokens where the tokens are
@@ -64,80 +72,107 @@ wc_status launch_logprobs(const LogprobArgs &g, uint64_t m, hipStream_t stream)
 // as possible share the reading; tiles of 64 tokens where prompts repeat
 // their adapter over many tokens, so that it is read once per tile.
 struct AdapterPlan {
-    uint32_t rank_pad, rank_blocks, tile, turns, splits, steps;  // k_adapters_down
+    bool few;                                                    // k_adapters_few
+    uint32_t rank_pad, rank_blocks, tile, turns;                 // k_adapters_down
     uint32_t up_tile, row_blocks, row_block;                     // k_adapters_up
-    uint64_t tiles, up_tiles, scratch;
+    uint64_t tiles, up_tiles, unscale, scratch;                  // unscale: its place in the scratch
 };
 
 AdapterPlan adapter_plan(uint64_t m, uint32_t rank, uint32_t cols, uint32_t rows)
 {
     AdapterPlan p{};
     const bool many = m > 512;
-    p.rank_pad = (rank + 15) / 16 * 16;
-    p.rank_blocks = (uint32_t)ceil_div(rank, 64);
-    p.tile = many ? 64 : 16;
+    p.rank_pad = (rank + 31) / 32 * 32;
+    // one launch where all blocks' reading of A from the caches costs less
+    // than the second launch: at most 64 MiB, a block per 1,024 to 4,096 rows
+    const uint64_t reading = m * rank * cols * 2;
+    for (uint32_t r = 1024; r <= 4096 && rank <= 64 && m <= 64 && !p.few; r *= 2) {
+        p.row_block = r;
+        p.row_blocks = (uint32_t)ceil_div(rows, r);
+        p.few = reading * p.row_blocks <= (64ull << 20);
+    }
     p.turns = many ? 1 : (uint32_t)(m < 16 ? m : 16);
+    if (p.few) {
+        p.tile = p.up_tile = 16;
+        p.tiles = p.up_tiles = ceil_div(m, 16);
+        return p;
+    }
+    p.rank_blocks = (uint32_t)ceil_div(rank, 64);
+    p.tile = many ? 32 : 16;
     p.tiles = ceil_div(m, p.tile);
-    const uint64_t steps = ceil_div(cols, 32), blocks = p.tiles * p.turns * p.rank_blocks;
-    uint64_t splits = blocks < 2 * kCus ? 2 * kCus / blocks : 1;
-    const uint64_t most = ceil_div(steps, 8);  // two steps for each of a block's waves
-    if (splits > most) splits = most;
-    if (splits > 16) splits = 16;
-    p.steps = (uint32_t)(ceil_div(ceil_div(steps, splits), 4) * 4);
-    p.splits = (uint32_t)ceil_div(steps, p.steps);
-    p.up_tile = many ? (rank <= 64 ? 64 : rank <= 128 ? 32 : 16) : 16;
+    // k_adapters_up_many takes 128 tokens and 64 rows at a time, k_adapters_up 16 and 256
+    const bool wide = many && rank <= 64;
+    p.up_tile = wide ? 128 : 16;
     p.up_tiles = ceil_div(m, p.up_tile);
+    const uint32_t least = wide ? 64 : 256;
     uint64_t rb = ceil_div(4 * kCus, p.up_tiles * p.turns);
     const uint64_t rmost = ceil_div(rows, 256);
     if (rb > rmost) rb = rmost;
-    p.row_block = (uint32_t)(ceil_div(ceil_div(rows, rb), 256) * 256);
+    p.row_block = (uint32_t)(ceil_div(ceil_div(rows, rb), least) * least);
     p.row_blocks = (uint32_t)ceil_div(rows, p.row_block);
-    p.scratch = (uint64_t)p.splits * m * p.rank_pad * 4;
+    p.unscale = 2ull * Terms<WC_T_BF16, WC_T_FP32>::kCount * m * p.rank_pad;  // the most terms of all types
+    p.scratch = p.unscale + 4 * m * p.rank_blocks;
     return p;
 }
 
 bool valid_adapters(uint64_t m, uint32_t rank, uint32_t cols, uint32_t rows)
 {
     return m <= (1ull << 31) && rank >= 1 && rank <= kAdapterMaxRank && cols >= 8 && cols % 8 == 0 && rows >= 1 &&
-           rows <= (1u << 30) && cols <= (1u << 30);
+           cols <= (1u << 30) && (uint64_t)rows * rank < (1ull << 31);
 }
 
-template <int T, int TT>
+template <int T, int YT, int TT>
 void launch_down(const AdapterArgs &g, const AdapterPlan &p, hipStream_t stream)
 {
-    const dim3 grid((uint32_t)(p.tiles * p.splits), p.rank_blocks, p.turns), block(256);
-    if (g.rank <= 16) hipLaunchKernelGGL((k_adapters_down<T, TT, 1>), grid, block, 0, stream, g);
-    else if (g.rank <= 32) hipLaunchKernelGGL((k_adapters_down<T, TT, 2>), grid, block, 0, stream, g);
-    else hipLaunchKernelGGL((k_adapters_down<T, TT, 4>), grid, block, 0, stream, g);
+    const dim3 grid((uint32_t)p.tiles, p.rank_blocks, p.turns), block(64 * kDownWaves);
+    if (g.rank <= 16) hipLaunchKernelGGL((k_adapters_down<T, YT, TT, 1>), grid, block, 0, stream, g);
+    else if (g.rank <= 32) hipLaunchKernelGGL((k_adapters_down<T, YT, TT, 2>), grid, block, 0, stream, g);
+    else hipLaunchKernelGGL((k_adapters_down<T, YT, TT, 4>), grid, block, 0, stream, g);
 }
 
 template <int T, int YT>
 void launch_up(const AdapterArgs &g, const AdapterPlan &p, hipStream_t stream)
 {
     const dim3 grid((uint32_t)(p.up_tiles * p.row_blocks), 1, p.turns), block(256);
-    const uint32_t tt = p.up_tile / 16;
-    if (tt == 4 && g.rank <= 32) hipLaunchKernelGGL((k_adapters_up<T, YT, 4, 1>), grid, block, 0, stream, g);
-    else if (tt == 4) hipLaunchKernelGGL((k_adapters_up<T, YT, 4, 2>), grid, block, 0, stream, g);
-    else if (tt == 2) hipLaunchKernelGGL((k_adapters_up<T, YT, 2, 4>), grid, block, 0, stream, g);
-    else if (g.rank <= 32) hipLaunchKernelGGL((k_adapters_up<T, YT, 1, 1>), grid, block, 0, stream, g);
-    else if (g.rank <= 64) hipLaunchKernelGGL((k_adapters_up<T, YT, 1, 2>), grid, block, 0, stream, g);
-    else if (g.rank <= 128) hipLaunchKernelGGL((k_adapters_up<T, YT, 1, 4>), grid, block, 0, stream, g);
-    else hipLaunchKernelGGL((k_adapters_up<T, YT, 1, 8>), grid, block, 0, stream, g);
+    if (p.up_tile == 128 && g.rank <= 32) hipLaunchKernelGGL((k_adapters_up_many<T, YT, 1>), grid, block, 0, stream, g);
+    else if (p.up_tile == 128) hipLaunchKernelGGL((k_adapters_up_many<T, YT, 2>), grid, block, 0, stream, g);
+    else if (g.rank <= 32) hipLaunchKernelGGL((k_adapters_up<T, YT, 1, false>), grid, block, 0, stream, g);
+    else if (g.rank <= 64) hipLaunchKernelGGL((k_adapters_up<T, YT, 2, false>), grid, block, 0, stream, g);
+    else hipLaunchKernelGGL((k_adapters_up<T, YT, 2, true>), grid, block, 0, stream, g);
+}
+
+template <int T, int YT>
+void launch_few(const AdapterArgs &g, const AdapterPlan &p, hipStream_t stream)
+{
+    const dim3 grid((uint32_t)(ceil_div(p.tiles * p.turns, 8) * 8 * p.row_blocks)), block(1024);
+    if (g.rank <= 16) hipLaunchKernelGGL((k_adapters_few<T, YT, 1>), grid, block, 0, stream, g);
+    else if (g.rank <= 32) hipLaunchKernelGGL((k_adapters_few<T, YT, 2>), grid, block, 0, stream, g);
+    else hipLaunchKernelGGL((k_adapters_few<T, YT, 4>), grid, block, 0, stream, g);
+}
+
+template <int T, int YT>
+wc_status launch_adapters(const AdapterArgs &g, const AdapterPlan &p, hipStream_t stream)
+{
+    if (p.few) {
+        launch_few<T, YT>(g, p, stream);
+    } else {
+        if (p.tile == 32) launch_down<T, YT, 2>(g, p, stream);
+        else launch_down<T, YT, 1>(g, p, stream);
+        launch_up<T, YT>(g, p, stream);
+    }
+    return launched();
 }
 
 template <int T>
 wc_status launch_adapters(const AdapterArgs &g, const AdapterPlan &p, uint32_t y_type, hipStream_t stream)
 {
-    if (p.tile == 64) launch_down<T, 4>(g, p, stream);
-    else launch_down<T, 1>(g, p, stream);
-    if (y_type == WC_T_FP32) launch_up<T, WC_T_FP32>(g, p, stream);
-    else launch_up<T, T>(g, p, stream);
-    return launched();
+    return y_type == WC_T_FP32 ? launch_adapters<T, WC_T_FP32>(g, p, stream) : launch_adapters<T, T>(g, p, stream);
 }
 
 // Launch shapes and scratch of the mixture-of-experts layer.
 struct MoePlan {
-    uint32_t route_tiles, route_splits, route_steps, experts_pad, slots, up_tiles, down_tiles, parts;
+    bool one;       // k_moe_route_one
+    uint32_t route_tiles, route_splits, route_steps, experts_pad, slots, up_tiles, down_tiles, down_waves, parts;
     uint64_t logits, ids, weights, h, part, bytes;  // offsets in the scratch
 };
 
@@ -146,26 +181,36 @@ MoePlan moe_plan(uint32_t m, uint32_t experts, uint32_t top_k, uint32_t cols, ui
     MoePlan p{};
     p.route_tiles = (experts + 15) / 16;
     p.experts_pad = 16 * p.route_tiles;
+    // one launch for the router where a block reads it in a few microseconds
+    p.one = (uint64_t)experts * cols * 2 <= (512u << 10) && experts <= 256;
     const uint32_t steps = (cols + 31) / 32;
     uint32_t splits = 128 / p.route_tiles;
     const uint32_t most = (steps + 7) / 8;  // two steps for each of a block's waves
     if (splits > most) splits = most;
-    if (splits > 16) splits = 16;
+    if (splits > kMoeRouteSplits) splits = kMoeRouteSplits;
     if (splits < 1) splits = 1;
-    p.route_steps = (uint32_t)(ceil_div(ceil_div(steps, splits), 4) * 4);
+    p.route_steps = (uint32_t)(ceil_div(ceil_div(steps, splits), 8) * 8);
     p.route_splits = (uint32_t)ceil_div(steps, p.route_steps);
     p.slots = m * top_k < experts ? m * top_k : experts;
     p.up_tiles = (inner + 15) / 16;
     p.down_tiles = (cols + 15) / 16;
+    // k_moe_down: 512 blocks of eight waves, split into parts where the
+    // columns are too few, which takes another launch; where all of W2's
+    // experts are under 64 MiB that costs more than it gives, and blocks have
+    // sixteen waves instead
+    const uint64_t reads = 2ull * p.slots * cols * inner;
     p.parts = 1;
-    while (p.parts < 16 && p.down_tiles * p.parts < kCus) p.parts *= 2;
+    p.down_waves = 8;
+    if (p.down_tiles <= kCus && reads < (64ull << 20)) p.down_waves = 16;
+    else
+        while (p.parts < 16 && p.down_tiles * p.parts < 7 * kCus / 4) p.parts *= 2;
     uint64_t at = 0;
     auto take = [&](uint64_t bytes) {
         const uint64_t here = at;
         at = ceil_div(at + bytes, 256) * 256;
         return here;
     };
-    p.logits = take(4ull * p.route_splits * m * p.experts_pad);
+    p.logits = take(p.one ? 0 : 4ull * p.route_splits * m * p.experts_pad);
     p.ids = take(4ull * m * top_k);
     p.weights = take(4ull * m * top_k);
     p.h = take(4ull * m * top_k * inner);
@@ -184,13 +229,20 @@ bool valid_moe(uint64_t m, uint32_t experts, uint32_t top_k, uint32_t cols, uint
 template <int T, int TT>
 wc_status launch_moe(const MoeArgs &g, const MoePlan &p, hipStream_t stream)
 {
-    hipLaunchKernelGGL((k_moe_route<T, TT>), dim3(p.route_tiles * p.route_splits), dim3(256), 0, stream, g);
-    const dim3 tokens(g.m), wave(64);
-    if (g.experts <= 64) hipLaunchKernelGGL(k_moe_select<1>, tokens, wave, 0, stream, g);
-    else if (g.experts <= 256) hipLaunchKernelGGL(k_moe_select<4>, tokens, wave, 0, stream, g);
-    else hipLaunchKernelGGL(k_moe_select<16>, tokens, wave, 0, stream, g);
+    const dim3 tokens(g.m);
+    if (p.one) {
+        if (g.experts <= 64) hipLaunchKernelGGL((k_moe_route_one<T, 1>), tokens, dim3(1024), 0, stream, g);
+        else hipLaunchKernelGGL((k_moe_route_one<T, 4>), tokens, dim3(1024), 0, stream, g);
+    } else {
+        hipLaunchKernelGGL((k_moe_route<T, TT>), dim3(p.route_tiles * p.route_splits), dim3(256), 0, stream, g);
+        if (g.experts <= 64) hipLaunchKernelGGL(k_moe_select<1>, tokens, dim3(64), 0, stream, g);
+        else if (g.experts <= 256) hipLaunchKernelGGL(k_moe_select<4>, tokens, dim3(64), 0, stream, g);
+        else hipLaunchKernelGGL(k_moe_select<16>, tokens, dim3(64), 0, stream, g);
+    }
     hipLaunchKernelGGL((k_moe_up<T, TT>), dim3(p.slots * p.up_tiles), dim3(256), 0, stream, g);
-    hipLaunchKernelGGL((k_moe_down<T, TT>), dim3(p.down_tiles * p.parts), dim3(64 * kMoeDownWaves), 0, stream, g);
+    const dim3 down(p.down_tiles * p.parts);
+    if (p.down_waves == 16) hipLaunchKernelGGL((k_moe_down<T, TT, 16>), down, dim3(1024), 0, stream, g);
+    else hipLaunchKernelGGL((k_moe_down<T, TT, 8>), down, dim3(512), 0, stream, g);
     if (p.parts > 1)
         hipLaunchKernelGGL(k_moe_join<T>, dim3((g.m * (g.cols / 4) + 255) / 256), dim3(256), 0, stream, g);
     return launched();
@@ -230,7 +282,7 @@ wc_status wc_token_logprobs(const wc_logprobs *a, void *d_scratch, uint64_t scra
     if (a->top && (!a->top_logprobs || !a->top_ids || !aligned(a->top_logprobs, 4) || !aligned(a->top_ids, 8)))
         return WC_ERR_ARG;
     LogprobArgs g{};
-    logprob_slices(a->m, a->vocab, &g.slices, &g.slice);
+    logprob_slices(a->vocab, &g.slices, &g.slice);
     if (a->m * g.slices > kMaxGrid) return WC_ERR_ARG;
     const uint64_t need = logprob_scratch(a->m, a->vocab, a->top);
     if (scratch_bytes < need) return WC_ERR_CAPACITY;
@@ -278,14 +330,16 @@ wc_status wc_token_logprobs_backward(const wc_logprobs_grad *a, uint32_t *d_err,
     g.grad_logprob = a->grad_logprob;
     g.grad_entropy = a->grad_entropy;
     g.vocab = a->vocab;
-    g.blocks = a->out == a->logits ? 1 : (uint32_t)ceil_div(a->vocab, kSweep);
+    g.blocks = a->out == a->logits ? 1 : (uint32_t)ceil_div(a->vocab, kGradThreads * kBatch);
     g.err = d_err;
     if (a->m > kMaxGrid / g.blocks) return WC_ERR_ARG;
-    const dim3 grid((uint32_t)(a->m * g.blocks)), block(kRowThreads);
+    const dim3 grid((uint32_t)(a->m * g.blocks));
+    // past the caches where the logits do not fit into the last of them (256 MiB)
+    const bool large = a->m * a->vocab * es > (128ull << 20);
     switch (a->type) {
-    case WC_T_BF16: hipLaunchKernelGGL(k_logprobs_grad<WC_T_BF16>, grid, block, 0, stream, g); break;
-    case WC_T_FP16: hipLaunchKernelGGL(k_logprobs_grad<WC_T_FP16>, grid, block, 0, stream, g); break;
-    default: hipLaunchKernelGGL(k_logprobs_grad<WC_T_FP32>, grid, block, 0, stream, g); break;
+    case WC_T_BF16: launch_grad<WC_T_BF16>(g, grid, large, stream); break;
+    case WC_T_FP16: launch_grad<WC_T_FP16>(g, grid, large, stream); break;
+    default: launch_grad<WC_T_FP32>(g, grid, large, stream); break;
     }
     return launched();
 }
@@ -309,9 +363,9 @@ wc_status wc_add_adapters(const wc_adapters *a, void *d_scratch, uint64_t scratc
     if (!a->y || !aligned(a->y, type_bytes(a->y_type)) || (a->m > 1 && a->y_stride < a->rows)) return WC_ERR_ARG;
     if (!a->ids || !aligned(a->ids, 8) || !aligned(a->scales, 4)) return WC_ERR_ARG;
     const AdapterPlan p = adapter_plan(a->m, a->rank, a->cols, a->rows);
-    if (p.tiles * p.splits > kMaxGrid || p.up_tiles * p.row_blocks > kMaxGrid) return WC_ERR_ARG;
+    if (p.tiles > kMaxGrid || p.up_tiles * p.row_blocks > kMaxGrid) return WC_ERR_ARG;
     if (scratch_bytes < p.scratch) return WC_ERR_CAPACITY;
-    if (!d_scratch || !aligned(d_scratch, 16)) return WC_ERR_ARG;
+    if (p.scratch && (!d_scratch || !aligned(d_scratch, 16))) return WC_ERR_ARG;
     AdapterArgs g{};
     g.x = static_cast<const uint16_t *>(a->x);
     g.x_stride = a->x_stride;
@@ -326,10 +380,9 @@ wc_status wc_add_adapters(const wc_adapters *a, void *d_scratch, uint64_t scratc
     g.rank = a->rank;
     g.cols = a->cols;
     g.rows = a->rows;
-    g.u = static_cast<float *>(d_scratch);
+    g.u = static_cast<uint16_t *>(d_scratch);
+    g.unscale = reinterpret_cast<float *>(static_cast<char *>(d_scratch) + p.unscale);
     g.rank_pad = p.rank_pad;
-    g.splits = p.splits;
-    g.steps = p.steps;
     g.row_block = p.row_block;
     g.err = d_err;
     return a->type == WC_T_BF16 ? launch_adapters<WC_T_BF16>(g, p, a->y_type, stream)

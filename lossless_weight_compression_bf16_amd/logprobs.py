@@ -36,15 +36,22 @@ def _check(logits, tokens):
         raise ValueError("the vocabulary is empty")
 
 
-def _forward(logits, tokens, top, check, stream):
+def _forward(logits, tokens, top, check, stream, views=True):
     z, t = _ops.rows_of(logits), tokens.contiguous()
     m, vocab = z.shape
 
     def call(raw):
         dev = z.device
-        out = TokenLogprobs(*(torch.empty(m, dtype=torch.float32, device=dev) for _ in range(3)),
-                            torch.empty((m, top), dtype=torch.float32, device=dev),
-                            torch.empty((m, top), dtype=torch.int64, device=dev))
+        if not views:  # autograd's outputs are tensors of their own
+            rows = [torch.empty(m, dtype=torch.float32, device=dev) for _ in range(3)]
+            best = torch.empty((m, top), dtype=torch.float32, device=dev)
+        elif top:  # one allocation for the fp32 outputs
+            *rows, best = torch.empty(m * (3 + top), dtype=torch.float32, device=dev).split((m, m, m, m * top))
+            best = best.view(m, top)
+        else:
+            rows = torch.empty((3, m), dtype=torch.float32, device=dev).unbind(0)
+            best = torch.empty((m, 0), dtype=torch.float32, device=dev)
+        out = TokenLogprobs(*rows, best, torch.empty((m, top), dtype=torch.int64, device=dev))
         nbytes = B.wc_token_logprobs_scratch(m, vocab, top)
         scratch = torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
         err = torch.zeros(1, dtype=torch.int32, device=dev) if check else None
@@ -123,7 +130,7 @@ def token_logprobs_backward(logits: torch.Tensor, tokens: torch.Tensor, lse: tor
 class _TokenLogprobs(torch.autograd.Function):
     @staticmethod
     def forward(ctx, logits, tokens, top, check):
-        r = _forward(logits, tokens, top, check, None)
+        r = _forward(logits, tokens, top, check, None, views=False)
         ctx.save_for_backward(logits, tokens, r.lse, r.entropy)
         ctx.mark_non_differentiable(r.lse, r.top_logprobs, r.top_ids)
         ctx.set_materialize_grads(False)

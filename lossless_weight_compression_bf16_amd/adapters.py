@@ -14,16 +14,7 @@ from . import _ops
 MAX_RANK = 256
 
 
-def add_adapters(x: torch.Tensor, y: torch.Tensor, a: torch.Tensor, b: torch.Tensor, ids: torch.Tensor,
-                 scales: torch.Tensor | None = None, check: bool = True, stream=None) -> torch.Tensor:
-    """y[t] += scales[i] B_i (A_i x[t]) with i = ids[t], in place; returns y.
-
-    x: m x cols BF16 or FP16; y: m x rows, FP32 or the type of x; a: n x rank
-    x cols and b: n x rows x rank in the type of x (rank at most 256, smaller
-    ones padded with zeros; cols a multiple of 8); ids: m int64, -1 for a
-    token without an adapter; scales: n FP32.  With check (which waits for
-    the GPU) an id out of range raises; without, its row of y stays as it
-    is."""
+def _check(x, y, a, b, ids, scales):
     for t, what in ((x, "x"), (y, "y"), (a, "a"), (b, "b"), (ids, "ids")):
         _ops.check_tensor(t, what, x.device)
     if x.dtype not in _ops.HALVES or a.dtype != x.dtype or b.dtype != x.dtype:
@@ -37,31 +28,57 @@ def add_adapters(x: torch.Tensor, y: torch.Tensor, a: torch.Tensor, b: torch.Ten
     if y.shape[0] != m or a.shape[2] != cols or tuple(b.shape) != (n, rows, rank):
         raise ValueError(f"shapes do not match: x {tuple(x.shape)}, y {tuple(y.shape)}, a {tuple(a.shape)}, "
                          f"b {tuple(b.shape)}")
-    if not 1 <= rank <= MAX_RANK or cols % 8 or not cols or not rows:
-        raise ValueError(f"the rank must be 1 to {MAX_RANK} and cols a multiple of 8, got {rank} and {cols}")
     if ids.dtype != torch.int64 or ids.shape != (m,):
         raise ValueError(f"ids must be {m} int64 numbers, one per row of x")
     if not a.is_contiguous() or not b.is_contiguous() or a.data_ptr() % 16:
         raise ValueError("a and b must be contiguous, and a 16-byte aligned")
-    if m and (y.stride(1) != 1 and rows > 1 or y.stride(0) < rows and m > 1):
+    if not _ops.rows_apart(y):
         raise ValueError("y must have unit column stride and rows that do not overlap")
     if scales is not None:
         _ops.check_tensor(scales, "scales", x.device)
         if scales.dtype != torch.float32 or scales.shape != (n,):
             raise ValueError(f"scales must be {n} float32 numbers")
-        scales = scales.contiguous()
+    raise ValueError(f"the rank must be 1 to {MAX_RANK}, cols a multiple of 8 and rank * rows below 2^31, got {rank}, "
+                     f"{cols} and {rows}")
+
+
+def add_adapters(x: torch.Tensor, y: torch.Tensor, a: torch.Tensor, b: torch.Tensor, ids: torch.Tensor,
+                 scales: torch.Tensor | None = None, check: bool = True, stream=None) -> torch.Tensor:
+    """y[t] += scales[i] B_i (A_i x[t]) with i = ids[t], in place; returns y.
+
+    x: m x cols BF16 or FP16; y: m x rows, FP32 or the type of x; a: n x rank
+    x cols and b: n x rows x rank in the type of x (rank at most 256, smaller
+    ones padded with zeros; cols a multiple of 8); ids: m int64, -1 for a
+    token without an adapter; scales: n FP32.  With check (which waits for
+    the GPU) an id out of range raises; without, its row of y stays as it
+    is."""
+    dev, dtype, y_type = x.device, x.dtype, y.dtype
+    if not (x.is_cuda and y.device == dev and a.device == dev and b.device == dev and ids.device == dev
+            and dtype in _ops.HALVES and a.dtype == dtype and b.dtype == dtype
+            and (y_type == dtype or y_type == torch.float32) and ids.dtype == torch.int64
+            and len(shape := x.shape) == 2 and len(sy := y.shape) == 2 and len(sa := a.shape) == 3
+            and sy[0] == shape[0] and sa[2] == shape[1] and b.shape == (sa[0], sy[1], sa[1]) and ids.shape == shape[:1]
+            and 1 <= sa[1] <= MAX_RANK and shape[1] and not shape[1] % 8 and sy[1] and sy[1] * sa[1] < 1 << 31
+            and a.is_contiguous() and b.is_contiguous() and not a.data_ptr() % 16 and _ops.rows_apart(y)
+            and (scales is None or scales.dtype == torch.float32 and scales.shape == sa[:1] and scales.device == dev)):
+        _check(x, y, a, b, ids, scales)
+    m, cols = shape
+    n, rank, _ = sa
+    rows = sy[1]
     x = _ops.rows16(x)
     ids = ids.contiguous()
+    scales = scales.contiguous() if scales is not None else None
 
     def call(raw):
-        nbytes = B.wc_add_adapters_scratch(m, rank, cols, rows)
-        scratch = torch.empty(nbytes, dtype=torch.uint8, device=x.device) if nbytes else None
-        err = torch.zeros(1, dtype=torch.int32, device=x.device) if check else None
+        lib = B.lib()
+        nbytes = lib.wc_add_adapters_scratch(m, rank, cols, rows)
+        scratch = torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
+        err = _ops.error_word(check, dev)
         g = B.wc_adapters(x.data_ptr(), x.stride(0), y.data_ptr(), y.stride(0), a.data_ptr(), b.data_ptr(),
                           ids.data_ptr(), scales.data_ptr() if scales is not None else 0, m, n, rank, cols, rows,
-                          _ops.TYPES[x.dtype], _ops.TYPES[y.dtype])
-        B.wc_add_adapters(g, scratch, nbytes, err, raw)
-        _ops.raise_bits(err, "add_adapters")
+                          _ops.TYPES[dtype], _ops.TYPES[y_type])
+        _ops.done(lib.wc_add_adapters(g, scratch.data_ptr() if nbytes else 0, nbytes, err.data_ptr() if check else 0,
+                                      raw), err, "add_adapters")
         return y
 
-    return _ops.on_stream(x.device, stream, call)
+    return _ops.on_stream(dev, stream, call)

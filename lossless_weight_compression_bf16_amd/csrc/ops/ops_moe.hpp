@@ -100,13 +100,20 @@ __global__ __launch_bounds__(256) void k_moe_route(MoeArgs g)
         acc[t] = f32x4{0.f, 0.f, 0.f, 0.f};
     }
     const uint32_t s0 = split * g.route_steps, s1 = min((g.cols + 31) / 32, s0 + g.route_steps);
-    for (uint32_t j = 0; s0 + wave_step<4>(wave, j) < s1; j++) {
-        const uint32_t k = 32 * (s0 + wave_step<4>(wave, j)) + 8 * gr;
-        const bool in = k < g.cols;
-        const X8 rv = __builtin_bit_cast(X8, in ? load16<16>(rr + k) : zero4());
+    for (uint32_t j = 0; s0 + wave_step<4>(wave, j) < s1; j += 2) {
+        X8 rv[2], xv[2][TT];
 #pragma unroll
-        for (int t = 0; t < TT; t++)
-            acc[t] = Ty::mfma(rv, __builtin_bit_cast(X8, in ? load16<16>(xr[t] + k) : zero4()), acc[t]);
+        for (int u = 0; u < 2; u++) {
+            const uint32_t st = s0 + wave_step<4>(wave, j + u), c = 32 * st + 8 * gr, k = min(c, g.cols - 8);
+            const bool in = st < s1 && c < g.cols;
+            rv[u] = __builtin_bit_cast(X8, only(in, load16<16>(rr + k)));
+#pragma unroll
+            for (int t = 0; t < TT; t++) xv[u][t] = __builtin_bit_cast(X8, only(in, load16<16>(xr[t] + k)));
+        }
+#pragma unroll
+        for (int u = 0; u < 2; u++)
+#pragma unroll
+            for (int t = 0; t < TT; t++) acc[t] = Ty::mfma(rv[u], xv[u][t], acc[t]);
     }
 #pragma unroll
     for (int t = 0; t < TT; t++) part[wave][t][lane] = acc[t];
@@ -190,7 +197,7 @@ __global__ __launch_bounds__(1024) void k_moe_route_one(MoeArgs g)
 {
     using Ty = Type<T>;
     using X8 = typename Ty::x8;
-    constexpr uint32_t W = 16;
+    constexpr uint32_t W = 16, U = 8;
     __shared__ float logits[W][64 * PER];
     const uint32_t wave = threadIdx.x >> 6, lane = threadIdx.x & 63, i = lane & 15, gr = lane >> 4;
     const uint32_t tiles = g.experts_pad / 16, steps = (g.cols + 31) / 32;
@@ -200,11 +207,17 @@ __global__ __launch_bounds__(1024) void k_moe_route_one(MoeArgs g)
         const uint32_t e0 = 16 * (it / pieces), pc = it % pieces, s1 = min(steps, (pc + 1) * piece);
         const uint16_t *rr = g.router + (uint64_t)min(e0 + i, g.experts - 1) * g.cols;
         f32x4 acc{0.f, 0.f, 0.f, 0.f};
-#pragma unroll 4
-        for (uint32_t st = pc * piece; st < s1; st++) {
-            const uint32_t c = 32 * st + 8 * gr, k = min(c, g.cols - 8);
-            const X8 rv = __builtin_bit_cast(X8, only(c < g.cols, load16<16>(rr + k)));
-            acc = Ty::mfma(rv, __builtin_bit_cast(X8, only(c < g.cols, load16<16>(xr + k))), acc);
+        for (uint32_t st = pc * piece; st < s1; st += U) {
+            X8 rv[U], xv[U];
+#pragma unroll
+            for (uint32_t u = 0; u < U; u++) {
+                const uint32_t c = 32 * (st + u) + 8 * gr, k = min(c, g.cols - 8);
+                const bool in = st + u < s1 && c < g.cols;
+                rv[u] = __builtin_bit_cast(X8, only(in, load16<16>(rr + k)));
+                xv[u] = __builtin_bit_cast(X8, only(in, load16<16>(xr + k)));
+            }
+#pragma unroll
+            for (uint32_t u = 0; u < U; u++) acc = Ty::mfma(rv[u], xv[u], acc);
         }
         if (i == 0) *reinterpret_cast<f32x4 *>(&logits[pc][e0 + 4 * gr]) = acc;
     }
@@ -353,15 +366,19 @@ __global__ __launch_bounds__(256) void k_moe_up(MoeArgs g)
 
 // One piece of one expert in k_moe_down: steps s0 .. s1 of W2's 16 rows (the
 // lane's at w2) against the expert's tokens, up to 16 NT of them, added into
-// sums.
-template <int T, int NT>
+// sums.  With kHalf, for up to 8 tokens, there are only 8 rows, and the
+// operands' other halves are the same rows and tokens at the second half of
+// the steps: of the product, the two quarters count where both are alike.
+template <int T, int NT, bool kHalf>
 __device__ __forceinline__ void moe_down_piece(const MoeArgs &g, const uint16_t *w2, const int32_t *place, uint32_t count,
                                                uint32_t s0, uint32_t s1, f32x4 (*sums)[4])
 {
     using Ty = Type<T>;
     using X8 = typename Ty::x8;
     constexpr int U = NT == 1 ? 4 : NT == 2 ? 2 : 1;  // steps on their way at once: NT U x 2 KiB of h
-    const uint32_t lane = threadIdx.x & 63, i = lane & 15, gr = lane >> 4;
+    const uint32_t lane = threadIdx.x & 63, gr = lane >> 4, i = kHalf ? lane & 7 : lane & 15;
+    const uint32_t half = kHalf ? (s1 - s0 + 1) / 2 : 0, second = kHalf && (lane & 8) ? half : 0;
+    const uint32_t e1 = kHalf ? min(s1, s0 + second + half) : s1;  // the end of the lane's steps
     const uint64_t plane = (uint64_t)g.m * g.top_k * g.inner;
     const uint16_t *hr[NT];
     int32_t at[NT];
@@ -372,13 +389,13 @@ __device__ __forceinline__ void moe_down_piece(const MoeArgs &g, const uint16_t 
         hr[t] = g.h + (uint64_t)at[t] * g.inner;
         acc[0][t] = acc[1][t] = f32x4{0.f, 0.f, 0.f, 0.f};
     }
-    for (uint32_t st = s0; st < s1; st += U) {
+    for (uint32_t st = s0; st < (kHalf ? s0 + half : s1); st += U) {
         X8 a[U], h0[U][NT], h1[U][NT];
 #pragma unroll
         for (int u = 0; u < U; u++) {
             // past the piece, or the rows' end, the operands are zero
-            const uint32_t c = 32 * (st + u) + 8 * gr, k = min(c, g.inner - 8);
-            const bool in = st + u < s1 && c < g.inner;
+            const uint32_t c = 32 * (st + u + second) + 8 * gr, k = min(c, g.inner - 8);
+            const bool in = st + u + second < e1 && c < g.inner;
             a[u] = __builtin_bit_cast(X8, only(in, load16<16>(w2 + k)));
 #pragma unroll
             for (int t = 0; t < NT; t++) {
@@ -398,26 +415,34 @@ __device__ __forceinline__ void moe_down_piece(const MoeArgs &g, const uint16_t 
     for (int t = 0; t < NT; t++) {
         if (16 * t + i < count) {
             const float p = g.weights[at[t]];
-            f32x4 &s = sums[(uint32_t)at[t] / g.top_k][gr];
-            s += p * (MoeTerms<T>::kScale[0] * acc[0][t] + MoeTerms<T>::kScale[1] * acc[1][t]);
+            const f32x4 v = p * (MoeTerms<T>::kScale[0] * acc[0][t] + MoeTerms<T>::kScale[1] * acc[1][t]);
+            if constexpr (!kHalf) {
+                sums[(uint32_t)at[t] / g.top_k][gr] += v;
+            } else {
+                f32x4 &s = sums[(uint32_t)at[t] / g.top_k][gr & 1];
+                if (lane < 32 && !(lane & 8)) s += v;
+                __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "wavefront");  // a wave's own LDS: in order
+                if (lane >= 32 && (lane & 8)) s += v;
+            }
         }
     }
 }
 
-// 16 columns of y (rows of W2).  Grid: columns / 16 x parts.  The experts
+// 16 columns of y (rows of W2), with kHalf 8.  Grid: columns / 16 (8) x parts.  The experts
 // with tokens, each cut into pieces along the inner rows where they are few,
 // go round the W waves of all parts; a wave adds its tokens' products, times
 // their weights, into a slice of LDS of its own, and at the end the slices
 // are added in the order of the waves.
-template <int T, int TT, int W>
+template <int T, int TT, int W, bool kHalf>
 __global__ __launch_bounds__(64 * W, 4) void k_moe_down(MoeArgs g)
 {
     using Ty = Type<T>;
+    constexpr uint32_t kRows = kHalf ? 8 : 16;
     __shared__ MoeSet set;
     __shared__ f32x4 sums[W][16 * TT][4];   // [wave][token][column / 4]
     __shared__ int32_t place[W][64];
-    const uint32_t wave = threadIdx.x >> 6, lane = threadIdx.x & 63, i = lane & 15;
-    const uint32_t part = blockIdx.x % g.parts, n0 = 16 * (blockIdx.x / g.parts);
+    const uint32_t wave = threadIdx.x >> 6, lane = threadIdx.x & 63, i = lane & (kRows - 1);
+    const uint32_t part = blockIdx.x % g.parts, n0 = kRows * (blockIdx.x / g.parts);
     for (uint32_t q = lane; q < 64 * TT; q += 64) sums[wave][q >> 2][q & 3] = f32x4{0.f, 0.f, 0.f, 0.f};
     set.fill(g);
     uint32_t expert;
@@ -438,14 +463,14 @@ __global__ __launch_bounds__(64 * W, 4) void k_moe_down(MoeArgs g)
         __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "wavefront");
         const uint16_t *w2 = g.w2 + (uint64_t)expert * g.down_expert + row;
         const uint32_t s0 = (it % pieces) * piece, s1 = min(steps, s0 + piece);
-        if (TT == 1 || count <= 16) moe_down_piece<T, 1>(g, w2, place[wave], count, s0, s1, sums[wave]);
-        else if (TT == 2 || count <= 32) moe_down_piece<T, 2>(g, w2, place[wave], count, s0, s1, sums[wave]);
-        else moe_down_piece<T, 4>(g, w2, place[wave], count, s0, s1, sums[wave]);
+        if (TT == 1 || count <= 16) moe_down_piece<T, 1, kHalf>(g, w2, place[wave], count, s0, s1, sums[wave]);
+        else if (TT == 2 || count <= 32) moe_down_piece<T, 2, false>(g, w2, place[wave], count, s0, s1, sums[wave]);
+        else moe_down_piece<T, 4, false>(g, w2, place[wave], count, s0, s1, sums[wave]);
     }
     __syncthreads();
     for (uint32_t q = threadIdx.x; q < 4 * g.m; q += 64 * W) {
         const uint32_t t = q >> 2, n = n0 + 4 * (q & 3);
-        if (n >= g.cols) continue;
+        if (4 * (q & 3) >= kRows || n >= g.cols) continue;
         f32x4 v = sums[0][t][q & 3];
 #pragma unroll
         for (int w = 1; w < W; w++) v += sums[w][t][q & 3];

@@ -84,12 +84,12 @@ AdapterPlan adapter_plan(uint64_t m, uint32_t rank, uint32_t cols, uint32_t rows
     const bool many = m > 512;
     p.rank_pad = (rank + 31) / 32 * 32;
     // one launch where all blocks' reading of A from the caches costs less
-    // than the second launch: at most 64 MiB, a block per 1,024 to 4,096 rows
+    // than the second launch: at most 16 MiB, a block per 1,024 to 4,096 rows
     const uint64_t reading = m * rank * cols * 2;
     for (uint32_t r = 1024; r <= 4096 && rank <= 64 && m <= 64 && !p.few; r *= 2) {
         p.row_block = r;
         p.row_blocks = (uint32_t)ceil_div(rows, r);
-        p.few = reading * p.row_blocks <= (64ull << 20);
+        p.few = reading * p.row_blocks <= (16ull << 20);
     }
     p.turns = many ? 1 : (uint32_t)(m < 16 ? m : 16);
     if (p.few) {
@@ -105,7 +105,7 @@ AdapterPlan adapter_plan(uint64_t m, uint32_t rank, uint32_t cols, uint32_t rows
     p.up_tile = wide ? 128 : 16;
     p.up_tiles = ceil_div(m, p.up_tile);
     const uint32_t least = wide ? 64 : 256;
-    uint64_t rb = ceil_div(4 * kCus, p.up_tiles * p.turns);
+    uint64_t rb = ceil_div((wide ? 4 : 8) * kCus, p.up_tiles * p.turns);
     const uint64_t rmost = ceil_div(rows, 256);
     if (rb > rmost) rb = rmost;
     p.row_block = (uint32_t)(ceil_div(ceil_div(rows, rb), least) * least);
@@ -172,6 +172,7 @@ wc_status launch_adapters(const AdapterArgs &g, const AdapterPlan &p, uint32_t y
 // Launch shapes and scratch of the mixture-of-experts layer.
 struct MoePlan {
     bool one;       // k_moe_route_one
+    bool half;      // k_moe_down on 8 columns
     uint32_t route_tiles, route_splits, route_steps, experts_pad, slots, up_tiles, down_tiles, down_waves, parts;
     uint64_t logits, ids, weights, h, part, bytes;  // offsets in the scratch
 };
@@ -181,8 +182,9 @@ MoePlan moe_plan(uint32_t m, uint32_t experts, uint32_t top_k, uint32_t cols, ui
     MoePlan p{};
     p.route_tiles = (experts + 15) / 16;
     p.experts_pad = 16 * p.route_tiles;
-    // one launch for the router where a block reads it in a few microseconds
-    p.one = (uint64_t)experts * cols * 2 <= (512u << 10) && experts <= 256;
+    // one launch for the router where one compute unit reads it in the time of
+    // a second launch: 64 KiB take 6 us, 256 KiB 13 us against 3 + 3 us in two
+    p.one = (uint64_t)experts * cols * 2 <= (64u << 10) && experts <= 256;
     const uint32_t steps = (cols + 31) / 32;
     uint32_t splits = 128 / p.route_tiles;
     const uint32_t most = (steps + 7) / 8;  // two steps for each of a block's waves
@@ -193,17 +195,21 @@ MoePlan moe_plan(uint32_t m, uint32_t experts, uint32_t top_k, uint32_t cols, ui
     p.route_splits = (uint32_t)ceil_div(steps, p.route_steps);
     p.slots = m * top_k < experts ? m * top_k : experts;
     p.up_tiles = (inner + 15) / 16;
-    p.down_tiles = (cols + 15) / 16;
-    // k_moe_down: 512 blocks of eight waves, split into parts where the
-    // columns are too few, which takes another launch; where all of W2's
+    // k_moe_down: 448 blocks or more of eight waves keep the memory busy.
+    // Where the columns are too few, blocks of 8 of them, which take up to 8
+    // tokens; then parts, which take another launch; where all of W2's
     // experts are under 64 MiB that costs more than it gives, and blocks have
-    // sixteen waves instead
+    // sixteen waves instead.
     const uint64_t reads = 2ull * p.slots * cols * inner;
+    const uint32_t enough = 7 * kCus / 4;
+    p.down_tiles = (cols + 15) / 16;
+    p.half = m <= 8 && p.down_tiles < enough;
+    if (p.half) p.down_tiles = (cols + 7) / 8;
     p.parts = 1;
     p.down_waves = 8;
-    if (p.down_tiles <= kCus && reads < (64ull << 20)) p.down_waves = 16;
+    if (p.down_tiles < enough && reads < (64ull << 20)) p.down_waves = 16;
     else
-        while (p.parts < 16 && p.down_tiles * p.parts < 7 * kCus / 4) p.parts *= 2;
+        while (p.parts < 16 && p.down_tiles * p.parts < enough) p.parts *= 2;
     uint64_t at = 0;
     auto take = [&](uint64_t bytes) {
         const uint64_t here = at;
@@ -241,8 +247,10 @@ wc_status launch_moe(const MoeArgs &g, const MoePlan &p, hipStream_t stream)
     }
     hipLaunchKernelGGL((k_moe_up<T, TT>), dim3(p.slots * p.up_tiles), dim3(256), 0, stream, g);
     const dim3 down(p.down_tiles * p.parts);
-    if (p.down_waves == 16) hipLaunchKernelGGL((k_moe_down<T, TT, 16>), down, dim3(1024), 0, stream, g);
-    else hipLaunchKernelGGL((k_moe_down<T, TT, 8>), down, dim3(512), 0, stream, g);
+    if (p.half && p.down_waves == 16) hipLaunchKernelGGL((k_moe_down<T, 1, 16, true>), down, dim3(1024), 0, stream, g);
+    else if (p.half) hipLaunchKernelGGL((k_moe_down<T, 1, 8, true>), down, dim3(512), 0, stream, g);
+    else if (p.down_waves == 16) hipLaunchKernelGGL((k_moe_down<T, TT, 16, false>), down, dim3(1024), 0, stream, g);
+    else hipLaunchKernelGGL((k_moe_down<T, TT, 8, false>), down, dim3(512), 0, stream, g);
     if (p.parts > 1)
         hipLaunchKernelGGL(k_moe_join<T>, dim3((g.m * (g.cols / 4) + 255) / 256), dim3(256), 0, stream, g);
     return launched();

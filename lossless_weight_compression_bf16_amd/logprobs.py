@@ -6,7 +6,6 @@ alternatives, and the gradient of the logits.
 """
 from __future__ import annotations
 
-import ctypes
 from typing import NamedTuple
 
 import torch
@@ -21,8 +20,8 @@ class TokenLogprobs(NamedTuple):
     logprob: torch.Tensor        # m, fp32: log probability of each row's token (0 for token -1)
     entropy: torch.Tensor        # m, fp32, in nats
     lse: torch.Tensor            # m, fp32: log of the sum of the exponentials
-    top_logprobs: torch.Tensor   # m x top, fp32, largest first
-    top_ids: torch.Tensor        # m x top, int64; equal logits by their index, NaN last
+    top_logprobs: torch.Tensor | None   # m x top, fp32, largest first; None without alternatives
+    top_ids: torch.Tensor | None        # m x top, int64; equal logits by their index, NaN last
 
 
 def _check(logits, tokens):
@@ -36,33 +35,42 @@ def _check(logits, tokens):
         raise ValueError("the vocabulary is empty")
 
 
+def _good(logits, tokens, device) -> bool:
+    return (logits.is_cuda and tokens.device == device and logits.dim() == 2 and logits.dtype in _ops.TYPES
+            and tokens.dtype == torch.int64 and tokens.shape == logits.shape[:1] and logits.shape[1] > 0)
+
+
 def _forward(logits, tokens, top, check, stream, views=True):
     z, t = _ops.rows_of(logits), tokens.contiguous()
     m, vocab = z.shape
+    dev = z.device
 
     def call(raw):
-        dev = z.device
+        best = ids = None
         if not views:  # autograd's outputs are tensors of their own
             rows = [torch.empty(m, dtype=torch.float32, device=dev) for _ in range(3)]
-            best = torch.empty((m, top), dtype=torch.float32, device=dev)
+            if top:
+                best = torch.empty((m, top), dtype=torch.float32, device=dev)
         elif top:  # one allocation for the fp32 outputs
-            *rows, best = torch.empty(m * (3 + top), dtype=torch.float32, device=dev).split((m, m, m, m * top))
+            *rows, best = torch.empty(m * (3 + top), dtype=torch.float32, device=dev).split_with_sizes(
+                (m, m, m, m * top))
             best = best.view(m, top)
         else:
             rows = torch.empty((3, m), dtype=torch.float32, device=dev).unbind(0)
-            best = torch.empty((m, 0), dtype=torch.float32, device=dev)
-        out = TokenLogprobs(*rows, best, torch.empty((m, top), dtype=torch.int64, device=dev))
-        nbytes = B.wc_token_logprobs_scratch(m, vocab, top)
+        if top:
+            ids = torch.empty((m, top), dtype=torch.int64, device=dev)
+        lib = B.lib()
+        nbytes = lib.wc_token_logprobs_scratch(m, vocab, top)
         scratch = torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
-        err = torch.zeros(1, dtype=torch.int32, device=dev) if check else None
+        err = _ops.error_word(check, dev)
         a = B.wc_logprobs(z.data_ptr(), z.stride(0), t.data_ptr(), m, vocab, top, _ops.TYPES[z.dtype], 0,
-                          out.logprob.data_ptr(), out.entropy.data_ptr(), out.lse.data_ptr(),
-                          out.top_logprobs.data_ptr(), out.top_ids.data_ptr())
-        B.wc_token_logprobs(a, scratch, nbytes, err, raw)
-        _ops.raise_bits(err, "token_logprobs")
-        return out
+                          rows[0].data_ptr(), rows[1].data_ptr(), rows[2].data_ptr(),
+                          best.data_ptr() if top else 0, ids.data_ptr() if top else 0)
+        _ops.done(lib.wc_token_logprobs(a, scratch.data_ptr() if nbytes else 0, nbytes,
+                                        err.data_ptr() if check else 0, raw), err, "token_logprobs")
+        return TokenLogprobs(*rows, best, ids)
 
-    return _ops.on_stream(z.device, stream, call)
+    return _ops.on_stream(dev, stream, call)
 
 
 def token_logprobs(logits: torch.Tensor, tokens: torch.Tensor, top: int = 0, check: bool = True,
@@ -74,7 +82,8 @@ def token_logprobs(logits: torch.Tensor, tokens: torch.Tensor, top: int = 0, che
     nothing but -inf has lse and log probabilities -inf and entropy 0; a row
     with NaN or +inf has NaN statistics.  With check (which waits for the
     GPU) a token out of range raises; without, its logprob is NaN."""
-    _check(logits, tokens)
+    if not _good(logits, tokens, logits.device):
+        _check(logits, tokens)
     if not 0 <= top <= min(MAX_TOP, logits.shape[1]):
         raise ValueError(f"top must be between 0 and {min(MAX_TOP, logits.shape[1])}, got {top}")
     if logits.requires_grad and torch.is_grad_enabled():
@@ -84,47 +93,48 @@ def token_logprobs(logits: torch.Tensor, tokens: torch.Tensor, top: int = 0, che
     return _forward(logits, tokens, top, check, stream)
 
 
+def _row_values(v, m, what, device):
+    if v is None:
+        return None
+    if not (v.dtype == torch.float32 and v.shape == (m,) and v.device == device):
+        _ops.check_tensor(v, what, device)
+        raise ValueError(f"{what} must be {m} float32 numbers")
+    return v.contiguous()
+
+
 def token_logprobs_backward(logits: torch.Tensor, tokens: torch.Tensor, lse: torch.Tensor, entropy=None,
                             grad_logprob=None, grad_entropy=None, out=None, check: bool = True,
                             stream=None) -> torch.Tensor:
     """The gradient of the logits, in their type, from the gradients of
     logprob and entropy (either may be None) and the lse and entropy that
     ``token_logprobs`` gave.  `out` may be the logits themselves."""
-    _check(logits, tokens)
+    dev = logits.device
+    if not _good(logits, tokens, dev):
+        _check(logits, tokens)
     z, t = _ops.rows_of(logits), tokens.contiguous()
     m, vocab = z.shape
-    if grad_entropy is not None and entropy is None:
-        raise ValueError("the gradient of the entropy needs the entropy")
-    kept = []  # contiguous copies live until the call is enqueued
-
-    def row_values(v, what):
-        if v is None:
-            return 0
-        _ops.check_tensor(v, what, z.device)
-        if v.dtype != torch.float32 or v.shape != (m,):
-            raise ValueError(f"{what} must be {m} float32 numbers")
-        kept.append(v if v.is_contiguous() else v.contiguous())
-        return kept[-1].data_ptr()
-
     if lse is None:
         raise ValueError("lse is needed")
-    p_lse, p_ent = row_values(lse, "lse"), row_values(entropy, "entropy")
-    p_glp, p_gent = row_values(grad_logprob, "grad_logprob"), row_values(grad_entropy, "grad_entropy")
+    if grad_entropy is not None and entropy is None:
+        raise ValueError("the gradient of the entropy needs the entropy")
+    lse, entropy = _row_values(lse, m, "lse", dev), _row_values(entropy, m, "entropy", dev)
+    gl, ge = _row_values(grad_logprob, m, "grad_logprob", dev), _row_values(grad_entropy, m, "grad_entropy", dev)
     if out is not None:
-        _ops.check_tensor(out, "out", z.device)
-        if out.dtype != z.dtype or out.shape != z.shape or (out.numel() and _ops.rows_of(out) is not out):
+        _ops.check_tensor(out, "out", dev)
+        if out.dtype != z.dtype or out.shape != z.shape or not _ops.rows_apart(out):
             raise ValueError("out must be like the logits, with unit column stride and rows that do not overlap")
 
     def call(raw):
-        o = torch.empty((m, vocab), dtype=z.dtype, device=z.device) if out is None else out
-        err = torch.zeros(1, dtype=torch.int32, device=z.device) if check else None
-        a = B.wc_logprobs_grad(z.data_ptr(), z.stride(0), o.data_ptr(), o.stride(0), t.data_ptr(), p_lse, p_ent,
-                               p_glp, p_gent, m, vocab, _ops.TYPES[z.dtype])
-        B.wc_token_logprobs_backward(a, err, raw)
-        _ops.raise_bits(err, "token_logprobs_backward")
+        o = torch.empty((m, vocab), dtype=z.dtype, device=dev) if out is None else out
+        err = _ops.error_word(check, dev)
+        a = B.wc_logprobs_grad(z.data_ptr(), z.stride(0), o.data_ptr(), o.stride(0), t.data_ptr(), lse.data_ptr(),
+                               entropy.data_ptr() if entropy is not None else 0, gl.data_ptr() if gl is not None else 0,
+                               ge.data_ptr() if ge is not None else 0, m, vocab, _ops.TYPES[z.dtype])
+        _ops.done(B.lib().wc_token_logprobs_backward(a, err.data_ptr() if check else 0, raw), err,
+                  "token_logprobs_backward")
         return o
 
-    return _ops.on_stream(z.device, stream, call)
+    return _ops.on_stream(dev, stream, call)
 
 
 class _TokenLogprobs(torch.autograd.Function):
@@ -132,7 +142,7 @@ class _TokenLogprobs(torch.autograd.Function):
     def forward(ctx, logits, tokens, top, check):
         r = _forward(logits, tokens, top, check, None, views=False)
         ctx.save_for_backward(logits, tokens, r.lse, r.entropy)
-        ctx.mark_non_differentiable(r.lse, r.top_logprobs, r.top_ids)
+        ctx.mark_non_differentiable(*(v for v in (r.lse, r.top_logprobs, r.top_ids) if v is not None))
         ctx.set_materialize_grads(False)
         return tuple(r)
 

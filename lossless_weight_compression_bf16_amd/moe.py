@@ -23,17 +23,7 @@ def _check_experts(t, what, shape, dtype, device):
         raise ValueError(f"{what} must have unit column stride and 16-byte aligned rows")
 
 
-def moe_layer(x: torch.Tensor, router: torch.Tensor, w1: torch.Tensor, w3: torch.Tensor, w2: torch.Tensor,
-              top_k: int, renormalize: bool = True, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
-    """sum over the top_k experts e of each token of weight_e W2_e
-    (silu(W1_e x) * (W3_e x)), m x cols in the type of x.
-
-    x: m x cols BF16 or FP16, m at most 64; router: experts x cols; w1 (gate)
-    and w3 (up): experts x inner x cols with the same strides (views of one
-    stacked tensor will do); w2 (down): experts x cols x inner; cols and
-    inner multiples of 8.  The weights are the softmax over all experts,
-    divided by the sum of the chosen ones with `renormalize`.  Equal logits
-    go to the expert with the lower number."""
+def _check(x, router, w1, w3, w2, top_k, out):
     _ops.check_tensor(x, "x")
     _ops.check_tensor(router, "router", x.device)
     if x.dtype not in _ops.HALVES or router.dtype != x.dtype:
@@ -54,20 +44,53 @@ def moe_layer(x: torch.Tensor, router: torch.Tensor, w1: torch.Tensor, w3: torch
         raise ValueError("w1 and w3 must have the same strides")
     if out is not None:
         _ops.check_tensor(out, "out", x.device)
-        if out.dtype != x.dtype or out.shape != x.shape or (m and _ops.rows_of(out) is not out):
+        if out.dtype != x.dtype or out.shape != x.shape or not _ops.rows_apart(out):
             raise ValueError("out must be like x, with unit column stride and rows that do not overlap")
+
+
+def _good(x, router, w1, w3, w2, top_k) -> bool:
+    """The plain case: everything contiguous."""
+    dev, dtype = x.device, x.dtype
+    if not (x.is_cuda and router.device == dev and w1.device == dev and w3.device == dev and w2.device == dev
+            and dtype in _ops.HALVES and router.dtype == dtype and w1.dtype == dtype and w3.dtype == dtype
+            and w2.dtype == dtype and x.dim() == 2 and router.dim() == 2):
+        return False
+    (m, cols), experts, s1 = x.shape, router.shape[0], w1.shape
+    return (len(s1) == 3 and router.shape[1] == cols and s1 == (experts, s1[1], cols) and w3.shape == s1
+            and w2.shape == (experts, cols, s1[1]) and m <= MAX_TOKENS and experts <= MAX_EXPERTS
+            and 1 <= top_k <= experts and top_k <= MAX_TOP_K and 8 <= cols <= 1 << 20 and 8 <= s1[1] <= 1 << 20
+            and not cols % 8 and not s1[1] % 8 and w1.is_contiguous() and w3.is_contiguous() and w2.is_contiguous()
+            and not (w1.data_ptr() | w3.data_ptr() | w2.data_ptr()) % 16)
+
+
+def moe_layer(x: torch.Tensor, router: torch.Tensor, w1: torch.Tensor, w3: torch.Tensor, w2: torch.Tensor,
+              top_k: int, renormalize: bool = True, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """sum over the top_k experts e of each token of weight_e W2_e
+    (silu(W1_e x) * (W3_e x)), m x cols in the type of x.
+
+    x: m x cols BF16 or FP16, m at most 64; router: experts x cols; w1 (gate)
+    and w3 (up): experts x inner x cols with the same strides (views of one
+    stacked tensor will do); w2 (down): experts x cols x inner; cols and
+    inner multiples of 8.  The weights are the softmax over all experts,
+    divided by the sum of the chosen ones with `renormalize`.  Equal logits
+    go to the expert with the lower number."""
+    if out is not None or not _good(x, router, w1, w3, w2, top_k):
+        _check(x, router, w1, w3, w2, top_k, out)
     x = _ops.rows16(x)
     router = router if router.is_contiguous() and router.data_ptr() % 16 == 0 else router.clone(
         memory_format=torch.contiguous_format)
+    (m, cols), (experts, inner, _), dev = x.shape, w1.shape, x.device
 
     def call(raw):
-        o = torch.empty((m, cols), dtype=x.dtype, device=x.device) if out is None else out
-        nbytes = B.wc_moe_layer_scratch(m, experts, top_k, cols, inner)
-        scratch = torch.empty(nbytes, dtype=torch.uint8, device=x.device)
+        lib = B.lib()
+        o = torch.empty((m, cols), dtype=x.dtype, device=dev) if out is None else out
+        nbytes = lib.wc_moe_layer_scratch(m, experts, top_k, cols, inner)
+        scratch = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+        up, down = w1.stride(), w2.stride()
         g = B.wc_moe(x.data_ptr(), x.stride(0), router.data_ptr(), w1.data_ptr(), w3.data_ptr(), w2.data_ptr(),
-                     w1.stride(0), w1.stride(1), w2.stride(0), w2.stride(1), o.data_ptr(), o.stride(0), m, experts,
-                     top_k, cols, inner, _ops.TYPES[x.dtype], int(renormalize))
-        B.wc_moe_layer(g, scratch, nbytes, raw)
+                     up[0], up[1], down[0], down[1], o.data_ptr(), o.stride(0), m, experts, top_k, cols, inner,
+                     _ops.TYPES[x.dtype], 1 if renormalize else 0)
+        _ops.done(lib.wc_moe_layer(g, scratch.data_ptr(), nbytes, raw), None, "moe_layer")
         return o
 
-    return _ops.on_stream(x.device, stream, call)
+    return _ops.on_stream(dev, stream, call)

@@ -82,7 +82,7 @@ def _near(got, want, tol, what):
 
 def _check(z, tokens, top, r, what, rows=None):
     zs = z.double().cpu().numpy()
-    r = [t.cpu().numpy() for t in r]
+    r = [None if t is None else t.cpu().numpy() for t in r]
     for i in range(zs.shape[0]) if rows is None else rows:
         row, t = zs[i], int(tokens[i])
         lse, lp, ent = _expect(row, t)

@@ -459,7 +459,7 @@ typedef struct {
     const void *w3;         /* the same (up) */
     const void *w2;         /* experts x cols x inner (down) */
     uint64_t up_expert;     /* elements from one expert, and one row, of w1 and w3 to the next: */
-    uint64_t up_row;        /*   multiples of 8 */
+    uint64_t up_row;        /*   multiples of 8, rows at most 2^26 */
     uint64_t down_expert;   /* of w2 */
     uint64_t down_row;
     void *out;              /* m x cols, rows out_stride elements apart, any alignment */

@@ -33,6 +33,10 @@ struct Unaligned<4> {
     typedef uint32_t x2 __attribute__((ext_vector_type(2), aligned(4)));
     typedef uint32_t x4 __attribute__((ext_vector_type(4), aligned(4)));
 };
+template <>
+struct Unaligned<16> {
+    typedef u32x4 x4;
+};
 
 template <int T>
 struct Type;

@@ -7,14 +7,14 @@
 //   k_moe_select  softmax and the top_k of each token: one wave per token
 //   k_moe_route_one  both, where the router is small: one block per token
 //   k_moe_up      h = silu(W1 x) * (W3 x), for every expert with tokens
-//   k_moe_down    y = sum p W2 h, in the order of the experts
-//   k_moe_join    where few rows of y make k_moe_down split the experts
+//   k_moe_down    p W2 h of every expert, and k_moe_join their sums; or
+//   k_moe_down_few  both at once, for up to 8 tokens on small experts
 // What bounds it: every expert that has tokens is read once, 6 bytes per
 // row and column; with few tokens that is all the time there is.  So weights
-// go from memory into the matrix cores' registers in their own row-major
-// layout (no repacked copy), 16 rows of weights against 16 tokens per MFMA,
-// and experts with more than 16 tokens meet them all while their weights are
-// in registers.  Products are exact and summed in fp32.
+// stay in their own row-major layout (no repacked copy), are read in whole
+// lines and reach the matrix cores through LDS (Strip), 16 rows of weights
+// against 16 tokens per MFMA, and experts with more than 16 tokens meet them
+// all while their weights are there.  Products are exact and summed in fp32.
 //
 // h leaves k_moe_up as two 16-bit terms, BF16 h = a + b (16 bits), FP16
 // h / 256 = a + b / 4096 with a and b accumulated apart (22 bits, |h| up to
@@ -45,8 +45,8 @@ struct MoeArgs {
     int32_t *ids;         // m x top_k
     float *weights;       // m x top_k
     uint16_t *h;          // 2 terms x (m top_k) x inner
-    float *part;          // parts x m x cols
-    uint32_t experts_pad, route_splits, route_steps, slots, parts;
+    float *part;          // (m top_k) x cols: each expert's part of y
+    uint32_t experts_pad, route_splits, route_steps, slots;
 };
 
 template <int T>
@@ -278,83 +278,204 @@ struct MoeSet {
     }
 };
 
-// A wave's share of the columns for 16 rows (the lane's at `row`) of W1 and W3
-// of one expert against its tokens, up to 16 NT of them, into part.
-template <int T, int NT, int TT>
-__device__ __forceinline__ void moe_up_rows(const MoeArgs &g, uint64_t row, const int32_t *place, uint32_t count,
-                                            f32x4 (&part)[4][2 * TT][64])
+// Sixteen rows of weights through a wave's own LDS, 256 columns at a time.
+// Read in operand order, an instruction takes 64 bytes of each of 16 rows,
+// halves of lines; read along the rows, 512 bytes of each of two, whole
+// lines, past the caches: 7.1 against 5.8 TB/s over a large buffer, and 6.3
+// against 3.6 TB/s where every compute unit has 256 KiB to read.  LDS turns
+// one order into the other; rows lie 576 bytes apart, so that the 16 rows of
+// an operand spread over all banks.
+constexpr uint32_t kStripCols = 256, kStripPitch = 36;  // pitch in 16 bytes
+struct Strip {
+    u32x4 q[16 * kStripPitch];
+};
+
+// acc[m][o][t] += W_m X_t over columns c0 .. c1 (multiples of 8) for M
+// matrices of 16 rows and NT tiles of 16 tokens whose numbers are sums of O
+// terms.  weights[m]: the first row; row(r): elements from there to row r;
+// tokens(o, t): the lane's column of term o.  Loads past the end repeat the
+// last 8 columns, and the operands are zero there.  With kHalves rows 8..15
+// and columns 8..15 end at c1b.  The next columns are on their way while these
+// are multiplied.
+template <int T, int M, int O, int NT, bool kHalves, class Row, class Tokens>
+__device__ __forceinline__ void strip_product(const uint16_t *const (&weights)[M], Row row, Tokens tokens, uint32_t c0,
+                                              uint32_t c1, uint32_t c1b, Strip *strips, f32x4 (&acc)[M][O][NT])
 {
     using Ty = Type<T>;
     using X8 = typename Ty::x8;
-    constexpr int U = NT == 4 ? 2 : 4;  // steps on their way at once
-    const uint32_t wave = threadIdx.x >> 6, lane = threadIdx.x & 63, i = lane & 15, gr = lane >> 4;
-    const uint16_t *w1 = g.w1 + row, *w3 = g.w3 + row, *xr[NT];
-    f32x4 acc[2][NT];
+    constexpr int kSteps = kStripCols / 32, S = 16 / (O * NT) < kSteps ? 16 / (O * NT) : kSteps;
+    const uint32_t lane = threadIdx.x & 63, i = lane & 15, gr = lane >> 4, hi = lane >> 5, lo = lane & 31;
+    uint32_t off[8];
 #pragma unroll
-    for (int t = 0; t < NT; t++) {
-        xr[t] = g.x + (uint64_t)((uint32_t)place[min(16 * t + i, count - 1)] / g.top_k) * g.x_stride;
-        acc[0][t] = acc[1][t] = f32x4{0.f, 0.f, 0.f, 0.f};
-    }
-    for (uint32_t j = 0; 32 * wave_step<4>(wave, j) < g.cols; j += U) {
-        X8 a[U], b[U], xv[U][NT];
+    for (int u = 0; u < 8; u++) off[u] = row(2 * u + hi);
+    const uint16_t *tk[O][NT];
 #pragma unroll
-        for (int u = 0; u < U; u++) {
-            // past the rows' end the loads repeat their last numbers, and the operands are zero
-            const uint32_t c = 32 * wave_step<4>(wave, j + u) + 8 * gr, k = min(c, g.cols - 8);
-            const bool in = c < g.cols;
-            a[u] = __builtin_bit_cast(X8, only(in, load16<16>(w1 + k)));
-            b[u] = __builtin_bit_cast(X8, only(in, load16<16>(w3 + k)));
+    for (int o = 0; o < O; o++)
 #pragma unroll
-            for (int t = 0; t < NT; t++) xv[u][t] = __builtin_bit_cast(X8, only(in, load16<16>(xr[t] + k)));
+        for (int t = 0; t < NT; t++) tk[o][t] = tokens(o, t);
+    u32x4 v[M][8], x[S][O][NT];
+    const uint32_t last = c1 - 8, lastb = kHalves && c1b ? c1b - 8 : 0;
+    const uint32_t xend = kHalves && i >= 8 ? c1b : c1, xlast = kHalves && i >= 8 ? lastb : last;
+    auto fetch = [&](uint32_t c) {
+#pragma unroll
+        for (int m = 0; m < M; m++)
+#pragma unroll
+            for (int u = 0; u < 8; u++)
+                v[m][u] = read16<16, true>(weights[m] + (off[u] + min(c + 8 * lo, kHalves && u >= 4 ? lastb : last)));
+    };
+    auto fetch_x = [&](uint32_t c, int s0) {
+#pragma unroll
+        for (int s = 0; s < S; s++) {
+            const uint32_t k = min(c + 32 * (s0 + s) + 8 * gr, xlast);
+#pragma unroll
+            for (int o = 0; o < O; o++)
+#pragma unroll
+                for (int t = 0; t < NT; t++) x[s][o][t] = load16<16>(tk[o][t] + k);
         }
-#pragma unroll
-        for (int u = 0; u < U; u++)
-#pragma unroll
-            for (int t = 0; t < NT; t++) {
-                acc[0][t] = Ty::mfma(a[u], xv[u][t], acc[0][t]);
-                acc[1][t] = Ty::mfma(b[u], xv[u][t], acc[1][t]);
-            }
+    };
+    if (c0 < c1) {
+        fetch(c0);
+        fetch_x(c0, 0);
     }
+    for (uint32_t c = c0; c < c1; c += kStripCols) {
+        __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "wavefront");  // a wave's own LDS: in order
 #pragma unroll
-    for (int t = 0; t < NT; t++) {
-        part[wave][t][lane] = acc[0][t];
-        part[wave][TT + t][lane] = acc[1][t];
+        for (int m = 0; m < M; m++)
+#pragma unroll
+            for (int u = 0; u < 8; u++)
+                strips[m].q[(2 * u + hi) * kStripPitch + lo] = only(c + 8 * lo < (kHalves && u >= 4 ? c1b : c1), v[m][u]);
+        __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "wavefront");
+        if (c + kStripCols < c1) fetch(c + kStripCols);
+#pragma unroll
+        for (int s0 = 0; s0 < kSteps; s0 += S) {
+            if (s0) fetch_x(c, s0);
+#pragma unroll
+            for (int s = 0; s < S; s++) {
+                const bool in = c + 32 * (s0 + s) + 8 * gr < xend;
+                X8 a[M];
+#pragma unroll
+                for (int m = 0; m < M; m++)
+                    a[m] = __builtin_bit_cast(X8, strips[m].q[i * kStripPitch + 4 * (s0 + s) + gr]);
+#pragma unroll
+                for (int o = 0; o < O; o++)
+#pragma unroll
+                    for (int t = 0; t < NT; t++) {
+                        const X8 b = __builtin_bit_cast(X8, only(in, x[s][o][t]));
+#pragma unroll
+                        for (int m = 0; m < M; m++) acc[m][o][t] = Ty::mfma(a[m], b, acc[m][o][t]);
+                    }
+            }
+        }
+        if (c + kStripCols < c1) fetch_x(c + kStripCols, 0);
     }
 }
 
-// h of 16 inner rows of one expert.  Grid: slots x inner / 16; a slot is the
-// p-th expert that has tokens.  Columns over the four waves.
-template <int T, int TT>
-__global__ __launch_bounds__(256) void k_moe_up(MoeArgs g)
+// A wave's share of the columns for 16 rows of W1 and W3 of one expert against
+// its tokens, up to 16 NT of them.
+template <int T, int NT, int TT>
+__device__ __forceinline__ void moe_up_rows(const MoeArgs &g, uint32_t expert, uint32_t n0, const int32_t *place,
+                                            uint32_t count, uint32_t c0, uint32_t c1, Strip *strips,
+                                            f32x4 (&gate)[TT], f32x4 (&up)[TT])
 {
-    __shared__ MoeSet set;
-    __shared__ f32x4 part[4][2 * TT][64];
-    __shared__ int32_t place[64];  // token top_k + choice of column c
-    const uint32_t wave = threadIdx.x >> 6, lane = threadIdx.x & 63, i = lane & 15, gr = lane >> 4;
-    const uint32_t slot = blockIdx.x % g.slots, n0 = 16 * (blockIdx.x / g.slots);
+    const uint32_t i = threadIdx.x & 15;
+    const uint64_t at = (uint64_t)expert * g.up_expert + (uint64_t)n0 * g.up_row;
+    const uint16_t *const weights[2] = {g.w1 + at, g.w3 + at};
+    const uint32_t rows = min(g.inner - n0, 16u), stride = (uint32_t)g.up_row;
+    f32x4 acc[2][1][NT];
+#pragma unroll
+    for (int t = 0; t < NT; t++) acc[0][0][t] = acc[1][0][t] = f32x4{0.f, 0.f, 0.f, 0.f};
+    strip_product<T, 2, 1, NT, false>(
+        weights, [&](uint32_t r) { return min(r, rows - 1) * stride; },
+        [&](int, int t) { return g.x + (uint64_t)((uint32_t)place[min(16 * t + i, count - 1)] / g.top_k) * g.x_stride; },
+        c0, c1, c1, strips, acc);
+#pragma unroll
+    for (int t = 0; t < NT; t++) {
+        gate[t] = acc[0][0][t];
+        up[t] = acc[1][0][t];
+    }
+}
+
+// A wave's share of the inner rows c0 .. c1 (kHalves: .. c1b) for 16 rows of
+// W2 of one expert against its tokens' h from `shift` on; column: the lane's.
+template <int T, int NT, int TT, bool kHalves, class Row>
+__device__ __forceinline__ void moe_down_rows(const MoeArgs &g, const uint16_t *w2, Row row, const int32_t *place,
+                                              uint32_t count, uint32_t column, uint32_t shift, uint32_t c0, uint32_t c1,
+                                              uint32_t c1b, Strip *strips, f32x4 (&sum)[TT])
+{
+    const uint64_t plane = (uint64_t)g.m * g.top_k * g.inner;
+    const uint16_t *const weights[1] = {w2};
+    f32x4 acc[1][2][NT];
+#pragma unroll
+    for (int t = 0; t < NT; t++) acc[0][0][t] = acc[0][1][t] = f32x4{0.f, 0.f, 0.f, 0.f};
+    strip_product<T, 1, 2, NT, kHalves>(
+        weights, row,
+        [&](int o, int t) { return g.h + o * plane + (uint64_t)place[min(16 * t + column, count - 1)] * g.inner + shift; },
+        c0, c1, c1b, strips, acc);
+#pragma unroll
+    for (int t = 0; t < NT; t++) sum[t] = MoeTerms<T>::kScale[0] * acc[0][0][t] + MoeTerms<T>::kScale[1] * acc[0][1][t];
+}
+
+// The columns of one of four waves: a quarter, in multiples of `unit`.
+__device__ __forceinline__ void wave_quarter(uint32_t cols, uint32_t unit, uint32_t wave, uint32_t &c0, uint32_t &c1)
+{
+    const uint32_t per = ((cols + 4 * unit - 1) / (4 * unit)) * unit;
+    c0 = min(cols, wave * per);
+    c1 = min(cols, c0 + per);
+}
+
+// A block's expert, the slot-th that has tokens, and its tokens: place[c] is
+// token top_k + choice of column c.  Their number; 0 past the last expert.
+__device__ __forceinline__ uint32_t moe_block(const MoeArgs &g, uint32_t slot, MoeSet &set, int32_t (&place)[64],
+                                              uint32_t &expert)
+{
     set.fill(g);
-    uint32_t expert;
-    if (slot >= set.find(slot, expert)) return;
+    if (slot >= set.find(slot, expert)) return 0;
     const int32_t mine = set.choice(g, expert);
     const uint64_t mask = __ballot(mine >= 0);
-    const uint32_t count = (uint32_t)__popcll(mask);
-    if (mine >= 0) place[__popcll(mask & ((1ull << lane) - 1))] = mine;  // the same from every wave
+    if (mine >= 0) place[__popcll(mask & ((1ull << (threadIdx.x & 63)) - 1))] = mine;  // the same from every wave
     __syncthreads();
-    const uint64_t row = (uint64_t)expert * g.up_expert + (uint64_t)min(n0 + i, g.inner - 1) * g.up_row;
-    if (TT == 1 || count <= 16) moe_up_rows<T, 1, TT>(g, row, place, count, part);
-    else if (TT == 2 || count <= 32) moe_up_rows<T, 2, TT>(g, row, place, count, part);
-    else moe_up_rows<T, 4, TT>(g, row, place, count, part);
+    return (uint32_t)__popcll(mask);
+}
+
+// h of 16 inner rows of one expert.  Grid: slots x inner / 16.  Columns over
+// the four waves.
+template <int T, int TT>
+__global__ __launch_bounds__(256, 2) void k_moe_up(MoeArgs g)
+{
+    __shared__ MoeSet set;
+    __shared__ int32_t place[64];
+    __shared__ Strip strips[4][2];
+    f32x4(*part)[2 * TT][64] = reinterpret_cast<f32x4(*)[2 * TT][64]>(&strips[0][0]);  // [4], when the strips are done
+    static_assert(sizeof(strips) >= 4 * 2 * TT * 64 * 16, "the waves' sums fit into the strips");
+    const uint32_t wave = threadIdx.x >> 6, lane = threadIdx.x & 63, i = lane & 15, gr = lane >> 4;
+    const uint32_t slot = blockIdx.x % g.slots, n0 = 16 * (blockIdx.x / g.slots);
+    uint32_t expert, c0, c1;
+    const uint32_t count = moe_block(g, slot, set, place, expert);
+    if (count == 0) return;
+    wave_quarter(g.cols, kStripCols, wave, c0, c1);
+    f32x4 gate[TT], up[TT];
+    if (TT == 1 || count <= 16) moe_up_rows<T, 1, TT>(g, expert, n0, place, count, c0, c1, strips[wave], gate, up);
+    else if (TT == 2 || count <= 32) moe_up_rows<T, 2, TT>(g, expert, n0, place, count, c0, c1, strips[wave], gate, up);
+    else moe_up_rows<T, 4, TT>(g, expert, n0, place, count, c0, c1, strips[wave], gate, up);
+    __syncthreads();
+#pragma unroll
+    for (int t = 0; t < TT; t++) {
+        if (16 * t < (int)count) {
+            part[wave][t][lane] = gate[t];
+            part[wave][TT + t][lane] = up[t];
+        }
+    }
     __syncthreads();
     const uint32_t n = n0 + 4 * gr, c = 16 * wave + i;
     if (wave < TT && c < count && n < g.inner) {
-        const f32x4 gate = (part[0][wave][lane] + part[1][wave][lane]) + (part[2][wave][lane] + part[3][wave][lane]);
         const uint32_t q = TT + wave;
-        const f32x4 up = (part[0][q][lane] + part[1][q][lane]) + (part[2][q][lane] + part[3][q][lane]);
+        const f32x4 gv = (part[0][wave][lane] + part[1][wave][lane]) + (part[2][wave][lane] + part[3][wave][lane]);
+        const f32x4 uv = (part[0][q][lane] + part[1][q][lane]) + (part[2][q][lane] + part[3][q][lane]);
         uint16_t a[4], b[4];
 #pragma unroll
         for (int e = 0; e < 4; e++) {
-            const float v = gate[e];
-            MoeTerms<T>::split(v / (1.f + exp2_fast(-v * kLog2e)) * up[e], a[e], b[e]);
+            const float v = gv[e];
+            MoeTerms<T>::split(v / (1.f + exp2_fast(-v * kLog2e)) * uv[e], a[e], b[e]);
         }
         uint16_t *h = g.h + (uint64_t)place[c] * g.inner + n;
         const u32x2 va{(uint32_t)a[0] | ((uint32_t)a[1] << 16), (uint32_t)a[2] | ((uint32_t)a[3] << 16)};
@@ -364,96 +485,81 @@ __global__ __launch_bounds__(256) void k_moe_up(MoeArgs g)
     }
 }
 
-// One piece of one expert in k_moe_down: steps s0 .. s1 of W2's 16 rows (the
-// lane's at w2) against the expert's tokens, up to 16 NT of them, added into
-// sums.  With kHalf, for up to 8 tokens, there are only 8 rows, and the
-// operands' other halves are the same rows and tokens at the second half of
-// the steps: of the product, the two quarters count where both are alike.
-template <int T, int NT, bool kHalf>
-__device__ __forceinline__ void moe_down_piece(const MoeArgs &g, const uint16_t *w2, const int32_t *place, uint32_t count,
-                                               uint32_t s0, uint32_t s1, f32x4 (*sums)[4])
+// p W2 h of one expert into part[token top_k + choice].  Grid: slots x
+// columns / 64 (kSplit: / 16).  A wave has 16 rows of W2 of its own, or with
+// kSplit, where blocks would be too few, a quarter of the inner rows.
+template <int T, int TT, bool kSplit>
+__global__ __launch_bounds__(256, 3) void k_moe_down(MoeArgs g)
 {
-    using Ty = Type<T>;
-    using X8 = typename Ty::x8;
-    constexpr int U = NT == 1 ? 4 : NT == 2 ? 2 : 1;  // steps on their way at once: NT U x 2 KiB of h
-    const uint32_t lane = threadIdx.x & 63, gr = lane >> 4, i = kHalf ? lane & 7 : lane & 15;
-    const uint32_t half = kHalf ? (s1 - s0 + 1) / 2 : 0, second = kHalf && (lane & 8) ? half : 0;
-    const uint32_t e1 = kHalf ? min(s1, s0 + second + half) : s1;  // the end of the lane's steps
-    const uint64_t plane = (uint64_t)g.m * g.top_k * g.inner;
-    const uint16_t *hr[NT];
-    int32_t at[NT];
-    f32x4 acc[2][NT];
-#pragma unroll
-    for (int t = 0; t < NT; t++) {
-        at[t] = place[min(16 * t + i, count - 1)];
-        hr[t] = g.h + (uint64_t)at[t] * g.inner;
-        acc[0][t] = acc[1][t] = f32x4{0.f, 0.f, 0.f, 0.f};
+    __shared__ MoeSet set;
+    __shared__ int32_t place[64];
+    __shared__ Strip strips[4];
+    f32x4(*sums)[TT][64] = reinterpret_cast<f32x4(*)[TT][64]>(&strips[0]);  // [4], when the strips are done
+    static_assert(sizeof(strips) >= 4 * TT * 64 * 16, "the waves' sums fit into the strips");
+    const uint32_t wave = threadIdx.x >> 6, lane = threadIdx.x & 63, i = lane & 15, gr = lane >> 4;
+    const uint32_t slot = blockIdx.x % g.slots;
+    const uint32_t n0 = kSplit ? 16 * (blockIdx.x / g.slots) : 64 * (blockIdx.x / g.slots) + 16 * wave;
+    uint32_t expert, c0 = 0, c1 = g.inner;
+    const uint32_t count = moe_block(g, slot, set, place, expert);
+    if (count == 0) return;
+    if (kSplit) wave_quarter(g.inner, kStripCols, wave, c0, c1);
+    f32x4 sum[TT];
+    if (n0 < g.cols) {
+        const uint16_t *w2 = g.w2 + (uint64_t)expert * g.down_expert + (uint64_t)n0 * g.down_row;
+        const uint32_t rows = min(g.cols - n0, 16u), stride = (uint32_t)g.down_row;
+        auto row = [&](uint32_t r) { return min(r, rows - 1) * stride; };
+        if (TT == 1 || count <= 16) moe_down_rows<T, 1, TT, false>(g, w2, row, place, count, i, 0, c0, c1, c1, &strips[wave], sum);
+        else if (TT == 2 || count <= 32) moe_down_rows<T, 2, TT, false>(g, w2, row, place, count, i, 0, c0, c1, c1, &strips[wave], sum);
+        else moe_down_rows<T, 4, TT, false>(g, w2, row, place, count, i, 0, c0, c1, c1, &strips[wave], sum);
     }
-    for (uint32_t st = s0; st < (kHalf ? s0 + half : s1); st += U) {
-        X8 a[U], h0[U][NT], h1[U][NT];
+    if constexpr (kSplit) {
+        __syncthreads();
 #pragma unroll
-        for (int u = 0; u < U; u++) {
-            // past the piece, or the rows' end, the operands are zero
-            const uint32_t c = 32 * (st + u + second) + 8 * gr, k = min(c, g.inner - 8);
-            const bool in = st + u + second < e1 && c < g.inner;
-            a[u] = __builtin_bit_cast(X8, only(in, load16<16>(w2 + k)));
-#pragma unroll
-            for (int t = 0; t < NT; t++) {
-                h0[u][t] = __builtin_bit_cast(X8, only(in, load16<16>(hr[t] + k)));
-                h1[u][t] = __builtin_bit_cast(X8, only(in, load16<16>(hr[t] + plane + k)));
-            }
-        }
-#pragma unroll
-        for (int u = 0; u < U; u++)
-#pragma unroll
-            for (int t = 0; t < NT; t++) {
-                acc[0][t] = Ty::mfma(a[u], h0[u][t], acc[0][t]);
-                acc[1][t] = Ty::mfma(a[u], h1[u][t], acc[1][t]);
-            }
+        for (int t = 0; t < TT; t++)
+            if (16 * t < (int)count) sums[wave][t][lane] = sum[t];
+        __syncthreads();
     }
+    const uint32_t n = n0 + 4 * gr;
+    if (n >= g.cols) return;
 #pragma unroll
-    for (int t = 0; t < NT; t++) {
-        if (16 * t + i < count) {
-            const float p = g.weights[at[t]];
-            const f32x4 v = p * (MoeTerms<T>::kScale[0] * acc[0][t] + MoeTerms<T>::kScale[1] * acc[1][t]);
-            if constexpr (!kHalf) {
-                sums[(uint32_t)at[t] / g.top_k][gr] += v;
-            } else {
-                f32x4 &s = sums[(uint32_t)at[t] / g.top_k][gr & 1];
-                if (lane < 32 && !(lane & 8)) s += v;
-                __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "wavefront");  // a wave's own LDS: in order
-                if (lane >= 32 && (lane & 8)) s += v;
-            }
-        }
+    for (int t = 0; t < TT; t++) {
+        if ((kSplit && t != (int)wave) || 16 * t + i >= count) continue;
+        f32x4 v = sum[t];
+        if constexpr (kSplit) v = (sums[0][t][lane] + sums[1][t][lane]) + (sums[2][t][lane] + sums[3][t][lane]);
+        const uint32_t at = (uint32_t)place[16 * t + i];
+        *reinterpret_cast<f32x4 *>(g.part + (uint64_t)at * g.cols + n) = g.weights[at] * v;
     }
 }
 
-// 16 columns of y (rows of W2), with kHalf 8.  Grid: columns / 16 (8) x parts.  The experts
-// with tokens, each cut into pieces along the inner rows where they are few,
-// go round the W waves of all parts; a wave adds its tokens' products, times
-// their weights, into a slice of LDS of its own, and at the end the slices
-// are added in the order of the waves.
-template <int T, int TT, int W, bool kHalf>
-__global__ __launch_bounds__(64 * W, 4) void k_moe_down(MoeArgs g)
+// y of 8 columns (rows of W2) for up to 8 tokens, where all experts of W2
+// together are small and another launch to join them would cost more than it
+// gives.  The operands' 16 rows are the 8 rows at the first and at the second
+// half of the inner rows, and so are the tokens' columns: of the product, the
+// two quarters count where both are alike.  The experts with tokens, each cut
+// into pieces along the inner rows where they are few, go round the sixteen
+// waves; a wave adds its tokens' products, times their weights, into a slice
+// of LDS of its own, and at the end the slices are added in the order of the
+// waves.
+template <int T>
+__global__ __launch_bounds__(1024) void k_moe_down_few(MoeArgs g)
 {
-    using Ty = Type<T>;
-    constexpr uint32_t kRows = kHalf ? 8 : 16;
+    constexpr uint32_t W = 16, kTokens = 8;
     __shared__ MoeSet set;
-    __shared__ f32x4 sums[W][16 * TT][4];   // [wave][token][column / 4]
-    __shared__ int32_t place[W][64];
-    const uint32_t wave = threadIdx.x >> 6, lane = threadIdx.x & 63, i = lane & (kRows - 1);
-    const uint32_t part = blockIdx.x % g.parts, n0 = kRows * (blockIdx.x / g.parts);
-    for (uint32_t q = lane; q < 64 * TT; q += 64) sums[wave][q >> 2][q & 3] = f32x4{0.f, 0.f, 0.f, 0.f};
+    __shared__ Strip strips[W];
+    __shared__ f32x4 sums[W][kTokens][2];  // [wave][token][column / 4]
+    __shared__ int32_t place[W][kTokens];
+    const uint32_t wave = threadIdx.x >> 6, lane = threadIdx.x & 63, gr = lane >> 4, i = lane & 7, second = (lane >> 3) & 1;
+    const uint32_t n0 = 8 * blockIdx.x;
+    if (lane < 2 * kTokens) sums[wave][lane >> 1][lane & 1] = f32x4{0.f, 0.f, 0.f, 0.f};
     set.fill(g);
     uint32_t expert;
     const uint32_t active = set.find(0, expert);
-    // pieces of an expert: enough for every wave, as evenly as may be
-    const uint32_t waves = W * g.parts, steps = (g.inner + 31) / 32;
-    uint32_t pieces = active >= 8 * waves ? 1u : min((4 * waves + active - 1) / active, max(steps / 8, 1u));
-    const uint32_t piece = (steps + pieces - 1) / pieces;
-    pieces = (steps + piece - 1) / piece;
-    const uint64_t row = (uint64_t)min(n0 + i, g.cols - 1) * g.down_row;
-    for (uint32_t it = wave + W * part; it < active * pieces; it += waves) {
+    // pieces of an expert, each 256 columns twice or more: as many as give every wave one
+    const uint32_t most = (g.inner + 2 * kStripCols - 1) / (2 * kStripCols);
+    const uint32_t pieces = min((W + active - 1) / active, most);
+    const uint32_t piece = ((g.inner + 16 * pieces - 1) / (16 * pieces)) * 16, half = piece / 2;
+    const uint32_t rows = min(g.cols - n0, 8u), stride = (uint32_t)g.down_row;
+    for (uint32_t it = wave; it < active * pieces; it += W) {
         set.find(it / pieces, expert);
         const int32_t mine = set.choice(g, expert);
         const uint64_t mask = __ballot(mine >= 0);
@@ -461,37 +567,47 @@ __global__ __launch_bounds__(64 * W, 4) void k_moe_down(MoeArgs g)
         __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "wavefront");  // a wave's own LDS: in order
         if (mine >= 0) place[wave][__popcll(mask & ((1ull << lane) - 1))] = mine;
         __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "wavefront");
-        const uint16_t *w2 = g.w2 + (uint64_t)expert * g.down_expert + row;
-        const uint32_t s0 = (it % pieces) * piece, s1 = min(steps, s0 + piece);
-        if (TT == 1 || count <= 16) moe_down_piece<T, 1, kHalf>(g, w2, place[wave], count, s0, s1, sums[wave]);
-        else if (TT == 2 || count <= 32) moe_down_piece<T, 2, false>(g, w2, place[wave], count, s0, s1, sums[wave]);
-        else moe_down_piece<T, 4, false>(g, w2, place[wave], count, s0, s1, sums[wave]);
+        const uint32_t p0 = (it % pieces) * piece, p1 = min(g.inner, p0 + piece);
+        if (p0 >= p1) continue;
+        const uint32_t len = min(half, p1 - p0), rest = p1 - p0 - len;  // the second half may be shorter, or nothing
+        const uint32_t ahead = rest ? half : 0;
+        const uint16_t *w2 = g.w2 + (uint64_t)expert * g.down_expert + (uint64_t)n0 * g.down_row + p0;
+        f32x4 sum[1];
+        moe_down_rows<T, 1, 1, true>(
+            g, w2, [&](uint32_t r) { return min(r & 7, rows - 1) * stride + (r >> 3) * ahead; }, place[wave], count, i,
+            p0 + second * ahead, 0, len, rest, &strips[wave], sum);
+        if (i < count) {
+            const uint32_t at = (uint32_t)place[wave][i];
+            const f32x4 v = g.weights[at] * sum[0];
+            f32x4 &s = sums[wave][at / g.top_k][gr & 1];
+            if (lane < 32 && !second) s += v;
+            __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "wavefront");
+            if (lane >= 32 && second) s += v;
+        }
     }
     __syncthreads();
-    for (uint32_t q = threadIdx.x; q < 4 * g.m; q += 64 * W) {
-        const uint32_t t = q >> 2, n = n0 + 4 * (q & 3);
-        if (4 * (q & 3) >= kRows || n >= g.cols) continue;
-        f32x4 v = sums[0][t][q & 3];
+    const uint32_t t = threadIdx.x >> 1, n = n0 + 4 * (threadIdx.x & 1);
+    if (t < g.m && n < g.cols) {
+        f32x4 v = sums[0][t][threadIdx.x & 1];
 #pragma unroll
-        for (int w = 1; w < W; w++) v += sums[w][t][q & 3];
-        if (g.parts == 1) {
-            uint16_t *o = g.out + t * g.out_stride + n;
+        for (uint32_t w = 1; w < W; w++) v += sums[w][t][threadIdx.x & 1];
+        uint16_t *o = g.out + t * g.out_stride + n;
 #pragma unroll
-            for (int e = 0; e < 4; e++) o[e] = Ty::from_f32(v[e]);
-        } else {
-            *reinterpret_cast<f32x4 *>(g.part + ((uint64_t)part * g.m + t) * g.cols + n) = v;
-        }
+        for (int e = 0; e < 4; e++) o[e] = Type<T>::from_f32(v[e]);
     }
 }
 
+// y from the experts' parts, in the order of each token's choices.
 template <int T>
 __global__ __launch_bounds__(256) void k_moe_join(MoeArgs g)
 {
     const uint32_t q = blockIdx.x * 256 + threadIdx.x, per = g.cols / 4;
     if (q >= g.m * per) return;
     const uint32_t t = q / per, n = 4 * (q % per);
+    const float *p = g.part + (uint64_t)t * g.top_k * g.cols + n;
     f32x4 v{0.f, 0.f, 0.f, 0.f};
-    for (uint32_t p = 0; p < g.parts; p++) v += *reinterpret_cast<const f32x4 *>(g.part + ((uint64_t)p * g.m + t) * g.cols + n);
+#pragma unroll 4
+    for (uint32_t s = 0; s < g.top_k; s++) v += *reinterpret_cast<const f32x4 *>(p + (uint64_t)s * g.cols);
     uint16_t *o = g.out + t * g.out_stride + n;
 #pragma unroll
     for (int e = 0; e < 4; e++) o[e] = Type<T>::from_f32(v[e]);

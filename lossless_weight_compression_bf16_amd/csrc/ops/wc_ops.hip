@@ -172,8 +172,9 @@ wc_status launch_adapters(const AdapterArgs &g, const AdapterPlan &p, uint32_t y
 // Launch shapes and scratch of the mixture-of-experts layer.
 struct MoePlan {
     bool one;       // k_moe_route_one
-    bool half;      // k_moe_down on 8 columns
-    uint32_t route_tiles, route_splits, route_steps, experts_pad, slots, up_tiles, down_tiles, down_waves, parts;
+    bool few;       // k_moe_down_few
+    bool split;     // k_moe_down with four waves for 16 columns
+    uint32_t route_tiles, route_splits, route_steps, experts_pad, slots, up_tiles, down_tiles;
     uint64_t logits, ids, weights, h, part, bytes;  // offsets in the scratch
 };
 
@@ -195,21 +196,12 @@ MoePlan moe_plan(uint32_t m, uint32_t experts, uint32_t top_k, uint32_t cols, ui
     p.route_splits = (uint32_t)ceil_div(steps, p.route_steps);
     p.slots = m * top_k < experts ? m * top_k : experts;
     p.up_tiles = (inner + 15) / 16;
-    // k_moe_down: 448 blocks or more of eight waves keep the memory busy.
-    // Where the columns are too few, blocks of 8 of them, which take up to 8
-    // tokens; then parts, which take another launch; where all of W2's
-    // experts are under 64 MiB that costs more than it gives, and blocks have
-    // sixteen waves instead.
-    const uint64_t reads = 2ull * p.slots * cols * inner;
-    const uint32_t enough = 7 * kCus / 4;
-    p.down_tiles = (cols + 15) / 16;
-    p.half = m <= 8 && p.down_tiles < enough;
-    if (p.half) p.down_tiles = (cols + 7) / 8;
-    p.parts = 1;
-    p.down_waves = 8;
-    if (p.down_tiles < enough && reads < (64ull << 20)) p.down_waves = 16;
-    else
-        while (p.parts < 16 && p.down_tiles * p.parts < enough) p.parts *= 2;
+    // y: in one launch where W2's experts together are under 64 MiB and the
+    // tokens at most 8 (the join's launch costs about 4 us); otherwise a wave
+    // for 16 columns of an expert, or four where that gives too few blocks
+    p.few = m <= 8 && 2ull * p.slots * cols * inner < (64ull << 20);
+    p.split = (uint64_t)p.slots * ceil_div(cols, 64) < 8 * kCus;
+    p.down_tiles = (uint32_t)ceil_div(cols, p.few ? 8 : p.split ? 16 : 64);
     uint64_t at = 0;
     auto take = [&](uint64_t bytes) {
         const uint64_t here = at;
@@ -220,7 +212,7 @@ MoePlan moe_plan(uint32_t m, uint32_t experts, uint32_t top_k, uint32_t cols, ui
     p.ids = take(4ull * m * top_k);
     p.weights = take(4ull * m * top_k);
     p.h = take(4ull * m * top_k * inner);
-    p.part = take(p.parts > 1 ? 4ull * p.parts * m * cols : 0);
+    p.part = take(p.few ? 0 : 4ull * m * top_k * cols);
     p.bytes = at;
     return p;
 }
@@ -246,13 +238,14 @@ wc_status launch_moe(const MoeArgs &g, const MoePlan &p, hipStream_t stream)
         else hipLaunchKernelGGL(k_moe_select<16>, tokens, dim3(64), 0, stream, g);
     }
     hipLaunchKernelGGL((k_moe_up<T, TT>), dim3(p.slots * p.up_tiles), dim3(256), 0, stream, g);
-    const dim3 down(p.down_tiles * p.parts);
-    if (p.half && p.down_waves == 16) hipLaunchKernelGGL((k_moe_down<T, 1, 16, true>), down, dim3(1024), 0, stream, g);
-    else if (p.half) hipLaunchKernelGGL((k_moe_down<T, 1, 8, true>), down, dim3(512), 0, stream, g);
-    else if (p.down_waves == 16) hipLaunchKernelGGL((k_moe_down<T, TT, 16, false>), down, dim3(1024), 0, stream, g);
-    else hipLaunchKernelGGL((k_moe_down<T, TT, 8, false>), down, dim3(512), 0, stream, g);
-    if (p.parts > 1)
-        hipLaunchKernelGGL(k_moe_join<T>, dim3((g.m * (g.cols / 4) + 255) / 256), dim3(256), 0, stream, g);
+    if (p.few) {
+        hipLaunchKernelGGL(k_moe_down_few<T>, dim3(p.down_tiles), dim3(1024), 0, stream, g);
+        return launched();
+    }
+    const dim3 down(p.slots * p.down_tiles);
+    if (p.split) hipLaunchKernelGGL((k_moe_down<T, TT, true>), down, dim3(256), 0, stream, g);
+    else hipLaunchKernelGGL((k_moe_down<T, TT, false>), down, dim3(256), 0, stream, g);
+    hipLaunchKernelGGL(k_moe_join<T>, dim3((g.m * (g.cols / 4) + 255) / 256), dim3(256), 0, stream, g);
     return launched();
 }
 
@@ -413,11 +406,11 @@ wc_status wc_moe_layer(const wc_moe *a, void *d_scratch, uint64_t scratch_bytes,
     if (!a->w1 || !a->w3 || !a->w2 || !aligned(a->w1, 16) || !aligned(a->w3, 16) || !aligned(a->w2, 16))
         return WC_ERR_ARG;
     if (a->up_row < a->cols || a->up_row % 8 || a->up_expert % 8 || a->down_row < a->inner || a->down_row % 8 ||
-        a->down_expert % 8)
+        a->down_expert % 8 || a->up_row > (1u << 26) || a->down_row > (1u << 26))
         return WC_ERR_ARG;
     if (!a->out || !aligned(a->out, 2) || (a->m > 1 && a->out_stride < a->cols)) return WC_ERR_ARG;
     const MoePlan p = moe_plan((uint32_t)a->m, a->experts, a->top_k, a->cols, a->inner);
-    if ((uint64_t)p.slots * p.up_tiles > kMaxGrid) return WC_ERR_ARG;
+    if ((uint64_t)p.slots * p.up_tiles > kMaxGrid || (uint64_t)p.slots * p.down_tiles > kMaxGrid) return WC_ERR_ARG;
     if (scratch_bytes < p.bytes) return WC_ERR_CAPACITY;
     if (!d_scratch || !aligned(d_scratch, 256)) return WC_ERR_ARG;
     char *s = static_cast<char *>(d_scratch);
@@ -449,7 +442,6 @@ wc_status wc_moe_layer(const wc_moe *a, void *d_scratch, uint64_t scratch_bytes,
     g.route_splits = p.route_splits;
     g.route_steps = p.route_steps;
     g.slots = p.slots;
-    g.parts = p.parts;
     return a->type == WC_T_BF16 ? launch_moe_tiles<WC_T_BF16>(g, p, stream)
                                 : launch_moe_tiles<WC_T_FP16>(g, p, stream);
 }

@@ -19,8 +19,9 @@ def _check_experts(t, what, shape, dtype, device):
         raise TypeError(f"{what} must have the type of x, {dtype}")
     if tuple(t.shape) != shape:
         raise ValueError(f"{what} must be {shape}, got {tuple(t.shape)}")
-    if t.stride(2) != 1 or t.stride(1) % 8 or t.stride(0) % 8 or t.stride(1) < shape[2] or t.data_ptr() % 16:
-        raise ValueError(f"{what} must have unit column stride and 16-byte aligned rows")
+    if (t.stride(2) != 1 or t.stride(1) % 8 or t.stride(0) % 8 or not shape[2] <= t.stride(1) <= 1 << 26
+            or t.data_ptr() % 16):
+        raise ValueError(f"{what} must have unit column stride and 16-byte aligned rows, at most 2^26 elements apart")
 
 
 def _check(x, router, w1, w3, w2, top_k, out):

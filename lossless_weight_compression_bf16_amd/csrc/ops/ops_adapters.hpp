@@ -451,28 +451,28 @@ __global__ __launch_bounds__(256) void k_adapters_up(AdapterArgs g)
 // 64 rows of B, which reach them through LDS in operand order: B would
 // otherwise pass through the L1 cache once per 32 tokens, twice as many bytes
 // as y, and how much can be on its way into that cache is what bounds a
-// kernel that only streams.
-template <int T, int YT, int KS>
-__global__ __launch_bounds__(256, 4) void k_adapters_up_many(AdapterArgs g)
+// kernel that only streams.  y is read and written in whole lines, 64 elements
+// of a token at a time, and past the caches where it is larger than they are
+// (kStream); the products come to that order through LDS as well.
+template <int T, int YT, int KS, bool kStream>
+__global__ __launch_bounds__(256, 3) void k_adapters_up_many(AdapterArgs g)
 {
     using Ty = Type<T>;
-    using YE = typename Type<YT>::elem;
+    using Y = Type<YT>;
+    using YE = typename Y::elem;
     using X8 = typename Ty::x8;
-    constexpr int kTerms = Terms<T, YT>::kCount, TT = 2;
+    constexpr int kTerms = Terms<T, YT>::kCount, TT = 2, kPer = Y::kPer16;
+    constexpr uint32_t kLanes = 64 / kPer, kRows = 64 / kLanes, kVecs = 32 / kRows;  // of y: lanes a row, rows a load, loads
+    constexpr uint32_t kPitch = 68;  // floats of a token's 64 products in LDS: rows in different banks
     __shared__ u32x4 sb[2][4][KS][64];
+    __shared__ float products[4][32][kPitch];
     const uint32_t wave = threadIdx.x >> 6, lane = threadIdx.x & 63, i = lane & 15, gr = lane >> 4;
     const uint32_t row_blocks = (g.rows + g.row_block - 1) / g.row_block;
     const uint32_t block = xcd_block();
     const uint64_t tile = (uint64_t)(block / row_blocks) * 128;
     const uint32_t n0 = (block % row_blocks) * g.row_block, n1 = min(g.rows, n0 + g.row_block);
+    const uint32_t yrow = lane / kLanes, ycol = lane % kLanes * kPer;  // the lane's place in a load of y
     TileIds low(g, tile, 64), high(g, tile + 64, 64);
-    uint64_t token[TT];
-    YE *yr[TT];
-#pragma unroll
-    for (int t = 0; t < TT; t++) {
-        token[t] = min(tile + 32 * wave + 16 * t + i, g.m - 1);
-        yr[t] = static_cast<YE *>(g.y) + token[t] * g.y_stride;
-    }
     uint64_t mlow, mhigh;
     uint32_t adapter;
     while (low.pending | high.pending) {
@@ -482,29 +482,33 @@ __global__ __launch_bounds__(256, 4) void k_adapters_up_many(AdapterArgs g)
             mlow = 0;
             high.next(adapter, mhigh);
         }
-        const uint32_t mask = (uint32_t)((wave & 2 ? mhigh : mlow) >> (32 * (wave & 1)));
+        const uint32_t mask = (uint32_t)((wave & 2 ? mhigh : mlow) >> (32 * (wave & 1)));  // the wave's tokens
         X8 u[TT][KS][kTerms];
         float unscale[TT];
-        bool mine[TT];
 #pragma unroll
         for (int t = 0; t < TT; t++) {
-            mine[t] = (mask >> (16 * t + i)) & 1;
+            const uint64_t token = min(tile + 32 * wave + 16 * t + i, g.m - 1);
 #pragma unroll
             for (int s = 0; s < KS; s++)
 #pragma unroll
                 for (int c = 0; c < kTerms; c++)
-                    u[t][s][c] = __builtin_bit_cast(X8, load16<16>(g.u + (c * g.m + token[t]) * g.rank_pad + 32 * s + 8 * gr));
-            unscale[t] = T == WC_T_FP16 ? g.unscale[token[t]] : 1.f;
+                    u[t][s][c] = __builtin_bit_cast(X8, load16<16>(g.u + (c * g.m + token) * g.rank_pad + 32 * s + 8 * gr));
+            unscale[t] = T == WC_T_FP16 ? g.unscale[token] : 1.f;
         }
-        const BRows<T, YT, KS> rows(g, adapter, 0);
+        const BRows<T, WC_T_FP32, KS> rows(g, adapter, 0);  // row i of tile p is row 16 p + i
+        YE *const y0 = static_cast<YE *>(g.y) + (tile + 32 * wave) * g.y_stride + ycol;
         u32x4 nextb[KS];
         rows.load(g, n0, (int)wave, nextb);
         uint32_t turn = 0;
         for (uint32_t nb = n0; nb < n1; nb += 64, turn ^= 1) {
-            YRow<YT> y[TT];
-            if (mask && nb + 64 <= n1) {
+            const bool whole = nb + 64 <= n1;
+            u32x4 y[kVecs];
+            if (whole) {
 #pragma unroll
-                for (int t = 0; t < TT; t++) y[t].load(yr[t] + nb, gr);
+                for (uint32_t q = 0; q < kVecs; q++) {
+                    const uint32_t r = q * kRows + yrow;
+                    if ((mask >> r) & 1) y[q] = read16<Y::kBytes, kStream>(y0 + r * g.y_stride + nb);
+                }
             }
 #pragma unroll
             for (int s = 0; s < KS; s++) sb[turn][wave][s][lane] = rows.kept(nextb[s], s);
@@ -512,24 +516,36 @@ __global__ __launch_bounds__(256, 4) void k_adapters_up_many(AdapterArgs g)
             if (nb + 64 < n1) rows.load(g, nb + 64, (int)wave, nextb);
             if (!mask) continue;
 #pragma unroll
-            for (int t = 0; t < TT; t++) {
-                f32x4 sum[4];
+            for (int t = 0; t < TT; t++)
 #pragma unroll
                 for (int p = 0; p < 4; p++) {
-                    sum[p] = f32x4{0.f, 0.f, 0.f, 0.f};
+                    f32x4 sum{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                     for (int s = 0; s < KS; s++) {
                         const X8 bv = __builtin_bit_cast(X8, sb[turn][p][s][lane]);
 #pragma unroll
-                        for (int c = kTerms - 1; c >= 0; c--) sum[p] = Ty::mfma(bv, u[t][s][c], sum[p]);
+                        for (int c = kTerms - 1; c >= 0; c--) sum = Ty::mfma(bv, u[t][s][c], sum);
                     }
+                    *reinterpret_cast<f32x4 *>(&products[wave][16 * t + i][16 * p + 4 * gr]) = unscale[t] * sum;
                 }
-                if (mine[t]) {
-                    if (nb + 64 <= n1) y[t].add(yr[t] + nb, gr, sum, unscale[t]);
-                    else y_add_some<YT>(yr[t] + nb, gr, n1 - nb, sum[0], sum[1], sum[2], sum[3], unscale[t]);
+            __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "wavefront");  // a wave's own LDS: in order
+#pragma unroll
+            for (uint32_t q = 0; q < kVecs; q++) {
+                const uint32_t r = q * kRows + yrow;
+                if (!((mask >> r) & 1)) continue;
+                YE *const yp = y0 + r * g.y_stride + nb;
+                float f[kPer];
+                if (whole) {
+                    Y::unpack(y[q], f);
+#pragma unroll
+                    for (int e = 0; e < kPer; e++) f[e] += products[wave][r][ycol + e];
+                    write16<Y::kBytes, kStream>(yp, Y::pack(f));
+                } else {
+                    for (uint32_t e = 0; e < (uint32_t)kPer && nb + ycol + e < n1; e++)
+                        yp[e] = Y::from_f32(Y::to_f32(yp[e]) + products[wave][r][ycol + e]);
                 }
-                __builtin_amdgcn_sched_barrier(0);  // one tile's sums at a time: registers for four waves
             }
+            __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "wavefront");
         }
         __syncthreads();
     }

@@ -7,8 +7,8 @@
 //   k_moe_select  softmax and the top_k of each token: one wave per token
 //   k_moe_route_one  both, where the router is small: one block per token
 //   k_moe_up      h = silu(W1 x) * (W3 x), for every expert with tokens
-//   k_moe_down    p W2 h of every expert, and k_moe_join their sums; or
-//   k_moe_down_few  both at once, for up to 8 tokens on small experts
+//   k_moe_down    p W2 h of every expert
+//   k_moe_join    their sums
 // What bounds it: every expert that has tokens is read once, 6 bytes per
 // row and column; with few tokens that is all the time there is.  So weights
 // stay in their own row-major layout (no repacked copy), are read in whole
@@ -294,12 +294,11 @@ struct Strip {
 // matrices of 16 rows and NT tiles of 16 tokens whose numbers are sums of O
 // terms.  weights[m]: the first row; row(r): elements from there to row r;
 // tokens(o, t): the lane's column of term o.  Loads past the end repeat the
-// last 8 columns, and the operands are zero there.  With kHalves rows 8..15
-// and columns 8..15 end at c1b.  The next columns are on their way while these
-// are multiplied.
-template <int T, int M, int O, int NT, bool kHalves, class Row, class Tokens>
+// last 8 columns, and the operands are zero there.  The next columns are on
+// their way while these are multiplied.
+template <int T, int M, int O, int NT, class Row, class Tokens>
 __device__ __forceinline__ void strip_product(const uint16_t *const (&weights)[M], Row row, Tokens tokens, uint32_t c0,
-                                              uint32_t c1, uint32_t c1b, Strip *strips, f32x4 (&acc)[M][O][NT])
+                                              uint32_t c1, Strip *strips, f32x4 (&acc)[M][O][NT])
 {
     using Ty = Type<T>;
     using X8 = typename Ty::x8;
@@ -314,19 +313,17 @@ __device__ __forceinline__ void strip_product(const uint16_t *const (&weights)[M
 #pragma unroll
         for (int t = 0; t < NT; t++) tk[o][t] = tokens(o, t);
     u32x4 v[M][8], x[S][O][NT];
-    const uint32_t last = c1 - 8, lastb = kHalves && c1b ? c1b - 8 : 0;
-    const uint32_t xend = kHalves && i >= 8 ? c1b : c1, xlast = kHalves && i >= 8 ? lastb : last;
     auto fetch = [&](uint32_t c) {
+        const uint32_t k = min(c + 8 * lo, c1 - 8);
 #pragma unroll
         for (int m = 0; m < M; m++)
 #pragma unroll
-            for (int u = 0; u < 8; u++)
-                v[m][u] = read16<16, true>(weights[m] + (off[u] + min(c + 8 * lo, kHalves && u >= 4 ? lastb : last)));
+            for (int u = 0; u < 8; u++) v[m][u] = read16<16, true>(weights[m] + (off[u] + k));
     };
     auto fetch_x = [&](uint32_t c, int s0) {
 #pragma unroll
         for (int s = 0; s < S; s++) {
-            const uint32_t k = min(c + 32 * (s0 + s) + 8 * gr, xlast);
+            const uint32_t k = min(c + 32 * (s0 + s) + 8 * gr, c1 - 8);
 #pragma unroll
             for (int o = 0; o < O; o++)
 #pragma unroll
@@ -339,11 +336,11 @@ __device__ __forceinline__ void strip_product(const uint16_t *const (&weights)[M
     }
     for (uint32_t c = c0; c < c1; c += kStripCols) {
         __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "wavefront");  // a wave's own LDS: in order
+        const bool there = c + 8 * lo < c1;
 #pragma unroll
         for (int m = 0; m < M; m++)
 #pragma unroll
-            for (int u = 0; u < 8; u++)
-                strips[m].q[(2 * u + hi) * kStripPitch + lo] = only(c + 8 * lo < (kHalves && u >= 4 ? c1b : c1), v[m][u]);
+            for (int u = 0; u < 8; u++) strips[m].q[(2 * u + hi) * kStripPitch + lo] = only(there, v[m][u]);
         __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "wavefront");
         if (c + kStripCols < c1) fetch(c + kStripCols);
 #pragma unroll
@@ -351,7 +348,7 @@ __device__ __forceinline__ void strip_product(const uint16_t *const (&weights)[M
             if (s0) fetch_x(c, s0);
 #pragma unroll
             for (int s = 0; s < S; s++) {
-                const bool in = c + 32 * (s0 + s) + 8 * gr < xend;
+                const bool in = c + 32 * (s0 + s) + 8 * gr < c1;
                 X8 a[M];
 #pragma unroll
                 for (int m = 0; m < M; m++)
@@ -384,10 +381,10 @@ __device__ __forceinline__ void moe_up_rows(const MoeArgs &g, uint32_t expert, u
     f32x4 acc[2][1][NT];
 #pragma unroll
     for (int t = 0; t < NT; t++) acc[0][0][t] = acc[1][0][t] = f32x4{0.f, 0.f, 0.f, 0.f};
-    strip_product<T, 2, 1, NT, false>(
+    strip_product<T, 2, 1, NT>(
         weights, [&](uint32_t r) { return min(r, rows - 1) * stride; },
         [&](int, int t) { return g.x + (uint64_t)((uint32_t)place[min(16 * t + i, count - 1)] / g.top_k) * g.x_stride; },
-        c0, c1, c1, strips, acc);
+        c0, c1, strips, acc);
 #pragma unroll
     for (int t = 0; t < NT; t++) {
         gate[t] = acc[0][0][t];
@@ -395,22 +392,22 @@ __device__ __forceinline__ void moe_up_rows(const MoeArgs &g, uint32_t expert, u
     }
 }
 
-// A wave's share of the inner rows c0 .. c1 (kHalves: .. c1b) for 16 rows of
-// W2 of one expert against its tokens' h from `shift` on; column: the lane's.
-template <int T, int NT, int TT, bool kHalves, class Row>
-__device__ __forceinline__ void moe_down_rows(const MoeArgs &g, const uint16_t *w2, Row row, const int32_t *place,
-                                              uint32_t count, uint32_t column, uint32_t shift, uint32_t c0, uint32_t c1,
-                                              uint32_t c1b, Strip *strips, f32x4 (&sum)[TT])
+// A wave's share of the inner rows c0 .. c1 for 16 rows of W2 of one expert
+// against its tokens' h.
+template <int T, int NT, int TT>
+__device__ __forceinline__ void moe_down_rows(const MoeArgs &g, uint32_t expert, uint32_t n0, const int32_t *place,
+                                              uint32_t count, uint32_t c0, uint32_t c1, Strip *strips, f32x4 (&sum)[TT])
 {
+    const uint32_t i = threadIdx.x & 15, rows = min(g.cols - n0, 16u), stride = (uint32_t)g.down_row;
+    const uint16_t *const weights[1] = {g.w2 + (uint64_t)expert * g.down_expert + (uint64_t)n0 * g.down_row};
     const uint64_t plane = (uint64_t)g.m * g.top_k * g.inner;
-    const uint16_t *const weights[1] = {w2};
     f32x4 acc[1][2][NT];
 #pragma unroll
     for (int t = 0; t < NT; t++) acc[0][0][t] = acc[0][1][t] = f32x4{0.f, 0.f, 0.f, 0.f};
-    strip_product<T, 1, 2, NT, kHalves>(
-        weights, row,
-        [&](int o, int t) { return g.h + o * plane + (uint64_t)place[min(16 * t + column, count - 1)] * g.inner + shift; },
-        c0, c1, c1b, strips, acc);
+    strip_product<T, 1, 2, NT>(
+        weights, [&](uint32_t r) { return min(r, rows - 1) * stride; },
+        [&](int o, int t) { return g.h + o * plane + (uint64_t)place[min(16 * t + i, count - 1)] * g.inner; },
+        c0, c1, strips, acc);
 #pragma unroll
     for (int t = 0; t < NT; t++) sum[t] = MoeTerms<T>::kScale[0] * acc[0][0][t] + MoeTerms<T>::kScale[1] * acc[0][1][t];
 }
@@ -428,11 +425,28 @@ __device__ __forceinline__ void wave_quarter(uint32_t cols, uint32_t unit, uint3
 __device__ __forceinline__ uint32_t moe_block(const MoeArgs &g, uint32_t slot, MoeSet &set, int32_t (&place)[64],
                                               uint32_t &expert)
 {
+    const uint32_t lane = threadIdx.x & 63, choices = g.m * g.top_k;
+    const uint64_t below = (1ull << lane) - 1;
+    if (choices <= 64) {
+        // a choice per lane; experts in the order of their first choice.  No
+        // barrier: every wave writes the same places and reads its own.
+        const int32_t id = lane < choices ? g.ids[lane] : -1;
+        uint64_t pending = __ballot(id >= 0), mask = 0;
+        for (uint32_t p = 0; p <= slot; p++) {
+            if (!pending) return 0;
+            expert = (uint32_t)__builtin_amdgcn_readlane(id, __builtin_ctzll(pending));
+            mask = __ballot(id == (int32_t)expert);
+            pending &= ~mask;
+        }
+        if ((mask >> lane) & 1) place[__popcll(mask & below)] = (int32_t)lane;
+        __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "wavefront");
+        return (uint32_t)__popcll(mask);
+    }
     set.fill(g);
     if (slot >= set.find(slot, expert)) return 0;
     const int32_t mine = set.choice(g, expert);
     const uint64_t mask = __ballot(mine >= 0);
-    if (mine >= 0) place[__popcll(mask & ((1ull << (threadIdx.x & 63)) - 1))] = mine;  // the same from every wave
+    if (mine >= 0) place[__popcll(mask & below)] = mine;  // the same from every wave
     __syncthreads();
     return (uint32_t)__popcll(mask);
 }
@@ -505,12 +519,9 @@ __global__ __launch_bounds__(256, 3) void k_moe_down(MoeArgs g)
     if (kSplit) wave_quarter(g.inner, kStripCols, wave, c0, c1);
     f32x4 sum[TT];
     if (n0 < g.cols) {
-        const uint16_t *w2 = g.w2 + (uint64_t)expert * g.down_expert + (uint64_t)n0 * g.down_row;
-        const uint32_t rows = min(g.cols - n0, 16u), stride = (uint32_t)g.down_row;
-        auto row = [&](uint32_t r) { return min(r, rows - 1) * stride; };
-        if (TT == 1 || count <= 16) moe_down_rows<T, 1, TT, false>(g, w2, row, place, count, i, 0, c0, c1, c1, &strips[wave], sum);
-        else if (TT == 2 || count <= 32) moe_down_rows<T, 2, TT, false>(g, w2, row, place, count, i, 0, c0, c1, c1, &strips[wave], sum);
-        else moe_down_rows<T, 4, TT, false>(g, w2, row, place, count, i, 0, c0, c1, c1, &strips[wave], sum);
+        if (TT == 1 || count <= 16) moe_down_rows<T, 1, TT>(g, expert, n0, place, count, c0, c1, &strips[wave], sum);
+        else if (TT == 2 || count <= 32) moe_down_rows<T, 2, TT>(g, expert, n0, place, count, c0, c1, &strips[wave], sum);
+        else moe_down_rows<T, 4, TT>(g, expert, n0, place, count, c0, c1, &strips[wave], sum);
     }
     if constexpr (kSplit) {
         __syncthreads();
@@ -531,82 +542,16 @@ __global__ __launch_bounds__(256, 3) void k_moe_down(MoeArgs g)
     }
 }
 
-// y of 8 columns (rows of W2) for up to 8 tokens, where all experts of W2
-// together are small and another launch to join them would cost more than it
-// gives.  The operands' 16 rows are the 8 rows at the first and at the second
-// half of the inner rows, and so are the tokens' columns: of the product, the
-// two quarters count where both are alike.  The experts with tokens, each cut
-// into pieces along the inner rows where they are few, go round the sixteen
-// waves; a wave adds its tokens' products, times their weights, into a slice
-// of LDS of its own, and at the end the slices are added in the order of the
-// waves.
-template <int T>
-__global__ __launch_bounds__(1024) void k_moe_down_few(MoeArgs g)
-{
-    constexpr uint32_t W = 16, kTokens = 8;
-    __shared__ MoeSet set;
-    __shared__ Strip strips[W];
-    __shared__ f32x4 sums[W][kTokens][2];  // [wave][token][column / 4]
-    __shared__ int32_t place[W][kTokens];
-    const uint32_t wave = threadIdx.x >> 6, lane = threadIdx.x & 63, gr = lane >> 4, i = lane & 7, second = (lane >> 3) & 1;
-    const uint32_t n0 = 8 * blockIdx.x;
-    if (lane < 2 * kTokens) sums[wave][lane >> 1][lane & 1] = f32x4{0.f, 0.f, 0.f, 0.f};
-    set.fill(g);
-    uint32_t expert;
-    const uint32_t active = set.find(0, expert);
-    // pieces of an expert, each 256 columns twice or more: as many as give every wave one
-    const uint32_t most = (g.inner + 2 * kStripCols - 1) / (2 * kStripCols);
-    const uint32_t pieces = min((W + active - 1) / active, most);
-    const uint32_t piece = ((g.inner + 16 * pieces - 1) / (16 * pieces)) * 16, half = piece / 2;
-    const uint32_t rows = min(g.cols - n0, 8u), stride = (uint32_t)g.down_row;
-    for (uint32_t it = wave; it < active * pieces; it += W) {
-        set.find(it / pieces, expert);
-        const int32_t mine = set.choice(g, expert);
-        const uint64_t mask = __ballot(mine >= 0);
-        const uint32_t count = (uint32_t)__popcll(mask);
-        __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "wavefront");  // a wave's own LDS: in order
-        if (mine >= 0) place[wave][__popcll(mask & ((1ull << lane) - 1))] = mine;
-        __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "wavefront");
-        const uint32_t p0 = (it % pieces) * piece, p1 = min(g.inner, p0 + piece);
-        if (p0 >= p1) continue;
-        const uint32_t len = min(half, p1 - p0), rest = p1 - p0 - len;  // the second half may be shorter, or nothing
-        const uint32_t ahead = rest ? half : 0;
-        const uint16_t *w2 = g.w2 + (uint64_t)expert * g.down_expert + (uint64_t)n0 * g.down_row + p0;
-        f32x4 sum[1];
-        moe_down_rows<T, 1, 1, true>(
-            g, w2, [&](uint32_t r) { return min(r & 7, rows - 1) * stride + (r >> 3) * ahead; }, place[wave], count, i,
-            p0 + second * ahead, 0, len, rest, &strips[wave], sum);
-        if (i < count) {
-            const uint32_t at = (uint32_t)place[wave][i];
-            const f32x4 v = g.weights[at] * sum[0];
-            f32x4 &s = sums[wave][at / g.top_k][gr & 1];
-            if (lane < 32 && !second) s += v;
-            __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "wavefront");
-            if (lane >= 32 && second) s += v;
-        }
-    }
-    __syncthreads();
-    const uint32_t t = threadIdx.x >> 1, n = n0 + 4 * (threadIdx.x & 1);
-    if (t < g.m && n < g.cols) {
-        f32x4 v = sums[0][t][threadIdx.x & 1];
-#pragma unroll
-        for (uint32_t w = 1; w < W; w++) v += sums[w][t][threadIdx.x & 1];
-        uint16_t *o = g.out + t * g.out_stride + n;
-#pragma unroll
-        for (int e = 0; e < 4; e++) o[e] = Type<T>::from_f32(v[e]);
-    }
-}
-
 // y from the experts' parts, in the order of each token's choices.
 template <int T>
-__global__ __launch_bounds__(256) void k_moe_join(MoeArgs g)
+__global__ __launch_bounds__(64) void k_moe_join(MoeArgs g)
 {
-    const uint32_t q = blockIdx.x * 256 + threadIdx.x, per = g.cols / 4;
+    const uint32_t q = blockIdx.x * 64 + threadIdx.x, per = g.cols / 4;
     if (q >= g.m * per) return;
     const uint32_t t = q / per, n = 4 * (q % per);
     const float *p = g.part + (uint64_t)t * g.top_k * g.cols + n;
     f32x4 v{0.f, 0.f, 0.f, 0.f};
-#pragma unroll 4
+#pragma unroll 8
     for (uint32_t s = 0; s < g.top_k; s++) v += *reinterpret_cast<const f32x4 *>(p + (uint64_t)s * g.cols);
     uint16_t *o = g.out + t * g.out_stride + n;
 #pragma unroll

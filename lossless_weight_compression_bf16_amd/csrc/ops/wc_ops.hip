@@ -134,8 +134,14 @@ template <int T, int YT>
 void launch_up(const AdapterArgs &g, const AdapterPlan &p, hipStream_t stream)
 {
     const dim3 grid((uint32_t)(p.up_tiles * p.row_blocks), 1, p.turns), block(256);
-    if (p.up_tile == 128 && g.rank <= 32) hipLaunchKernelGGL((k_adapters_up_many<T, YT, 1>), grid, block, 0, stream, g);
-    else if (p.up_tile == 128) hipLaunchKernelGGL((k_adapters_up_many<T, YT, 2>), grid, block, 0, stream, g);
+    const bool large = g.m * g.rows * type_bytes(YT) > (128ull << 20);  // y does not stay in the caches
+    if (p.up_tile == 128 && g.rank <= 32) {
+        if (large) hipLaunchKernelGGL((k_adapters_up_many<T, YT, 1, true>), grid, block, 0, stream, g);
+        else hipLaunchKernelGGL((k_adapters_up_many<T, YT, 1, false>), grid, block, 0, stream, g);
+    } else if (p.up_tile == 128) {
+        if (large) hipLaunchKernelGGL((k_adapters_up_many<T, YT, 2, true>), grid, block, 0, stream, g);
+        else hipLaunchKernelGGL((k_adapters_up_many<T, YT, 2, false>), grid, block, 0, stream, g);
+    }
     else if (g.rank <= 32) hipLaunchKernelGGL((k_adapters_up<T, YT, 1, false>), grid, block, 0, stream, g);
     else if (g.rank <= 64) hipLaunchKernelGGL((k_adapters_up<T, YT, 2, false>), grid, block, 0, stream, g);
     else hipLaunchKernelGGL((k_adapters_up<T, YT, 2, true>), grid, block, 0, stream, g);
@@ -172,7 +178,6 @@ wc_status launch_adapters(const AdapterArgs &g, const AdapterPlan &p, uint32_t y
 // Launch shapes and scratch of the mixture-of-experts layer.
 struct MoePlan {
     bool one;       // k_moe_route_one
-    bool few;       // k_moe_down_few
     bool split;     // k_moe_down with four waves for 16 columns
     uint32_t route_tiles, route_splits, route_steps, experts_pad, slots, up_tiles, down_tiles;
     uint64_t logits, ids, weights, h, part, bytes;  // offsets in the scratch
@@ -196,12 +201,9 @@ MoePlan moe_plan(uint32_t m, uint32_t experts, uint32_t top_k, uint32_t cols, ui
     p.route_splits = (uint32_t)ceil_div(steps, p.route_steps);
     p.slots = m * top_k < experts ? m * top_k : experts;
     p.up_tiles = (inner + 15) / 16;
-    // y: in one launch where W2's experts together are under 64 MiB and the
-    // tokens at most 8 (the join's launch costs about 4 us); otherwise a wave
-    // for 16 columns of an expert, or four where that gives too few blocks
-    p.few = m <= 8 && 2ull * p.slots * cols * inner < (64ull << 20);
+    // a wave for 16 rows of W2, or four where that gives too few blocks
     p.split = (uint64_t)p.slots * ceil_div(cols, 64) < 8 * kCus;
-    p.down_tiles = (uint32_t)ceil_div(cols, p.few ? 8 : p.split ? 16 : 64);
+    p.down_tiles = (uint32_t)ceil_div(cols, p.split ? 16 : 64);
     uint64_t at = 0;
     auto take = [&](uint64_t bytes) {
         const uint64_t here = at;
@@ -212,7 +214,7 @@ MoePlan moe_plan(uint32_t m, uint32_t experts, uint32_t top_k, uint32_t cols, ui
     p.ids = take(4ull * m * top_k);
     p.weights = take(4ull * m * top_k);
     p.h = take(4ull * m * top_k * inner);
-    p.part = take(p.few ? 0 : 4ull * m * top_k * cols);
+    p.part = take(4ull * m * top_k * cols);
     p.bytes = at;
     return p;
 }
@@ -238,14 +240,10 @@ wc_status launch_moe(const MoeArgs &g, const MoePlan &p, hipStream_t stream)
         else hipLaunchKernelGGL(k_moe_select<16>, tokens, dim3(64), 0, stream, g);
     }
     hipLaunchKernelGGL((k_moe_up<T, TT>), dim3(p.slots * p.up_tiles), dim3(256), 0, stream, g);
-    if (p.few) {
-        hipLaunchKernelGGL(k_moe_down_few<T>, dim3(p.down_tiles), dim3(1024), 0, stream, g);
-        return launched();
-    }
     const dim3 down(p.slots * p.down_tiles);
     if (p.split) hipLaunchKernelGGL((k_moe_down<T, TT, true>), down, dim3(256), 0, stream, g);
     else hipLaunchKernelGGL((k_moe_down<T, TT, false>), down, dim3(256), 0, stream, g);
-    hipLaunchKernelGGL(k_moe_join<T>, dim3((g.m * (g.cols / 4) + 255) / 256), dim3(256), 0, stream, g);
+    hipLaunchKernelGGL(k_moe_join<T>, dim3((g.m * (g.cols / 4) + 63) / 64), dim3(64), 0, stream, g);
     return launched();
 }
 

@@ -7,8 +7,8 @@
 // side by side and share their adapter, the tokens of a batch of single
 // requests differ and take one turn each, spread over the grid's z.
 //   k_adapters_few   few tokens: both products in one launch
-//   k_adapters_down  u_t = s_i A_i x_t, the columns split over the waves of a
-//                    block
+//   k_adapters_down  u_t = s_i A_i x_t; for many tokens k_adapters_down_many,
+//                    in parts along the columns, and k_adapters_terms
 //   k_adapters_up    y_t += B_i u_t, or, for many tokens, k_adapters_up_many
 // What bounds it: x read once, y read and written once.  u stays in 32 bits:
 // it enters the matrix cores as a sum of 16-bit numbers, of BF16 or, after a
@@ -42,7 +42,9 @@ struct AdapterArgs {
     uint32_t n, rank, cols, rows;
     uint16_t *u;            // terms x m x rank_pad: k_adapters_down's result
     float *unscale;         // m x rank blocks: what k_adapters_up multiplies its products by
+    float *part;            // splits x m x rank_pad: k_adapters_down_many's result
     uint32_t rank_pad;      // the rank rounded up to 32
+    uint32_t splits, split_cols;
     uint32_t row_block;     // rows of y per block of k_adapters_up and k_adapters_few
     uint32_t *err;
 };
@@ -129,80 +131,75 @@ __device__ __forceinline__ float term_scale(float most, float &unscale)
     return __builtin_ldexpf(1.f, ex);
 }
 
-// u = s A x, as terms.  Grid: x = tiles, y = blocks of 64 ranks (RT tiles of
-// 16), z = turns.  The columns go round the waves of the block.  Each XCD
-// takes a contiguous range of the tiles (xcd_block), so that the tiles of a
-// prompt find their A in one L2 cache; dealt out one by one, all eight caches
-// fetched every A, and that cost more than x (8192 tokens of 16 adapters,
-// 4096 columns, rank 64: 77 us).
-template <int T, int YT, int TT, int RT>
+// Eight values of u of one token, from rank k, as terms.
+template <int T, int YT>
+__device__ __forceinline__ void put_terms(const AdapterArgs &g, uint64_t token, uint32_t k, const float *f)
+{
+    constexpr int kTerms = Terms<T, YT>::kCount;
+    typename Type<T>::x8 u[kTerms];
+    Terms<T, YT>::split(f, u);
+#pragma unroll
+    for (int c = 0; c < kTerms; c++)
+        *reinterpret_cast<u32x4 *>(g.u + (c * g.m + token) * g.rank_pad + k) = __builtin_bit_cast(u32x4, u[c]);
+}
+
+// u = s A x, as terms, of tiles of 16 tokens.  Grid: x = tiles, y = blocks of
+// 64 ranks (RT tiles of 16), z = turns.  The columns go round the waves of the
+// block, four steps of 32 (of which a lane has 8: all there, or none) on their
+// way at once.
+template <int T, int YT, int RT>
 __global__ __launch_bounds__(64 * kDownWaves, 2) void k_adapters_down(AdapterArgs g)
 {
-    constexpr int Q = 4;
     using Ty = Type<T>;
     using X8 = typename Ty::x8;
-    constexpr int W = kDownWaves, kTerms = Terms<T, YT>::kCount, kPad = 16 * RT + 4;  // + 4: tokens in different banks
-    __shared__ f32x4 part[W][RT * TT][64];
-    __shared__ float su[16 * TT][kPad];
+    constexpr int Q = 4, W = kDownWaves, kPad = 16 * RT + 4;  // + 4: tokens in different banks
+    __shared__ f32x4 part[W][RT][64];
+    __shared__ float su[16][kPad];
     const uint32_t wave = threadIdx.x >> 6, lane = threadIdx.x & 63, i = lane & 15, gr = lane >> 4;
-    const uint64_t tile = (uint64_t)xcd_block() * (16 * TT);
+    const uint64_t tile = (uint64_t)blockIdx.x * 16;
     const uint32_t r0 = blockIdx.y * 64, steps = (g.cols + 31) / 32;
-    TileIds ids(g, tile, 16 * TT);
-    const uint16_t *xr[TT];
-#pragma unroll
-    for (int t = 0; t < TT; t++) xr[t] = g.x + min(tile + 16 * t + i, g.m - 1) * g.x_stride;
+    TileIds ids(g, tile, 16);
+    const uint16_t *xr = g.x + min(tile + i, g.m - 1) * g.x_stride;
     uint32_t adapter, turn = 0;
     uint64_t mask;
     while (ids.next(adapter, mask)) {
         if (turn++ % gridDim.z != blockIdx.z) continue;
         const uint16_t *ar[RT];
+        f32x4 acc[RT];
 #pragma unroll
-        for (int r = 0; r < RT; r++)
+        for (int r = 0; r < RT; r++) {
             ar[r] = g.a + ((uint64_t)adapter * g.rank + min(r0 + 16 * r + i, g.rank - 1)) * g.cols;
-        f32x4 acc[RT][TT];
-#pragma unroll
-        for (int r = 0; r < RT; r++)
-#pragma unroll
-            for (int t = 0; t < TT; t++) acc[r][t] = f32x4{0.f, 0.f, 0.f, 0.f};
-        // A step is 32 columns, of which a lane has 8: all there, or none.
-        // Four steps are on their way at once: x comes from memory, and a
-        // block per compute unit has registers to wait with.
+            acc[r] = f32x4{0.f, 0.f, 0.f, 0.f};
+        }
         for (uint32_t j = 0; wave_step<W>(wave, j) < steps; j += Q) {
-            X8 av[Q][RT], xv[Q][TT];
+            X8 av[Q][RT], xv[Q];
 #pragma unroll
             for (int q = 0; q < Q; q++) {
-                const uint32_t k = 32 * wave_step<W>(wave, j + q) + 8 * gr;
-                const bool in = k < g.cols;
+                const uint32_t c = 32 * wave_step<W>(wave, j + q) + 8 * gr, k = min(c, g.cols - 8);
+                const bool in = c < g.cols;
+                xv[q] = __builtin_bit_cast(X8, only(in, load16<16>(xr + k)));
 #pragma unroll
-                for (int t = 0; t < TT; t++)
-                    xv[q][t] = __builtin_bit_cast(X8, in ? load16<16>(xr[t] + k) : u32x4{0u, 0u, 0u, 0u});
-#pragma unroll
-                for (int r = 0; r < RT; r++)
-                    av[q][r] = __builtin_bit_cast(X8, in ? load16<16>(ar[r] + k) : u32x4{0u, 0u, 0u, 0u});
+                for (int r = 0; r < RT; r++) av[q][r] = __builtin_bit_cast(X8, only(in, load16<16>(ar[r] + k)));
             }
 #pragma unroll
             for (int q = 0; q < Q; q++)
 #pragma unroll
-                for (int r = 0; r < RT; r++)
-#pragma unroll
-                    for (int t = 0; t < TT; t++) acc[r][t] = Ty::mfma(av[q][r], xv[q][t], acc[r][t]);
+                for (int r = 0; r < RT; r++) acc[r] = Ty::mfma(av[q][r], xv[q], acc[r]);
         }
 #pragma unroll
-        for (int r = 0; r < RT; r++)
-#pragma unroll
-            for (int t = 0; t < TT; t++) part[wave][r * TT + t][lane] = acc[r][t];
+        for (int r = 0; r < RT; r++) part[wave][r][lane] = acc[r];
         __syncthreads();
         const float scale = g.scales ? g.scales[adapter] : 1.f;
-        for (uint32_t q = threadIdx.x; q < 64 * RT * TT; q += 64 * W) {  // four ranks of a token
-            const uint32_t c = q >> 6, l = q & 63, t = c % TT, r = 16 * (c / TT) + 4 * (l >> 4);
+        for (uint32_t q = threadIdx.x; q < 64 * RT; q += 64 * W) {  // four ranks of a token
+            const uint32_t c = q >> 6, l = q & 63, r = 16 * c + 4 * (l >> 4);
             f32x4 v = part[0][c][l];
 #pragma unroll
             for (int w = 1; w < W; w++) v += part[w][c][l];
 #pragma unroll
-            for (int e = 0; e < 4; e++) su[16 * t + (l & 15)][r + e] = r0 + r + e < g.rank ? scale * v[e] : 0.f;
+            for (int e = 0; e < 4; e++) su[l & 15][r + e] = r0 + r + e < g.rank ? scale * v[e] : 0.f;
         }
         __syncthreads();
-        for (uint32_t q = threadIdx.x; q < 16 * TT * 2 * RT; q += 64 * W) {  // eight ranks of a token
+        for (uint32_t q = threadIdx.x; q < 16 * 2 * RT; q += 64 * W) {  // eight ranks of a token
             const uint32_t t = q / (2 * RT), r = 8 * (q % (2 * RT));
             if (!((mask >> t) & 1) || r0 + r >= g.rank_pad) continue;
             float most = 0.f, unscale;
@@ -212,19 +209,150 @@ __global__ __launch_bounds__(64 * kDownWaves, 2) void k_adapters_down(AdapterArg
             float f[8];
 #pragma unroll
             for (int e = 0; e < 8; e++) f[e] = sc * su[t][r + e];
-            X8 u[kTerms];
-            Terms<T, YT>::split(f, u);
-            const uint64_t at = (tile + t) * g.rank_pad + r0 + r;
+            put_terms<T, YT>(g, tile + t, r0 + r, f);
+            if (RT == 1) {  // the rank's padding to 32
 #pragma unroll
-            for (int c = 0; c < kTerms; c++)
-                *reinterpret_cast<u32x4 *>(g.u + c * g.m * g.rank_pad + at) = __builtin_bit_cast(u32x4, u[c]);
-            if (RT == 1)  // the rank's padding to 32
-                for (int c = 0; c < kTerms; c++)
-                    *reinterpret_cast<u32x4 *>(g.u + c * g.m * g.rank_pad + at + 16) = u32x4{0u, 0u, 0u, 0u};
+                for (int e = 0; e < 8; e++) f[e] = 0.f;
+                put_terms<T, YT>(g, tile + t, r + 16, f);
+            }
             if (r == 0) g.unscale[(tile + t) * gridDim.y + blockIdx.y] = unscale;
         }
         __syncthreads();
     }
+}
+
+// A x of many tokens, without the scales, in parts along the columns.  Grid:
+// x = tiles of 128 tokens x splits, y = blocks of 64 ranks (RT tiles of 16).
+// The four waves of a block take 32 tokens each; their rows and those of A
+// are read in whole lines and come to operand order in LDS (Strip), A once
+// for the block.  With 32 tokens a block and all columns, A passed through
+// the L1 cache twice as often as x, and that took 75 us where this takes ABL0
+// (8192 tokens, 4096 columns, rank 64).  The next columns are on their way
+// while these are multiplied.
+template <int T, int RT>
+__global__ __launch_bounds__(256) void k_adapters_down_many(AdapterArgs g)
+{
+    using Ty = Type<T>;
+    using X8 = typename Ty::x8;
+    __shared__ Strip sa[RT], sx[4][2];
+    const uint32_t wave = threadIdx.x >> 6, lane = threadIdx.x & 63, i = lane & 15, gr = lane >> 4;
+    const uint32_t hi = lane >> 5, lo = lane & 31;
+    const uint32_t block = xcd_block(), split = block % g.splits, r0 = blockIdx.y * 64;
+    const uint64_t tile = (uint64_t)(block / g.splits) * 128, first = tile + 32 * wave;
+    const uint32_t c0 = split * g.split_cols, c1 = min(g.cols, c0 + g.split_cols);
+    TileIds low(g, tile, 64), high(g, tile + 64, 64);
+    const uint16_t *xr[2][8];  // the rows of the lane's loads
+#pragma unroll
+    for (int t = 0; t < 2; t++)
+#pragma unroll
+        for (int u = 0; u < 8; u++) xr[t][u] = g.x + min(first + 16 * t + 2 * u + hi, g.m - 1) * g.x_stride;
+    uint64_t mlow, mhigh;
+    uint32_t adapter;
+    while (low.pending | high.pending) {
+        if (low.next(adapter, mlow)) {
+            high.take(adapter, mhigh);
+        } else {
+            mlow = 0;
+            high.next(adapter, mhigh);
+        }
+        const uint32_t mask = (uint32_t)((wave & 2 ? mhigh : mlow) >> (32 * (wave & 1)));  // the wave's tokens
+        const uint16_t *a = g.a + (uint64_t)adapter * g.rank * g.cols;
+        f32x4 acc[RT][2];
+#pragma unroll
+        for (int r = 0; r < RT; r++) acc[r][0] = acc[r][1] = f32x4{0.f, 0.f, 0.f, 0.f};
+        u32x4 xv[2][8], av[2 * RT];
+        auto fetch = [&](uint32_t c) {
+            const uint32_t k = min(c + 8 * lo, g.cols - 8);
+            if (mask) {
+#pragma unroll
+                for (int t = 0; t < 2; t++)
+#pragma unroll
+                    for (int u = 0; u < 8; u++) xv[t][u] = read16<16, true>(xr[t][u] + k);
+            }
+#pragma unroll
+            for (int u = 0; u < 2 * RT; u++)  // a quarter of A's rows
+                av[u] = load16<16>(a + (uint64_t)min(r0 + 4 * RT * wave + 2 * u + hi, g.rank - 1) * g.cols + k);
+        };
+        if (c0 < c1) fetch(c0);
+        for (uint32_t c = c0; c < c1; c += kStripCols) {
+            const bool there = c + 8 * lo < c1;
+            __syncthreads();  // the last columns' readers are done
+            if (mask) {
+#pragma unroll
+                for (int t = 0; t < 2; t++)
+#pragma unroll
+                    for (int u = 0; u < 8; u++) sx[wave][t].q[(2 * u + hi) * kStripPitch + lo] = only(there, xv[t][u]);
+            }
+#pragma unroll
+            for (int u = 0; u < 2 * RT; u++) {
+                const uint32_t r = 4 * RT * wave + 2 * u + hi;
+                sa[r >> 4].q[(r & 15) * kStripPitch + lo] = only(there, av[u]);
+            }
+            __syncthreads();
+            if (c + kStripCols < c1) fetch(c + kStripCols);
+            if (!mask) continue;
+#pragma unroll
+            for (int s = 0; s < (int)kStripCols / 32; s++) {
+                X8 xo[2];
+#pragma unroll
+                for (int t = 0; t < 2; t++) xo[t] = __builtin_bit_cast(X8, sx[wave][t].q[i * kStripPitch + 4 * s + gr]);
+#pragma unroll
+                for (int r = 0; r < RT; r++) {
+                    const X8 ao = __builtin_bit_cast(X8, sa[r].q[i * kStripPitch + 4 * s + gr]);
+#pragma unroll
+                    for (int t = 0; t < 2; t++) acc[r][t] = Ty::mfma(ao, xo[t], acc[r][t]);
+                }
+            }
+        }
+#pragma unroll
+        for (int t = 0; t < 2; t++) {
+            if (!((mask >> (16 * t + i)) & 1)) continue;
+            float *p = g.part + ((uint64_t)split * g.m + first + 16 * t + i) * g.rank_pad + r0 + 4 * gr;
+#pragma unroll
+            for (int r = 0; r < RT; r++)
+                if (r0 + 16 * r < g.rank_pad) *reinterpret_cast<f32x4 *>(p + 16 * r) = acc[r][t];
+        }
+    }
+}
+
+// u from its parts: eight lanes for the 64 ranks of a block of one token.
+template <int T, int YT>
+__global__ __launch_bounds__(256) void k_adapters_terms(AdapterArgs g)
+{
+    const uint32_t blocks = (g.rank_pad + 63) / 64;
+    const uint64_t q = (uint64_t)blockIdx.x * 32 + threadIdx.x / 8, token = q / blocks;
+    const uint32_t rb = (uint32_t)(q % blocks), k = 64 * rb + 8 * (threadIdx.x % 8);
+    if (token >= g.m) return;
+    const int64_t id = g.ids[token];
+    if (id < 0 || id >= (int64_t)g.n) return;  // the same for a token's lanes
+    float f[8];
+#pragma unroll
+    for (int e = 0; e < 8; e++) f[e] = 0.f;
+    if (k < g.rank_pad) {
+        const float *p = g.part + token * g.rank_pad + k;
+        for (uint32_t s = 0; s < g.splits; s++, p += g.m * g.rank_pad) {
+            const f32x4 v = *reinterpret_cast<const f32x4 *>(p), w = *reinterpret_cast<const f32x4 *>(p + 4);
+#pragma unroll
+            for (int e = 0; e < 4; e++) {
+                f[e] += v[e];
+                f[4 + e] += w[e];
+            }
+        }
+    }
+    const float scale = g.scales ? g.scales[id] : 1.f;
+    float most = 0.f, unscale;
+#pragma unroll
+    for (int e = 0; e < 8; e++) {
+        f[e] = k + e < g.rank ? scale * f[e] : 0.f;
+        most = fmaxf(most, fabsf(f[e]));
+    }
+    if constexpr (T == WC_T_FP16)
+        for (int o = 1; o < 8; o *= 2) most = fmaxf(most, __shfl_xor(most, o, 8));
+    const float sc = term_scale<T>(most, unscale);
+#pragma unroll
+    for (int e = 0; e < 8; e++) f[e] *= sc;
+    if (k < g.rank_pad) put_terms<T, YT>(g, token, k, f);
+    if (threadIdx.x % 8 == 0) g.unscale[token * blocks + rb] = unscale;
 }
 
 // The same within a wave: u of one token (32 KS values, those of the lane; the
@@ -455,7 +583,7 @@ __global__ __launch_bounds__(256) void k_adapters_up(AdapterArgs g)
 // of a token at a time, and past the caches where it is larger than they are
 // (kStream); the products come to that order through LDS as well.
 template <int T, int YT, int KS, bool kStream>
-__global__ __launch_bounds__(256, 3) void k_adapters_up_many(AdapterArgs g)
+__global__ __launch_bounds__(256, KS == 2 && (T == WC_T_FP16 || YT == WC_T_FP32) ? 2 : 3) void k_adapters_up_many(AdapterArgs g)
 {
     using Ty = Type<T>;
     using Y = Type<YT>;

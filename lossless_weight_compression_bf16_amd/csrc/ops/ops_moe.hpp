@@ -74,13 +74,6 @@ struct MoeTerms<WC_T_FP16> {
 };
 
 __device__ __forceinline__ u32x4 zero4() { return u32x4{0u, 0u, 0u, 0u}; }
-__device__ __forceinline__ u32x4 only(bool in, u32x4 v)  // all lanes load, some drop what they got
-{
-#pragma unroll
-    for (int e = 0; e < 4; e++) v[e] = in ? v[e] : 0u;
-    return v;
-}
-
 // logits[split][t][e]: 16 experts per block, the columns of a split over its
 // four waves.
 template <int T, int TT>
@@ -276,18 +269,6 @@ struct MoeSet {
                 if (ids[lane * g.top_k + s] == (int32_t)expert) at = (int32_t)(lane * g.top_k + s);
         return at;
     }
-};
-
-// Sixteen rows of weights through a wave's own LDS, 256 columns at a time.
-// Read in operand order, an instruction takes 64 bytes of each of 16 rows,
-// halves of lines; read along the rows, 512 bytes of each of two, whole
-// lines, past the caches: 7.1 against 5.8 TB/s over a large buffer, and 6.3
-// against 3.6 TB/s where every compute unit has 256 KiB to read.  LDS turns
-// one order into the other; rows lie 576 bytes apart, so that the 16 rows of
-// an operand spread over all banks.
-constexpr uint32_t kStripCols = 256, kStripPitch = 36;  // pitch in 16 bytes
-struct Strip {
-    u32x4 q[16 * kStripPitch];
 };
 
 // acc[m][o][t] += W_m X_t over columns c0 .. c1 (multiples of 8) for M

@@ -73,9 +73,9 @@ void launch_grad(const LogprobGradArgs &g, dim3 grid, bool large, hipStream_t st
 // their adapter over many tokens, so that it is read once per tile.
 struct AdapterPlan {
     bool few;                                                    // k_adapters_few
-    uint32_t rank_pad, rank_blocks, tile, turns;                 // k_adapters_down
+    uint32_t rank_pad, rank_blocks, tile, turns, splits, split_cols;  // k_adapters_down, k_adapters_down_many
     uint32_t up_tile, row_blocks, row_block;                     // k_adapters_up
-    uint64_t tiles, up_tiles, unscale, scratch;                  // unscale: its place in the scratch
+    uint64_t tiles, up_tiles, unscale, part, scratch;            // unscale, part: their places in the scratch
 };
 
 AdapterPlan adapter_plan(uint64_t m, uint32_t rank, uint32_t cols, uint32_t rows)
@@ -98,20 +98,27 @@ AdapterPlan adapter_plan(uint64_t m, uint32_t rank, uint32_t cols, uint32_t rows
         return p;
     }
     p.rank_blocks = (uint32_t)ceil_div(rank, 64);
-    p.tile = many ? 32 : 16;
+    p.tile = many ? 128 : 16;
     p.tiles = ceil_div(m, p.tile);
+    const uint64_t most = ceil_div(cols, kStripCols);
+    uint64_t splits = many ? ceil_div(kCus, p.tiles * p.rank_blocks) : 1;
+    if (splits > most) splits = most;
+    if (splits > 8) splits = 8;
+    p.split_cols = (uint32_t)(ceil_div(most, splits) * kStripCols);
+    p.splits = (uint32_t)ceil_div(cols, p.split_cols);
     // k_adapters_up_many takes 128 tokens and 64 rows at a time, k_adapters_up 16 and 256
     const bool wide = many && rank <= 64;
     p.up_tile = wide ? 128 : 16;
     p.up_tiles = ceil_div(m, p.up_tile);
     const uint32_t least = wide ? 64 : 256;
     uint64_t rb = ceil_div((wide ? 4 : 8) * kCus, p.up_tiles * p.turns);
-    const uint64_t rmost = ceil_div(rows, 256);
+    const uint64_t rmost = ceil_div(rows, least);
     if (rb > rmost) rb = rmost;
     p.row_block = (uint32_t)(ceil_div(ceil_div(rows, rb), least) * least);
     p.row_blocks = (uint32_t)ceil_div(rows, p.row_block);
     p.unscale = 2ull * Terms<WC_T_BF16, WC_T_FP32>::kCount * m * p.rank_pad;  // the most terms of all types
-    p.scratch = p.unscale + 4 * m * p.rank_blocks;
+    p.part = ceil_div(p.unscale + 4 * m * p.rank_blocks, 16) * 16;
+    p.scratch = p.part + (many ? 4ull * p.splits * m * p.rank_pad : 0);
     return p;
 }
 
@@ -121,13 +128,23 @@ bool valid_adapters(uint64_t m, uint32_t rank, uint32_t cols, uint32_t rows)
            cols <= (1u << 30) && (uint64_t)rows * rank < (1ull << 31);
 }
 
-template <int T, int YT, int TT>
+template <int T, int YT>
 void launch_down(const AdapterArgs &g, const AdapterPlan &p, hipStream_t stream)
 {
     const dim3 grid((uint32_t)p.tiles, p.rank_blocks, p.turns), block(64 * kDownWaves);
-    if (g.rank <= 16) hipLaunchKernelGGL((k_adapters_down<T, YT, TT, 1>), grid, block, 0, stream, g);
-    else if (g.rank <= 32) hipLaunchKernelGGL((k_adapters_down<T, YT, TT, 2>), grid, block, 0, stream, g);
-    else hipLaunchKernelGGL((k_adapters_down<T, YT, TT, 4>), grid, block, 0, stream, g);
+    if (g.rank <= 16) hipLaunchKernelGGL((k_adapters_down<T, YT, 1>), grid, block, 0, stream, g);
+    else if (g.rank <= 32) hipLaunchKernelGGL((k_adapters_down<T, YT, 2>), grid, block, 0, stream, g);
+    else hipLaunchKernelGGL((k_adapters_down<T, YT, 4>), grid, block, 0, stream, g);
+}
+
+template <int T, int YT>
+void launch_down_many(const AdapterArgs &g, const AdapterPlan &p, hipStream_t stream)
+{
+    const dim3 grid((uint32_t)(p.tiles * p.splits), p.rank_blocks), block(256);
+    if (g.rank <= 16) hipLaunchKernelGGL((k_adapters_down_many<T, 1>), grid, block, 0, stream, g);
+    else if (g.rank <= 32) hipLaunchKernelGGL((k_adapters_down_many<T, 2>), grid, block, 0, stream, g);
+    else hipLaunchKernelGGL((k_adapters_down_many<T, 4>), grid, block, 0, stream, g);
+    hipLaunchKernelGGL((k_adapters_terms<T, YT>), dim3((uint32_t)ceil_div(g.m * p.rank_blocks, 32)), block, 0, stream, g);
 }
 
 template <int T, int YT>
@@ -162,8 +179,8 @@ wc_status launch_adapters(const AdapterArgs &g, const AdapterPlan &p, hipStream_
     if (p.few) {
         launch_few<T, YT>(g, p, stream);
     } else {
-        if (p.tile == 32) launch_down<T, YT, 2>(g, p, stream);
-        else launch_down<T, YT, 1>(g, p, stream);
+        if (p.tile == 128) launch_down_many<T, YT>(g, p, stream);
+        else launch_down<T, YT>(g, p, stream);
         launch_up<T, YT>(g, p, stream);
     }
     return launched();
@@ -362,7 +379,7 @@ wc_status wc_add_adapters(const wc_adapters *a, void *d_scratch, uint64_t scratc
     if (!a->y || !aligned(a->y, type_bytes(a->y_type)) || (a->m > 1 && a->y_stride < a->rows)) return WC_ERR_ARG;
     if (!a->ids || !aligned(a->ids, 8) || !aligned(a->scales, 4)) return WC_ERR_ARG;
     const AdapterPlan p = adapter_plan(a->m, a->rank, a->cols, a->rows);
-    if (p.tiles > kMaxGrid || p.up_tiles * p.row_blocks > kMaxGrid) return WC_ERR_ARG;
+    if (p.tiles * p.splits > kMaxGrid || p.up_tiles * p.row_blocks > kMaxGrid) return WC_ERR_ARG;
     if (scratch_bytes < p.scratch) return WC_ERR_CAPACITY;
     if (p.scratch && (!d_scratch || !aligned(d_scratch, 16))) return WC_ERR_ARG;
     AdapterArgs g{};
@@ -381,7 +398,10 @@ wc_status wc_add_adapters(const wc_adapters *a, void *d_scratch, uint64_t scratc
     g.rows = a->rows;
     g.u = static_cast<uint16_t *>(d_scratch);
     g.unscale = reinterpret_cast<float *>(static_cast<char *>(d_scratch) + p.unscale);
+    g.part = reinterpret_cast<float *>(static_cast<char *>(d_scratch) + p.part);
     g.rank_pad = p.rank_pad;
+    g.splits = p.splits;
+    g.split_cols = p.split_cols;
     g.row_block = p.row_block;
     g.err = d_err;
     return a->type == WC_T_BF16 ? launch_adapters<WC_T_BF16>(g, p, a->y_type, stream)

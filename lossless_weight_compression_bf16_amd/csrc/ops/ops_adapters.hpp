@@ -2,14 +2,16 @@
 // projection:  y_t += s_i B_i (A_i x_t)  with i = ids[t], A_i of rank x cols,
 // B_i of rows x rank.
 //
-// On the matrix cores, over tiles of 16 (few tokens) or 64 consecutive tokens
+// On the matrix cores, over tiles of 16 (few tokens) or 128 consecutive tokens
 // and, within a tile, one adapter after the other: the tokens of a prompt lie
 // side by side and share their adapter, the tokens of a batch of single
-// requests differ and take one turn each, spread over the grid's z.
-//   k_adapters_few   few tokens: both products in one launch
-//   k_adapters_down  u_t = s_i A_i x_t; for many tokens k_adapters_down_many,
-//                    in parts along the columns, and k_adapters_terms
-//   k_adapters_up    y_t += B_i u_t, or, for many tokens, k_adapters_up_many
+// requests differ and take one turn each, spread over the grid.
+//   k_adapters_few    few tokens: both products in one launch
+//   k_adapters_down   A_i x_t in parts along the columns; for many tokens
+//                     k_adapters_down_many
+//   k_adapters_terms  u_t = s_i times the sum of the parts, as terms (below)
+//   k_adapters_up     y_t += B_i u_t, u from the parts up to rank 64; for many
+//                     tokens k_adapters_up_many
 // What bounds it: x read once, y read and written once.  u stays in 32 bits:
 // it enters the matrix cores as a sum of 16-bit numbers, of BF16 or, after a
 // scaling by a power of two per token that brings its largest value to
@@ -40,9 +42,9 @@ struct AdapterArgs {
     const float *scales;    // n, or null: 1
     uint64_t m;
     uint32_t n, rank, cols, rows;
-    uint16_t *u;            // terms x m x rank_pad: k_adapters_down's result
-    float *unscale;         // m x rank blocks: what k_adapters_up multiplies its products by
-    float *part;            // splits x m x rank_pad: k_adapters_down_many's result
+    float *part;            // splits x m x rank_pad: A x in parts
+    uint16_t *u;            // terms x m x rank_pad: k_adapters_terms' result
+    float *unscale;         // m x rank blocks: what the products of the terms are multiplied by
     uint32_t rank_pad;      // the rank rounded up to 32
     uint32_t splits, split_cols;
     uint32_t row_block;     // rows of y per block of k_adapters_up and k_adapters_few
@@ -143,27 +145,32 @@ __device__ __forceinline__ void put_terms(const AdapterArgs &g, uint64_t token, 
         *reinterpret_cast<u32x4 *>(g.u + (c * g.m + token) * g.rank_pad + k) = __builtin_bit_cast(u32x4, u[c]);
 }
 
-// u = s A x, as terms, of tiles of 16 tokens.  Grid: x = tiles, y = blocks of
-// 64 ranks (RT tiles of 16), z = turns.  The columns go round the waves of the
-// block, four steps of 32 (of which a lane has 8: all there, or none) on their
-// way at once.
-template <int T, int YT, int RT>
+// A x of tiles of 16 tokens, without the scales, in parts along the columns.
+// Grid: x = tiles x splits, y = blocks of 64 ranks (RT tiles of 16), z = turns.
+// The columns go round the waves of the block, four steps of 32 (of which a
+// lane has 8: all there, or none) on their way at once.  What bounds it is the
+// latency of its loads, so that a block takes no more columns than are on
+// their way at once where there are compute units for it: 61 tokens of 32
+// adapters of rank 16, 4096 columns, take 5.4 us in four parts, 12.2 in one
+// with every token's row read for every adapter.
+template <int T, int RT>
 __global__ __launch_bounds__(64 * kDownWaves, 2) void k_adapters_down(AdapterArgs g)
 {
     using Ty = Type<T>;
     using X8 = typename Ty::x8;
-    constexpr int Q = 4, W = kDownWaves, kPad = 16 * RT + 4;  // + 4: tokens in different banks
+    constexpr int Q = 4, W = kDownWaves;
     __shared__ f32x4 part[W][RT][64];
-    __shared__ float su[16][kPad];
     const uint32_t wave = threadIdx.x >> 6, lane = threadIdx.x & 63, i = lane & 15, gr = lane >> 4;
-    const uint64_t tile = (uint64_t)blockIdx.x * 16;
-    const uint32_t r0 = blockIdx.y * 64, steps = (g.cols + 31) / 32;
+    const uint64_t tile = (uint64_t)(blockIdx.x / g.splits) * 16;
+    const uint32_t split = blockIdx.x % g.splits, c0 = split * g.split_cols, c1 = min(g.cols, c0 + g.split_cols);
+    const uint32_t r0 = blockIdx.y * 64, steps = (c1 - c0 + 31) / 32;
     TileIds ids(g, tile, 16);
-    const uint16_t *xr = g.x + min(tile + i, g.m - 1) * g.x_stride;
     uint32_t adapter, turn = 0;
     uint64_t mask;
     while (ids.next(adapter, mask)) {
         if (turn++ % gridDim.z != blockIdx.z) continue;
+        // lanes of other tokens repeat the first one's loads
+        const uint16_t *xr = g.x + (tile + ((mask >> i) & 1 ? i : (uint32_t)__builtin_ctzll(mask))) * g.x_stride;
         const uint16_t *ar[RT];
         f32x4 acc[RT];
 #pragma unroll
@@ -175,8 +182,8 @@ __global__ __launch_bounds__(64 * kDownWaves, 2) void k_adapters_down(AdapterArg
             X8 av[Q][RT], xv[Q];
 #pragma unroll
             for (int q = 0; q < Q; q++) {
-                const uint32_t c = 32 * wave_step<W>(wave, j + q) + 8 * gr, k = min(c, g.cols - 8);
-                const bool in = c < g.cols;
+                const uint32_t c = c0 + 32 * wave_step<W>(wave, j + q) + 8 * gr, k = min(c, g.cols - 8);
+                const bool in = c < c1;
                 xv[q] = __builtin_bit_cast(X8, only(in, load16<16>(xr + k)));
 #pragma unroll
                 for (int r = 0; r < RT; r++) av[q][r] = __builtin_bit_cast(X8, only(in, load16<16>(ar[r] + k)));
@@ -189,33 +196,13 @@ __global__ __launch_bounds__(64 * kDownWaves, 2) void k_adapters_down(AdapterArg
 #pragma unroll
         for (int r = 0; r < RT; r++) part[wave][r][lane] = acc[r];
         __syncthreads();
-        const float scale = g.scales ? g.scales[adapter] : 1.f;
         for (uint32_t q = threadIdx.x; q < 64 * RT; q += 64 * W) {  // four ranks of a token
-            const uint32_t c = q >> 6, l = q & 63, r = 16 * c + 4 * (l >> 4);
+            const uint32_t c = q >> 6, l = q & 63, t = l & 15, r = r0 + 16 * c + 4 * (l >> 4);
             f32x4 v = part[0][c][l];
 #pragma unroll
             for (int w = 1; w < W; w++) v += part[w][c][l];
-#pragma unroll
-            for (int e = 0; e < 4; e++) su[l & 15][r + e] = r0 + r + e < g.rank ? scale * v[e] : 0.f;
-        }
-        __syncthreads();
-        for (uint32_t q = threadIdx.x; q < 16 * 2 * RT; q += 64 * W) {  // eight ranks of a token
-            const uint32_t t = q / (2 * RT), r = 8 * (q % (2 * RT));
-            if (!((mask >> t) & 1) || r0 + r >= g.rank_pad) continue;
-            float most = 0.f, unscale;
-            if constexpr (T == WC_T_FP16)
-                for (uint32_t e = 0; e < 16 * RT; e++) most = fmaxf(most, fabsf(su[t][e]));
-            const float sc = term_scale<T>(most, unscale);
-            float f[8];
-#pragma unroll
-            for (int e = 0; e < 8; e++) f[e] = sc * su[t][r + e];
-            put_terms<T, YT>(g, tile + t, r0 + r, f);
-            if (RT == 1) {  // the rank's padding to 32
-#pragma unroll
-                for (int e = 0; e < 8; e++) f[e] = 0.f;
-                put_terms<T, YT>(g, tile + t, r + 16, f);
-            }
-            if (r == 0) g.unscale[(tile + t) * gridDim.y + blockIdx.y] = unscale;
+            if (((mask >> t) & 1) && r < g.rank_pad)
+                *reinterpret_cast<f32x4 *>(g.part + ((uint64_t)split * g.m + tile + t) * g.rank_pad + r) = v;
         }
         __syncthreads();
     }
@@ -226,7 +213,7 @@ __global__ __launch_bounds__(64 * kDownWaves, 2) void k_adapters_down(AdapterArg
 // The four waves of a block take 32 tokens each; their rows and those of A
 // are read in whole lines and come to operand order in LDS (Strip), A once
 // for the block.  With 32 tokens a block and all columns, A passed through
-// the L1 cache twice as often as x, and that took 75 us where this takes ABL0
+// the L1 cache twice as often as x, and that took 75 us where this takes 39
 // (8192 tokens, 4096 columns, rank 64).  The next columns are on their way
 // while these are multiplied.
 template <int T, int RT>
@@ -495,81 +482,105 @@ __device__ __noinline__ void y_add_some(typename Type<YT>::elem *p, uint32_t gr,
 }
 
 // y += B u.  Grid: x = tiles x row blocks, z = turns.  A wave takes 64 rows
-// of B at a time; u stays in its registers, or, with kBlocks blocks of 64
-// ranks (each with its own scaling), is read again for every 64 rows.
+// of B at a time; u, the sum of its parts, stays in its registers, or, with
+// kBlocks blocks of 64 ranks (each with its own scaling), is read again for
+// every 64 rows, as terms.  54 tokens of 32 adapters of rank 16, 14336 rows,
+// FP32: 11.7 us (2.3 TB/s of B and y).  What bounds it is each wave's chain of
+// waits (ids, then u, B and y at once, then the stores) over the waves that
+// fit: 256 or 1024 rows a block took 15.5 and 12.3 us, and loading the next
+// rows ahead costs registers, hence waves (16.3 us).
 template <int T, int YT, int KS, bool kBlocks>
-__global__ __launch_bounds__(256) void k_adapters_up(AdapterArgs g)
+__global__ __launch_bounds__(256, KS == 1 ? 4 : 2) void k_adapters_up(AdapterArgs g)
 {
-    constexpr int TT = 1;
     using Ty = Type<T>;
     using YE = typename Type<YT>::elem;
     using X8 = typename Ty::x8;
     constexpr int kTerms = Terms<T, YT>::kCount;
     const uint32_t wave = threadIdx.x >> 6, lane = threadIdx.x & 63, i = lane & 15, gr = lane >> 4;
     const uint32_t row_blocks = (g.rows + g.row_block - 1) / g.row_block, rank_blocks = kBlocks ? (g.rank_pad + 63) / 64 : 1;
-    const uint64_t tile = (uint64_t)(blockIdx.x / row_blocks) * (16 * TT);
+    const uint64_t tile = (uint64_t)(blockIdx.x / row_blocks) * 16;
     const uint32_t n0 = (blockIdx.x % row_blocks) * g.row_block, n1 = min(g.rows, n0 + g.row_block);
-    TileIds ids(g, tile, 16 * TT);
-    uint64_t token[TT];
-    YE *yr[TT];
-#pragma unroll
-    for (int t = 0; t < TT; t++) {
-        token[t] = min(tile + 16 * t + i, g.m - 1);
-        yr[t] = static_cast<YE *>(g.y) + token[t] * g.y_stride;
-    }
+    TileIds ids(g, tile, 16);
     uint32_t adapter, turn = 0;
     uint64_t mask;
     while (ids.next(adapter, mask)) {
         if (turn++ % gridDim.z != blockIdx.z) continue;
-        X8 u[TT][KS][kTerms];
-        float unscale[TT];
-        // every lane reads its column's u, also of a token that is another adapter's (then it is dropped)
-        auto fetch_u = [&](uint32_t rb) {
-#pragma unroll
-            for (int t = 0; t < TT; t++) {
-#pragma unroll
-                for (int s = 0; s < KS; s++)
-#pragma unroll
-                    for (int c = 0; c < kTerms; c++) {
-                        const uint32_t k = min(64 * rb + 32 * s, g.rank_pad - 32) + 8 * gr;  // past it B is zero
-                        u[t][s][c] = __builtin_bit_cast(X8, load16<16>(g.u + (c * g.m + token[t]) * g.rank_pad + k));
-                    }
-                unscale[t] = T == WC_T_FP16 ? g.unscale[token[t] * rank_blocks + rb] : 1.f;
-            }
-        };
-        fetch_u(0);
+        const bool mine = (mask >> i) & 1;
+        // lanes of other tokens repeat the first one's loads
+        const uint64_t token = tile + (mine ? i : (uint32_t)__builtin_ctzll(mask));
+        YE *const yr = static_cast<YE *>(g.y) + token * g.y_stride;
         const BRows<T, YT, KS> rows(g, adapter, 0);
-        for (uint32_t nb = n0 + 64 * wave; nb < n1; nb += 256) {
-            X8 bv[4][KS];
-            YRow<YT> y[TT];
-            const bool whole = nb + 64 <= n1;
-            // all of the tile's y is on its way before the first store, which the compiler may not move loads past
-            if (whole) {
-#pragma unroll
-                for (int t = 0; t < TT; t++) y[t].load(yr[t] + nb, gr);
-            }
+        X8 bv[4][KS], u[KS][kTerms];
+        YRow<YT> y;
+        uint32_t nb = n0 + 64 * wave;
+        auto fetch = [&]() {
+            if (nb + 64 <= n1) y.load(yr + nb, gr);
             rows.load(g, nb, bv);
+        };
+        auto fetch_terms = [&](uint32_t rb) {
 #pragma unroll
-            for (int t = 0; t < TT; t++) {
-                f32x4 sum[4];
-                for (uint32_t rb = 0; rb < rank_blocks; rb++) {
-                    if (kBlocks && rb) BRows<T, YT, KS>(g, adapter, 64 * rb).load(g, nb, bv);
-                    if (kBlocks) fetch_u(rb);
+            for (int s = 0; s < KS; s++)
 #pragma unroll
-                    for (int p = 0; p < 4; p++) {
-                        f32x4 acc{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                        for (int s = 0; s < KS; s++)
-#pragma unroll
-                            for (int c = kTerms - 1; c >= 0; c--) acc = Ty::mfma(bv[p][s], u[t][s][c], acc);
-                        if (!kBlocks) sum[p] = acc;
-                        else sum[p] = rb ? sum[p] + unscale[t] * acc : unscale[t] * acc;
-                    }
+                for (int c = 0; c < kTerms; c++) {
+                    const uint32_t k = min(64 * rb + 32 * s, g.rank_pad - 32) + 8 * gr;  // past it B is zero
+                    u[s][c] = __builtin_bit_cast(X8, load16<16>(g.u + (c * g.m + token) * g.rank_pad + k));
                 }
-                if (!((mask >> (16 * t + i)) & 1)) continue;
-                if (whole) y[t].add(yr[t] + nb, gr, sum, kBlocks ? 1.f : unscale[t]);
-                else y_add_some<YT>(yr[t] + nb, gr, n1 - nb, sum[0], sum[1], sum[2], sum[3], kBlocks ? 1.f : unscale[t]);
+            return T == WC_T_FP16 ? g.unscale[token * rank_blocks + rb] : 1.f;
+        };
+        if (nb >= n1) continue;
+        fetch();
+        float unscale = 1.f;
+        if constexpr (!kBlocks) {
+            float f[KS][8];
+            const float *p = g.part + token * g.rank_pad + 8 * gr;
+            const float scale = g.scales ? g.scales[adapter] : 1.f;
+#pragma unroll
+            for (int s = 0; s < KS; s++)
+#pragma unroll
+                for (int e = 0; e < 8; e++) f[s][e] = 0.f;
+            constexpr uint32_t kAtOnce = 4;  // parts on their way
+            for (uint32_t z = 0; z < g.splits; z += kAtOnce) {
+                f32x4 v[kAtOnce][KS][2];
+#pragma unroll
+                for (uint32_t q = 0; q < kAtOnce; q++)
+#pragma unroll
+                    for (int s = 0; s < 2 * KS; s++)
+                        v[q][s / 2][s % 2] = *reinterpret_cast<const f32x4 *>(
+                            p + min(z + q, g.splits - 1) * (g.m * g.rank_pad) + 32 * (s / 2) + 4 * (s % 2));
+#pragma unroll
+                for (uint32_t q = 0; q < kAtOnce; q++)
+#pragma unroll
+                    for (int s = 0; s < KS; s++)
+#pragma unroll
+                        for (int e = 0; e < 8; e++) f[s][e] += z + q < g.splits ? v[q][s][e / 4][e % 4] : 0.f;
             }
+#pragma unroll
+            for (int s = 0; s < KS; s++)
+#pragma unroll
+                for (int e = 0; e < 8; e++) f[s][e] = 32 * s + 8 * gr + e < g.rank ? scale * f[s][e] : 0.f;
+            unscale = adapter_terms<T, YT, KS>(f, u);
+        }
+        while (nb < n1) {
+            f32x4 sum[4];
+            for (uint32_t rb = 0; rb < rank_blocks; rb++) {
+                float us = 1.f;
+                if (kBlocks && rb) BRows<T, YT, KS>(g, adapter, 64 * rb).load(g, nb, bv);
+                if (kBlocks) us = fetch_terms(rb);
+#pragma unroll
+                for (int p = 0; p < 4; p++) {
+                    f32x4 acc{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                    for (int s = 0; s < KS; s++)
+#pragma unroll
+                        for (int c = kTerms - 1; c >= 0; c--) acc = Ty::mfma(bv[p][s], u[s][c], acc);
+                    if (!kBlocks) sum[p] = acc;
+                    else sum[p] = rb ? sum[p] + us * acc : us * acc;
+                }
+            }
+            if (mine && nb + 64 <= n1) y.add(yr + nb, gr, sum, unscale);
+            else if (mine) y_add_some<YT>(yr + nb, gr, n1 - nb, sum[0], sum[1], sum[2], sum[3], unscale);
+            nb += 256;
+            if (nb < n1) fetch();
         }
     }
 }

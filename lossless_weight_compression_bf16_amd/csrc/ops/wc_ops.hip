@@ -69,13 +69,14 @@ void launch_grad(const LogprobGradArgs &g, dim3 grid, bool large, hipStream_t st
 
 // Launch shapes of the adapters: tiles of 16 tokens where the tokens are
 // few, each turn of a tile (an adapter) its own block, so that as many blocks
-// as possible share the reading; tiles of 64 tokens where prompts repeat
+// as possible share the reading; tiles of 128 tokens where prompts repeat
 // their adapter over many tokens, so that it is read once per tile.
 struct AdapterPlan {
     bool few;                                                    // k_adapters_few
+    bool terms;                                                  // k_adapters_terms
     uint32_t rank_pad, rank_blocks, tile, turns, splits, split_cols;  // k_adapters_down, k_adapters_down_many
-    uint32_t up_tile, row_blocks, row_block;                     // k_adapters_up
-    uint64_t tiles, up_tiles, unscale, part, scratch;            // unscale, part: their places in the scratch
+    uint32_t up_tile, row_blocks, row_block;                     // k_adapters_up, k_adapters_up_many
+    uint64_t tiles, up_tiles, u, unscale, scratch;               // u, unscale: their places in the scratch
 };
 
 AdapterPlan adapter_plan(uint64_t m, uint32_t rank, uint32_t cols, uint32_t rows)
@@ -100,11 +101,14 @@ AdapterPlan adapter_plan(uint64_t m, uint32_t rank, uint32_t cols, uint32_t rows
     p.rank_blocks = (uint32_t)ceil_div(rank, 64);
     p.tile = many ? 128 : 16;
     p.tiles = ceil_div(m, p.tile);
-    const uint64_t most = ceil_div(cols, kStripCols);
-    uint64_t splits = many ? ceil_div(kCus, p.tiles * p.rank_blocks) : 1;
+    // columns of a block: as many of its loads as are on their way at once, or
+    // more where the tiles alone fill the compute units
+    const uint32_t step = many ? kStripCols : 32 * 4 * kDownWaves;
+    const uint64_t most = ceil_div(cols, step);
+    uint64_t splits = ceil_div(kCus, p.tiles * p.rank_blocks * p.turns);
     if (splits > most) splits = most;
     if (splits > 8) splits = 8;
-    p.split_cols = (uint32_t)(ceil_div(most, splits) * kStripCols);
+    p.split_cols = (uint32_t)(ceil_div(most, splits) * step);
     p.splits = (uint32_t)ceil_div(cols, p.split_cols);
     // k_adapters_up_many takes 128 tokens and 64 rows at a time, k_adapters_up 16 and 256
     const bool wide = many && rank <= 64;
@@ -116,9 +120,10 @@ AdapterPlan adapter_plan(uint64_t m, uint32_t rank, uint32_t cols, uint32_t rows
     if (rb > rmost) rb = rmost;
     p.row_block = (uint32_t)(ceil_div(ceil_div(rows, rb), least) * least);
     p.row_blocks = (uint32_t)ceil_div(rows, p.row_block);
-    p.unscale = 2ull * Terms<WC_T_BF16, WC_T_FP32>::kCount * m * p.rank_pad;  // the most terms of all types
-    p.part = ceil_div(p.unscale + 4 * m * p.rank_blocks, 16) * 16;
-    p.scratch = p.part + (many ? 4ull * p.splits * m * p.rank_pad : 0);
+    p.terms = many || rank > 64;
+    p.u = 4ull * p.splits * m * p.rank_pad;
+    p.unscale = p.u + (p.terms ? 2ull * Terms<WC_T_BF16, WC_T_FP32>::kCount * m * p.rank_pad : 0);  // the most terms of all types
+    p.scratch = p.unscale + (p.terms ? 4 * m * p.rank_blocks : 0);
     return p;
 }
 
@@ -128,23 +133,22 @@ bool valid_adapters(uint64_t m, uint32_t rank, uint32_t cols, uint32_t rows)
            cols <= (1u << 30) && (uint64_t)rows * rank < (1ull << 31);
 }
 
-template <int T, int YT>
+template <int T>
 void launch_down(const AdapterArgs &g, const AdapterPlan &p, hipStream_t stream)
 {
-    const dim3 grid((uint32_t)p.tiles, p.rank_blocks, p.turns), block(64 * kDownWaves);
-    if (g.rank <= 16) hipLaunchKernelGGL((k_adapters_down<T, YT, 1>), grid, block, 0, stream, g);
-    else if (g.rank <= 32) hipLaunchKernelGGL((k_adapters_down<T, YT, 2>), grid, block, 0, stream, g);
-    else hipLaunchKernelGGL((k_adapters_down<T, YT, 4>), grid, block, 0, stream, g);
+    const dim3 grid((uint32_t)(p.tiles * p.splits), p.rank_blocks, p.turns), block(64 * kDownWaves);
+    if (g.rank <= 16) hipLaunchKernelGGL((k_adapters_down<T, 1>), grid, block, 0, stream, g);
+    else if (g.rank <= 32) hipLaunchKernelGGL((k_adapters_down<T, 2>), grid, block, 0, stream, g);
+    else hipLaunchKernelGGL((k_adapters_down<T, 4>), grid, block, 0, stream, g);
 }
 
-template <int T, int YT>
+template <int T>
 void launch_down_many(const AdapterArgs &g, const AdapterPlan &p, hipStream_t stream)
 {
     const dim3 grid((uint32_t)(p.tiles * p.splits), p.rank_blocks), block(256);
     if (g.rank <= 16) hipLaunchKernelGGL((k_adapters_down_many<T, 1>), grid, block, 0, stream, g);
     else if (g.rank <= 32) hipLaunchKernelGGL((k_adapters_down_many<T, 2>), grid, block, 0, stream, g);
     else hipLaunchKernelGGL((k_adapters_down_many<T, 4>), grid, block, 0, stream, g);
-    hipLaunchKernelGGL((k_adapters_terms<T, YT>), dim3((uint32_t)ceil_div(g.m * p.rank_blocks, 32)), block, 0, stream, g);
 }
 
 template <int T, int YT>
@@ -179,8 +183,11 @@ wc_status launch_adapters(const AdapterArgs &g, const AdapterPlan &p, hipStream_
     if (p.few) {
         launch_few<T, YT>(g, p, stream);
     } else {
-        if (p.tile == 128) launch_down_many<T, YT>(g, p, stream);
-        else launch_down<T, YT>(g, p, stream);
+        if (p.tile == 128) launch_down_many<T>(g, p, stream);
+        else launch_down<T>(g, p, stream);
+        if (p.terms)
+            hipLaunchKernelGGL((k_adapters_terms<T, YT>), dim3((uint32_t)ceil_div(g.m * p.rank_blocks, 32)), dim3(256),
+                               0, stream, g);
         launch_up<T, YT>(g, p, stream);
     }
     return launched();
@@ -396,9 +403,9 @@ wc_status wc_add_adapters(const wc_adapters *a, void *d_scratch, uint64_t scratc
     g.rank = a->rank;
     g.cols = a->cols;
     g.rows = a->rows;
-    g.u = static_cast<uint16_t *>(d_scratch);
+    g.part = static_cast<float *>(d_scratch);
+    g.u = reinterpret_cast<uint16_t *>(static_cast<char *>(d_scratch) + p.u);
     g.unscale = reinterpret_cast<float *>(static_cast<char *>(d_scratch) + p.unscale);
-    g.part = reinterpret_cast<float *>(static_cast<char *>(d_scratch) + p.part);
     g.rank_pad = p.rank_pad;
     g.splits = p.splits;
     g.split_cols = p.split_cols;

@@ -263,6 +263,11 @@ wc_status launch_moe(const MoeArgs &g, const MoePlan &p, hipStream_t stream)
         else if (g.experts <= 256) hipLaunchKernelGGL(k_moe_select<4>, tokens, dim3(64), 0, stream, g);
         else hipLaunchKernelGGL(k_moe_select<16>, tokens, dim3(64), 0, stream, g);
     }
+    if (g.m == 1) {
+        hipLaunchKernelGGL(k_moe_up_one<T>, dim3((uint32_t)(g.top_k * p.up_tiles)), dim3(256), 0, stream, g);
+        hipLaunchKernelGGL(k_moe_down_one<T>, dim3(g.cols / 8), dim3(1024), 0, stream, g);
+        return launched();
+    }
     hipLaunchKernelGGL((k_moe_up<T, TT>), dim3(p.slots * p.up_tiles), dim3(256), 0, stream, g);
     const dim3 down(p.slots * p.down_tiles);
     if (p.split) hipLaunchKernelGGL((k_moe_down<T, TT, true>), down, dim3(256), 0, stream, g);

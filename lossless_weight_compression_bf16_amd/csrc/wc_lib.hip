@@ -29,7 +29,7 @@ using namespace wc;
 
 namespace {
 
-constexpr int kVersion = 10200;  // 1.2.0: format variants, CRC-32, fused decode + GEMM
+constexpr int kVersion = 10300;  // 1.3.0: log probabilities, adapters, mixture of experts (csrc/ops)
 
 bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 

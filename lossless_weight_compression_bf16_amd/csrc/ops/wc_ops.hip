@@ -67,10 +67,10 @@ void launch_grad(const LogprobGradArgs &g, dim3 grid, bool large, hipStream_t st
     else hipLaunchKernelGGL((k_logprobs_grad<T, false>), grid, dim3(kGradThreads), 0, stream, g);
 }
 
-// Launch shapes of the adapters: tiles of 16 tokens where the tokens are
-// few, each turn of a tile (an adapter) its own block, so that as many blocks
-// as possible share the reading; tiles of 128 tokens where prompts repeat
-// their adapter over many tokens, so that it is read once per tile.
+// Launch shapes of the adapters: tiles of 16 tokens, each turn of a tile (an
+// adapter) its own block, so that as many blocks as possible share the
+// reading; or, with `many`, tiles of 128 tokens, where prompts repeat their
+// adapter over many tokens, so that it is read once per tile.
 struct AdapterPlan {
     bool few;                                                    // k_adapters_few
     bool terms;                                                  // k_adapters_terms
@@ -79,10 +79,9 @@ struct AdapterPlan {
     uint64_t tiles, up_tiles, u, unscale, scratch;               // u, unscale: their places in the scratch
 };
 
-AdapterPlan adapter_plan(uint64_t m, uint32_t rank, uint32_t cols, uint32_t rows)
+AdapterPlan adapter_plan(uint64_t m, uint32_t rank, uint32_t cols, uint32_t rows, bool many)
 {
     AdapterPlan p{};
-    const bool many = m > 512;
     p.rank_pad = (rank + 31) / 32 * 32;
     // one launch where all blocks' reading of A from the caches costs less
     // than the second launch: at most 16 MiB, a block per 1,024 to 4,096 rows
@@ -126,6 +125,14 @@ AdapterPlan adapter_plan(uint64_t m, uint32_t rank, uint32_t cols, uint32_t rows
     p.scratch = p.unscale + (p.terms ? 4 * m * p.rank_blocks : 0);
     return p;
 }
+
+// Tiles of 128 tokens: where the tokens are many and an adapter has 64 of them
+// or more (their number is the host's only word on how long its runs are: a
+// tile of 128 takes its adapters one after the other).  us a call, tiles of 16
+// and of 128, rank 64, 4096 x 4096: 256 tokens of 2 adapters 35.5 and 27.8,
+// 2048 of 8 54 and 48, of 32 74 and 82, 8192 of 64 157 and 117; rank 16, 1024
+// tokens of 64 28 and 69, 8192 of 128 on 14336 rows 201 and 210.
+bool many_tokens(uint64_t m, uint32_t n) { return m >= 256 && m >= 64ull * n; }
 
 bool valid_adapters(uint64_t m, uint32_t rank, uint32_t cols, uint32_t rows)
 {
@@ -375,7 +382,10 @@ wc_status wc_token_logprobs_backward(const wc_logprobs_grad *a, uint32_t *d_err,
 uint64_t wc_add_adapters_scratch(uint64_t m, uint32_t rank, uint32_t cols, uint32_t rows)
 {
     if (m == 0 || !valid_adapters(m, rank, cols, rows)) return 0;
-    return adapter_plan(m, rank, cols, rows).scratch;
+    // enough for either plan: the adapters' number is not known here
+    const uint64_t small = adapter_plan(m, rank, cols, rows, false).scratch;
+    const uint64_t large = many_tokens(m, 1) ? adapter_plan(m, rank, cols, rows, true).scratch : 0;
+    return small > large ? small : large;
 }
 
 wc_status wc_add_adapters(const wc_adapters *a, void *d_scratch, uint64_t scratch_bytes, uint32_t *d_err,
@@ -390,7 +400,7 @@ wc_status wc_add_adapters(const wc_adapters *a, void *d_scratch, uint64_t scratc
     if (!a->x || !aligned(a->x, 16) || (a->m > 1 && (a->x_stride < a->cols || a->x_stride % 8))) return WC_ERR_ARG;
     if (!a->y || !aligned(a->y, type_bytes(a->y_type)) || (a->m > 1 && a->y_stride < a->rows)) return WC_ERR_ARG;
     if (!a->ids || !aligned(a->ids, 8) || !aligned(a->scales, 4)) return WC_ERR_ARG;
-    const AdapterPlan p = adapter_plan(a->m, a->rank, a->cols, a->rows);
+    const AdapterPlan p = adapter_plan(a->m, a->rank, a->cols, a->rows, many_tokens(a->m, a->n));
     if (p.tiles * p.splits > kMaxGrid || p.up_tiles * p.row_blocks > kMaxGrid) return WC_ERR_ARG;
     if (scratch_bytes < p.scratch) return WC_ERR_CAPACITY;
     if (p.scratch && (!d_scratch || !aligned(d_scratch, 16))) return WC_ERR_ARG;

@@ -84,7 +84,8 @@ def _check(args, dev, what):
 SIZES = [(1, 1, 1, 8, 1), (1, 8, 16, 4096, 4096), (3, 2, 5, 40, 17), (16, 16, 16, 256, 64), (17, 3, 20, 264, 100),
          (61, 32, 16, 512, 1000), (64, 1, 33, 136, 72), (100, 7, 64, 520, 257), (5, 3, 256, 104, 50),
          (70, 5, 130, 64, 33), (513, 4, 16, 256, 65), (600, 700, 8, 64, 40), (700, 5, 20, 1032, 300),
-         (1000, 3, 100, 72, 130), (520, 2, 200, 264, 96), (530, 3, 64, 96, 600)]
+         (1000, 3, 100, 72, 130), (520, 2, 200, 264, 96), (530, 3, 64, 96, 600), (256, 4, 48, 264, 130), (640, 11, 70, 136, 90),
+         (700, 90, 40, 1064, 520)]
 
 
 @pytest.mark.parametrize("dtype,ydtype", [(BF, F32), (BF, BF), (HF, F32), (HF, HF)])

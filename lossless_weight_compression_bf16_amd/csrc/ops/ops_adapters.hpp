@@ -209,11 +209,12 @@ __global__ __launch_bounds__(64 * kDownWaves, 2) void k_adapters_down(AdapterArg
 }
 
 // A x of many tokens, without the scales, in parts along the columns.  Grid:
-// x = tiles of 128 tokens x splits, y = blocks of 64 ranks (RT tiles of 16).
+// x = tiles of 128 tokens x splits, y = blocks of 64 ranks (RT tiles of 16),
+// z = turns.
 // The four waves of a block take 32 tokens each; their rows and those of A
 // are read in whole lines and come to operand order in LDS (Strip), A once
 // for the block.  With 32 tokens a block and all columns, A passed through
-// the L1 cache twice as often as x, and that took 75 us where this takes 39
+// the L1 cache twice as often as x, and that took 75 us where this takes 37
 // (8192 tokens, 4096 columns, rank 64).  The next columns are on their way
 // while these are multiplied.
 template <int T, int RT>
@@ -234,7 +235,7 @@ __global__ __launch_bounds__(256) void k_adapters_down_many(AdapterArgs g)
 #pragma unroll
         for (int u = 0; u < 8; u++) xr[t][u] = g.x + min(first + 16 * t + 2 * u + hi, g.m - 1) * g.x_stride;
     uint64_t mlow, mhigh;
-    uint32_t adapter;
+    uint32_t adapter, turn = 0;
     while (low.pending | high.pending) {
         if (low.next(adapter, mlow)) {
             high.take(adapter, mhigh);
@@ -242,6 +243,7 @@ __global__ __launch_bounds__(256) void k_adapters_down_many(AdapterArgs g)
             mlow = 0;
             high.next(adapter, mhigh);
         }
+        if (turn++ % gridDim.z != blockIdx.z) continue;
         const uint32_t mask = (uint32_t)((wave & 2 ? mhigh : mlow) >> (32 * (wave & 1)));  // the wave's tokens
         const uint16_t *a = g.a + (uint64_t)adapter * g.rank * g.cols;
         f32x4 acc[RT][2];
@@ -586,13 +588,14 @@ __global__ __launch_bounds__(256, KS == 1 ? 4 : 2) void k_adapters_up(AdapterArg
 }
 
 // y += B u for many tokens and ranks up to 64.  Grid: x = tiles of 128 tokens
-// x row blocks.  The four waves of a block take 32 tokens each and the same
+// x row blocks, z = turns.  The four waves of a block take 32 tokens each and the same
 // 64 rows of B, which reach them through LDS in operand order: B would
 // otherwise pass through the L1 cache once per 32 tokens, twice as many bytes
 // as y, and how much can be on its way into that cache is what bounds a
 // kernel that only streams.  y is read and written in whole lines, 64 elements
 // of a token at a time, and past the caches where it is larger than they are
-// (kStream); the products come to that order through LDS as well.
+// (kStream); the products come to that order through LDS as well.  8192 tokens
+// of 16 adapters of rank 64, 14336 rows, BF16: 112 us, 4.2 TB/s of y.
 template <int T, int YT, int KS, bool kStream>
 __global__ __launch_bounds__(256, KS == 2 && (T == WC_T_FP16 || YT == WC_T_FP32) ? 2 : 3) void k_adapters_up_many(AdapterArgs g)
 {
@@ -613,7 +616,7 @@ __global__ __launch_bounds__(256, KS == 2 && (T == WC_T_FP16 || YT == WC_T_FP32)
     const uint32_t yrow = lane / kLanes, ycol = lane % kLanes * kPer;  // the lane's place in a load of y
     TileIds low(g, tile, 64), high(g, tile + 64, 64);
     uint64_t mlow, mhigh;
-    uint32_t adapter;
+    uint32_t adapter, turn = 0;
     while (low.pending | high.pending) {
         if (low.next(adapter, mlow)) {
             high.take(adapter, mhigh);
@@ -621,6 +624,7 @@ __global__ __launch_bounds__(256, KS == 2 && (T == WC_T_FP16 || YT == WC_T_FP32)
             mlow = 0;
             high.next(adapter, mhigh);
         }
+        if (turn++ % gridDim.z != blockIdx.z) continue;
         const uint32_t mask = (uint32_t)((wave & 2 ? mhigh : mlow) >> (32 * (wave & 1)));  // the wave's tokens
         X8 u[TT][KS][kTerms];
         float unscale[TT];
@@ -638,8 +642,8 @@ __global__ __launch_bounds__(256, KS == 2 && (T == WC_T_FP16 || YT == WC_T_FP32)
         YE *const y0 = static_cast<YE *>(g.y) + (tile + 32 * wave) * g.y_stride + ycol;
         u32x4 nextb[KS];
         rows.load(g, n0, (int)wave, nextb);
-        uint32_t turn = 0;
-        for (uint32_t nb = n0; nb < n1; nb += 64, turn ^= 1) {
+        uint32_t buf = 0;
+        for (uint32_t nb = n0; nb < n1; nb += 64, buf ^= 1) {
             const bool whole = nb + 64 <= n1;
             u32x4 y[kVecs];
             if (whole) {
@@ -650,7 +654,7 @@ __global__ __launch_bounds__(256, KS == 2 && (T == WC_T_FP16 || YT == WC_T_FP32)
                 }
             }
 #pragma unroll
-            for (int s = 0; s < KS; s++) sb[turn][wave][s][lane] = rows.kept(nextb[s], s);
+            for (int s = 0; s < KS; s++) sb[buf][wave][s][lane] = rows.kept(nextb[s], s);
             __syncthreads();  // the other buffer's last readers passed the barrier before this one
             if (nb + 64 < n1) rows.load(g, nb + 64, (int)wave, nextb);
             if (!mask) continue;
@@ -661,7 +665,7 @@ __global__ __launch_bounds__(256, KS == 2 && (T == WC_T_FP16 || YT == WC_T_FP32)
                     f32x4 sum{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                     for (int s = 0; s < KS; s++) {
-                        const X8 bv = __builtin_bit_cast(X8, sb[turn][p][s][lane]);
+                        const X8 bv = __builtin_bit_cast(X8, sb[buf][p][s][lane]);
 #pragma unroll
                         for (int c = kTerms - 1; c >= 0; c--) sum = Ty::mfma(bv, u[t][s][c], sum);
                     }

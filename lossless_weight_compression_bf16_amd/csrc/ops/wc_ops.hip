@@ -79,7 +79,7 @@ struct AdapterPlan {
     uint64_t tiles, up_tiles, u, unscale, scratch;               // u, unscale: their places in the scratch
 };
 
-AdapterPlan adapter_plan(uint64_t m, uint32_t rank, uint32_t cols, uint32_t rows, bool many)
+AdapterPlan adapter_plan(uint64_t m, uint32_t n, uint32_t rank, uint32_t cols, uint32_t rows, bool many)
 {
     AdapterPlan p{};
     p.rank_pad = (rank + 31) / 32 * 32;
@@ -91,7 +91,11 @@ AdapterPlan adapter_plan(uint64_t m, uint32_t rank, uint32_t cols, uint32_t rows
         p.row_blocks = (uint32_t)ceil_div(rows, r);
         p.few = reading * p.row_blocks <= (16ull << 20);
     }
-    p.turns = many ? 1 : (uint32_t)(m < 16 ? m : 16);
+    // a tile of 128 tokens has few adapters, and the blocks of turns that it
+    // does not have cost little: us for one turn and three, rank 64, 8192
+    // tokens, 14336 rows: of 1 adapter 135 and 138, of 16 167 and 154, of 128
+    // 293 and 240
+    p.turns = many ? (n < 1 ? 1 : n < 3 ? n : 3) : (uint32_t)(m < 16 ? m : 16);
     if (p.few) {
         p.tile = p.up_tile = 16;
         p.tiles = p.up_tiles = ceil_div(m, 16);
@@ -104,7 +108,9 @@ AdapterPlan adapter_plan(uint64_t m, uint32_t rank, uint32_t cols, uint32_t rows
     // more where the tiles alone fill the compute units
     const uint32_t step = many ? kStripCols : 32 * 4 * kDownWaves;
     const uint64_t most = ceil_div(cols, step);
-    uint64_t splits = ceil_div(kCus, p.tiles * p.rank_blocks * p.turns);
+    // with tiles of 128, a second turn for every adapter's first tile
+    const uint64_t blocks = many ? p.tiles + (n < p.tiles ? n : p.tiles) : p.tiles * p.turns;
+    uint64_t splits = ceil_div(kCus, blocks * p.rank_blocks);
     if (splits > most) splits = most;
     if (splits > 8) splits = 8;
     p.split_cols = (uint32_t)(ceil_div(most, splits) * step);
@@ -114,7 +120,7 @@ AdapterPlan adapter_plan(uint64_t m, uint32_t rank, uint32_t cols, uint32_t rows
     p.up_tile = wide ? 128 : 16;
     p.up_tiles = ceil_div(m, p.up_tile);
     const uint32_t least = wide ? 64 : 256;
-    uint64_t rb = ceil_div((wide ? 4 : 8) * kCus, p.up_tiles * p.turns);
+    uint64_t rb = ceil_div((wide ? 4 : 8) * kCus, p.up_tiles * (many ? 1 : p.turns));
     const uint64_t rmost = ceil_div(rows, least);
     if (rb > rmost) rb = rmost;
     p.row_block = (uint32_t)(ceil_div(ceil_div(rows, rb), least) * least);
@@ -128,10 +134,10 @@ AdapterPlan adapter_plan(uint64_t m, uint32_t rank, uint32_t cols, uint32_t rows
 
 // Tiles of 128 tokens: where the tokens are many and an adapter has 64 of them
 // or more (their number is the host's only word on how long its runs are: a
-// tile of 128 takes its adapters one after the other).  us a call, tiles of 16
-// and of 128, rank 64, 4096 x 4096: 256 tokens of 2 adapters 35.5 and 27.8,
-// 2048 of 8 54 and 48, of 32 74 and 82, 8192 of 64 157 and 117; rank 16, 1024
-// tokens of 64 28 and 69, 8192 of 128 on 14336 rows 201 and 210.
+// tile of 128 takes its adapters three at a time).  us a call, tiles of 16 and
+// of 128, 4096 x 4096: rank 64, 256 tokens of 2 adapters 35 and 22, 2048 of 8
+// 54 and 41, of 32 73 and 64, of 64 83 and 90; rank 16, 1024 tokens of 16 28
+// and 29, of 32 28 and 34, of 64 29 and 46.
 bool many_tokens(uint64_t m, uint32_t n) { return m >= 256 && m >= 64ull * n; }
 
 bool valid_adapters(uint64_t m, uint32_t rank, uint32_t cols, uint32_t rows)
@@ -152,7 +158,7 @@ void launch_down(const AdapterArgs &g, const AdapterPlan &p, hipStream_t stream)
 template <int T>
 void launch_down_many(const AdapterArgs &g, const AdapterPlan &p, hipStream_t stream)
 {
-    const dim3 grid((uint32_t)(p.tiles * p.splits), p.rank_blocks), block(256);
+    const dim3 grid((uint32_t)(p.tiles * p.splits), p.rank_blocks, p.turns), block(256);
     if (g.rank <= 16) hipLaunchKernelGGL((k_adapters_down_many<T, 1>), grid, block, 0, stream, g);
     else if (g.rank <= 32) hipLaunchKernelGGL((k_adapters_down_many<T, 2>), grid, block, 0, stream, g);
     else hipLaunchKernelGGL((k_adapters_down_many<T, 4>), grid, block, 0, stream, g);
@@ -383,8 +389,8 @@ uint64_t wc_add_adapters_scratch(uint64_t m, uint32_t rank, uint32_t cols, uint3
 {
     if (m == 0 || !valid_adapters(m, rank, cols, rows)) return 0;
     // enough for either plan: the adapters' number is not known here
-    const uint64_t small = adapter_plan(m, rank, cols, rows, false).scratch;
-    const uint64_t large = many_tokens(m, 1) ? adapter_plan(m, rank, cols, rows, true).scratch : 0;
+    const uint64_t small = adapter_plan(m, 0, rank, cols, rows, false).scratch;
+    const uint64_t large = many_tokens(m, 1) ? adapter_plan(m, 0, rank, cols, rows, true).scratch : 0;
     return small > large ? small : large;
 }
 
@@ -400,7 +406,7 @@ wc_status wc_add_adapters(const wc_adapters *a, void *d_scratch, uint64_t scratc
     if (!a->x || !aligned(a->x, 16) || (a->m > 1 && (a->x_stride < a->cols || a->x_stride % 8))) return WC_ERR_ARG;
     if (!a->y || !aligned(a->y, type_bytes(a->y_type)) || (a->m > 1 && a->y_stride < a->rows)) return WC_ERR_ARG;
     if (!a->ids || !aligned(a->ids, 8) || !aligned(a->scales, 4)) return WC_ERR_ARG;
-    const AdapterPlan p = adapter_plan(a->m, a->rank, a->cols, a->rows, many_tokens(a->m, a->n));
+    const AdapterPlan p = adapter_plan(a->m, a->n, a->rank, a->cols, a->rows, many_tokens(a->m, a->n));
     if (p.tiles * p.splits > kMaxGrid || p.up_tiles * p.row_blocks > kMaxGrid) return WC_ERR_ARG;
     if (scratch_bytes < p.scratch) return WC_ERR_CAPACITY;
     if (p.scratch && (!d_scratch || !aligned(d_scratch, 16))) return WC_ERR_ARG;

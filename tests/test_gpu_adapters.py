@@ -222,3 +222,10 @@ def test_refusals(dev):
     with pytest.raises(B.WcError, match="index out of range"):
         A.add_adapters(x, z, a, b, ids, s)
     assert torch.equal(z[2], y[2])
+
+
+@pytest.mark.parametrize("m", [5, 300])
+def test_no_adapters_at_all(dev, m):
+    x, y, a, b, _, _ = _inputs(m, 1, 16, 128, 96, BF, F32, 8)
+    got = A.add_adapters(x.to(dev), y.to(dev), a[:0].to(dev), b[:0].to(dev), torch.full((m,), -1, device=dev))
+    assert torch.equal(got.cpu(), y)

@@ -699,6 +699,8 @@ __global__ __launch_bounds__(256, KS == 2 && (T == WC_T_FP16 || YT == WC_T_FP32)
 // columns, while its first rows of B and y are on their way.  The row blocks
 // of a tile's turn are on one XCD (blocks are dealt to the XCDs in the order
 // of their number), where A comes from the L2 cache after the first of them.
+// One token, rank 16, 4096 x 4096: 8.7 us, of which most is waiting for the
+// ids, then A and x, then the other waves; two launches took 18.3 us a call.
 // Grid: turns x tiles of 16 tokens, rounded up to 8, x row blocks.
 template <int T, int YT, int RT>
 __global__ __launch_bounds__(1024) void k_adapters_few(AdapterArgs g)

@@ -434,7 +434,10 @@ __device__ __forceinline__ uint32_t moe_block(const MoeArgs &g, uint32_t slot, M
 }
 
 // h of 16 inner rows of one expert.  Grid: slots x inner / 16.  Columns over
-// the four waves.
+// the four waves.  Reading W1 and W3 is the bound: 64 tokens, 256 experts of
+// 2048 x 7168, 1.91 ms, 13 tokens, 8 of 14336 x 4096, 277 us, 6.8 TB/s both
+// times.  Operands straight from memory, 64 bytes of each of 16 rows at a time,
+// took 4.5 ms for the former's whole layer where this takes 3.0.
 template <int T, int TT>
 __global__ __launch_bounds__(256, 2) void k_moe_up(MoeArgs g)
 {
@@ -483,7 +486,8 @@ __global__ __launch_bounds__(256, 2) void k_moe_up(MoeArgs g)
 
 // p W2 h of one expert into part[token top_k + choice].  Grid: slots x
 // columns / 64 (kSplit: / 16).  A wave has 16 rows of W2 of its own, or with
-// kSplit, where blocks would be too few, a quarter of the inner rows.
+// kSplit, where blocks would be too few, a quarter of the inner rows.  Reading
+// W2 is the bound: the same two layers, 1.07 ms (6.1 TB/s) and 181 us (5.2).
 template <int T, int TT, bool kSplit>
 __global__ __launch_bounds__(256, 3) void k_moe_down(MoeArgs g)
 {

@@ -374,24 +374,31 @@ __device__ __forceinline__ void moe_up_rows(const MoeArgs &g, uint32_t expert, u
     }
 }
 
-// A wave's share of the inner rows c0 .. c1 for 16 rows of W2 of one expert
-// against its tokens' h.
+// A wave's share of the inner rows c0 .. c1 for twice 16 rows of W2 of one
+// expert, from n[0] and n[1], against its tokens' h.
 template <int T, int NT, int TT>
-__device__ __forceinline__ void moe_down_rows(const MoeArgs &g, uint32_t expert, uint32_t n0, const int32_t *place,
-                                              uint32_t count, uint32_t c0, uint32_t c1, Strip *strips, f32x4 (&sum)[TT])
+__device__ __forceinline__ void moe_down_rows(const MoeArgs &g, uint32_t expert, const uint32_t (&n)[2],
+                                              const int32_t *place, uint32_t count, uint32_t c0, uint32_t c1,
+                                              Strip *strips, f32x4 (&sum)[2][TT])
 {
-    const uint32_t i = threadIdx.x & 15, rows = min(g.cols - n0, 16u), stride = (uint32_t)g.down_row;
-    const uint16_t *const weights[1] = {g.w2 + (uint64_t)expert * g.down_expert + (uint64_t)n0 * g.down_row};
+    const uint32_t i = threadIdx.x & 15, rows = min(g.cols, 16u), stride = (uint32_t)g.down_row;
+    const uint16_t *const w = g.w2 + (uint64_t)expert * g.down_expert;
+    const uint16_t *const weights[2] = {w + n[0] * g.down_row, w + n[1] * g.down_row};
     const uint64_t plane = (uint64_t)g.m * g.top_k * g.inner;
-    f32x4 acc[1][2][NT];
+    f32x4 acc[2][2][NT];
 #pragma unroll
-    for (int t = 0; t < NT; t++) acc[0][0][t] = acc[0][1][t] = f32x4{0.f, 0.f, 0.f, 0.f};
-    strip_product<T, 1, 2, NT>(
+    for (int t = 0; t < NT; t++)
+#pragma unroll
+        for (int m = 0; m < 2; m++) acc[m][0][t] = acc[m][1][t] = f32x4{0.f, 0.f, 0.f, 0.f};
+    strip_product<T, 2, 2, NT>(
         weights, [&](uint32_t r) { return min(r, rows - 1) * stride; },
         [&](int o, int t) { return g.h + o * plane + (uint64_t)place[min(16 * t + i, count - 1)] * g.inner; },
         c0, c1, strips, acc);
 #pragma unroll
-    for (int t = 0; t < NT; t++) sum[t] = MoeTerms<T>::kScale[0] * acc[0][0][t] + MoeTerms<T>::kScale[1] * acc[0][1][t];
+    for (int t = 0; t < NT; t++)
+#pragma unroll
+        for (int m = 0; m < 2; m++)
+            sum[m][t] = MoeTerms<T>::kScale[0] * acc[m][0][t] + MoeTerms<T>::kScale[1] * acc[m][1][t];
 }
 
 // The columns of one of four waves: a quarter, in multiples of `unit`.
@@ -437,7 +444,7 @@ __device__ __forceinline__ uint32_t moe_block(const MoeArgs &g, uint32_t slot, M
 // the four waves.  Reading W1 and W3 is the bound: 64 tokens, 256 experts of
 // 2048 x 7168, 1.91 ms, 13 tokens, 8 of 14336 x 4096, 277 us, 6.8 TB/s both
 // times.  Operands straight from memory, 64 bytes of each of 16 rows at a time,
-// took 4.5 ms for the former's whole layer where this takes 3.0.
+// took 4.5 ms for the former's whole layer where this takes 2.9.
 template <int T, int TT>
 __global__ __launch_bounds__(256, 2) void k_moe_up(MoeArgs g)
 {
@@ -485,46 +492,58 @@ __global__ __launch_bounds__(256, 2) void k_moe_up(MoeArgs g)
 }
 
 // p W2 h of one expert into part[token top_k + choice].  Grid: slots x
-// columns / 64 (kSplit: / 16).  A wave has 16 rows of W2 of its own, or with
-// kSplit, where blocks would be too few, a quarter of the inner rows.  Reading
-// W2 is the bound: the same two layers, 1.07 ms (6.1 TB/s) and 181 us (5.2).
+// columns / 128 (kSplit: / 32).  A wave has twice 16 rows of W2 of its own, or
+// with kSplit, where blocks would be too few, a quarter of their inner rows.
+// Where the last 16 rows would run past the end they begin earlier: those that
+// two waves have come out the same.  Reading W2 is the bound: the
+// same two layers, 940 us (6.9 TB/s) and 149 us (6.3).  With 16 rows a wave
+// the two terms of h were as many lines on their way into the L1 cache as the
+// rows, and more for 13 tokens: 1075 and 181 us.
 template <int T, int TT, bool kSplit>
-__global__ __launch_bounds__(256, 3) void k_moe_down(MoeArgs g)
+__global__ __launch_bounds__(256, 2) void k_moe_down(MoeArgs g)
 {
     __shared__ MoeSet set;
     __shared__ int32_t place[64];
-    __shared__ Strip strips[4];
-    f32x4(*sums)[TT][64] = reinterpret_cast<f32x4(*)[TT][64]>(&strips[0]);  // [4], when the strips are done
-    static_assert(sizeof(strips) >= 4 * TT * 64 * 16, "the waves' sums fit into the strips");
+    __shared__ Strip strips[4][2];
+    f32x4(*sums)[2 * TT][64] = reinterpret_cast<f32x4(*)[2 * TT][64]>(&strips[0][0]);  // [4], when the strips are done
+    static_assert(sizeof(strips) >= 4 * 2 * TT * 64 * 16, "the waves' sums fit into the strips");
     const uint32_t wave = threadIdx.x >> 6, lane = threadIdx.x & 63, i = lane & 15, gr = lane >> 4;
     const uint32_t slot = blockIdx.x % g.slots;
-    const uint32_t n0 = kSplit ? 16 * (blockIdx.x / g.slots) : 64 * (blockIdx.x / g.slots) + 16 * wave;
+    const uint32_t n0 = kSplit ? 32 * (blockIdx.x / g.slots) : 128 * (blockIdx.x / g.slots) + 32 * wave;
+    const uint32_t last = g.cols > 16 ? g.cols - 16 : 0u, rows[2] = {min(n0, last), min(n0 + 16, last)};
     uint32_t expert, c0 = 0, c1 = g.inner;
     const uint32_t count = moe_block(g, slot, set, place, expert);
     if (count == 0) return;
     if (kSplit) wave_quarter(g.inner, kStripCols, wave, c0, c1);
-    f32x4 sum[TT];
+    f32x4 sum[2][TT];
     if (n0 < g.cols) {
-        if (TT == 1 || count <= 16) moe_down_rows<T, 1, TT>(g, expert, n0, place, count, c0, c1, &strips[wave], sum);
-        else if (TT == 2 || count <= 32) moe_down_rows<T, 2, TT>(g, expert, n0, place, count, c0, c1, &strips[wave], sum);
-        else moe_down_rows<T, 4, TT>(g, expert, n0, place, count, c0, c1, &strips[wave], sum);
+        Strip *const st = strips[wave];
+        if (TT == 1 || count <= 16) moe_down_rows<T, 1, TT>(g, expert, rows, place, count, c0, c1, st, sum);
+        else if (TT == 2 || count <= 32) moe_down_rows<T, 2, TT>(g, expert, rows, place, count, c0, c1, st, sum);
+        else moe_down_rows<T, 4, TT>(g, expert, rows, place, count, c0, c1, st, sum);
     }
     if constexpr (kSplit) {
         __syncthreads();
 #pragma unroll
-        for (int t = 0; t < TT; t++)
-            if (16 * t < (int)count) sums[wave][t][lane] = sum[t];
+        for (int m = 0; m < 2; m++)
+#pragma unroll
+            for (int t = 0; t < TT; t++)
+                if (16 * t < (int)count) sums[wave][m * TT + t][lane] = sum[m][t];
         __syncthreads();
     }
-    const uint32_t n = n0 + 4 * gr;
-    if (n >= g.cols) return;
+    if (n0 >= g.cols) return;
 #pragma unroll
-    for (int t = 0; t < TT; t++) {
-        if ((kSplit && t != (int)wave) || 16 * t + i >= count) continue;
-        f32x4 v = sum[t];
-        if constexpr (kSplit) v = (sums[0][t][lane] + sums[1][t][lane]) + (sums[2][t][lane] + sums[3][t][lane]);
-        const uint32_t at = (uint32_t)place[16 * t + i];
-        *reinterpret_cast<f32x4 *>(g.part + (uint64_t)at * g.cols + n) = g.weights[at] * v;
+    for (int m = 0; m < 2; m++) {
+        const uint32_t n = rows[m] + 4 * gr;
+#pragma unroll
+        for (int t = 0; t < TT; t++) {
+            const int q = m * TT + t;
+            if ((kSplit && q % 4 != (int)wave) || 16 * t + i >= count || n >= g.cols) continue;
+            f32x4 v = sum[m][t];
+            if constexpr (kSplit) v = (sums[0][q][lane] + sums[1][q][lane]) + (sums[2][q][lane] + sums[3][q][lane]);
+            const uint32_t at = (uint32_t)place[16 * t + i];
+            *reinterpret_cast<f32x4 *>(g.part + (uint64_t)at * g.cols + n) = g.weights[at] * v;
+        }
     }
 }
 

@@ -238,9 +238,9 @@ MoePlan moe_plan(uint32_t m, uint32_t experts, uint32_t top_k, uint32_t cols, ui
     p.route_splits = (uint32_t)ceil_div(steps, p.route_steps);
     p.slots = m * top_k < experts ? m * top_k : experts;
     p.up_tiles = (inner + 15) / 16;
-    // a wave for 16 rows of W2, or four where that gives too few blocks
-    p.split = (uint64_t)p.slots * ceil_div(cols, 64) < 8 * kCus;
-    p.down_tiles = (uint32_t)ceil_div(cols, p.split ? 16 : 64);
+    // a wave for twice 16 rows of W2, or four where that gives too few blocks
+    p.split = (uint64_t)p.slots * ceil_div(cols, 128) < 4 * kCus;
+    p.down_tiles = (uint32_t)ceil_div(cols, p.split ? 32 : 128);
     uint64_t at = 0;
     auto take = [&](uint64_t bytes) {
         const uint64_t here = at;

@@ -442,7 +442,7 @@ __device__ __forceinline__ uint32_t moe_block(const MoeArgs &g, uint32_t slot, M
 
 // h of 16 inner rows of one expert.  Grid: slots x inner / 16.  Columns over
 // the four waves.  Reading W1 and W3 is the bound: 64 tokens, 256 experts of
-// 2048 x 7168, 1.91 ms, 13 tokens, 8 of 14336 x 4096, 277 us, 6.8 TB/s both
+// 2048 x 7168, 1.91 ms, 13 tokens, 8 of 14336 x 4096, 270 us, 6.9 TB/s both
 // times.  Operands straight from memory, 64 bytes of each of 16 rows at a time,
 // took 4.5 ms for the former's whole layer where this takes 2.9.
 template <int T, int TT>

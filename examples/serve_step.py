@@ -59,7 +59,7 @@ def compress(w) -> Model:
 
 
 def step(model: Model, x, ids, tokens, top_k=2, top=5):
-    """x: m x cols BF16 (m at most 16 here), ids: an adapter per token or -1,
+    """x: m x cols BF16, m at most 64, ids: an adapter per token or -1,
     tokens: the next tokens to score.  Scores, logits and their gradient."""
     y, = gemm.decode_gemm(model.projection, [x])
     adapters.add_adapters(x, y, model.a, model.b, ids, model.scales)

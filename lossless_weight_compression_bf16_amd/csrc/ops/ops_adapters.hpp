@@ -120,19 +120,6 @@ struct Terms<WC_T_FP16, YT> {
     }
 };
 
-// What FP16 values are multiplied by before they are split: the power of two
-// that brings `most`, the largest of them, to 2^14..2^15; its inverse in
-// `unscale`.  1 for BF16, whose range is that of FP32.
-template <int T>
-__device__ __forceinline__ float term_scale(float most, float &unscale)
-{
-    unscale = 1.f;
-    if (T != WC_T_FP16 || !(most > 0.f && most < kInf)) return 1.f;
-    const int ex = max(-100, min(100, 15 - __builtin_amdgcn_frexp_expf(most)));
-    unscale = __builtin_ldexpf(1.f, -ex);
-    return __builtin_ldexpf(1.f, ex);
-}
-
 // Eight values of u of one token, from rank k, as terms.
 template <int T, int YT>
 __device__ __forceinline__ void put_terms(const AdapterArgs &g, uint64_t token, uint32_t k, const float *f)

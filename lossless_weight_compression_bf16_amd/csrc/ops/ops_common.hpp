@@ -186,6 +186,19 @@ __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_ex
 __device__ __forceinline__ float nan32() { return __builtin_bit_cast(float, 0x7FC00000u); }
 constexpr float kInf = __builtin_inff();
 
+// What FP16 values are multiplied by before they are split: the power of two
+// that brings `most`, the largest of them, to 2^14..2^15; its inverse in
+// `unscale`.  1 for BF16, whose range is that of FP32.
+template <int T>
+__device__ __forceinline__ float term_scale(float most, float &unscale)
+{
+    unscale = 1.f;
+    if (T != WC_T_FP16 || !(most > 0.f && most < kInf)) return 1.f;
+    const int ex = max(-100, min(100, 15 - __builtin_amdgcn_frexp_expf(most)));
+    unscale = __builtin_ldexpf(1.f, -ex);
+    return __builtin_ldexpf(1.f, ex);
+}
+
 // Whole numbers in the order of floats (-0 = 0), 1 for NaN, 0 for nothing.
 __device__ __forceinline__ uint32_t key_of(float f)
 {

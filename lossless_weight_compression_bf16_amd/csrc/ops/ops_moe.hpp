@@ -17,10 +17,11 @@
 // against 16 tokens per MFMA, and experts with more than 16 tokens meet them
 // all while their weights are there.  Products are exact and summed in fp32.
 //
-// h leaves k_moe_up as two 16-bit terms, BF16 h = a + b (16 bits), FP16
-// h / 256 = a + b / 4096 with a and b accumulated apart (22 bits, |h| up to
-// 2^24 and down to 2^-20), so that y is rounded once, at the end: one term
-// alone would add as much error as that rounding.
+// h is fp32.  The matrix cores take it as a sum of 16-bit terms that the
+// second product makes of it as it is read: of BF16 three, which are all of
+// its 24 bits; of FP16 two of 11 bits, after a scaling by a power of two that
+// brings the largest of a token's h in that expert to 2^14..2^15, so that
+// they hold 22 bits of it and of whatever is down to 2^-17 of it, at any size.
 //
 // MFMA 16x16x32 (lane l = 16 g + i): A operand row i, k = 8 g .. 8 g + 7;
 // B operand column i, the same k; D column i, rows 4 g .. 4 g + 3.  Here A is
@@ -45,36 +46,58 @@ struct MoeArgs {
     float *logits;        // route_splits x m x experts_pad
     int32_t *ids;         // m x top_k
     float *weights;       // m x top_k
-    uint16_t *h;          // 2 terms x (m top_k) x inner
+    float *h;             // (m top_k) x inner
+    uint32_t *most;       // m top_k: bits of the largest |h|
     float *part;          // (m top_k) x cols: each expert's part of y
     uint32_t experts_pad, route_splits, route_steps, slots;
 };
 
+// Eight values of h as terms.  BF16: truncated, so that what is left after
+// two of 8 bits is the third.  FP16: values scaled as above; rounded towards
+// zero, so that none becomes an infinity.  An infinity is its own first term.
 template <int T>
-struct MoeTerms;  // h as two 16-bit terms, and what their sums are multiplied by
+struct MoeTerms;
 template <>
 struct MoeTerms<WC_T_BF16> {
-    static constexpr float kScale[2] = {1.f, 1.f};
-    __device__ static void split(float h, uint16_t &a, uint16_t &b)
+    static constexpr int kCount = 3;
+    __device__ __forceinline__ static void split(const float *f, bf16x8 (&out)[kCount])
     {
-        a = Type<WC_T_BF16>::from_f32(h);
-        const float t = Type<WC_T_BF16>::to_f32(a);
-        b = Type<WC_T_BF16>::from_f32(fabsf(t) < kInf ? h - t : 0.f);
+        u32x4 v[kCount];
+#pragma unroll
+        for (int e = 0; e < 4; e++) {
+            float lo = f[2 * e], hi = f[2 * e + 1];
+#pragma unroll
+            for (int c = 0; c < kCount; c++) {
+                const uint32_t l = __builtin_bit_cast(uint32_t, lo), h = __builtin_bit_cast(uint32_t, hi);
+                v[c][e] = __builtin_amdgcn_perm(h, l, 0x07060302u);  // the upper halves of both
+                const float tl = __builtin_bit_cast(float, l & 0xFFFF0000u), th = __builtin_bit_cast(float, h & 0xFFFF0000u);
+                lo = c || fabsf(lo) < kInf ? lo - tl : 0.f;
+                hi = c || fabsf(hi) < kInf ? hi - th : 0.f;
+            }
+        }
+#pragma unroll
+        for (int c = 0; c < kCount; c++) out[c] = __builtin_bit_cast(bf16x8, v[c]);
     }
 };
 template <>
 struct MoeTerms<WC_T_FP16> {
-    static constexpr float kScale[2] = {256.f, 1.f / 16.f};
-    __device__ static void split(float h, uint16_t &a, uint16_t &b)
+    static constexpr int kCount = 2;
+    __device__ __forceinline__ static void split(const float *f, f16x8 (&out)[kCount])
     {
-        const float v = h * (1.f / 256.f);
-        a = Type<WC_T_FP16>::from_f32(v);
-        const float t = Type<WC_T_FP16>::to_f32(a);
-        b = Type<WC_T_FP16>::from_f32(fabsf(t) < kInf ? (v - t) * 4096.f : 0.f);
+        u32x4 a, b;
+#pragma unroll
+        for (int e = 0; e < 4; e++) {
+            const auto t = __builtin_amdgcn_cvt_pkrtz(f[2 * e], f[2 * e + 1]);
+            const float lo = (float)t[0], hi = (float)t[1];
+            a[e] = __builtin_bit_cast(uint32_t, t);
+            b[e] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_pkrtz(fabsf(lo) < kInf ? f[2 * e] - lo : 0.f,
+                                                                           fabsf(hi) < kInf ? f[2 * e + 1] - hi : 0.f));
+        }
+        out[0] = __builtin_bit_cast(f16x8, a);
+        out[1] = __builtin_bit_cast(f16x8, b);
     }
 };
 
-__device__ __forceinline__ u32x4 zero4() { return u32x4{0u, 0u, 0u, 0u}; }
 // logits[split][t][e]: 16 experts per block, the columns of a split over its
 // four waves.
 template <int T, int TT>
@@ -163,6 +186,7 @@ __device__ __forceinline__ void moe_choose(const MoeArgs &g, uint32_t t, F logit
     }
     if (lane < g.top_k) {
         g.ids[t * g.top_k + lane] = (int32_t)id;
+        g.most[t * g.top_k + lane] = 0;
         g.weights[t * g.top_k + lane] = mine / (g.renormalize ? chosen : sum);
     }
 }
@@ -272,29 +296,28 @@ struct MoeSet {
     }
 };
 
-// acc[m][o][t] += W_m X_t over columns c0 .. c1 (multiples of 8) for M
-// matrices of 16 rows and NT tiles of 16 tokens whose numbers are sums of O
-// terms.  weights[m]: the first row; row(r): elements from there to row r;
-// tokens(o, t): the lane's column of term o.  Loads past the end repeat the
-// last 8 columns, and the operands are zero there.  The next columns are on
-// their way while these are multiplied.
-template <int T, int M, int O, int NT, class Row, class Tokens>
+// acc[m][t] += W_m X_t over columns c0 .. c1 (multiples of 8) for M matrices
+// of 16 rows and NT tiles of 16 tokens, whose numbers are 16-bit or, with
+// kTerms, fp32 and taken as terms of scale[t] times them.  weights[m]: the
+// first row; row(r): elements from there to row r; tokens(t): the lane's
+// column.  Loads past the end repeat the last 8 columns, and the operands are
+// zero there.  The next columns are on their way while these are multiplied.
+template <int T, int M, bool kTerms, int NT, class Row, class Tokens>
 __device__ __forceinline__ void strip_product(const uint16_t *const (&weights)[M], Row row, Tokens tokens, uint32_t c0,
-                                              uint32_t c1, Strip *strips, f32x4 (&acc)[M][O][NT])
+                                              uint32_t c1, Strip *strips, const float (&scale)[NT], f32x4 (&acc)[M][NT])
 {
     using Ty = Type<T>;
     using X8 = typename Ty::x8;
-    constexpr int kSteps = kStripCols / 32, S = 16 / (O * NT) < kSteps ? 16 / (O * NT) : kSteps;
+    constexpr int kSteps = kStripCols / 32, V = kTerms ? 2 : 1;  // vectors of 16 bytes for 8 numbers
+    constexpr int S = 16 / (V * NT) < kSteps ? 16 / (V * NT) : kSteps, C = kTerms ? MoeTerms<T>::kCount : 1;
     const uint32_t lane = threadIdx.x & 63, i = lane & 15, gr = lane >> 4, hi = lane >> 5, lo = lane & 31;
     uint32_t off[8];
 #pragma unroll
     for (int u = 0; u < 8; u++) off[u] = row(2 * u + hi);
-    const uint16_t *tk[O][NT];
+    const char *tk[NT];
 #pragma unroll
-    for (int o = 0; o < O; o++)
-#pragma unroll
-        for (int t = 0; t < NT; t++) tk[o][t] = tokens(o, t);
-    u32x4 v[M][8], x[S][O][NT];
+    for (int t = 0; t < NT; t++) tk[t] = reinterpret_cast<const char *>(tokens(t));
+    u32x4 v[M][8], x[S][NT][V];
     auto fetch = [&](uint32_t c) {
         const uint32_t k = min(c + 8 * lo, c1 - 8);
 #pragma unroll
@@ -307,9 +330,9 @@ __device__ __forceinline__ void strip_product(const uint16_t *const (&weights)[M
         for (int s = 0; s < S; s++) {
             const uint32_t k = min(c + 32 * (s0 + s) + 8 * gr, c1 - 8);
 #pragma unroll
-            for (int o = 0; o < O; o++)
+            for (int t = 0; t < NT; t++)
 #pragma unroll
-                for (int t = 0; t < NT; t++) x[s][o][t] = load16<16>(tk[o][t] + k);
+                for (int e = 0; e < V; e++) x[s][t][e] = load16<16>(tk[t] + (16 * V * (k / 8) + 16 * e));
         }
     };
     if (c0 < c1) {
@@ -336,13 +359,24 @@ __device__ __forceinline__ void strip_product(const uint16_t *const (&weights)[M
                 for (int m = 0; m < M; m++)
                     a[m] = __builtin_bit_cast(X8, strips[m].q[i * kStripPitch + 4 * (s0 + s) + gr]);
 #pragma unroll
-                for (int o = 0; o < O; o++)
+                for (int t = 0; t < NT; t++) {
+                    X8 b[C];
+                    if constexpr (kTerms) {
+                        float f[8];
 #pragma unroll
-                    for (int t = 0; t < NT; t++) {
-                        const X8 b = __builtin_bit_cast(X8, only(in, x[s][o][t]));
-#pragma unroll
-                        for (int m = 0; m < M; m++) acc[m][o][t] = Ty::mfma(a[m], b, acc[m][o][t]);
+                        for (int e = 0; e < 8; e++) {
+                            const uint32_t w = x[s][t][e / 4][e % 4];
+                            f[e] = in ? __builtin_bit_cast(float, w) * scale[t] : 0.f;
+                        }
+                        MoeTerms<T>::split(f, b);
+                    } else {
+                        b[0] = __builtin_bit_cast(X8, only(in, x[s][t][0]));
                     }
+#pragma unroll
+                    for (int o = C - 1; o >= 0; o--)
+#pragma unroll
+                        for (int m = 0; m < M; m++) acc[m][t] = Ty::mfma(a[m], b[o], acc[m][t]);
+                }
             }
         }
         if (c + kStripCols < c1) fetch_x(c + kStripCols, 0);
@@ -360,17 +394,18 @@ __device__ __forceinline__ void moe_up_rows(const MoeArgs &g, uint32_t expert, u
     const uint64_t at = (uint64_t)expert * g.up_expert + (uint64_t)n0 * g.up_row;
     const uint16_t *const weights[2] = {g.w1 + at, g.w3 + at};
     const uint32_t rows = min(g.inner - n0, 16u), stride = (uint32_t)g.up_row;
-    f32x4 acc[2][1][NT];
+    f32x4 acc[2][NT];
+    const float scale[NT] = {};  // of no use here
 #pragma unroll
-    for (int t = 0; t < NT; t++) acc[0][0][t] = acc[1][0][t] = f32x4{0.f, 0.f, 0.f, 0.f};
-    strip_product<T, 2, 1, NT>(
+    for (int t = 0; t < NT; t++) acc[0][t] = acc[1][t] = f32x4{0.f, 0.f, 0.f, 0.f};
+    strip_product<T, 2, false, NT>(
         weights, [&](uint32_t r) { return min(r, rows - 1) * stride; },
-        [&](int, int t) { return g.x + (uint64_t)((uint32_t)place[min(16 * t + i, count - 1)] / g.top_k) * g.x_stride; },
-        c0, c1, strips, acc);
+        [&](int t) { return g.x + (uint64_t)((uint32_t)place[min(16 * t + i, count - 1)] / g.top_k) * g.x_stride; },
+        c0, c1, strips, scale, acc);
 #pragma unroll
     for (int t = 0; t < NT; t++) {
-        gate[t] = acc[0][0][t];
-        up[t] = acc[1][0][t];
+        gate[t] = acc[0][t];
+        up[t] = acc[1][t];
     }
 }
 
@@ -384,21 +419,22 @@ __device__ __forceinline__ void moe_down_rows(const MoeArgs &g, uint32_t expert,
     const uint32_t i = threadIdx.x & 15, rows = min(g.cols, 16u), stride = (uint32_t)g.down_row;
     const uint16_t *const w = g.w2 + (uint64_t)expert * g.down_expert;
     const uint16_t *const weights[2] = {w + n[0] * g.down_row, w + n[1] * g.down_row};
-    const uint64_t plane = (uint64_t)g.m * g.top_k * g.inner;
-    f32x4 acc[2][2][NT];
+    f32x4 acc[2][NT];
+    float scale[NT], unscale[NT];
+    uint32_t at[NT];
 #pragma unroll
-    for (int t = 0; t < NT; t++)
-#pragma unroll
-        for (int m = 0; m < 2; m++) acc[m][0][t] = acc[m][1][t] = f32x4{0.f, 0.f, 0.f, 0.f};
-    strip_product<T, 2, 2, NT>(
+    for (int t = 0; t < NT; t++) {
+        acc[0][t] = acc[1][t] = f32x4{0.f, 0.f, 0.f, 0.f};
+        at[t] = (uint32_t)place[min(16 * t + i, count - 1)];
+        scale[t] = term_scale<T>(T == WC_T_FP16 ? __builtin_bit_cast(float, g.most[at[t]]) : 0.f, unscale[t]);
+    }
+    strip_product<T, 2, true, NT>(
         weights, [&](uint32_t r) { return min(r, rows - 1) * stride; },
-        [&](int o, int t) { return g.h + o * plane + (uint64_t)place[min(16 * t + i, count - 1)] * g.inner; },
-        c0, c1, strips, acc);
+        [&](int t) { return g.h + (uint64_t)at[t] * g.inner; }, c0, c1, strips, scale, acc);
 #pragma unroll
     for (int t = 0; t < NT; t++)
 #pragma unroll
-        for (int m = 0; m < 2; m++)
-            sum[m][t] = MoeTerms<T>::kScale[0] * acc[m][0][t] + MoeTerms<T>::kScale[1] * acc[m][1][t];
+        for (int m = 0; m < 2; m++) sum[m][t] = unscale[t] * acc[m][t];
 }
 
 // The columns of one of four waves: a quarter, in multiples of `unit`.
@@ -473,21 +509,32 @@ __global__ __launch_bounds__(256, 2) void k_moe_up(MoeArgs g)
     }
     __syncthreads();
     const uint32_t n = n0 + 4 * gr, c = 16 * wave + i;
-    if (wave < TT && c < count && n < g.inner) {
+    if (wave >= TT) return;
+    float most = 0.f;
+    if (c < count && n < g.inner) {
         const uint32_t q = TT + wave;
         const f32x4 gv = (part[0][wave][lane] + part[1][wave][lane]) + (part[2][wave][lane] + part[3][wave][lane]);
         const f32x4 uv = (part[0][q][lane] + part[1][q][lane]) + (part[2][q][lane] + part[3][q][lane]);
-        uint16_t a[4], b[4];
+        f32x4 h;
 #pragma unroll
         for (int e = 0; e < 4; e++) {
-            const float v = gv[e];
-            MoeTerms<T>::split(v / (1.f + exp2_fast(-v * kLog2e)) * uv[e], a[e], b[e]);
+            const float v = gv[e], w = v / (1.f + exp2_fast(-v * kLog2e)) * uv[e];
+            h[e] = w;
+            most = fmaxf(most, fabsf(w));
         }
-        uint16_t *h = g.h + (uint64_t)place[c] * g.inner + n;
-        const u32x2 va{(uint32_t)a[0] | ((uint32_t)a[1] << 16), (uint32_t)a[2] | ((uint32_t)a[3] << 16)};
-        const u32x2 vb{(uint32_t)b[0] | ((uint32_t)b[1] << 16), (uint32_t)b[2] | ((uint32_t)b[3] << 16)};
-        *reinterpret_cast<u32x2 *>(h) = va;
-        *reinterpret_cast<u32x2 *>(h + (uint64_t)g.m * g.top_k * g.inner) = vb;
+        *reinterpret_cast<f32x4 *>(g.h + (uint64_t)place[c] * g.inner + n) = h;
+    }
+    if constexpr (T == WC_T_FP16) {
+        // A maximum does not depend on the order.  It is looked at first: few
+        // blocks raise it, and all of them raising the same few words would
+        // take longer than their weights (13 tokens on 8 wide experts: 580 us).
+        most = fmaxf(most, __shfl_xor(most, 16, 64));
+        most = fmaxf(most, __shfl_xor(most, 32, 64));
+        if (gr == 0 && c < count) {
+            uint32_t *const p = g.most + place[c];
+            const uint32_t bits = __builtin_bit_cast(uint32_t, most);
+            if (__hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) < bits) atomicMax(p, bits);
+        }
     }
 }
 
@@ -497,8 +544,10 @@ __global__ __launch_bounds__(256, 2) void k_moe_up(MoeArgs g)
 // Where the last 16 rows would run past the end they begin earlier: those that
 // two waves have come out the same.  Reading W2 is the bound: the
 // same two layers, 940 us (6.9 TB/s) and 149 us (6.3).  With 16 rows a wave
-// the two terms of h were as many lines on their way into the L1 cache as the
-// rows, and more for 13 tokens: 1075 and 181 us.
+// h was as many lines on their way into the L1 cache as the rows, and more for
+// 13 tokens: 1075 and 181 us.  Making h's terms costs where an expert has more
+// than 32 tokens: 64 tokens on 2 experts of 14336 x 4096, BF16, 388 us for the
+// layer, 338 with h rounded to two BF16 terms by the first product.
 template <int T, int TT, bool kSplit>
 __global__ __launch_bounds__(256, 2) void k_moe_down(MoeArgs g)
 {
@@ -625,7 +674,7 @@ __global__ __launch_bounds__(256) void k_moe_up_one(MoeArgs g)
     rows_product<T, 2 * R>(rows, 0, g.cols, [&](uint32_t c, float *f) { Type<T>::unpack(load16<16>(g.x + c), f); }, acc);
 #pragma unroll
     for (int r = 0; r < 2 * R; r++) acc[r] = wave_sum(acc[r]);
-    float *h = reinterpret_cast<float *>(g.h) + (uint64_t)s * g.inner + n0;
+    float *h = g.h + (uint64_t)s * g.inner + n0;
 #pragma unroll
     for (int r = 0; r < R; r++)
         if (lane == (uint32_t)r) h[r] = acc[r] / (1.f + exp2_fast(-acc[r] * kLog2e)) * acc[R + r];
@@ -648,7 +697,7 @@ __global__ __launch_bounds__(1024) void k_moe_down_one(MoeArgs g)
     for (uint32_t q = wave; q < g.top_k * pieces; q += W) {
         const uint32_t s = q / pieces, c0 = q % pieces * per * 512, c1 = min(g.inner, c0 + per * 512);
         const uint16_t *w = g.w2 + (uint64_t)(uint32_t)g.ids[s] * g.down_expert + (uint64_t)n0 * g.down_row;
-        const float *h = reinterpret_cast<const float *>(g.h) + (uint64_t)s * g.inner, p = g.weights[s];
+        const float *h = g.h + (uint64_t)s * g.inner, p = g.weights[s];
         const uint16_t *rows[R];
         float part[R];
 #pragma unroll

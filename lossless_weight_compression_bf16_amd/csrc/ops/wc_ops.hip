@@ -217,7 +217,7 @@ struct MoePlan {
     bool one;       // k_moe_route_one
     bool split;     // k_moe_down with four waves for 16 columns
     uint32_t route_tiles, route_splits, route_steps, experts_pad, slots, up_tiles, down_tiles;
-    uint64_t logits, ids, weights, h, part, bytes;  // offsets in the scratch
+    uint64_t logits, ids, weights, most, h, part, bytes;  // offsets in the scratch
 };
 
 MoePlan moe_plan(uint32_t m, uint32_t experts, uint32_t top_k, uint32_t cols, uint32_t inner)
@@ -250,6 +250,7 @@ MoePlan moe_plan(uint32_t m, uint32_t experts, uint32_t top_k, uint32_t cols, ui
     p.logits = take(p.one ? 0 : 4ull * p.route_splits * m * p.experts_pad);
     p.ids = take(4ull * m * top_k);
     p.weights = take(4ull * m * top_k);
+    p.most = take(4ull * m * top_k);
     p.h = take(4ull * m * top_k * inner);
     p.part = take(4ull * m * top_k * cols);
     p.bytes = at;
@@ -482,7 +483,8 @@ wc_status wc_moe_layer(const wc_moe *a, void *d_scratch, uint64_t scratch_bytes,
     g.logits = reinterpret_cast<float *>(s + p.logits);
     g.ids = reinterpret_cast<int32_t *>(s + p.ids);
     g.weights = reinterpret_cast<float *>(s + p.weights);
-    g.h = reinterpret_cast<uint16_t *>(s + p.h);
+    g.most = reinterpret_cast<uint32_t *>(s + p.most);
+    g.h = reinterpret_cast<float *>(s + p.h);
     g.part = reinterpret_cast<float *>(s + p.part);
     g.experts_pad = p.experts_pad;
     g.route_splits = p.route_splits;

@@ -9,7 +9,10 @@
 // seen, S = sum 2^d and W = sum 2^d d with d = (z - m) log2 e, and corrects S
 // and W when a batch of 32 logits raises m:
 //   S' = c S,  W' = c (W + delta S),  delta = (m - m') log2 e,  c = 2^delta.
-// With the row's M, S, W: lse = M + ln S, H = ln S - ln 2 W / S.
+// With the row's M, S, W: lse = M + ln S, H = ln S - ln 2 W / S.  The maximum
+// is subtracted first: that is exact for the logits near it and 0 for itself,
+// whatever their size.  (z log2 e - m log2 e in one fused operation leaves the
+// rounding of m log2 e in every d: past 2^127 at m = 3e9.)
 //
 // The alternatives need no sort of the row.  Let T be the n-th largest of
 // the maxima of 256 classes of threads: at least n logits are >= T, so every
@@ -335,10 +338,9 @@ __device__ inline Stat slice_pass(const typename Type<T>::elem *row, uint32_t lo
 #pragma unroll
         for (uint32_t i = 1; i < kBatch; i++) bmax = fmaxf(bmax, f[i]);
         if (bmax > a.m) raise(a, bmax);
-        const float ml = a.m * kLog2e;
 #pragma unroll
         for (uint32_t i = 0; i < kBatch; i++) {
-            const float d = __builtin_fmaf(f[i], kLog2e, -ml);
+            const float d = (f[i] - a.m) * kLog2e;
             const float e = exp2_fast(d);
             a.s += e;
             a.w = __builtin_fmaf(e, fmaxf(d, -1000.f), a.w);  // a masked logit adds 0 * -1000, not 0 * -inf
@@ -356,8 +358,8 @@ __device__ inline Stat slice_pass(const typename Type<T>::elem *row, uint32_t lo
     return block_stat(a, sh);
 }
 
-// A row's statistics with its true maximum and exact differences, by the
-// whole block: for rows whose logits are too large for slice_pass.
+// A row's statistics with its true maximum, by the whole block: for rows
+// whose logits are all below kFloor, and for the gradient.
 template <int T, class Sh>
 __device__ __noinline__ Stat exact_stat(const typename Type<T>::elem *row, uint32_t vocab, Sh &sh)
 {
@@ -390,10 +392,9 @@ struct LogprobArgs {
 };
 
 // Writes a row's statistics; returns its lse for the alternatives.  Called
-// by the whole block; z is the logit of the row's token t.  S is 0 where every logit is below kFloor or the
-// largest above 2^127 / log2 e (masks of the type's lowest value in a whole
-// row, infinities, -inf in a whole row): such a row is computed again with
-// its true maximum and exact differences.
+// by the whole block; z is the logit of the row's token t.  S is 0 where every
+// logit is below kFloor (masks of the type's lowest value in a whole row, -inf
+// in a whole row): such a row is computed again with its true maximum.
 template <int T, class Sh>
 __device__ inline float write_row(const LogprobArgs &g, uint64_t r, Stat a, int64_t t, float z, Sh &sh)
 {

@@ -51,8 +51,9 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
 
 def on_stream(device: torch.device, stream, call):
     """call(raw stream) with the device and stream of the call current, so
-    that what it allocates belongs to that stream.  stream: None (the
-    device's current one), a torch stream or a raw hipStream_t."""
+    that what it allocates and copies belongs to that stream: copies of
+    arguments are made within call.  stream: None (the device's current one),
+    a torch stream or a raw hipStream_t."""
     if stream is None:
         if device.index == torch.cuda.current_device():
             return call(_raw_stream(device.index))

@@ -65,17 +65,16 @@ def add_adapters(x: torch.Tensor, y: torch.Tensor, a: torch.Tensor, b: torch.Ten
     m, cols = shape
     n, rank, _ = sa
     rows = sy[1]
-    x = _ops.rows16(x)
-    ids = ids.contiguous()
-    scales = scales.contiguous() if scales is not None else None
 
     def call(raw):
         lib = B.lib()
+        z, i = _ops.rows16(x), ids.contiguous()
+        s = scales.contiguous() if scales is not None else None
         nbytes = lib.wc_add_adapters_scratch(m, rank, cols, rows)
         scratch = torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
         err = _ops.error_word(check, dev)
-        g = B.wc_adapters(x.data_ptr(), x.stride(0), y.data_ptr(), y.stride(0), a.data_ptr(), b.data_ptr(),
-                          ids.data_ptr(), scales.data_ptr() if scales is not None else 0, m, n, rank, cols, rows,
+        g = B.wc_adapters(z.data_ptr(), z.stride(0), y.data_ptr(), y.stride(0), a.data_ptr(), b.data_ptr(),
+                          i.data_ptr(), s.data_ptr() if s is not None else 0, m, n, rank, cols, rows,
                           _ops.TYPES[dtype], _ops.TYPES[y_type])
         _ops.done(lib.wc_add_adapters(g, scratch.data_ptr() if nbytes else 0, nbytes, err.data_ptr() if check else 0,
                                       raw), err, "add_adapters")

@@ -41,11 +41,11 @@ def _good(logits, tokens, device) -> bool:
 
 
 def _forward(logits, tokens, top, check, stream, views=True):
-    z, t = _ops.rows_of(logits), tokens.contiguous()
-    m, vocab = z.shape
-    dev = z.device
+    m, vocab = logits.shape
+    dev = logits.device
 
     def call(raw):
+        z, t = _ops.rows_of(logits), tokens.contiguous()
         best = ids = None
         if not views:  # autograd's outputs are tensors of their own
             rows = [torch.empty(m, dtype=torch.float32, device=dev) for _ in range(3)]
@@ -93,13 +93,10 @@ def token_logprobs(logits: torch.Tensor, tokens: torch.Tensor, top: int = 0, che
     return _forward(logits, tokens, top, check, stream)
 
 
-def _row_values(v, m, what, device):
-    if v is None:
-        return None
-    if not (v.dtype == torch.float32 and v.shape == (m,) and v.device == device):
+def _check_row_values(v, m, what, device):
+    if v is not None and not (v.dtype == torch.float32 and v.shape == (m,) and v.device == device):
         _ops.check_tensor(v, what, device)
         raise ValueError(f"{what} must be {m} float32 numbers")
-    return v.contiguous()
 
 
 def token_logprobs_backward(logits: torch.Tensor, tokens: torch.Tensor, lse: torch.Tensor, entropy=None,
@@ -111,24 +108,30 @@ def token_logprobs_backward(logits: torch.Tensor, tokens: torch.Tensor, lse: tor
     dev = logits.device
     if not _good(logits, tokens, dev):
         _check(logits, tokens)
-    z, t = _ops.rows_of(logits), tokens.contiguous()
-    m, vocab = z.shape
+    m, vocab = logits.shape
     if lse is None:
         raise ValueError("lse is needed")
     if grad_entropy is not None and entropy is None:
         raise ValueError("the gradient of the entropy needs the entropy")
-    lse, entropy = _row_values(lse, m, "lse", dev), _row_values(entropy, m, "entropy", dev)
-    gl, ge = _row_values(grad_logprob, m, "grad_logprob", dev), _row_values(grad_entropy, m, "grad_entropy", dev)
+    _check_row_values(lse, m, "lse", dev)
+    _check_row_values(entropy, m, "entropy", dev)
+    _check_row_values(grad_logprob, m, "grad_logprob", dev)
+    _check_row_values(grad_entropy, m, "grad_entropy", dev)
     if out is not None:
         _ops.check_tensor(out, "out", dev)
-        if out.dtype != z.dtype or out.shape != z.shape or not _ops.rows_apart(out):
+        if out.dtype != logits.dtype or out.shape != logits.shape or not _ops.rows_apart(out):
             raise ValueError("out must be like the logits, with unit column stride and rows that do not overlap")
 
     def call(raw):
+        z, t = _ops.rows_of(logits), tokens.contiguous()
+        s = lse.contiguous()  # each copy is kept until the call is on the stream
+        ent = entropy.contiguous() if entropy is not None else None
+        gl = grad_logprob.contiguous() if grad_logprob is not None else None
+        ge = grad_entropy.contiguous() if grad_entropy is not None else None
         o = torch.empty((m, vocab), dtype=z.dtype, device=dev) if out is None else out
         err = _ops.error_word(check, dev)
-        a = B.wc_logprobs_grad(z.data_ptr(), z.stride(0), o.data_ptr(), o.stride(0), t.data_ptr(), lse.data_ptr(),
-                               entropy.data_ptr() if entropy is not None else 0, gl.data_ptr() if gl is not None else 0,
+        a = B.wc_logprobs_grad(z.data_ptr(), z.stride(0), o.data_ptr(), o.stride(0), t.data_ptr(), s.data_ptr(),
+                               ent.data_ptr() if ent is not None else 0, gl.data_ptr() if gl is not None else 0,
                                ge.data_ptr() if ge is not None else 0, m, vocab, _ops.TYPES[z.dtype])
         _ops.done(B.lib().wc_token_logprobs_backward(a, err.data_ptr() if check else 0, raw), err,
                   "token_logprobs_backward")

@@ -77,18 +77,18 @@ def moe_layer(x: torch.Tensor, router: torch.Tensor, w1: torch.Tensor, w3: torch
     go to the expert with the lower number."""
     if out is not None or not _good(x, router, w1, w3, w2, top_k):
         _check(x, router, w1, w3, w2, top_k, out)
-    x = _ops.rows16(x)
-    router = router if router.is_contiguous() and router.data_ptr() % 16 == 0 else router.clone(
-        memory_format=torch.contiguous_format)
     (m, cols), (experts, inner, _), dev = x.shape, w1.shape, x.device
 
     def call(raw):
         lib = B.lib()
+        z = _ops.rows16(x)
+        r = router if router.is_contiguous() and router.data_ptr() % 16 == 0 else router.clone(
+            memory_format=torch.contiguous_format)
         o = torch.empty((m, cols), dtype=x.dtype, device=dev) if out is None else out
         nbytes = lib.wc_moe_layer_scratch(m, experts, top_k, cols, inner)
         scratch = torch.empty(nbytes, dtype=torch.uint8, device=dev)
         up, down = w1.stride(), w2.stride()
-        g = B.wc_moe(x.data_ptr(), x.stride(0), router.data_ptr(), w1.data_ptr(), w3.data_ptr(), w2.data_ptr(),
+        g = B.wc_moe(z.data_ptr(), z.stride(0), r.data_ptr(), w1.data_ptr(), w3.data_ptr(), w2.data_ptr(),
                      up[0], up[1], down[0], down[1], o.data_ptr(), o.stride(0), m, experts, top_k, cols, inner,
                      _ops.TYPES[x.dtype], 1 if renormalize else 0)
         _ops.done(lib.wc_moe_layer(g, scratch.data_ptr(), nbytes, raw), None, "moe_layer")

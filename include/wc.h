@@ -394,7 +394,9 @@ wc_status wc_token_logprobs(const wc_logprobs *a, void *d_scratch, uint64_t scra
  * (log p_j + entropy)) with p_j = exp(z_j - lse), rounded once to `type`.
  * Either gradient may be NULL (zero).  Rows whose token is -1 or out of
  * range have no part of grad_logprob; rows with lse -inf have a zero
- * gradient.  `out` may be `logits` itself (with the same stride). */
+ * gradient.  `out` may be `logits` itself (with the same stride); otherwise
+ * the two must have no memory in common (WC_ERR_ARG): apart as a whole, or
+ * side by side in rows of the same stride. */
 typedef struct {
     const void *logits;
     uint64_t stride;
@@ -417,7 +419,9 @@ wc_status wc_token_logprobs_backward(const wc_logprobs_grad *a, uint32_t *d_err,
  * y_t += scales[i] B_i (A_i x_t) with i = ids[t].  ids[t] = -1: no adapter,
  * y_t stays; another number outside [0, n): y_t stays and WC_EF_BAD_INDEX.
  * Tokens may have adapters in any order; tokens side by side with the same
- * one share its reading.  Adapters of smaller ranks are padded with zeros. */
+ * one share its reading.  Adapters of smaller ranks are padded with zeros.
+ * y must have no memory in common with the inputs; with x that is checked
+ * (WC_ERR_ARG): apart as a whole, or side by side in rows of the same pitch. */
 typedef struct {
     const void *x;         /* m x cols, rows x_stride elements apart, 16-byte aligned rows */
     uint64_t x_stride;     /* a multiple of 8 */

@@ -66,6 +66,14 @@ def on_stream(device: torch.device, stream, call):
         return call(stream.cuda_stream)
 
 
+def may_overlap(a: torch.Tensor, b: torch.Tensor) -> bool:
+    """Whether the memory from the first to the last element of a and of b (2-D) has a byte in common."""
+    def ends(t):
+        return t.data_ptr(), t.data_ptr() + t.element_size() * (1 + sum((n - 1) * s for n, s in zip(t.shape, t.stride())))
+    (a0, a1), (b0, b1) = ends(a), ends(b)
+    return a0 < b1 and b0 < a1
+
+
 def error_word(check: bool, device):
     return torch.zeros(1, dtype=torch.int32, device=device) if check else None
 

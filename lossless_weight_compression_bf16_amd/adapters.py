@@ -49,7 +49,8 @@ def add_adapters(x: torch.Tensor, y: torch.Tensor, a: torch.Tensor, b: torch.Ten
     x: m x cols BF16 or FP16; y: m x rows, FP32 or the type of x; a: n x rank
     x cols and b: n x rows x rank in the type of x (rank at most 256, smaller
     ones padded with zeros; cols a multiple of 8); ids: m int64, -1 for a
-    token without an adapter; scales: n FP32.  With check (which waits for
+    token without an adapter; scales: n FP32.  y may lie in x's memory (x is
+    copied first).  With check (which waits for
     the GPU) an id out of range raises; without, its row of y stays as it
     is."""
     dev, dtype, y_type = x.device, x.dtype, y.dtype
@@ -76,8 +77,13 @@ def add_adapters(x: torch.Tensor, y: torch.Tensor, a: torch.Tensor, b: torch.Ten
         g = B.wc_adapters(z.data_ptr(), z.stride(0), y.data_ptr(), y.stride(0), a.data_ptr(), b.data_ptr(),
                           i.data_ptr(), s.data_ptr() if s is not None else 0, m, n, rank, cols, rows,
                           _ops.TYPES[dtype], _ops.TYPES[y_type])
-        _ops.done(lib.wc_add_adapters(g, scratch.data_ptr() if nbytes else 0, nbytes, err.data_ptr() if check else 0,
-                                      raw), err, "add_adapters")
+        where = scratch.data_ptr() if nbytes else 0, nbytes, err.data_ptr() if check else 0, raw
+        rc = lib.wc_add_adapters(g, *where)
+        if rc == B.WC_ERR_ARG and _ops.may_overlap(z, y):  # y in x's memory: from a copy of x
+            z = z.clone(memory_format=torch.contiguous_format)
+            g.x, g.x_stride = z.data_ptr(), cols
+            rc = lib.wc_add_adapters(g, *where)
+        _ops.done(rc, err, "add_adapters")
         return y
 
     return _ops.on_stream(dev, stream, call)

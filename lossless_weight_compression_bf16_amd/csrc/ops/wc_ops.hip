@@ -22,6 +22,17 @@ constexpr uint64_t kMaxGrid = 0x7FFFFFFFull;
 bool valid_type(uint32_t t) { return t <= WC_T_FP32; }
 uintptr_t type_bytes(uint32_t t) { return t == WC_T_FP32 ? 4 : 2; }
 
+// Whether two sets of m rows have no byte in common, rows and pitches in
+// bytes: apart as a whole, or side by side in rows of one pitch.
+bool rows_apart(const void *a, uint64_t a_pitch, uint64_t a_row, const void *b, uint64_t b_pitch, uint64_t b_row, uint64_t m)
+{
+    const uint64_t p = reinterpret_cast<uintptr_t>(a), q = reinterpret_cast<uintptr_t>(b);
+    if (p + (m - 1) * a_pitch + a_row <= q || q + (m - 1) * b_pitch + b_row <= p) return true;
+    if (m == 1 || a_pitch != b_pitch) return false;
+    const uint64_t off = q >= p ? (q - p) % a_pitch : (a_pitch - (p - q) % a_pitch) % a_pitch;  // of b's rows in a's
+    return off >= a_row && off + b_row <= a_pitch;
+}
+
 wc_status launched() { return hipGetLastError() == hipSuccess ? WC_OK : WC_ERR_HIP; }
 
 // Blocks of a row of the log probabilities: one, up to the batches that its
@@ -357,10 +368,12 @@ wc_status wc_token_logprobs_backward(const wc_logprobs_grad *a, uint32_t *d_err,
     if (a->m > 1 && (a->stride < a->vocab || a->out_stride < a->vocab)) return WC_ERR_ARG;
     const uintptr_t es = type_bytes(a->type);
     if (!a->logits || !a->out || !aligned(a->logits, es) || !aligned(a->out, es)) return WC_ERR_ARG;
-    if (a->out == a->logits && a->m > 1 && a->out_stride != a->stride) return WC_ERR_ARG;
     if (!a->tokens || !aligned(a->tokens, 8) || !a->lse || !aligned(a->lse, 4)) return WC_ERR_ARG;
     if (!aligned(a->grad_logprob, 4) || !aligned(a->grad_entropy, 4)) return WC_ERR_ARG;
     if (a->grad_entropy && (!a->entropy || !aligned(a->entropy, 4))) return WC_ERR_ARG;
+    if ((a->out != a->logits || (a->m > 1 && a->out_stride != a->stride)) &&
+        !rows_apart(a->logits, es * a->stride, es * a->vocab, a->out, es * a->out_stride, es * a->vocab, a->m))
+        return WC_ERR_ARG;
     LogprobGradArgs g{};
     g.logits = a->logits;
     g.out = a->out;
@@ -411,6 +424,9 @@ wc_status wc_add_adapters(const wc_adapters *a, void *d_scratch, uint64_t scratc
     if (p.tiles * p.splits > kMaxGrid || p.up_tiles * p.row_blocks > kMaxGrid) return WC_ERR_ARG;
     if (scratch_bytes < p.scratch) return WC_ERR_CAPACITY;
     if (p.scratch && (!d_scratch || !aligned(d_scratch, 16))) return WC_ERR_ARG;
+    // a block may read x where another has written y
+    const uint64_t yb = type_bytes(a->y_type);
+    if (!rows_apart(a->x, 2 * a->x_stride, 2ull * a->cols, a->y, yb * a->y_stride, yb * a->rows, a->m)) return WC_ERR_ARG;
     AdapterArgs g{};
     g.x = static_cast<const uint16_t *>(a->x);
     g.x_stride = a->x_stride;

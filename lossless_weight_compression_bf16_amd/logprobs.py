@@ -104,7 +104,8 @@ def token_logprobs_backward(logits: torch.Tensor, tokens: torch.Tensor, lse: tor
                             stream=None) -> torch.Tensor:
     """The gradient of the logits, in their type, from the gradients of
     logprob and entropy (either may be None) and the lse and entropy that
-    ``token_logprobs`` gave.  `out` may be the logits themselves."""
+    ``token_logprobs`` gave.  `out` may be the logits themselves (elsewhere
+    in their memory, they are copied first)."""
     dev = logits.device
     if not _good(logits, tokens, dev):
         _check(logits, tokens)
@@ -133,8 +134,12 @@ def token_logprobs_backward(logits: torch.Tensor, tokens: torch.Tensor, lse: tor
         a = B.wc_logprobs_grad(z.data_ptr(), z.stride(0), o.data_ptr(), o.stride(0), t.data_ptr(), s.data_ptr(),
                                ent.data_ptr() if ent is not None else 0, gl.data_ptr() if gl is not None else 0,
                                ge.data_ptr() if ge is not None else 0, m, vocab, _ops.TYPES[z.dtype])
-        _ops.done(B.lib().wc_token_logprobs_backward(a, err.data_ptr() if check else 0, raw), err,
-                  "token_logprobs_backward")
+        rc = B.lib().wc_token_logprobs_backward(a, err.data_ptr() if check else 0, raw)
+        if rc == B.WC_ERR_ARG and _ops.may_overlap(z, o):  # out across the logits: from a copy of them
+            z = z.clone(memory_format=torch.contiguous_format)
+            a.logits, a.stride = z.data_ptr(), vocab
+            rc = B.lib().wc_token_logprobs_backward(a, err.data_ptr() if check else 0, raw)
+        _ops.done(rc, err, "token_logprobs_backward")
         return o
 
     return _ops.on_stream(dev, stream, call)

@@ -159,5 +159,18 @@ class _TokenLogprobs(torch.autograd.Function):
         logits, tokens, lse, entropy = ctx.saved_tensors
         if grad_logprob is None and grad_entropy is None:
             return None, None, None, None
-        return (token_logprobs_backward(logits, tokens, lse, entropy, grad_logprob, grad_entropy, check=False),
-                None, None, None)
+        grad = token_logprobs_backward(logits, tokens, lse, entropy, grad_logprob, grad_entropy, check=False)
+        if torch.is_grad_enabled():  # create_graph: the kernel's result has no graph of its own
+            grad = _Once.apply(grad, logits, grad_logprob, grad_entropy)
+        return grad, None, None, None
+
+
+class _Once(torch.autograd.Function):
+    """A gradient that depends on its inputs, and whose own gradient is an error rather than nothing."""
+    @staticmethod
+    def forward(ctx, grad, *inputs):
+        return grad.view_as(grad)
+
+    @staticmethod
+    def backward(ctx, *_):
+        raise RuntimeError("token_logprobs cannot be differentiated twice")

@@ -80,7 +80,9 @@ def token_logprobs(logits: torch.Tensor, tokens: torch.Tensor, top: int = 0, che
 
     Token -1 stands for no token (logprob 0).  -inf masks a logit; a row of
     nothing but -inf has lse and log probabilities -inf and entropy 0; a row
-    with NaN or +inf has NaN statistics.  With check (which waits for the
+    with NaN or +inf has NaN statistics.  logprob and entropy can be
+    differentiated, once; lse and top_logprobs raise when a gradient comes
+    back to them.  With check (which waits for the
     GPU) a token out of range raises; without, its logprob is NaN."""
     if not _good(logits, tokens, logits.device):
         _check(logits, tokens)
@@ -150,12 +152,16 @@ class _TokenLogprobs(torch.autograd.Function):
     def forward(ctx, logits, tokens, top, check):
         r = _forward(logits, tokens, top, check, None, views=False)
         ctx.save_for_backward(logits, tokens, r.lse, r.entropy)
-        ctx.mark_non_differentiable(*(v for v in (r.lse, r.top_logprobs, r.top_ids) if v is not None))
+        if r.top_ids is not None:
+            ctx.mark_non_differentiable(r.top_ids)
         ctx.set_materialize_grads(False)
         return tuple(r)
 
     @staticmethod
-    def backward(ctx, grad_logprob, grad_entropy, *_):
+    def backward(ctx, grad_logprob, grad_entropy, grad_lse, grad_top, _):
+        if grad_lse is not None or grad_top is not None:
+            raise RuntimeError("token_logprobs has gradients of logprob and entropy only: detach lse and top_logprobs, "
+                               "or take them from torch where a loss needs them")
         logits, tokens, lse, entropy = ctx.saved_tensors
         if grad_logprob is None and grad_entropy is None:
             return None, None, None, None

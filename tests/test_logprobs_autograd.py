@@ -58,3 +58,33 @@ def test_second_order_raises(node):
     d, = torch.autograd.grad((weight * node(z, t).logprob).sum(), z, create_graph=True)
     with pytest.raises(RuntimeError, match="differentiated twice"):
         torch.autograd.grad(d.sum() + weight.sum(), weight)
+
+
+def test_gradients_of_the_other_outputs_raise(node):
+    z, t = _case()
+    for loss in (lambda r: 0.1 * r.lse.square().sum() - r.logprob.sum(),
+                 lambda r: r.top_logprobs.sum() - r.logprob.sum(), lambda r: r.lse.sum()):
+        with pytest.raises(RuntimeError, match="logprob and entropy only"):
+            torch.autograd.grad(loss(node(z, t, top=2)), z)
+    r = node(z, t, top=2)
+    assert not r.top_ids.requires_grad
+    got, = torch.autograd.grad((r.logprob * r.lse.detach()).sum() + r.top_logprobs.detach().sum(), z)
+    logp, lse = torch.log_softmax(z, 1), torch.logsumexp(z, 1).detach()
+    want, = torch.autograd.grad((logp.gather(1, t[:, None])[:, 0] * lse).sum(), z)
+    assert torch.allclose(got, want, rtol=0, atol=1e-12)
+
+
+@pytest.mark.gpu
+def test_the_kernels_node():
+    if not torch.cuda.is_available():
+        pytest.skip("no HIP device")
+    z = torch.randn((5, 3001), generator=torch.Generator().manual_seed(1)).cuda().requires_grad_()
+    t = torch.arange(5, device="cuda")
+    r = L.token_logprobs(z, t, top=3)
+    assert torch.autograd.grad(r.logprob.sum(), z, retain_graph=True)[0].isfinite().all()
+    for loss in (r.logprob.sum() + r.lse.sum(), r.logprob.sum() + r.top_logprobs.sum()):
+        with pytest.raises(RuntimeError, match="logprob and entropy only"):
+            torch.autograd.grad(loss, z, retain_graph=True)
+    d, = torch.autograd.grad(r.logprob.sum(), z, create_graph=True)
+    with pytest.raises(RuntimeError, match="differentiated twice"):
+        d.square().sum().backward()

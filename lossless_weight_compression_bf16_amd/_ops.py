@@ -74,6 +74,12 @@ def may_overlap(a: torch.Tensor, b: torch.Tensor) -> bool:
     return a0 < b1 and b0 < a1
 
 
+def no_backward(what: str):
+    """For a call that autograd would have to follow, and cannot."""
+    raise RuntimeError(f"{what} has no backward pass: call it under torch.no_grad(), or with tensors that do not require "
+                       "a gradient")
+
+
 def error_word(check: bool, device):
     return torch.zeros(1, dtype=torch.int32, device=device) if check else None
 

@@ -50,7 +50,8 @@ def add_adapters(x: torch.Tensor, y: torch.Tensor, a: torch.Tensor, b: torch.Ten
     x cols and b: n x rows x rank in the type of x (rank at most 256, smaller
     ones padded with zeros; cols a multiple of 8); ids: m int64, -1 for a
     token without an adapter; scales: n FP32.  y may lie in x's memory (x is
-    copied first).  With check (which waits for
+    copied first).  There is no backward pass: tensors that require a gradient
+    raise unless gradients are switched off.  With check (which waits for
     the GPU) an id out of range raises; without, its row of y stays as it
     is."""
     dev, dtype, y_type = x.device, x.dtype, y.dtype
@@ -63,6 +64,9 @@ def add_adapters(x: torch.Tensor, y: torch.Tensor, a: torch.Tensor, b: torch.Ten
             and a.is_contiguous() and b.is_contiguous() and not a.data_ptr() % 16 and _ops.rows_apart(y)
             and (scales is None or scales.dtype == torch.float32 and scales.shape == sa[:1] and scales.device == dev)):
         _check(x, y, a, b, ids, scales)
+    if torch.is_grad_enabled() and (x.requires_grad or y.requires_grad or a.requires_grad or b.requires_grad
+                                    or scales is not None and scales.requires_grad):
+        _ops.no_backward("add_adapters")
     m, cols = shape
     n, rank, _ = sa
     rows = sy[1]

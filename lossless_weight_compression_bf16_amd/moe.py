@@ -74,9 +74,13 @@ def moe_layer(x: torch.Tensor, router: torch.Tensor, w1: torch.Tensor, w3: torch
     stacked tensor will do); w2 (down): experts x cols x inner; cols and
     inner multiples of 8.  The weights are the softmax over all experts,
     divided by the sum of the chosen ones with `renormalize`.  Equal logits
-    go to the expert with the lower number."""
+    go to the expert with the lower number.  There is no backward pass:
+    tensors that require a gradient raise unless gradients are switched off."""
     if out is not None or not _good(x, router, w1, w3, w2, top_k):
         _check(x, router, w1, w3, w2, top_k, out)
+    if torch.is_grad_enabled() and (x.requires_grad or router.requires_grad or w1.requires_grad or w3.requires_grad
+                                    or w2.requires_grad or out is not None and out.requires_grad):
+        _ops.no_backward("moe_layer")
     (m, cols), (experts, inner, _), dev = x.shape, w1.shape, x.device
 
     def call(raw):

@@ -1,0 +1,56 @@
+"""Operators without a backward pass among tensors that autograd follows."""
+import pytest
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+
+import lossless_weight_compression_bf16_amd as wc  # noqa: E402
+from lossless_weight_compression_bf16_amd import adapters as A, moe as M  # noqa: E402
+
+BF = torch.bfloat16
+
+
+@pytest.fixture(scope="module")
+def dev():
+    if not torch.cuda.is_available():
+        pytest.skip("no HIP device")
+    wc.lib()
+    return torch.device("cuda:0")
+
+
+def _adapters(dev, m=4):
+    n, rank, c, rows = 2, 8, 64, 32
+    g = torch.Generator().manual_seed(m)
+    x, y, a, b = (torch.randn(s, generator=g).to(BF).to(dev) for s in ((m, c), (m, rows), (n, rank, c), (n, rows, rank)))
+    return x, y, a, b, torch.arange(m, device=dev) % n, torch.rand(n, generator=g).to(dev)
+
+
+def _experts(dev, m=4):
+    e, h, i = 3, 16, 8
+    g = torch.Generator().manual_seed(m)
+    return [torch.randn(s, generator=g).to(BF).to(dev) for s in ((m, h), (e, h), (e, i, h), (e, i, h), (e, h, i))]
+
+
+def test_tensors_that_require_a_gradient_raise(dev):
+    args = _adapters(dev)
+    want = A.add_adapters(args[0], args[1].clone(), *args[2:])
+    for k in (0, 1, 2, 3, 5):
+        some = [t.clone() for t in args]
+        some[k].requires_grad_()
+        with pytest.raises(RuntimeError, match="no backward pass"):
+            A.add_adapters(*some)
+        assert torch.equal(some[1], args[1])
+        with torch.no_grad():
+            assert torch.equal(A.add_adapters(*some), want)
+    args = _experts(dev)
+    want = M.moe_layer(*args, 2)
+    for k in range(5):
+        some = [t.clone() for t in args]
+        some[k].requires_grad_()
+        with pytest.raises(RuntimeError, match="no backward pass"):
+            M.moe_layer(*some, 2)
+        with torch.no_grad():
+            assert torch.equal(M.moe_layer(*some, 2), want)
+    with pytest.raises(RuntimeError, match="no backward pass"):
+        M.moe_layer(*args, 2, out=torch.zeros_like(want).requires_grad_())

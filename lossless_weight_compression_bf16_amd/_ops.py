@@ -9,6 +9,7 @@ on the GPU.)
 from __future__ import annotations
 
 import torch
+from torch.autograd.graph import increment_version as written  # what autograd has to know of a tensor written in place
 
 from . import _binding as B
 

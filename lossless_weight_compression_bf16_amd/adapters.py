@@ -81,6 +81,7 @@ def add_adapters(x: torch.Tensor, y: torch.Tensor, a: torch.Tensor, b: torch.Ten
         g = B.wc_adapters(z.data_ptr(), z.stride(0), y.data_ptr(), y.stride(0), a.data_ptr(), b.data_ptr(),
                           i.data_ptr(), s.data_ptr() if s is not None else 0, m, n, rank, cols, rows,
                           _ops.TYPES[dtype], _ops.TYPES[y_type])
+        _ops.written(y)
         where = scratch.data_ptr() if nbytes else 0, nbytes, err.data_ptr() if check else 0, raw
         rc = lib.wc_add_adapters(g, *where)
         if rc == B.WC_ERR_ARG and _ops.may_overlap(z, y):  # y in x's memory: from a copy of x

@@ -124,6 +124,9 @@ def token_logprobs_backward(logits: torch.Tensor, tokens: torch.Tensor, lse: tor
         _ops.check_tensor(out, "out", dev)
         if out.dtype != logits.dtype or out.shape != logits.shape or not _ops.rows_apart(out):
             raise ValueError("out must be like the logits, with unit column stride and rows that do not overlap")
+        if out.requires_grad and torch.is_grad_enabled():
+            raise RuntimeError("out requires a gradient: call token_logprobs_backward under torch.no_grad(), or with "
+                               "another out")
 
     def call(raw):
         z, t = _ops.rows_of(logits), tokens.contiguous()
@@ -132,6 +135,8 @@ def token_logprobs_backward(logits: torch.Tensor, tokens: torch.Tensor, lse: tor
         gl = grad_logprob.contiguous() if grad_logprob is not None else None
         ge = grad_entropy.contiguous() if grad_entropy is not None else None
         o = torch.empty((m, vocab), dtype=z.dtype, device=dev) if out is None else out
+        if out is not None:
+            _ops.written(out)
         err = _ops.error_word(check, dev)
         a = B.wc_logprobs_grad(z.data_ptr(), z.stride(0), o.data_ptr(), o.stride(0), t.data_ptr(), s.data_ptr(),
                                ent.data_ptr() if ent is not None else 0, gl.data_ptr() if gl is not None else 0,

@@ -89,6 +89,8 @@ def moe_layer(x: torch.Tensor, router: torch.Tensor, w1: torch.Tensor, w3: torch
         r = router if router.is_contiguous() and router.data_ptr() % 16 == 0 else router.clone(
             memory_format=torch.contiguous_format)
         o = torch.empty((m, cols), dtype=x.dtype, device=dev) if out is None else out
+        if out is not None:
+            _ops.written(out)
         nbytes = lib.wc_moe_layer_scratch(m, experts, top_k, cols, inner)
         scratch = torch.empty(nbytes, dtype=torch.uint8, device=dev)
         up, down = w1.stride(), w2.stride()

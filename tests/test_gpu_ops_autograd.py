@@ -6,7 +6,7 @@ pytestmark = pytest.mark.gpu
 torch = pytest.importorskip("torch")
 
 import lossless_weight_compression_bf16_amd as wc  # noqa: E402
-from lossless_weight_compression_bf16_amd import adapters as A, moe as M  # noqa: E402
+from lossless_weight_compression_bf16_amd import adapters as A, logprobs as L, moe as M  # noqa: E402
 
 BF = torch.bfloat16
 
@@ -54,3 +54,45 @@ def test_tensors_that_require_a_gradient_raise(dev):
             assert torch.equal(M.moe_layer(*some, 2), want)
     with pytest.raises(RuntimeError, match="no backward pass"):
         M.moe_layer(*args, 2, out=torch.zeros_like(want).requires_grad_())
+
+
+def _saved(t):
+    """A loss whose backward pass needs t as it is now."""
+    w = torch.ones_like(t).requires_grad_()
+    return (w * t).sum()
+
+
+def test_what_is_written_in_place_is_known_to_autograd(dev):
+    x, y, a, b, ids, s = _adapters(dev)
+    loss = _saved(y)
+    A.add_adapters(x, y, a, b, ids, s)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        loss.backward()
+    args = _experts(dev)
+    out = torch.zeros_like(args[0])
+    loss = _saved(out)
+    M.moe_layer(*args, 2, out=out)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        loss.backward()
+    z, t = torch.randn((3, 100), device=dev), torch.arange(3, device=dev)
+    r = L.token_logprobs(z, t)
+    loss = _saved(z)
+    L.token_logprobs_backward(z, t, r.lse, r.entropy, torch.ones(3, device=dev), out=z)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        loss.backward()
+
+
+def test_a_gradient_is_not_written_over_a_tensor_that_requires_one(dev):
+    z, t = torch.randn((3, 100), device=dev).requires_grad_(), torch.arange(3, device=dev)
+    one = torch.ones(3, device=dev)
+    r = L.token_logprobs(z.detach(), t)
+    before = z.detach().clone()
+    want = L.token_logprobs_backward(z, t, r.lse, r.entropy, one)
+    with pytest.raises(RuntimeError, match="requires a gradient"):
+        L.token_logprobs_backward(z, t, r.lse, r.entropy, one, out=z)
+    assert torch.equal(z.detach(), before)
+    with torch.no_grad():
+        assert torch.equal(L.token_logprobs_backward(z, t, r.lse, r.entropy, one, out=z), want)
+    with torch.inference_mode():  # tensors without versions
+        z = before.clone()
+        assert torch.equal(L.token_logprobs_backward(z, t, r.lse, r.entropy, one, out=z), want)

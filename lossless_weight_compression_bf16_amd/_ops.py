@@ -9,6 +9,7 @@ on the GPU.)
 from __future__ import annotations
 
 import torch
+from torch.autograd import forward_ad
 from torch.autograd.graph import increment_version as written  # what autograd has to know of a tensor written in place
 
 from . import _binding as B
@@ -79,6 +80,18 @@ def no_backward(what: str):
     """For a call that autograd would have to follow, and cannot."""
     raise RuntimeError(f"{what} has no backward pass: call it under torch.no_grad(), or with tensors that do not require "
                        "a gradient")
+
+
+def forward_mode() -> bool:
+    """Whether the call is made within a level of forward-mode differentiation (a look at a number: asking every
+    tensor would take as long as the checks of a call)."""
+    return getattr(forward_ad, "_current_level", 0) >= 0
+
+
+def no_tangents(what: str, *tensors):
+    """Raises where a tensor carries a forward-mode tangent, which the call would drop."""
+    if any(t is not None and forward_ad.unpack_dual(t).tangent is not None for t in tensors):
+        raise RuntimeError(f"{what} has no forward-mode derivative")
 
 
 def error_word(check: bool, device):

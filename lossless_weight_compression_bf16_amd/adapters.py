@@ -67,6 +67,8 @@ def add_adapters(x: torch.Tensor, y: torch.Tensor, a: torch.Tensor, b: torch.Ten
     if torch.is_grad_enabled() and (x.requires_grad or y.requires_grad or a.requires_grad or b.requires_grad
                                     or scales is not None and scales.requires_grad):
         _ops.no_backward("add_adapters")
+    if _ops.forward_mode():
+        _ops.no_tangents("add_adapters", x, y, a, b, scales)
     m, cols = shape
     n, rank, _ = sa
     rows = sy[1]

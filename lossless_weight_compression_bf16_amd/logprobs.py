@@ -88,6 +88,8 @@ def token_logprobs(logits: torch.Tensor, tokens: torch.Tensor, top: int = 0, che
         _check(logits, tokens)
     if not 0 <= top <= min(MAX_TOP, logits.shape[1]):
         raise ValueError(f"top must be between 0 and {min(MAX_TOP, logits.shape[1])}, got {top}")
+    if _ops.forward_mode():
+        _ops.no_tangents("token_logprobs", logits)
     if logits.requires_grad and torch.is_grad_enabled():
         if stream is not None:
             raise ValueError("with gradients the call runs on the current stream: use torch.cuda.stream")
@@ -120,6 +122,8 @@ def token_logprobs_backward(logits: torch.Tensor, tokens: torch.Tensor, lse: tor
     _check_row_values(entropy, m, "entropy", dev)
     _check_row_values(grad_logprob, m, "grad_logprob", dev)
     _check_row_values(grad_entropy, m, "grad_entropy", dev)
+    if _ops.forward_mode():
+        _ops.no_tangents("token_logprobs_backward", logits, lse, entropy, grad_logprob, grad_entropy, out)
     if out is not None:
         _ops.check_tensor(out, "out", dev)
         if out.dtype != logits.dtype or out.shape != logits.shape or not _ops.rows_apart(out):

@@ -81,6 +81,8 @@ def moe_layer(x: torch.Tensor, router: torch.Tensor, w1: torch.Tensor, w3: torch
     if torch.is_grad_enabled() and (x.requires_grad or router.requires_grad or w1.requires_grad or w3.requires_grad
                                     or w2.requires_grad or out is not None and out.requires_grad):
         _ops.no_backward("moe_layer")
+    if _ops.forward_mode():
+        _ops.no_tangents("moe_layer", x, router, w1, w3, w2, out)
     (m, cols), (experts, inner, _), dev = x.shape, w1.shape, x.device
 
     def call(raw):

@@ -5,6 +5,8 @@ pytestmark = pytest.mark.gpu
 
 torch = pytest.importorskip("torch")
 
+from torch.autograd import forward_ad  # noqa: E402
+
 import lossless_weight_compression_bf16_amd as wc  # noqa: E402
 from lossless_weight_compression_bf16_amd import adapters as A, logprobs as L, moe as M  # noqa: E402
 
@@ -96,3 +98,19 @@ def test_a_gradient_is_not_written_over_a_tensor_that_requires_one(dev):
     with torch.inference_mode():  # tensors without versions
         z = before.clone()
         assert torch.equal(L.token_logprobs_backward(z, t, r.lse, r.entropy, one, out=z), want)
+
+
+def test_forward_mode_raises(dev):
+    z, t = torch.randn((3, 100), device=dev), torch.arange(3, device=dev)
+    r = L.token_logprobs(z, t)
+    one = torch.ones(3, device=dev)
+    ad, ex = _adapters(dev), _experts(dev)
+    calls = [(lambda v: L.token_logprobs(v, t, top=2), z),
+             (lambda v: L.token_logprobs_backward(z, t, r.lse, r.entropy, v), one),
+             (lambda v: A.add_adapters(v, *ad[1:]), ad[0]), (lambda v: A.add_adapters(ad[0], v, *ad[2:]), ad[1]),
+             (lambda v: M.moe_layer(v, *ex[1:], 2), ex[0]), (lambda v: M.moe_layer(*ex[:4], v, 2), ex[4])]
+    with forward_ad.dual_level():
+        for call, at in calls:
+            call(at)  # no tangent
+            with pytest.raises(RuntimeError, match="no forward-mode derivative"):
+                call(forward_ad.make_dual(at, torch.ones_like(at)))

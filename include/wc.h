@@ -454,7 +454,7 @@ wc_status wc_add_adapters(const wc_adapters *a, void *d_scratch, uint64_t scratc
  * largest logits (equal ones by their number, NaN last), their weights p, or
  * with `renormalize` p divided by the sum of the chosen ones, and
  * out = sum_e weight_e W2_e (silu(W1_e x) * (W3_e x)), rounded once to
- * `type`.  Experts without tokens are not read. */
+ * `type`.  A NaN among a token's logits makes its weights NaN.  Experts without tokens are not read. */
 typedef struct {
     const void *x;          /* m x cols, rows x_stride elements apart, 16-byte aligned rows */
     uint64_t x_stride;      /* a multiple of 8 */

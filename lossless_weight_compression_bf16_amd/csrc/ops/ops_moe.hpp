@@ -187,7 +187,8 @@ __device__ __forceinline__ void moe_choose(const MoeArgs &g, uint32_t t, F logit
     if (lane < g.top_k) {
         g.ids[t * g.top_k + lane] = (int32_t)id;
         g.most[t * g.top_k + lane] = 0;
-        g.weights[t * g.top_k + lane] = mine / (g.renormalize ? chosen : sum);
+        // p of a token with a NaN among its logits are NaN, the chosen ones' sum with them
+        g.weights[t * g.top_k + lane] = mine / (g.renormalize && sum == sum ? chosen : sum);
     }
 }
 

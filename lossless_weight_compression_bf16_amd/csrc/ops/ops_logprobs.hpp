@@ -573,7 +573,7 @@ __global__ __launch_bounds__(kGradThreads) void k_logprobs_grad(LogprobGradArgs 
     auto grad = [&](float z, uint32_t j) {
         const float lp = (z - lse) - shift;
         const float p = exp2_fast(lp * kLog2e);
-        const float d = -p * __builtin_fmaf(h, fmaxf(lp, -1e30f), gh);  // p = 0: 0 times a finite number
+        const float d = -p * __builtin_fmaf(h, fmaxf(lp, -200.f), gh);  // p is 0 below -104: 0 times a finite number
         return j == t ? d + g : d;
     };
     for (uint32_t base = first; base < a.vocab; base += a.blocks * kSweep) {

@@ -19,7 +19,7 @@ torch = pytest.importorskip("torch")
 
 import lossless_weight_compression_bf16_amd as wc  # noqa: E402
 from lossless_weight_compression_bf16_amd import logprobs as L  # noqa: E402
-from test_gpu_logprobs import ROUND, _check, _expect, _order, _special_rows  # noqa: E402
+from test_gpu_logprobs import ROUND, _check, _expect, _grad64, _order, _special_rows  # noqa: E402
 
 EPS = 2.0 ** -24
 BF, HF, F32 = torch.bfloat16, torch.float16, torch.float32
@@ -133,3 +133,22 @@ def test_special_rows_of_joined_parts(dev, dtype):
         t = torch.full((z.shape[0],), k)
         _say(f"[logprobs range] special rows {dtype} {v} token {k}")
         _check(z, t, 20, L.token_logprobs(z.to(dev), t.to(dev), top=20), f"{dtype} {v} token {k}")
+
+
+@pytest.mark.parametrize("size", [1.0, 1e9, -1e20, 1e30])
+def test_large_gradient_of_the_entropy_at_masked_logits(dev, size):
+    """A scaled loss: a masked logit has p = 0 and a gradient of 0, whatever the gradient of the entropy."""
+    m, v = 3, 3001
+    z = torch.randn((m, v), generator=torch.Generator().manual_seed(5)) * 3
+    z[:, ::2] = -math.inf
+    z[1, 1::4] = -1e10
+    z[2, 1::4] = -300.0
+    t = torch.tensor([1, 3, 5])
+    r = L.token_logprobs(z.to(dev), t.to(dev))
+    ge = torch.tensor([size, -0.5 * size, 0.25 * size])
+    want, bound = _grad64(z, t, r.lse.cpu(), r.entropy.cpu(), torch.ones(m), ge)
+    got = L.token_logprobs_backward(z.to(dev), t.to(dev), r.lse, r.entropy, torch.ones(m, device=dev), ge.to(dev))
+    got = got.double().cpu()
+    assert bool((got[:, ::2] == 0).all())
+    tol = 2 * EPS * bound + 1.01 * ROUND[F32] * want.abs() + torch.finfo(F32).tiny * max(1.0, abs(size))
+    assert bool(((got - want).abs() <= tol).all())

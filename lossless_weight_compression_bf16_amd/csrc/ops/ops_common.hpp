@@ -194,7 +194,7 @@ __device__ __forceinline__ float term_scale(float most, float &unscale)
 {
     unscale = 1.f;
     if (T != WC_T_FP16 || !(most > 0.f && most < kInf)) return 1.f;
-    const int ex = max(-100, min(100, 15 - __builtin_amdgcn_frexp_expf(most)));
+    const int ex = min(100, 15 - __builtin_amdgcn_frexp_expf(most));  // -113 at least; 2^-100 for the smallest values
     unscale = __builtin_ldexpf(1.f, -ex);
     return __builtin_ldexpf(1.f, ex);
 }

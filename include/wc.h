@@ -348,7 +348,8 @@ uint64_t wc_noalloc_max_chunks(wc_format format);
  * products with its (compressed) weights.  The conventions above hold for
  * them too: device pointers owned by the caller, nothing allocated, nothing
  * synchronised, enqueued on `stream`.  Sums, softmax statistics and
- * intermediate products are held in 32 bits. */
+ * intermediate products are held in 32 bits; a second product takes all bits
+ * of a first one's result with BF16 weights, 22 of them with FP16 weights. */
 
 /* Element types of activations, logits and uncompressed weights. */
 #define WC_T_BF16 0u

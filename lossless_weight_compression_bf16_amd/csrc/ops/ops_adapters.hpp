@@ -13,10 +13,11 @@
 //   k_adapters_up     y_t += B_i u_t, u from the parts up to rank 64; for many
 //                     tokens k_adapters_up_many
 // What bounds it: x read once, y read and written once.  u stays in 32 bits:
-// it enters the matrix cores as a sum of 16-bit numbers, of BF16 or, after a
-// scaling by a power of two per token that brings its largest value to
-// 2^14..2^15, of FP16; products with the 16-bit B are exact and summed in
-// fp32, so y is rounded once, to its own type.
+// it enters the matrix cores as a sum of 16-bit numbers (Terms), for FP16
+// after a scaling by a power of two per token that brings its largest value
+// to 2^14..2^15; products with the 16-bit B are exact and summed in fp32, so y
+// is rounded once, to its own type.  (Two BF16 terms, 16 bits, for a 16-bit y
+// would save 3% of 8192 tokens at rank 64 and 7% of 2048 at rank 256.)
 //
 // MFMA 16x16x32 (lane l = 16 g + i): A operand row i, k = 8 g .. 8 g + 7;
 // B operand column i, the same k; D column i, rows 4 g .. 4 g + 3.  Here A is
@@ -84,49 +85,13 @@ struct TileIds {
     }
 };
 
-// 32-bit numbers as sums of 16-bit ones.  BF16 (8 significant bits each):
-// three terms leave out less than 2^-24 of a number; for a 16-bit y, which
-// keeps 8 bits itself, two, which leave out 2^-16.  FP16 (11 each): two.
-template <int T, int YT>
-struct Terms;
-template <int YT>
-struct Terms<WC_T_BF16, YT> {
-    static constexpr int kCount = YT == WC_T_FP32 ? 3 : 2;
-    __device__ static void split(const float *f, bf16x8 *out)
-    {
-#pragma unroll
-        for (int e = 0; e < 8; e++) {
-            float v = f[e];
-#pragma unroll
-            for (int c = 0; c < kCount; c++) {
-                const __bf16 a = (__bf16)v;
-                out[c][e] = a;
-                v = fabsf((float)a) < kInf ? v - (float)a : 0.f;  // an infinity is its own first term
-            }
-        }
-    }
-};
-template <int YT>
-struct Terms<WC_T_FP16, YT> {
-    static constexpr int kCount = 2;
-    __device__ static void split(const float *f, f16x8 *out)
-    {
-#pragma unroll
-        for (int e = 0; e < 8; e++) {
-            const _Float16 a = (_Float16)f[e];
-            out[0][e] = a;
-            out[1][e] = (_Float16)(fabsf((float)a) < kInf ? f[e] - (float)a : 0.f);
-        }
-    }
-};
-
 // Eight values of u of one token, from rank k, as terms.
-template <int T, int YT>
+template <int T>
 __device__ __forceinline__ void put_terms(const AdapterArgs &g, uint64_t token, uint32_t k, const float *f)
 {
-    constexpr int kTerms = Terms<T, YT>::kCount;
+    constexpr int kTerms = Terms<T>::kCount;
     typename Type<T>::x8 u[kTerms];
-    Terms<T, YT>::split(f, u);
+    Terms<T>::split(f, u);
 #pragma unroll
     for (int c = 0; c < kTerms; c++)
         *reinterpret_cast<u32x4 *>(g.u + (c * g.m + token) * g.rank_pad + k) = __builtin_bit_cast(u32x4, u[c]);
@@ -292,7 +257,7 @@ __global__ __launch_bounds__(256) void k_adapters_down_many(AdapterArgs g)
 }
 
 // u from its parts: eight lanes for the 64 ranks of a block of one token.
-template <int T, int YT>
+template <int T>
 __global__ __launch_bounds__(256) void k_adapters_terms(AdapterArgs g)
 {
     const uint32_t blocks = (g.rank_pad + 63) / 64;
@@ -327,13 +292,13 @@ __global__ __launch_bounds__(256) void k_adapters_terms(AdapterArgs g)
     const float sc = term_scale<T>(most, unscale);
 #pragma unroll
     for (int e = 0; e < 8; e++) f[e] *= sc;
-    if (k < g.rank_pad) put_terms<T, YT>(g, token, k, f);
+    if (k < g.rank_pad) put_terms<T>(g, token, k, f);
     if (threadIdx.x % 8 == 0) g.unscale[token * blocks + rb] = unscale;
 }
 
 // The same within a wave: u of one token (32 KS values, those of the lane; the
 // lanes of a token are 16 apart) as terms.
-template <int T, int YT, int KS, int C>
+template <int T, int KS, int C>
 __device__ __forceinline__ float adapter_terms(float (&f)[KS][8], typename Type<T>::x8 (&u)[KS][C])
 {
     float most = 0.f, unscale;
@@ -351,7 +316,7 @@ __device__ __forceinline__ float adapter_terms(float (&f)[KS][8], typename Type<
         if constexpr (T == WC_T_FP16)
 #pragma unroll
             for (int e = 0; e < 8; e++) f[s][e] *= sc;
-        Terms<T, YT>::split(f[s], u[s]);
+        Terms<T>::split(f[s], u[s]);
     }
     return unscale;
 }
@@ -484,7 +449,7 @@ __global__ __launch_bounds__(256, KS == 1 ? 4 : 2) void k_adapters_up(AdapterArg
     using Ty = Type<T>;
     using YE = typename Type<YT>::elem;
     using X8 = typename Ty::x8;
-    constexpr int kTerms = Terms<T, YT>::kCount;
+    constexpr int kTerms = Terms<T>::kCount;
     const uint32_t wave = threadIdx.x >> 6, lane = threadIdx.x & 63, i = lane & 15, gr = lane >> 4;
     const uint32_t row_blocks = (g.rows + g.row_block - 1) / g.row_block, rank_blocks = kBlocks ? (g.rank_pad + 63) / 64 : 1;
     const uint64_t tile = (uint64_t)(blockIdx.x / row_blocks) * 16;
@@ -547,7 +512,7 @@ __global__ __launch_bounds__(256, KS == 1 ? 4 : 2) void k_adapters_up(AdapterArg
             for (int s = 0; s < KS; s++)
 #pragma unroll
                 for (int e = 0; e < 8; e++) f[s][e] = 32 * s + 8 * gr + e < g.rank ? scale * f[s][e] : 0.f;
-            unscale = adapter_terms<T, YT, KS>(f, u);
+            unscale = adapter_terms<T, KS>(f, u);
         }
         while (nb < n1) {
             f32x4 sum[4];
@@ -590,7 +555,7 @@ __global__ __launch_bounds__(256, KS == 2 && (T == WC_T_FP16 || YT == WC_T_FP32)
     using Y = Type<YT>;
     using YE = typename Y::elem;
     using X8 = typename Ty::x8;
-    constexpr int kTerms = Terms<T, YT>::kCount, TT = 2, kPer = Y::kPer16;
+    constexpr int kTerms = Terms<T>::kCount, TT = 2, kPer = Y::kPer16;
     constexpr uint32_t kLanes = 64 / kPer, kRows = 64 / kLanes, kVecs = 32 / kRows;  // of y: lanes a row, rows a load, loads
     constexpr uint32_t kPitch = 68;  // floats of a token's 64 products in LDS: rows in different banks
     __shared__ u32x4 sb[2][4][KS][64];
@@ -695,7 +660,7 @@ __global__ __launch_bounds__(1024) void k_adapters_few(AdapterArgs g)
     using Ty = Type<T>;
     using YE = typename Type<YT>::elem;
     using X8 = typename Ty::x8;
-    constexpr int kTerms = Terms<T, YT>::kCount, KS = (RT + 1) / 2, Q = RT == 4 ? 1 : 4;
+    constexpr int kTerms = Terms<T>::kCount, KS = (RT + 1) / 2, Q = RT == 4 ? 1 : 4;
     constexpr int kPad = 32 * KS + 4;  // + 4: tokens in different banks
     __shared__ f32x4 part[16][RT][64];
     __shared__ float su[16][kPad];
@@ -770,7 +735,7 @@ __global__ __launch_bounds__(1024) void k_adapters_few(AdapterArgs g)
             f[s][e] = mine && k < 16 * RT ? su[i][k] : 0.f;
         }
     X8 u[KS][kTerms];
-    const float unscale = adapter_terms<T, YT, KS>(f, u);
+    const float unscale = adapter_terms<T, KS>(f, u);
     while (nb < n1) {
         f32x4 d[4];
 #pragma unroll

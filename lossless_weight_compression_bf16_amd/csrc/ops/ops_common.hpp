@@ -186,6 +186,48 @@ __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_ex
 __device__ __forceinline__ float nan32() { return __builtin_bit_cast(float, 0x7FC00000u); }
 constexpr float kInf = __builtin_inff();
 
+// Eight fp32 numbers as sums of 16-bit ones, for the matrix cores.  BF16: three
+// terms, the number itself (each is truncated, so that what two of 8 bits leave
+// is the third).  FP16: two, of numbers scaled as below, 22 bits and a sign.
+// An infinity is its own first term.
+template <int T>
+struct Terms;
+template <>
+struct Terms<WC_T_BF16> {
+    static constexpr int kCount = 3;
+    __device__ __forceinline__ static void split(const float *f, bf16x8 *out)
+    {
+        u32x4 v[kCount];
+#pragma unroll
+        for (int e = 0; e < 4; e++) {
+            float lo = f[2 * e], hi = f[2 * e + 1];
+#pragma unroll
+            for (int c = 0; c < kCount; c++) {
+                const uint32_t l = __builtin_bit_cast(uint32_t, lo), h = __builtin_bit_cast(uint32_t, hi);
+                v[c][e] = __builtin_amdgcn_perm(h, l, 0x07060302u);  // the upper halves of both
+                const float tl = __builtin_bit_cast(float, l & 0xFFFF0000u), th = __builtin_bit_cast(float, h & 0xFFFF0000u);
+                lo = c || fabsf(lo) < kInf ? lo - tl : 0.f;
+                hi = c || fabsf(hi) < kInf ? hi - th : 0.f;
+            }
+        }
+#pragma unroll
+        for (int c = 0; c < kCount; c++) out[c] = __builtin_bit_cast(bf16x8, v[c]);
+    }
+};
+template <>
+struct Terms<WC_T_FP16> {
+    static constexpr int kCount = 2;
+    __device__ __forceinline__ static void split(const float *f, f16x8 *out)
+    {
+#pragma unroll
+        for (int e = 0; e < 8; e++) {
+            const _Float16 a = (_Float16)f[e];
+            out[0][e] = a;
+            out[1][e] = (_Float16)(fabsf((float)a) < kInf ? f[e] - (float)a : 0.f);
+        }
+    }
+};
+
 // What FP16 values are multiplied by before they are split: the power of two
 // that brings `most`, the largest of them, to 2^14..2^15; its inverse in
 // `unscale`.  1 for BF16, whose range is that of FP32.

@@ -52,52 +52,6 @@ struct MoeArgs {
     uint32_t experts_pad, route_splits, route_steps, slots;
 };
 
-// Eight values of h as terms.  BF16: truncated, so that what is left after
-// two of 8 bits is the third.  FP16: values scaled as above; rounded towards
-// zero, so that none becomes an infinity.  An infinity is its own first term.
-template <int T>
-struct MoeTerms;
-template <>
-struct MoeTerms<WC_T_BF16> {
-    static constexpr int kCount = 3;
-    __device__ __forceinline__ static void split(const float *f, bf16x8 (&out)[kCount])
-    {
-        u32x4 v[kCount];
-#pragma unroll
-        for (int e = 0; e < 4; e++) {
-            float lo = f[2 * e], hi = f[2 * e + 1];
-#pragma unroll
-            for (int c = 0; c < kCount; c++) {
-                const uint32_t l = __builtin_bit_cast(uint32_t, lo), h = __builtin_bit_cast(uint32_t, hi);
-                v[c][e] = __builtin_amdgcn_perm(h, l, 0x07060302u);  // the upper halves of both
-                const float tl = __builtin_bit_cast(float, l & 0xFFFF0000u), th = __builtin_bit_cast(float, h & 0xFFFF0000u);
-                lo = c || fabsf(lo) < kInf ? lo - tl : 0.f;
-                hi = c || fabsf(hi) < kInf ? hi - th : 0.f;
-            }
-        }
-#pragma unroll
-        for (int c = 0; c < kCount; c++) out[c] = __builtin_bit_cast(bf16x8, v[c]);
-    }
-};
-template <>
-struct MoeTerms<WC_T_FP16> {
-    static constexpr int kCount = 2;
-    __device__ __forceinline__ static void split(const float *f, f16x8 (&out)[kCount])
-    {
-        u32x4 a, b;
-#pragma unroll
-        for (int e = 0; e < 4; e++) {
-            const auto t = __builtin_amdgcn_cvt_pkrtz(f[2 * e], f[2 * e + 1]);
-            const float lo = (float)t[0], hi = (float)t[1];
-            a[e] = __builtin_bit_cast(uint32_t, t);
-            b[e] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_pkrtz(fabsf(lo) < kInf ? f[2 * e] - lo : 0.f,
-                                                                           fabsf(hi) < kInf ? f[2 * e + 1] - hi : 0.f));
-        }
-        out[0] = __builtin_bit_cast(f16x8, a);
-        out[1] = __builtin_bit_cast(f16x8, b);
-    }
-};
-
 // logits[split][t][e]: 16 experts per block, the columns of a split over its
 // four waves.
 template <int T, int TT>
@@ -310,7 +264,7 @@ __device__ __forceinline__ void strip_product(const uint16_t *const (&weights)[M
     using Ty = Type<T>;
     using X8 = typename Ty::x8;
     constexpr int kSteps = kStripCols / 32, V = kTerms ? 2 : 1;  // vectors of 16 bytes for 8 numbers
-    constexpr int S = 16 / (V * NT) < kSteps ? 16 / (V * NT) : kSteps, C = kTerms ? MoeTerms<T>::kCount : 1;
+    constexpr int S = 16 / (V * NT) < kSteps ? 16 / (V * NT) : kSteps, C = kTerms ? Terms<T>::kCount : 1;
     const uint32_t lane = threadIdx.x & 63, i = lane & 15, gr = lane >> 4, hi = lane >> 5, lo = lane & 31;
     uint32_t off[8];
 #pragma unroll
@@ -369,7 +323,7 @@ __device__ __forceinline__ void strip_product(const uint16_t *const (&weights)[M
                             const uint32_t w = x[s][t][e / 4][e % 4];
                             f[e] = in ? __builtin_bit_cast(float, w) * scale[t] : 0.f;
                         }
-                        MoeTerms<T>::split(f, b);
+                        Terms<T>::split(f, b);
                     } else {
                         b[0] = __builtin_bit_cast(X8, only(in, x[s][t][0]));
                     }

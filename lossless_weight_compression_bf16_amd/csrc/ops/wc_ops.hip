@@ -138,7 +138,7 @@ AdapterPlan adapter_plan(uint64_t m, uint32_t n, uint32_t rank, uint32_t cols, u
     p.row_blocks = (uint32_t)ceil_div(rows, p.row_block);
     p.terms = many || rank > 64;
     p.u = 4ull * p.splits * m * p.rank_pad;
-    p.unscale = p.u + (p.terms ? 2ull * Terms<WC_T_BF16, WC_T_FP32>::kCount * m * p.rank_pad : 0);  // the most terms of all types
+    p.unscale = p.u + (p.terms ? 2ull * Terms<WC_T_BF16>::kCount * m * p.rank_pad : 0);  // the most terms of all types
     p.scratch = p.unscale + (p.terms ? 4 * m * p.rank_blocks : 0);
     return p;
 }
@@ -210,7 +210,7 @@ wc_status launch_adapters(const AdapterArgs &g, const AdapterPlan &p, hipStream_
         if (p.tile == 128) launch_down_many<T>(g, p, stream);
         else launch_down<T>(g, p, stream);
         if (p.terms)
-            hipLaunchKernelGGL((k_adapters_terms<T, YT>), dim3((uint32_t)ceil_div(g.m * p.rank_blocks, 32)), dim3(256),
+            hipLaunchKernelGGL(k_adapters_terms<T>, dim3((uint32_t)ceil_div(g.m * p.rank_blocks, 32)), dim3(256),
                                0, stream, g);
         launch_up<T, YT>(g, p, stream);
     }

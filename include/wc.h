@@ -370,7 +370,7 @@ typedef struct {
     const void *logits;
     uint64_t stride;
     const int64_t *tokens;   /* m */
-    uint64_t m;
+    uint64_t m;              /* below 2^31 */
     uint32_t vocab;          /* 1 .. 2^22 */
     uint32_t top;            /* 0 .. 64, at most vocab */
     uint32_t type;           /* WC_T_* */
@@ -408,7 +408,7 @@ typedef struct {
     const float *entropy;       /* may be NULL without grad_entropy */
     const float *grad_logprob;  /* may be NULL */
     const float *grad_entropy;  /* may be NULL */
-    uint64_t m;
+    uint64_t m;                 /* below 2^31 */
     uint32_t vocab;
     uint32_t type;
 } wc_logprobs_grad;
@@ -432,7 +432,7 @@ typedef struct {
     const void *b;         /* n x rows x rank */
     const int64_t *ids;    /* m */
     const float *scales;   /* n, or NULL: 1 */
-    uint64_t m;
+    uint64_t m;            /* at most 2^31 */
     uint32_t n;
     uint32_t rank;         /* 1 .. 256 */
     uint32_t cols;         /* a multiple of 8 */
@@ -473,7 +473,8 @@ typedef struct {
     uint32_t experts;       /* 1 .. 1024 */
     uint32_t top_k;         /* 1 .. 16, at most experts */
     uint32_t cols;          /* a multiple of 8, at most 2^20 */
-    uint32_t inner;         /* a multiple of 8, at most 2^20 */
+    uint32_t inner;         /* a multiple of 8, at most 2^20; the smaller of m top_k and
+                             * experts, times inner in whole 16s, below 2^28 */
     uint32_t type;          /* WC_T_BF16 or WC_T_FP16: of everything above */
     uint32_t renormalize;
 } wc_moe;

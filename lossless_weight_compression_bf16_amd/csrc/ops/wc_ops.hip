@@ -17,7 +17,9 @@ namespace {
 
 bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 uint64_t ceil_div(uint64_t a, uint64_t b) { return (a + b - 1) / b; }
-constexpr uint64_t kMaxGrid = 0x7FFFFFFFull;
+constexpr uint64_t kMaxRows = 0x7FFFFFFFull;
+// Blocks of a launch: HIP counts a grid's threads along x in 32 bits.
+constexpr uint64_t max_blocks(uint64_t threads) { return 0xFFFFFFFFull / threads; }
 
 bool valid_type(uint32_t t) { return t <= WC_T_FP32; }
 uintptr_t type_bytes(uint32_t t) { return t == WC_T_FP32 ? 4 : 2; }
@@ -53,12 +55,33 @@ uint64_t logprob_scratch(uint64_t m, uint32_t vocab, uint32_t top)
     return slices == 1 ? 0 : m * slices * (16 + 8ull * top);
 }
 
-template <int T, bool kTop, int NT>
-void launch_rows(const LogprobArgs &g, uint64_t m, hipStream_t stream)
+// The same from row r on.
+LogprobArgs from_row(LogprobArgs g, uint64_t r, uintptr_t bytes)
 {
-    hipLaunchKernelGGL((k_logprobs<T, kTop, NT>), dim3((uint32_t)(m * g.slices)), dim3(NT), 0, stream, g);
-    if (g.slices > 1)
-        hipLaunchKernelGGL((k_logprobs_join<T, kTop>), dim3((uint32_t)m), dim3(kJoinThreads), 0, stream, g);
+    g.logits = static_cast<const char *>(g.logits) + r * g.stride * bytes;
+    g.tokens += r;
+    g.logprob += r;
+    g.entropy += r;
+    g.lse += r;
+    if (g.top) {
+        g.top_logprobs += r * g.top;
+        g.top_ids += r * g.top;
+    }
+    return g;
+}
+
+template <int T, bool kTop, int NT>
+void launch_rows(const LogprobArgs &all, uint64_t m, hipStream_t stream)
+{
+    static_assert(NT >= kJoinThreads, "the join's grid is the smaller one");
+    const uint64_t most = max_blocks(NT) / all.slices;
+    for (uint64_t r = 0; r < m; r += most) {  // every launch's parts in the same scratch
+        const LogprobArgs g = from_row(all, r, type_bytes(T));
+        const uint64_t rows = m - r < most ? m - r : most;
+        hipLaunchKernelGGL((k_logprobs<T, kTop, NT>), dim3((uint32_t)(rows * g.slices)), dim3(NT), 0, stream, g);
+        if (g.slices > 1)
+            hipLaunchKernelGGL((k_logprobs_join<T, kTop>), dim3((uint32_t)rows), dim3(kJoinThreads), 0, stream, g);
+    }
 }
 
 template <int T>
@@ -72,10 +95,26 @@ wc_status launch_logprobs(const LogprobArgs &g, uint64_t m, hipStream_t stream)
 }
 
 template <int T>
-void launch_grad(const LogprobGradArgs &g, dim3 grid, bool large, hipStream_t stream)
+void launch_grad(LogprobGradArgs g, uint64_t m, hipStream_t stream)
 {
-    if (large) hipLaunchKernelGGL((k_logprobs_grad<T, true>), grid, dim3(kGradThreads), 0, stream, g);
-    else hipLaunchKernelGGL((k_logprobs_grad<T, false>), grid, dim3(kGradThreads), 0, stream, g);
+    const uintptr_t es = type_bytes(T);
+    // past the caches where the logits do not fit into the last of them (256 MiB)
+    const bool large = m * g.vocab * es > (128ull << 20);
+    const uint64_t most = max_blocks(kGradThreads) / g.blocks;
+    while (m) {
+        const uint64_t rows = m < most ? m : most;
+        const dim3 grid((uint32_t)(rows * g.blocks));
+        if (large) hipLaunchKernelGGL((k_logprobs_grad<T, true>), grid, dim3(kGradThreads), 0, stream, g);
+        else hipLaunchKernelGGL((k_logprobs_grad<T, false>), grid, dim3(kGradThreads), 0, stream, g);
+        m -= rows;
+        g.logits = static_cast<const char *>(g.logits) + rows * g.stride * es;
+        g.out = static_cast<char *>(g.out) + rows * g.out_stride * es;
+        g.tokens += rows;
+        g.lse += rows;
+        if (g.entropy) g.entropy += rows;
+        if (g.grad_logprob) g.grad_logprob += rows;
+        if (g.grad_entropy) g.grad_entropy += rows;
+    }
 }
 
 // Launch shapes of the adapters: tiles of 16 tokens, each turn of a tile (an
@@ -96,11 +135,11 @@ AdapterPlan adapter_plan(uint64_t m, uint32_t n, uint32_t rank, uint32_t cols, u
     p.rank_pad = (rank + 31) / 32 * 32;
     // one launch where all blocks' reading of A from the caches costs less
     // than the second launch: at most 16 MiB, a block per 1,024 to 4,096 rows
-    const uint64_t reading = m * rank * cols * 2;
+    const uint64_t reading = m * rank * cols * 2, pairs = ceil_div(ceil_div(m, 16) * (m < 16 ? m : 16), 8) * 8;
     for (uint32_t r = 1024; r <= 4096 && rank <= 64 && m <= 64 && !p.few; r *= 2) {
         p.row_block = r;
         p.row_blocks = (uint32_t)ceil_div(rows, r);
-        p.few = reading * p.row_blocks <= (16ull << 20);
+        p.few = reading * p.row_blocks <= (16ull << 20) && pairs * p.row_blocks <= max_blocks(1024);
     }
     // a tile of 128 tokens has few adapters, and the blocks of turns that it
     // does not have cost little: us for one turn and three, rank 64, 8192
@@ -150,6 +189,12 @@ AdapterPlan adapter_plan(uint64_t m, uint32_t n, uint32_t rank, uint32_t cols, u
 // 54 and 41, of 32 73 and 64, of 64 83 and 90; rank 16, 1024 tokens of 16 28
 // and 29, of 32 28 and 34, of 64 29 and 46.
 bool many_tokens(uint64_t m, uint32_t n) { return m >= 256 && m >= 64ull * n; }
+
+// Tokens of one set of launches: no grid of theirs comes near max_blocks
+// (2^20 tiles of 16 tokens, and then one block of rows, or fewer tiles with
+// up to 2,048 blocks more), and the scratch stays small.  Columns are in
+// parts for less than 2^15 tokens only, up to 8 of them.
+constexpr uint64_t kMaxTokens = 1ull << 24;
 
 bool valid_adapters(uint64_t m, uint32_t rank, uint32_t cols, uint32_t rows)
 {
@@ -272,7 +317,7 @@ bool valid_moe(uint64_t m, uint32_t experts, uint32_t top_k, uint32_t cols, uint
 {
     return m <= kMoeMaxTokens && experts >= 1 && experts <= kMoeMaxExperts && top_k >= 1 && top_k <= kMoeMaxTop &&
            top_k <= experts && cols >= 8 && cols % 8 == 0 && cols <= (1u << 20) && inner >= 8 && inner % 8 == 0 &&
-           inner <= (1u << 20);
+           inner <= (1u << 20) && (m * top_k < experts ? m * top_k : experts) * ((inner + 15) / 16) <= max_blocks(256);
 }
 
 template <int T, int TT>
@@ -315,7 +360,7 @@ extern "C" {
 
 uint64_t wc_token_logprobs_scratch(uint64_t m, uint32_t vocab, uint32_t top)
 {
-    if (m == 0 || vocab == 0 || vocab > kMaxVocab || top > kMaxTop) return 0;
+    if (m == 0 || m > kMaxRows || vocab == 0 || vocab > kMaxVocab || top > kMaxTop) return 0;
     return logprob_scratch(m, vocab, top);
 }
 
@@ -326,7 +371,7 @@ wc_status wc_token_logprobs(const wc_logprobs *a, void *d_scratch, uint64_t scra
         return WC_ERR_ARG;
     if (d_err && !aligned(d_err, 4)) return WC_ERR_ARG;
     if (a->m == 0) return WC_OK;
-    if (a->m > kMaxGrid || (a->m > 1 && a->stride < a->vocab)) return WC_ERR_ARG;
+    if (a->m > kMaxRows || (a->m > 1 && a->stride < a->vocab)) return WC_ERR_ARG;
     if (!a->logits || !aligned(a->logits, type_bytes(a->type)) || !a->tokens || !aligned(a->tokens, 8))
         return WC_ERR_ARG;
     if (!a->logprob || !a->entropy || !a->lse || !aligned(a->logprob, 4) || !aligned(a->entropy, 4) ||
@@ -336,7 +381,6 @@ wc_status wc_token_logprobs(const wc_logprobs *a, void *d_scratch, uint64_t scra
         return WC_ERR_ARG;
     LogprobArgs g{};
     logprob_slices(a->vocab, &g.slices, &g.slice);
-    if (a->m * g.slices > kMaxGrid) return WC_ERR_ARG;
     const uint64_t need = logprob_scratch(a->m, a->vocab, a->top);
     if (scratch_bytes < need) return WC_ERR_CAPACITY;
     if (need && (!d_scratch || !aligned(d_scratch, 16))) return WC_ERR_ARG;
@@ -365,7 +409,7 @@ wc_status wc_token_logprobs_backward(const wc_logprobs_grad *a, uint32_t *d_err,
     if (!a || !valid_type(a->type) || a->vocab == 0 || a->vocab > kMaxVocab) return WC_ERR_ARG;
     if (d_err && !aligned(d_err, 4)) return WC_ERR_ARG;
     if (a->m == 0) return WC_OK;
-    if (a->m > 1 && (a->stride < a->vocab || a->out_stride < a->vocab)) return WC_ERR_ARG;
+    if (a->m > kMaxRows || (a->m > 1 && (a->stride < a->vocab || a->out_stride < a->vocab))) return WC_ERR_ARG;
     const uintptr_t es = type_bytes(a->type);
     if (!a->logits || !a->out || !aligned(a->logits, es) || !aligned(a->out, es)) return WC_ERR_ARG;
     if (!a->tokens || !aligned(a->tokens, 8) || !a->lse || !aligned(a->lse, 4)) return WC_ERR_ARG;
@@ -387,14 +431,10 @@ wc_status wc_token_logprobs_backward(const wc_logprobs_grad *a, uint32_t *d_err,
     g.vocab = a->vocab;
     g.blocks = a->out == a->logits ? 1 : (uint32_t)ceil_div(a->vocab, kGradThreads * kBatch);
     g.err = d_err;
-    if (a->m > kMaxGrid / g.blocks) return WC_ERR_ARG;
-    const dim3 grid((uint32_t)(a->m * g.blocks));
-    // past the caches where the logits do not fit into the last of them (256 MiB)
-    const bool large = a->m * a->vocab * es > (128ull << 20);
     switch (a->type) {
-    case WC_T_BF16: launch_grad<WC_T_BF16>(g, grid, large, stream); break;
-    case WC_T_FP16: launch_grad<WC_T_FP16>(g, grid, large, stream); break;
-    default: launch_grad<WC_T_FP32>(g, grid, large, stream); break;
+    case WC_T_BF16: launch_grad<WC_T_BF16>(g, a->m, stream); break;
+    case WC_T_FP16: launch_grad<WC_T_FP16>(g, a->m, stream); break;
+    default: launch_grad<WC_T_FP32>(g, a->m, stream); break;
     }
     return launched();
 }
@@ -403,6 +443,7 @@ uint64_t wc_add_adapters_scratch(uint64_t m, uint32_t rank, uint32_t cols, uint3
 {
     if (m == 0 || !valid_adapters(m, rank, cols, rows)) return 0;
     // enough for either plan: the adapters' number is not known here
+    if (m > kMaxTokens) m = kMaxTokens;
     const uint64_t small = adapter_plan(m, 0, rank, cols, rows, false).scratch;
     const uint64_t large = many_tokens(m, 1) ? adapter_plan(m, 0, rank, cols, rows, true).scratch : 0;
     return small > large ? small : large;
@@ -420,37 +461,43 @@ wc_status wc_add_adapters(const wc_adapters *a, void *d_scratch, uint64_t scratc
     if (!a->x || !aligned(a->x, 16) || (a->m > 1 && (a->x_stride < a->cols || a->x_stride % 8))) return WC_ERR_ARG;
     if (!a->y || !aligned(a->y, type_bytes(a->y_type)) || (a->m > 1 && a->y_stride < a->rows)) return WC_ERR_ARG;
     if (!a->ids || !aligned(a->ids, 8) || !aligned(a->scales, 4)) return WC_ERR_ARG;
-    const AdapterPlan p = adapter_plan(a->m, a->n, a->rank, a->cols, a->rows, many_tokens(a->m, a->n));
-    if (p.tiles * p.splits > kMaxGrid || p.up_tiles * p.row_blocks > kMaxGrid) return WC_ERR_ARG;
+    auto plan = [&](uint64_t m) { return adapter_plan(m, a->n, a->rank, a->cols, a->rows, many_tokens(m, a->n)); };
+    AdapterPlan p = plan(a->m < kMaxTokens ? a->m : kMaxTokens);
     if (scratch_bytes < p.scratch) return WC_ERR_CAPACITY;
     if (p.scratch && (!d_scratch || !aligned(d_scratch, 16))) return WC_ERR_ARG;
-    // a block may read x where another has written y
     const uint64_t yb = type_bytes(a->y_type);
+    // a block may read x where another has written y
     if (!rows_apart(a->x, 2 * a->x_stride, 2ull * a->cols, a->y, yb * a->y_stride, yb * a->rows, a->m)) return WC_ERR_ARG;
-    AdapterArgs g{};
-    g.x = static_cast<const uint16_t *>(a->x);
-    g.x_stride = a->x_stride;
-    g.y = a->y;
-    g.y_stride = a->y_stride;
-    g.a = static_cast<const uint16_t *>(a->a);
-    g.b = static_cast<const uint16_t *>(a->b);
-    g.ids = a->ids;
-    g.scales = a->scales;
-    g.m = a->m;
-    g.n = a->n;
-    g.rank = a->rank;
-    g.cols = a->cols;
-    g.rows = a->rows;
-    g.part = static_cast<float *>(d_scratch);
-    g.u = reinterpret_cast<uint16_t *>(static_cast<char *>(d_scratch) + p.u);
-    g.unscale = reinterpret_cast<float *>(static_cast<char *>(d_scratch) + p.unscale);
-    g.rank_pad = p.rank_pad;
-    g.splits = p.splits;
-    g.split_cols = p.split_cols;
-    g.row_block = p.row_block;
-    g.err = d_err;
-    return a->type == WC_T_BF16 ? launch_adapters<WC_T_BF16>(g, p, a->y_type, stream)
-                                : launch_adapters<WC_T_FP16>(g, p, a->y_type, stream);
+    wc_status status = WC_OK;
+    for (uint64_t t = 0; t < a->m && status == WC_OK; t += kMaxTokens) {
+        const uint64_t m = a->m - t < kMaxTokens ? a->m - t : kMaxTokens;
+        if (t && m < kMaxTokens) p = plan(m);  // the last: its scratch is smaller, also with columns in 8 parts
+        AdapterArgs g{};
+        g.x = static_cast<const uint16_t *>(a->x) + t * a->x_stride;
+        g.x_stride = a->x_stride;
+        g.y = static_cast<char *>(a->y) + t * a->y_stride * yb;
+        g.y_stride = a->y_stride;
+        g.a = static_cast<const uint16_t *>(a->a);
+        g.b = static_cast<const uint16_t *>(a->b);
+        g.ids = a->ids + t;
+        g.scales = a->scales;
+        g.m = m;
+        g.n = a->n;
+        g.rank = a->rank;
+        g.cols = a->cols;
+        g.rows = a->rows;
+        g.part = static_cast<float *>(d_scratch);
+        g.u = reinterpret_cast<uint16_t *>(static_cast<char *>(d_scratch) + p.u);
+        g.unscale = reinterpret_cast<float *>(static_cast<char *>(d_scratch) + p.unscale);
+        g.rank_pad = p.rank_pad;
+        g.splits = p.splits;
+        g.split_cols = p.split_cols;
+        g.row_block = p.row_block;
+        g.err = d_err;
+        status = a->type == WC_T_BF16 ? launch_adapters<WC_T_BF16>(g, p, a->y_type, stream)
+                                      : launch_adapters<WC_T_FP16>(g, p, a->y_type, stream);
+    }
+    return status;
 }
 
 uint64_t wc_moe_layer_scratch(uint64_t m, uint32_t experts, uint32_t top_k, uint32_t cols, uint32_t inner)
@@ -473,7 +520,6 @@ wc_status wc_moe_layer(const wc_moe *a, void *d_scratch, uint64_t scratch_bytes,
         return WC_ERR_ARG;
     if (!a->out || !aligned(a->out, 2) || (a->m > 1 && a->out_stride < a->cols)) return WC_ERR_ARG;
     const MoePlan p = moe_plan((uint32_t)a->m, a->experts, a->top_k, a->cols, a->inner);
-    if ((uint64_t)p.slots * p.up_tiles > kMaxGrid || (uint64_t)p.slots * p.down_tiles > kMaxGrid) return WC_ERR_ARG;
     if (scratch_bytes < p.bytes) return WC_ERR_CAPACITY;
     if (!d_scratch || !aligned(d_scratch, 256)) return WC_ERR_ARG;
     char *s = static_cast<char *>(d_scratch);

@@ -1,0 +1,33 @@
+"""Sizes past what a call takes, refused at the C boundary (and scratch sizes
+of 0) before anything is launched."""
+import pytest
+
+import lossless_weight_compression_bf16_amd as wc
+from lossless_weight_compression_bf16_amd import _binding as B
+
+torch = pytest.importorskip("torch")
+
+
+def test_scratch_of_sizes_past_the_limits():
+    lib = wc.lib()
+    assert lib.wc_token_logprobs_scratch((1 << 31) - 1, 131073, 0) == ((1 << 31) - 1) * 2 * 16
+    assert lib.wc_token_logprobs_scratch(1 << 31, 131073, 0) == 0
+    # experts with tokens times rows of 16: below 2^24
+    assert lib.wc_moe_layer_scratch(64, 1024, 16, 8, (1 << 18) - 16) > 0
+    assert lib.wc_moe_layer_scratch(64, 1024, 16, 8, 1 << 18) == 0
+    assert lib.wc_moe_layer_scratch(8, 1024, 16, 8, 1 << 20) > 0
+    # adapters: several sets of launches share the scratch of one
+    assert lib.wc_add_adapters_scratch(1 << 31, 8, 64, 48) == lib.wc_add_adapters_scratch(1 << 24, 8, 64, 48) > 0
+
+
+def test_refusals_past_the_limits():
+    if torch.cuda.is_available():
+        pytest.skip("addresses of no memory: only where nothing can be launched on them")
+    lib = wc.lib()
+    z = B.wc_logprobs(0x1000, 10, 0x2000, 1 << 31, 10, 0, B.WC_T_BF16, 0, 0x3000, 0x4000, 0x5000, 0, 0)
+    assert lib.wc_token_logprobs(z, None, 0, None, None) == B.WC_ERR_ARG
+    d = B.wc_logprobs_grad(0x1000, 10, 0x1000, 10, 0x2000, 0x3000, 0, 0, 0, 1 << 31, 10, B.WC_T_BF16)
+    assert lib.wc_token_logprobs_backward(d, None, None) == B.WC_ERR_ARG
+    e = B.wc_moe(0x10000, 8, 0x20000, 0x30000, 0x40000, 0x50000, 1 << 21, 8, 1 << 21, 1 << 18, 0x60000, 8, 64, 1024, 16, 8,
+                 1 << 18, B.WC_T_BF16, 1)
+    assert lib.wc_moe_layer(e, 0x100000, 1 << 50, None) == B.WC_ERR_ARG

@@ -12,7 +12,6 @@ namespace ops {
 
 constexpr uint32_t kCus = 256;  // compute units of an MI355X: what the launch shapes are planned for
 
-typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
@@ -25,12 +24,10 @@ template <int kAlign>
 struct Unaligned;
 template <>
 struct Unaligned<2> {
-    typedef uint32_t x2 __attribute__((ext_vector_type(2), aligned(2)));
     typedef uint32_t x4 __attribute__((ext_vector_type(4), aligned(2)));
 };
 template <>
 struct Unaligned<4> {
-    typedef uint32_t x2 __attribute__((ext_vector_type(2), aligned(4)));
     typedef uint32_t x4 __attribute__((ext_vector_type(4), aligned(4)));
 };
 template <>

@@ -309,6 +309,9 @@ __device__ inline Stat slice_pass(const typename Type<T>::elem *row, uint32_t lo
     uint32_t round = 0;
     u32x4 cur[kVecs], nxt[kVecs];
     // a round's vector u of a thread: elements base + (NT u + tid) kPer ..
+    // Past the caches with 256 threads, that is, where rows are many: us past
+    // them and through them, BF16, 2048 rows of 128256 93 and 104, 512 rows 32
+    // and 33, 1024 rows of 32000 21.4 and 21.1, 1000 of 8192 13.6 both.
     auto fetch = [&](u32x4 *v, uint32_t base) {
 #pragma unroll
         for (uint32_t u = 0; u < kVecs; u++)

@@ -87,8 +87,11 @@ void launch_rows(const LogprobArgs &all, uint64_t m, hipStream_t stream)
 template <int T>
 wc_status launch_logprobs(const LogprobArgs &g, uint64_t m, hipStream_t stream)
 {
-    // few rows: more threads for each, and logits that may still be in the caches
-    const bool few = m * g.slices < 2 * kCus;
+    // 1,024 threads a row while every row has a compute unit of its own, else
+    // 256; us with 1,024 and with 256, BF16, 5 best: 64 rows of 128256 17 and
+    // 22, 256 rows 21 and 26, 300 rows 35 and 29, 512 rows 42 and 32, 2048 rows
+    // 146 and 93; 256 rows of 50257 14.7 and 16.0, 300 rows 25 and 19
+    const bool few = m * g.slices <= kCus;
     if (g.top) few ? launch_rows<T, true, 1024>(g, m, stream) : launch_rows<T, true, 256>(g, m, stream);
     else few ? launch_rows<T, false, 1024>(g, m, stream) : launch_rows<T, false, 256>(g, m, stream);
     return launched();

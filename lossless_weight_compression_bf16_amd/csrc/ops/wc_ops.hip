@@ -136,10 +136,16 @@ AdapterPlan adapter_plan(uint64_t m, uint32_t n, uint32_t rank, uint32_t cols, u
 {
     AdapterPlan p{};
     p.rank_pad = (rank + 31) / 32 * 32;
-    // one launch where all blocks' reading of A from the caches costs less
-    // than the second launch: at most 16 MiB, a block per 1,024 to 4,096 rows
+    // one launch where reading A again costs less than the second launch: at
+    // most 256 KiB of A for a block, which waits for them, and 16 MiB for all,
+    // a block per 1,024 to 4,096 rows.  us in one launch and in two, FP32 y,
+    // 4096 x 4096, one token of rank 16 (128 KiB) 10.7 and 15.4, of 32 13.0 and
+    // 15.1, of 48 18.0 and 14.7, of 64 23 and 14.7; 64 tokens of rank 16 (8 MiB)
+    // 14.3 and 17.5; 512 x 4096, one of rank 64 (64 KiB) 10.7 and 14.8; 4096 x
+    // 14336, 32 tokens of rank 16 in 16 MiB 14.5, in 56 MiB 21.1, and 21.4.
+    // Ranks over 64 would not leave k_adapters_few registers.
     const uint64_t reading = m * rank * cols * 2, pairs = ceil_div(ceil_div(m, 16) * (m < 16 ? m : 16), 8) * 8;
-    for (uint32_t r = 1024; r <= 4096 && rank <= 64 && m <= 64 && !p.few; r *= 2) {
+    for (uint32_t r = 1024; r <= 4096 && rank <= 64 && m <= 64 && 2ull * rank * cols <= (256u << 10) && !p.few; r *= 2) {
         p.row_block = r;
         p.row_blocks = (uint32_t)ceil_div(rows, r);
         p.few = reading * p.row_blocks <= (16ull << 20) && pairs * p.row_blocks <= max_blocks(1024);

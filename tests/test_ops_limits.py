@@ -31,3 +31,12 @@ def test_refusals_past_the_limits():
     e = B.wc_moe(0x10000, 8, 0x20000, 0x30000, 0x40000, 0x50000, 1 << 21, 8, 1 << 21, 1 << 18, 0x60000, 8, 64, 1024, 16, 8,
                  1 << 18, B.WC_T_BF16, 1)
     assert lib.wc_moe_layer(e, 0x100000, 1 << 50, None) == B.WC_ERR_ARG
+
+
+def test_adapters_in_one_launch_need_no_scratch():
+    """One launch where a block reads at most 256 KiB of A, and all of them 16 MiB."""
+    lib = wc.lib()
+    for m, rank, cols, rows, one in ((1, 16, 4096, 4096, True), (1, 32, 4096, 4096, True), (1, 33, 4096, 4096, False),
+                                     (1, 64, 2048, 4096, True), (1, 64, 2056, 4096, False), (64, 16, 4096, 4096, True),
+                                     (64, 16, 4096, 14336, False), (65, 16, 64, 64, False), (1, 65, 64, 64, False)):
+        assert (lib.wc_add_adapters_scratch(m, rank, cols, rows) == 0) == one, (m, rank, cols, rows)

@@ -174,7 +174,8 @@ AdapterPlan adapter_plan(uint64_t m, uint32_t n, uint32_t rank, uint32_t cols, u
     if (splits > 8) splits = 8;
     p.split_cols = (uint32_t)(ceil_div(most, splits) * step);
     p.splits = (uint32_t)ceil_div(cols, p.split_cols);
-    // k_adapters_up_many takes 128 tokens and 64 rows at a time, k_adapters_up 16 and 256
+    // k_adapters_up_many takes 128 tokens and 64 rows at a time, k_adapters_up
+    // 16 and 256; the former has registers for the terms of 64 ranks, no more
     const bool wide = many && rank <= 64;
     p.up_tile = wide ? 128 : 16;
     p.up_tiles = ceil_div(m, p.up_tile);
@@ -303,7 +304,11 @@ MoePlan moe_plan(uint32_t m, uint32_t experts, uint32_t top_k, uint32_t cols, ui
     p.route_splits = (uint32_t)ceil_div(steps, p.route_steps);
     p.slots = m * top_k < experts ? m * top_k : experts;
     p.up_tiles = (inner + 15) / 16;
-    // a wave for twice 16 rows of W2, or four where that gives too few blocks
+    // a wave for twice 16 rows of W2, or four where that gives too few blocks.
+    // us of a layer with one and with four, BF16, blocks of one: 256 (13 tokens
+    // on 8 experts of 4096 x 14336) 469 and 426; 512 (16 tokens, 32 of 2048 x
+    // 2048) 160 and 147, but (64 tokens, 32 of 2048 x 1024) 95 and 103; 1024 (64
+    // of 2048 x 1024) 162 and 183; 2048 (64 of 4096 x 1536) 400 and 447
     p.split = (uint64_t)p.slots * ceil_div(cols, 128) < 4 * kCus;
     p.down_tiles = (uint32_t)ceil_div(cols, p.split ? 32 : 128);
     uint64_t at = 0;

@@ -10,7 +10,7 @@ from __future__ import annotations
 
 import torch
 from torch.autograd import forward_ad
-from torch.autograd.graph import increment_version as written  # what autograd has to know of a tensor written in place
+from torch.autograd.graph import increment_version
 
 from . import _binding as B
 
@@ -92,6 +92,15 @@ def no_tangents(what: str, *tensors):
     """Raises where a tensor carries a forward-mode tangent, which the call would drop."""
     if any(t is not None and forward_ad.unpack_dual(t).tangent is not None for t in tensors):
         raise RuntimeError(f"{what} has no forward-mode derivative")
+
+
+_increment_version = getattr(torch._C, "_increment_version", None) or (lambda tensors: increment_version(*tensors))
+
+
+def written(t: torch.Tensor):
+    """What autograd has to know of a tensor that a call writes in place.  (increment_version without its own check
+    of a type, half of its time.)"""
+    _increment_version((t,))
 
 
 def error_word(check: bool, device):

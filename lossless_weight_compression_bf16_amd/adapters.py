@@ -80,16 +80,17 @@ def add_adapters(x: torch.Tensor, y: torch.Tensor, a: torch.Tensor, b: torch.Ten
         nbytes = lib.wc_add_adapters_scratch(m, rank, cols, rows)
         scratch = torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
         err = _ops.error_word(check, dev)
-        g = B.wc_adapters(z.data_ptr(), z.stride(0), y.data_ptr(), y.stride(0), a.data_ptr(), b.data_ptr(),
-                          i.data_ptr(), s.data_ptr() if s is not None else 0, m, n, rank, cols, rows,
-                          _ops.TYPES[dtype], _ops.TYPES[y_type])
+        (z_row, _), (y_row, _) = z.stride(), y.stride()
+        g = B.wc_adapters(z.data_ptr(), z_row, y.data_ptr(), y_row, a.data_ptr(), b.data_ptr(), i.data_ptr(),
+                          s.data_ptr() if s is not None else 0, m, n, rank, cols, rows, _ops.TYPES[dtype],
+                          _ops.TYPES[y_type])
         _ops.written(y)
-        where = scratch.data_ptr() if nbytes else 0, nbytes, err.data_ptr() if check else 0, raw
-        rc = lib.wc_add_adapters(g, *where)
+        room, word = scratch.data_ptr() if nbytes else 0, err.data_ptr() if check else 0
+        rc = lib.wc_add_adapters(g, room, nbytes, word, raw)
         if rc == B.WC_ERR_ARG and _ops.may_overlap(z, y):  # y in x's memory: from a copy of x
             z = z.clone(memory_format=torch.contiguous_format)
             g.x, g.x_stride = z.data_ptr(), cols
-            rc = lib.wc_add_adapters(g, *where)
+            rc = lib.wc_add_adapters(g, room, nbytes, word, raw)
         _ops.done(rc, err, "add_adapters")
         return y
 

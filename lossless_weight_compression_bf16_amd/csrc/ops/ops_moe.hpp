@@ -251,15 +251,20 @@ struct MoeSet {
     }
 };
 
-// acc[m][t] += W_m X_t over columns c0 .. c1 (multiples of 8) for M matrices
+// acc[m][0][t] += W_m X_t over columns c0 .. c1 (multiples of 8) for M matrices
 // of 16 rows and NT tiles of 16 tokens, whose numbers are 16-bit or, with
 // kTerms, fp32 and taken as terms of scale[t] times them.  weights[m]: the
 // first row; row(r): elements from there to row r; tokens(t): the lane's
-// column.  Loads past the end repeat the last 8 columns, and the operands are
+// column.  acc[m][1][t] takes all terms but the first, so that these small
+// products are not rounded to the large sum each time (of 64 tokens' results,
+// 24 experts of 2048 x 7168, BF16, 0.05% are not the nearest number to the
+// exact one, 0.07% with one sum; 13 tokens, 8 of 14336 x 4096, FP16, 0.39% and
+// 0.46%; products and sums of fp32 numbers give 0.17% and 0.89%).  Loads past the end repeat the last 8 columns, and the operands are
 // zero there.  The next columns are on their way while these are multiplied.
 template <int T, int M, bool kTerms, int NT, class Row, class Tokens>
 __device__ __forceinline__ void strip_product(const uint16_t *const (&weights)[M], Row row, Tokens tokens, uint32_t c0,
-                                              uint32_t c1, Strip *strips, const float (&scale)[NT], f32x4 (&acc)[M][NT])
+                                              uint32_t c1, Strip *strips, const float (&scale)[NT],
+                                              f32x4 (&acc)[M][kTerms ? 2 : 1][NT])
 {
     using Ty = Type<T>;
     using X8 = typename Ty::x8;
@@ -330,7 +335,7 @@ __device__ __forceinline__ void strip_product(const uint16_t *const (&weights)[M
 #pragma unroll
                     for (int o = C - 1; o >= 0; o--)
 #pragma unroll
-                        for (int m = 0; m < M; m++) acc[m][t] = Ty::mfma(a[m], b[o], acc[m][t]);
+                        for (int m = 0; m < M; m++) acc[m][o ? 1 : 0][t] = Ty::mfma(a[m], b[o], acc[m][o ? 1 : 0][t]);
                 }
             }
         }
@@ -349,18 +354,18 @@ __device__ __forceinline__ void moe_up_rows(const MoeArgs &g, uint32_t expert, u
     const uint64_t at = (uint64_t)expert * g.up_expert + (uint64_t)n0 * g.up_row;
     const uint16_t *const weights[2] = {g.w1 + at, g.w3 + at};
     const uint32_t rows = min(g.inner - n0, 16u), stride = (uint32_t)g.up_row;
-    f32x4 acc[2][NT];
+    f32x4 acc[2][1][NT];
     const float scale[NT] = {};  // of no use here
 #pragma unroll
-    for (int t = 0; t < NT; t++) acc[0][t] = acc[1][t] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int t = 0; t < NT; t++) acc[0][0][t] = acc[1][0][t] = f32x4{0.f, 0.f, 0.f, 0.f};
     strip_product<T, 2, false, NT>(
         weights, [&](uint32_t r) { return min(r, rows - 1) * stride; },
         [&](int t) { return g.x + (uint64_t)((uint32_t)place[min(16 * t + i, count - 1)] / g.top_k) * g.x_stride; },
         c0, c1, strips, scale, acc);
 #pragma unroll
     for (int t = 0; t < NT; t++) {
-        gate[t] = acc[0][t];
-        up[t] = acc[1][t];
+        gate[t] = acc[0][0][t];
+        up[t] = acc[1][0][t];
     }
 }
 
@@ -374,12 +379,12 @@ __device__ __forceinline__ void moe_down_rows(const MoeArgs &g, uint32_t expert,
     const uint32_t i = threadIdx.x & 15, rows = min(g.cols, 16u), stride = (uint32_t)g.down_row;
     const uint16_t *const w = g.w2 + (uint64_t)expert * g.down_expert;
     const uint16_t *const weights[2] = {w + n[0] * g.down_row, w + n[1] * g.down_row};
-    f32x4 acc[2][NT];
+    f32x4 acc[2][2][NT];
     float scale[NT], unscale[NT];
     uint32_t at[NT];
 #pragma unroll
     for (int t = 0; t < NT; t++) {
-        acc[0][t] = acc[1][t] = f32x4{0.f, 0.f, 0.f, 0.f};
+        acc[0][0][t] = acc[0][1][t] = acc[1][0][t] = acc[1][1][t] = f32x4{0.f, 0.f, 0.f, 0.f};
         at[t] = (uint32_t)place[min(16 * t + i, count - 1)];
         scale[t] = term_scale<T>(T == WC_T_FP16 ? __builtin_bit_cast(float, g.most[at[t]]) : 0.f, unscale[t]);
     }
@@ -389,7 +394,7 @@ __device__ __forceinline__ void moe_down_rows(const MoeArgs &g, uint32_t expert,
 #pragma unroll
     for (int t = 0; t < NT; t++)
 #pragma unroll
-        for (int m = 0; m < 2; m++) sum[m][t] = unscale[t] * acc[m][t];
+        for (int m = 0; m < 2; m++) sum[m][t] = unscale[t] * (acc[m][0][t] + acc[m][1][t]);
 }
 
 // The columns of one of four waves: a quarter, in multiples of `unit`.

@@ -259,8 +259,9 @@ struct MoeSet {
 // products are not rounded to the large sum each time (of 64 tokens' results,
 // 24 experts of 2048 x 7168, BF16, 0.05% are not the nearest number to the
 // exact one, 0.07% with one sum; 13 tokens, 8 of 14336 x 4096, FP16, 0.39% and
-// 0.46%; products and sums of fp32 numbers give 0.17% and 0.89%).  Loads past the end repeat the last 8 columns, and the operands are
-// zero there.  The next columns are on their way while these are multiplied.
+// 0.46%; products and sums of fp32 numbers give 0.17% and 0.89%).  Loads past
+// the end repeat the last 8 columns, and the operands are zero there.  The
+// next columns are on their way while these are multiplied.
 template <int T, int M, bool kTerms, int NT, class Row, class Tokens>
 __device__ __forceinline__ void strip_product(const uint16_t *const (&weights)[M], Row row, Tokens tokens, uint32_t c0,
                                               uint32_t c1, Strip *strips, const float (&scale)[NT],
@@ -455,6 +456,10 @@ __global__ __launch_bounds__(256, 2) void k_moe_up(MoeArgs g)
     const uint32_t count = moe_block(g, slot, set, place, expert);
     if (count == 0) return;
     wave_quarter(g.cols, kStripCols, wave, c0, c1);
+    const uint32_t c = 16 * wave + i;
+    uint32_t seen = 0;  // the largest |h| so far, or less; looked at here, where nothing waits for it
+    if (T == WC_T_FP16 && wave < TT && c < count)
+        seen = __hip_atomic_load(g.most + place[c], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     f32x4 gate[TT], up[TT];
     if (TT == 1 || count <= 16) moe_up_rows<T, 1, TT>(g, expert, n0, place, count, c0, c1, strips[wave], gate, up);
     else if (TT == 2 || count <= 32) moe_up_rows<T, 2, TT>(g, expert, n0, place, count, c0, c1, strips[wave], gate, up);
@@ -468,7 +473,7 @@ __global__ __launch_bounds__(256, 2) void k_moe_up(MoeArgs g)
         }
     }
     __syncthreads();
-    const uint32_t n = n0 + 4 * gr, c = 16 * wave + i;
+    const uint32_t n = n0 + 4 * gr;
     if (wave >= TT) return;
     float most = 0.f;
     if (c < count && n < g.inner) {
@@ -485,16 +490,13 @@ __global__ __launch_bounds__(256, 2) void k_moe_up(MoeArgs g)
         *reinterpret_cast<f32x4 *>(g.h + (uint64_t)place[c] * g.inner + n) = h;
     }
     if constexpr (T == WC_T_FP16) {
-        // A maximum does not depend on the order.  It is looked at first: few
-        // blocks raise it, and all of them raising the same few words would
-        // take longer than their weights (13 tokens on 8 wide experts: 580 us).
+        // A maximum does not depend on the order.  Few blocks raise it, and
+        // all of them raising the same few words would take longer than their
+        // weights (13 tokens on 8 wide experts: 580 us for the layer).
         most = fmaxf(most, __shfl_xor(most, 16, 64));
         most = fmaxf(most, __shfl_xor(most, 32, 64));
-        if (gr == 0 && c < count) {
-            uint32_t *const p = g.most + place[c];
-            const uint32_t bits = __builtin_bit_cast(uint32_t, most);
-            if (__hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) < bits) atomicMax(p, bits);
-        }
+        const uint32_t bits = __builtin_bit_cast(uint32_t, most);
+        if (gr == 0 && c < count && seen < bits) atomicMax(g.most + place[c], bits);
     }
 }
 

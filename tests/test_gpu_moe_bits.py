@@ -115,3 +115,21 @@ def test_an_infinite_h_is_the_infinity_of_its_sum(dev):
         w2 = torch.full((1, 8, 8), -0.5, dtype=BF)
         y = M.moe_layer(x.to(dev), torch.zeros((1, 8), dtype=BF, device=dev), w1.to(dev), w3.to(dev), w2.to(dev), 1)
         assert bool((y == -float("inf")).all())
+
+
+def test_half_precision_repeats_and_graph(dev):
+    """FP16's scaling comes from each call's own h: nothing of a call with larger h is left for the next."""
+    g = torch.Generator().manual_seed(3)
+    m, e, h, i = 40, 6, 256, 264
+    x, r, w1, w3, w2 = ((torch.randn(s, generator=g) / f).to(HF).to(dev) for s, f in (
+        ((m, h), 1.0), ((e, h), 16.0), ((e, i, h), 16.0), ((e, i, h), 16.0), ((e, h, i), 16.0)))
+    y1 = M.moe_layer(x, r, w1, w3, w2, 2)
+    assert torch.equal(M.moe_layer(x, r, w1, w3, w2, 2), y1)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        y = M.moe_layer(x, r, w1, w3, w2, 2)
+    for k, f in enumerate((1.0, 2.0 ** 10, 2.0 ** -10, 1.0, 2.0 ** -12)):
+        w3.copy_((torch.randn((e, i, h), generator=g) * f / 16).to(HF))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(y, M.moe_layer(x, r, w1, w3, w2, 2)), f"replay {k}"

@@ -439,7 +439,7 @@ __device__ __noinline__ void y_add_some(typename Type<YT>::elem *p, uint32_t gr,
 // of B at a time; u, the sum of its parts, stays in its registers, or, with
 // kBlocks blocks of 64 ranks (each with its own scaling), is read again for
 // every 64 rows, as terms.  54 tokens of 32 adapters of rank 16, 14336 rows,
-// FP32: 11.7 us (2.3 TB/s of B and y).  What bounds it is each wave's chain of
+// FP32: 11.5 us (2.2 TB/s of B and y).  What bounds it is each wave's chain of
 // waits (ids, then u, B and y at once, then the stores) over the waves that
 // fit: 256 or 1024 rows a block took 15.5 and 12.3 us, and loading the next
 // rows ahead costs registers, hence waves (16.3 us).
@@ -547,7 +547,7 @@ __global__ __launch_bounds__(256, KS == 1 ? 4 : 2) void k_adapters_up(AdapterArg
 // kernel that only streams.  y is read and written in whole lines, 64 elements
 // of a token at a time, and past the caches where it is larger than they are
 // (kStream); the products come to that order through LDS as well.  8192 tokens
-// of 16 adapters of rank 64, 14336 rows, BF16: 112 us, 4.2 TB/s of y.
+// of 16 adapters of rank 64, 14336 rows, BF16: 119 us, 3.9 TB/s of y.
 template <int T, int YT, int KS, bool kStream>
 __global__ __launch_bounds__(256, KS == 2 && (T == WC_T_FP16 || YT == WC_T_FP32) ? 2 : 3) void k_adapters_up_many(AdapterArgs g)
 {
@@ -651,7 +651,7 @@ __global__ __launch_bounds__(256, KS == 2 && (T == WC_T_FP16 || YT == WC_T_FP32)
 // columns, while its first rows of B and y are on their way.  The row blocks
 // of a tile's turn are on one XCD (blocks are dealt to the XCDs in the order
 // of their number), where A comes from the L2 cache after the first of them.
-// One token, rank 16, 4096 x 4096: 8.7 us, of which most is waiting for the
+// One token, rank 16, 4096 x 4096: 8.2 us, of which most is waiting for the
 // ids, then A and x, then the other waves; two launches took 18.3 us a call.
 // Grid: turns x tiles of 16 tokens, rounded up to 8, x row blocks.
 template <int T, int YT, int RT>

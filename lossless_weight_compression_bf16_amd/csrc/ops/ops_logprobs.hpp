@@ -447,11 +447,12 @@ __device__ __forceinline__ float given_logit(const LogprobArgs &g, uint64_t r, i
 }
 
 // One block per slice of a row; with one slice it writes the row.  Many rows:
-// reading them is the bound (2048 rows of 128256 in BF16, 5 best: 93 us a call,
-// 5.7 TB/s; 7.1 is what reading alone reaches), and 256 threads a row leave
-// room for the blocks that hide one another's choice of the best.  Few rows:
-// the passes over a row by its one block, for which 1024 threads are there
-// (64 rows, 20 best: 16 us; one row of 50257, FP32: 9.6 us).
+// reading them is the bound (2048 rows of 128256 in BF16, 5 best: 94 us a call
+// in a row of calls, 5.6 TB/s, 101 under a kernel trace; 7.1 is what reading
+// alone reaches), and 256 threads a row leave room for the blocks that hide
+// one another's choice of the best.  Few rows: the passes over a row by its one
+// block, for which 1024 threads are there (64 rows, 20 best: 17 us; one row of
+// 50257, FP32: 9.8 us).
 template <int T, bool kTop, int NT>
 __global__ __launch_bounds__(NT) void k_logprobs(LogprobArgs g)
 {
@@ -524,8 +525,8 @@ __global__ __launch_bounds__(kJoinThreads) void k_logprobs_join(LogprobArgs g)
 // and writes every logit once; a thread takes 32 of them per round.  Every
 // element is read and written by one thread, the read first, so dz may be
 // the logits' own memory.  Reading and writing is the bound: 2048 rows of
-// 128256 in BF16, masked, 181 us, 5.8 TB/s of both, where a plain copy of as
-// much reaches 4.8; 100 rows of 50257 in FP32 10.3 us.
+// 128256 in BF16, masked, 180 us, 5.8 TB/s of both, where a copy of as much
+// reaches 6.5; 100 rows of 50257 in FP32 10.4 us.
 //
 // log p_j = z_j - lse; an lse of 2^16 or more (a row of nothing but the
 // type's lowest value, say) has no bits left for the probabilities in 32

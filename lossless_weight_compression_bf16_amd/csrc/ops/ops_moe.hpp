@@ -439,8 +439,8 @@ __device__ __forceinline__ uint32_t moe_block(const MoeArgs &g, uint32_t slot, M
 
 // h of 16 inner rows of one expert.  Grid: slots x inner / 16.  Columns over
 // the four waves.  Reading W1 and W3 is the bound: 64 tokens, 256 experts of
-// 2048 x 7168, 1.91 ms, 13 tokens, 8 of 14336 x 4096, 270 us, 6.9 TB/s both
-// times.  Operands straight from memory, 64 bytes of each of 16 rows at a time,
+// 2048 x 7168, 1.90 ms, 6.9 TB/s; 13 tokens, 8 of 14336 x 4096, FP16, 282 us,
+// 6.7 TB/s.  Operands straight from memory, 64 bytes of each of 16 rows at a time,
 // took 4.5 ms for the former's whole layer where this takes 2.9.
 template <int T, int TT>
 __global__ __launch_bounds__(256, 2) void k_moe_up(MoeArgs g)
@@ -504,12 +504,14 @@ __global__ __launch_bounds__(256, 2) void k_moe_up(MoeArgs g)
 // columns / 128 (kSplit: / 32).  A wave has twice 16 rows of W2 of its own, or
 // with kSplit, where blocks would be too few, a quarter of their inner rows.
 // Where the last 16 rows would run past the end they begin earlier: those that
-// two waves have come out the same.  Reading W2 is the bound: the
-// same two layers, 940 us (6.9 TB/s) and 149 us (6.3).  With 16 rows a wave
-// h was as many lines on their way into the L1 cache as the rows, and more for
-// 13 tokens: 1075 and 181 us.  Making h's terms costs where an expert has more
-// than 32 tokens: 64 tokens on 2 experts of 14336 x 4096, BF16, 388 us for the
-// layer, 338 with h rounded to two BF16 terms by the first product.
+// two waves have come out the same.  Reading W2 is the bound, and making the
+// terms of h beside it (5% of the first): the same two layers, 991 us (6.6
+// TB/s) and 164 us (5.7).  Where an expert has more than 32 tokens the terms
+// cost more: 64 tokens on 2 experts of 14336 x 4096, BF16, 385 us for the
+// layer, 338 with h rounded to two BF16 terms by the first product.  With 16
+// rows a wave h is as many lines on their way into the L1 cache as the rows,
+// and more for 13 tokens: with those two terms 1075 us, against 940 with 32
+// rows, and 181 against 149.
 template <int T, int TT, bool kSplit>
 __global__ __launch_bounds__(256, 2) void k_moe_down(MoeArgs g)
 {
@@ -579,7 +581,7 @@ __global__ __launch_bounds__(64) void k_moe_join(MoeArgs g)
 // reads whole rows, 512 columns at a time, eight of a lane, and multiplies them
 // in fp32 with a vector that stays in registers; h stays in fp32.  A block of
 // the second product has all of the token's experts, so that no launch joins
-// them.  8 of 64 experts of 1024 x 2048: 14.3 + 7.8 us (4.7 and 4.3 TB/s)
+// them.  8 of 64 experts of 1024 x 2048: 14.4 + 8.0 us (4.7 and 4.2 TB/s)
 // where the three kernels above take 15.1 + 11.4 + 3.9; 2 of 8 experts of
 // 14336 x 4096, where reading is all there is, 130 us for the layer and 126.
 

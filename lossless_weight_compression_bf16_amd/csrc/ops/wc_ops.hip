@@ -101,7 +101,9 @@ template <int T>
 void launch_grad(LogprobGradArgs g, uint64_t m, hipStream_t stream)
 {
     const uintptr_t es = type_bytes(T);
-    // past the caches where the logits do not fit into the last of them (256 MiB)
+    // past the caches where logits and gradient do not fit into the last of them
+    // (256 MiB); us through them and past them, MiB of logits: 19 11.6 and 12.4,
+    // 48 21.7 and 22.3, 125 49.3 both, 171 73 and 65, 502 192 and 180
     const bool large = m * g.vocab * es > (128ull << 20);
     const uint64_t most = max_blocks(kGradThreads) / g.blocks;
     while (m) {
@@ -151,9 +153,9 @@ AdapterPlan adapter_plan(uint64_t m, uint32_t n, uint32_t rank, uint32_t cols, u
         p.few = reading * p.row_blocks <= (16ull << 20) && pairs * p.row_blocks <= max_blocks(1024);
     }
     // a tile of 128 tokens has few adapters, and the blocks of turns that it
-    // does not have cost little: us for one turn and three, rank 64, 8192
-    // tokens, 14336 rows: of 1 adapter 135 and 138, of 16 167 and 154, of 128
-    // 293 and 240
+    // does not have cost little: us for one turn and three, BF16, rank 64, 8192
+    // tokens, 14336 rows: of 1 adapter 138 both, of 16 164 and 155, of 128 353
+    // and 239
     p.turns = many ? (n < 1 ? 1 : n < 3 ? n : 3) : (uint32_t)(m < 16 ? m : 16);
     if (p.few) {
         p.tile = p.up_tile = 16;
@@ -195,9 +197,9 @@ AdapterPlan adapter_plan(uint64_t m, uint32_t n, uint32_t rank, uint32_t cols, u
 // Tiles of 128 tokens: where the tokens are many and an adapter has 64 of them
 // or more (their number is the host's only word on how long its runs are: a
 // tile of 128 takes its adapters three at a time).  us a call, tiles of 16 and
-// of 128, 4096 x 4096: rank 64, 256 tokens of 2 adapters 35 and 22, 2048 of 8
-// 54 and 41, of 32 73 and 64, of 64 83 and 90; rank 16, 1024 tokens of 16 28
-// and 29, of 32 28 and 34, of 64 29 and 46.
+// of 128, BF16, 4096 x 4096: rank 64, 256 tokens of 2 adapters 35 and 22, 2048
+// of 8 55 and 41, of 32 79 and 59, of 64 82 and 86; rank 16, 1024 tokens of 16
+// 26 and 29, of 32 26 and 30, of 64 24 and 42.
 bool many_tokens(uint64_t m, uint32_t n) { return m >= 256 && m >= 64ull * n; }
 
 // Tokens of one set of launches: no grid of theirs comes near max_blocks
@@ -234,7 +236,9 @@ template <int T, int YT>
 void launch_up(const AdapterArgs &g, const AdapterPlan &p, hipStream_t stream)
 {
     const dim3 grid((uint32_t)(p.up_tiles * p.row_blocks), 1, p.turns), block(256);
-    const bool large = g.m * g.rows * type_bytes(YT) > (128ull << 20);  // y does not stay in the caches
+    // past the caches where y does not stay in them; us through them and past
+    // them, MiB of y: 64 60 and 65, 112 71 both, 128 83.6 and 82.9, 224 142 and 137
+    const bool large = g.m * g.rows * type_bytes(YT) > (128ull << 20);
     if (p.up_tile == 128 && g.rank <= 32) {
         if (large) hipLaunchKernelGGL((k_adapters_up_many<T, YT, 1, true>), grid, block, 0, stream, g);
         else hipLaunchKernelGGL((k_adapters_up_many<T, YT, 1, false>), grid, block, 0, stream, g);

@@ -94,6 +94,9 @@ def moe_layer(x: torch.Tensor, router: torch.Tensor, w1: torch.Tensor, w3: torch
         if out is not None:
             _ops.written(out)
         nbytes = lib.wc_moe_layer_scratch(m, experts, top_k, cols, inner)
+        if m and not nbytes:
+            raise ValueError(f"experts with tokens (at most {min(m * top_k, experts)}) times inner must be below 2^28, "
+                             f"got inner {inner}")
         scratch = torch.empty(nbytes, dtype=torch.uint8, device=dev)
         up, down = w1.stride(), w2.stride()
         g = B.wc_moe(z.data_ptr(), z.stride(0), r.data_ptr(), w1.data_ptr(), w3.data_ptr(), w2.data_ptr(),

@@ -40,3 +40,17 @@ def test_adapters_in_one_launch_need_no_scratch():
                                      (1, 64, 2048, 4096, True), (1, 64, 2056, 4096, False), (64, 16, 4096, 4096, True),
                                      (64, 16, 4096, 14336, False), (65, 16, 64, 64, False), (1, 65, 64, 64, False)):
         assert (lib.wc_add_adapters_scratch(m, rank, cols, rows) == 0) == one, (m, rank, cols, rows)
+
+
+@pytest.mark.gpu
+def test_experts_past_the_limit():
+    if not torch.cuda.is_available():
+        pytest.skip("no HIP device")
+    from lossless_weight_compression_bf16_amd.moe import moe_layer
+    bf, inner = torch.bfloat16, 1 << 18
+    x, r = torch.zeros((64, 8), dtype=bf, device="cuda"), torch.zeros((1024, 8), dtype=bf, device="cuda")
+    up = torch.zeros((1, inner, 8), dtype=bf, device="cuda").expand(1024, inner, 8)
+    down = torch.zeros((1, 8, inner), dtype=bf, device="cuda").expand(1024, 8, inner)
+    with pytest.raises(ValueError, match="below 2\\^28"):
+        moe_layer(x, r, up, up, down, 16)
+    assert moe_layer(x, r, up[:, :1024], up[:, :1024], down[:, :, :1024], 2).shape == x.shape

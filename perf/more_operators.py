@@ -1,7 +1,8 @@
-"""Cases of the operators that a training step, or the scoring of answers,
-takes beside the weights: matrix products grouped by expert over ragged rows
-with their gradients, and the cross entropy of a large vocabulary from hidden
-states, without logits in memory, with its gradients.
+"""Cases of products with a model's weights that leave nothing large in
+memory between them and what stands before or after them: products grouped by
+expert over ragged rows with their gradients, the cross entropy of a large
+vocabulary from hidden states, without logits, with its gradients, and
+products of few rows with weights of 4 bits and group scales.
 
 ``listed`` gives the cases, ``prepare`` what a program has in hand before a
 call, ``run`` one pass (the plain form in elementary torch operations, or with
@@ -32,9 +33,6 @@ def listed():
         # prompts on the 256 experts of 7168 x 2048 that the benchmark compresses; a buffer of fixed size, not filled
         {"name": "grouped-prompts", "op": "grouped", "tokens": 4096, "experts": 256, "top_k": 8, "cols": 7168, "rows": 2048,
          "dtype": "bf16", "padded": True},
-        # long prompts on few wide experts
-        {"name": "grouped-long", "op": "grouped", "tokens": 8192, "experts": 8, "top_k": 2, "cols": 4096, "rows": 14336,
-         "dtype": "bf16", "padded": False},
         # a short fine-tuning step on small experts
         {"name": "grouped-gradient-short", "op": "grouped_gradient", "tokens": 301, "experts": 16, "top_k": 2, "cols": 768,
          "rows": 2304, "dtype": "fp16", "padded": True},
@@ -50,12 +48,13 @@ def listed():
         # a short fine-tuning step of a small model, in half precision with a scaled loss
         {"name": "loss-gradient-short", "op": "loss_gradient", "m": 100, "vocab": 50257, "cols": 768, "dtype": "fp16",
          "penalty": False},
-        # a small batch on a long row of hidden values
-        {"name": "loss-gradient-small", "op": "loss_gradient", "m": 509, "vocab": 32001, "cols": 7168, "dtype": "bf16",
-         "penalty": True},
         # a whole fine-tuning batch, with a penalty on the size of the logits (a gradient of lse)
         {"name": "loss-gradient-batch", "op": "loss_gradient", "m": 4096, "vocab": 128256, "cols": 4096, "dtype": "bf16",
          "penalty": True},
+        # one new token through a projection of 4096 x 4096 held in 4 bits, where latency counts
+        {"name": "4bit-1-token", "op": "4bit", "m": 1, "rows": 4096, "cols": 4096, "group": 64, "dtype": "bf16", "zeros": False},
+        # a serving batch through a wide projection, with zero points
+        {"name": "4bit-batch", "op": "4bit", "m": 61, "rows": 14336, "cols": 4096, "group": 128, "dtype": "fp16", "zeros": True},
     ]
 
 
@@ -66,7 +65,11 @@ def _spread(rng, low, high, step=1):
 
 
 def draw(rng):
-    op = rng.choice(["grouped", "grouped_gradient", "loss", "loss_gradient"])
+    op = rng.choice(["grouped", "grouped_gradient", "loss", "loss_gradient", "4bit"])
+    if op == "4bit":
+        group = rng.choice([32, 64, 128])
+        return {"op": op, "m": _spread(rng, 1, 64), "rows": _spread(rng, 256, 14336), "cols": _spread(rng, 256, 14336, group),
+                "group": group, "dtype": rng.choice(["bf16", "fp16"]), "zeros": rng.random() < 0.5}
     if op.startswith("grouped"):
         cols, rows, top_k = _spread(rng, 256, 7168, 8), _spread(rng, 256, 14336, 8), _spread(rng, 1, 8)
         experts = _spread(rng, top_k, max(top_k, min(256, (7 << 29) // (cols * rows))))
@@ -91,7 +94,7 @@ def _normal(g, shape, std, dtype):
 def prepare(case, seed):
     g = torch.Generator(device="cuda")
     g.manual_seed(seed)
-    make = _prepare_grouped if case["op"].startswith("grouped") else _prepare_loss
+    make = {"g": _prepare_grouped, "l": _prepare_loss, "4": _prepare_4bit}[case["op"][0]]
     return {"case": case, **make(case, g)}
 
 
@@ -135,6 +138,20 @@ def _prepare_loss(case, g):
     return s
 
 
+def _prepare_4bit(case, g):
+    m, rows, cols, group, dtype = (case[f] for f in ("m", "rows", "cols", "group", "dtype"))
+    groups = cols // group
+    # normal weights in 16 steps of a third of their deviation, which differs from group to group
+    steps = torch.empty((rows, cols), device="cuda").normal_(0.0, 3.0, generator=g).round_()
+    zeros = torch.full((rows, groups), 8.0, device="cuda")
+    if case["zeros"]:
+        zeros += torch.randint(-2, 3, (rows, groups), generator=g, device="cuda")
+    q = (steps.view(rows, groups, group) + zeros[..., None]).clamp_(0, 15).to(torch.uint8).view(rows, cols)
+    scales = (0.5 + torch.rand((rows, groups), generator=g, device="cuda")) / (3 * math.sqrt(cols))
+    return {"x": _normal(g, (m, cols), 1.0, dtype), "q": q[:, ::2] | (q[:, 1::2] << 4), "scales": scales.to(TYPES[dtype]),
+            "zeros": zeros.to(TYPES[dtype]) if case["zeros"] else None}
+
+
 def _lse64(h, w):
     step, w = max(1, (1 << 27) // w.shape[0]), w.double()
     return torch.cat([torch.logsumexp(part.double() @ w.T, 1) for part in h.split(step)])
@@ -144,7 +161,7 @@ def _lse64(h, w):
 
 def run(state):
     return {"grouped": _run_grouped, "grouped_gradient": _run_grouped_gradient, "loss": _run_loss,
-            "loss_gradient": _run_loss_gradient}[state["case"]["op"]](state)
+            "loss_gradient": _run_loss_gradient, "4bit": _run_4bit}[state["case"]["op"]](state)
 
 
 def _padded(s, t):
@@ -208,6 +225,18 @@ def _run_loss_gradient(s):
     return (g @ w).to(s["hidden"].dtype), (g.T @ h).to(s["weight"].dtype)
 
 
+def _run_4bit(s):
+    group = s["case"]["group"]
+    if own:
+        from lossless_weight_compression_bf16_amd import fourbit
+        return fourbit.linear4(s["x"], fourbit.Weights4(s["q"], s["scales"], s["zeros"], group))
+    rows, groups = s["scales"].shape
+    q = torch.stack([s["q"] & 15, s["q"] >> 4], 2).view(rows, groups, group).float()
+    zeros = 8.0 if s["zeros"] is None else s["zeros"].float()[..., None]
+    w = ((q - zeros) * s["scales"].float()[..., None]).view(rows, -1)
+    return (s["x"].float() @ w.T).to(s["x"].dtype)
+
+
 # ------------------------------------------------------- what it cannot do without
 
 def work(case):
@@ -218,6 +247,10 @@ def work(case):
             return {"bytes": 2.0 * (used * cols + m * rows + hit * rows * cols) + 8 * e, "flops": 2.0 * used * rows * cols}
         return {"bytes": 2.0 * (used * (cols + rows) + m * cols + (hit + e) * rows * cols) + 8 * e,
                 "flops": 4.0 * used * rows * cols}
+    if case["op"] == "4bit":
+        m, rows, cols = case["m"], case["rows"], case["cols"]
+        per_group = 4.0 if case["zeros"] else 2.0
+        return {"bytes": rows * cols * (0.5 + per_group / case["group"]) + 2.0 * m * (rows + cols), "flops": 2.0 * m * rows * cols}
     m, v, cols = case["m"], case["vocab"], case["cols"]
     if case["op"] == "loss":
         return {"bytes": 2.0 * cols * (m + v) + 16 * m, "flops": 2.0 * m * v * cols}
@@ -229,7 +262,7 @@ def work(case):
 def exact(case, seed):
     s = prepare(case, seed)
     return {"grouped": _exact_grouped, "grouped_gradient": _exact_grouped_gradient, "loss": _exact_loss,
-            "loss_gradient": _exact_loss_gradient}[case["op"]](s)
+            "loss_gradient": _exact_loss_gradient, "4bit": _exact_4bit}[case["op"]](s)
 
 
 def _experts(s):
@@ -281,3 +314,15 @@ def _exact_loss_gradient(s):
         dh[at] = g @ w
         dw += g.T @ part
     return dh, dw
+
+
+def _exact_4bit(s):
+    group, x = s["case"]["group"], s["x"].double()
+    y = torch.zeros((x.shape[0], s["q"].shape[0]), dtype=torch.float64, device="cuda")
+    for i in range(s["scales"].shape[1]):  # a group of columns at a time
+        at = slice(i * group // 2, (i + 1) * group // 2)
+        zero = 8.0 if s["zeros"] is None else s["zeros"][:, i].double()
+        part = x[:, i * group:(i + 1) * group]
+        low, high = (s["q"][:, at] % 16).double(), (s["q"][:, at] // 16).double()
+        y += s["scales"][:, i].double() * (part[:, ::2] @ low.T + part[:, 1::2] @ high.T - zero * part.sum(1, keepdim=True))
+    return y

@@ -487,6 +487,132 @@ uint64_t wc_moe_layer_scratch(uint64_t m, uint32_t experts, uint32_t top_k, uint
  * not overlap x. */
 wc_status wc_moe_layer(const wc_moe *a, void *d_scratch, uint64_t scratch_bytes, hipStream_t stream);
 
+/* Matrix products grouped by expert over ragged rows, as in a mixture-of-
+ * experts layer whose rows have been sorted by expert: with lo_e = ends[e - 1]
+ * (0 for the first) and hi_e = ends[e],
+ *   y_r = W_e x_r  for lo_e <= r < hi_e,
+ * rounded once to `type`.  An expert may have no rows; its weights are not read.
+ * Rows behind the last expert's (ends[experts - 1] <= r < m) are not read;
+ * their y is left as it is, or zeros with zero_rest.  Ends that go back or
+ * past m: WC_EF_BAD_INDEX, and y undefined. */
+typedef struct {
+    const void *x;          /* m x cols, rows x_stride elements apart */
+    uint64_t x_stride;      /* all rows 16-byte aligned, strides multiples of 8 below 2^22 */
+    const void *w;          /* experts x rows x cols */
+    uint64_t w_expert;      /* elements from one expert to the next: a multiple of 8 */
+    uint64_t w_row;
+    const int64_t *ends;    /* experts, on the device */
+    void *y;                /* m x rows; no memory in common with x or w */
+    uint64_t y_stride;
+    uint64_t m;             /* below 2^31 */
+    uint32_t experts;       /* 1 .. 1024 */
+    uint32_t rows;          /* multiples of 8, at most 2^20 */
+    uint32_t cols;
+    uint32_t type;          /* WC_T_BF16 or WC_T_FP16: of x, w and y */
+    uint32_t zero_rest;
+    uint32_t reserved;
+} wc_grouped;
+
+/* Bytes of scratch that wc_grouped_linear needs (0 for many sizes, and for
+ * those that it rejects).  Pure host function. */
+uint64_t wc_grouped_linear_scratch(uint64_t m, uint32_t experts, uint32_t rows, uint32_t cols);
+
+/* d_scratch: 16-byte aligned; its contents need no preparation.  Sizes with
+ * (m / 128 + experts) ceil(rows / 32) or the like past 2^20 are rejected. */
+wc_status wc_grouped_linear(const wc_grouped *a, void *d_scratch, uint64_t scratch_bytes, uint32_t *d_err,
+                            hipStream_t stream);
+
+/* Its gradients from grad, the gradient of y:
+ *   grad_x_r = W_e^T grad_r,   grad_w_e = sum of grad_r x_r^T over the expert's rows
+ * each rounded once.  Either may be NULL.  grad_w of an expert without rows is
+ * zero; grad and x of rows behind the last expert's are not read, and grad_x of
+ * them is left as it is, or zeros with zero_rest. */
+typedef struct {
+    const void *x;          /* as above; may be NULL without grad_w */
+    uint64_t x_stride;
+    const void *w;          /* may be NULL without grad_x */
+    uint64_t w_expert;
+    uint64_t w_row;
+    const int64_t *ends;
+    const void *grad;       /* m x rows */
+    uint64_t grad_stride;
+    void *grad_x;           /* m x cols, or NULL; no memory in common with the inputs */
+    uint64_t grad_x_stride;
+    void *grad_w;           /* experts x rows x cols, contiguous, or NULL */
+    uint64_t m;
+    uint32_t experts;
+    uint32_t rows;
+    uint32_t cols;
+    uint32_t type;
+    uint32_t zero_rest;
+    uint32_t reserved;
+} wc_grouped_grad;
+
+uint64_t wc_grouped_linear_backward_scratch(uint64_t m, uint32_t experts, uint32_t rows, uint32_t cols);
+
+wc_status wc_grouped_linear_backward(const wc_grouped_grad *a, void *d_scratch, uint64_t scratch_bytes, uint32_t *d_err,
+                                     hipStream_t stream);
+
+/* Softmax cross entropy of given tokens from hidden states, over a large
+ * vocabulary, without the logits in memory: with z = H W^T (products of 16-bit
+ * numbers, summed in fp32, not rounded),
+ *   lse_r = log sum_v exp z_rv,   loss_r = lse_r - z_rt,  t = tokens[r].
+ * Token -1: loss 0; another token outside [0, vocab): loss NaN and
+ * WC_EF_BAD_INDEX.  A logit of NaN or +inf makes its row NaN; a row of nothing
+ * but -inf has lse -inf and loss +inf. */
+typedef struct {
+    const void *hidden;     /* m x cols; rows 16-byte aligned, strides multiples of 8 below 2^22 */
+    uint64_t hidden_stride;
+    const void *weight;     /* vocab x cols */
+    uint64_t weight_stride;
+    const int64_t *tokens;  /* m */
+    uint64_t m;             /* at most 2^19 */
+    uint32_t vocab;         /* 1 .. 2^22 */
+    uint32_t cols;          /* a multiple of 8, at most 2^20 */
+    uint32_t type;          /* WC_T_BF16 or WC_T_FP16: of hidden and weight */
+    uint32_t reserved;
+    float *loss;            /* m each */
+    float *lse;
+} wc_linear_loss;
+
+uint64_t wc_linear_cross_entropy_scratch(uint64_t m, uint32_t vocab, uint32_t cols);
+
+/* d_scratch: 256-byte aligned; its contents need no preparation. */
+wc_status wc_linear_cross_entropy(const wc_linear_loss *a, void *d_scratch, uint64_t scratch_bytes, uint32_t *d_err,
+                                  hipStream_t stream);
+
+/* Its gradients from those of loss and lse (either may be NULL: zero):
+ *   G_rv = (grad_loss_r + grad_lse_r) exp(z_rv - lse_r) - grad_loss_r [v = t_r],
+ *   grad_hidden = G W,   grad_weight = G^T H
+ * with grad_loss_r = 0 for tokens outside [0, vocab).  G is rounded to `type`
+ * once, the products' sums are fp32, and each result is rounded once.  G is
+ * made for a piece of the vocabulary at a time, at most 2^27 numbers.  A row
+ * without a part (both gradients 0, or lse -inf) has none, whatever its
+ * hidden values are.  Either result may be NULL. */
+typedef struct {
+    const void *hidden;       /* as above */
+    uint64_t hidden_stride;
+    const void *weight;
+    uint64_t weight_stride;
+    const int64_t *tokens;    /* m each */
+    const float *lse;
+    const float *grad_loss;   /* may be NULL */
+    const float *grad_lse;    /* may be NULL */
+    void *grad_hidden;        /* m x cols, or NULL; no memory in common with the inputs */
+    uint64_t grad_hidden_stride;
+    void *grad_weight;        /* vocab x cols, contiguous, or NULL */
+    uint64_t m;               /* 1 .. 2^19 */
+    uint32_t vocab;
+    uint32_t cols;
+    uint32_t type;
+    uint32_t reserved;
+} wc_linear_loss_grad;
+
+uint64_t wc_linear_cross_entropy_backward_scratch(uint64_t m, uint32_t vocab, uint32_t cols);
+
+wc_status wc_linear_cross_entropy_backward(const wc_linear_loss_grad *a, void *d_scratch, uint64_t scratch_bytes,
+                                           uint32_t *d_err, hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

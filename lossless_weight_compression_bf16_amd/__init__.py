@@ -5,7 +5,9 @@ written HIP kernels behind a C ABI (include/wc.h).  ``codec`` holds the
 tensor-level API; ``_binding`` mirrors the C ABI one to one.  ``logprobs``,
 ``adapters`` and ``moe`` are the operators of a serving step beside the
 weights: log probabilities and their gradient, low-rank adapters, and a
-mixture-of-experts layer.  Importing the
+mixture-of-experts layer; ``grouped`` and ``loss`` are a training step's:
+products grouped by expert, and cross entropy from hidden states, with their
+gradients.  Importing the
 package does not load the GPU library; the first codec call does, and fails
 if it has not been built.
 """
@@ -29,4 +31,10 @@ def __getattr__(name):
     if name == "moe_layer":
         from .moe import moe_layer
         return moe_layer
+    if name in ("grouped_linear", "grouped_linear_backward"):
+        from . import grouped
+        return getattr(grouped, name)
+    if name in ("linear_cross_entropy", "linear_cross_entropy_backward", "LinearCrossEntropy"):
+        from . import loss
+        return getattr(loss, name)
     raise AttributeError(name)

@@ -45,7 +45,9 @@ EXPORTS = ["wc_version", "wc_status_string", "wc_query_layout", "wc_plan_batch",
            "wc_decode_gemm_batch", "wc_decode_variant", "wc_encode_noalloc", "wc_noalloc_max_chunks",
            "wc_set_encoder_words", "wc_encode_variant", "wc_token_logprobs_scratch", "wc_token_logprobs",
            "wc_token_logprobs_backward", "wc_add_adapters_scratch", "wc_add_adapters",
-           "wc_moe_layer_scratch", "wc_moe_layer"]
+           "wc_moe_layer_scratch", "wc_moe_layer", "wc_grouped_linear_scratch", "wc_grouped_linear",
+           "wc_grouped_linear_backward_scratch", "wc_grouped_linear_backward", "wc_linear_cross_entropy_scratch",
+           "wc_linear_cross_entropy", "wc_linear_cross_entropy_backward_scratch", "wc_linear_cross_entropy_backward"]
 # encoder word-store forms (wc_set_encoder_words)
 ENC_WORDS_AUTO, ENC_WORDS_DIRECT, ENC_WORDS_STAGED = 0, 1, 2
 
@@ -112,6 +114,39 @@ class wc_moe(ctypes.Structure):
                 ("renormalize", ctypes.c_uint32)]
 
 
+class wc_grouped(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_void_p), ("x_stride", ctypes.c_uint64), ("w", ctypes.c_void_p),
+                ("w_expert", ctypes.c_uint64), ("w_row", ctypes.c_uint64), ("ends", ctypes.c_void_p),
+                ("y", ctypes.c_void_p), ("y_stride", ctypes.c_uint64), ("m", ctypes.c_uint64),
+                ("experts", ctypes.c_uint32), ("rows", ctypes.c_uint32), ("cols", ctypes.c_uint32),
+                ("type", ctypes.c_uint32), ("zero_rest", ctypes.c_uint32), ("reserved", ctypes.c_uint32)]
+
+
+class wc_grouped_grad(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_void_p), ("x_stride", ctypes.c_uint64), ("w", ctypes.c_void_p),
+                ("w_expert", ctypes.c_uint64), ("w_row", ctypes.c_uint64), ("ends", ctypes.c_void_p),
+                ("grad", ctypes.c_void_p), ("grad_stride", ctypes.c_uint64), ("grad_x", ctypes.c_void_p),
+                ("grad_x_stride", ctypes.c_uint64), ("grad_w", ctypes.c_void_p), ("m", ctypes.c_uint64),
+                ("experts", ctypes.c_uint32), ("rows", ctypes.c_uint32), ("cols", ctypes.c_uint32),
+                ("type", ctypes.c_uint32), ("zero_rest", ctypes.c_uint32), ("reserved", ctypes.c_uint32)]
+
+
+class wc_linear_loss(ctypes.Structure):
+    _fields_ = [("hidden", ctypes.c_void_p), ("hidden_stride", ctypes.c_uint64), ("weight", ctypes.c_void_p),
+                ("weight_stride", ctypes.c_uint64), ("tokens", ctypes.c_void_p), ("m", ctypes.c_uint64),
+                ("vocab", ctypes.c_uint32), ("cols", ctypes.c_uint32), ("type", ctypes.c_uint32),
+                ("reserved", ctypes.c_uint32), ("loss", ctypes.c_void_p), ("lse", ctypes.c_void_p)]
+
+
+class wc_linear_loss_grad(ctypes.Structure):
+    _fields_ = [("hidden", ctypes.c_void_p), ("hidden_stride", ctypes.c_uint64), ("weight", ctypes.c_void_p),
+                ("weight_stride", ctypes.c_uint64), ("tokens", ctypes.c_void_p), ("lse", ctypes.c_void_p),
+                ("grad_loss", ctypes.c_void_p), ("grad_lse", ctypes.c_void_p), ("grad_hidden", ctypes.c_void_p),
+                ("grad_hidden_stride", ctypes.c_uint64), ("grad_weight", ctypes.c_void_p), ("m", ctypes.c_uint64),
+                ("vocab", ctypes.c_uint32), ("cols", ctypes.c_uint32), ("type", ctypes.c_uint32),
+                ("reserved", ctypes.c_uint32)]
+
+
 _lib = None
 
 
@@ -155,6 +190,13 @@ def lib() -> ctypes.CDLL:
     L.wc_moe_layer_scratch.restype = U64
     L.wc_moe_layer.argtypes = [ctypes.POINTER(wc_moe), P, U64, P]
     L.wc_token_logprobs_backward.argtypes = [ctypes.POINTER(wc_logprobs_grad), P, P]
+    for name, args, sizes in (("wc_grouped_linear", wc_grouped, [U64, U32, U32, U32]),
+                              ("wc_grouped_linear_backward", wc_grouped_grad, [U64, U32, U32, U32]),
+                              ("wc_linear_cross_entropy", wc_linear_loss, [U64, U32, U32]),
+                              ("wc_linear_cross_entropy_backward", wc_linear_loss_grad, [U64, U32, U32])):
+        scratch, call = getattr(L, name + "_scratch"), getattr(L, name)
+        scratch.argtypes, scratch.restype = sizes, U64
+        call.argtypes, call.restype = [ctypes.POINTER(args), P, U64, P, P], I
     for name in ("wc_query_layout", "wc_plan_batch", "wc_encode", "wc_decode", "wc_encode_batch",
                  "wc_decode_batch", "wc_tile_order", "wc_decode_gemm_batch", "wc_decode_variant",
                  "wc_encode_noalloc", "wc_encode_variant", "wc_token_logprobs", "wc_token_logprobs_backward",
@@ -343,6 +385,42 @@ def wc_moe_layer_scratch(m: int, experts: int, top_k: int, cols: int, inner: int
 
 def wc_moe_layer(args: wc_moe, d_scratch, scratch_bytes: int, stream=None):
     _check(lib().wc_moe_layer(args, _ptr(d_scratch), scratch_bytes, _stream(stream)), "wc_moe_layer")
+
+
+def wc_grouped_linear_scratch(m: int, experts: int, rows: int, cols: int) -> int:
+    return lib().wc_grouped_linear_scratch(m, experts, rows, cols)
+
+
+def wc_grouped_linear(args: wc_grouped, d_scratch, scratch_bytes: int, d_err=None, stream=None):
+    rc = lib().wc_grouped_linear(args, _ptr(d_scratch), scratch_bytes, _ptr(d_err), _stream(stream))
+    _check(rc, "wc_grouped_linear")
+
+
+def wc_grouped_linear_backward_scratch(m: int, experts: int, rows: int, cols: int) -> int:
+    return lib().wc_grouped_linear_backward_scratch(m, experts, rows, cols)
+
+
+def wc_grouped_linear_backward(args: wc_grouped_grad, d_scratch, scratch_bytes: int, d_err=None, stream=None):
+    rc = lib().wc_grouped_linear_backward(args, _ptr(d_scratch), scratch_bytes, _ptr(d_err), _stream(stream))
+    _check(rc, "wc_grouped_linear_backward")
+
+
+def wc_linear_cross_entropy_scratch(m: int, vocab: int, cols: int) -> int:
+    return lib().wc_linear_cross_entropy_scratch(m, vocab, cols)
+
+
+def wc_linear_cross_entropy(args: wc_linear_loss, d_scratch, scratch_bytes: int, d_err=None, stream=None):
+    rc = lib().wc_linear_cross_entropy(args, _ptr(d_scratch), scratch_bytes, _ptr(d_err), _stream(stream))
+    _check(rc, "wc_linear_cross_entropy")
+
+
+def wc_linear_cross_entropy_backward_scratch(m: int, vocab: int, cols: int) -> int:
+    return lib().wc_linear_cross_entropy_backward_scratch(m, vocab, cols)
+
+
+def wc_linear_cross_entropy_backward(args: wc_linear_loss_grad, d_scratch, scratch_bytes: int, d_err=None, stream=None):
+    rc = lib().wc_linear_cross_entropy_backward(args, _ptr(d_scratch), scratch_bytes, _ptr(d_err), _stream(stream))
+    _check(rc, "wc_linear_cross_entropy_backward")
 
 
 def wc_check_division(samples_per_divisor: int = 256) -> int:

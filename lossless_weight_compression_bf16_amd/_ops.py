@@ -116,3 +116,22 @@ def done(rc: int, err, what: str):
         bits = int(err.item())
         if bits:
             raise B.WcError(f"{what}: device reported {', '.join(B.error_names(bits))} (bits {bits:#x})")
+
+
+class _Once(torch.autograd.Function):
+    """A gradient that depends on its inputs, and whose own gradient is an error rather than nothing."""
+    @staticmethod
+    def forward(ctx, what, grad, *inputs):
+        ctx.what = what
+        return grad.view_as(grad)
+
+    @staticmethod
+    def backward(ctx, *_):
+        raise RuntimeError(f"{ctx.what} cannot be differentiated twice")
+
+
+def once(what: str, grads, *inputs):
+    """What a backward pass returns of its kernels' results: under create_graph they have no graph of their own."""
+    if not torch.is_grad_enabled():
+        return grads
+    return tuple(None if g is None else _Once.apply(what, g, *inputs) for g in grads)

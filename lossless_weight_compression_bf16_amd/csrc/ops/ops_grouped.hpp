@@ -1,0 +1,389 @@
+// ops_grouped.hpp -- matrix products grouped by expert over ragged rows.  Rows
+// lo_e .. hi_e of x belong to expert e (lo_e = ends[e - 1], hi_e = ends[e]):
+//   y_r = W_e x_r,   dx_r = W_e^T dy_r,   dW_e = sum_r dy_r x_r^T.
+//
+//   k_grouped_few  y, for few rows of each expert
+//   k_grouped      y, or dx, by tiles of an expert's rows
+//   k_grouped_dw   dW, by tiles of an expert's weights
+//   k_join         sums of products that were split along k
+// The ends stay on the device: a block finds its expert and rows from them by
+// itself (every wave adds up the experts' tiles by lane moves).
+#pragma once
+
+#include "ops_common.hpp"
+#include "ops_moe.hpp"
+#include "ops_tiles.hpp"
+
+namespace wc {
+namespace ops {
+
+constexpr uint32_t kGroupedMaxExperts = 1024;
+
+struct GroupedArgs {
+    const uint16_t *x, *w;
+    const int64_t *ends;
+    uint16_t *y;
+    uint64_t x_stride, w_expert, y_stride;  // strides in elements
+    uint32_t w_row;
+    uint32_t m, experts;
+    uint32_t n, k;      // columns of y and of x
+    uint32_t zero_rest; // rows behind the last expert's: zeros, else left as they are
+    uint32_t slots;     // k_grouped_few
+    uint32_t splits;    // of k, each with its own m x n of part
+    float *part;
+    uint32_t *err;
+};
+
+// Rows of an expert, whatever the ends are (from 0 on, and not past m).
+__device__ __forceinline__ uint32_t group_end(const int64_t *ends, uint32_t e, uint32_t m)
+{
+    const int64_t v = ends[e];
+    return v < 0 ? 0u : v < (int64_t)m ? (uint32_t)v : m;
+}
+__device__ __forceinline__ void group_rows(const int64_t *ends, uint32_t e, uint32_t m, uint32_t &lo, uint32_t &hi)
+{
+    lo = e ? group_end(ends, e - 1, m) : 0u;
+    hi = max(lo, group_end(ends, e, m));
+}
+
+// Ends that go back, or past the rows.
+__device__ __forceinline__ void check_ends(const int64_t *ends, uint32_t experts, uint32_t m, uint32_t *err)
+{
+    if (!err || blockIdx.x) return;
+    for (uint32_t e = threadIdx.x; e < experts; e += blockDim.x)
+        if (ends[e] > (int64_t)m || ends[e] < (e ? ends[e - 1] : 0)) report(err, WC_EF_BAD_INDEX);
+}
+
+__device__ __forceinline__ uint32_t wave_upto(uint32_t v)  // the sum of lanes 0 .. this one
+{
+    v += lanes_moved<0x111, 0xF>(v, 0u);
+    v += lanes_moved<0x112, 0xF>(v, 0u);
+    v += lanes_moved<0x114, 0xF>(v, 0u);
+    v += lanes_moved<0x118, 0xF>(v, 0u);
+    v += lanes_moved<0x142, 0xA>(v, 0u);
+    v += lanes_moved<0x143, 0xC>(v, 0u);
+    return v;
+}
+
+// The experts' rows in units, of which each expert has units(count).  A wave's
+// view: lane l has the experts from per l on.
+struct Groups {
+    uint32_t per, mine, upto, total;
+
+    template <class F>
+    __device__ __forceinline__ void count(const GroupedArgs &g, F units)
+    {
+        const uint32_t lane = threadIdx.x & 63;
+        per = (g.experts + 63) / 64;
+        mine = 0;
+        for (uint32_t q = 0; q < per; q++) {
+            const uint32_t e = per * lane + q;
+            if (e >= g.experts) break;
+            uint32_t lo, hi;
+            group_rows(g.ends, e, g.m, lo, hi);
+            mine += units(hi - lo);
+        }
+        upto = wave_upto(mine);
+        total = (uint32_t)__builtin_amdgcn_readlane((int)upto, 63);
+    }
+    // The expert of unit u < total, its rows, and the unit's place among its own.
+    template <class F>
+    __device__ __forceinline__ void find(const GroupedArgs &g, uint32_t u, F units, uint32_t &expert, uint32_t &lo, uint32_t &hi,
+                                         uint32_t &place) const
+    {
+        const uint32_t lane = threadIdx.x & 63, owner = (uint32_t)__builtin_ctzll(__ballot(upto > u));
+        uint32_t rest = u - (upto - mine), e = 0, from = 0, to = 0;
+        if (lane == owner)
+            for (uint32_t q = 0; q < per; q++) {
+                e = per * lane + q;
+                group_rows(g.ends, e, g.m, from, to);
+                const uint32_t n = units(to - from);
+                if (rest < n) break;
+                rest -= n;
+            }
+        expert = (uint32_t)__builtin_amdgcn_readlane((int)e, owner);
+        lo = (uint32_t)__builtin_amdgcn_readlane((int)from, owner);
+        hi = (uint32_t)__builtin_amdgcn_readlane((int)to, owner);
+        place = (uint32_t)__builtin_amdgcn_readlane((int)rest, owner);
+    }
+};
+
+// y (kPAlong) or dx by tiles: an expert's rows in tiles of BM against tiles of
+// BN columns.  Grid: 8 ceil(tiles / 8) for the most tiles there can be, which is one
+// more for each expert than the rows fill.
+template <int T, int BM, int BN, bool kPAlong>
+__global__ __launch_bounds__(256, BM + BN > 384 ? 1 : 2) void k_grouped(GroupedArgs g)
+{
+    using Ti = Tile<T, BM, BN, 2, 2, true, kPAlong>;
+    __shared__ __attribute__((aligned(1024))) char q0[Ti::Q::kBytes];
+    __shared__ __attribute__((aligned(1024))) char p0[Ti::P::kBytes];
+    __shared__ __attribute__((aligned(1024))) char q1[Ti::Q::kBytes];
+    __shared__ __attribute__((aligned(1024))) char p1[Ti::P::kBytes];
+    check_ends(g.ends, g.experts, g.m, g.err);
+    auto tiles = [](uint32_t rows) { return (rows + BM - 1) / BM; };
+    Groups groups;
+    groups.count(g, tiles);
+    const uint32_t last = group_end(g.ends, g.experts - 1, g.m), rest = g.zero_rest ? tiles(g.m - last) : 0;
+    const uint32_t down = groups.total + rest, across = (g.n + BN - 1) / BN, t = xcd_piece(blockIdx.x, down * across * g.splits);
+    if (t >= down * across * g.splits) return;
+    const uint32_t split = t / (down * across);
+    uint32_t r, c, expert = 0, lo = 0, hi = 0, place = 0;
+    tile_of(t % (down * across), down, across, r, c);
+    const bool zero = r >= groups.total;
+    if (zero) {
+        lo = last;
+        hi = g.m;
+        place = r - groups.total;
+    } else {
+        groups.find(g, r, tiles, expert, lo, hi, place);
+    }
+    if ((uint64_t)place * BM >= hi - lo) return;  // bad ends
+    const uint32_t m0 = lo + BM * place, rows = min((uint32_t)BM, hi - m0), n0 = BN * c;
+    const uint32_t stages = (g.k + kTileK - 1) / kTileK, s0 = stages * split / g.splits, s1 = stages * (split + 1) / g.splits;
+    const uint32_t k0 = kTileK * s0, k = zero || s0 >= s1 ? 0 : min(g.k, kTileK * s1) - k0;
+    const uint16_t *w = g.w + expert * g.w_expert;
+    Ti ti;
+    ti.q.init(g.x + m0 * g.x_stride + k0, g.x_stride, rows, k);
+    if constexpr (kPAlong) ti.p.init(w + (uint64_t)n0 * g.w_row + k0, g.w_row, min((uint32_t)BN, g.n - n0), k);
+    else ti.p.init(w + (uint64_t)k0 * g.w_row + n0, g.w_row, k, g.n - n0);
+    ti.product(q0, p0, q1, p1, k);
+    each_four(ti, [&](uint32_t row, uint32_t col, f32x4 v) {
+        if (row >= rows || n0 + col >= g.n) return;
+        if (g.splits > 1) *reinterpret_cast<f32x4 *>(g.part + ((uint64_t)split * g.m + m0 + row) * g.n + n0 + col) = v;
+        else store_four<T>(g.y + (m0 + row) * g.y_stride + n0 + col, v);
+    });
+}
+
+struct GroupedDwArgs {
+    const uint16_t *x, *dy;
+    const int64_t *ends;
+    uint16_t *dw;                 // experts x n x k, contiguous
+    uint64_t x_stride, dy_stride;
+    uint32_t m, experts, n, k;    // columns of dy and of x
+    uint32_t splits;              // of an expert's rows, each with its own dW in part
+    float *part;
+    uint32_t *err;
+};
+
+// dW by tiles of BM rows and BN columns of it.  Grid: 8 ceil(tiles / 8).
+template <int T, int BM, int BN>
+__global__ __launch_bounds__(256, BM + BN > 384 ? 1 : 2) void k_grouped_dw(GroupedDwArgs g)
+{
+    using Ti = Tile<T, BM, BN, 2, 2, false, false>;
+    __shared__ __attribute__((aligned(1024))) char q0[Ti::Q::kBytes];
+    __shared__ __attribute__((aligned(1024))) char p0[Ti::P::kBytes];
+    __shared__ __attribute__((aligned(1024))) char q1[Ti::Q::kBytes];
+    __shared__ __attribute__((aligned(1024))) char p1[Ti::P::kBytes];
+    check_ends(g.ends, g.experts, g.m, g.err);
+    const uint32_t down = (g.n + BM - 1) / BM, across = (g.k + BN - 1) / BN, each = down * across;
+    const uint32_t t = xcd_piece(blockIdx.x, each * g.experts * g.splits);
+    if (t >= each * g.experts * g.splits) return;
+    const uint32_t expert = t / (each * g.splits), split = t / each % g.splits;
+    uint32_t r, c, lo, hi;
+    tile_of(t % each, down, across, r, c);
+    group_rows(g.ends, expert, g.m, lo, hi);
+    const uint32_t stages = (hi - lo + kTileK - 1) / kTileK;
+    const uint32_t from = min(hi, lo + kTileK * (uint32_t)((uint64_t)stages * split / g.splits));
+    const uint32_t rows = min(hi, lo + kTileK * (uint32_t)((uint64_t)stages * (split + 1) / g.splits)) - from;
+    const uint32_t m0 = BM * r, n0 = BN * c;
+    Ti ti;
+    ti.q.init(g.dy + from * g.dy_stride + m0, g.dy_stride, rows, g.n - m0);
+    ti.p.init(g.x + from * g.x_stride + n0, g.x_stride, rows, g.k - n0);
+    ti.product(q0, p0, q1, p1, rows);
+    const uint64_t all = (uint64_t)g.experts * g.n * g.k;
+    each_four(ti, [&](uint32_t row, uint32_t col, f32x4 v) {
+        if (m0 + row >= g.n || n0 + col >= g.k) return;
+        const uint64_t at = ((uint64_t)expert * g.n + m0 + row) * g.k + n0 + col;
+        if (g.splits > 1) *reinterpret_cast<f32x4 *>(g.part + split * all + at) = v;
+        else store_four<T>(g.dw + at, v);
+    });
+}
+
+constexpr uint32_t kLossRowBlocks = 256;
+
+// What numbers are multiplied by where they are FP16 (term_scale), from the
+// largest of each of kLossRowBlocks parts; 1 for BF16.
+template <int T>
+__device__ __forceinline__ float loss_scale(const float *most, float &unscale)
+{
+    unscale = 1.f;
+    if (T != WC_T_FP16) return 1.f;
+    float v = 0.f;
+#pragma unroll
+    for (uint32_t q = 0; q < kLossRowBlocks / 64; q++) v = fmaxf(v, most[64 * q + (threadIdx.x & 63)]);
+    return term_scale<T>(wave_max(v), unscale);
+}
+
+// out = the sum of `splits` parts of rows x cols each, in their order.
+// Rows from `rows_end` on (ends[experts - 1] where that is given) are left as they are.
+struct JoinArgs {
+    const float *part;
+    uint16_t *out;
+    uint64_t out_stride;
+    uint64_t rows;
+    uint32_t cols, splits;
+    const int64_t *last;   // or NULL
+    const float *most;     // or NULL: what FP16 numbers were scaled by (loss_scale)
+};
+
+template <int T>
+__global__ __launch_bounds__(256) void k_join(JoinArgs g)
+{
+    float unscale = 1.f;
+    if (g.most) loss_scale<T>(g.most, unscale);
+    const uint32_t per = g.cols / 4;
+    const uint64_t q = (uint64_t)blockIdx.x * 256 + threadIdx.x, row = q / per;
+    if (row >= g.rows || (g.last && (int64_t)row >= *g.last)) return;
+    const uint32_t col = 4 * (uint32_t)(q % per);
+    const float *p = g.part + row * g.cols + col;
+    f32x4 v = *reinterpret_cast<const f32x4 *>(p);
+    for (uint32_t s = 1; s < g.splits; s++) v += *reinterpret_cast<const f32x4 *>(p + s * g.rows * g.cols);
+    if (T == WC_T_FP16 && g.most) v *= unscale;
+    store_four<T>(g.out + row * g.out_stride + col, v);
+}
+
+// Sixteen rows of weights from n and the sixteen after them (fewer than 32:
+// the second ones overlap the first) against up to 16 NT rows of x.
+template <int T, int NT>
+__device__ __forceinline__ void few_rows(const uint16_t *w, uint32_t pitch, uint32_t n, const uint32_t (&first)[2],
+                                         const uint16_t *x, uint64_t x_stride, uint32_t count, uint32_t c0, uint32_t c1,
+                                         Strip *strips, f32x4 (&sum)[2][4])
+{
+    const uint32_t i = threadIdx.x & 15, rows = min(16u, n);
+    const uint16_t *const weights[2] = {w + (uint64_t)first[0] * pitch, w + (uint64_t)first[1] * pitch};
+    f32x4 acc[2][1][NT];
+    const float scale[NT] = {};  // of no use here
+#pragma unroll
+    for (int t = 0; t < NT; t++) acc[0][0][t] = acc[1][0][t] = f32x4{0.f, 0.f, 0.f, 0.f};
+    strip_product<T, 2, false, NT>(
+        weights, [&](uint32_t r) { return min(r, rows - 1) * pitch; },
+        [&](int t) { return x + min(16 * t + i, count - 1) * x_stride; }, c0, c1, strips, scale, acc);
+#pragma unroll
+    for (int t = 0; t < NT; t++)
+#pragma unroll
+        for (int m = 0; m < 2; m++) sum[m][t] = acc[m][0][t];
+}
+
+// 32 rows of weights (n of them in all) from n0 on against `count` <= 64 rows of
+// x, columns of all k.  kSplit: the block's four waves share the columns, and
+// f(t, sums) is called by the wave t with the sums of 16 rows of x; otherwise the rows
+// are the wave's own, and it calls f for every t.  sums[m]: the lane's four
+// of weights' rows first[m] + 4 gr on, against row 16 t + i of x.
+template <int T, bool kSplit, class F>
+__device__ __forceinline__ void few_product(const uint16_t *w, uint32_t pitch, uint32_t n, uint32_t n0, uint32_t k,
+                                            const uint16_t *x, uint64_t x_stride, uint32_t count, Strip (*strips)[2], F f)
+{
+    const uint32_t wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+    const uint32_t most = n < 16 ? 0 : n - 16, first[2] = {min(n0, most), min(n0 + 16, most)};
+    uint32_t c0 = 0, c1 = k;
+    if (kSplit) wave_quarter(k, kStripCols, wave, c0, c1);
+    f32x4 sum[2][4];
+    const uint32_t tiles = (count + 15) / 16;
+    if (tiles <= 1) few_rows<T, 1>(w, pitch, n, first, x, x_stride, count, c0, c1, strips[wave], sum);
+    else if (tiles <= 2) few_rows<T, 2>(w, pitch, n, first, x, x_stride, count, c0, c1, strips[wave], sum);
+    else few_rows<T, 4>(w, pitch, n, first, x, x_stride, count, c0, c1, strips[wave], sum);
+    if constexpr (!kSplit) {
+#pragma unroll
+        for (uint32_t t = 0; t < 4; t++)
+            if (t < tiles) f(t, first, sum[0][t], sum[1][t]);
+    } else {
+        f32x4(*part)[8][64] = reinterpret_cast<f32x4(*)[8][64]>(&strips[0][0]);  // [4], when the strips are done
+        static_assert(sizeof(Strip) * 8 >= 4 * 8 * 64 * 16, "the waves' sums fit into the strips");
+        __syncthreads();
+#pragma unroll
+        for (uint32_t t = 0; t < 4; t++)
+            if (t < tiles) {
+                part[wave][2 * t][lane] = sum[0][t];
+                part[wave][2 * t + 1][lane] = sum[1][t];
+            }
+        __syncthreads();
+        if (wave < tiles) {
+            f32x4 v[2];
+#pragma unroll
+            for (int m = 0; m < 2; m++) {
+                const uint32_t q = 2 * wave + m;
+                v[m] = (part[0][q][lane] + part[1][q][lane]) + (part[2][q][lane] + part[3][q][lane]);
+            }
+            f(wave, first, v[0], v[1]);
+        }
+        __syncthreads();  // before the strips are written again
+    }
+}
+
+// Eight rows of weights (n of them in all) from n0 on against one row of x, by
+// a wave.  f(row, sum) by one lane for each row that exists.
+template <int T, class F>
+__device__ __forceinline__ void one_product(const uint16_t *w, uint32_t pitch, uint32_t n, uint32_t n0, uint32_t k,
+                                            const uint16_t *x, F f)
+{
+    constexpr int R = 8;
+    const uint32_t lane = threadIdx.x & 63;
+    const uint16_t *rows[R];
+    float acc[R], mine = 0.f;
+#pragma unroll
+    for (int r = 0; r < R; r++) {
+        rows[r] = w + (uint64_t)min(n0 + r, n - 1) * pitch;
+        acc[r] = 0.f;
+    }
+    rows_product<T, R>(rows, 0, k, [&](uint32_t c, float *v) { Type<T>::unpack(load16<16>(x + c), v); }, acc);
+#pragma unroll
+    for (int r = 0; r < R; r++) {
+        acc[r] = wave_sum(acc[r]);
+        if (lane == (uint32_t)r) mine = acc[r];
+    }
+    if (lane < R && n0 + lane < n) f(n0 + lane, mine);
+}
+
+// y for experts with few rows: a block has 32 rows of weights (128 without
+// kSplit) of the slot-th expert that has rows.  Reading the weights is the
+// bound, so they go in whole lines past the caches, and 64 rows of x meet them
+// at a time; a single one meets them without the matrix cores.  Grid: slots x ceil(n / 32
+// or 128); one slot more where the rows behind the last expert's are to be zeros.
+template <int T, bool kSplit>
+__global__ __launch_bounds__(256, 2) void k_grouped_few(GroupedArgs g)
+{
+    __shared__ Strip strips[4][2];
+    check_ends(g.ends, g.experts, g.m, g.err);
+    const uint32_t wave = threadIdx.x >> 6, i = threadIdx.x & 15, gr = (threadIdx.x & 63) >> 4;
+    const uint32_t slot = blockIdx.x % g.slots, n0 = blockIdx.x / g.slots * (kSplit ? 32 : 128) + (kSplit ? 0 : 32 * wave);
+    auto any = [](uint32_t rows) { return rows ? 1u : 0u; };
+    Groups groups;
+    groups.count(g, any);
+    uint32_t expert, lo, hi, place;
+    if (slot >= groups.total) {
+        const uint32_t last = group_end(g.ends, g.experts - 1, g.m);
+        if (slot > groups.total || !g.zero_rest) return;
+        const uint32_t from = kSplit ? 32 * (blockIdx.x / g.slots) : 128 * (blockIdx.x / g.slots), per = kSplit ? 4 : 16;
+        for (uint32_t q = threadIdx.x; q < (g.m - last) * per; q += 256) {
+            const uint32_t c = from + 8 * (q % per);
+            if (c < g.n) *reinterpret_cast<u32x4 *>(g.y + (last + q / per) * g.y_stride + c) = u32x4{0, 0, 0, 0};
+        }
+        return;
+    }
+    groups.find(g, slot, any, expert, lo, hi, place);
+    const uint16_t *w = g.w + expert * g.w_expert;
+    for (uint32_t r0 = lo; r0 < hi; r0 += 64) {
+        const uint32_t count = min(64u, hi - r0);
+        const uint16_t *x = g.x + r0 * g.x_stride;
+        if (count == 1) {
+            uint16_t *y = g.y + r0 * g.y_stride;
+            for (uint32_t q = 0; q < (kSplit ? 1 : 4); q++) {
+                const uint32_t n = kSplit ? n0 + 8 * wave : n0 + 8 * q;
+                if (n < g.n) one_product<T>(w, g.w_row, g.n, n, g.k, x, [&](uint32_t r, float v) { y[r] = Type<T>::from_f32(v); });
+            }
+        } else if (kSplit || n0 < g.n) {
+            few_product<T, kSplit>(w, g.w_row, g.n, n0, g.k, x, g.x_stride, count, strips,
+                                   [&](uint32_t t, const uint32_t(&first)[2], f32x4 v0, f32x4 v1) {
+                                       const uint32_t r = 16 * t + i;
+                                       if (r >= count) return;
+                                       uint16_t *y = g.y + (r0 + r) * g.y_stride + 4 * gr;
+                                       const uint32_t a = first[0] + 4 * gr, b = first[1] + 4 * gr;
+                                       if (a >= n0 && a < g.n) store_four<T>(y + first[0], v0);
+                                       if (b >= n0 + 16 && b < g.n) store_four<T>(y + first[1], v1);
+                                   });
+        }
+    }
+}
+
+}  // namespace ops
+}  // namespace wc

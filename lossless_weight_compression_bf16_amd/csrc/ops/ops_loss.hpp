@@ -1,0 +1,339 @@
+// ops_loss.hpp -- softmax cross entropy over a large vocabulary from hidden
+// states, without the logits in memory, and its gradient:
+//   z = H W^T,  lse_r = log sum_v exp z_rv,  loss_r = lse_r - z_r,t,
+//   G_rv = (gl_r + gz_r) exp(z_rv - lse_r) - gl_r [v = t_r],  dH = G W,  dW = G^T H
+// with gl and gz the gradients of loss and lse (gl = 0 where there is no token).
+//
+//   k_loss_few, k_loss        statistics (largest logit, sum of exponentials) of 32, 128 or 256 columns of z
+//   k_loss_join               lse and loss of a row from them
+//   k_loss_rows               what the gradient needs of a row, and H without the rows that have no part in it
+//   k_loss_grad_few, k_loss_grad  G of a piece of the vocabulary: z again, then the formula
+//   k_product                 dH += G W and dW = G^T H of that piece
+#pragma once
+
+#include "ops_common.hpp"
+#include "ops_grouped.hpp"
+#include "ops_tiles.hpp"
+
+namespace wc {
+namespace ops {
+
+struct LossArgs {
+    const uint16_t *h, *w;
+    uint64_t h_stride;
+    uint32_t w_row;
+    const int64_t *tokens;
+    uint32_t m, vocab, k;
+    uint32_t parts;      // tiles of the vocabulary
+    float2 *part;        // m x parts: the largest logit of a tile, and the sum of exp(z - it)
+    float *given;        // m: the logit of the row's token
+    float *loss, *lse;
+    uint32_t *err;
+};
+
+// Largest logit and sum of exponentials so far; -inf and 0 of nothing, and of
+// nothing but -inf.  NaN and +inf make the sum NaN.
+struct Stat {
+    float most, sum;
+
+    __device__ __forceinline__ static float base(float most) { return most == -kInf ? 0.f : most; }
+    __device__ __forceinline__ void join(float most2, float sum2)
+    {
+        const float all = fmaxf(most, most2), b = base(all);
+        sum = sum * exp2_fast((most - b) * kLog2e) + sum2 * exp2_fast((most2 - b) * kLog2e);
+        most = all;
+    }
+};
+
+// Statistics of a block's tile: rows of m0, columns of n0 on.
+template <int T, int BM, int BN>
+__global__ __launch_bounds__(256, BM + BN > 384 ? 1 : 2) void k_loss(LossArgs g)
+{
+    using Ti = Tile<T, BM, BN, 2, 2, true, true>;
+    __shared__ __attribute__((aligned(1024))) char q0[Ti::Q::kBytes];
+    __shared__ __attribute__((aligned(1024))) char p0[Ti::P::kBytes];
+    __shared__ __attribute__((aligned(1024))) char q1[Ti::Q::kBytes];
+    __shared__ __attribute__((aligned(1024))) char p1[Ti::P::kBytes];
+    float2(*stats)[BM] = reinterpret_cast<float2(*)[BM]>(q0);  // [2], when the operands are done
+    const uint32_t down = (g.m + BM - 1) / BM, t = xcd_piece(blockIdx.x, down * g.parts);
+    if (t >= down * g.parts) return;
+    uint32_t r, c;
+    tile_of(t, down, g.parts, r, c);
+    const uint32_t m0 = BM * r, rows = min((uint32_t)BM, g.m - m0), n0 = BN * c, cols = min((uint32_t)BN, g.vocab - n0);
+    const uint32_t wave = threadIdx.x >> 6, lane = threadIdx.x & 63, i = lane & 15, gr = lane >> 4;
+    Ti ti;
+    ti.q.init(g.h + m0 * g.h_stride, g.h_stride, rows, g.k);
+    ti.p.init(g.w + (uint64_t)n0 * g.w_row, g.w_row, cols, g.k);
+    ti.product(q0, p0, q1, p1, g.k);
+#pragma unroll
+    for (int b = 0; b < Ti::kM; b++) {
+        const uint32_t row = 16 * (wave / 2 + 2 * b) + i, first = 16 * (wave % 2) + 4 * gr;
+        const int64_t token = row < rows ? g.tokens[m0 + row] - n0 : -1;
+        Stat s{-kInf, 0.f};
+#pragma unroll
+        for (int a = 0; a < Ti::kN; a++)
+#pragma unroll
+            for (int e = 0; e < 4; e++) {
+                const uint32_t col = first + 32 * a + e;
+                const float z = ti.acc[a][b][e];
+                if (col < cols) s.most = fmaxf(s.most, z);
+                if (token == (int64_t)col && col < cols) g.given[m0 + row] = z;
+            }
+        const float base = Stat::base(s.most);
+#pragma unroll
+        for (int a = 0; a < Ti::kN; a++)
+#pragma unroll
+            for (int e = 0; e < 4; e++)
+                if (first + 32 * a + e < cols) s.sum += exp2_fast((ti.acc[a][b][e] - base) * kLog2e);
+        s.join(__shfl_xor(s.most, 16, 64), __shfl_xor(s.sum, 16, 64));
+        s.join(__shfl_xor(s.most, 32, 64), __shfl_xor(s.sum, 32, 64));
+        if (gr == 0) stats[wave % 2][row] = float2{s.most, s.sum};
+    }
+    __syncthreads();
+    if (threadIdx.x < rows) {
+        const float2 one = stats[0][threadIdx.x], two = stats[1][threadIdx.x];
+        Stat s{one.x, one.y};
+        s.join(two.x, two.y);
+        g.part[(uint64_t)(m0 + threadIdx.x) * g.parts + c] = float2{s.most, s.sum};
+    }
+}
+
+// The same for up to 64 rows: 32 columns of z for a block (128 without kSplit).
+template <int T, bool kSplit>
+__global__ __launch_bounds__(256, 2) void k_loss_few(LossArgs g)
+{
+    __shared__ Strip strips[4][2];
+    const uint32_t wave = threadIdx.x >> 6, i = threadIdx.x & 15, gr = (threadIdx.x & 63) >> 4;
+    const uint32_t part = kSplit ? blockIdx.x : 4 * blockIdx.x + wave, n0 = 32 * part;
+    if (g.m == 1) {
+        const int64_t token = g.tokens[0];
+        for (uint32_t q = 0; q < (kSplit ? 1 : 4); q++) {
+            const uint32_t n = n0 + 8 * (kSplit ? wave : q);
+            if (n >= g.vocab) break;
+            float mine = -kInf;
+            one_product<T>(g.w, g.w_row, g.vocab, n, g.k, g.h, [&](uint32_t v, float sum) {
+                mine = sum;
+                if ((int64_t)v == token) g.given[0] = sum;
+            });
+            const float most = wave_max(mine);
+            const float sum = wave_sum((threadIdx.x & 63) < 8 && n + (threadIdx.x & 63) < g.vocab
+                                           ? exp2_fast((mine - Stat::base(most)) * kLog2e) : 0.f);
+            if ((threadIdx.x & 63) == 0) g.part[n / 8] = float2{most, sum};
+        }
+        return;
+    }
+    if (!kSplit && n0 >= g.vocab) return;
+    few_product<T, kSplit>(g.w, g.w_row, g.vocab, n0, g.k, g.h, g.h_stride, g.m, strips,
+                           [&](uint32_t t, const uint32_t(&first)[2], f32x4 v0, f32x4 v1) {
+                               const uint32_t row = 16 * t + i;
+                               const int64_t token = row < g.m ? g.tokens[row] : -1;
+                               Stat s{-kInf, 0.f};
+#pragma unroll
+                               for (int m = 0; m < 2; m++)
+#pragma unroll
+                                   for (uint32_t e = 0; e < 4; e++) {
+                                       const uint32_t v = first[m] + 4 * gr + e;
+                                       const float z = m ? v1[e] : v0[e];
+                                       if (v < n0 + 16 * m || v >= g.vocab) continue;  // of the rows before
+                                       s.most = fmaxf(s.most, z);
+                                       if (token == (int64_t)v) g.given[row] = z;
+                                   }
+                               const float base = Stat::base(s.most);
+#pragma unroll
+                               for (int m = 0; m < 2; m++)
+#pragma unroll
+                                   for (uint32_t e = 0; e < 4; e++) {
+                                       const uint32_t v = first[m] + 4 * gr + e;
+                                       if (v < n0 + 16 * m || v >= g.vocab) continue;
+                                       s.sum += exp2_fast(((m ? v1[e] : v0[e]) - base) * kLog2e);
+                                   }
+                               s.join(__shfl_xor(s.most, 16, 64), __shfl_xor(s.sum, 16, 64));
+                               s.join(__shfl_xor(s.most, 32, 64), __shfl_xor(s.sum, 32, 64));
+                               if (gr == 0 && row < g.m) g.part[(uint64_t)row * g.parts + part] = float2{s.most, s.sum};
+                           });
+}
+
+// One block per row.
+__global__ __launch_bounds__(256) void k_loss_join(LossArgs g)
+{
+    __shared__ float2 waves[4];
+    const uint32_t r = blockIdx.x;
+    const float2 *p = g.part + (uint64_t)r * g.parts;
+    Stat s{-kInf, 0.f};
+    for (uint32_t q = threadIdx.x; q < g.parts; q += 256) s.join(p[q].x, p[q].y);
+#pragma unroll
+    for (int o = 1; o < 64; o *= 2) s.join(__shfl_xor(s.most, o, 64), __shfl_xor(s.sum, o, 64));
+    if ((threadIdx.x & 63) == 0) waves[threadIdx.x >> 6] = float2{s.most, s.sum};
+    __syncthreads();
+    if (threadIdx.x) return;
+#pragma unroll
+    for (int w = 1; w < 4; w++) s.join(waves[w].x, waves[w].y);
+    const float log_sum = __builtin_amdgcn_logf(s.sum) * kLn2;
+    g.lse[r] = s.most == -kInf && s.sum == 0.f ? -kInf : s.most + log_sum;
+    const int64_t t = g.tokens[r];
+    float loss = 0.f;
+    if (t >= 0 && t < (int64_t)g.vocab) {
+        // the difference of logits first: the two are near each other where a loss is small
+        loss = s.most == -kInf && s.sum == 0.f ? kInf : (s.most - g.given[r]) + log_sum;
+    } else if (t != -1) {
+        loss = nan32();
+        report(g.err, WC_EF_BAD_INDEX);
+    }
+    g.loss[r] = loss;
+}
+
+struct LossGradArgs {
+    const uint16_t *h, *w;
+    uint64_t h_stride;
+    uint32_t w_row;
+    const int64_t *tokens;
+    const float *lse, *grad_loss, *grad_lse;
+    uint32_t m, vocab, k;
+    // scratch
+    uint16_t *live;      // m x k: H, rows without a part in the gradient as zeros; or NULL
+    f32x4 *rows;         // m: lse, gl + gz, gl, token
+    float *most;         // kLossRowBlocks: the largest |gl|, |gl + gz| of some rows
+    uint16_t *grad;      // m x pitch: G of a piece
+    uint32_t pitch, v0, width;
+    uint32_t *err;
+};
+
+__global__ __launch_bounds__(256) void k_loss_rows(LossGradArgs g)
+{
+    float most = 0.f;
+    for (uint32_t r = blockIdx.x; r < g.m; r += gridDim.x) {
+        const int64_t t = g.tokens[r];
+        const bool is = t >= 0 && t < (int64_t)g.vocab;
+        const float lse = g.lse[r], none = lse == -kInf ? 0.f : 1.f;
+        const float gl = is && g.grad_loss && none ? g.grad_loss[r] : 0.f;
+        const float all = gl + (g.grad_lse && none ? g.grad_lse[r] : 0.f);
+        const bool live = gl != 0.f || all != 0.f;
+        most = fmaxf(most, fmaxf(fabsf(gl), fabsf(all)));
+        if (threadIdx.x == 0) {
+            g.rows[r] = f32x4{lse, all, gl, __builtin_bit_cast(float, is ? (int32_t)t : -1)};
+            if (!is && t != -1) report(g.err, WC_EF_BAD_INDEX);
+        }
+        if (g.live)
+            for (uint32_t c = 8 * threadIdx.x; c < g.k; c += 2048)
+                *reinterpret_cast<u32x4 *>(g.live + (uint64_t)r * g.k + c) =
+                    only(live, *reinterpret_cast<const u32x4 *>(g.h + r * g.h_stride + c));
+    }
+    if (threadIdx.x == 0) g.most[blockIdx.x] = most;
+}
+
+__device__ __forceinline__ float loss_gradient(f32x4 row, float z, uint32_t v, float scale)
+{
+    const float all = row[1], p = all == 0.f ? 0.f : all * exp2_fast((z - row[0]) * kLog2e);
+    return scale * ((int32_t)v == __builtin_bit_cast(int32_t, (float)row[3]) ? p - row[2] : p);
+}
+
+// G of a tile.
+template <int T, int BM, int BN>
+__global__ __launch_bounds__(256, BM + BN > 384 ? 1 : 2) void k_loss_grad(LossGradArgs g)
+{
+    using Ti = Tile<T, BM, BN, 2, 2, true, true>;
+    __shared__ __attribute__((aligned(1024))) char q0[Ti::Q::kBytes];
+    __shared__ __attribute__((aligned(1024))) char p0[Ti::P::kBytes];
+    __shared__ __attribute__((aligned(1024))) char q1[Ti::Q::kBytes];
+    __shared__ __attribute__((aligned(1024))) char p1[Ti::P::kBytes];
+    const uint32_t down = (g.m + BM - 1) / BM, across = (g.width + BN - 1) / BN, t = xcd_piece(blockIdx.x, down * across);
+    if (t >= down * across) return;
+    uint32_t r, c;
+    tile_of(t, down, across, r, c);
+    const uint32_t m0 = BM * r, rows = min((uint32_t)BM, g.m - m0), n0 = BN * c, cols = min((uint32_t)BN, g.width - n0);
+    Ti ti;
+    ti.q.init(g.h + m0 * g.h_stride, g.h_stride, rows, g.k);
+    ti.p.init(g.w + (uint64_t)(g.v0 + n0) * g.w_row, g.w_row, cols, g.k);
+    ti.product(q0, p0, q1, p1, g.k);
+    float unscale;
+    const float scale = loss_scale<T>(g.most, unscale);
+    each_four(ti, [&](uint32_t row, uint32_t col, f32x4 z) {
+        if (row >= rows || n0 + col >= g.pitch) return;
+        const f32x4 info = g.rows[m0 + row];
+#pragma unroll
+        for (uint32_t e = 0; e < 4; e++) z[e] = col + e < cols ? loss_gradient(info, z[e], g.v0 + n0 + col + e, scale) : 0.f;
+        store_four<T>(g.grad + (uint64_t)(m0 + row) * g.pitch + n0 + col, z);
+    });
+}
+
+// The same for up to 64 rows.
+template <int T, bool kSplit>
+__global__ __launch_bounds__(256, 2) void k_loss_grad_few(LossGradArgs g)
+{
+    __shared__ Strip strips[4][2];
+    const uint32_t wave = threadIdx.x >> 6, i = threadIdx.x & 15, gr = (threadIdx.x & 63) >> 4;
+    const uint32_t n0 = 32 * (kSplit ? blockIdx.x : 4 * blockIdx.x + wave);
+    if (!kSplit && n0 >= g.width) return;
+    float unscale;
+    const float scale = loss_scale<T>(g.most, unscale);
+    few_product<T, kSplit>(g.w + (uint64_t)g.v0 * g.w_row, g.w_row, g.width, n0, g.k, g.h, g.h_stride, g.m, strips,
+                           [&](uint32_t t, const uint32_t(&first)[2], f32x4 v0, f32x4 v1) {
+                               const uint32_t row = 16 * t + i;
+                               if (row >= g.m) return;
+                               const f32x4 info = g.rows[row];
+                               uint16_t *to = g.grad + (uint64_t)row * g.pitch;
+#pragma unroll
+                               for (int m = 0; m < 2; m++)
+#pragma unroll
+                                   for (uint32_t e = 0; e < 4; e++) {
+                                       const uint32_t v = first[m] + 4 * gr + e;
+                                       if (v < n0 + 16 * m || v >= g.width) continue;
+                                       const float z = m ? v1[e] : v0[e];
+                                       to[v] = Type<T>::from_f32(loss_gradient(info, z, g.v0 + v, scale));
+                                   }
+                               if (gr == 0 && n0 + 32 >= g.width)
+                                   for (uint32_t v = g.width; v < g.pitch; v++) to[v] = 0;
+                           });
+}
+
+struct ProductArgs {
+    const uint16_t *q, *p;
+    uint64_t q_stride, p_stride;
+    uint32_t m, n, k;         // of D
+    uint32_t splits;          // of k, each with its own m x n of part
+    float *part;              // or NULL: D goes to out
+    uint32_t add;             // to what part holds
+    uint16_t *out;
+    uint64_t out_stride;
+    const float *most;        // of G, by which it was scaled
+};
+
+// D = Q P^T of whole matrices.  kQAlong: k along the rows of Q's memory; P has it across.
+template <int T, int BM, int BN, bool kQAlong>
+__global__ __launch_bounds__(256, BM + BN > 384 ? 1 : 2) void k_product(ProductArgs g)
+{
+    using Ti = Tile<T, BM, BN, 2, 2, kQAlong, false>;
+    __shared__ __attribute__((aligned(1024))) char q0[Ti::Q::kBytes];
+    __shared__ __attribute__((aligned(1024))) char p0[Ti::P::kBytes];
+    __shared__ __attribute__((aligned(1024))) char q1[Ti::Q::kBytes];
+    __shared__ __attribute__((aligned(1024))) char p1[Ti::P::kBytes];
+    const uint32_t down = (g.m + BM - 1) / BM, across = (g.n + BN - 1) / BN, each = down * across;
+    const uint32_t t = xcd_piece(blockIdx.x, each * g.splits);
+    if (t >= each * g.splits) return;
+    const uint32_t split = t / each;
+    uint32_t r, c;
+    tile_of(t % each, down, across, r, c);
+    const uint32_t m0 = BM * r, rows = min((uint32_t)BM, g.m - m0), n0 = BN * c;
+    const uint32_t stages = (g.k + kTileK - 1) / kTileK, k0 = kTileK * (uint32_t)((uint64_t)stages * split / g.splits);
+    const uint32_t k1 = min(g.k, kTileK * (uint32_t)((uint64_t)stages * (split + 1) / g.splits)), k = k1 > k0 ? k1 - k0 : 0;
+    Ti ti;
+    // G has whole 16 bytes of a row, zeros behind its width
+    if constexpr (kQAlong) ti.q.init(g.q + m0 * g.q_stride + k0, g.q_stride, rows, (k + 7) / 8 * 8);
+    else ti.q.init(g.q + k0 * g.q_stride + m0, g.q_stride, k, (g.m + 7) / 8 * 8 - m0);
+    ti.p.init(g.p + k0 * g.p_stride + n0, g.p_stride, k, g.n - n0);
+    ti.product(q0, p0, q1, p1, k);
+    float unscale;
+    loss_scale<T>(g.most, unscale);
+    each_four(ti, [&](uint32_t row, uint32_t col, f32x4 v) {
+        if (row >= rows || n0 + col >= g.n) return;
+        if (g.part) {
+            f32x4 *to = reinterpret_cast<f32x4 *>(g.part + ((uint64_t)split * g.m + m0 + row) * g.n + n0 + col);
+            *to = g.add ? *to + v : v;
+        } else {
+            store_four<T>(g.out + (m0 + row) * g.out_stride + n0 + col, v * unscale);
+        }
+    });
+}
+
+}  // namespace ops
+}  // namespace wc

@@ -1,0 +1,469 @@
+// wc_products.hip -- C ABI of the products of a training step beside the
+// compressed weights (see include/wc.h): products grouped by expert, cross
+// entropy from hidden states, and their gradients.  Argument checks, launch
+// shapes and scratch layout; like the other calls these only enqueue on the
+// caller's stream.
+#include <hip/hip_runtime.h>
+#include <math.h>
+#include <stdint.h>
+
+#include "wc.h"
+#include "ops_common.hpp"
+#include "ops_grouped.hpp"
+#include "ops_host.hpp"
+#include "ops_loss.hpp"
+
+using namespace wc::ops;
+
+namespace {
+
+// Rows that a tile's window can hold: 256 of them below 2^31 bytes.
+constexpr uint64_t kMaxPitch = (1ull << 22) - 8;
+constexpr uint32_t kMaxCols = 1u << 20;
+
+struct TilePlan {
+    bool large;  // 256 x 256, else 128 x 128
+    uint32_t splits;
+};
+
+// The tile and the parts of k with the least time, of `tiles` (of 256, of 128)
+// with `stages` of k each: a compute unit takes 1.5 us for a stage of one large
+// tile, 1.1 us for one of two small ones and 0.75 of a single one, and the
+// parts' sums are written and read in fp32.
+TilePlan tile_plan(uint64_t large, uint64_t small, uint64_t stages, uint64_t results, bool joined)
+{
+    TilePlan best{false, 1};
+    double least = 1e30;
+    for (int size = 0; size < 2; size++) {
+        for (uint32_t s = 1; s <= 16 && (s == 1 || stages >= 4 * s); s *= 2) {
+            const double tiles = (double)(size ? large : small) * s, each = (double)ceil_div(stages, s) + 3;
+            const double rounds = size ? ceil(tiles / kCus) : tiles <= kCus ? 1.0 : ceil(tiles / (2 * kCus));
+            double t = rounds * each * (size ? 1.5 : tiles <= kCus ? 0.75 : 1.1);
+            if (s > 1) t += (joined ? 0.0 : 4.0) + (double)results * s * 8 / 4e6;
+            if (t < least) {
+                least = t;
+                best = {size == 1, s};
+            }
+        }
+    }
+    return best;
+}
+
+// ------------------------------------------------------------- grouped by expert
+
+uint64_t tiles_of(uint64_t m, uint32_t experts, uint64_t tile)  // the most there can be
+{
+    return m / tile + (m < experts ? m : experts);
+}
+uint64_t tiles_expected(uint64_t m, uint32_t experts, uint64_t tile)  // with the rows dealt evenly
+{
+    const uint64_t hit = m < experts ? m : experts;
+    return hit * ceil_div(ceil_div(m, hit), tile);
+}
+
+// y or dx of m rows with n columns each, from k
+TilePlan grouped_plan(uint64_t m, uint32_t experts, uint32_t n, uint32_t k)
+{
+    return tile_plan(tiles_expected(m, experts, 256) * ceil_div(n, 256), tiles_expected(m, experts, 128) * ceil_div(n, 128),
+                     ceil_div(k, kTileK), m * n, false);
+}
+
+// few rows of each expert: the weights are read once and no tile would be full
+bool grouped_few(uint64_t m, uint32_t experts) { return m <= 48ull * (m < experts ? m : experts); }
+
+TilePlan grouped_dw_plan(uint64_t m, uint32_t experts, uint32_t n, uint32_t k)
+{
+    const uint64_t hit = m < experts ? (m ? m : 1) : experts;
+    return tile_plan(experts * ceil_div(n, 256) * ceil_div(k, 256), experts * ceil_div(n, 128) * ceil_div(k, 128),
+                     ceil_div(ceil_div(m, hit), kTileK), (uint64_t)experts * n * k, false);
+}
+
+uint64_t part_bytes(uint64_t results, uint32_t splits) { return splits > 1 ? 4 * results * splits : 0; }
+
+bool valid_grouped(uint64_t m, uint32_t experts, uint32_t rows, uint32_t cols)
+{
+    if (m > kMaxRows || experts < 1 || experts > kGroupedMaxExperts || rows < 8 || rows % 8 || rows > kMaxCols || cols < 8 ||
+        cols % 8 || cols > kMaxCols)
+        return false;
+    const uint64_t most = max_blocks(256) / 16 - 8, wide = rows > cols ? rows : cols;
+    return (m / 128 + experts) * ceil_div(wide, 32) <= most && experts * ceil_div(rows, 128) * ceil_div(cols, 128) <= most;
+}
+
+void launch_join(int type, const JoinArgs &g, hipStream_t stream)
+{
+    const uint64_t blocks = ceil_div(g.rows * (g.cols / 4), 256);
+    if (!blocks) return;
+    if (type == WC_T_BF16) hipLaunchKernelGGL(k_join<WC_T_BF16>, dim3((uint32_t)blocks), dim3(256), 0, stream, g);
+    else hipLaunchKernelGGL(k_join<WC_T_FP16>, dim3((uint32_t)blocks), dim3(256), 0, stream, g);
+}
+
+uint32_t xcd_grid(uint64_t pieces) { return (uint32_t)(8 * ceil_div(pieces, 8)); }
+
+// y, or dx (kPAlong false), by tiles
+template <int T, bool kPAlong>
+void launch_grouped(GroupedArgs g, const TilePlan &p, hipStream_t stream)
+{
+    g.splits = p.splits;
+    const uint64_t tile = p.large ? 256 : 128;
+    // rows behind the last expert's fill a tile more, and may take one that the experts' would have
+    const uint64_t tiles = (tiles_of(g.m, g.experts, tile) + 1) * ceil_div(g.n, tile) * g.splits;
+    if (p.large) hipLaunchKernelGGL((k_grouped<T, 256, 256, kPAlong>), dim3(xcd_grid(tiles)), dim3(256), 0, stream, g);
+    else hipLaunchKernelGGL((k_grouped<T, 128, 128, kPAlong>), dim3(xcd_grid(tiles)), dim3(256), 0, stream, g);
+    if (g.splits > 1)
+        launch_join(T, JoinArgs{g.part, g.y, g.y_stride, g.m, g.n, g.splits, g.zero_rest ? nullptr : g.ends + g.experts - 1, nullptr},
+                    stream);
+}
+
+template <int T>
+wc_status launch_grouped_linear(GroupedArgs g, hipStream_t stream)
+{
+    if (grouped_few(g.m, g.experts)) {
+        const bool split = g.k > 1024;
+        g.slots = (g.m < g.experts ? g.m : g.experts) + (g.zero_rest ? 1 : 0);
+        const dim3 grid((uint32_t)(g.slots * ceil_div(g.n, split ? 32 : 128)));
+        if (split) hipLaunchKernelGGL((k_grouped_few<T, true>), grid, dim3(256), 0, stream, g);
+        else hipLaunchKernelGGL((k_grouped_few<T, false>), grid, dim3(256), 0, stream, g);
+    } else {
+        launch_grouped<T, true>(g, grouped_plan(g.m, g.experts, g.n, g.k), stream);
+    }
+    return launched();
+}
+
+template <int T>
+void launch_grouped_dw(GroupedDwArgs g, const TilePlan &p, hipStream_t stream)
+{
+    g.splits = p.splits;
+    const uint64_t tile = p.large ? 256 : 128, tiles = g.experts * ceil_div(g.n, tile) * ceil_div(g.k, tile) * g.splits;
+    if (p.large) hipLaunchKernelGGL((k_grouped_dw<T, 256, 256>), dim3(xcd_grid(tiles)), dim3(256), 0, stream, g);
+    else hipLaunchKernelGGL((k_grouped_dw<T, 128, 128>), dim3(xcd_grid(tiles)), dim3(256), 0, stream, g);
+    if (g.splits > 1)
+        launch_join(T, JoinArgs{g.part, g.dw, g.k, (uint64_t)g.experts * g.n, g.k, g.splits, nullptr, nullptr}, stream);
+}
+
+// ------------------------------------------------------------- cross entropy
+
+constexpr uint64_t kLossMaxRows = 1ull << 19;
+constexpr uint32_t kLossSlice = 1u << 15;  // rows of one set of launches of the forward pass
+// G of a piece of the vocabulary: at most 2^27 numbers, what the last cache holds
+constexpr uint64_t kLossPiece = 1ull << 27;
+
+bool valid_loss(uint64_t m, uint32_t vocab, uint32_t cols)
+{
+    return m <= kLossMaxRows && vocab >= 1 && vocab <= (1u << 22) && cols >= 8 && cols % 8 == 0 && cols <= kMaxCols;
+}
+
+bool loss_few(uint64_t m) { return m <= 64; }
+bool loss_large(uint64_t m, uint32_t vocab, uint32_t k)
+{
+    return tile_plan(ceil_div(m, 256) * ceil_div(vocab, 256), ceil_div(m, 128) * ceil_div(vocab, 128), ceil_div(k, kTileK), 0, true)
+        .large;
+}
+uint32_t loss_parts(uint64_t m, uint32_t vocab, uint32_t k)
+{
+    return (uint32_t)ceil_div(vocab, m == 1 ? 8 : loss_few(m) ? 32 : loss_large(m, vocab, k) ? 256 : 128);
+}
+uint64_t up256(uint64_t n) { return ceil_div(n, 256) * 256; }
+
+template <int T>
+void launch_loss(const LossArgs &g, hipStream_t stream)
+{
+    if (loss_few(g.m)) {
+        const bool split = g.k > 1024;
+        const dim3 grid((uint32_t)ceil_div(g.vocab, split ? 32 : 128));
+        if (split) hipLaunchKernelGGL((k_loss_few<T, true>), grid, dim3(256), 0, stream, g);
+        else hipLaunchKernelGGL((k_loss_few<T, false>), grid, dim3(256), 0, stream, g);
+    } else if (loss_large(g.m, g.vocab, g.k)) {
+        hipLaunchKernelGGL((k_loss<T, 256, 256>), dim3(xcd_grid(ceil_div(g.m, 256) * g.parts)), dim3(256), 0, stream, g);
+    } else {
+        hipLaunchKernelGGL((k_loss<T, 128, 128>), dim3(xcd_grid(ceil_div(g.m, 128) * g.parts)), dim3(256), 0, stream, g);
+    }
+    hipLaunchKernelGGL(k_loss_join, dim3(g.m), dim3(256), 0, stream, g);
+}
+
+struct LossGradPlan {
+    uint32_t piece;          // columns of the vocabulary
+    TilePlan dh, dw;
+    uint64_t live, rows, most, grad, dh_part, dw_part, bytes;  // offsets in the scratch
+    bool dh_sums;            // dH goes through fp32 sums
+};
+
+LossGradPlan loss_grad_plan(uint64_t m, uint32_t vocab, uint32_t k)
+{
+    LossGradPlan p{};
+    uint64_t piece = kLossPiece / m / 256 * 256;
+    if (piece < 256) piece = 256;
+    const uint64_t pieces = ceil_div(vocab, piece);
+    p.piece = (uint32_t)(pieces == 1 ? vocab : ceil_div(ceil_div(vocab, pieces), 256) * 256);
+    p.dh = tile_plan(ceil_div(m, 256) * ceil_div(k, 256), ceil_div(m, 128) * ceil_div(k, 128), ceil_div(p.piece, kTileK), m * k,
+                     pieces > 1);
+    p.dw = tile_plan(ceil_div(p.piece, 256) * ceil_div(k, 256), ceil_div(p.piece, 128) * ceil_div(k, 128), ceil_div(m, kTileK),
+                     (uint64_t)p.piece * k, false);
+    p.dh_sums = pieces > 1 || p.dh.splits > 1;
+    uint64_t at = 0;
+    auto take = [&](uint64_t bytes) {
+        const uint64_t here = at;
+        at = up256(at + bytes);
+        return here;
+    };
+    p.rows = take(16 * m);
+    p.most = take(4 * kLossRowBlocks);
+    p.live = take(2 * m * k);
+    p.grad = take(2 * m * ((p.piece + 7) / 8 * 8));
+    p.dh_part = take(p.dh_sums ? 4 * m * k * p.dh.splits : 0);
+    p.dw_part = take(part_bytes((uint64_t)p.piece * k, p.dw.splits));
+    p.bytes = at;
+    return p;
+}
+
+template <int T, bool kQAlong>
+void launch_product(const ProductArgs &g, bool large, hipStream_t stream)
+{
+    const uint64_t tile = large ? 256 : 128, tiles = ceil_div(g.m, tile) * ceil_div(g.n, tile) * g.splits;
+    if (large) hipLaunchKernelGGL((k_product<T, 256, 256, kQAlong>), dim3(xcd_grid(tiles)), dim3(256), 0, stream, g);
+    else hipLaunchKernelGGL((k_product<T, 128, 128, kQAlong>), dim3(xcd_grid(tiles)), dim3(256), 0, stream, g);
+}
+
+template <int T>
+void launch_loss_grad(const wc_linear_loss_grad &a, LossGradArgs g, const LossGradPlan &p, char *s, hipStream_t stream)
+{
+    hipLaunchKernelGGL(k_loss_rows, dim3(kLossRowBlocks), dim3(256), 0, stream, g);
+    float *dh_part = reinterpret_cast<float *>(s + p.dh_part), *dw_part = reinterpret_cast<float *>(s + p.dw_part);
+    for (uint64_t v0 = 0; v0 < g.vocab; v0 += p.piece) {
+        g.v0 = (uint32_t)v0;
+        g.width = (uint32_t)(g.vocab - v0 < p.piece ? g.vocab - v0 : p.piece);
+        g.pitch = (g.width + 7) / 8 * 8;
+        if (loss_few(g.m)) {
+            const bool split = g.k > 1024;
+            const dim3 grid((uint32_t)ceil_div(g.width, split ? 32 : 128));
+            if (split) hipLaunchKernelGGL((k_loss_grad_few<T, true>), grid, dim3(256), 0, stream, g);
+            else hipLaunchKernelGGL((k_loss_grad_few<T, false>), grid, dim3(256), 0, stream, g);
+        } else if (loss_large(g.m, p.piece, g.k)) {
+            const uint64_t tiles = ceil_div(g.m, 256) * ceil_div(g.width, 256);
+            hipLaunchKernelGGL((k_loss_grad<T, 256, 256>), dim3(xcd_grid(tiles)), dim3(256), 0, stream, g);
+        } else {
+            const uint64_t tiles = ceil_div(g.m, 128) * ceil_div(g.width, 128);
+            hipLaunchKernelGGL((k_loss_grad<T, 128, 128>), dim3(xcd_grid(tiles)), dim3(256), 0, stream, g);
+        }
+        if (a.grad_hidden) {
+            ProductArgs d{g.grad, g.w + v0 * g.w_row, g.pitch, g.w_row, g.m, g.k, g.width, p.dh.splits,
+                          p.dh_sums ? dh_part : nullptr, v0 ? 1u : 0u, static_cast<uint16_t *>(a.grad_hidden),
+                          a.grad_hidden_stride, g.most};
+            launch_product<T, true>(d, p.dh.large, stream);
+        }
+        if (a.grad_weight) {
+            uint16_t *out = static_cast<uint16_t *>(a.grad_weight) + v0 * g.k;
+            ProductArgs d{g.grad, g.live, g.pitch, g.k, g.width, g.k, g.m, p.dw.splits,
+                          p.dw.splits > 1 ? dw_part : nullptr, 0, out, g.k, g.most};
+            launch_product<T, false>(d, p.dw.large, stream);
+            if (p.dw.splits > 1) launch_join(T, JoinArgs{dw_part, out, g.k, g.width, g.k, p.dw.splits, nullptr, g.most}, stream);
+        }
+    }
+    if (a.grad_hidden && p.dh_sums)
+        launch_join(T, JoinArgs{dh_part, static_cast<uint16_t *>(a.grad_hidden), a.grad_hidden_stride, g.m, g.k, p.dh.splits,
+                                nullptr, g.most},
+                    stream);
+}
+
+bool rows16(const void *p, uint64_t stride, uint64_t width) { return p && aligned(p, 16) && stride >= width && stride % 8 == 0 && stride <= kMaxPitch; }
+
+}  // namespace
+
+extern "C" {
+
+uint64_t wc_grouped_linear_scratch(uint64_t m, uint32_t experts, uint32_t rows, uint32_t cols)
+{
+    if (m == 0 || !valid_grouped(m, experts, rows, cols) || grouped_few(m, experts)) return 0;
+    return part_bytes(m * rows, grouped_plan(m, experts, rows, cols).splits);
+}
+
+wc_status wc_grouped_linear(const wc_grouped *a, void *d_scratch, uint64_t scratch_bytes, uint32_t *d_err, hipStream_t stream)
+{
+    if (!a || (a->type != WC_T_BF16 && a->type != WC_T_FP16) || !valid_grouped(a->m, a->experts, a->rows, a->cols))
+        return WC_ERR_ARG;
+    if (d_err && !aligned(d_err, 4)) return WC_ERR_ARG;
+    if (a->m == 0) return WC_OK;
+    if (!rows16(a->x, a->x_stride, a->cols) || !rows16(a->w, a->w_row, a->cols) || a->w_expert % 8 ||
+        !rows16(a->y, a->y_stride, a->rows) || !a->ends || !aligned(a->ends, 8))
+        return WC_ERR_ARG;
+    if (!rows_apart(a->x, 2 * a->x_stride, 2ull * a->cols, a->y, 2 * a->y_stride, 2ull * a->rows, a->m)) return WC_ERR_ARG;
+    const uint64_t need = wc_grouped_linear_scratch(a->m, a->experts, a->rows, a->cols);
+    if (scratch_bytes < need) return WC_ERR_CAPACITY;
+    if (need && (!d_scratch || !aligned(d_scratch, 16))) return WC_ERR_ARG;
+    GroupedArgs g{};
+    g.x = static_cast<const uint16_t *>(a->x);
+    g.w = static_cast<const uint16_t *>(a->w);
+    g.ends = a->ends;
+    g.y = static_cast<uint16_t *>(a->y);
+    g.x_stride = a->x_stride;
+    g.w_expert = a->w_expert;
+    g.y_stride = a->y_stride;
+    g.w_row = (uint32_t)a->w_row;
+    g.m = (uint32_t)a->m;
+    g.experts = a->experts;
+    g.n = a->rows;
+    g.k = a->cols;
+    g.zero_rest = a->zero_rest;
+    g.splits = 1;
+    g.part = static_cast<float *>(d_scratch);
+    g.err = d_err;
+    return a->type == WC_T_BF16 ? launch_grouped_linear<WC_T_BF16>(g, stream) : launch_grouped_linear<WC_T_FP16>(g, stream);
+}
+
+uint64_t wc_grouped_linear_backward_scratch(uint64_t m, uint32_t experts, uint32_t rows, uint32_t cols)
+{
+    if (m == 0 || !valid_grouped(m, experts, rows, cols)) return 0;
+    // one after the other
+    const uint64_t dx = part_bytes(m * cols, grouped_plan(m, experts, cols, rows).splits);
+    const uint64_t dw = part_bytes((uint64_t)experts * rows * cols, grouped_dw_plan(m, experts, rows, cols).splits);
+    return dx > dw ? dx : dw;
+}
+
+wc_status wc_grouped_linear_backward(const wc_grouped_grad *a, void *d_scratch, uint64_t scratch_bytes, uint32_t *d_err,
+                                     hipStream_t stream)
+{
+    if (!a || (a->type != WC_T_BF16 && a->type != WC_T_FP16) || !valid_grouped(a->m, a->experts, a->rows, a->cols))
+        return WC_ERR_ARG;
+    if (d_err && !aligned(d_err, 4)) return WC_ERR_ARG;
+    if (!a->ends || !aligned(a->ends, 8) || (a->m && !rows16(a->grad, a->grad_stride, a->rows))) return WC_ERR_ARG;
+    if (a->m && a->grad_x && (!rows16(a->w, a->w_row, a->cols) || a->w_expert % 8 || !rows16(a->grad_x, a->grad_x_stride, a->cols) ||
+                              !rows_apart(a->grad, 2 * a->grad_stride, 2ull * a->rows, a->grad_x, 2 * a->grad_x_stride,
+                                          2ull * a->cols, a->m)))
+        return WC_ERR_ARG;
+    if (a->grad_w && (!aligned(a->grad_w, 16) || (a->m && !rows16(a->x, a->x_stride, a->cols)))) return WC_ERR_ARG;
+    const uint64_t need = wc_grouped_linear_backward_scratch(a->m, a->experts, a->rows, a->cols);
+    if (scratch_bytes < need) return WC_ERR_CAPACITY;
+    if (need && (!d_scratch || !aligned(d_scratch, 16))) return WC_ERR_ARG;
+    if (a->grad_x && a->m) {
+        GroupedArgs g{};
+        g.x = static_cast<const uint16_t *>(a->grad);
+        g.w = static_cast<const uint16_t *>(a->w);
+        g.ends = a->ends;
+        g.y = static_cast<uint16_t *>(a->grad_x);
+        g.x_stride = a->grad_stride;
+        g.w_expert = a->w_expert;
+        g.y_stride = a->grad_x_stride;
+        g.w_row = (uint32_t)a->w_row;
+        g.m = (uint32_t)a->m;
+        g.experts = a->experts;
+        g.n = a->cols;
+        g.k = a->rows;
+        g.zero_rest = a->zero_rest;
+        g.part = static_cast<float *>(d_scratch);
+        g.err = d_err;
+        const TilePlan p = grouped_plan(a->m, a->experts, a->cols, a->rows);
+        if (a->type == WC_T_BF16) launch_grouped<WC_T_BF16, false>(g, p, stream);
+        else launch_grouped<WC_T_FP16, false>(g, p, stream);
+    }
+    if (a->grad_w) {
+        GroupedDwArgs g{};
+        g.x = static_cast<const uint16_t *>(a->x);
+        g.dy = static_cast<const uint16_t *>(a->grad);
+        g.ends = a->ends;
+        g.dw = static_cast<uint16_t *>(a->grad_w);
+        g.x_stride = a->x_stride;
+        g.dy_stride = a->grad_stride;
+        g.m = (uint32_t)a->m;
+        g.experts = a->experts;
+        g.n = a->rows;
+        g.k = a->cols;
+        g.part = static_cast<float *>(d_scratch);
+        g.err = d_err;
+        const TilePlan p = grouped_dw_plan(a->m, a->experts, a->rows, a->cols);
+        if (a->type == WC_T_BF16) launch_grouped_dw<WC_T_BF16>(g, p, stream);
+        else launch_grouped_dw<WC_T_FP16>(g, p, stream);
+    }
+    return launched();
+}
+
+uint64_t wc_linear_cross_entropy_scratch(uint64_t m, uint32_t vocab, uint32_t cols)
+{
+    if (m == 0 || !valid_loss(m, vocab, cols)) return 0;
+    const uint64_t most = m < kLossSlice ? m : kLossSlice;
+    // of all the sets of launches: the last one's tiles may be smaller
+    uint64_t bytes = up256(8 * most * loss_parts(most, vocab, cols));
+    if (m > most && m % most) {
+        const uint64_t last = up256(8 * (m % most) * loss_parts(m % most, vocab, cols));
+        bytes = bytes > last ? bytes : last;
+    }
+    return bytes + up256(4 * most);
+}
+
+wc_status wc_linear_cross_entropy(const wc_linear_loss *a, void *d_scratch, uint64_t scratch_bytes, uint32_t *d_err,
+                                  hipStream_t stream)
+{
+    if (!a || (a->type != WC_T_BF16 && a->type != WC_T_FP16) || !valid_loss(a->m, a->vocab, a->cols)) return WC_ERR_ARG;
+    if (d_err && !aligned(d_err, 4)) return WC_ERR_ARG;
+    if (a->m == 0) return WC_OK;
+    if (!rows16(a->hidden, a->hidden_stride, a->cols) || !rows16(a->weight, a->weight_stride, a->cols) || !a->tokens ||
+        !aligned(a->tokens, 8) || !a->loss || !aligned(a->loss, 4) || !a->lse || !aligned(a->lse, 4))
+        return WC_ERR_ARG;
+    const uint64_t need = wc_linear_cross_entropy_scratch(a->m, a->vocab, a->cols);
+    if (scratch_bytes < need) return WC_ERR_CAPACITY;
+    if (!d_scratch || !aligned(d_scratch, 256)) return WC_ERR_ARG;
+    const uint64_t most = a->m < kLossSlice ? a->m : kLossSlice;
+    for (uint64_t r = 0; r < a->m; r += most) {
+        LossArgs g{};
+        g.h = static_cast<const uint16_t *>(a->hidden) + r * a->hidden_stride;
+        g.w = static_cast<const uint16_t *>(a->weight);
+        g.h_stride = a->hidden_stride;
+        g.w_row = (uint32_t)a->weight_stride;
+        g.tokens = a->tokens + r;
+        g.m = (uint32_t)(a->m - r < most ? a->m - r : most);
+        g.vocab = a->vocab;
+        g.k = a->cols;
+        g.parts = loss_parts(g.m, a->vocab, a->cols);
+        g.given = static_cast<float *>(d_scratch);
+        g.part = reinterpret_cast<float2 *>(static_cast<char *>(d_scratch) + up256(4 * most));
+        g.loss = a->loss + r;
+        g.lse = a->lse + r;
+        g.err = d_err;
+        if (a->type == WC_T_BF16) launch_loss<WC_T_BF16>(g, stream);
+        else launch_loss<WC_T_FP16>(g, stream);
+    }
+    return launched();
+}
+
+uint64_t wc_linear_cross_entropy_backward_scratch(uint64_t m, uint32_t vocab, uint32_t cols)
+{
+    if (m == 0 || !valid_loss(m, vocab, cols)) return 0;
+    return loss_grad_plan(m, vocab, cols).bytes;
+}
+
+wc_status wc_linear_cross_entropy_backward(const wc_linear_loss_grad *a, void *d_scratch, uint64_t scratch_bytes, uint32_t *d_err,
+                                           hipStream_t stream)
+{
+    if (!a || (a->type != WC_T_BF16 && a->type != WC_T_FP16) || a->m == 0 || !valid_loss(a->m, a->vocab, a->cols))
+        return WC_ERR_ARG;
+    if (d_err && !aligned(d_err, 4)) return WC_ERR_ARG;
+    if (!rows16(a->hidden, a->hidden_stride, a->cols) || !rows16(a->weight, a->weight_stride, a->cols) || !a->tokens ||
+        !aligned(a->tokens, 8) || !a->lse || !aligned(a->lse, 4) || !aligned(a->grad_loss, 4) || !aligned(a->grad_lse, 4))
+        return WC_ERR_ARG;
+    if (a->grad_hidden && !rows16(a->grad_hidden, a->grad_hidden_stride, a->cols)) return WC_ERR_ARG;
+    if (a->grad_weight && !aligned(a->grad_weight, 16)) return WC_ERR_ARG;
+    const LossGradPlan p = loss_grad_plan(a->m, a->vocab, a->cols);
+    if (scratch_bytes < p.bytes) return WC_ERR_CAPACITY;
+    if (!d_scratch || !aligned(d_scratch, 256)) return WC_ERR_ARG;
+    char *s = static_cast<char *>(d_scratch);
+    LossGradArgs g{};
+    g.h = static_cast<const uint16_t *>(a->hidden);
+    g.w = static_cast<const uint16_t *>(a->weight);
+    g.h_stride = a->hidden_stride;
+    g.w_row = (uint32_t)a->weight_stride;
+    g.tokens = a->tokens;
+    g.lse = a->lse;
+    g.grad_loss = a->grad_loss;
+    g.grad_lse = a->grad_lse;
+    g.m = (uint32_t)a->m;
+    g.vocab = a->vocab;
+    g.k = a->cols;
+    g.live = a->grad_weight ? reinterpret_cast<uint16_t *>(s + p.live) : nullptr;
+    g.rows = reinterpret_cast<f32x4 *>(s + p.rows);
+    g.most = reinterpret_cast<float *>(s + p.most);
+    g.grad = reinterpret_cast<uint16_t *>(s + p.grad);
+    g.err = d_err;
+    if (a->type == WC_T_BF16) launch_loss_grad<WC_T_BF16>(*a, g, p, s, stream);
+    else launch_loss_grad<WC_T_FP16>(*a, g, p, s, stream);
+    return launched();
+}
+
+}  // extern "C"

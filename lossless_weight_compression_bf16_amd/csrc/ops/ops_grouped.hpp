@@ -5,7 +5,7 @@
 //   k_grouped_few  y, for few rows of each expert
 //   k_grouped      y, or dx, by tiles of an expert's rows
 //   k_grouped_dw   dW, by tiles of an expert's weights
-//   k_join         sums of products that were split along k
+//   k_grouped_join, k_join  sums of products that were split along k
 // The ends stay on the device: a block finds its expert and rows from them by
 // itself (every wave adds up the experts' tiles by lane moves).
 #pragma once
@@ -29,8 +29,7 @@ struct GroupedArgs {
     uint32_t n, k;      // columns of y and of x
     uint32_t zero_rest; // rows behind the last expert's: zeros, else left as they are
     uint32_t slots;     // k_grouped_few
-    uint32_t splits;    // of k, each with its own m x n of part
-    float *part;
+    float *part;        // tiles in parts along k; or NULL: none
     uint32_t *err;
 };
 
@@ -68,18 +67,17 @@ __device__ __forceinline__ uint32_t wave_upto(uint32_t v)  // the sum of lanes 0
 // The experts' rows in units, of which each expert has units(count).  A wave's
 // view: lane l has the experts from per l on.
 struct Groups {
-    uint32_t per, mine, upto, total;
+    uint32_t per, mine, upto, total, lo, hi;  // lo, hi: of the lane's last expert
 
     template <class F>
     __device__ __forceinline__ void count(const GroupedArgs &g, F units)
     {
         const uint32_t lane = threadIdx.x & 63;
         per = (g.experts + 63) / 64;
-        mine = 0;
+        mine = lo = hi = 0;
         for (uint32_t q = 0; q < per; q++) {
             const uint32_t e = per * lane + q;
             if (e >= g.experts) break;
-            uint32_t lo, hi;
             group_rows(g.ends, e, g.m, lo, hi);
             mine += units(hi - lo);
         }
@@ -92,8 +90,8 @@ struct Groups {
                                          uint32_t &place) const
     {
         const uint32_t lane = threadIdx.x & 63, owner = (uint32_t)__builtin_ctzll(__ballot(upto > u));
-        uint32_t rest = u - (upto - mine), e = 0, from = 0, to = 0;
-        if (lane == owner)
+        uint32_t rest = u - (upto - mine), e = lane, from = this->lo, to = this->hi;
+        if (per > 1 && lane == owner)
             for (uint32_t q = 0; q < per; q++) {
                 e = per * lane + q;
                 group_rows(g.ends, e, g.m, from, to);
@@ -108,50 +106,124 @@ struct Groups {
     }
 };
 
-// y (kPAlong) or dx by tiles: an expert's rows in tiles of BM against tiles of
-// BN columns.  Grid: 8 ceil(tiles / 8) for the most tiles there can be, which is one
-// more for each expert than the rows fill.
-template <int T, int BM, int BN, bool kPAlong>
-__global__ __launch_bounds__(256, BM + BN > 384 ? 1 : 2) void k_grouped(GroupedArgs g)
-{
-    using Ti = Tile<T, BM, BN, 2, 2, true, kPAlong>;
-    __shared__ __attribute__((aligned(1024))) char q0[Ti::Q::kBytes];
-    __shared__ __attribute__((aligned(1024))) char p0[Ti::P::kBytes];
-    __shared__ __attribute__((aligned(1024))) char q1[Ti::Q::kBytes];
-    __shared__ __attribute__((aligned(1024))) char p1[Ti::P::kBytes];
-    check_ends(g.ends, g.experts, g.m, g.err);
-    auto tiles = [](uint32_t rows) { return (rows + BM - 1) / BM; };
+// The tiles of y or dx, and how they are dealt to the blocks.  As many whole ones
+// as fill the compute units some number of times; the tiles that are left, if they
+// would leave half of the compute units or more without one, in parts along
+// k, whose sums k_grouped_join adds up; then tiles of the rows behind the
+// last expert's, which are only to be zeros.
+template <int BM, int BN>
+struct GroupedPieces {
+    static constexpr uint32_t kSlots = kCus * tile_blocks(BM, BN);
     Groups groups;
-    groups.count(g, tiles);
-    const uint32_t last = group_end(g.ends, g.experts - 1, g.m), rest = g.zero_rest ? tiles(g.m - last) : 0;
-    const uint32_t down = groups.total + rest, across = (g.n + BN - 1) / BN, t = xcd_piece(blockIdx.x, down * across * g.splits);
-    if (t >= down * across * g.splits) return;
-    const uint32_t split = t / (down * across);
-    uint32_t r, c, expert = 0, lo = 0, hi = 0, place = 0;
-    tile_of(t % (down * across), down, across, r, c);
-    const bool zero = r >= groups.total;
-    if (zero) {
-        lo = last;
-        hi = g.m;
-        place = r - groups.total;
-    } else {
-        groups.find(g, r, tiles, expert, lo, hi, place);
+    uint32_t last, down, across, whole, left, splits, stages, zeros;
+
+    __device__ __forceinline__ static uint32_t tiles(uint32_t rows) { return (rows + BM - 1) / BM; }
+
+    __device__ __forceinline__ void init(const GroupedArgs &g)
+    {
+        groups.count(g, tiles);
+        last = group_end(g.ends, g.experts - 1, g.m);
+        down = groups.total;
+        across = (g.n + BN - 1) / BN;
+        stages = (g.k + kTileK - 1) / kTileK;
+        const uint32_t all = down * across;
+        whole = all / kSlots * kSlots;
+        left = all - whole;
+        // at least 8 stages in a part
+        splits = g.part && left ? max(1u, min(min(kSlots / left, stages / 8), 16u)) : 1u;
+        zeros = g.zero_rest ? tiles(g.m - last) * across : 0u;
     }
-    if ((uint64_t)place * BM >= hi - lo) return;  // bad ends
-    const uint32_t m0 = lo + BM * place, rows = min((uint32_t)BM, hi - m0), n0 = BN * c;
-    const uint32_t stages = (g.k + kTileK - 1) / kTileK, s0 = stages * split / g.splits, s1 = stages * (split + 1) / g.splits;
-    const uint32_t k0 = kTileK * s0, k = zero || s0 >= s1 ? 0 : min(g.k, kTileK * s1) - k0;
+    // Block b's kind of piece (0: whole tile, 1: part, 2: zeros, 3: none) and its number,
+    // every XCD with a contiguous range of each kind.
+    __device__ __forceinline__ uint32_t piece(uint32_t b, uint32_t &t) const
+    {
+        uint32_t at = b / 8;
+        if (at < whole / 8) {
+            t = b % 8 * (whole / 8) + at;
+            return 0;
+        }
+        at -= whole / 8;
+        const uint32_t parts = (left * splits + 7) / 8, behind = (zeros + 7) / 8;
+        if (at < parts) {
+            t = b % 8 * parts + at;
+            return t < left * splits ? 1 : 3;
+        }
+        at -= parts;
+        t = b % 8 * behind + at;
+        return at < behind && t < zeros ? 2 : 3;
+    }
+    // The expert, rows and first column of tile t.
+    __device__ __forceinline__ bool tile(const GroupedArgs &g, uint32_t t, uint32_t &expert, uint32_t &m0, uint32_t &rows,
+                                         uint32_t &n0) const
+    {
+        uint32_t r, c, lo, hi, place;
+        tile_of(t, down, across, r, c);
+        groups.find(g, r, tiles, expert, lo, hi, place);
+        m0 = lo + BM * place;
+        n0 = BN * c;
+        if ((uint64_t)place * BM >= hi - lo) return false;  // bad ends
+        rows = min((uint32_t)BM, hi - m0);
+        return true;
+    }
+};
+
+// y (kPAlong) or dx by tiles: an expert's rows in tiles of BM against tiles of
+// BN columns.  Grid: 8 ceil(tiles / 8) for the most pieces there can be.
+template <int T, int BM, int BN, bool kPAlong>
+__global__ __launch_bounds__(256, tile_blocks(BM, BN)) void k_grouped(GroupedArgs g)
+{
+    using Ti = Tile<T, BM, BN, true, kPAlong>;
+    __shared__ __attribute__((aligned(1024))) char b0[Ti::kBytes];
+    __shared__ __attribute__((aligned(1024))) char b1[Ti::kBytes];
+    check_ends(g.ends, g.experts, g.m, g.err);
+    GroupedPieces<BM, BN> p;
+    p.init(g);
+    uint32_t t, expert, m0, rows, n0;
+    const uint32_t kind = p.piece(blockIdx.x, t);
+    if (kind == 3) return;
+    if (kind == 2) {
+        m0 = p.last + BM * (t / p.across);
+        n0 = BN * (t % p.across);
+        const uint32_t cols = min((uint32_t)BN, g.n - n0) / 8;
+        for (uint32_t q = threadIdx.x; q < min((uint32_t)BM, g.m - m0) * cols; q += 256)
+            *reinterpret_cast<u32x4 *>(g.y + (m0 + q / cols) * g.y_stride + n0 + 8 * (q % cols)) = u32x4{0, 0, 0, 0};
+        return;
+    }
+    const uint32_t split = kind ? t / p.left : 0, splits = kind ? p.splits : 1;
+    if (!p.tile(g, kind ? p.whole + t % p.left : t, expert, m0, rows, n0)) return;
+    const uint32_t k0 = kTileK * (p.stages * split / splits), k = min(g.k, kTileK * (p.stages * (split + 1) / splits)) - k0;
     const uint16_t *w = g.w + expert * g.w_expert;
     Ti ti;
     ti.q.init(g.x + m0 * g.x_stride + k0, g.x_stride, rows, k);
     if constexpr (kPAlong) ti.p.init(w + (uint64_t)n0 * g.w_row + k0, g.w_row, min((uint32_t)BN, g.n - n0), k);
     else ti.p.init(w + (uint64_t)k0 * g.w_row + n0, g.w_row, k, g.n - n0);
-    ti.product(q0, p0, q1, p1, k);
+    ti.product(b0, b1, nullptr, k, rows);
+    float *part = g.part + (uint64_t)t * (BM * BN);
     each_four(ti, [&](uint32_t row, uint32_t col, f32x4 v) {
         if (row >= rows || n0 + col >= g.n) return;
-        if (g.splits > 1) *reinterpret_cast<f32x4 *>(g.part + ((uint64_t)split * g.m + m0 + row) * g.n + n0 + col) = v;
+        if (splits > 1) *reinterpret_cast<f32x4 *>(part + row * BN + col) = v;
         else store_four<T>(g.y + (m0 + row) * g.y_stride + n0 + col, v);
     });
+}
+
+// The sums of the tiles in parts, in the order of k.  Grid: kSlots / 2 tiles, and 8 blocks for each.
+template <int T, int BM, int BN>
+__global__ __launch_bounds__(256) void k_grouped_join(GroupedArgs g)
+{
+    GroupedPieces<BM, BN> p;
+    p.init(g);
+    const uint32_t q = blockIdx.x / 8;
+    uint32_t expert, m0, rows, n0;
+    if (p.splits == 1 || q >= p.left || !p.tile(g, p.whole + q, expert, m0, rows, n0)) return;
+    const uint32_t from = BM / 8 * (blockIdx.x % 8);
+    for (uint32_t e = threadIdx.x; e < BM / 8 * BN / 4; e += 256) {
+        const uint32_t row = from + e / (BN / 4), col = 4 * (e % (BN / 4));
+        if (row >= rows || n0 + col >= g.n) continue;
+        const float *part = g.part + (uint64_t)q * (BM * BN) + row * BN + col;
+        f32x4 v = *reinterpret_cast<const f32x4 *>(part);
+        for (uint32_t s = 1; s < p.splits; s++) v += *reinterpret_cast<const f32x4 *>(part + (uint64_t)s * p.left * (BM * BN));
+        store_four<T>(g.y + (m0 + row) * g.y_stride + n0 + col, v);
+    }
 }
 
 struct GroupedDwArgs {
@@ -165,20 +237,20 @@ struct GroupedDwArgs {
     uint32_t *err;
 };
 
-// dW by tiles of BM rows and BN columns of it.  Grid: 8 ceil(tiles / 8).
+// dW by tiles of BM rows and BN columns of it.  Grid: experts x 8 ceil(tiles of one / 8).
 template <int T, int BM, int BN>
-__global__ __launch_bounds__(256, BM + BN > 384 ? 1 : 2) void k_grouped_dw(GroupedDwArgs g)
+__global__ __launch_bounds__(256, tile_blocks(BM, BN)) void k_grouped_dw(GroupedDwArgs g)
 {
-    using Ti = Tile<T, BM, BN, 2, 2, false, false>;
-    __shared__ __attribute__((aligned(1024))) char q0[Ti::Q::kBytes];
-    __shared__ __attribute__((aligned(1024))) char p0[Ti::P::kBytes];
-    __shared__ __attribute__((aligned(1024))) char q1[Ti::Q::kBytes];
-    __shared__ __attribute__((aligned(1024))) char p1[Ti::P::kBytes];
+    using Ti = Tile<T, BM, BN, false, false>;
+    __shared__ __attribute__((aligned(1024))) char b0[Ti::kBytes];
+    __shared__ __attribute__((aligned(1024))) char b1[Ti::kBytes];
     check_ends(g.ends, g.experts, g.m, g.err);
     const uint32_t down = (g.n + BM - 1) / BM, across = (g.k + BN - 1) / BN, each = down * across;
-    const uint32_t t = xcd_piece(blockIdx.x, each * g.experts * g.splits);
-    if (t >= each * g.experts * g.splits) return;
-    const uint32_t expert = t / (each * g.splits), split = t / each % g.splits;
+    // every XCD has an eighth of each expert: the experts have different numbers of rows
+    const uint32_t pieces = each * g.splits, per = (pieces + 7) / 8, expert = blockIdx.x / 8 / per;
+    const uint32_t t = blockIdx.x % 8 * per + blockIdx.x / 8 % per;
+    if (expert >= g.experts || t >= pieces) return;
+    const uint32_t split = t / each;
     uint32_t r, c, lo, hi;
     tile_of(t % each, down, across, r, c);
     group_rows(g.ends, expert, g.m, lo, hi);
@@ -189,7 +261,7 @@ __global__ __launch_bounds__(256, BM + BN > 384 ? 1 : 2) void k_grouped_dw(Group
     Ti ti;
     ti.q.init(g.dy + from * g.dy_stride + m0, g.dy_stride, rows, g.n - m0);
     ti.p.init(g.x + from * g.x_stride + n0, g.x_stride, rows, g.k - n0);
-    ti.product(q0, p0, q1, p1, rows);
+    ti.product(b0, b1, nullptr, rows);
     const uint64_t all = (uint64_t)g.experts * g.n * g.k;
     each_four(ti, [&](uint32_t row, uint32_t col, f32x4 v) {
         if (m0 + row >= g.n || n0 + col >= g.k) return;
@@ -201,29 +273,32 @@ __global__ __launch_bounds__(256, BM + BN > 384 ? 1 : 2) void k_grouped_dw(Group
 
 constexpr uint32_t kLossRowBlocks = 256;
 
-// What numbers are multiplied by where they are FP16 (term_scale), from the
-// largest of each of kLossRowBlocks parts; 1 for BF16.
+// What G is multiplied by before it is rounded: 1 (BF16) or 2^14 (FP16) over the
+// largest gradient of a row, from the largest of each of kLossRowBlocks parts.  So
+// where all rows have the same one, as under a mean, what it is has no rounding
+// of its own (a mean over 3584 rows, BF16: the gradients 0.26% off, mostly all by the same
+// factor, and 0.18% so), and FP16 numbers stay in range.
 template <int T>
 __device__ __forceinline__ float loss_scale(const float *most, float &unscale)
 {
-    unscale = 1.f;
-    if (T != WC_T_FP16) return 1.f;
+    constexpr float kTop = T == WC_T_FP16 ? 16384.f : 1.f;
     float v = 0.f;
 #pragma unroll
     for (uint32_t q = 0; q < kLossRowBlocks / 64; q++) v = fmaxf(v, most[64 * q + (threadIdx.x & 63)]);
-    return term_scale<T>(wave_max(v), unscale);
+    v = wave_max(v);
+    if (!(v > 0x1p-100f && v < 0x1p100f)) return term_scale<T>(v, unscale);
+    unscale = v * (1.f / kTop);
+    return kTop / v;
 }
 
 // out = the sum of `splits` parts of rows x cols each, in their order.
-// Rows from `rows_end` on (ends[experts - 1] where that is given) are left as they are.
 struct JoinArgs {
     const float *part;
     uint16_t *out;
     uint64_t out_stride;
     uint64_t rows;
     uint32_t cols, splits;
-    const int64_t *last;   // or NULL
-    const float *most;     // or NULL: what FP16 numbers were scaled by (loss_scale)
+    const float *most;     // or NULL: what the numbers were scaled by (loss_scale)
 };
 
 template <int T>
@@ -233,12 +308,12 @@ __global__ __launch_bounds__(256) void k_join(JoinArgs g)
     if (g.most) loss_scale<T>(g.most, unscale);
     const uint32_t per = g.cols / 4;
     const uint64_t q = (uint64_t)blockIdx.x * 256 + threadIdx.x, row = q / per;
-    if (row >= g.rows || (g.last && (int64_t)row >= *g.last)) return;
+    if (row >= g.rows) return;
     const uint32_t col = 4 * (uint32_t)(q % per);
     const float *p = g.part + row * g.cols + col;
     f32x4 v = *reinterpret_cast<const f32x4 *>(p);
     for (uint32_t s = 1; s < g.splits; s++) v += *reinterpret_cast<const f32x4 *>(p + s * g.rows * g.cols);
-    if (T == WC_T_FP16 && g.most) v *= unscale;
+    v *= unscale;
     store_four<T>(g.out + row * g.out_stride + col, v);
 }
 
@@ -247,7 +322,7 @@ __global__ __launch_bounds__(256) void k_join(JoinArgs g)
 template <int T, int NT>
 __device__ __forceinline__ void few_rows(const uint16_t *w, uint32_t pitch, uint32_t n, const uint32_t (&first)[2],
                                          const uint16_t *x, uint64_t x_stride, uint32_t count, uint32_t c0, uint32_t c1,
-                                         Strip *strips, f32x4 (&sum)[2][4])
+                                         Strip *strips, f32x4 (&sum)[2][2])
 {
     const uint32_t i = threadIdx.x & 15, rows = min(16u, n);
     const uint16_t *const weights[2] = {w + (uint64_t)first[0] * pitch, w + (uint64_t)first[1] * pitch};
@@ -264,7 +339,7 @@ __device__ __forceinline__ void few_rows(const uint16_t *w, uint32_t pitch, uint
         for (int m = 0; m < 2; m++) sum[m][t] = acc[m][0][t];
 }
 
-// 32 rows of weights (n of them in all) from n0 on against `count` <= 64 rows of
+// 32 rows of weights (n of them in all) from n0 on against `count` <= 32 rows of
 // x, columns of all k.  kSplit: the block's four waves share the columns, and
 // f(t, sums) is called by the wave t with the sums of 16 rows of x; otherwise the rows
 // are the wave's own, and it calls f for every t.  sums[m]: the lane's four
@@ -277,21 +352,20 @@ __device__ __forceinline__ void few_product(const uint16_t *w, uint32_t pitch, u
     const uint32_t most = n < 16 ? 0 : n - 16, first[2] = {min(n0, most), min(n0 + 16, most)};
     uint32_t c0 = 0, c1 = k;
     if (kSplit) wave_quarter(k, kStripCols, wave, c0, c1);
-    f32x4 sum[2][4];
+    f32x4 sum[2][2];
     const uint32_t tiles = (count + 15) / 16;
     if (tiles <= 1) few_rows<T, 1>(w, pitch, n, first, x, x_stride, count, c0, c1, strips[wave], sum);
-    else if (tiles <= 2) few_rows<T, 2>(w, pitch, n, first, x, x_stride, count, c0, c1, strips[wave], sum);
-    else few_rows<T, 4>(w, pitch, n, first, x, x_stride, count, c0, c1, strips[wave], sum);
+    else few_rows<T, 2>(w, pitch, n, first, x, x_stride, count, c0, c1, strips[wave], sum);
     if constexpr (!kSplit) {
 #pragma unroll
-        for (uint32_t t = 0; t < 4; t++)
+        for (uint32_t t = 0; t < 2; t++)
             if (t < tiles) f(t, first, sum[0][t], sum[1][t]);
     } else {
-        f32x4(*part)[8][64] = reinterpret_cast<f32x4(*)[8][64]>(&strips[0][0]);  // [4], when the strips are done
-        static_assert(sizeof(Strip) * 8 >= 4 * 8 * 64 * 16, "the waves' sums fit into the strips");
+        f32x4(*part)[4][64] = reinterpret_cast<f32x4(*)[4][64]>(&strips[0][0]);  // [4], when the strips are done
+        static_assert(sizeof(Strip) * 8 >= 4 * 4 * 64 * 16, "the waves' sums fit into the strips");
         __syncthreads();
 #pragma unroll
-        for (uint32_t t = 0; t < 4; t++)
+        for (uint32_t t = 0; t < 2; t++)
             if (t < tiles) {
                 part[wave][2 * t][lane] = sum[0][t];
                 part[wave][2 * t + 1][lane] = sum[1][t];
@@ -336,7 +410,7 @@ __device__ __forceinline__ void one_product(const uint16_t *w, uint32_t pitch, u
 
 // y for experts with few rows: a block has 32 rows of weights (128 without
 // kSplit) of the slot-th expert that has rows.  Reading the weights is the
-// bound, so they go in whole lines past the caches, and 64 rows of x meet them
+// bound, so they go in whole lines past the caches, and 32 rows of x meet them
 // at a time; a single one meets them without the matrix cores.  Grid: slots x ceil(n / 32
 // or 128); one slot more where the rows behind the last expert's are to be zeros.
 template <int T, bool kSplit>
@@ -362,8 +436,8 @@ __global__ __launch_bounds__(256, 2) void k_grouped_few(GroupedArgs g)
     }
     groups.find(g, slot, any, expert, lo, hi, place);
     const uint16_t *w = g.w + expert * g.w_expert;
-    for (uint32_t r0 = lo; r0 < hi; r0 += 64) {
-        const uint32_t count = min(64u, hi - r0);
+    for (uint32_t r0 = lo; r0 < hi; r0 += 32) {
+        const uint32_t count = min(32u, hi - r0);
         const uint16_t *x = g.x + r0 * g.x_stride;
         if (count == 1) {
             uint16_t *y = g.y + r0 * g.y_stride;

@@ -4,7 +4,7 @@
 //   G_rv = (gl_r + gz_r) exp(z_rv - lse_r) - gl_r [v = t_r],  dH = G W,  dW = G^T H
 // with gl and gz the gradients of loss and lse (gl = 0 where there is no token).
 //
-//   k_loss_few, k_loss        statistics (largest logit, sum of exponentials) of 32, 128 or 256 columns of z
+//   k_loss_few, k_loss        statistics (largest logit, sum of exponentials) of a tile of z
 //   k_loss_join               lse and loss of a row from them
 //   k_loss_rows               what the gradient needs of a row, and H without the rows that have no part in it
 //   k_loss_grad_few, k_loss_grad  G of a piece of the vocabulary: z again, then the formula
@@ -47,14 +47,12 @@ struct Stat {
 
 // Statistics of a block's tile: rows of m0, columns of n0 on.
 template <int T, int BM, int BN>
-__global__ __launch_bounds__(256, BM + BN > 384 ? 1 : 2) void k_loss(LossArgs g)
+__global__ __launch_bounds__(256, tile_blocks(BM, BN)) void k_loss(LossArgs g)
 {
-    using Ti = Tile<T, BM, BN, 2, 2, true, true>;
-    __shared__ __attribute__((aligned(1024))) char q0[Ti::Q::kBytes];
-    __shared__ __attribute__((aligned(1024))) char p0[Ti::P::kBytes];
-    __shared__ __attribute__((aligned(1024))) char q1[Ti::Q::kBytes];
-    __shared__ __attribute__((aligned(1024))) char p1[Ti::P::kBytes];
-    float2(*stats)[BM] = reinterpret_cast<float2(*)[BM]>(q0);  // [2], when the operands are done
+    using Ti = Tile<T, BM, BN, true, true>;
+    __shared__ __attribute__((aligned(1024))) char b0[Ti::kBytes];
+    __shared__ __attribute__((aligned(1024))) char b1[Ti::kBytes];
+    float2(*stats)[BM] = reinterpret_cast<float2(*)[BM]>(b0);  // a wave's, when the operands are done
     const uint32_t down = (g.m + BM - 1) / BM, t = xcd_piece(blockIdx.x, down * g.parts);
     if (t >= down * g.parts) return;
     uint32_t r, c;
@@ -64,17 +62,17 @@ __global__ __launch_bounds__(256, BM + BN > 384 ? 1 : 2) void k_loss(LossArgs g)
     Ti ti;
     ti.q.init(g.h + m0 * g.h_stride, g.h_stride, rows, g.k);
     ti.p.init(g.w + (uint64_t)n0 * g.w_row, g.w_row, cols, g.k);
-    ti.product(q0, p0, q1, p1, g.k);
+    ti.product(b0, b1, nullptr, g.k, rows);
 #pragma unroll
     for (int b = 0; b < Ti::kM; b++) {
-        const uint32_t row = 16 * (wave / 2 + 2 * b) + i, first = 16 * (wave % 2) + 4 * gr;
+        const uint32_t row = 16 * (wave / Ti::kWavesN + Ti::kWavesM * b) + i, first = 16 * (wave % Ti::kWavesN) + 4 * gr;
         const int64_t token = row < rows ? g.tokens[m0 + row] - n0 : -1;
         Stat s{-kInf, 0.f};
 #pragma unroll
         for (int a = 0; a < Ti::kN; a++)
 #pragma unroll
             for (int e = 0; e < 4; e++) {
-                const uint32_t col = first + 32 * a + e;
+                const uint32_t col = first + 16 * Ti::kWavesN * a + e;
                 const float z = ti.acc[a][b][e];
                 if (col < cols) s.most = fmaxf(s.most, z);
                 if (token == (int64_t)col && col < cols) g.given[m0 + row] = z;
@@ -84,83 +82,108 @@ __global__ __launch_bounds__(256, BM + BN > 384 ? 1 : 2) void k_loss(LossArgs g)
         for (int a = 0; a < Ti::kN; a++)
 #pragma unroll
             for (int e = 0; e < 4; e++)
-                if (first + 32 * a + e < cols) s.sum += exp2_fast((ti.acc[a][b][e] - base) * kLog2e);
+                if (first + 16 * Ti::kWavesN * a + e < cols) s.sum += exp2_fast((ti.acc[a][b][e] - base) * kLog2e);
         s.join(__shfl_xor(s.most, 16, 64), __shfl_xor(s.sum, 16, 64));
         s.join(__shfl_xor(s.most, 32, 64), __shfl_xor(s.sum, 32, 64));
-        if (gr == 0) stats[wave % 2][row] = float2{s.most, s.sum};
+        if (gr == 0) stats[wave % Ti::kWavesN][row] = float2{s.most, s.sum};
     }
     __syncthreads();
     if (threadIdx.x < rows) {
-        const float2 one = stats[0][threadIdx.x], two = stats[1][threadIdx.x];
-        Stat s{one.x, one.y};
-        s.join(two.x, two.y);
+        Stat s{stats[0][threadIdx.x].x, stats[0][threadIdx.x].y};
+#pragma unroll
+        for (int w = 1; w < Ti::kWavesN; w++) s.join(stats[w][threadIdx.x].x, stats[w][threadIdx.x].y);
         g.part[(uint64_t)(m0 + threadIdx.x) * g.parts + c] = float2{s.most, s.sum};
     }
 }
 
-// The same for up to 64 rows: 32 columns of z for a block (128 without kSplit).
+// The same for up to 32 rows: 32 columns of z for a block (128 without kSplit).
 template <int T, bool kSplit>
 __global__ __launch_bounds__(256, 2) void k_loss_few(LossArgs g)
 {
     __shared__ Strip strips[4][2];
-    const uint32_t wave = threadIdx.x >> 6, i = threadIdx.x & 15, gr = (threadIdx.x & 63) >> 4;
-    const uint32_t part = kSplit ? blockIdx.x : 4 * blockIdx.x + wave, n0 = 32 * part;
+    __shared__ float2 stats[4][32];
+    const uint32_t wave = threadIdx.x >> 6, lane = threadIdx.x & 63, i = lane & 15, gr = lane >> 4;
+    const uint32_t n0 = kSplit ? 32 * blockIdx.x : 128 * blockIdx.x + 32 * wave;
+    constexpr uint32_t kShares = kSplit ? 1 : 4;  // waves with statistics of the same row
     if (g.m == 1) {
         const int64_t token = g.tokens[0];
+        Stat s{-kInf, 0.f};
         for (uint32_t q = 0; q < (kSplit ? 1 : 4); q++) {
             const uint32_t n = n0 + 8 * (kSplit ? wave : q);
             if (n >= g.vocab) break;
             float mine = -kInf;
-            one_product<T>(g.w, g.w_row, g.vocab, n, g.k, g.h, [&](uint32_t v, float sum) {
-                mine = sum;
-                if ((int64_t)v == token) g.given[0] = sum;
+            one_product<T>(g.w, g.w_row, g.vocab, n, g.k, g.h, [&](uint32_t v, float z) {
+                mine = z;
+                if ((int64_t)v == token) g.given[0] = z;
             });
-            const float most = wave_max(mine);
-            const float sum = wave_sum((threadIdx.x & 63) < 8 && n + (threadIdx.x & 63) < g.vocab
-                                           ? exp2_fast((mine - Stat::base(most)) * kLog2e) : 0.f);
-            if ((threadIdx.x & 63) == 0) g.part[n / 8] = float2{most, sum};
+            const float most = wave_max(mine), base = Stat::base(most);
+            s.join(most, wave_sum(lane < 8 && n + lane < g.vocab ? exp2_fast((mine - base) * kLog2e) : 0.f));
         }
-        return;
+        if (lane == 0) stats[wave][0] = float2{s.most, s.sum};
+    } else if (kSplit || n0 < g.vocab) {
+        few_product<T, kSplit>(g.w, g.w_row, g.vocab, n0, g.k, g.h, g.h_stride, g.m, strips,
+                               [&](uint32_t t, const uint32_t(&first)[2], f32x4 v0, f32x4 v1) {
+                                   const uint32_t row = 16 * t + i;
+                                   const int64_t token = row < g.m ? g.tokens[row] : -1;
+                                   Stat s{-kInf, 0.f};
+#pragma unroll
+                                   for (int m = 0; m < 2; m++)
+#pragma unroll
+                                       for (uint32_t e = 0; e < 4; e++) {
+                                           const uint32_t v = first[m] + 4 * gr + e;
+                                           const float z = m ? v1[e] : v0[e];
+                                           if (v < n0 + 16 * m || v >= g.vocab) continue;  // of the rows before
+                                           s.most = fmaxf(s.most, z);
+                                           if (token == (int64_t)v) g.given[row] = z;
+                                       }
+                                   const float base = Stat::base(s.most);
+#pragma unroll
+                                   for (int m = 0; m < 2; m++)
+#pragma unroll
+                                       for (uint32_t e = 0; e < 4; e++) {
+                                           const uint32_t v = first[m] + 4 * gr + e;
+                                           if (v < n0 + 16 * m || v >= g.vocab) continue;
+                                           s.sum += exp2_fast(((m ? v1[e] : v0[e]) - base) * kLog2e);
+                                       }
+                                   s.join(__shfl_xor(s.most, 16, 64), __shfl_xor(s.sum, 16, 64));
+                                   s.join(__shfl_xor(s.most, 32, 64), __shfl_xor(s.sum, 32, 64));
+                                   if (gr == 0) stats[kSplit ? 0 : wave][row] = float2{s.most, s.sum};
+                               });
+    } else if (lane < 32) {
+        stats[wave][lane] = float2{-kInf, 0.f};
     }
-    if (!kSplit && n0 >= g.vocab) return;
-    few_product<T, kSplit>(g.w, g.w_row, g.vocab, n0, g.k, g.h, g.h_stride, g.m, strips,
-                           [&](uint32_t t, const uint32_t(&first)[2], f32x4 v0, f32x4 v1) {
-                               const uint32_t row = 16 * t + i;
-                               const int64_t token = row < g.m ? g.tokens[row] : -1;
-                               Stat s{-kInf, 0.f};
+    __syncthreads();
+    if (threadIdx.x < g.m) {
+        Stat s{-kInf, 0.f};
 #pragma unroll
-                               for (int m = 0; m < 2; m++)
-#pragma unroll
-                                   for (uint32_t e = 0; e < 4; e++) {
-                                       const uint32_t v = first[m] + 4 * gr + e;
-                                       const float z = m ? v1[e] : v0[e];
-                                       if (v < n0 + 16 * m || v >= g.vocab) continue;  // of the rows before
-                                       s.most = fmaxf(s.most, z);
-                                       if (token == (int64_t)v) g.given[row] = z;
-                                   }
-                               const float base = Stat::base(s.most);
-#pragma unroll
-                               for (int m = 0; m < 2; m++)
-#pragma unroll
-                                   for (uint32_t e = 0; e < 4; e++) {
-                                       const uint32_t v = first[m] + 4 * gr + e;
-                                       if (v < n0 + 16 * m || v >= g.vocab) continue;
-                                       s.sum += exp2_fast(((m ? v1[e] : v0[e]) - base) * kLog2e);
-                                   }
-                               s.join(__shfl_xor(s.most, 16, 64), __shfl_xor(s.sum, 16, 64));
-                               s.join(__shfl_xor(s.most, 32, 64), __shfl_xor(s.sum, 32, 64));
-                               if (gr == 0 && row < g.m) g.part[(uint64_t)row * g.parts + part] = float2{s.most, s.sum};
-                           });
+        for (uint32_t w = 0; w < 4; w++)
+            if (w < kShares || g.m == 1) s.join(stats[w][threadIdx.x].x, stats[w][threadIdx.x].y);
+        g.part[(uint64_t)threadIdx.x * g.parts + blockIdx.x] = float2{s.most, s.sum};
+    }
 }
 
 // One block per row.
 __global__ __launch_bounds__(256) void k_loss_join(LossArgs g)
 {
+    constexpr uint32_t kAtOnce = 8;  // parts of a thread whose loads are on their way together
     __shared__ float2 waves[4];
     const uint32_t r = blockIdx.x;
     const float2 *p = g.part + (uint64_t)r * g.parts;
+    const int64_t t = g.tokens[r];
+    const float given = g.given[r];  // not used, and not written, without a token
     Stat s{-kInf, 0.f};
-    for (uint32_t q = threadIdx.x; q < g.parts; q += 256) s.join(p[q].x, p[q].y);
+    for (uint32_t q0 = threadIdx.x; q0 < g.parts; q0 += 256 * kAtOnce) {
+        float2 v[kAtOnce];
+        float most = -kInf, sum = 0.f;
+#pragma unroll
+        for (uint32_t q = 0; q < kAtOnce; q++) v[q] = p[min(q0 + 256 * q, g.parts - 1)];
+#pragma unroll
+        for (uint32_t q = 0; q < kAtOnce; q++) most = fmaxf(most, v[q].x);
+#pragma unroll
+        for (uint32_t q = 0; q < kAtOnce; q++)
+            if (q0 + 256 * q < g.parts) sum += v[q].y * exp2_fast((v[q].x - Stat::base(most)) * kLog2e);
+        s.join(most, sum);
+    }
 #pragma unroll
     for (int o = 1; o < 64; o *= 2) s.join(__shfl_xor(s.most, o, 64), __shfl_xor(s.sum, o, 64));
     if ((threadIdx.x & 63) == 0) waves[threadIdx.x >> 6] = float2{s.most, s.sum};
@@ -169,12 +192,12 @@ __global__ __launch_bounds__(256) void k_loss_join(LossArgs g)
 #pragma unroll
     for (int w = 1; w < 4; w++) s.join(waves[w].x, waves[w].y);
     const float log_sum = __builtin_amdgcn_logf(s.sum) * kLn2;
-    g.lse[r] = s.most == -kInf && s.sum == 0.f ? -kInf : s.most + log_sum;
-    const int64_t t = g.tokens[r];
+    const bool nothing = s.most == -kInf && s.sum == 0.f;
+    g.lse[r] = nothing ? -kInf : s.most + log_sum;
     float loss = 0.f;
     if (t >= 0 && t < (int64_t)g.vocab) {
         // the difference of logits first: the two are near each other where a loss is small
-        loss = s.most == -kInf && s.sum == 0.f ? kInf : (s.most - g.given[r]) + log_sum;
+        loss = nothing ? kInf : (s.most - given) + log_sum;
     } else if (t != -1) {
         loss = nan32();
         report(g.err, WC_EF_BAD_INDEX);
@@ -229,13 +252,11 @@ __device__ __forceinline__ float loss_gradient(f32x4 row, float z, uint32_t v, f
 
 // G of a tile.
 template <int T, int BM, int BN>
-__global__ __launch_bounds__(256, BM + BN > 384 ? 1 : 2) void k_loss_grad(LossGradArgs g)
+__global__ __launch_bounds__(256, tile_blocks(BM, BN)) void k_loss_grad(LossGradArgs g)
 {
-    using Ti = Tile<T, BM, BN, 2, 2, true, true>;
-    __shared__ __attribute__((aligned(1024))) char q0[Ti::Q::kBytes];
-    __shared__ __attribute__((aligned(1024))) char p0[Ti::P::kBytes];
-    __shared__ __attribute__((aligned(1024))) char q1[Ti::Q::kBytes];
-    __shared__ __attribute__((aligned(1024))) char p1[Ti::P::kBytes];
+    using Ti = Tile<T, BM, BN, true, true>;
+    __shared__ __attribute__((aligned(1024))) char b0[Ti::kBytes];
+    __shared__ __attribute__((aligned(1024))) char b1[Ti::kBytes];
     const uint32_t down = (g.m + BM - 1) / BM, across = (g.width + BN - 1) / BN, t = xcd_piece(blockIdx.x, down * across);
     if (t >= down * across) return;
     uint32_t r, c;
@@ -244,19 +265,28 @@ __global__ __launch_bounds__(256, BM + BN > 384 ? 1 : 2) void k_loss_grad(LossGr
     Ti ti;
     ti.q.init(g.h + m0 * g.h_stride, g.h_stride, rows, g.k);
     ti.p.init(g.w + (uint64_t)(g.v0 + n0) * g.w_row, g.w_row, cols, g.k);
-    ti.product(q0, p0, q1, p1, g.k);
+    ti.product(b0, b1, nullptr, g.k, rows);
     float unscale;
     const float scale = loss_scale<T>(g.most, unscale);
-    each_four(ti, [&](uint32_t row, uint32_t col, f32x4 z) {
-        if (row >= rows || n0 + col >= g.pitch) return;
-        const f32x4 info = g.rows[m0 + row];
+    const uint32_t wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
 #pragma unroll
-        for (uint32_t e = 0; e < 4; e++) z[e] = col + e < cols ? loss_gradient(info, z[e], g.v0 + n0 + col + e, scale) : 0.f;
-        store_four<T>(g.grad + (uint64_t)(m0 + row) * g.pitch + n0 + col, z);
-    });
+    for (int b = 0; b < Ti::kM; b++) {
+        const uint32_t row = 16 * (wave / Ti::kWavesN + Ti::kWavesM * b) + (lane & 15);
+        if (row >= rows) continue;
+        const f32x4 info = g.rows[m0 + row];
+        uint16_t *to = g.grad + (uint64_t)(m0 + row) * g.pitch + n0;
+#pragma unroll
+        for (int a = 0; a < Ti::kN; a++) {
+            const uint32_t col = 16 * (wave % Ti::kWavesN + Ti::kWavesN * a) + 4 * (lane >> 4);
+            f32x4 z = ti.acc[a][b];
+#pragma unroll
+            for (uint32_t e = 0; e < 4; e++) z[e] = col + e < cols ? loss_gradient(info, z[e], g.v0 + n0 + col + e, scale) : 0.f;
+            if (n0 + col < g.pitch) store_four<T>(to + col, z);
+        }
+    }
 }
 
-// The same for up to 64 rows.
+// The same for up to 32 rows.
 template <int T, bool kSplit>
 __global__ __launch_bounds__(256, 2) void k_loss_grad_few(LossGradArgs g)
 {
@@ -300,13 +330,11 @@ struct ProductArgs {
 
 // D = Q P^T of whole matrices.  kQAlong: k along the rows of Q's memory; P has it across.
 template <int T, int BM, int BN, bool kQAlong>
-__global__ __launch_bounds__(256, BM + BN > 384 ? 1 : 2) void k_product(ProductArgs g)
+__global__ __launch_bounds__(256, tile_blocks(BM, BN)) void k_product(ProductArgs g)
 {
-    using Ti = Tile<T, BM, BN, 2, 2, kQAlong, false>;
-    __shared__ __attribute__((aligned(1024))) char q0[Ti::Q::kBytes];
-    __shared__ __attribute__((aligned(1024))) char p0[Ti::P::kBytes];
-    __shared__ __attribute__((aligned(1024))) char q1[Ti::Q::kBytes];
-    __shared__ __attribute__((aligned(1024))) char p1[Ti::P::kBytes];
+    using Ti = Tile<T, BM, BN, kQAlong, false>;
+    __shared__ __attribute__((aligned(1024))) char b0[Ti::kBytes];
+    __shared__ __attribute__((aligned(1024))) char b1[Ti::kBytes];
     const uint32_t down = (g.m + BM - 1) / BM, across = (g.n + BN - 1) / BN, each = down * across;
     const uint32_t t = xcd_piece(blockIdx.x, each * g.splits);
     if (t >= each * g.splits) return;
@@ -321,7 +349,7 @@ __global__ __launch_bounds__(256, BM + BN > 384 ? 1 : 2) void k_product(ProductA
     if constexpr (kQAlong) ti.q.init(g.q + m0 * g.q_stride + k0, g.q_stride, rows, (k + 7) / 8 * 8);
     else ti.q.init(g.q + k0 * g.q_stride + m0, g.q_stride, k, (g.m + 7) / 8 * 8 - m0);
     ti.p.init(g.p + k0 * g.p_stride + n0, g.p_stride, k, g.n - n0);
-    ti.product(q0, p0, q1, p1, k);
+    ti.product(b0, b1, nullptr, k);
     float unscale;
     loss_scale<T>(g.most, unscale);
     each_four(ti, [&](uint32_t row, uint32_t col, f32x4 v) {

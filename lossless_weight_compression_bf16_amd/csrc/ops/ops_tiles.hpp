@@ -32,6 +32,16 @@ typedef short s16x4 __attribute__((ext_vector_type(4)));
 constexpr uint32_t kTileK = 64;         // k of one stage
 constexpr uint32_t kNowhere = 1u << 31;  // an offset past the end of every window
 
+// What is the same in every lane, said so: a window in vector registers would be
+// taken apart lane by lane at every load.
+__device__ __forceinline__ uint32_t uniform(uint32_t v) { return (uint32_t)__builtin_amdgcn_readfirstlane((int)v); }
+template <class P>
+__device__ __forceinline__ const P *uniform(const P *p)
+{
+    const uint64_t v = reinterpret_cast<uint64_t>(p);
+    return reinterpret_cast<const P *>((uint64_t)uniform((uint32_t)(v >> 32)) << 32 | uniform((uint32_t)v));
+}
+
 // One operand of a tile: R rows (of D, or columns of it) by kTileK values of k,
 // loaded 1024 bytes at a time, and every load in a place of its own in LDS.
 // kAlong: k runs along the rows of memory, a load takes 8 rows of 128 bytes; 16-byte
@@ -39,7 +49,7 @@ constexpr uint32_t kNowhere = 1u << 31;  // an offset past the end of every wind
 // of memory, and a load takes 512 / R rows of 2 R bytes.
 template <int R, bool kAlong, int kWaves>
 struct Operand {
-    static_assert(R == 64 || R == 128 || R == 256, "");
+    static_assert(R == 64 || R == 128 || R == 256, "and 64 only along");
     static constexpr uint32_t kLoads = R / 8 / kWaves;  // of each wave and stage
     static_assert(R / 8 % kWaves == 0, "whole loads");
     static constexpr uint32_t kRowsOfLoad = kAlong ? 8 : 512 / R;
@@ -48,7 +58,7 @@ struct Operand {
     {
         if (kAlong) return load * 1024;
         if (R == 256) return load * 1088 + (load >> 2) * 128;
-        return load * (1024 + 128);
+        return load * 1024 + (load >> 1) * 128;
     }
     static constexpr uint32_t kBytes = place(R / 8 - 1) + 1024;
     __device__ __forceinline__ static uint32_t swap(uint32_t k) { return R == 256 ? 2 * (k & 1) : 2 * (k & 3); }
@@ -65,10 +75,10 @@ struct Operand {
     __device__ __forceinline__ void init(const void *from, uint64_t row_elems, uint32_t n, uint32_t k)
     {
         const uint32_t wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-        base = static_cast<const char *>(from);
-        pitch = 2 * (uint32_t)row_elems;
-        rows = n;
-        width = 2 * k;
+        base = uniform(static_cast<const char *>(from));
+        pitch = uniform(2 * (uint32_t)row_elems);
+        rows = uniform(n);
+        width = uniform(2 * k);
 #pragma unroll
         for (uint32_t j = 0; j < kLoads; j++) {
             constexpr uint32_t kPerRow = 64 / kRowsOfLoad;  // lanes of a row
@@ -125,10 +135,14 @@ struct Operand {
     }
 };
 
+// Blocks of a tile's kernel on a compute unit.
+constexpr int tile_blocks(int BM, int BN) { return BM + BN > 384 ? 1 : 2; }
+
 // A wave has every kWavesM-th 16 rows of Q and every kWavesN-th of P.
-template <int T, int BM, int BN, int kWavesM, int kWavesN, bool kQAlong, bool kPAlong>
+template <int T, int BM, int BN, bool kQAlong, bool kPAlong, int kStages = 2>
 struct Tile {
-    static constexpr int kWaves = kWavesM * kWavesN, kThreads = 64 * kWaves, kWavesDown = kWavesM, kWavesAcross = kWavesN;
+    static constexpr int kWavesM = BM == 64 ? 1 : 2, kWavesN = 4 / kWavesM;
+    static constexpr int kWaves = 4;
     static constexpr int kM = BM / kWavesM / 16, kN = BN / kWavesN / 16;
     using Q = Operand<BM, kQAlong, kWaves>;
     using P = Operand<BN, kPAlong, kWaves>;
@@ -160,6 +174,13 @@ struct Tile {
         }
     }
 
+    // Branches of the whole wave around products of rows that do not exist.  Not
+    // where the accumulators are named: around branches the compiler moves
+    // them, without the waits that it does not know of.  Not for 64 rows, where
+    // reading P is the bound and the branches cost (61 rows of 128256 x 4096
+    // against all of them: 207 us, 178 without).
+    static constexpr bool kSkip = BM == 128;
+
     struct Half {  // operands of 32 values of k
         X8 p[kN], q[kM];
     };
@@ -182,25 +203,28 @@ struct Tile {
     }
 
     // The products of h, with the reading of `into` spread among them, and
-    // kEach loads of a later stage with each of the first ones.
+    // kEach loads of a later stage with each of the first ones.  Sixteens of
+    // Q's rows from `live` on do not exist: tiles of 128 leave them out (kSkip).
     template <int kEach>
     __device__ __forceinline__ void multiply(const Half &h, Half &into, const char *qs, const char *ps, uint32_t sub,
-                                             const Stage &s, char *ql, char *pl, uint32_t wave)
+                                             const Stage &s, char *ql, char *pl, uint32_t wave, int live)
     {
         constexpr int kReads = kM + kN, kProducts = kM * kN, kPer = kProducts / kReads;
         static_assert(!kEach || kEach * kReads >= kLoads, "all loads");
 #pragma unroll
         for (int n = 0; n < kReads; n++) {
-            read(into, qs, ps, wave, sub, n);
+            if (!kSkip || n < kN || n - kN < live) read(into, qs, ps, wave, sub, n);
             if constexpr (kEach > 0) {
 #pragma unroll
                 for (int j = kEach * n; j < kEach * (n + 1); j++)
                     if (j < kLoads) load(s, ql, pl, wave, j);
             }
+            if (!kSkip || n * kPer / kN < live) {
 #pragma unroll
-            for (int e = 0; e < kPer; e++) {
-                const int at = n * kPer + e;
-                mfma(h.p[at % kN], h.q[at / kN], acc[at % kN][at / kN]);
+                for (int e = 0; e < kPer; e++) {
+                    const int at = n * kPer + e;
+                    mfma(h.p[at % kN], h.q[at / kN], acc[at % kN][at / kN]);
+                }
             }
             __builtin_amdgcn_sched_barrier(0);
         }
@@ -210,46 +234,71 @@ struct Tile {
 
     static constexpr int kEach = (kLoads + kM + kN - 1) / (kM + kN);
 
-    // One stage out of (qs, ps), whose first half is in h[0]; the next one is in
-    // (qt, pt) at the end of the first half, and the one after it comes into (qs, ps).
-    __device__ __forceinline__ void stage(Half *h, char *qs, char *ps, const char *qt, const char *pt, uint32_t wave, uint32_t k0,
-                                          uint32_t k)
+    // The wait for reads of LDS, and for all loads but the last n.
+    template <int n>
+    __device__ __forceinline__ static void wait_all_but()
     {
-        const Stage s = begin(k0 + 2 * kTileK, k);
-        multiply<0>(h[0], h[1], qs, ps, 1, s, nullptr, nullptr, wave);
-        __builtin_amdgcn_s_waitcnt(0x0070);  // loads and reads done
-        asm volatile("s_barrier" ::: "memory");
-        __builtin_amdgcn_sched_barrier(0);
-        multiply<kEach>(h[1], h[0], qt, pt, 0, s, qs, ps, wave);
+        __builtin_amdgcn_s_waitcnt((n & 15) | ((n >> 4) << 14) | 0x0070);
     }
 
-    __device__ __forceinline__ void product(char *q0, char *p0, char *q1, char *p1, uint32_t k)
+    // One stage, whose first half is in h[0]; the next one has come at the end of
+    // the first half, and the one kStages after it comes into its place.
+    __device__ __forceinline__ void stage(Half *h, char *here, const char *next, uint32_t wave, int live, uint32_t k0, uint32_t k)
     {
+        const Stage s = begin(k0 + kStages * kTileK, k);
+        multiply<0>(h[0], h[1], here, here + Q::kBytes, 1, s, nullptr, nullptr, wave, live);
+        wait_all_but<(kStages - 2) * kLoads>();
+        asm volatile("s_barrier" ::: "memory");
+        __builtin_amdgcn_sched_barrier(0);
+        multiply<kEach>(h[1], h[0], next, next + Q::kBytes, 0, s, here, here + Q::kBytes, wave, live);
+    }
+
+    static constexpr uint32_t kBytes = Q::kBytes + P::kBytes;  // of a stage in LDS
+    static constexpr uint32_t kThird = kStages == 3 ? kBytes : 16;
+
+    // The product over k values of k, of `rows` of Q's rows.  s2: where kStages is 3.
+    __device__ __forceinline__ void product(char *s0, char *s1, char *s2, uint32_t k, uint32_t rows = BM)
+    {
+        k = uniform(k);
         const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+        // this wave's sixteens: wave / kWavesN, and every kWavesM-th after it
+        const int sixteens = (int)((uniform(rows) + 15) / 16) - (int)(wave / kWavesN);
+        const int live = sixteens <= 0 ? 0 : (sixteens + kWavesM - 1) / kWavesM;
 #pragma unroll
         for (int a = 0; a < kN; a++)
 #pragma unroll
             for (int b = 0; b < kM; b++) acc[a][b] = f32x4{0.f, 0.f, 0.f, 0.f};
-        Stage s = begin(0, k);
 #pragma unroll
-        for (int j = 0; j < kLoads; j++) load(s, q0, p0, wave, j);
-        __builtin_amdgcn_s_waitcnt(0x0070);
+        for (int n = 0; n < kStages; n++) {
+            const Stage s = begin(n * kTileK, k);
+            char *to = n == 0 ? s0 : n == 1 ? s1 : s2;
+#pragma unroll
+            for (int j = 0; j < kLoads; j++) load(s, to, to + Q::kBytes, wave, j);
+        }
+        wait_all_but<(kStages - 1) * kLoads>();
         asm volatile("s_barrier" ::: "memory");
         __builtin_amdgcn_sched_barrier(0);
-        s = begin(kTileK, k);
-#pragma unroll
-        for (int j = 0; j < kLoads; j++) load(s, q1, p1, wave, j);
         Half h[2];
 #pragma unroll
-        for (int n = 0; n < kM + kN; n++) read(h[0], q0, p0, wave, 0, n);
+        for (int n = 0; n < kM + kN; n++) read(h[0], s0, s0 + Q::kBytes, wave, 0, n);
         uint32_t k0 = 0;
-        for (; k0 + kTileK < k; k0 += 2 * kTileK) {
-            stage(h, q0, p0, q1, p1, wave, k0, k);
-            stage(h, q1, p1, q0, p0, wave, k0 + kTileK, k);
+        if constexpr (kStages == 2) {
+            for (; k0 + kTileK < k; k0 += 2 * kTileK) {
+                stage(h, s0, s1, wave, live, k0, k);
+                stage(h, s1, s0, wave, live, k0 + kTileK, k);
+            }
+            if (k0 < k) stage(h, s0, s1, wave, live, k0, k);
+        } else {
+            for (; k0 + 2 * kTileK < k; k0 += 3 * kTileK) {
+                stage(h, s0, s1, wave, live, k0, k);
+                stage(h, s1, s2, wave, live, k0 + kTileK, k);
+                stage(h, s2, s0, wave, live, k0 + 2 * kTileK, k);
+            }
+            if (k0 < k) stage(h, s0, s1, wave, live, k0, k);
+            if (k0 + kTileK < k) stage(h, s1, s2, wave, live, k0 + kTileK, k);
         }
-        if (k0 < k) stage(h, q0, p0, q1, p1, wave, k0, k);
         settle();
-        __builtin_amdgcn_s_waitcnt(0x0070);  // loads past the last k have not landed before
+        wait_all_but<0>();  // loads past the last k have not landed before
         __syncthreads();
     }
 };
@@ -280,8 +329,8 @@ __device__ __forceinline__ void each_four(const Tile &t, F f)
     for (int b = 0; b < Tile::kM; b++)
 #pragma unroll
         for (int a = 0; a < Tile::kN; a++)
-            f(16 * (wave / Tile::kWavesAcross + Tile::kWavesDown * b) + i,
-              16 * (wave % Tile::kWavesAcross + Tile::kWavesAcross * a) + 4 * gr, t.acc[a][b]);
+            f(16 * (wave / Tile::kWavesN + Tile::kWavesM * b) + i,
+              16 * (wave % Tile::kWavesN + Tile::kWavesN * a) + 4 * gr, t.acc[a][b]);
 }
 
 template <int T>

@@ -21,8 +21,13 @@ namespace {
 constexpr uint64_t kMaxPitch = (1ull << 22) - 8;
 constexpr uint32_t kMaxCols = 1u << 20;
 
+#ifndef FORCE
+#define FORCE(x) x
+#endif
+// Tiles of a product, and the parts of k that it is split into.
+enum TileSize { kFlat, kSmall, kLarge };  // 64 rows (by 256 columns, or 128 with P across), 128 x 128, 256 x 256
 struct TilePlan {
-    bool large;  // 256 x 256, else 128 x 128
+    TileSize size;
     uint32_t splits;
 };
 
@@ -32,7 +37,7 @@ struct TilePlan {
 // parts' sums are written and read in fp32.
 TilePlan tile_plan(uint64_t large, uint64_t small, uint64_t stages, uint64_t results, bool joined)
 {
-    TilePlan best{false, 1};
+    TilePlan best{kSmall, 1};
     double least = 1e30;
     for (int size = 0; size < 2; size++) {
         for (uint32_t s = 1; s <= 16 && (s == 1 || stages >= 4 * s); s *= 2) {
@@ -42,7 +47,7 @@ TilePlan tile_plan(uint64_t large, uint64_t small, uint64_t stages, uint64_t res
             if (s > 1) t += (joined ? 0.0 : 4.0) + (double)results * s * 8 / 4e6;
             if (t < least) {
                 least = t;
-                best = {size == 1, s};
+                best = {size ? kLarge : kSmall, s};
             }
         }
     }
@@ -61,15 +66,21 @@ uint64_t tiles_expected(uint64_t m, uint32_t experts, uint64_t tile)  // with th
     return hit * ceil_div(ceil_div(m, hit), tile);
 }
 
-// y or dx of m rows with n columns each, from k
-TilePlan grouped_plan(uint64_t m, uint32_t experts, uint32_t n, uint32_t k)
+// The tiles of y or dx of m rows with n columns each, from k
+TileSize grouped_size(uint64_t m, uint32_t experts, uint32_t n, uint32_t k)
 {
-    return tile_plan(tiles_expected(m, experts, 256) * ceil_div(n, 256), tiles_expected(m, experts, 128) * ceil_div(n, 128),
-                     ceil_div(k, kTileK), m * n, false);
+    if (m <= 64ull * (m < experts ? m : experts)) return kFlat;
+    return FORCE((tile_plan(tiles_expected(m, experts, 256) * ceil_div(n, 256), tiles_expected(m, experts, 128) * ceil_div(n, 128),
+                     ceil_div(k, kTileK), m * n, false).size));
+}
+// Room for the tiles in parts: one of every slot.
+uint64_t grouped_part(TileSize size)
+{
+    return size == kLarge ? 4ull * 256 * 256 * kCus : size == kSmall ? 4ull * 128 * 128 * 2 * kCus : 0;
 }
 
-// few rows of each expert: the weights are read once and no tile would be full
-bool grouped_few(uint64_t m, uint32_t experts) { return m <= 48ull * (m < experts ? m : experts); }
+// few rows of each expert: no tile would be full
+bool grouped_few(uint64_t m, uint32_t experts) { return m <= 8ull * (m < experts ? m : experts); }
 
 TilePlan grouped_dw_plan(uint64_t m, uint32_t experts, uint32_t n, uint32_t k)
 {
@@ -99,19 +110,27 @@ void launch_join(int type, const JoinArgs &g, hipStream_t stream)
 
 uint32_t xcd_grid(uint64_t pieces) { return (uint32_t)(8 * ceil_div(pieces, 8)); }
 
-// y, or dx (kPAlong false), by tiles
-template <int T, bool kPAlong>
-void launch_grouped(GroupedArgs g, const TilePlan &p, hipStream_t stream)
+// y, or dx (kPAlong false), by tiles of BM x BN
+template <int T, int BM, int BN, bool kPAlong>
+void launch_tiles(const GroupedArgs &g, hipStream_t stream)
 {
-    g.splits = p.splits;
-    const uint64_t tile = p.large ? 256 : 128;
+    constexpr uint32_t slots = GroupedPieces<BM, BN>::kSlots;
     // rows behind the last expert's fill a tile more, and may take one that the experts' would have
-    const uint64_t tiles = (tiles_of(g.m, g.experts, tile) + 1) * ceil_div(g.n, tile) * g.splits;
-    if (p.large) hipLaunchKernelGGL((k_grouped<T, 256, 256, kPAlong>), dim3(xcd_grid(tiles)), dim3(256), 0, stream, g);
-    else hipLaunchKernelGGL((k_grouped<T, 128, 128, kPAlong>), dim3(xcd_grid(tiles)), dim3(256), 0, stream, g);
-    if (g.splits > 1)
-        launch_join(T, JoinArgs{g.part, g.y, g.y_stride, g.m, g.n, g.splits, g.zero_rest ? nullptr : g.ends + g.experts - 1, nullptr},
-                    stream);
+    const uint64_t tiles = (tiles_of(g.m, g.experts, BM) + 1) * ceil_div(g.n, BN);
+    // a last round in parts has no more blocks than slots; the XCDs' ranges of parts and zeros are rounded up
+    const uint32_t blocks = xcd_grid(tiles + (g.part ? slots : 0) + 16);
+    hipLaunchKernelGGL((k_grouped<T, BM, BN, kPAlong>), dim3(blocks), dim3(256), 0, stream, g);
+    if (g.part) hipLaunchKernelGGL((k_grouped_join<T, BM, BN>), dim3(slots / 2 * 8), dim3(256), 0, stream, g);
+}
+template <int T, bool kPAlong>
+void launch_grouped(GroupedArgs g, TileSize size, hipStream_t stream)
+{
+    if (size == kLarge) launch_tiles<T, 256, 256, kPAlong>(g, stream);
+    else if (size == kSmall) launch_tiles<T, 128, 128, kPAlong>(g, stream);
+    else {
+        g.part = nullptr;
+        launch_tiles<T, 64, kPAlong ? 256 : 128, kPAlong>(g, stream);
+    }
 }
 
 template <int T>
@@ -124,7 +143,7 @@ wc_status launch_grouped_linear(GroupedArgs g, hipStream_t stream)
         if (split) hipLaunchKernelGGL((k_grouped_few<T, true>), grid, dim3(256), 0, stream, g);
         else hipLaunchKernelGGL((k_grouped_few<T, false>), grid, dim3(256), 0, stream, g);
     } else {
-        launch_grouped<T, true>(g, grouped_plan(g.m, g.experts, g.n, g.k), stream);
+        launch_grouped<T, true>(g, grouped_size(g.m, g.experts, g.n, g.k), stream);
     }
     return launched();
 }
@@ -133,11 +152,12 @@ template <int T>
 void launch_grouped_dw(GroupedDwArgs g, const TilePlan &p, hipStream_t stream)
 {
     g.splits = p.splits;
-    const uint64_t tile = p.large ? 256 : 128, tiles = g.experts * ceil_div(g.n, tile) * ceil_div(g.k, tile) * g.splits;
-    if (p.large) hipLaunchKernelGGL((k_grouped_dw<T, 256, 256>), dim3(xcd_grid(tiles)), dim3(256), 0, stream, g);
-    else hipLaunchKernelGGL((k_grouped_dw<T, 128, 128>), dim3(xcd_grid(tiles)), dim3(256), 0, stream, g);
+    const uint64_t tile = p.size == kLarge ? 256 : 128;
+    const dim3 grid(g.experts * xcd_grid(ceil_div(g.n, tile) * ceil_div(g.k, tile) * g.splits)), block(256);
+    if (p.size == kLarge) hipLaunchKernelGGL((k_grouped_dw<T, 256, 256>), grid, block, 0, stream, g);
+    else hipLaunchKernelGGL((k_grouped_dw<T, 128, 128>), grid, block, 0, stream, g);
     if (g.splits > 1)
-        launch_join(T, JoinArgs{g.part, g.dw, g.k, (uint64_t)g.experts * g.n, g.k, g.splits, nullptr, nullptr}, stream);
+        launch_join(T, JoinArgs{g.part, g.dw, g.k, (uint64_t)g.experts * g.n, g.k, g.splits, nullptr}, stream);
 }
 
 // ------------------------------------------------------------- cross entropy
@@ -152,15 +172,15 @@ bool valid_loss(uint64_t m, uint32_t vocab, uint32_t cols)
     return m <= kLossMaxRows && vocab >= 1 && vocab <= (1u << 22) && cols >= 8 && cols % 8 == 0 && cols <= kMaxCols;
 }
 
-bool loss_few(uint64_t m) { return m <= 64; }
-bool loss_large(uint64_t m, uint32_t vocab, uint32_t k)
+bool loss_few(uint64_t m) { return m <= 16; }
+TileSize loss_tile(uint64_t m, uint32_t vocab, uint32_t k)
 {
-    return tile_plan(ceil_div(m, 256) * ceil_div(vocab, 256), ceil_div(m, 128) * ceil_div(vocab, 128), ceil_div(k, kTileK), 0, true)
-        .large;
+    if (m <= 64) return kFlat;
+    return tile_plan(ceil_div(m, 256) * ceil_div(vocab, 256), ceil_div(m, 128) * ceil_div(vocab, 128), ceil_div(k, kTileK), 0, true).size;
 }
 uint32_t loss_parts(uint64_t m, uint32_t vocab, uint32_t k)
 {
-    return (uint32_t)ceil_div(vocab, m == 1 ? 8 : loss_few(m) ? 32 : loss_large(m, vocab, k) ? 256 : 128);
+    return (uint32_t)ceil_div(vocab, loss_few(m) ? (k > 1024 ? 32 : 128) : loss_tile(m, vocab, k) == kSmall ? 128 : 256);
 }
 uint64_t up256(uint64_t n) { return ceil_div(n, 256) * 256; }
 
@@ -172,10 +192,12 @@ void launch_loss(const LossArgs &g, hipStream_t stream)
         const dim3 grid((uint32_t)ceil_div(g.vocab, split ? 32 : 128));
         if (split) hipLaunchKernelGGL((k_loss_few<T, true>), grid, dim3(256), 0, stream, g);
         else hipLaunchKernelGGL((k_loss_few<T, false>), grid, dim3(256), 0, stream, g);
-    } else if (loss_large(g.m, g.vocab, g.k)) {
-        hipLaunchKernelGGL((k_loss<T, 256, 256>), dim3(xcd_grid(ceil_div(g.m, 256) * g.parts)), dim3(256), 0, stream, g);
     } else {
-        hipLaunchKernelGGL((k_loss<T, 128, 128>), dim3(xcd_grid(ceil_div(g.m, 128) * g.parts)), dim3(256), 0, stream, g);
+        const TileSize size = loss_tile(g.m, g.vocab, g.k);
+        const dim3 grid(xcd_grid(ceil_div(g.m, size == kLarge ? 256 : size == kSmall ? 128 : 64) * g.parts)), block(256);
+        if (size == kLarge) hipLaunchKernelGGL((k_loss<T, 256, 256>), grid, block, 0, stream, g);
+        else if (size == kSmall) hipLaunchKernelGGL((k_loss<T, 128, 128>), grid, block, 0, stream, g);
+        else hipLaunchKernelGGL((k_loss<T, 64, 256>), grid, block, 0, stream, g);
     }
     hipLaunchKernelGGL(k_loss_join, dim3(g.m), dim3(256), 0, stream, g);
 }
@@ -237,30 +259,31 @@ void launch_loss_grad(const wc_linear_loss_grad &a, LossGradArgs g, const LossGr
             const dim3 grid((uint32_t)ceil_div(g.width, split ? 32 : 128));
             if (split) hipLaunchKernelGGL((k_loss_grad_few<T, true>), grid, dim3(256), 0, stream, g);
             else hipLaunchKernelGGL((k_loss_grad_few<T, false>), grid, dim3(256), 0, stream, g);
-        } else if (loss_large(g.m, p.piece, g.k)) {
-            const uint64_t tiles = ceil_div(g.m, 256) * ceil_div(g.width, 256);
-            hipLaunchKernelGGL((k_loss_grad<T, 256, 256>), dim3(xcd_grid(tiles)), dim3(256), 0, stream, g);
         } else {
-            const uint64_t tiles = ceil_div(g.m, 128) * ceil_div(g.width, 128);
-            hipLaunchKernelGGL((k_loss_grad<T, 128, 128>), dim3(xcd_grid(tiles)), dim3(256), 0, stream, g);
+            const TileSize size = loss_tile(g.m, p.piece, g.k);
+            const uint32_t bm = size == kLarge ? 256 : size == kSmall ? 128 : 64, bn = size == kSmall ? 128 : 256;
+            const dim3 grid(xcd_grid(ceil_div(g.m, bm) * ceil_div(g.width, bn))), block(256);
+            if (size == kLarge) hipLaunchKernelGGL((k_loss_grad<T, 256, 256>), grid, block, 0, stream, g);
+            else if (size == kSmall) hipLaunchKernelGGL((k_loss_grad<T, 128, 128>), grid, block, 0, stream, g);
+            else hipLaunchKernelGGL((k_loss_grad<T, 64, 256>), grid, block, 0, stream, g);
         }
         if (a.grad_hidden) {
             ProductArgs d{g.grad, g.w + v0 * g.w_row, g.pitch, g.w_row, g.m, g.k, g.width, p.dh.splits,
                           p.dh_sums ? dh_part : nullptr, v0 ? 1u : 0u, static_cast<uint16_t *>(a.grad_hidden),
                           a.grad_hidden_stride, g.most};
-            launch_product<T, true>(d, p.dh.large, stream);
+            launch_product<T, true>(d, p.dh.size == kLarge, stream);
         }
         if (a.grad_weight) {
             uint16_t *out = static_cast<uint16_t *>(a.grad_weight) + v0 * g.k;
             ProductArgs d{g.grad, g.live, g.pitch, g.k, g.width, g.k, g.m, p.dw.splits,
                           p.dw.splits > 1 ? dw_part : nullptr, 0, out, g.k, g.most};
-            launch_product<T, false>(d, p.dw.large, stream);
-            if (p.dw.splits > 1) launch_join(T, JoinArgs{dw_part, out, g.k, g.width, g.k, p.dw.splits, nullptr, g.most}, stream);
+            launch_product<T, false>(d, p.dw.size == kLarge, stream);
+            if (p.dw.splits > 1) launch_join(T, JoinArgs{dw_part, out, g.k, g.width, g.k, p.dw.splits, g.most}, stream);
         }
     }
     if (a.grad_hidden && p.dh_sums)
         launch_join(T, JoinArgs{dh_part, static_cast<uint16_t *>(a.grad_hidden), a.grad_hidden_stride, g.m, g.k, p.dh.splits,
-                                nullptr, g.most},
+                                g.most},
                     stream);
 }
 
@@ -273,7 +296,7 @@ extern "C" {
 uint64_t wc_grouped_linear_scratch(uint64_t m, uint32_t experts, uint32_t rows, uint32_t cols)
 {
     if (m == 0 || !valid_grouped(m, experts, rows, cols) || grouped_few(m, experts)) return 0;
-    return part_bytes(m * rows, grouped_plan(m, experts, rows, cols).splits);
+    return grouped_part(grouped_size(m, experts, rows, cols));
 }
 
 wc_status wc_grouped_linear(const wc_grouped *a, void *d_scratch, uint64_t scratch_bytes, uint32_t *d_err, hipStream_t stream)
@@ -303,7 +326,6 @@ wc_status wc_grouped_linear(const wc_grouped *a, void *d_scratch, uint64_t scrat
     g.n = a->rows;
     g.k = a->cols;
     g.zero_rest = a->zero_rest;
-    g.splits = 1;
     g.part = static_cast<float *>(d_scratch);
     g.err = d_err;
     return a->type == WC_T_BF16 ? launch_grouped_linear<WC_T_BF16>(g, stream) : launch_grouped_linear<WC_T_FP16>(g, stream);
@@ -313,7 +335,7 @@ uint64_t wc_grouped_linear_backward_scratch(uint64_t m, uint32_t experts, uint32
 {
     if (m == 0 || !valid_grouped(m, experts, rows, cols)) return 0;
     // one after the other
-    const uint64_t dx = part_bytes(m * cols, grouped_plan(m, experts, cols, rows).splits);
+    const uint64_t dx = grouped_part(grouped_size(m, experts, cols, rows));
     const uint64_t dw = part_bytes((uint64_t)experts * rows * cols, grouped_dw_plan(m, experts, rows, cols).splits);
     return dx > dw ? dx : dw;
 }
@@ -350,7 +372,7 @@ wc_status wc_grouped_linear_backward(const wc_grouped_grad *a, void *d_scratch, 
         g.zero_rest = a->zero_rest;
         g.part = static_cast<float *>(d_scratch);
         g.err = d_err;
-        const TilePlan p = grouped_plan(a->m, a->experts, a->cols, a->rows);
+        const TileSize p = grouped_size(a->m, a->experts, a->cols, a->rows);
         if (a->type == WC_T_BF16) launch_grouped<WC_T_BF16, false>(g, p, stream);
         else launch_grouped<WC_T_FP16, false>(g, p, stream);
     }

@@ -613,6 +613,38 @@ uint64_t wc_linear_cross_entropy_backward_scratch(uint64_t m, uint32_t vocab, ui
 wc_status wc_linear_cross_entropy_backward(const wc_linear_loss_grad *a, void *d_scratch, uint64_t scratch_bytes,
                                            uint32_t *d_err, hipStream_t stream);
 
+/* Products of few rows with weights of 4 bits and group scales: with g = k / group,
+ *   w_rk = scales_rg (q_rk - zeros_rg),   y = x w^T,
+ * q in 0 .. 15, two in a byte (the even column in the low half).  Products of
+ * x with whole numbers are exact, their sums over a group, and those of
+ * the scaled groups, are fp32, and y is rounded once.  32 rows of x meet the weights
+ * at a time (16 where there are no more): meant for few. */
+typedef struct {
+    const void *x;          /* m x cols, rows x_stride elements apart, 16-byte aligned rows */
+    uint64_t x_stride;      /* a multiple of 8 */
+    const void *q;          /* rows x cols / 2 bytes, 16-byte aligned */
+    const void *scales;     /* rows x cols / group */
+    const void *zeros;      /* the same, or NULL: 8 */
+    void *y;                /* m x rows, rows y_stride elements apart, any alignment; no memory in common with x */
+    uint64_t y_stride;
+    uint64_t m;             /* below 2^31 */
+    uint32_t rows;          /* 1 .. 2^24; rows / 16 times m / 16 below 2^22 */
+    uint32_t cols;          /* a multiple of group, at most 2^20 */
+    uint32_t group;         /* 32, 64 or 128 */
+    uint32_t type;          /* WC_T_BF16 or WC_T_FP16: of x, scales, zeros and y */
+} wc_fourbit;
+
+wc_status wc_linear4(const wc_fourbit *a, hipStream_t stream);
+
+/* The 4-bit form of rows x cols weights of `type` (w_stride elements from row
+ * to row): without zeros, scale = largest |w| of the group / 7 and
+ * q = w / scale to the nearest, + 8; with zeros, of lo = min(w, 0) and
+ * hi = max(w, 0), scale = (hi - lo) / 15, zero = -lo / scale to the nearest, and
+ * q = w / scale to the nearest, + zero; q within 0 .. 15, the scale rounded to
+ * `type` before w is divided by it.  A scale of 0 (a group of zeros), NaN or infinity: q is the zero. */
+wc_status wc_quantize4(const void *w, uint64_t w_stride, uint64_t rows, uint32_t cols, uint32_t group, uint32_t type, void *q,
+                       void *scales, void *zeros, hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

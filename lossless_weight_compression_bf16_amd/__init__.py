@@ -7,7 +7,7 @@ tensor-level API; ``_binding`` mirrors the C ABI one to one.  ``logprobs``,
 weights: log probabilities and their gradient, low-rank adapters, and a
 mixture-of-experts layer; ``grouped`` and ``loss`` are a training step's:
 products grouped by expert, and cross entropy from hidden states, with their
-gradients.  Importing the
+gradients; ``fourbit`` multiplies weights of 4 bits.  Importing the
 package does not load the GPU library; the first codec call does, and fails
 if it has not been built.
 """
@@ -37,4 +37,7 @@ def __getattr__(name):
     if name in ("linear_cross_entropy", "linear_cross_entropy_backward", "LinearCrossEntropy"):
         from . import loss
         return getattr(loss, name)
+    if name in ("linear4", "quantize4", "Weights4"):
+        from . import fourbit
+        return getattr(fourbit, name)
     raise AttributeError(name)

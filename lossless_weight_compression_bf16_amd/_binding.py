@@ -47,7 +47,8 @@ EXPORTS = ["wc_version", "wc_status_string", "wc_query_layout", "wc_plan_batch",
            "wc_token_logprobs_backward", "wc_add_adapters_scratch", "wc_add_adapters",
            "wc_moe_layer_scratch", "wc_moe_layer", "wc_grouped_linear_scratch", "wc_grouped_linear",
            "wc_grouped_linear_backward_scratch", "wc_grouped_linear_backward", "wc_linear_cross_entropy_scratch",
-           "wc_linear_cross_entropy", "wc_linear_cross_entropy_backward_scratch", "wc_linear_cross_entropy_backward"]
+           "wc_linear_cross_entropy", "wc_linear_cross_entropy_backward_scratch", "wc_linear_cross_entropy_backward",
+           "wc_linear4", "wc_quantize4"]
 # encoder word-store forms (wc_set_encoder_words)
 ENC_WORDS_AUTO, ENC_WORDS_DIRECT, ENC_WORDS_STAGED = 0, 1, 2
 
@@ -147,6 +148,13 @@ class wc_linear_loss_grad(ctypes.Structure):
                 ("reserved", ctypes.c_uint32)]
 
 
+class wc_fourbit(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_void_p), ("x_stride", ctypes.c_uint64), ("q", ctypes.c_void_p),
+                ("scales", ctypes.c_void_p), ("zeros", ctypes.c_void_p), ("y", ctypes.c_void_p),
+                ("y_stride", ctypes.c_uint64), ("m", ctypes.c_uint64), ("rows", ctypes.c_uint32),
+                ("cols", ctypes.c_uint32), ("group", ctypes.c_uint32), ("type", ctypes.c_uint32)]
+
+
 _lib = None
 
 
@@ -190,6 +198,8 @@ def lib() -> ctypes.CDLL:
     L.wc_moe_layer_scratch.restype = U64
     L.wc_moe_layer.argtypes = [ctypes.POINTER(wc_moe), P, U64, P]
     L.wc_token_logprobs_backward.argtypes = [ctypes.POINTER(wc_logprobs_grad), P, P]
+    L.wc_linear4.argtypes, L.wc_linear4.restype = [ctypes.POINTER(wc_fourbit), P], I
+    L.wc_quantize4.argtypes, L.wc_quantize4.restype = [P, U64, U64, U32, U32, U32, P, P, P, P], I
     for name, args, sizes in (("wc_grouped_linear", wc_grouped, [U64, U32, U32, U32]),
                               ("wc_grouped_linear_backward", wc_grouped_grad, [U64, U32, U32, U32]),
                               ("wc_linear_cross_entropy", wc_linear_loss, [U64, U32, U32]),
@@ -421,6 +431,15 @@ def wc_linear_cross_entropy_backward_scratch(m: int, vocab: int, cols: int) -> i
 def wc_linear_cross_entropy_backward(args: wc_linear_loss_grad, d_scratch, scratch_bytes: int, d_err=None, stream=None):
     rc = lib().wc_linear_cross_entropy_backward(args, _ptr(d_scratch), scratch_bytes, _ptr(d_err), _stream(stream))
     _check(rc, "wc_linear_cross_entropy_backward")
+
+
+def wc_linear4(args: wc_fourbit, stream=None):
+    _check(lib().wc_linear4(args, _stream(stream)), "wc_linear4")
+
+
+def wc_quantize4(w, w_stride: int, rows: int, cols: int, group: int, type: int, q, scales, zeros=None, stream=None):
+    _check(lib().wc_quantize4(_ptr(w), w_stride, rows, cols, group, type, _ptr(q), _ptr(scales), _ptr(zeros), _stream(stream)),
+           "wc_quantize4")
 
 
 def wc_check_division(samples_per_divisor: int = 256) -> int:

@@ -12,7 +12,8 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libwc.so")
 SOURCES = [os.path.join(CSRC, "wc_lib.hip"), os.path.join(CSRC, "wc_noalloc.hip"),
-           os.path.join(CSRC, "ops", "wc_ops.hip"), os.path.join(CSRC, "ops", "wc_products.hip")]
+           os.path.join(CSRC, "ops", "wc_ops.hip"), os.path.join(CSRC, "ops", "wc_products.hip"),
+           os.path.join(CSRC, "ops", "wc_fourbit.hip")]
 
 ARCH = "gfx950"
 

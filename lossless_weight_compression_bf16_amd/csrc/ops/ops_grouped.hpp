@@ -36,7 +36,9 @@ struct GroupedArgs {
 // Rows of an expert, whatever the ends are (from 0 on, and not past m).
 __device__ __forceinline__ uint32_t group_end(const int64_t *ends, uint32_t e, uint32_t m)
 {
-    const int64_t v = ends[e];
+    // nothing writes the ends while the kernel runs: one number for all lanes is a scalar load, which does not wait for the
+    // vector memory's queue
+    const int64_t v = ((__attribute__((address_space(4))) const int64_t *)ends)[e];
     return v < 0 ? 0u : v < (int64_t)m ? (uint32_t)v : m;
 }
 __device__ __forceinline__ void group_rows(const int64_t *ends, uint32_t e, uint32_t m, uint32_t &lo, uint32_t &hi)
@@ -89,20 +91,21 @@ struct Groups {
     __device__ __forceinline__ void find(const GroupedArgs &g, uint32_t u, F units, uint32_t &expert, uint32_t &lo, uint32_t &hi,
                                          uint32_t &place) const
     {
-        const uint32_t lane = threadIdx.x & 63, owner = (uint32_t)__builtin_ctzll(__ballot(upto > u));
-        uint32_t rest = u - (upto - mine), e = lane, from = this->lo, to = this->hi;
-        if (per > 1 && lane == owner)
-            for (uint32_t q = 0; q < per; q++) {
-                e = per * lane + q;
-                group_rows(g.ends, e, g.m, from, to);
-                const uint32_t n = units(to - from);
-                if (rest < n) break;
-                rest -= n;
-            }
-        expert = (uint32_t)__builtin_amdgcn_readlane((int)e, owner);
-        lo = (uint32_t)__builtin_amdgcn_readlane((int)from, owner);
-        hi = (uint32_t)__builtin_amdgcn_readlane((int)to, owner);
-        place = (uint32_t)__builtin_amdgcn_readlane((int)rest, owner);
+        const uint32_t owner = (uint32_t)__builtin_ctzll(__ballot(upto > u));
+        place = u - (uint32_t)__builtin_amdgcn_readlane((int)(upto - mine), owner);
+        expert = per * owner;
+        if (per == 1) {
+            lo = (uint32_t)__builtin_amdgcn_readlane((int)this->lo, owner);
+            hi = (uint32_t)__builtin_amdgcn_readlane((int)this->hi, owner);
+            return;
+        }
+        for (uint32_t q = 0; q < per; q++) {
+            expert = min(per * owner + q, g.experts - 1);
+            group_rows(g.ends, expert, g.m, lo, hi);
+            const uint32_t n = units(hi - lo);
+            if (place < n) break;
+            place -= n;
+        }
     }
 };
 
@@ -168,42 +171,77 @@ struct GroupedPieces {
 };
 
 // y (kPAlong) or dx by tiles: an expert's rows in tiles of BM against tiles of
-// BN columns.  Grid: 8 ceil(tiles / 8) for the most pieces there can be.
+// BN columns.  Grid: 8 ceil(tiles / 8) for the most pieces there can be, or kCus (each_tile).
 template <int T, int BM, int BN, bool kPAlong>
 __global__ __launch_bounds__(256, tile_blocks(BM, BN)) void k_grouped(GroupedArgs g)
 {
     using Ti = Tile<T, BM, BN, true, kPAlong>;
+    struct Job {
+        typename Ti::Place place;
+        uint32_t m0, rows, n0, part;  // part: of the tiles in parts, or none
+    };
     __shared__ __attribute__((aligned(1024))) char b0[Ti::kBytes];
     __shared__ __attribute__((aligned(1024))) char b1[Ti::kBytes];
     check_ends(g.ends, g.experts, g.m, g.err);
     GroupedPieces<BM, BN> p;
     p.init(g);
-    uint32_t t, expert, m0, rows, n0;
-    const uint32_t kind = p.piece(blockIdx.x, t);
-    if (kind == 3) return;
-    if (kind == 2) {
-        m0 = p.last + BM * (t / p.across);
-        n0 = BN * (t % p.across);
-        const uint32_t cols = min((uint32_t)BN, g.n - n0) / 8;
-        for (uint32_t q = threadIdx.x; q < min((uint32_t)BM, g.m - m0) * cols; q += 256)
-            *reinterpret_cast<u32x4 *>(g.y + (m0 + q / cols) * g.y_stride + n0 + 8 * (q % cols)) = u32x4{0, 0, 0, 0};
-        return;
+    Ti ti(g.x_stride, g.w_row);
+    uint32_t turn = 0;
+    each_tile<Ti, Job>(
+        ti, b0, b1,
+        [&](uint32_t, Job &j) {
+            for (;; turn++) {
+                uint32_t t, expert;
+                const uint32_t kind = p.piece(block_of(turn), t);
+                if (kind == 3) return false;
+                if (kind == 2) {
+                    const uint32_t m0 = p.last + BM * (t / p.across), n0 = BN * (t % p.across), cols = min((uint32_t)BN, g.n - n0) / 8;
+                    for (uint32_t q = threadIdx.x; q < min((uint32_t)BM, g.m - m0) * cols; q += 256)
+                        *reinterpret_cast<u32x4 *>(g.y + (m0 + q / cols) * g.y_stride + n0 + 8 * (q % cols)) = u32x4{0, 0, 0, 0};
+                    continue;
+                }
+                const uint32_t split = kind ? t / p.left : 0, splits = kind ? p.splits : 1;
+                if (!p.tile(g, kind ? p.whole + t % p.left : t, expert, j.m0, j.rows, j.n0)) continue;
+                j.part = splits > 1 ? t : ~0u;
+                const uint32_t k0 = kTileK * (p.stages * split / splits), k = min(g.k, kTileK * (p.stages * (split + 1) / splits)) - k0;
+                const uint16_t *w = g.w + expert * g.w_expert;
+                j.place.q = Ti::Q::Where::at(g.x + j.m0 * g.x_stride + k0, j.rows, k);
+                if constexpr (kPAlong) j.place.p = Ti::P::Where::at(w + (uint64_t)j.n0 * g.w_row + k0, min((uint32_t)BN, g.n - j.n0), k);
+                else j.place.p = Ti::P::Where::at(w + (uint64_t)k0 * g.w_row + j.n0, k, g.n - j.n0);
+                j.place.k = k;
+                turn++;
+                return true;
+            }
+        },
+        [&](const Ti &ti, const Job &j) {
+            if (j.part != ~0u) {
+                float *part = g.part + (uint64_t)j.part * (BM * BN);
+                each_four(ti, [&](uint32_t row, uint32_t col, f32x4 v) {
+                    if (row < j.rows && j.n0 + col < g.n) *reinterpret_cast<f32x4 *>(part + row * BN + col) = v;
+                });
+            } else {
+                uint16_t *y = g.y + j.m0 * g.y_stride + j.n0;
+                each_eight<T>(ti, AsIs{}, [&](uint32_t row, uint32_t col, u32x4 v) {
+                    if (row < j.rows && j.n0 + col < g.n) *reinterpret_cast<u32x4 *>(y + row * g.y_stride + col) = v;
+                });
+            }
+        });
+}
+
+// The sum of n parts, `step` numbers apart, in their order; eight are on their way at once.
+__device__ __forceinline__ f32x4 sum_parts(const float *p, uint64_t step, uint32_t n)
+{
+    f32x4 sum = *reinterpret_cast<const f32x4 *>(p);
+    uint32_t s = 1;
+    for (; s + 8 <= n; s += 8) {
+        f32x4 v[8];
+#pragma unroll
+        for (uint32_t q = 0; q < 8; q++) v[q] = *reinterpret_cast<const f32x4 *>(p + (s + q) * step);
+#pragma unroll
+        for (uint32_t q = 0; q < 8; q++) sum += v[q];
     }
-    const uint32_t split = kind ? t / p.left : 0, splits = kind ? p.splits : 1;
-    if (!p.tile(g, kind ? p.whole + t % p.left : t, expert, m0, rows, n0)) return;
-    const uint32_t k0 = kTileK * (p.stages * split / splits), k = min(g.k, kTileK * (p.stages * (split + 1) / splits)) - k0;
-    const uint16_t *w = g.w + expert * g.w_expert;
-    Ti ti;
-    ti.q.init(g.x + m0 * g.x_stride + k0, g.x_stride, rows, k);
-    if constexpr (kPAlong) ti.p.init(w + (uint64_t)n0 * g.w_row + k0, g.w_row, min((uint32_t)BN, g.n - n0), k);
-    else ti.p.init(w + (uint64_t)k0 * g.w_row + n0, g.w_row, k, g.n - n0);
-    ti.product(b0, b1, nullptr, k, rows);
-    float *part = g.part + (uint64_t)t * (BM * BN);
-    each_four(ti, [&](uint32_t row, uint32_t col, f32x4 v) {
-        if (row >= rows || n0 + col >= g.n) return;
-        if (splits > 1) *reinterpret_cast<f32x4 *>(part + row * BN + col) = v;
-        else store_four<T>(g.y + (m0 + row) * g.y_stride + n0 + col, v);
-    });
+    for (; s < n; s++) sum += *reinterpret_cast<const f32x4 *>(p + s * step);
+    return sum;
 }
 
 // The sums of the tiles in parts, in the order of k.  Grid: kSlots / 2 tiles, and 8 blocks for each.
@@ -220,9 +258,7 @@ __global__ __launch_bounds__(256) void k_grouped_join(GroupedArgs g)
         const uint32_t row = from + e / (BN / 4), col = 4 * (e % (BN / 4));
         if (row >= rows || n0 + col >= g.n) continue;
         const float *part = g.part + (uint64_t)q * (BM * BN) + row * BN + col;
-        f32x4 v = *reinterpret_cast<const f32x4 *>(part);
-        for (uint32_t s = 1; s < p.splits; s++) v += *reinterpret_cast<const f32x4 *>(part + (uint64_t)s * p.left * (BM * BN));
-        store_four<T>(g.y + (m0 + row) * g.y_stride + n0 + col, v);
+        store_four<T>(g.y + (m0 + row) * g.y_stride + n0 + col, sum_parts(part, (uint64_t)p.left * (BM * BN), p.splits));
     }
 }
 
@@ -237,38 +273,62 @@ struct GroupedDwArgs {
     uint32_t *err;
 };
 
-// dW by tiles of BM rows and BN columns of it.  Grid: experts x 8 ceil(tiles of one / 8).
+// dW by tiles of BM rows and BN columns of it.  Grid: experts x 8 ceil(tiles of one / 8), or kCus (each_tile).
 template <int T, int BM, int BN>
 __global__ __launch_bounds__(256, tile_blocks(BM, BN)) void k_grouped_dw(GroupedDwArgs g)
 {
     using Ti = Tile<T, BM, BN, false, false>;
+    struct Job {
+        typename Ti::Place place;
+        uint32_t expert, split, m0, rows, n0;
+    };
     __shared__ __attribute__((aligned(1024))) char b0[Ti::kBytes];
     __shared__ __attribute__((aligned(1024))) char b1[Ti::kBytes];
     check_ends(g.ends, g.experts, g.m, g.err);
     const uint32_t down = (g.n + BM - 1) / BM, across = (g.k + BN - 1) / BN, each = down * across;
     // every XCD has an eighth of each expert: the experts have different numbers of rows
-    const uint32_t pieces = each * g.splits, per = (pieces + 7) / 8, expert = blockIdx.x / 8 / per;
-    const uint32_t t = blockIdx.x % 8 * per + blockIdx.x / 8 % per;
-    if (expert >= g.experts || t >= pieces) return;
-    const uint32_t split = t / each;
-    uint32_t r, c, lo, hi;
-    tile_of(t % each, down, across, r, c);
-    group_rows(g.ends, expert, g.m, lo, hi);
-    const uint32_t stages = (hi - lo + kTileK - 1) / kTileK;
-    const uint32_t from = min(hi, lo + kTileK * (uint32_t)((uint64_t)stages * split / g.splits));
-    const uint32_t rows = min(hi, lo + kTileK * (uint32_t)((uint64_t)stages * (split + 1) / g.splits)) - from;
-    const uint32_t m0 = BM * r, n0 = BN * c;
-    Ti ti;
-    ti.q.init(g.dy + from * g.dy_stride + m0, g.dy_stride, rows, g.n - m0);
-    ti.p.init(g.x + from * g.x_stride + n0, g.x_stride, rows, g.k - n0);
-    ti.product(b0, b1, nullptr, rows);
-    const uint64_t all = (uint64_t)g.experts * g.n * g.k;
-    each_four(ti, [&](uint32_t row, uint32_t col, f32x4 v) {
-        if (m0 + row >= g.n || n0 + col >= g.k) return;
-        const uint64_t at = ((uint64_t)expert * g.n + m0 + row) * g.k + n0 + col;
-        if (g.splits > 1) *reinterpret_cast<f32x4 *>(g.part + split * all + at) = v;
-        else store_four<T>(g.dw + at, v);
-    });
+    const uint32_t pieces = each * g.splits, per = (pieces + 7) / 8;
+    Ti ti(g.dy_stride, g.x_stride);
+    uint32_t turn = 0;
+    each_tile<Ti, Job>(
+        ti, b0, b1,
+        [&](uint32_t, Job &j) {
+            for (;; turn++) {
+                const uint32_t b = block_of(turn), t = b % 8 * per + b / 8 % per;
+                j.expert = b / 8 / per;
+                if (j.expert >= g.experts) return false;
+                if (t >= pieces) continue;
+                j.split = t / each;
+                uint32_t r, c, lo, hi;
+                tile_of(t % each, down, across, r, c);
+                group_rows(g.ends, j.expert, g.m, lo, hi);
+                const uint32_t stages = (hi - lo + kTileK - 1) / kTileK;
+                const uint32_t from = min(hi, lo + kTileK * (uint32_t)((uint64_t)stages * j.split / g.splits));
+                const uint32_t to = min(hi, lo + kTileK * (uint32_t)((uint64_t)stages * (j.split + 1) / g.splits));
+                j.m0 = BM * r;
+                j.n0 = BN * c;
+                j.rows = BM;
+                j.place.q = Ti::Q::Where::at(g.dy + from * g.dy_stride + j.m0, to - from, g.n - j.m0);
+                j.place.p = Ti::P::Where::at(g.x + from * g.x_stride + j.n0, to - from, g.k - j.n0);
+                j.place.k = to - from;
+                turn++;
+                return true;
+            }
+        },
+        [&](const Ti &ti, const Job &j) {
+            const uint64_t at = ((uint64_t)j.expert * g.n + j.m0) * g.k + j.n0;
+            if (g.splits > 1) {
+                float *part = g.part + j.split * ((uint64_t)g.experts * g.n * g.k) + at;
+                each_four(ti, [&](uint32_t row, uint32_t col, f32x4 v) {
+                    if (j.m0 + row < g.n && j.n0 + col < g.k) *reinterpret_cast<f32x4 *>(part + (uint64_t)row * g.k + col) = v;
+                });
+            } else {
+                uint16_t *dw = g.dw + at;
+                each_eight<T>(ti, AsIs{}, [&](uint32_t row, uint32_t col, u32x4 v) {
+                    if (j.m0 + row < g.n && j.n0 + col < g.k) *reinterpret_cast<u32x4 *>(dw + (uint64_t)row * g.k + col) = v;
+                });
+            }
+        });
 }
 
 constexpr uint32_t kLossRowBlocks = 256;
@@ -310,10 +370,7 @@ __global__ __launch_bounds__(256) void k_join(JoinArgs g)
     const uint64_t q = (uint64_t)blockIdx.x * 256 + threadIdx.x, row = q / per;
     if (row >= g.rows) return;
     const uint32_t col = 4 * (uint32_t)(q % per);
-    const float *p = g.part + row * g.cols + col;
-    f32x4 v = *reinterpret_cast<const f32x4 *>(p);
-    for (uint32_t s = 1; s < g.splits; s++) v += *reinterpret_cast<const f32x4 *>(p + s * g.rows * g.cols);
-    v *= unscale;
+    const f32x4 v = sum_parts(g.part + row * g.cols + col, g.rows * g.cols, g.splits) * unscale;
     store_four<T>(g.out + row * g.out_stride + col, v);
 }
 

@@ -45,55 +45,85 @@ struct Stat {
     }
 };
 
-// Statistics of a block's tile: rows of m0, columns of n0 on.
+// A tile of z: rows from m0 on against columns from n0 on.
+template <class Ti>
+struct LogitsJob {
+    typename Ti::Place place;
+    uint32_t m0, rows, n0, cols;
+
+    // Tile (r, c) of m rows of h and v rows of w, of k values each.
+    template <int BM, int BN>
+    __device__ __forceinline__ void set(uint32_t r, uint32_t c, const uint16_t *h, uint64_t h_stride, uint32_t m, const uint16_t *w,
+                                        uint64_t w_row, uint32_t v, uint32_t k)
+    {
+        m0 = BM * r;
+        rows = min((uint32_t)BM, m - m0);
+        n0 = BN * c;
+        cols = min((uint32_t)BN, v - n0);
+        place.q = Ti::Q::Where::at(h + m0 * h_stride, rows, k);
+        place.p = Ti::P::Where::at(w + n0 * w_row, cols, k);
+        place.k = k;
+    }
+};
+
+// Statistics of a block's tiles.  Grid: 8 ceil(tiles / 8), or kCus (each_tile).
 template <int T, int BM, int BN>
 __global__ __launch_bounds__(256, tile_blocks(BM, BN)) void k_loss(LossArgs g)
 {
     using Ti = Tile<T, BM, BN, true, true>;
+    using Job = LogitsJob<Ti>;
     __shared__ __attribute__((aligned(1024))) char b0[Ti::kBytes];
     __shared__ __attribute__((aligned(1024))) char b1[Ti::kBytes];
-    float2(*stats)[BM] = reinterpret_cast<float2(*)[BM]>(b0);  // a wave's, when the operands are done
-    const uint32_t down = (g.m + BM - 1) / BM, t = xcd_piece(blockIdx.x, down * g.parts);
-    if (t >= down * g.parts) return;
-    uint32_t r, c;
-    tile_of(t, down, g.parts, r, c);
-    const uint32_t m0 = BM * r, rows = min((uint32_t)BM, g.m - m0), n0 = BN * c, cols = min((uint32_t)BN, g.vocab - n0);
+    __shared__ float2 own[Ti::kNamed ? Ti::kWavesN : 1][Ti::kNamed ? BM : 1];
+    // a wave's: where no other tile's operands are on their way, in their place
+    float2(*stats)[BM] = reinterpret_cast<float2(*)[BM]>(Ti::kNamed ? (void *)own : (void *)b0);
+    const uint32_t down = (g.m + BM - 1) / BM;
     const uint32_t wave = threadIdx.x >> 6, lane = threadIdx.x & 63, i = lane & 15, gr = lane >> 4;
-    Ti ti;
-    ti.q.init(g.h + m0 * g.h_stride, g.h_stride, rows, g.k);
-    ti.p.init(g.w + (uint64_t)n0 * g.w_row, g.w_row, cols, g.k);
-    ti.product(b0, b1, nullptr, g.k, rows);
+    Ti ti(g.h_stride, g.w_row);
+    each_tile<Ti, Job>(
+        ti, b0, b1,
+        [&](uint32_t n, Job &j) {
+            const uint32_t t = xcd_piece(block_of(n), down * g.parts);
+            if (t >= down * g.parts) return false;
+            uint32_t r, c;
+            tile_of(t, down, g.parts, r, c);
+            j.template set<BM, BN>(r, c, g.h, g.h_stride, g.m, g.w, g.w_row, g.vocab, g.k);
+            return true;
+        },
+        [&](const Ti &ti, const Job &j) {
+            if constexpr (!Ti::kNamed) Ti::all_done();
 #pragma unroll
-    for (int b = 0; b < Ti::kM; b++) {
-        const uint32_t row = 16 * (wave / Ti::kWavesN + Ti::kWavesM * b) + i, first = 16 * (wave % Ti::kWavesN) + 4 * gr;
-        const int64_t token = row < rows ? g.tokens[m0 + row] - n0 : -1;
-        Stat s{-kInf, 0.f};
+            for (int b = 0; b < Ti::kM; b++) {
+                const uint32_t row = Ti::q_row(wave, b) + i;
+                const int64_t token = row < j.rows ? g.tokens[j.m0 + row] - j.n0 : -1;
+                Stat s{-kInf, 0.f};
 #pragma unroll
-        for (int a = 0; a < Ti::kN; a++)
+                for (int a = 0; a < Ti::kN; a++)
 #pragma unroll
-            for (int e = 0; e < 4; e++) {
-                const uint32_t col = first + 16 * Ti::kWavesN * a + e;
-                const float z = ti.acc[a][b][e];
-                if (col < cols) s.most = fmaxf(s.most, z);
-                if (token == (int64_t)col && col < cols) g.given[m0 + row] = z;
+                    for (int e = 0; e < 4; e++) {
+                        const uint32_t col = Ti::p_row(wave, a) + 4 * gr + e;
+                        const float z = ti.acc[a][b][e];
+                        if (col < j.cols) s.most = fmaxf(s.most, z);
+                        if (token == (int64_t)col && col < j.cols) g.given[j.m0 + row] = z;
+                    }
+                const float base = Stat::base(s.most);
+#pragma unroll
+                for (int a = 0; a < Ti::kN; a++)
+#pragma unroll
+                    for (int e = 0; e < 4; e++)
+                        if (Ti::p_row(wave, a) + 4 * gr + e < j.cols) s.sum += exp2_fast((ti.acc[a][b][e] - base) * kLog2e);
+                s.join(__shfl_xor(s.most, 16, 64), __shfl_xor(s.sum, 16, 64));
+                s.join(__shfl_xor(s.most, 32, 64), __shfl_xor(s.sum, 32, 64));
+                if (gr == 0) stats[wave % Ti::kWavesN][row] = float2{s.most, s.sum};
             }
-        const float base = Stat::base(s.most);
+            lds_barrier();
+            if (threadIdx.x < j.rows) {
+                Stat s{stats[0][threadIdx.x].x, stats[0][threadIdx.x].y};
 #pragma unroll
-        for (int a = 0; a < Ti::kN; a++)
-#pragma unroll
-            for (int e = 0; e < 4; e++)
-                if (first + 16 * Ti::kWavesN * a + e < cols) s.sum += exp2_fast((ti.acc[a][b][e] - base) * kLog2e);
-        s.join(__shfl_xor(s.most, 16, 64), __shfl_xor(s.sum, 16, 64));
-        s.join(__shfl_xor(s.most, 32, 64), __shfl_xor(s.sum, 32, 64));
-        if (gr == 0) stats[wave % Ti::kWavesN][row] = float2{s.most, s.sum};
-    }
-    __syncthreads();
-    if (threadIdx.x < rows) {
-        Stat s{stats[0][threadIdx.x].x, stats[0][threadIdx.x].y};
-#pragma unroll
-        for (int w = 1; w < Ti::kWavesN; w++) s.join(stats[w][threadIdx.x].x, stats[w][threadIdx.x].y);
-        g.part[(uint64_t)(m0 + threadIdx.x) * g.parts + c] = float2{s.most, s.sum};
-    }
+                for (int w = 1; w < Ti::kWavesN; w++) s.join(stats[w][threadIdx.x].x, stats[w][threadIdx.x].y);
+                g.part[(uint64_t)(j.m0 + threadIdx.x) * g.parts + j.n0 / BN] = float2{s.most, s.sum};
+            }
+        });
 }
 
 // The same for up to 32 rows: 32 columns of z for a block (128 without kSplit).
@@ -250,40 +280,46 @@ __device__ __forceinline__ float loss_gradient(f32x4 row, float z, uint32_t v, f
     return scale * ((int32_t)v == __builtin_bit_cast(int32_t, (float)row[3]) ? p - row[2] : p);
 }
 
-// G of a tile.
+// G of a block's tiles.  Grid: 8 ceil(tiles / 8), or kCus (each_tile).
 template <int T, int BM, int BN>
 __global__ __launch_bounds__(256, tile_blocks(BM, BN)) void k_loss_grad(LossGradArgs g)
 {
     using Ti = Tile<T, BM, BN, true, true>;
+    using Job = LogitsJob<Ti>;
     __shared__ __attribute__((aligned(1024))) char b0[Ti::kBytes];
     __shared__ __attribute__((aligned(1024))) char b1[Ti::kBytes];
-    const uint32_t down = (g.m + BM - 1) / BM, across = (g.width + BN - 1) / BN, t = xcd_piece(blockIdx.x, down * across);
-    if (t >= down * across) return;
-    uint32_t r, c;
-    tile_of(t, down, across, r, c);
-    const uint32_t m0 = BM * r, rows = min((uint32_t)BM, g.m - m0), n0 = BN * c, cols = min((uint32_t)BN, g.width - n0);
-    Ti ti;
-    ti.q.init(g.h + m0 * g.h_stride, g.h_stride, rows, g.k);
-    ti.p.init(g.w + (uint64_t)(g.v0 + n0) * g.w_row, g.w_row, cols, g.k);
-    ti.product(b0, b1, nullptr, g.k, rows);
+    const uint32_t down = (g.m + BM - 1) / BM, across = (g.width + BN - 1) / BN, wave = threadIdx.x >> 6;
     float unscale;
     const float scale = loss_scale<T>(g.most, unscale);
-    const uint32_t wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+    Ti ti(g.h_stride, g.w_row);
+    each_tile<Ti, Job>(
+        ti, b0, b1,
+        [&](uint32_t n, Job &j) {
+            const uint32_t t = xcd_piece(block_of(n), down * across);
+            if (t >= down * across) return false;
+            uint32_t r, c;
+            tile_of(t, down, across, r, c);
+            j.template set<BM, BN>(r, c, g.h, g.h_stride, g.m, g.w + (uint64_t)g.v0 * g.w_row, g.w_row, g.width, g.k);
+            return true;
+        },
+        [&](const Ti &ti, const Job &j) {
+            f32x4 info[Ti::kM];
 #pragma unroll
-    for (int b = 0; b < Ti::kM; b++) {
-        const uint32_t row = 16 * (wave / Ti::kWavesN + Ti::kWavesM * b) + (lane & 15);
-        if (row >= rows) continue;
-        const f32x4 info = g.rows[m0 + row];
-        uint16_t *to = g.grad + (uint64_t)(m0 + row) * g.pitch + n0;
+            for (int b = 0; b < Ti::kM; b++) info[b] = g.rows[j.m0 + min(Ti::q_row(wave, b) + (threadIdx.x & 15), j.rows - 1)];
+            uint16_t *to = g.grad + (uint64_t)j.m0 * g.pitch + j.n0;
+            each_eight<T>(
+                ti,
+                [&](uint32_t row, uint32_t col, f32x4 z) {
+                    const f32x4 of_row = info[(row / 16 - wave / Ti::kWavesN) / Ti::kWavesM];
 #pragma unroll
-        for (int a = 0; a < Ti::kN; a++) {
-            const uint32_t col = 16 * (wave % Ti::kWavesN + Ti::kWavesN * a) + 4 * (lane >> 4);
-            f32x4 z = ti.acc[a][b];
-#pragma unroll
-            for (uint32_t e = 0; e < 4; e++) z[e] = col + e < cols ? loss_gradient(info, z[e], g.v0 + n0 + col + e, scale) : 0.f;
-            if (n0 + col < g.pitch) store_four<T>(to + col, z);
-        }
-    }
+                    for (uint32_t e = 0; e < 4; e++)
+                        z[e] = col + e < j.cols ? loss_gradient(of_row, z[e], g.v0 + j.n0 + col + e, scale) : 0.f;
+                    return z;
+                },
+                [&](uint32_t row, uint32_t col, u32x4 v) {
+                    if (row < j.rows && j.n0 + col < g.pitch) *reinterpret_cast<u32x4 *>(to + (uint64_t)row * g.pitch + col) = v;
+                });
+        });
 }
 
 // The same for up to 32 rows.
@@ -328,39 +364,60 @@ struct ProductArgs {
     const float *most;        // of G, by which it was scaled
 };
 
-// D = Q P^T of whole matrices.  kQAlong: k along the rows of Q's memory; P has it across.
+// D = Q P^T of whole matrices.  kQAlong: k along the rows of Q's memory; P has
+// it across.  Grid: 8 ceil(tiles / 8), or kCus (each_tile).
 template <int T, int BM, int BN, bool kQAlong>
 __global__ __launch_bounds__(256, tile_blocks(BM, BN)) void k_product(ProductArgs g)
 {
     using Ti = Tile<T, BM, BN, kQAlong, false>;
+    struct Job {
+        typename Ti::Place place;
+        uint32_t split, m0, rows, n0;
+    };
     __shared__ __attribute__((aligned(1024))) char b0[Ti::kBytes];
     __shared__ __attribute__((aligned(1024))) char b1[Ti::kBytes];
     const uint32_t down = (g.m + BM - 1) / BM, across = (g.n + BN - 1) / BN, each = down * across;
-    const uint32_t t = xcd_piece(blockIdx.x, each * g.splits);
-    if (t >= each * g.splits) return;
-    const uint32_t split = t / each;
-    uint32_t r, c;
-    tile_of(t % each, down, across, r, c);
-    const uint32_t m0 = BM * r, rows = min((uint32_t)BM, g.m - m0), n0 = BN * c;
-    const uint32_t stages = (g.k + kTileK - 1) / kTileK, k0 = kTileK * (uint32_t)((uint64_t)stages * split / g.splits);
-    const uint32_t k1 = min(g.k, kTileK * (uint32_t)((uint64_t)stages * (split + 1) / g.splits)), k = k1 > k0 ? k1 - k0 : 0;
-    Ti ti;
-    // G has whole 16 bytes of a row, zeros behind its width
-    if constexpr (kQAlong) ti.q.init(g.q + m0 * g.q_stride + k0, g.q_stride, rows, (k + 7) / 8 * 8);
-    else ti.q.init(g.q + k0 * g.q_stride + m0, g.q_stride, k, (g.m + 7) / 8 * 8 - m0);
-    ti.p.init(g.p + k0 * g.p_stride + n0, g.p_stride, k, g.n - n0);
-    ti.product(b0, b1, nullptr, k);
+    const uint32_t stages = (g.k + kTileK - 1) / kTileK;
     float unscale;
     loss_scale<T>(g.most, unscale);
-    each_four(ti, [&](uint32_t row, uint32_t col, f32x4 v) {
-        if (row >= rows || n0 + col >= g.n) return;
-        if (g.part) {
-            f32x4 *to = reinterpret_cast<f32x4 *>(g.part + ((uint64_t)split * g.m + m0 + row) * g.n + n0 + col);
-            *to = g.add ? *to + v : v;
-        } else {
-            store_four<T>(g.out + (m0 + row) * g.out_stride + n0 + col, v * unscale);
-        }
-    });
+    Ti ti(g.q_stride, g.p_stride);
+    each_tile<Ti, Job>(
+        ti, b0, b1,
+        [&](uint32_t n, Job &j) {
+            const uint32_t t = xcd_piece(block_of(n), each * g.splits);
+            if (t >= each * g.splits) return false;
+            uint32_t r, c;
+            tile_of(t % each, down, across, r, c);
+            j.split = t / each;
+            j.m0 = BM * r;
+            j.rows = min((uint32_t)BM, g.m - j.m0);
+            j.n0 = BN * c;
+            const uint32_t k0 = kTileK * (uint32_t)((uint64_t)stages * j.split / g.splits);
+            const uint32_t k = min(g.k, kTileK * (uint32_t)((uint64_t)stages * (j.split + 1) / g.splits)) - k0;
+            // G has whole 16 bytes of a row, zeros behind its width
+            if constexpr (kQAlong) j.place.q = Ti::Q::Where::at(g.q + j.m0 * g.q_stride + k0, j.rows, (k + 7) / 8 * 8);
+            else j.place.q = Ti::Q::Where::at(g.q + k0 * g.q_stride + j.m0, k, (g.m + 7) / 8 * 8 - j.m0);
+            j.place.p = Ti::P::Where::at(g.p + k0 * g.p_stride + j.n0, k, g.n - j.n0);
+            j.place.k = k;
+            return true;
+        },
+        [&](const Ti &ti, const Job &j) {
+            if (g.part) {
+                float *part = g.part + ((uint64_t)j.split * g.m + j.m0) * g.n + j.n0;
+                each_four(ti, [&](uint32_t row, uint32_t col, f32x4 v) {
+                    if (row >= j.rows || j.n0 + col >= g.n) return;
+                    f32x4 *to = reinterpret_cast<f32x4 *>(part + (uint64_t)row * g.n + col);
+                    *to = g.add ? *to + v : v;
+                });
+            } else {
+                uint16_t *out = g.out + j.m0 * g.out_stride + j.n0;
+                each_eight<T>(ti, [&](uint32_t, uint32_t, f32x4 v) { return v * unscale; },
+                              [&](uint32_t row, uint32_t col, u32x4 v) {
+                                  if (row < j.rows && j.n0 + col < g.n)
+                                      *reinterpret_cast<u32x4 *>(out + row * g.out_stride + col) = v;
+                              });
+            }
+        });
 }
 
 }  // namespace ops

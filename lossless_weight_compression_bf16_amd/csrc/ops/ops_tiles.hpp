@@ -63,22 +63,27 @@ struct Operand {
     static constexpr uint32_t kBytes = place(R / 8 - 1) + 1024;
     __device__ __forceinline__ static uint32_t swap(uint32_t k) { return R == 256 ? 2 * (k & 1) : 2 * (k & 3); }
 
-    const char *base;
+    // Where an operand lies.  kAlong: `base` is the tile's first row, `rows` exist, each
+    // of width / 2 values of k.  Otherwise `base` is the tile's first column in
+    // row 0 of `rows` rows of k, of which `width` bytes exist from there on.
+    struct Where {
+        const char *base;
+        uint32_t rows, width;
+
+        __device__ __forceinline__ Where said_uniform() const { return {uniform(base), uniform(rows), uniform(width)}; }
+        __device__ __forceinline__ static Where at(const void *from, uint32_t n, uint32_t values)
+        {
+            return {static_cast<const char *>(from), n, 2 * values};
+        }
+    };
+
     uint32_t pitch;        // bytes, below 2^23
-    uint32_t rows;         // of memory that exist
-    uint32_t width;        // bytes of a row that exist
     uint32_t off[kLoads];  // the lane's in each load
 
-    // kAlong: `from` is the tile's first row, `n` rows exist, each of `k` values.
-    // Otherwise `from` is the tile's first column in row 0 of `n` rows of k;
-    // `k` columns exist from there on.
-    __device__ __forceinline__ void init(const void *from, uint64_t row_elems, uint32_t n, uint32_t k)
+    __device__ __forceinline__ void init(uint64_t row_elems)
     {
         const uint32_t wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-        base = uniform(static_cast<const char *>(from));
         pitch = uniform(2 * (uint32_t)row_elems);
-        rows = uniform(n);
-        width = uniform(2 * k);
 #pragma unroll
         for (uint32_t j = 0; j < kLoads; j++) {
             constexpr uint32_t kPerRow = 64 / kRowsOfLoad;  // lanes of a row
@@ -92,27 +97,29 @@ struct Operand {
         uint32_t none[2];               // of every second load: past the window for lanes whose k do not exist
     };
     // The stage of k0 .. k0 + 63, of `k` values of k in all.
-    __device__ __forceinline__ Stage stage(uint32_t k0, uint32_t k) const
+    __device__ __forceinline__ Stage stage(const Where &w, uint32_t k0, uint32_t k) const
     {
         Stage s;
         if constexpr (kAlong) {
-            const uint32_t n = rows && k0 < k ? (rows - 1) * pitch + width - 2 * k0 : 0;
-            s.window = __builtin_amdgcn_make_buffer_rsrc((void *)(base + 2ull * k0), 0, n, 0x00020000);
+            const uint32_t n = w.rows && k0 < k ? (w.rows - 1) * pitch + w.width - 2 * k0 : 0;
+            s.window = __builtin_amdgcn_make_buffer_rsrc((void *)uniform(w.base + 2ull * k0), 0, uniform(n), 0x00020000);
 #pragma unroll
             for (uint32_t j = 0; j < 2; j++) {
                 const uint32_t wave = threadIdx.x >> 6, lane = threadIdx.x & 63, r = (wave * kLoads + j) * 8 + (lane >> 3);
                 s.none[j] = k0 + 8 * ((lane & 7) ^ ((r >> 1) & 7)) < k ? 0u : kNowhere;
             }
         } else {
-            const uint32_t left = k0 < rows ? rows - k0 : 0, n = left ? (min(left, kTileK) - 1) * pitch + width : 0;
-            s.window = __builtin_amdgcn_make_buffer_rsrc((void *)(base + (uint64_t)k0 * pitch), 0, n, 0x00020000);
+            const uint32_t left = k0 < w.rows ? w.rows - k0 : 0, n = left ? (min(left, kTileK) - 1) * pitch + w.width : 0;
+            s.window = __builtin_amdgcn_make_buffer_rsrc((void *)uniform(w.base + (uint64_t)k0 * pitch), 0, uniform(n), 0x00020000);
         }
         return s;
     }
-    __device__ __forceinline__ void load(const Stage &s, char *to, uint32_t wave, uint32_t j) const
+    __device__ __forceinline__ void load(const Stage &s, char *to, uint32_t wave, uint32_t j, bool stream) const
     {
         const uint32_t at = kAlong ? off[j] | s.none[j & 1] : off[j];
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(s.window, (lds_void *)(to + place(wave * kLoads + j)), 16, at, 0, 0, 0);
+        lds_void *const there = (lds_void *)(to + place(wave * kLoads + j));
+        if (stream) __builtin_amdgcn_raw_ptr_buffer_load_lds(s.window, there, 16, at, 0, 0, 2);  // not to be kept in the caches
+        else __builtin_amdgcn_raw_ptr_buffer_load_lds(s.window, there, 16, at, 0, 0, 0);
     }
 
     // Sixteen rows from r0 on (a multiple of 16) and 32 values of k, half `sub` of the stage, in operand order.
@@ -135,11 +142,11 @@ struct Operand {
     }
 };
 
-// Blocks of a tile's kernel on a compute unit.
+// A compute unit's blocks of a kernel of tiles.
 constexpr int tile_blocks(int BM, int BN) { return BM + BN > 384 ? 1 : 2; }
 
-// A wave has every kWavesM-th 16 rows of Q and every kWavesN-th of P.
-template <int T, int BM, int BN, bool kQAlong, bool kPAlong, int kStages = 2>
+// A wave has every kWavesM-th 16 rows of Q and every kWavesN-th 32 rows of P.
+template <int T, int BM, int BN, bool kQAlong, bool kPAlong>
 struct Tile {
     static constexpr int kWavesM = BM == 64 ? 1 : 2, kWavesN = 4 / kWavesM;
     static constexpr int kWaves = 4;
@@ -151,6 +158,19 @@ struct Tile {
     Q q;
     P p;
     f32x4 acc[kN][kM];
+    struct Place {  // of a tile's operands, with k values of k
+        typename Q::Where q;
+        typename P::Where p;
+        uint32_t k;
+
+        __device__ __forceinline__ Place said_uniform() const { return {q.said_uniform(), p.said_uniform(), uniform(k)}; }
+    };
+
+    __device__ __forceinline__ Tile(uint64_t q_pitch, uint64_t p_pitch)
+    {
+        q.init(q_pitch);
+        p.init(p_pitch);
+    }
 
     // 256 accumulators of a lane are more than the compiler keeps in place by
     // itself: they are named as accumulation registers.
@@ -174,6 +194,12 @@ struct Tile {
         }
     }
 
+    // Tiles of 64 rows are bound by reading P, once and past the caches.  us of 61
+    // rows on a vocabulary of 128256 x 4096 and of 122 rows of 8 experts of 14336 x
+    // 4096: through the caches 208 and 167, past them 188 and 148, and with every
+    // two blocks beginning at another stage 161 and 149.
+    static constexpr bool kStreamP = BM == 64;
+
     // Branches of the whole wave around products of rows that do not exist.  Not
     // where the accumulators are named: around branches the compiler moves
     // them, without the waits that it does not know of.  Not for 64 rows, where
@@ -181,25 +207,40 @@ struct Tile {
     // against all of them: 207 us, 178 without).
     static constexpr bool kSkip = BM == 128;
 
+    // A result where it is used: until there it stays in its accumulation register.
+    __device__ __forceinline__ f32x4 result(int a, int b) const
+    {
+        f32x4 v = acc[a][b];
+        if constexpr (kNamed) asm volatile("" : "+a"(v));
+        return v;
+    }
+
+    // The first row within the tile of the wave's b-th sixteen of Q, and of its a-th of P.
+    __device__ __forceinline__ static constexpr uint32_t q_row(uint32_t wave, int b) { return 16 * (wave / kWavesN + kWavesM * b); }
+    __device__ __forceinline__ static constexpr uint32_t p_row(uint32_t wave, int a)
+    {
+        return 32 * (wave % kWavesN + kWavesN * (a / 2)) + 16 * (a % 2);
+    }
+
     struct Half {  // operands of 32 values of k
         X8 p[kN], q[kM];
     };
 
     __device__ __forceinline__ static void read(Half &h, const char *qs, const char *ps, uint32_t wave, uint32_t sub, int n)
     {
-        if (n < kN) h.p[n] = __builtin_bit_cast(X8, P::operand(ps, 16 * (wave % kWavesN) + 16 * kWavesN * n, sub));
-        else h.q[n - kN] = __builtin_bit_cast(X8, Q::operand(qs, 16 * (wave / kWavesN) + 16 * kWavesM * (n - kN), sub));
+        if (n < kN) h.p[n] = __builtin_bit_cast(X8, P::operand(ps, p_row(wave, n), sub));
+        else h.q[n - kN] = __builtin_bit_cast(X8, Q::operand(qs, q_row(wave, n - kN), sub));
     }
     static constexpr int kLoads = Q::kLoads + P::kLoads;
     struct Stage {
         typename Q::Stage q;
         typename P::Stage p;
     };
-    __device__ __forceinline__ Stage begin(uint32_t k0, uint32_t k) const { return {q.stage(k0, k), p.stage(k0, k)}; }
+    __device__ __forceinline__ Stage begin(const Place &w, uint32_t k0) const { return {q.stage(w.q, k0, w.k), p.stage(w.p, k0, w.k)}; }
     __device__ __forceinline__ void load(const Stage &s, char *qs, char *ps, uint32_t wave, int j) const
     {
-        if (j < (int)Q::kLoads) q.load(s.q, qs, wave, j);
-        else p.load(s.p, ps, wave, j - Q::kLoads);
+        if (j < (int)Q::kLoads) q.load(s.q, qs, wave, j, false);
+        else p.load(s.p, ps, wave, j - Q::kLoads, kStreamP);
     }
 
     // The products of h, with the reading of `into` spread among them, and
@@ -234,74 +275,139 @@ struct Tile {
 
     static constexpr int kEach = (kLoads + kM + kN - 1) / (kM + kN);
 
-    // The wait for reads of LDS, and for all loads but the last n.
-    template <int n>
-    __device__ __forceinline__ static void wait_all_but()
+    // Every wave's reads of LDS, and its loads, are done.
+    __device__ __forceinline__ static void all_done()
     {
-        __builtin_amdgcn_s_waitcnt((n & 15) | ((n >> 4) << 14) | 0x0070);
-    }
-
-    // One stage, whose first half is in h[0]; the next one has come at the end of
-    // the first half, and the one kStages after it comes into its place.
-    __device__ __forceinline__ void stage(Half *h, char *here, const char *next, uint32_t wave, int live, uint32_t k0, uint32_t k)
-    {
-        const Stage s = begin(k0 + kStages * kTileK, k);
-        multiply<0>(h[0], h[1], here, here + Q::kBytes, 1, s, nullptr, nullptr, wave, live);
-        wait_all_but<(kStages - 2) * kLoads>();
+        __builtin_amdgcn_s_waitcnt(0x0070);
         asm volatile("s_barrier" ::: "memory");
         __builtin_amdgcn_sched_barrier(0);
-        multiply<kEach>(h[1], h[0], next, next + Q::kBytes, 0, s, here, here + Q::kBytes, wave, live);
     }
 
     static constexpr uint32_t kBytes = Q::kBytes + P::kBytes;  // of a stage in LDS
-    static constexpr uint32_t kThird = kStages == 3 ? kBytes : 16;
 
-    // The product over k values of k, of `rows` of Q's rows.  s2: where kStages is 3.
-    __device__ __forceinline__ void product(char *s0, char *s1, char *s2, uint32_t k, uint32_t rows = BM)
+    // One stage, whose first half is in h[0]; the next one, in `next`, has come at
+    // the end of the first half, and stage `s`, the one after it, comes into this one's place.
+    __device__ __forceinline__ void stage(Half *h, char *here, const char *next, const Stage &s, uint32_t wave, int live)
     {
-        k = uniform(k);
-        const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-        // this wave's sixteens: wave / kWavesN, and every kWavesM-th after it
-        const int sixteens = (int)((uniform(rows) + 15) / 16) - (int)(wave / kWavesN);
-        const int live = sixteens <= 0 ? 0 : (sixteens + kWavesM - 1) / kWavesM;
+        multiply<0>(h[0], h[1], here, here + Q::kBytes, 1, s, nullptr, nullptr, wave, live);
+        all_done();
+        multiply<kEach>(h[1], h[0], next, next + Q::kBytes, 0, s, here, here + Q::kBytes, wave, live);
+    }
+
+    // The first two stages, of k0 and k1 on, on their way, and the first half read.
+    __device__ __forceinline__ void first(const Place &w, uint32_t k0, uint32_t k1, Half *h, char *s0, char *s1) const
+    {
+        const uint32_t wave = uniform(threadIdx.x >> 6);
+        Stage s = begin(w, k0);
+#pragma unroll
+        for (int j = 0; j < kLoads; j++) load(s, s0, s0 + Q::kBytes, wave, j);
+        s = begin(w, k1);
+#pragma unroll
+        for (int j = 0; j < kLoads; j++) load(s, s1, s1 + Q::kBytes, wave, j);
+        __builtin_amdgcn_s_waitcnt((kLoads & 15) | ((kLoads >> 4) << 14) | 0x0070);  // all but the second stage's
+        asm volatile("s_barrier" ::: "memory");
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int n = 0; n < kM + kN; n++) read(h[0], s0, s0 + Q::kBytes, wave, 0, n);
+    }
+    __device__ __forceinline__ void clear()
+    {
 #pragma unroll
         for (int a = 0; a < kN; a++)
 #pragma unroll
             for (int b = 0; b < kM; b++) acc[a][b] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int n = 0; n < kStages; n++) {
-            const Stage s = begin(n * kTileK, k);
-            char *to = n == 0 ? s0 : n == 1 ? s1 : s2;
-#pragma unroll
-            for (int j = 0; j < kLoads; j++) load(s, to, to + Q::kBytes, wave, j);
-        }
-        wait_all_but<(kStages - 1) * kLoads>();
-        asm volatile("s_barrier" ::: "memory");
-        __builtin_amdgcn_sched_barrier(0);
+        settle();
+    }
+
+    // The product of a tile of which `rows` of Q's rows exist.  Where P is streamed,
+    // blocks begin at different stages (pairs of an XCD's at the same one), so
+    // that not all of them ask for the same columns of all rows at the same time.
+    __device__ __forceinline__ void product(const Place &of, char *s0, char *s1, uint32_t rows)
+    {
+        const Place w = of.said_uniform();
+        const uint32_t wave = uniform(threadIdx.x >> 6);
+        // this wave's sixteens: wave / kWavesN, and every kWavesM-th after it
+        const int sixteens = (int)((uniform(rows) + 15) / 16) - (int)(wave / kWavesN);
+        const int live = sixteens <= 0 ? 0 : (sixteens + kWavesM - 1) / kWavesM;
+        const uint32_t k = w.k, stages = (k + kTileK - 1) / kTileK;
+        uint32_t next = kStreamP && stages ? kTileK * (blockIdx.x / 16 % stages) : 0;
+        uint32_t left = stages;  // whose loads have not been asked for
+        auto turn = [&]() {      // k0 of the next stage; past the last k when there is none
+            const uint32_t at = left ? next : k;
+            left -= left ? 1 : 0;
+            next = next + kTileK < k ? next + kTileK : 0;
+            return at;
+        };
         Half h[2];
-#pragma unroll
-        for (int n = 0; n < kM + kN; n++) read(h[0], s0, s0 + Q::kBytes, wave, 0, n);
-        uint32_t k0 = 0;
-        if constexpr (kStages == 2) {
-            for (; k0 + kTileK < k; k0 += 2 * kTileK) {
-                stage(h, s0, s1, wave, live, k0, k);
-                stage(h, s1, s0, wave, live, k0 + kTileK, k);
-            }
-            if (k0 < k) stage(h, s0, s1, wave, live, k0, k);
-        } else {
-            for (; k0 + 2 * kTileK < k; k0 += 3 * kTileK) {
-                stage(h, s0, s1, wave, live, k0, k);
-                stage(h, s1, s2, wave, live, k0 + kTileK, k);
-                stage(h, s2, s0, wave, live, k0 + 2 * kTileK, k);
-            }
-            if (k0 < k) stage(h, s0, s1, wave, live, k0, k);
-            if (k0 + kTileK < k) stage(h, s1, s2, wave, live, k0 + kTileK, k);
+        clear();
+        const uint32_t k0 = turn(), k1 = turn();
+        first(w, k0, k1, h, s0, s1);
+        uint32_t n = 0;
+        for (; n + 1 < stages; n += 2) {
+            stage(h, s0, s1, begin(w, turn()), wave, live);
+            stage(h, s1, s0, begin(w, turn()), wave, live);
+        }
+        if (n < stages) stage(h, s0, s1, begin(w, turn()), wave, live);
+        settle();
+    }
+
+    // The same within a row of tiles: the first half is in h[0] and the first two
+    // stages are in s0 and s1, or on their way, and so are those of `next` when
+    // this one is done.  Stages are taken by twos, at least two.
+    __device__ __forceinline__ void product(const Place &of, const Place &after, Half *h, char *s0, char *s1)
+    {
+        const Place w = of.said_uniform(), next = after.said_uniform();
+        const uint32_t wave = uniform(threadIdx.x >> 6), most = w.k > 2 * kTileK ? (w.k + 2 * kTileK - 1) / (2 * kTileK) : 1;
+        clear();
+        for (uint32_t n = 1; n <= most; n++) {
+            const bool last = n == most;
+            const Place to{last ? next.q : w.q, last ? next.p : w.p, last ? next.k : w.k};
+            const uint32_t k0 = last ? 0 : 2 * n * kTileK;
+            stage(h, s0, s1, begin(to, k0), wave, kM);
+            stage(h, s1, s0, begin(to, k0 + kTileK), wave, kM);
         }
         settle();
-        wait_all_but<0>();  // loads past the last k have not landed before
-        __syncthreads();
     }
 };
+
+// The tiles of a block: job(n, j) gives its n-th, or none, and done(t, j) has its
+// product.  Where a tile fills the compute unit (256 x 256) the block takes
+// one after the other, a grid of kCus blocks, with the next one's first stages on their
+// way before this one is stored; otherwise a block has one, and those beside it fill such gaps.
+template <class Tile, class Job, class Get, class Done>
+__device__ __forceinline__ void each_tile(Tile &t, char *s0, char *s1, Get get, Done done)
+{
+    Job j;
+    if (!get(0, j)) return;
+    if constexpr (Tile::kNamed) {
+        typename Tile::Half h[2];
+        t.first(j.place, 0, kTileK, h, s0, s1);
+        for (uint32_t n = 1;; n++) {
+            Job next;
+            const bool more = uniform((uint32_t)get(n, next)) != 0;
+            if (!more) next.place = {{j.place.q.base, 0, 0}, {j.place.p.base, 0, 0}, 0};
+            t.product(j.place, next.place, h, s0, s1);
+            done(t, j);
+            if (!more) break;
+            j = next;
+        }
+        __builtin_amdgcn_s_waitcnt(0x0070);
+    } else {
+        t.product(j.place, s0, s1, j.rows);
+        done(t, j);
+    }
+}
+
+// A barrier for what the waves have written to LDS, which does not wait for loads.
+__device__ __forceinline__ void lds_barrier()
+{
+    __builtin_amdgcn_s_waitcnt(0xC07F);
+    asm volatile("s_barrier" ::: "memory");
+}
+
+
+// The n-th piece of this block is that of block b of a grid of one piece a block.
+__device__ __forceinline__ uint32_t block_of(uint32_t n) { return blockIdx.x + n * gridDim.x; }
 
 // Block b of a grid of at least 8 ceil(n / 8) to one of n pieces of work, each
 // of the 8 XCDs (every eighth block) with a contiguous range of them; n or more: none.
@@ -320,27 +426,71 @@ __device__ __forceinline__ void tile_of(uint32_t t, uint32_t rows, uint32_t cols
     c = at / high;
 }
 
+// The lane's number, which the compiler does not know to be that of the last
+// tile: it would compute all places of all results before the first tile, and
+// have no registers for them.
+__device__ __forceinline__ uint32_t lane_here()
+{
+    uint32_t lane = threadIdx.x & 63;
+    asm volatile("" : "+v"(lane));
+    return lane;
+}
+
 // f(row of the tile, column, the four values of D from there on) for every four of this lane.
 template <class Tile, class F>
 __device__ __forceinline__ void each_four(const Tile &t, F f)
 {
-    const uint32_t wave = threadIdx.x >> 6, lane = threadIdx.x & 63, i = lane & 15, gr = lane >> 4;
+    const uint32_t wave = uniform(threadIdx.x >> 6), lane = lane_here(), i = lane & 15, gr = lane >> 4;
 #pragma unroll
-    for (int b = 0; b < Tile::kM; b++)
+    for (int b = 0; b < Tile::kM; b++) {
 #pragma unroll
-        for (int a = 0; a < Tile::kN; a++)
-            f(16 * (wave / Tile::kWavesN + Tile::kWavesM * b) + i,
-              16 * (wave % Tile::kWavesN + Tile::kWavesN * a) + 4 * gr, t.acc[a][b]);
+        for (int a = 0; a < Tile::kN; a++) f(Tile::q_row(wave, b) + i, Tile::p_row(wave, a) + 4 * gr, t.result(a, b));
+        __builtin_amdgcn_sched_barrier(0);  // or all accumulators are copied at once, for which there are no registers
+    }
 }
 
+// Four numbers as 16-bit ones.
+template <int T>
+__device__ __forceinline__ uint64_t pack_four(f32x4 v)
+{
+    const float f[8] = {v[0], v[1], v[2], v[3], 0.f, 0.f, 0.f, 0.f};
+    const u32x4 p = Type<T>::pack(f);
+    return (uint64_t)p[1] << 32 | p[0];
+}
 template <int T>
 __device__ __forceinline__ void store_four(uint16_t *to, f32x4 v)
 {
-    uint64_t q = 0;
-#pragma unroll
-    for (int e = 0; e < 4; e++) q |= (uint64_t)Type<T>::from_f32(v[e]) << (16 * e);
-    *reinterpret_cast<uint64_t *>(to) = q;
+    *reinterpret_cast<uint64_t *>(to) = pack_four<T>(v);
 }
+
+// f(row of the tile, column, eight 16-bit values of D from there on) for every eight of this lane, of
+// what g(row, column, four of D) makes of D.  Lanes of neighbouring groups trade their
+// halves of two sixteens, so that a lane stores 16 bytes and four of them
+// 64 bytes of a row: half as many stores, of twice the length, as fours would take (dW of
+// 100 rows on a vocabulary of 50257 x 768, 77 MB: 44 -> 38 us).
+template <int T, class Tile, class G, class F>
+__device__ __forceinline__ void each_eight(const Tile &t, G g, F f)
+{
+    const uint32_t wave = uniform(threadIdx.x >> 6), lane = lane_here(), i = lane & 15, gr = lane >> 4;
+#pragma unroll
+    for (int b = 0; b < Tile::kM; b++) {
+        const uint32_t row = Tile::q_row(wave, b) + i;
+#pragma unroll
+        for (int a = 0; a < Tile::kN; a += 2) {
+            const uint32_t col = Tile::p_row(wave, a);
+            const uint64_t one = pack_four<T>(g(row, col + 4 * gr, t.result(a, b)));
+            const uint64_t two = pack_four<T>(g(row, col + 16 + 4 * gr, t.result(a + 1, b)));
+            // odd groups' `one` against even groups' `two`
+            const auto lo = __builtin_amdgcn_permlane16_swap((uint32_t)one, (uint32_t)two, false, false);
+            const auto hi = __builtin_amdgcn_permlane16_swap((uint32_t)(one >> 32), (uint32_t)(two >> 32), false, false);
+            f(row, col + 16 * (gr & 1) + 8 * (gr >> 1), u32x4{lo[0], hi[0], lo[1], hi[1]});
+        }
+        __builtin_amdgcn_sched_barrier(0);
+    }
+}
+struct AsIs {
+    __device__ __forceinline__ f32x4 operator()(uint32_t, uint32_t, f32x4 v) const { return v; }
+};
 
 }  // namespace ops
 }  // namespace wc

@@ -32,19 +32,21 @@ struct TilePlan {
 };
 
 // The tile and the parts of k with the least time, of `tiles` (of 256, of 128)
-// with `stages` of k each: a compute unit takes 1.5 us for a stage of one large
-// tile, 1.1 us for one of two small ones and 0.75 of a single one, and the
-// parts' sums are written and read in fp32.
-TilePlan tile_plan(uint64_t large, uint64_t small, uint64_t stages, uint64_t results, bool joined)
+// with `stages` of k each.  What a compute unit takes for a stage, and for the
+// beginning and the end of a tile: one large tile 1.5 and 10 us, two small ones
+// 1.1 and 5, a single small one 0.75 and 3.5.  Parts are summed in fp32 by
+// another launch.
+TilePlan tile_plan(uint64_t large, uint64_t small, uint64_t stages, uint64_t results, bool joined, uint32_t most = 64)
 {
     TilePlan best{kSmall, 1};
     double least = 1e30;
     for (int size = 0; size < 2; size++) {
-        for (uint32_t s = 1; s <= 16 && (s == 1 || stages >= 4 * s); s *= 2) {
-            const double tiles = (double)(size ? large : small) * s, each = (double)ceil_div(stages, s) + 3;
-            const double rounds = size ? ceil(tiles / kCus) : tiles <= kCus ? 1.0 : ceil(tiles / (2 * kCus));
-            double t = rounds * each * (size ? 1.5 : tiles <= kCus ? 0.75 : 1.1);
-            if (s > 1) t += (joined ? 0.0 : 4.0) + (double)results * s * 8 / 4e6;
+        for (uint32_t s = 1; s <= most && (s == 1 || stages >= 4 * s); s *= 2) {
+            const double tiles = (double)(size ? large : small) * s, each = (double)ceil_div(stages, s);
+            const bool single = !size && tiles <= kCus;
+            const double rounds = size ? ceil(tiles / kCus) : single ? 1.0 : ceil(tiles / (2 * kCus));
+            double t = rounds * (size ? 1.5 * each + 10 : single ? 0.75 * each + 3.5 : 1.1 * each + 5);
+            if (s > 1) t += (joined ? 0.0 : 5.0) + (double)results * s * 8 / 4e6;
             if (t < least) {
                 least = t;
                 best = {size ? kLarge : kSmall, s};
@@ -71,12 +73,16 @@ TileSize grouped_size(uint64_t m, uint32_t experts, uint32_t n, uint32_t k)
 {
     if (m <= 64ull * (m < experts ? m : experts)) return kFlat;
     return FORCE((tile_plan(tiles_expected(m, experts, 256) * ceil_div(n, 256), tiles_expected(m, experts, 128) * ceil_div(n, 128),
-                     ceil_div(k, kTileK), m * n, false).size));
+                     ceil_div(k, kTileK), m * n, true, 1).size));
 }
-// Room for the tiles in parts: one of every slot.
-uint64_t grouped_part(TileSize size)
+// Room for the tiles of the last round in parts, one for every slot, where that
+// round is more than a sixth of the time.
+uint64_t grouped_part(TileSize size, uint64_t m, uint32_t experts, uint32_t n, uint32_t k, uint32_t flat_n)
 {
-    return size == kLarge ? 4ull * 256 * 256 * kCus : size == kSmall ? 4ull * 128 * 128 * 2 * kCus : 0;
+    const uint64_t bm = size == kLarge ? 256 : size == kSmall ? 128 : 64, bn = size == kFlat ? flat_n : bm;
+    const uint64_t slots = kCus * (size == kLarge ? 1 : 2);
+    const bool few = tiles_expected(m, experts, bm) * ceil_div(n, bn) < 6 * slots;
+    return few && k >= 16 * kTileK ? 4 * bm * bn * slots : 0;
 }
 
 // few rows of each expert: no tile would be full
@@ -109,6 +115,10 @@ void launch_join(int type, const JoinArgs &g, hipStream_t stream)
 }
 
 uint32_t xcd_grid(uint64_t pieces) { return (uint32_t)(8 * ceil_div(pieces, 8)); }
+// Blocks of a kernel that takes one large tile after the other.
+uint32_t large_grid(uint64_t pieces) { return xcd_grid(pieces < kCus ? pieces : kCus); }
+
+constexpr int kFlatAlong = 256, kFlatAcross = 128;  // columns of the flat tiles
 
 // y, or dx (kPAlong false), by tiles of BM x BN
 template <int T, int BM, int BN, bool kPAlong>
@@ -118,7 +128,8 @@ void launch_tiles(const GroupedArgs &g, hipStream_t stream)
     // rows behind the last expert's fill a tile more, and may take one that the experts' would have
     const uint64_t tiles = (tiles_of(g.m, g.experts, BM) + 1) * ceil_div(g.n, BN);
     // a last round in parts has no more blocks than slots; the XCDs' ranges of parts and zeros are rounded up
-    const uint32_t blocks = xcd_grid(tiles + (g.part ? slots : 0) + 16);
+    const uint64_t pieces = tiles + (g.part ? slots : 0) + 16;
+    const uint32_t blocks = BM == 256 ? large_grid(pieces) : xcd_grid(pieces);
     hipLaunchKernelGGL((k_grouped<T, BM, BN, kPAlong>), dim3(blocks), dim3(256), 0, stream, g);
     if (g.part) hipLaunchKernelGGL((k_grouped_join<T, BM, BN>), dim3(slots / 2 * 8), dim3(256), 0, stream, g);
 }
@@ -127,10 +138,7 @@ void launch_grouped(GroupedArgs g, TileSize size, hipStream_t stream)
 {
     if (size == kLarge) launch_tiles<T, 256, 256, kPAlong>(g, stream);
     else if (size == kSmall) launch_tiles<T, 128, 128, kPAlong>(g, stream);
-    else {
-        g.part = nullptr;
-        launch_tiles<T, 64, kPAlong ? 256 : 128, kPAlong>(g, stream);
-    }
+    else launch_tiles<T, 64, kPAlong ? kFlatAlong : kFlatAcross, kPAlong>(g, stream);
 }
 
 template <int T>
@@ -153,7 +161,8 @@ void launch_grouped_dw(GroupedDwArgs g, const TilePlan &p, hipStream_t stream)
 {
     g.splits = p.splits;
     const uint64_t tile = p.size == kLarge ? 256 : 128;
-    const dim3 grid(g.experts * xcd_grid(ceil_div(g.n, tile) * ceil_div(g.k, tile) * g.splits)), block(256);
+    const uint64_t pieces = g.experts * xcd_grid(ceil_div(g.n, tile) * ceil_div(g.k, tile) * g.splits);
+    const dim3 grid(p.size == kLarge ? large_grid(pieces) : (uint32_t)pieces), block(256);
     if (p.size == kLarge) hipLaunchKernelGGL((k_grouped_dw<T, 256, 256>), grid, block, 0, stream, g);
     else hipLaunchKernelGGL((k_grouped_dw<T, 128, 128>), grid, block, 0, stream, g);
     if (g.splits > 1)
@@ -176,7 +185,7 @@ bool loss_few(uint64_t m) { return m <= 16; }
 TileSize loss_tile(uint64_t m, uint32_t vocab, uint32_t k)
 {
     if (m <= 64) return kFlat;
-    return tile_plan(ceil_div(m, 256) * ceil_div(vocab, 256), ceil_div(m, 128) * ceil_div(vocab, 128), ceil_div(k, kTileK), 0, true).size;
+    return tile_plan(ceil_div(m, 256) * ceil_div(vocab, 256), ceil_div(m, 128) * ceil_div(vocab, 128), ceil_div(k, kTileK), 0, true, 1).size;
 }
 uint32_t loss_parts(uint64_t m, uint32_t vocab, uint32_t k)
 {
@@ -194,7 +203,8 @@ void launch_loss(const LossArgs &g, hipStream_t stream)
         else hipLaunchKernelGGL((k_loss_few<T, false>), grid, dim3(256), 0, stream, g);
     } else {
         const TileSize size = loss_tile(g.m, g.vocab, g.k);
-        const dim3 grid(xcd_grid(ceil_div(g.m, size == kLarge ? 256 : size == kSmall ? 128 : 64) * g.parts)), block(256);
+        const uint64_t tiles = ceil_div(g.m, size == kLarge ? 256 : size == kSmall ? 128 : 64) * g.parts;
+        const dim3 grid(size == kLarge ? large_grid(tiles) : xcd_grid(tiles)), block(256);
         if (size == kLarge) hipLaunchKernelGGL((k_loss<T, 256, 256>), grid, block, 0, stream, g);
         else if (size == kSmall) hipLaunchKernelGGL((k_loss<T, 128, 128>), grid, block, 0, stream, g);
         else hipLaunchKernelGGL((k_loss<T, 64, 256>), grid, block, 0, stream, g);
@@ -241,7 +251,7 @@ template <int T, bool kQAlong>
 void launch_product(const ProductArgs &g, bool large, hipStream_t stream)
 {
     const uint64_t tile = large ? 256 : 128, tiles = ceil_div(g.m, tile) * ceil_div(g.n, tile) * g.splits;
-    if (large) hipLaunchKernelGGL((k_product<T, 256, 256, kQAlong>), dim3(xcd_grid(tiles)), dim3(256), 0, stream, g);
+    if (large) hipLaunchKernelGGL((k_product<T, 256, 256, kQAlong>), dim3(large_grid(tiles)), dim3(256), 0, stream, g);
     else hipLaunchKernelGGL((k_product<T, 128, 128, kQAlong>), dim3(xcd_grid(tiles)), dim3(256), 0, stream, g);
 }
 
@@ -262,7 +272,8 @@ void launch_loss_grad(const wc_linear_loss_grad &a, LossGradArgs g, const LossGr
         } else {
             const TileSize size = loss_tile(g.m, p.piece, g.k);
             const uint32_t bm = size == kLarge ? 256 : size == kSmall ? 128 : 64, bn = size == kSmall ? 128 : 256;
-            const dim3 grid(xcd_grid(ceil_div(g.m, bm) * ceil_div(g.width, bn))), block(256);
+            const uint64_t tiles = ceil_div(g.m, bm) * ceil_div(g.width, bn);
+            const dim3 grid(size == kLarge ? large_grid(tiles) : xcd_grid(tiles)), block(256);
             if (size == kLarge) hipLaunchKernelGGL((k_loss_grad<T, 256, 256>), grid, block, 0, stream, g);
             else if (size == kSmall) hipLaunchKernelGGL((k_loss_grad<T, 128, 128>), grid, block, 0, stream, g);
             else hipLaunchKernelGGL((k_loss_grad<T, 64, 256>), grid, block, 0, stream, g);
@@ -296,7 +307,7 @@ extern "C" {
 uint64_t wc_grouped_linear_scratch(uint64_t m, uint32_t experts, uint32_t rows, uint32_t cols)
 {
     if (m == 0 || !valid_grouped(m, experts, rows, cols) || grouped_few(m, experts)) return 0;
-    return grouped_part(grouped_size(m, experts, rows, cols));
+    return grouped_part(grouped_size(m, experts, rows, cols), m, experts, rows, cols, kFlatAlong);
 }
 
 wc_status wc_grouped_linear(const wc_grouped *a, void *d_scratch, uint64_t scratch_bytes, uint32_t *d_err, hipStream_t stream)
@@ -326,7 +337,7 @@ wc_status wc_grouped_linear(const wc_grouped *a, void *d_scratch, uint64_t scrat
     g.n = a->rows;
     g.k = a->cols;
     g.zero_rest = a->zero_rest;
-    g.part = static_cast<float *>(d_scratch);
+    g.part = need ? static_cast<float *>(d_scratch) : nullptr;
     g.err = d_err;
     return a->type == WC_T_BF16 ? launch_grouped_linear<WC_T_BF16>(g, stream) : launch_grouped_linear<WC_T_FP16>(g, stream);
 }
@@ -335,7 +346,7 @@ uint64_t wc_grouped_linear_backward_scratch(uint64_t m, uint32_t experts, uint32
 {
     if (m == 0 || !valid_grouped(m, experts, rows, cols)) return 0;
     // one after the other
-    const uint64_t dx = grouped_part(grouped_size(m, experts, cols, rows));
+    const uint64_t dx = grouped_part(grouped_size(m, experts, cols, rows), m, experts, cols, rows, kFlatAcross);
     const uint64_t dw = part_bytes((uint64_t)experts * rows * cols, grouped_dw_plan(m, experts, rows, cols).splits);
     return dx > dw ? dx : dw;
 }
@@ -370,9 +381,9 @@ wc_status wc_grouped_linear_backward(const wc_grouped_grad *a, void *d_scratch, 
         g.n = a->cols;
         g.k = a->rows;
         g.zero_rest = a->zero_rest;
-        g.part = static_cast<float *>(d_scratch);
         g.err = d_err;
         const TileSize p = grouped_size(a->m, a->experts, a->cols, a->rows);
+        if (grouped_part(p, a->m, a->experts, a->cols, a->rows, kFlatAcross)) g.part = static_cast<float *>(d_scratch);
         if (a->type == WC_T_BF16) launch_grouped<WC_T_BF16, false>(g, p, stream);
         else launch_grouped<WC_T_FP16, false>(g, p, stream);
     }

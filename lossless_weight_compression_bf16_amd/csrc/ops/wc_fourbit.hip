@@ -19,21 +19,30 @@ bool valid_fourbit(uint64_t rows, uint32_t cols, uint32_t group)
            cols <= (1u << 20);
 }
 
-template <int T, int GROUP>
+template <int T, int GROUP, int NT, int SLICE, int WAVES>
 void launch_linear4(Linear4Args g, hipStream_t stream)
 {
-    // enough sixteens of rows for a block that all have a compute unit
-    const uint64_t tiles = ceil_div(g.rows, 16);
-    g.row_tiles = (uint32_t)ceil_div(tiles, kCus);
+    const uint64_t tiles = ceil_div(g.rows, 16), turns = ceil_div(g.m, 16 * NT), slices = ceil_div(g.cols, SLICE);
+    const uint32_t waves = (uint32_t)(slices < WAVES ? slices : WAVES);
+    // a block for each compute unit: its LDS has room for one
+    const uint64_t blocks = turns < kCus ? kCus / turns : 1;
+    g.row_tiles = (uint32_t)ceil_div(tiles, blocks);
     if (g.row_tiles > kRowTiles4) g.row_tiles = kRowTiles4;
     g.row_blocks = (uint32_t)ceil_div(tiles, g.row_tiles);
-    const uint32_t slices = (uint32_t)ceil_div(g.cols, kSlice4);
-    const bool one = g.m <= 16;
-    constexpr int kOne = GROUP == 32 ? 8 : 16;  // waves: groups of 32 take registers for their scales
-    const uint32_t most = one ? kOne : 8, waves = slices < most ? slices : most;
-    const dim3 grid((uint32_t)(8 * ceil_div(g.row_blocks, 8) * ceil_div(g.m, one ? 16 : 32))), block(64 * waves);
-    if (one) hipLaunchKernelGGL((k_linear4<T, GROUP, 1, kOne>), grid, block, 0, stream, g);
-    else hipLaunchKernelGGL((k_linear4<T, GROUP, 2, 8>), grid, block, 0, stream, g);
+    const dim3 grid((uint32_t)(8 * ceil_div(g.row_blocks, 8) * turns)), block(64 * waves);
+    if (g.zeros) hipLaunchKernelGGL((k_linear4<T, GROUP, NT, SLICE, WAVES, true>), grid, block, 0, stream, g);
+    else hipLaunchKernelGGL((k_linear4<T, GROUP, NT, SLICE, WAVES, false>), grid, block, 0, stream, g);
+}
+
+template <int T, int GROUP>
+void launch_linear4(const Linear4Args &g, hipStream_t stream)
+{
+    // A wave takes 256 columns, or as many as a group has where there are not so many.  Rows of x: 16 by 16 waves, whose registers
+    // hold no more, and from 17 on 32 by 8 (4096 x 4096, groups of 64: 17 rows 10.2 us against 17.7 as two times
+    // 16, 64 rows 12.8 against 32; with 64 rows at once a wave has room for 128 columns only: 17.4).
+    if (g.cols < 256) launch_linear4<T, GROUP, 1, GROUP, 8>(g, stream);
+    else if (g.m <= 16) launch_linear4<T, GROUP, 1, 256, 16>(g, stream);
+    else launch_linear4<T, GROUP, 2, 256, 8>(g, stream);
 }
 
 template <int T>

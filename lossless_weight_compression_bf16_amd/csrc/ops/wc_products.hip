@@ -21,9 +21,6 @@ namespace {
 constexpr uint64_t kMaxPitch = (1ull << 22) - 8;
 constexpr uint32_t kMaxCols = 1u << 20;
 
-#ifndef FORCE
-#define FORCE(x) x
-#endif
 // Tiles of a product, and the parts of k that it is split into.
 enum TileSize { kFlat, kSmall, kLarge };  // 64 rows (by 256 columns, or 128 with P across), 128 x 128, 256 x 256
 struct TilePlan {
@@ -72,8 +69,9 @@ uint64_t tiles_expected(uint64_t m, uint32_t experts, uint64_t tile)  // with th
 TileSize grouped_size(uint64_t m, uint32_t experts, uint32_t n, uint32_t k)
 {
     if (m <= 64ull * (m < experts ? m : experts)) return kFlat;
-    return FORCE((tile_plan(tiles_expected(m, experts, 256) * ceil_div(n, 256), tiles_expected(m, experts, 128) * ceil_div(n, 128),
-                     ceil_div(k, kTileK), m * n, true, 1).size));
+    return tile_plan(tiles_expected(m, experts, 256) * ceil_div(n, 256), tiles_expected(m, experts, 128) * ceil_div(n, 128),
+                     ceil_div(k, kTileK), m * n, true, 1)
+        .size;
 }
 // Room for the tiles of the last round in parts, one for every slot, where that
 // round is more than a sixth of the time.
@@ -366,6 +364,7 @@ wc_status wc_grouped_linear_backward(const wc_grouped_grad *a, void *d_scratch, 
     const uint64_t need = wc_grouped_linear_backward_scratch(a->m, a->experts, a->rows, a->cols);
     if (scratch_bytes < need) return WC_ERR_CAPACITY;
     if (need && (!d_scratch || !aligned(d_scratch, 16))) return WC_ERR_ARG;
+    if (!(a->grad_x && a->m) && !a->grad_w) return WC_OK;
     if (a->grad_x && a->m) {
         GroupedArgs g{};
         g.x = static_cast<const uint16_t *>(a->grad);
@@ -476,6 +475,7 @@ wc_status wc_linear_cross_entropy_backward(const wc_linear_loss_grad *a, void *d
     const LossGradPlan p = loss_grad_plan(a->m, a->vocab, a->cols);
     if (scratch_bytes < p.bytes) return WC_ERR_CAPACITY;
     if (!d_scratch || !aligned(d_scratch, 256)) return WC_ERR_ARG;
+    if (!a->grad_hidden && !a->grad_weight) return WC_OK;
     char *s = static_cast<char *>(d_scratch);
     LossGradArgs g{};
     g.h = static_cast<const uint16_t *>(a->hidden);

@@ -10,7 +10,7 @@ from __future__ import annotations
 
 import torch
 from torch.autograd import forward_ad
-from torch.autograd.graph import increment_version
+from torch.autograd.graph import get_gradient_edge, increment_version
 
 from . import _binding as B
 
@@ -135,3 +135,32 @@ def once(what: str, grads, *inputs):
     if not torch.is_grad_enabled():
         return grads
     return tuple(None if g is None else _Once.apply(what, g, *inputs) for g in grads)
+
+
+def fresh_under_capture(what: str, *tensors):
+    """Raises where the call is captured into a graph and a leaf that requires a gradient belongs to a graph of
+    autograd's from before: the leaf's gradient would be accumulated on that one's stream, and where that is the
+    default stream, which a capture cannot wait for, autograd ends the process.
+
+    A leaf's accumulation is one node for as long as a graph holds it, so what is noted on it is there again only
+    if it lives; one that a captured call of these has made is known by its stream."""
+    if not torch.cuda.is_current_stream_capturing():
+        return
+    stream = torch.cuda.current_stream().cuda_stream
+    for t in tensors:
+        if not t.is_leaf or not t.requires_grad:
+            continue
+        get_gradient_edge(t).node.metadata.setdefault("wc_seen", True)
+        node = get_gradient_edge(t).node.metadata
+        if "wc_seen" in node and node.get("wc_captured") != stream:
+            raise RuntimeError(f"{what} is captured, and autograd still holds another graph of one of its leaves: delete that "
+                               "graph's outputs first, or capture the gradient's own call")
+
+
+def note_captured(*tensors):
+    """After a captured call with gradients: its leaves' accumulations are this capture's."""
+    if torch.cuda.is_current_stream_capturing():
+        stream = torch.cuda.current_stream().cuda_stream
+        for t in tensors:
+            if t.is_leaf and t.requires_grad:
+                get_gradient_edge(t).node.metadata["wc_captured"] = stream

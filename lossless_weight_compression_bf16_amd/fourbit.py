@@ -53,6 +53,8 @@ def _check(x, w, out):
         if out.dtype != x.dtype or out.shape != (x.shape[0], rows) or not _ops.rows_apart(out):
             raise ValueError(f"out must be {x.shape[0]} x {rows} in the type of x, with unit column stride and rows that do "
                              "not overlap")
+        if any(t is not None and _ops.may_overlap(out, t) for t in (w.q, w.scales, w.zeros)):
+            raise ValueError("out and the weights have memory in common")
 
 
 def _good(x, w) -> bool:

@@ -106,7 +106,7 @@ def grouped_linear(x: torch.Tensor, w: torch.Tensor, ends: torch.Tensor, out: to
     device, which never have to come to the host.  rows and cols are
     multiples of 8.  Rows behind the last expert's are not read: their y is
     zero, or in a given `out` what it was.  x and w can be differentiated,
-    once.  With check (which waits for the GPU) ends that go back, or past
+    once; captured into a graph only while autograd holds no other graph of them.  With check (which waits for the GPU) ends that go back, or past
     the rows, raise; without, y is undefined."""
     if out is not None or not _good(x, w, ends):
         _check(x, w, ends, out)
@@ -116,9 +116,12 @@ def grouped_linear(x: torch.Tensor, w: torch.Tensor, ends: torch.Tensor, out: to
         if out is not None or stream is not None:
             raise ValueError("with gradients the call runs on the current stream and makes its own result: use "
                              "torch.cuda.stream, and no out")
-        return _GroupedLinear.apply(x, w, ends, check)
-    if out is not None and _ops.may_overlap(out, w):
-        raise ValueError("out and w have memory in common")
+        _ops.fresh_under_capture("grouped_linear", x, w)
+        y = _GroupedLinear.apply(x, w, ends, check)
+        _ops.note_captured(x, w)
+        return y
+    if out is not None and (_ops.may_overlap(out, w) or _ops.may_overlap(out, ends)):
+        raise ValueError("out and w or ends have memory in common")
     return _forward(x, w, ends, out, check, stream)
 
 

@@ -82,7 +82,8 @@ def linear_cross_entropy(hidden: torch.Tensor, weight: torch.Tensor, tokens: tor
     multiple of 8; the logits are sums in fp32 and are not rounded.  Token -1
     stands for no token (loss 0, whatever the row holds).  hidden and weight
     can be differentiated, once, through loss and lse (a penalty on the
-    size of the logits is a function of lse).  With check (which waits for
+    size of the logits is a function of lse); captured into a graph only
+    while autograd holds no other graph of them.  With check (which waits for
     the GPU) a token out of range raises; without, its loss is NaN."""
     if not _good(hidden, weight, tokens):
         _check(hidden, weight, tokens)
@@ -91,7 +92,10 @@ def linear_cross_entropy(hidden: torch.Tensor, weight: torch.Tensor, tokens: tor
     if torch.is_grad_enabled() and (hidden.requires_grad or weight.requires_grad):
         if stream is not None:
             raise ValueError("with gradients the call runs on the current stream: use torch.cuda.stream")
-        return LinearCrossEntropy(*_LinearCrossEntropy.apply(hidden, weight, tokens, check))
+        _ops.fresh_under_capture("linear_cross_entropy", hidden, weight)
+        r = LinearCrossEntropy(*_LinearCrossEntropy.apply(hidden, weight, tokens, check))
+        _ops.note_captured(hidden, weight)
+        return r
     return _forward(hidden, weight, tokens, check, stream)
 
 

@@ -289,8 +289,8 @@ __global__ __launch_bounds__(256, tile_blocks(BM, BN)) void k_loss_grad(LossGrad
     __shared__ __attribute__((aligned(1024))) char b0[Ti::kBytes];
     __shared__ __attribute__((aligned(1024))) char b1[Ti::kBytes];
     const uint32_t down = (g.m + BM - 1) / BM, across = (g.width + BN - 1) / BN, wave = threadIdx.x >> 6;
-    float unscale;
-    const float scale = loss_scale<T>(g.most, unscale);
+    float unscale, early = 1.f;  // as in k_product
+    if constexpr (Ti::kNamed) early = loss_scale<T>(g.most, unscale);
     Ti ti(g.h_stride, g.w_row);
     each_tile<Ti, Job>(
         ti, b0, b1,
@@ -303,6 +303,8 @@ __global__ __launch_bounds__(256, tile_blocks(BM, BN)) void k_loss_grad(LossGrad
             return true;
         },
         [&](const Ti &ti, const Job &j) {
+            float scale = early;
+            if constexpr (!Ti::kNamed) scale = loss_scale<T>(g.most, unscale);
             f32x4 info[Ti::kM];
 #pragma unroll
             for (int b = 0; b < Ti::kM; b++) info[b] = g.rows[j.m0 + min(Ti::q_row(wave, b) + (threadIdx.x & 15), j.rows - 1)];
@@ -378,8 +380,9 @@ __global__ __launch_bounds__(256, tile_blocks(BM, BN)) void k_product(ProductArg
     __shared__ __attribute__((aligned(1024))) char b1[Ti::kBytes];
     const uint32_t down = (g.m + BM - 1) / BM, across = (g.n + BN - 1) / BN, each = down * across;
     const uint32_t stages = (g.k + kTileK - 1) / kTileK;
-    float unscale;
-    loss_scale<T>(g.most, unscale);
+    // asked for at the end where a block has one tile, and its loads would wait for this one
+    float early = 1.f;
+    if constexpr (Ti::kNamed) loss_scale<T>(g.most, early);
     Ti ti(g.q_stride, g.p_stride);
     each_tile<Ti, Job>(
         ti, b0, b1,
@@ -411,6 +414,8 @@ __global__ __launch_bounds__(256, tile_blocks(BM, BN)) void k_product(ProductArg
                 });
             } else {
                 uint16_t *out = g.out + j.m0 * g.out_stride + j.n0;
+                float unscale = early;
+                if constexpr (!Ti::kNamed) loss_scale<T>(g.most, unscale);
                 each_eight<T>(ti, [&](uint32_t, uint32_t, f32x4 v) { return v * unscale; },
                               [&](uint32_t row, uint32_t col, u32x4 v) {
                                   if (row < j.rows && j.n0 + col < g.n)

@@ -628,7 +628,7 @@ typedef struct {
     void *y;                /* m x rows, rows y_stride elements apart, any alignment; no memory in common with x */
     uint64_t y_stride;
     uint64_t m;             /* below 2^31 */
-    uint32_t rows;          /* 1 .. 2^24; rows / 16 times m / 16 below 2^22 */
+    uint32_t rows;          /* 1 .. 2^24; (rows / 512 + 16) times m / 16 below 2^22 - 256 */
     uint32_t cols;          /* a multiple of group, at most 2^20 */
     uint32_t group;         /* 32, 64 or 128 */
     uint32_t type;          /* WC_T_BF16 or WC_T_FP16: of x, scales, zeros and y */

@@ -75,7 +75,8 @@ wc_status wc_linear4(const wc_fourbit *a, hipStream_t stream)
     if (!a->q || !aligned(a->q, 16) || !a->scales || !aligned(a->scales, 2) || !aligned(a->zeros, 2)) return WC_ERR_ARG;
     if (!a->y || !aligned(a->y, 2) || (a->m > 1 && a->y_stride < a->rows)) return WC_ERR_ARG;
     if (!rows_apart(a->x, 2 * a->x_stride, 2ull * a->cols, a->y, 2 * a->y_stride, 2ull * a->rows, a->m)) return WC_ERR_ARG;
-    if (8 * ceil_div(ceil_div(a->rows, 16), 8) * ceil_div(a->m, 16) > max_blocks(1024)) return WC_ERR_ARG;
+    // blocks of 32 sixteens of rows, or fewer where that makes no more blocks than compute units; every XCD the same number
+    if ((ceil_div(a->rows, 16 * kRowTiles4) + 16) * ceil_div(a->m, 16) + kCus > max_blocks(1024)) return WC_ERR_ARG;
     Linear4Args g{};
     g.x = static_cast<const uint16_t *>(a->x);
     g.q = static_cast<const uint8_t *>(a->q);

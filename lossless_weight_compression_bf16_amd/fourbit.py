@@ -100,6 +100,8 @@ def linear4(x: torch.Tensor, w: Weights4, out: torch.Tensor | None = None, strea
             z = z.clone(memory_format=torch.contiguous_format)
             a.x, a.x_stride = z.data_ptr(), cols
             rc = B.lib().wc_linear4(a, raw)
+        if rc == B.WC_ERR_ARG:
+            raise ValueError(f"{m} rows of x and {rows} of weights are more than one launch takes")
         _ops.done(rc, None, "linear4")
         return y
 

@@ -178,7 +178,8 @@ def test_fourbit_refusals(L):
                {"group": 0}, {"group": 16}, {"group": 48}, {"group": 256}, {"x": 0}, {"x": 0x100008}, {"x_stride": 248},
                {"x_stride": 260}, {"q": 0}, {"q": 0x200008}, {"scales": 0}, {"scales": 0x300001}, {"zeros": 0x400001}, {"y": 0},
                {"y": 0x500001}, {"y_stride": 99}, {"m": 1 << 31}, {"y": 0x100000}, {"y": 0x100000 + 2 * 256 * 6},
-               {"m": (1 << 31) - 1, "rows": 1 << 24, "y_stride": 1 << 24, "y": 1 << 50}):
+               {"m": (1 << 31) - 1, "rows": 1 << 24, "y_stride": 1 << 24, "y": 1 << 50},
+               {"m": 2100, "rows": 1 << 24, "y_stride": 1 << 24, "y": 1 << 50}):
         assert call(_with(FOURBIT, **kw)) == B.WC_ERR_ARG, kw
     assert call(_with(FOURBIT, m=0)) == B.WC_OK  # nothing to do
 

@@ -8,6 +8,11 @@
 //   k_grouped_join, k_join  sums of products that were split along k
 // The ends stay on the device: a block finds its expert and rows from them by
 // itself (every wave adds up the experts' tiles by lane moves).
+//
+// What bounds them, and what they take: few rows, reading the weights once (122 rows of 8 experts of 14336 x 4096, by
+// tiles of 64: 147 us, 6.4 TB/s; one row of each of 8 of 1024 x 2048, by k_grouped_few: 11 us, one way through
+// memory); many, the matrix cores at the clock that their power leaves (16384 rows of 8 of 14336 x 4096: dx 1520 us, dW
+// 1550 us, 1.25 PFLOP/s); in between, tiles that are not full (32768 rows of 256 of 2048 x 7168: 1870 us, 4.3 TB/s).
 #pragma once
 
 #include "ops_common.hpp"

@@ -9,6 +9,12 @@
 //   k_loss_rows               what the gradient needs of a row, and H without the rows that have no part in it
 //   k_loss_grad_few, k_loss_grad  G of a piece of the vocabulary: z again, then the formula
 //   k_product                 dH += G W and dW = G^T H of that piece
+//
+// What bounds them, and what they take: up to 64 rows, reading W (61 rows, 128256 x 4096: 157 us, 6.7 TB/s); many rows, the
+// matrix cores at the clock that their power leaves (4096 rows: 3230 us, 1.33 PFLOP/s; the gradients, in four pieces of
+// 880, 760 and 755 us, 1.34); in between, stages of 0.9 us in which one wave on a SIMD reads, waits and multiplies in turn (100
+// rows, 50257 x 768: 31, 24 and 31 us).  G goes through memory once for each product: in the tile that made it, only one of the
+// two could use it, and the other would make it again, a third product for each.
 #pragma once
 
 #include "ops_common.hpp"

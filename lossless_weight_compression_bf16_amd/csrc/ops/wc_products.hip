@@ -67,10 +67,18 @@ uint64_t tiles_expected(uint64_t m, uint32_t experts, uint64_t tile)  // with th
     return hit * ceil_div(ceil_div(m, hit), tile);
 }
 
+// Tiles of 64 rows read the weights as fast as memory gives them, where k is long
+// enough.  us of 9 to 64 rows of each of 8 experts of 14336 x 4096 by tiles of 64 and of 128, 145 to 157 and 165 to
+// 180, of 64 of 1024 x 2048, 51 to 63 and 69 to 74, of 64 of 768 x 768, 19 to 21 and 16 to 18; of 65 to 128 rows of
+// 14336 x 4096 340 to 250 and 180 to 203.  The loss of 17 to 64 rows, a vocabulary of 128256 x 4096, 160 and 180, of
+// 50257 x 768, 25 and 22.
+constexpr uint32_t kFlatK = 1024;
+bool flat(uint64_t rows, uint32_t k) { return rows <= 64 && k > kFlatK; }
+
 // The tiles of y or dx of m rows with n columns each, from k
 TileSize grouped_size(uint64_t m, uint32_t experts, uint32_t n, uint32_t k)
 {
-    if (m <= 64ull * (m < experts ? m : experts)) return kFlat;
+    if (flat(ceil_div(m, m < experts ? m : experts), k)) return kFlat;
     return tile_plan(tiles_expected(m, experts, 256) * ceil_div(n, 256), tiles_expected(m, experts, 128) * ceil_div(n, 128),
                      ceil_div(k, kTileK), m * n, true, 1)
         .size;
@@ -85,8 +93,15 @@ uint64_t grouped_part(TileSize size, uint64_t m, uint32_t experts, uint32_t n, u
     return few && k >= 16 * kTileK ? 4 * bm * bn * slots : 0;
 }
 
-// few rows of each expert: no tile would be full
-bool grouped_few(uint64_t m, uint32_t experts) { return m <= 8ull * (m < experts ? m : experts); }
+// Few rows of each expert, whose weights are few or short: no tile, but more and smaller blocks.  us by
+// k_grouped_few and by tiles of 64: one row of 1024 x 2048 11 and 15, of each of 8 and 16 such experts 11.8 and 15.7, 23 and 17.6;
+// one row of 14336 x 4096 41 and 25, of each of 2 and 8 of 2048 x 7168 18 and 20.5, 55 and 45; of 64 of 768 x 768 16 and 20,
+// 8 rows of each 17 and 19.
+bool grouped_few(uint64_t m, uint32_t experts, uint32_t n, uint32_t k)
+{
+    const uint64_t hit = m < experts ? m : experts;
+    return m <= 8 * hit && (k <= kFlatK || hit * n * k < 1ull << 25);
+}
 
 TilePlan grouped_dw_plan(uint64_t m, uint32_t experts, uint32_t n, uint32_t k)
 {
@@ -118,6 +133,10 @@ uint32_t xcd_grid(uint64_t pieces) { return (uint32_t)(8 * ceil_div(pieces, 8));
 // Blocks of a kernel that takes one large tile after the other.
 uint32_t large_grid(uint64_t pieces) { return xcd_grid(pieces < kCus ? pieces : kCus); }
 
+// A block's four waves on the same rows of weights, or each on its own.  us of 2 to 16 rows, a vocabulary of 128256 x 4096: 157 to 160
+// and 166 to 174; of 50257 x 768 22 to 23 and 19 to 20; one row of each of 8 experts of 1024 x 2048 11.8 and 19.6.
+bool few_split(uint32_t k) { return k > 1024; }
+
 constexpr int kFlatAlong = 256, kFlatAcross = 128;  // columns of the flat tiles
 
 // y, or dx (kPAlong false), by tiles of BM x BN
@@ -144,8 +163,8 @@ void launch_grouped(GroupedArgs g, TileSize size, hipStream_t stream)
 template <int T>
 wc_status launch_grouped_linear(GroupedArgs g, hipStream_t stream)
 {
-    if (grouped_few(g.m, g.experts)) {
-        const bool split = g.k > 1024;
+    if (grouped_few(g.m, g.experts, g.n, g.k)) {
+        const bool split = few_split(g.k);
         g.slots = (g.m < g.experts ? g.m : g.experts) + (g.zero_rest ? 1 : 0);
         const dim3 grid((uint32_t)(g.slots * ceil_div(g.n, split ? 32 : 128)));
         if (split) hipLaunchKernelGGL((k_grouped_few<T, true>), grid, dim3(256), 0, stream, g);
@@ -181,15 +200,17 @@ bool valid_loss(uint64_t m, uint32_t vocab, uint32_t cols)
     return m <= kLossMaxRows && vocab >= 1 && vocab <= (1u << 22) && cols >= 8 && cols % 8 == 0 && cols <= kMaxCols;
 }
 
+// us by k_loss_few and by tiles: 12 and 16 rows of a vocabulary of 50257 x 768 20 and 25 (32 rows 26 and 25), of 128256 x
+// 4096 156 to 160 and 160 (32 rows 212 and 160)
 bool loss_few(uint64_t m) { return m <= 16; }
 TileSize loss_tile(uint64_t m, uint32_t vocab, uint32_t k)
 {
-    if (m <= 64) return kFlat;
+    if (flat(m, k)) return kFlat;
     return tile_plan(ceil_div(m, 256) * ceil_div(vocab, 256), ceil_div(m, 128) * ceil_div(vocab, 128), ceil_div(k, kTileK), 0, true, 1).size;
 }
 uint32_t loss_parts(uint64_t m, uint32_t vocab, uint32_t k)
 {
-    return (uint32_t)ceil_div(vocab, loss_few(m) ? (k > 1024 ? 32 : 128) : loss_tile(m, vocab, k) == kSmall ? 128 : 256);
+    return (uint32_t)ceil_div(vocab, loss_few(m) ? (few_split(k) ? 32 : 128) : loss_tile(m, vocab, k) == kSmall ? 128 : 256);
 }
 uint64_t up256(uint64_t n) { return ceil_div(n, 256) * 256; }
 
@@ -197,7 +218,7 @@ template <int T>
 void launch_loss(const LossArgs &g, hipStream_t stream)
 {
     if (loss_few(g.m)) {
-        const bool split = g.k > 1024;
+        const bool split = few_split(g.k);
         const dim3 grid((uint32_t)ceil_div(g.vocab, split ? 32 : 128));
         if (split) hipLaunchKernelGGL((k_loss_few<T, true>), grid, dim3(256), 0, stream, g);
         else hipLaunchKernelGGL((k_loss_few<T, false>), grid, dim3(256), 0, stream, g);
@@ -265,7 +286,7 @@ void launch_loss_grad(const wc_linear_loss_grad &a, LossGradArgs g, const LossGr
         g.width = (uint32_t)(g.vocab - v0 < p.piece ? g.vocab - v0 : p.piece);
         g.pitch = (g.width + 7) / 8 * 8;
         if (loss_few(g.m)) {
-            const bool split = g.k > 1024;
+            const bool split = few_split(g.k);
             const dim3 grid((uint32_t)ceil_div(g.width, split ? 32 : 128));
             if (split) hipLaunchKernelGGL((k_loss_grad_few<T, true>), grid, dim3(256), 0, stream, g);
             else hipLaunchKernelGGL((k_loss_grad_few<T, false>), grid, dim3(256), 0, stream, g);
@@ -306,7 +327,7 @@ extern "C" {
 
 uint64_t wc_grouped_linear_scratch(uint64_t m, uint32_t experts, uint32_t rows, uint32_t cols)
 {
-    if (m == 0 || !valid_grouped(m, experts, rows, cols) || grouped_few(m, experts)) return 0;
+    if (m == 0 || !valid_grouped(m, experts, rows, cols) || grouped_few(m, experts, rows, cols)) return 0;
     return grouped_part(grouped_size(m, experts, rows, cols), m, experts, rows, cols, kFlatAlong);
 }
 

@@ -60,7 +60,7 @@ def test_grouped_refusals(L):
 
 def test_grouped_scratch(L):
     # no last round to be split: few rows of each expert, or a short k
-    assert L.wc_grouped_linear_scratch(2, 8, 14336, 4096) == 0
+    assert L.wc_grouped_linear_scratch(2, 8, 1024, 2048) == 0
     assert L.wc_grouped_linear_scratch(600, 4, 48, 64) == 0
     for bad in ((0, 4, 48, 64), (600, 0, 48, 64), (600, 1025, 48, 64), (600, 4, 44, 64), (600, 4, 48, 60), (1 << 31, 4, 48, 64),
                 (1000, 4, (1 << 20) + 8, 64)):

@@ -67,18 +67,19 @@ uint64_t tiles_expected(uint64_t m, uint32_t experts, uint64_t tile)  // with th
     return hit * ceil_div(ceil_div(m, hit), tile);
 }
 
-// Tiles of 64 rows read the weights as fast as memory gives them, where k is long
-// enough.  us of 9 to 64 rows of each of 8 experts of 14336 x 4096 by tiles of 64 and of 128, 145 to 157 and 165 to
-// 180, of 64 of 1024 x 2048, 51 to 63 and 69 to 74, of 64 of 768 x 768, 19 to 21 and 16 to 18; of 65 to 128 rows of
-// 14336 x 4096 340 to 250 and 180 to 203.  The loss of 17 to 64 rows, a vocabulary of 128256 x 4096, 160 and 180, of
-// 50257 x 768, 25 and 22.
-constexpr uint32_t kFlatK = 1024;
-bool flat(uint64_t rows, uint32_t k) { return rows <= 64 && k > kFlatK; }
+// Tiles of 64 rows read the weights as fast as memory gives them, where there are enough of them; below that smaller ones
+// use more of the compute units.  us by tiles of 64 and of 128, 17 to 64 rows of a vocabulary of 128256 x 4096 160 and 180, of
+// 100000 x 768 34 to 37 and 43 to 45, of 32768 x 2048 45 and 35, of 50257 x 768 25 and 22; 9 to 64 rows of each of 8 experts of
+// 14336 x 4096 145 to 157 and 165 to 180 (dx 149 to 168 and 166 to 181), of 64 of 1024 x 2048 51 to 63 and 69 to 74 (dx 53 to 61 and
+// 64 to 70), of 8 of 2048 x 4096 32 to 41 and 28 to 35; 65 to 128 rows of each of 8 of 14336 x 4096 340 to 250 and 180 to 203.
+bool flat(uint64_t rows, uint64_t weights) { return rows <= 64 && weights > 1ull << 26; }
 
-// The tiles of y or dx of m rows with n columns each, from k
-TileSize grouped_size(uint64_t m, uint32_t experts, uint32_t n, uint32_t k)
+// The tiles of y of m rows with n columns each, from k, or of dx (across), whose tiles of 64 rows have 128 columns and are more: both
+// gradients of 602 rows, 9 to 60 of each of 16 experts of 2304 x 768, 43 us, and 48.5 by tiles of 128.
+TileSize grouped_size(uint64_t m, uint32_t experts, uint32_t n, uint32_t k, bool across)
 {
-    if (flat(ceil_div(m, m < experts ? m : experts), k)) return kFlat;
+    const uint64_t hit = m < experts ? m : experts, rows = ceil_div(m, hit);
+    if (flat(rows, hit * n * k) || (across && rows <= 64 && k > 1024)) return kFlat;
     return tile_plan(tiles_expected(m, experts, 256) * ceil_div(n, 256), tiles_expected(m, experts, 128) * ceil_div(n, 128),
                      ceil_div(k, kTileK), m * n, true, 1)
         .size;
@@ -100,7 +101,7 @@ uint64_t grouped_part(TileSize size, uint64_t m, uint32_t experts, uint32_t n, u
 bool grouped_few(uint64_t m, uint32_t experts, uint32_t n, uint32_t k)
 {
     const uint64_t hit = m < experts ? m : experts;
-    return m <= 8 * hit && (k <= kFlatK || hit * n * k < 1ull << 25);
+    return m <= 8 * hit && (k <= 1024 || hit * n * k < 1ull << 25);
 }
 
 TilePlan grouped_dw_plan(uint64_t m, uint32_t experts, uint32_t n, uint32_t k)
@@ -170,7 +171,7 @@ wc_status launch_grouped_linear(GroupedArgs g, hipStream_t stream)
         if (split) hipLaunchKernelGGL((k_grouped_few<T, true>), grid, dim3(256), 0, stream, g);
         else hipLaunchKernelGGL((k_grouped_few<T, false>), grid, dim3(256), 0, stream, g);
     } else {
-        launch_grouped<T, true>(g, grouped_size(g.m, g.experts, g.n, g.k), stream);
+        launch_grouped<T, true>(g, grouped_size(g.m, g.experts, g.n, g.k, false), stream);
     }
     return launched();
 }
@@ -205,7 +206,7 @@ bool valid_loss(uint64_t m, uint32_t vocab, uint32_t cols)
 bool loss_few(uint64_t m) { return m <= 16; }
 TileSize loss_tile(uint64_t m, uint32_t vocab, uint32_t k)
 {
-    if (flat(m, k)) return kFlat;
+    if (flat(m, (uint64_t)vocab * k)) return kFlat;
     return tile_plan(ceil_div(m, 256) * ceil_div(vocab, 256), ceil_div(m, 128) * ceil_div(vocab, 128), ceil_div(k, kTileK), 0, true, 1).size;
 }
 uint32_t loss_parts(uint64_t m, uint32_t vocab, uint32_t k)
@@ -328,7 +329,7 @@ extern "C" {
 uint64_t wc_grouped_linear_scratch(uint64_t m, uint32_t experts, uint32_t rows, uint32_t cols)
 {
     if (m == 0 || !valid_grouped(m, experts, rows, cols) || grouped_few(m, experts, rows, cols)) return 0;
-    return grouped_part(grouped_size(m, experts, rows, cols), m, experts, rows, cols, kFlatAlong);
+    return grouped_part(grouped_size(m, experts, rows, cols, false), m, experts, rows, cols, kFlatAlong);
 }
 
 wc_status wc_grouped_linear(const wc_grouped *a, void *d_scratch, uint64_t scratch_bytes, uint32_t *d_err, hipStream_t stream)
@@ -367,7 +368,7 @@ uint64_t wc_grouped_linear_backward_scratch(uint64_t m, uint32_t experts, uint32
 {
     if (m == 0 || !valid_grouped(m, experts, rows, cols)) return 0;
     // one after the other
-    const uint64_t dx = grouped_part(grouped_size(m, experts, cols, rows), m, experts, cols, rows, kFlatAcross);
+    const uint64_t dx = grouped_part(grouped_size(m, experts, cols, rows, true), m, experts, cols, rows, kFlatAcross);
     const uint64_t dw = part_bytes((uint64_t)experts * rows * cols, grouped_dw_plan(m, experts, rows, cols).splits);
     return dx > dw ? dx : dw;
 }
@@ -404,7 +405,7 @@ wc_status wc_grouped_linear_backward(const wc_grouped_grad *a, void *d_scratch, 
         g.k = a->rows;
         g.zero_rest = a->zero_rest;
         g.err = d_err;
-        const TileSize p = grouped_size(a->m, a->experts, a->cols, a->rows);
+        const TileSize p = grouped_size(a->m, a->experts, a->cols, a->rows, true);
         if (grouped_part(p, a->m, a->experts, a->cols, a->rows, kFlatAcross)) g.part = static_cast<float *>(d_scratch);
         if (a->type == WC_T_BF16) launch_grouped<WC_T_BF16, false>(g, p, stream);
         else launch_grouped<WC_T_FP16, false>(g, p, stream);

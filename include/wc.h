@@ -617,7 +617,7 @@ wc_status wc_linear_cross_entropy_backward(const wc_linear_loss_grad *a, void *d
  *   w_rk = scales_rg (q_rk - zeros_rg),   y = x w^T,
  * q in 0 .. 15, two in a byte (the even column in the low half).  Products of
  * x with whole numbers are exact, their sums over a group, and those of
- * the scaled groups, are fp32, and y is rounded once.  32 rows of x meet the weights
+ * the scaled groups, are fp32, and y is rounded once; an infinity in x makes its row of y NaN.  32 rows of x meet the weights
  * at a time (16 where there are no more): meant for few. */
 typedef struct {
     const void *x;          /* m x cols, rows x_stride elements apart, 16-byte aligned rows */

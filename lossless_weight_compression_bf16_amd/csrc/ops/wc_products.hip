@@ -75,7 +75,7 @@ uint64_t tiles_expected(uint64_t m, uint32_t experts, uint64_t tile)  // with th
 bool flat(uint64_t rows, uint64_t weights) { return rows <= 64 && weights > 1ull << 26; }
 
 // The tiles of y of m rows with n columns each, from k, or of dx (across), whose tiles of 64 rows have 128 columns and are more: both
-// gradients of 602 rows, 9 to 60 of each of 16 experts of 2304 x 768, 43 us, and 48.5 by tiles of 128.
+// gradients of 602 rows, dealt at random to 16 experts of 2304 x 768, 43 us, and 48.5 by tiles of 128.
 TileSize grouped_size(uint64_t m, uint32_t experts, uint32_t n, uint32_t k, bool across)
 {
     const uint64_t hit = m < experts ? m : experts, rows = ceil_div(m, hit);

@@ -29,7 +29,7 @@ using namespace wc;
 
 namespace {
 
-constexpr int kVersion = 10300;  // 1.3.0: log probabilities, adapters, mixture of experts (csrc/ops)
+constexpr int kVersion = 10400;  // 1.4.0: grouped products, loss from hidden states, 4-bit weights (csrc/ops)
 
 bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 

@@ -16,6 +16,7 @@
 #pragma once
 
 #include "ops_common.hpp"
+#include "ops_deal.hpp"
 #include "ops_moe.hpp"
 #include "ops_tiles.hpp"
 
@@ -114,16 +115,15 @@ struct Groups {
     }
 };
 
-// The tiles of y or dx, and how they are dealt to the blocks.  As many whole ones
-// as fill the compute units some number of times; the tiles that are left, if they
-// would leave half of the compute units or more without one, in parts along
-// k, whose sums k_grouped_join adds up; then tiles of the rows behind the
-// last expert's, which are only to be zeros.
+// The tiles of y or dx, and how they are dealt to the blocks (Dealing); the sums of the
+// last ones' parts are added up by k_grouped_join.
 template <int BM, int BN>
 struct GroupedPieces {
     static constexpr uint32_t kSlots = kCus * tile_blocks(BM, BN);
+    static_assert(kSlots % 8 == 0, "the XCDs have as many each");
     Groups groups;
-    uint32_t last, down, across, whole, left, splits, stages, zeros;
+    Dealing deal;
+    uint32_t last, down, across, stages;
 
     __device__ __forceinline__ static uint32_t tiles(uint32_t rows) { return (rows + BM - 1) / BM; }
 
@@ -134,31 +134,7 @@ struct GroupedPieces {
         down = groups.total;
         across = (g.n + BN - 1) / BN;
         stages = (g.k + kTileK - 1) / kTileK;
-        const uint32_t all = down * across;
-        whole = all / kSlots * kSlots;
-        left = all - whole;
-        // at least 8 stages in a part
-        splits = g.part && left ? max(1u, min(min(kSlots / left, stages / 8), 16u)) : 1u;
-        zeros = g.zero_rest ? tiles(g.m - last) * across : 0u;
-    }
-    // Block b's kind of piece (0: whole tile, 1: part, 2: zeros, 3: none) and its number,
-    // every XCD with a contiguous range of each kind.
-    __device__ __forceinline__ uint32_t piece(uint32_t b, uint32_t &t) const
-    {
-        uint32_t at = b / 8;
-        if (at < whole / 8) {
-            t = b % 8 * (whole / 8) + at;
-            return 0;
-        }
-        at -= whole / 8;
-        const uint32_t parts = (left * splits + 7) / 8, behind = (zeros + 7) / 8;
-        if (at < parts) {
-            t = b % 8 * parts + at;
-            return t < left * splits ? 1 : 3;
-        }
-        at -= parts;
-        t = b % 8 * behind + at;
-        return at < behind && t < zeros ? 2 : 3;
+        deal = Dealing::of(down * across, stages, kSlots, g.part != nullptr, g.zero_rest ? tiles(g.m - last) * across : 0u);
     }
     // The expert, rows and first column of tile t.
     __device__ __forceinline__ bool tile(const GroupedArgs &g, uint32_t t, uint32_t &expert, uint32_t &m0, uint32_t &rows,
@@ -195,18 +171,19 @@ __global__ __launch_bounds__(256, tile_blocks(BM, BN)) void k_grouped(GroupedArg
     each_tile<Ti, Job>(
         ti, b0, b1,
         [&](uint32_t, Job &j) {
-            for (;; turn++) {
+            for (;;) {
                 uint32_t t, expert;
-                const uint32_t kind = p.piece(block_of(turn), t);
-                if (kind == 3) return false;
-                if (kind == 2) {
+                const PieceKind kind = p.deal.next(blockIdx.x, gridDim.x, turn, t);
+                if (kind == kNoMore) return false;
+                if (kind == kZeros) {
                     const uint32_t m0 = p.last + BM * (t / p.across), n0 = BN * (t % p.across), cols = min((uint32_t)BN, g.n - n0) / 8;
                     for (uint32_t q = threadIdx.x; q < min((uint32_t)BM, g.m - m0) * cols; q += 256)
                         *reinterpret_cast<u32x4 *>(g.y + (m0 + q / cols) * g.y_stride + n0 + 8 * (q % cols)) = u32x4{0, 0, 0, 0};
                     continue;
                 }
-                const uint32_t split = kind ? t / p.left : 0, splits = kind ? p.splits : 1;
-                if (!p.tile(g, kind ? p.whole + t % p.left : t, expert, j.m0, j.rows, j.n0)) continue;
+                const bool part = kind == kPart;
+                const uint32_t split = part ? t / p.deal.left : 0, splits = part ? p.deal.splits : 1;
+                if (!p.tile(g, part ? p.deal.whole + t % p.deal.left : t, expert, j.m0, j.rows, j.n0)) continue;
                 j.part = splits > 1 ? t : ~0u;
                 const uint32_t k0 = kTileK * (p.stages * split / splits), k = min(g.k, kTileK * (p.stages * (split + 1) / splits)) - k0;
                 const uint16_t *w = g.w + expert * g.w_expert;
@@ -214,7 +191,6 @@ __global__ __launch_bounds__(256, tile_blocks(BM, BN)) void k_grouped(GroupedArg
                 if constexpr (kPAlong) j.place.p = Ti::P::Where::at(w + (uint64_t)j.n0 * g.w_row + k0, min((uint32_t)BN, g.n - j.n0), k);
                 else j.place.p = Ti::P::Where::at(w + (uint64_t)k0 * g.w_row + j.n0, k, g.n - j.n0);
                 j.place.k = k;
-                turn++;
                 return true;
             }
         },
@@ -257,13 +233,13 @@ __global__ __launch_bounds__(256) void k_grouped_join(GroupedArgs g)
     p.init(g);
     const uint32_t q = blockIdx.x / 8;
     uint32_t expert, m0, rows, n0;
-    if (p.splits == 1 || q >= p.left || !p.tile(g, p.whole + q, expert, m0, rows, n0)) return;
+    if (p.deal.splits == 1 || q >= p.deal.left || !p.tile(g, p.deal.whole + q, expert, m0, rows, n0)) return;
     const uint32_t from = BM / 8 * (blockIdx.x % 8);
     for (uint32_t e = threadIdx.x; e < BM / 8 * BN / 4; e += 256) {
         const uint32_t row = from + e / (BN / 4), col = 4 * (e % (BN / 4));
         if (row >= rows || n0 + col >= g.n) continue;
         const float *part = g.part + (uint64_t)q * (BM * BN) + row * BN + col;
-        store_four<T>(g.y + (m0 + row) * g.y_stride + n0 + col, sum_parts(part, (uint64_t)p.left * (BM * BN), p.splits));
+        store_four<T>(g.y + (m0 + row) * g.y_stride + n0 + col, sum_parts(part, (uint64_t)p.deal.left * (BM * BN), p.deal.splits));
     }
 }
 

@@ -584,8 +584,10 @@ wc_status wc_linear_cross_entropy(const wc_linear_loss *a, void *d_scratch, uint
 /* Its gradients from those of loss and lse (either may be NULL: zero):
  *   G_rv = (grad_loss_r + grad_lse_r) exp(z_rv - lse_r) - grad_loss_r [v = t_r],
  *   grad_hidden = G W,   grad_weight = G^T H
- * with grad_loss_r = 0 for tokens outside [0, vocab).  G is rounded to `type`
- * once, the products' sums are fp32, and each result is rounded once.  G is
+ * with grad_loss_r = 0 for tokens outside [0, vocab).  G is held as the sum of
+ * two numbers of `type` (16 bits of it in BF16, 22 in FP16), or with `rounded` as
+ * one, in half the time of both products; their sums are fp32, and each
+ * result is rounded once.  G is
  * made for a piece of the vocabulary at a time, at most 2^27 numbers.  A row
  * without a part (both gradients 0, or lse -inf) has none, whatever its
  * hidden values are.  Either result may be NULL. */
@@ -605,7 +607,7 @@ typedef struct {
     uint32_t vocab;
     uint32_t cols;
     uint32_t type;
-    uint32_t reserved;
+    uint32_t rounded;         /* G as one 16-bit number instead of two */
 } wc_linear_loss_grad;
 
 uint64_t wc_linear_cross_entropy_backward_scratch(uint64_t m, uint32_t vocab, uint32_t cols);

@@ -145,7 +145,7 @@ class wc_linear_loss_grad(ctypes.Structure):
                 ("grad_loss", ctypes.c_void_p), ("grad_lse", ctypes.c_void_p), ("grad_hidden", ctypes.c_void_p),
                 ("grad_hidden_stride", ctypes.c_uint64), ("grad_weight", ctypes.c_void_p), ("m", ctypes.c_uint64),
                 ("vocab", ctypes.c_uint32), ("cols", ctypes.c_uint32), ("type", ctypes.c_uint32),
-                ("reserved", ctypes.c_uint32)]
+                ("rounded", ctypes.c_uint32)]
 
 
 class wc_fourbit(ctypes.Structure):

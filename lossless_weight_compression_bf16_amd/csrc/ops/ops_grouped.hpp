@@ -317,8 +317,8 @@ constexpr uint32_t kLossRowBlocks = 256;
 // What G is multiplied by before it is rounded: 1 (BF16) or 2^14 (FP16) over the
 // largest gradient of a row, from the largest of each of kLossRowBlocks parts.  So
 // where all rows have the same one, as under a mean, what it is has no rounding
-// of its own (the gradients of a mean over 4096 rows, BF16, were 0.26% off, most of it one common
-// factor, and are 0.21%), and FP16 numbers stay in range.
+// of its own where G is rounded to one of them (the gradients of a mean over 4096 rows, BF16, were 0.26% off so, most of it
+// one common factor, and are 0.21%), and FP16 numbers stay in range.
 template <int T>
 __device__ __forceinline__ float loss_scale(const float *most, float &unscale)
 {

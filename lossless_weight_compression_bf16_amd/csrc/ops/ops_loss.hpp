@@ -10,10 +10,16 @@
 //   k_loss_grad_few, k_loss_grad  G of a piece of the vocabulary: z again, then the formula
 //   k_product                 dH += G W and dW = G^T H of that piece
 //
+// G is fp32 and meets the matrix cores as a sum of two 16-bit terms, 16 of its bits in BF16 and 22
+// in FP16, so that the gradients are as near to the exact ones as their own rounding leaves them (4096 rows, 128256 x 4096,
+// BF16: 0.166% off in the root mean square, as fp32 products rounded once are; 100 rows, 50257 x 768, FP16: 0.0209%). Each term is a
+// product of its own, one after the other in the same sums. A caller who asks for `rounded` has one
+// term: 0.207% and 0.0239% for 9760 us in place of 16200, and 84 in place of 113.
+//
 // What bounds them, and what they take: up to 64 rows, reading W (61 rows, 128256 x 4096: 157 us, 6.7 TB/s); many rows, the
-// matrix cores at the clock that their power leaves (4096 rows: 3230 us, 1.33 PFLOP/s; the gradients, in four pieces of
-// 880, 760 and 755 us, 1.34); in between, stages of 0.9 us in which one wave on a SIMD reads, waits and multiplies in turn (100
-// rows, 50257 x 768: 31, 24 and 31 us).  G goes through memory once for each product: in the tile that made it, only one of the
+// matrix cores at the clock that their power leaves (4096 rows: 3230 us, 1.33 PFLOP/s; the gradients 16200 us, 21.5 TFLOP with both terms, 1.33);
+// in between, stages of 0.9 us in which one wave on a SIMD reads, waits and multiplies in turn (100
+// rows, 50257 x 768: 113 us in all).  G goes through memory once for each product: in the tile that made it, only one of the
 // two could use it, and the other would make it again, a third product for each.
 #pragma once
 
@@ -253,6 +259,7 @@ struct LossGradArgs {
     f32x4 *rows;         // m: lse, gl + gz, gl, token
     float *most;         // kLossRowBlocks: the largest |gl|, |gl + gz| of some rows
     uint16_t *grad;      // m x pitch: G of a piece
+    uint64_t again;      // elements from there to what those numbers leave of G, or 0: nothing is kept of it
     uint32_t pitch, v0, width;
     uint32_t *err;
 };
@@ -286,8 +293,8 @@ __device__ __forceinline__ float loss_gradient(f32x4 row, float z, uint32_t v, f
     return scale * ((int32_t)v == __builtin_bit_cast(int32_t, (float)row[3]) ? p - row[2] : p);
 }
 
-// G of a block's tiles.  Grid: 8 ceil(tiles / 8), or kCus (each_tile).
-template <int T, int BM, int BN>
+// G of a block's tiles, in two terms with kWhole.  Grid: 8 ceil(tiles / 8), or kCus (each_tile).
+template <int T, int BM, int BN, bool kWhole>
 __global__ __launch_bounds__(256, tile_blocks(BM, BN)) void k_loss_grad(LossGradArgs g)
 {
     using Ti = Tile<T, BM, BN, true, true>;
@@ -315,18 +322,21 @@ __global__ __launch_bounds__(256, tile_blocks(BM, BN)) void k_loss_grad(LossGrad
 #pragma unroll
             for (int b = 0; b < Ti::kM; b++) info[b] = g.rows[j.m0 + min(Ti::q_row(wave, b) + (threadIdx.x & 15), j.rows - 1)];
             uint16_t *to = g.grad + (uint64_t)j.m0 * g.pitch + j.n0;
-            each_eight<T>(
-                ti,
-                [&](uint32_t row, uint32_t col, f32x4 z) {
-                    const f32x4 of_row = info[(row / 16 - wave / Ti::kWavesN) / Ti::kWavesM];
+            const auto gradient = [&](uint32_t row, uint32_t col, f32x4 z) {
+                const f32x4 of_row = info[(row / 16 - wave / Ti::kWavesN) / Ti::kWavesM];
 #pragma unroll
-                    for (uint32_t e = 0; e < 4; e++)
-                        z[e] = col + e < j.cols ? loss_gradient(of_row, z[e], g.v0 + j.n0 + col + e, scale) : 0.f;
-                    return z;
-                },
-                [&](uint32_t row, uint32_t col, u32x4 v) {
-                    if (row < j.rows && j.n0 + col < g.pitch) *reinterpret_cast<u32x4 *>(to + (uint64_t)row * g.pitch + col) = v;
-                });
+                for (uint32_t e = 0; e < 4; e++)
+                    z[e] = col + e < j.cols ? loss_gradient(of_row, z[e], g.v0 + j.n0 + col + e, scale) : 0.f;
+                return z;
+            };
+            const auto put = [&](uint32_t row, uint32_t col, u32x4 v, auto... rest) {
+                if (row >= j.rows || j.n0 + col >= g.pitch) return;
+                uint16_t *at = to + (uint64_t)row * g.pitch + col;
+                *reinterpret_cast<u32x4 *>(at) = v;
+                ((*reinterpret_cast<u32x4 *>(at + g.again) = rest), ...);
+            };
+            if constexpr (kWhole) each_eight_whole<T>(ti, gradient, put);
+            else each_eight<T>(ti, gradient, put);
         });
 }
 
@@ -353,15 +363,24 @@ __global__ __launch_bounds__(256, 2) void k_loss_grad_few(LossGradArgs g)
                                        const uint32_t v = first[m] + 4 * gr + e;
                                        if (v < n0 + 16 * m || v >= g.width) continue;
                                        const float z = m ? v1[e] : v0[e];
-                                       to[v] = Type<T>::from_f32(loss_gradient(info, z, g.v0 + v, scale));
+                                       const float all = loss_gradient(info, z, g.v0 + v, scale);
+                                       const uint16_t first_term = Type<T>::from_f32(all);
+                                       to[v] = first_term;
+                                       if (!g.again) continue;
+                                       const float had = Type<T>::to_f32(first_term);
+                                       to[g.again + v] = Type<T>::from_f32(fabsf(had) < kInf ? all - had : 0.f);
                                    }
                                if (gr == 0 && n0 + 32 >= g.width)
-                                   for (uint32_t v = g.width; v < g.pitch; v++) to[v] = 0;
+                                   for (uint32_t v = g.width; v < g.pitch; v++) {
+                                       to[v] = 0;
+                                       if (g.again) to[g.again + v] = 0;
+                                   }
                            });
 }
 
 struct ProductArgs {
     const uint16_t *q, *p;
+    uint64_t again;           // elements between the two terms of Q, where it has as many
     uint64_t q_stride, p_stride;
     uint32_t m, n, k;         // of D
     uint32_t splits;          // of k, each with its own m x n of part
@@ -372,9 +391,9 @@ struct ProductArgs {
     const float *most;        // of G, by which it was scaled
 };
 
-// D = Q P^T of whole matrices.  kQAlong: k along the rows of Q's memory; P has
+// D = Q P^T of whole matrices, Q in kTerms terms.  kQAlong: k along the rows of Q's memory; P has
 // it across.  Grid: 8 ceil(tiles / 8), or kCus (each_tile).
-template <int T, int BM, int BN, bool kQAlong>
+template <int T, int BM, int BN, bool kQAlong, int kTerms>
 __global__ __launch_bounds__(256, tile_blocks(BM, BN)) void k_product(ProductArgs g)
 {
     using Ti = Tile<T, BM, BN, kQAlong, false>;
@@ -390,7 +409,7 @@ __global__ __launch_bounds__(256, tile_blocks(BM, BN)) void k_product(ProductArg
     float early = 1.f;
     if constexpr (Ti::kNamed) loss_scale<T>(g.most, early);
     Ti ti(g.q_stride, g.p_stride);
-    each_tile<Ti, Job>(
+    each_tile<Ti, Job, kTerms>(
         ti, b0, b1,
         [&](uint32_t n, Job &j) {
             const uint32_t t = xcd_piece(block_of(n), each * g.splits);
@@ -428,7 +447,8 @@ __global__ __launch_bounds__(256, tile_blocks(BM, BN)) void k_product(ProductArg
                                       *reinterpret_cast<u32x4 *>(out + row * g.out_stride + col) = v;
                               });
             }
-        });
+        },
+        2 * g.again);
 }
 
 }  // namespace ops

@@ -294,14 +294,13 @@ struct Tile {
         multiply<kEach>(h[1], h[0], next, next + Q::kBytes, 0, s, here, here + Q::kBytes, wave, live);
     }
 
-    // The first two stages, of k0 and k1 on, on their way, and the first half read.
-    __device__ __forceinline__ void first(const Place &w, uint32_t k0, uint32_t k1, Half *h, char *s0, char *s1) const
+    // The first two stages on their way, and the first half read.
+    __device__ __forceinline__ void first(Stage s, const Stage &second, Half *h, char *s0, char *s1) const
     {
         const uint32_t wave = uniform(threadIdx.x >> 6);
-        Stage s = begin(w, k0);
 #pragma unroll
         for (int j = 0; j < kLoads; j++) load(s, s0, s0 + Q::kBytes, wave, j);
-        s = begin(w, k1);
+        s = second;
 #pragma unroll
         for (int j = 0; j < kLoads; j++) load(s, s1, s1 + Q::kBytes, wave, j);
         __builtin_amdgcn_s_waitcnt((kLoads & 15) | ((kLoads >> 4) << 14) | 0x0070);  // all but the second stage's
@@ -319,50 +318,61 @@ struct Tile {
         settle();
     }
 
+    // Where Q is a sum of kTerms matrices, `again` bytes apart: the sum of their products
+    // with P, one after the other over all of k.
+
     // The product of a tile of which `rows` of Q's rows exist.  Where P is streamed,
     // blocks begin at different stages (pairs of an XCD's at the same one), so
     // that not all of them ask for the same columns of all rows at the same time.
-    __device__ __forceinline__ void product(const Place &of, char *s0, char *s1, uint32_t rows)
+    template <int kTerms>
+    __device__ __forceinline__ void product(const Place &of, char *s0, char *s1, uint32_t rows, uint64_t again)
     {
+        static_assert(kTerms == 1 || !kStreamP, "every term from its first stage on");
         const Place w = of.said_uniform();
         const uint32_t wave = uniform(threadIdx.x >> 6);
         // this wave's sixteens: wave / kWavesN, and every kWavesM-th after it
         const int sixteens = (int)((uniform(rows) + 15) / 16) - (int)(wave / kWavesN);
         const int live = sixteens <= 0 ? 0 : (sixteens + kWavesM - 1) / kWavesM;
-        const uint32_t k = w.k, stages = (k + kTileK - 1) / kTileK;
+        const uint32_t k = w.k, of_term = (k + kTileK - 1) / kTileK, stages = kTerms * of_term;
         uint32_t next = kStreamP && stages ? kTileK * (blockIdx.x / 16 % stages) : 0;
         uint32_t left = stages;  // whose loads have not been asked for
-        auto turn = [&]() {      // k0 of the next stage; past the last k when there is none
+        auto turn = [&]() {      // the next stage; past the last k when there is none
+            Place to = w;
+            if (kTerms > 1) to.q.base += left > of_term ? 0 : again;
             const uint32_t at = left ? next : k;
             left -= left ? 1 : 0;
             next = next + kTileK < k ? next + kTileK : 0;
-            return at;
+            return begin(to, at);
         };
         Half h[2];
         clear();
-        const uint32_t k0 = turn(), k1 = turn();
-        first(w, k0, k1, h, s0, s1);
+        const Stage a = turn(), b = turn();
+        first(a, b, h, s0, s1);
         uint32_t n = 0;
         for (; n + 1 < stages; n += 2) {
-            stage(h, s0, s1, begin(w, turn()), wave, live);
-            stage(h, s1, s0, begin(w, turn()), wave, live);
+            stage(h, s0, s1, turn(), wave, live);
+            stage(h, s1, s0, turn(), wave, live);
         }
-        if (n < stages) stage(h, s0, s1, begin(w, turn()), wave, live);
+        if (n < stages) stage(h, s0, s1, turn(), wave, live);
         settle();
     }
 
     // The same within a row of tiles: the first half is in h[0] and the first two
     // stages are in s0 and s1, or on their way, and so are those of `next` when
     // this one is done.  Stages are taken by twos, at least two.
-    __device__ __forceinline__ void product(const Place &of, const Place &after, Half *h, char *s0, char *s1)
+    template <int kTerms>
+    __device__ __forceinline__ void product(const Place &of, const Place &after, Half *h, char *s0, char *s1, uint64_t again)
     {
+        static_assert(kTerms <= 2, "one and another");
         const Place w = of.said_uniform(), next = after.said_uniform();
-        const uint32_t wave = uniform(threadIdx.x >> 6), most = w.k > 2 * kTileK ? (w.k + 2 * kTileK - 1) / (2 * kTileK) : 1;
+        const uint32_t wave = uniform(threadIdx.x >> 6), of_term = w.k > 2 * kTileK ? (w.k + 2 * kTileK - 1) / (2 * kTileK) : 1;
+        const uint32_t most = kTerms * of_term;
         clear();
         for (uint32_t n = 1; n <= most; n++) {
-            const bool last = n == most;
-            const Place to{last ? next.q : w.q, last ? next.p : w.p, last ? next.k : w.k};
-            const uint32_t k0 = last ? 0 : 2 * n * kTileK;
+            const bool last = n == most, second = kTerms > 1 && n >= of_term;
+            Place to{last ? next.q : w.q, last ? next.p : w.p, last ? next.k : w.k};
+            if (kTerms > 1) to.q.base += second && !last ? again : 0;
+            const uint32_t k0 = last ? 0 : 2 * (second ? n - of_term : n) * kTileK;
             stage(h, s0, s1, begin(to, k0), wave, kM);
             stage(h, s1, s0, begin(to, k0 + kTileK), wave, kM);
         }
@@ -374,26 +384,27 @@ struct Tile {
 // product.  Where a tile fills the compute unit (256 x 256) the block takes
 // one after the other, a grid of kCus blocks, with the next one's first stages on their
 // way before this one is stored; otherwise a block has one, and those beside it fill such gaps.
-template <class Tile, class Job, class Get, class Done>
-__device__ __forceinline__ void each_tile(Tile &t, char *s0, char *s1, Get get, Done done)
+// again: between Q's two terms, where it has as many.
+template <class Tile, class Job, int kTerms = 1, class Get, class Done>
+__device__ __forceinline__ void each_tile(Tile &t, char *s0, char *s1, Get get, Done done, uint64_t again = 0)
 {
     Job j;
     if (!get(0, j)) return;
     if constexpr (Tile::kNamed) {
         typename Tile::Half h[2];
-        t.first(j.place, 0, kTileK, h, s0, s1);
+        t.first(t.begin(j.place, 0), t.begin(j.place, kTileK), h, s0, s1);
         for (uint32_t n = 1;; n++) {
             Job next;
             const bool more = uniform((uint32_t)get(n, next)) != 0;
             if (!more) next.place = {{j.place.q.base, 0, 0}, {j.place.p.base, 0, 0}, 0};
-            t.product(j.place, next.place, h, s0, s1);
+            t.template product<kTerms>(j.place, next.place, h, s0, s1, again);
             done(t, j);
             if (!more) break;
             j = next;
         }
         __builtin_amdgcn_s_waitcnt(0x0070);
     } else {
-        t.product(j.place, s0, s1, j.rows);
+        t.template product<kTerms>(j.place, s0, s1, j.rows, again);
         done(t, j);
     }
 }
@@ -484,6 +495,41 @@ __device__ __forceinline__ void each_eight(const Tile &t, G g, F f)
             const auto lo = __builtin_amdgcn_permlane16_swap((uint32_t)one, (uint32_t)two, false, false);
             const auto hi = __builtin_amdgcn_permlane16_swap((uint32_t)(one >> 32), (uint32_t)(two >> 32), false, false);
             f(row, col + 16 * (gr & 1) + 8 * (gr >> 1), u32x4{lo[0], hi[0], lo[1], hi[1]});
+        }
+        __builtin_amdgcn_sched_barrier(0);
+    }
+}
+// What the type leaves of four numbers, themselves packed in `of`; 0 where that is an infinity.
+template <int T>
+__device__ __forceinline__ f32x4 rest_of(f32x4 v, uint64_t of)
+{
+#pragma unroll
+    for (int e = 0; e < 4; e++) {
+        const float had = Type<T>::to_f32((uint16_t)(of >> (16 * e)));
+        v[e] = fabsf(had) < kInf ? v[e] - had : 0.f;
+    }
+    return v;
+}
+// The same as each_eight in two terms: f(row, column, eight values, eight of what they leave of D).
+template <int T, class Tile, class G, class F>
+__device__ __forceinline__ void each_eight_whole(const Tile &t, G g, F f)
+{
+    const uint32_t wave = uniform(threadIdx.x >> 6), lane = lane_here(), i = lane & 15, gr = lane >> 4;
+    const auto swapped = [](uint64_t one, uint64_t two) {
+        const auto lo = __builtin_amdgcn_permlane16_swap((uint32_t)one, (uint32_t)two, false, false);
+        const auto hi = __builtin_amdgcn_permlane16_swap((uint32_t)(one >> 32), (uint32_t)(two >> 32), false, false);
+        return u32x4{lo[0], hi[0], lo[1], hi[1]};
+    };
+#pragma unroll
+    for (int b = 0; b < Tile::kM; b++) {
+        const uint32_t row = Tile::q_row(wave, b) + i;
+#pragma unroll
+        for (int a = 0; a < Tile::kN; a += 2) {
+            const uint32_t col = Tile::p_row(wave, a);
+            const f32x4 u = g(row, col + 4 * gr, t.result(a, b)), v = g(row, col + 16 + 4 * gr, t.result(a + 1, b));
+            const uint64_t one = pack_four<T>(u), two = pack_four<T>(v);
+            const uint64_t rest = pack_four<T>(rest_of<T>(u, one)), rest2 = pack_four<T>(rest_of<T>(v, two));
+            f(row, col + 16 * (gr & 1) + 8 * (gr >> 1), swapped(one, two), swapped(rest, rest2));
         }
         __builtin_amdgcn_sched_barrier(0);
     }

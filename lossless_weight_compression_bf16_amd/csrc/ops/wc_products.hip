@@ -193,7 +193,10 @@ void launch_grouped_dw(GroupedDwArgs g, const TilePlan &p, hipStream_t stream)
 
 constexpr uint64_t kLossMaxRows = 1ull << 19;
 constexpr uint32_t kLossSlice = 1u << 15;  // rows of one set of launches of the forward pass
-// G of a piece of the vocabulary: at most 2^27 numbers, what the last cache holds
+// G of a piece of the vocabulary, all terms of it: at most 2^27 numbers, 256 MiB, what the last cache holds.  ms with pieces of 2^25,
+// 2^26, 2^27, 2^28 and 2^30: 4096 rows, 128256 x 4096, 16.4, 16.2, 16.3, 16.5 and 16.6 (rounded 10.3, 9.7, 9.8, 9.9 and 9.9); 16384
+// rows, 32000 x 2048, 12.4, 10.1, 9.3, 9.0 and 8.9; 65536 rows, 16384 x 1024, whose pieces are of 256 to 8192 columns
+// and whose sums of dH are read and written for each, 24.4, 16.1, 12.6, 11.1 and 10.3: what more scratch would give, and many rows pay.
 constexpr uint64_t kLossPiece = 1ull << 27;
 
 bool valid_loss(uint64_t m, uint32_t vocab, uint32_t cols)
@@ -241,17 +244,18 @@ struct LossGradPlan {
     bool dh_sums;            // dH goes through fp32 sums
 };
 
-LossGradPlan loss_grad_plan(uint64_t m, uint32_t vocab, uint32_t k)
+// terms: of G, each 16 bits
+LossGradPlan loss_grad_plan(uint64_t m, uint32_t vocab, uint32_t k, uint32_t terms)
 {
     LossGradPlan p{};
-    uint64_t piece = kLossPiece / m / 256 * 256;
+    uint64_t piece = kLossPiece / terms / m / 256 * 256;
     if (piece < 256) piece = 256;
     const uint64_t pieces = ceil_div(vocab, piece);
     p.piece = (uint32_t)(pieces == 1 ? vocab : ceil_div(ceil_div(vocab, pieces), 256) * 256);
-    p.dh = tile_plan(ceil_div(m, 256) * ceil_div(k, 256), ceil_div(m, 128) * ceil_div(k, 128), ceil_div(p.piece, kTileK), m * k,
-                     pieces > 1);
-    p.dw = tile_plan(ceil_div(p.piece, 256) * ceil_div(k, 256), ceil_div(p.piece, 128) * ceil_div(k, 128), ceil_div(m, kTileK),
-                     (uint64_t)p.piece * k, false);
+    p.dh = tile_plan(ceil_div(m, 256) * ceil_div(k, 256), ceil_div(m, 128) * ceil_div(k, 128), terms * ceil_div(p.piece, kTileK),
+                     m * k, pieces > 1);
+    p.dw = tile_plan(ceil_div(p.piece, 256) * ceil_div(k, 256), ceil_div(p.piece, 128) * ceil_div(k, 128),
+                     terms * ceil_div(m, kTileK), (uint64_t)p.piece * k, false);
     p.dh_sums = pieces > 1 || p.dh.splits > 1;
     uint64_t at = 0;
     auto take = [&](uint64_t bytes) {
@@ -262,23 +266,32 @@ LossGradPlan loss_grad_plan(uint64_t m, uint32_t vocab, uint32_t k)
     p.rows = take(16 * m);
     p.most = take(4 * kLossRowBlocks);
     p.live = take(2 * m * k);
-    p.grad = take(2 * m * ((p.piece + 7) / 8 * 8));
+    p.grad = take(2 * terms * m * ((p.piece + 7) / 8 * 8));
     p.dh_part = take(p.dh_sums ? 4 * m * k * p.dh.splits : 0);
     p.dw_part = take(part_bytes((uint64_t)p.piece * k, p.dw.splits));
     p.bytes = at;
     return p;
 }
 
-template <int T, bool kQAlong>
+template <int T, bool kQAlong, int kTerms>
 void launch_product(const ProductArgs &g, bool large, hipStream_t stream)
 {
     const uint64_t tile = large ? 256 : 128, tiles = ceil_div(g.m, tile) * ceil_div(g.n, tile) * g.splits;
-    if (large) hipLaunchKernelGGL((k_product<T, 256, 256, kQAlong>), dim3(large_grid(tiles)), dim3(256), 0, stream, g);
-    else hipLaunchKernelGGL((k_product<T, 128, 128, kQAlong>), dim3(xcd_grid(tiles)), dim3(256), 0, stream, g);
+    if (large) hipLaunchKernelGGL((k_product<T, 256, 256, kQAlong, kTerms>), dim3(large_grid(tiles)), dim3(256), 0, stream, g);
+    else hipLaunchKernelGGL((k_product<T, 128, 128, kQAlong, kTerms>), dim3(xcd_grid(tiles)), dim3(256), 0, stream, g);
+}
+template <int T, int BM, int BN>
+void launch_loss_grad_tiles(const LossGradArgs &g, hipStream_t stream)
+{
+    const uint64_t tiles = ceil_div(g.m, BM) * ceil_div(g.width, BN);
+    const dim3 grid(BM == 256 ? large_grid(tiles) : xcd_grid(tiles)), block(256);
+    if (g.again) hipLaunchKernelGGL((k_loss_grad<T, BM, BN, true>), grid, block, 0, stream, g);
+    else hipLaunchKernelGGL((k_loss_grad<T, BM, BN, false>), grid, block, 0, stream, g);
 }
 
 template <int T>
-void launch_loss_grad(const wc_linear_loss_grad &a, LossGradArgs g, const LossGradPlan &p, char *s, hipStream_t stream)
+void launch_loss_grad(const wc_linear_loss_grad &a, LossGradArgs g, const LossGradPlan &p, uint32_t terms, char *s,
+                      hipStream_t stream)
 {
     hipLaunchKernelGGL(k_loss_rows, dim3(kLossRowBlocks), dim3(256), 0, stream, g);
     float *dh_part = reinterpret_cast<float *>(s + p.dh_part), *dw_part = reinterpret_cast<float *>(s + p.dw_part);
@@ -286,6 +299,7 @@ void launch_loss_grad(const wc_linear_loss_grad &a, LossGradArgs g, const LossGr
         g.v0 = (uint32_t)v0;
         g.width = (uint32_t)(g.vocab - v0 < p.piece ? g.vocab - v0 : p.piece);
         g.pitch = (g.width + 7) / 8 * 8;
+        g.again = terms > 1 ? (uint64_t)g.m * g.pitch : 0;
         if (loss_few(g.m)) {
             const bool split = few_split(g.k);
             const dim3 grid((uint32_t)ceil_div(g.width, split ? 32 : 128));
@@ -293,24 +307,23 @@ void launch_loss_grad(const wc_linear_loss_grad &a, LossGradArgs g, const LossGr
             else hipLaunchKernelGGL((k_loss_grad_few<T, false>), grid, dim3(256), 0, stream, g);
         } else {
             const TileSize size = loss_tile(g.m, p.piece, g.k);
-            const uint32_t bm = size == kLarge ? 256 : size == kSmall ? 128 : 64, bn = size == kSmall ? 128 : 256;
-            const uint64_t tiles = ceil_div(g.m, bm) * ceil_div(g.width, bn);
-            const dim3 grid(size == kLarge ? large_grid(tiles) : xcd_grid(tiles)), block(256);
-            if (size == kLarge) hipLaunchKernelGGL((k_loss_grad<T, 256, 256>), grid, block, 0, stream, g);
-            else if (size == kSmall) hipLaunchKernelGGL((k_loss_grad<T, 128, 128>), grid, block, 0, stream, g);
-            else hipLaunchKernelGGL((k_loss_grad<T, 64, 256>), grid, block, 0, stream, g);
+            if (size == kLarge) launch_loss_grad_tiles<T, 256, 256>(g, stream);
+            else if (size == kSmall) launch_loss_grad_tiles<T, 128, 128>(g, stream);
+            else launch_loss_grad_tiles<T, 64, 256>(g, stream);
         }
         if (a.grad_hidden) {
-            ProductArgs d{g.grad, g.w + v0 * g.w_row, g.pitch, g.w_row, g.m, g.k, g.width, p.dh.splits,
+            ProductArgs d{g.grad, g.w + v0 * g.w_row, g.again, g.pitch, g.w_row, g.m, g.k, g.width, p.dh.splits,
                           p.dh_sums ? dh_part : nullptr, v0 ? 1u : 0u, static_cast<uint16_t *>(a.grad_hidden),
                           a.grad_hidden_stride, g.most};
-            launch_product<T, true>(d, p.dh.size == kLarge, stream);
+            if (g.again) launch_product<T, true, 2>(d, p.dh.size == kLarge, stream);
+            else launch_product<T, true, 1>(d, p.dh.size == kLarge, stream);
         }
         if (a.grad_weight) {
             uint16_t *out = static_cast<uint16_t *>(a.grad_weight) + v0 * g.k;
-            ProductArgs d{g.grad, g.live, g.pitch, g.k, g.width, g.k, g.m, p.dw.splits,
+            ProductArgs d{g.grad, g.live, g.again, g.pitch, g.k, g.width, g.k, g.m, p.dw.splits,
                           p.dw.splits > 1 ? dw_part : nullptr, 0, out, g.k, g.most};
-            launch_product<T, false>(d, p.dw.size == kLarge, stream);
+            if (g.again) launch_product<T, false, 2>(d, p.dw.size == kLarge, stream);
+            else launch_product<T, false, 1>(d, p.dw.size == kLarge, stream);
             if (p.dw.splits > 1) launch_join(T, JoinArgs{dw_part, out, g.k, g.width, g.k, p.dw.splits, g.most}, stream);
         }
     }
@@ -482,7 +495,8 @@ wc_status wc_linear_cross_entropy(const wc_linear_loss *a, void *d_scratch, uint
 uint64_t wc_linear_cross_entropy_backward_scratch(uint64_t m, uint32_t vocab, uint32_t cols)
 {
     if (m == 0 || !valid_loss(m, vocab, cols)) return 0;
-    return loss_grad_plan(m, vocab, cols).bytes;
+    const uint64_t whole = loss_grad_plan(m, vocab, cols, 2).bytes, rounded = loss_grad_plan(m, vocab, cols, 1).bytes;
+    return whole > rounded ? whole : rounded;
 }
 
 wc_status wc_linear_cross_entropy_backward(const wc_linear_loss_grad *a, void *d_scratch, uint64_t scratch_bytes, uint32_t *d_err,
@@ -496,8 +510,9 @@ wc_status wc_linear_cross_entropy_backward(const wc_linear_loss_grad *a, void *d
         return WC_ERR_ARG;
     if (a->grad_hidden && !rows16(a->grad_hidden, a->grad_hidden_stride, a->cols)) return WC_ERR_ARG;
     if (a->grad_weight && !aligned(a->grad_weight, 16)) return WC_ERR_ARG;
-    const LossGradPlan p = loss_grad_plan(a->m, a->vocab, a->cols);
-    if (scratch_bytes < p.bytes) return WC_ERR_CAPACITY;
+    const uint32_t terms = a->rounded ? 1 : 2;
+    const LossGradPlan p = loss_grad_plan(a->m, a->vocab, a->cols, terms);
+    if (scratch_bytes < wc_linear_cross_entropy_backward_scratch(a->m, a->vocab, a->cols)) return WC_ERR_CAPACITY;
     if (!d_scratch || !aligned(d_scratch, 256)) return WC_ERR_ARG;
     if (!a->grad_hidden && !a->grad_weight) return WC_OK;
     char *s = static_cast<char *>(d_scratch);
@@ -518,8 +533,8 @@ wc_status wc_linear_cross_entropy_backward(const wc_linear_loss_grad *a, void *d
     g.most = reinterpret_cast<float *>(s + p.most);
     g.grad = reinterpret_cast<uint16_t *>(s + p.grad);
     g.err = d_err;
-    if (a->type == WC_T_BF16) launch_loss_grad<WC_T_BF16>(*a, g, p, s, stream);
-    else launch_loss_grad<WC_T_FP16>(*a, g, p, s, stream);
+    if (a->type == WC_T_BF16) launch_loss_grad<WC_T_BF16>(*a, g, p, terms, s, stream);
+    else launch_loss_grad<WC_T_FP16>(*a, g, p, terms, s, stream);
     return launched();
 }
 

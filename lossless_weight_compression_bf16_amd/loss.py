@@ -74,7 +74,7 @@ def _forward(hidden, weight, tokens, check, stream, views=True):
 
 
 def linear_cross_entropy(hidden: torch.Tensor, weight: torch.Tensor, tokens: torch.Tensor, check: bool = True,
-                         stream=None) -> LinearCrossEntropy:
+                         stream=None, rounded: bool = False) -> LinearCrossEntropy:
     """loss[r] = lse[r] - z[r, tokens[r]] and lse[r] = log sum_v exp z[r, v]
     of the logits z = hidden weight^T, which are not kept.
 
@@ -83,7 +83,8 @@ def linear_cross_entropy(hidden: torch.Tensor, weight: torch.Tensor, tokens: tor
     stands for no token (loss 0, whatever the row holds).  hidden and weight
     can be differentiated, once, through loss and lse (a penalty on the
     size of the logits is a function of lse); captured into a graph only
-    while autograd holds no other graph of them.  With check (which waits for
+    while autograd holds no other graph of them.  `rounded` is the gradients':
+    see linear_cross_entropy_backward.  With check (which waits for
     the GPU) a token out of range raises; without, its loss is NaN."""
     if not _good(hidden, weight, tokens):
         _check(hidden, weight, tokens)
@@ -93,7 +94,7 @@ def linear_cross_entropy(hidden: torch.Tensor, weight: torch.Tensor, tokens: tor
         if stream is not None:
             raise ValueError("with gradients the call runs on the current stream: use torch.cuda.stream")
         _ops.fresh_under_capture("linear_cross_entropy", hidden, weight)
-        r = LinearCrossEntropy(*_LinearCrossEntropy.apply(hidden, weight, tokens, check))
+        r = LinearCrossEntropy(*_LinearCrossEntropy.apply(hidden, weight, tokens, check, rounded))
         _ops.note_captured(hidden, weight)
         return r
     return _forward(hidden, weight, tokens, check, stream)
@@ -101,13 +102,15 @@ def linear_cross_entropy(hidden: torch.Tensor, weight: torch.Tensor, tokens: tor
 
 def linear_cross_entropy_backward(hidden: torch.Tensor, weight: torch.Tensor, tokens: torch.Tensor, lse: torch.Tensor,
                                   grad_loss=None, grad_lse=None, need_hidden: bool = True, need_weight: bool = True,
-                                  check: bool = True, stream=None):
+                                  check: bool = True, stream=None, rounded: bool = False):
     """The gradients of hidden and weight, in their type (None where not
     needed), from those of loss and lse (either may be None) and the lse that
     ``linear_cross_entropy`` gave.  The gradient of the logits is made for
-    a piece of the vocabulary at a time, in the type of hidden, and both
-    products sum it in fp32.  A row without a token and without a gradient of
-    lse has no part in them, whatever it holds."""
+    a piece of the vocabulary at a time, as a sum of two numbers of the type of
+    hidden (16 bits of it in BF16, 22 in FP16), and both products sum it in fp32.
+    With `rounded` it is one such number, and both products take half as
+    long, but a gradient's error then is about that of two roundings to the type, not of one.  A
+    row without a token and without a gradient of lse has no part in them, whatever it holds."""
     if not _good(hidden, weight, tokens):
         _check(hidden, weight, tokens)
     m, dev = hidden.shape[0], hidden.device
@@ -123,10 +126,10 @@ def linear_cross_entropy_backward(hidden: torch.Tensor, weight: torch.Tensor, to
         _ops.no_tangents("linear_cross_entropy_backward", *given)
     if torch.is_grad_enabled() and any(t.requires_grad for t in given):
         _ops.no_backward("linear_cross_entropy_backward")
-    return _backward(hidden, weight, tokens, lse, grad_loss, grad_lse, need_hidden, need_weight, check, stream)
+    return _backward(hidden, weight, tokens, lse, grad_loss, grad_lse, need_hidden, need_weight, check, stream, rounded)
 
 
-def _backward(hidden, weight, tokens, lse, grad_loss, grad_lse, need_hidden, need_weight, check, stream):
+def _backward(hidden, weight, tokens, lse, grad_loss, grad_lse, need_hidden, need_weight, check, stream, rounded):
     (m, cols), vocab, dev = hidden.shape, weight.shape[0], hidden.device
     if not need_hidden and not need_weight:
         return None, None
@@ -146,7 +149,7 @@ def _backward(hidden, weight, tokens, lse, grad_loss, grad_lse, need_hidden, nee
         a = B.wc_linear_loss_grad(h.data_ptr(), h.stride(0), weight.data_ptr(), weight.stride(0), t.data_ptr(), s.data_ptr(),
                                   gl.data_ptr() if gl is not None else 0, gz.data_ptr() if gz is not None else 0,
                                   dh.data_ptr() if need_hidden else 0, cols, dw.data_ptr() if need_weight else 0, m, vocab,
-                                  cols, _ops.TYPES[h.dtype], 0)
+                                  cols, _ops.TYPES[h.dtype], 1 if rounded else 0)
         _ops.done(lib.wc_linear_cross_entropy_backward(a, scratch.data_ptr(), nbytes, err.data_ptr() if check else 0, raw),
                   err, "linear_cross_entropy_backward")
         return dh, dw
@@ -156,7 +159,8 @@ def _backward(hidden, weight, tokens, lse, grad_loss, grad_lse, need_hidden, nee
 
 class _LinearCrossEntropy(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, hidden, weight, tokens, check):
+    def forward(ctx, hidden, weight, tokens, check, rounded):
+        ctx.rounded = rounded
         r = _forward(hidden, weight, tokens, check, None, views=False)
         ctx.save_for_backward(hidden, weight, tokens, r.lse)
         ctx.set_materialize_grads(False)
@@ -165,8 +169,9 @@ class _LinearCrossEntropy(torch.autograd.Function):
     @staticmethod
     def backward(ctx, grad_loss, grad_lse):
         if grad_loss is None and grad_lse is None:
-            return None, None, None, None
+            return (None,) * 5
         hidden, weight, tokens, lse = ctx.saved_tensors
         need = ctx.needs_input_grad
-        found = _backward(hidden, weight, tokens, lse, grad_loss, grad_lse, need[0], need[1], False, None)
-        return *_ops.once("linear_cross_entropy", found, hidden, weight, grad_loss, grad_lse), None, None
+        found = _backward(hidden, weight, tokens, lse, grad_loss, grad_lse, need[0], need[1], False, None,
+                          ctx.rounded)
+        return *_ops.once("linear_cross_entropy", found, hidden, weight, grad_loss, grad_lse), None, None, None

@@ -342,17 +342,19 @@ struct JoinArgs {
     const float *most;     // or NULL: what the numbers were scaled by (loss_scale)
 };
 
+// Four numbers a thread, or where a launch cannot hold so many threads, every gridDim.x * 256th four.
 template <int T>
 __global__ __launch_bounds__(256) void k_join(JoinArgs g)
 {
     float unscale = 1.f;
     if (g.most) loss_scale<T>(g.most, unscale);
     const uint32_t per = g.cols / 4;
-    const uint64_t q = (uint64_t)blockIdx.x * 256 + threadIdx.x, row = q / per;
-    if (row >= g.rows) return;
-    const uint32_t col = 4 * (uint32_t)(q % per);
-    const f32x4 v = sum_parts(g.part + row * g.cols + col, g.rows * g.cols, g.splits) * unscale;
-    store_four<T>(g.out + row * g.out_stride + col, v);
+    for (uint64_t q = (uint64_t)blockIdx.x * 256 + threadIdx.x; q < g.rows * per; q += (uint64_t)gridDim.x * 256) {
+        const uint64_t row = q / per;
+        const uint32_t col = 4 * (uint32_t)(q % per);
+        const f32x4 v = sum_parts(g.part + row * g.cols + col, g.rows * g.cols, g.splits) * unscale;
+        store_four<T>(g.out + row * g.out_stride + col, v);
+    }
 }
 
 // Sixteen rows of weights from n and the sixteen after them (fewer than 32:

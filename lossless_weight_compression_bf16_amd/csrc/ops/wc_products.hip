@@ -124,7 +124,7 @@ bool valid_grouped(uint64_t m, uint32_t experts, uint32_t rows, uint32_t cols)
 
 void launch_join(int type, const JoinArgs &g, hipStream_t stream)
 {
-    const uint64_t blocks = ceil_div(g.rows * (g.cols / 4), 256);
+    const uint64_t fours = ceil_div(g.rows * (g.cols / 4), 256), blocks = fours < max_blocks(256) ? fours : max_blocks(256);
     if (!blocks) return;
     if (type == WC_T_BF16) hipLaunchKernelGGL(k_join<WC_T_BF16>, dim3((uint32_t)blocks), dim3(256), 0, stream, g);
     else hipLaunchKernelGGL(k_join<WC_T_FP16>, dim3((uint32_t)blocks), dim3(256), 0, stream, g);

@@ -502,7 +502,7 @@ typedef struct {
     uint64_t w_expert;      /* elements from one expert to the next: a multiple of 8 */
     uint64_t w_row;
     const int64_t *ends;    /* experts, on the device */
-    void *y;                /* m x rows; no memory in common with x or w */
+    void *y;                /* m x rows; no memory in common with x, w or ends */
     uint64_t y_stride;
     uint64_t m;             /* below 2^31 */
     uint32_t experts;       /* 1 .. 1024 */
@@ -536,9 +536,9 @@ typedef struct {
     const int64_t *ends;
     const void *grad;       /* m x rows */
     uint64_t grad_stride;
-    void *grad_x;           /* m x cols, or NULL; no memory in common with the inputs */
+    void *grad_x;           /* m x cols, or NULL; no memory in common with the inputs that are read */
     uint64_t grad_x_stride;
-    void *grad_w;           /* experts x rows x cols, contiguous, or NULL */
+    void *grad_w;           /* experts x rows x cols, contiguous, or NULL; none with x, grad, ends or grad_x */
     uint64_t m;
     uint32_t experts;
     uint32_t rows;
@@ -571,7 +571,7 @@ typedef struct {
     uint32_t cols;          /* a multiple of 8, at most 2^20 */
     uint32_t type;          /* WC_T_BF16 or WC_T_FP16: of hidden and weight */
     uint32_t reserved;
-    float *loss;            /* m each */
+    float *loss;            /* m each; no memory in common with each other or the inputs */
     float *lse;
 } wc_linear_loss;
 
@@ -602,7 +602,7 @@ typedef struct {
     const float *grad_lse;    /* may be NULL */
     void *grad_hidden;        /* m x cols, or NULL; no memory in common with the inputs */
     uint64_t grad_hidden_stride;
-    void *grad_weight;        /* vocab x cols, contiguous, or NULL */
+    void *grad_weight;        /* vocab x cols, contiguous, or NULL; no memory in common with the others */
     uint64_t m;               /* 1 .. 2^19 */
     uint32_t vocab;
     uint32_t cols;
@@ -627,7 +627,7 @@ typedef struct {
     const void *q;          /* rows x cols / 2 bytes, 16-byte aligned */
     const void *scales;     /* rows x cols / group */
     const void *zeros;      /* the same, or NULL: 8 */
-    void *y;                /* m x rows, rows y_stride elements apart, any alignment; no memory in common with x */
+    void *y;                /* m x rows, rows y_stride elements apart, any alignment; no memory in common with the inputs */
     uint64_t y_stride;
     uint64_t m;             /* below 2^31 */
     uint32_t rows;          /* 1 .. 2^24; (rows / 512 + 16) times m / 16 below 2^22 - 256 */
@@ -643,7 +643,8 @@ wc_status wc_linear4(const wc_fourbit *a, hipStream_t stream);
  * q = w / scale to the nearest, + 8; with zeros, of lo = min(w, 0) and
  * hi = max(w, 0), scale = (hi - lo) / 15, zero = -lo / scale to the nearest, and
  * q = w / scale to the nearest, + zero; q within 0 .. 15, the scale rounded to
- * `type` before w is divided by it.  A scale of 0 (a group of zeros), NaN or infinity: q is the zero. */
+ * `type` before w is divided by it.
+ * w, q, scales and zeros have no memory in common.  A scale of 0 (a group of zeros), NaN or infinity: q is the zero. */
 wc_status wc_quantize4(const void *w, uint64_t w_stride, uint64_t rows, uint32_t cols, uint32_t group, uint32_t type, void *q,
                        void *scales, void *zeros, hipStream_t stream);
 

@@ -75,6 +75,10 @@ wc_status wc_linear4(const wc_fourbit *a, hipStream_t stream)
     if (!a->q || !aligned(a->q, 16) || !a->scales || !aligned(a->scales, 2) || !aligned(a->zeros, 2)) return WC_ERR_ARG;
     if (!a->y || !aligned(a->y, 2) || (a->m > 1 && a->y_stride < a->rows)) return WC_ERR_ARG;
     if (!rows_apart(a->x, 2 * a->x_stride, 2ull * a->cols, a->y, 2 * a->y_stride, 2ull * a->rows, a->m)) return WC_ERR_ARG;
+    const uint64_t groups = 2ull * a->rows * (a->cols / a->group);
+    if (!apart(rows_of(a->y, a->y_stride, a->rows, a->m), line(a->q, (uint64_t)a->rows * a->cols / 2), line(a->scales, groups),
+               line(a->zeros, groups)))
+        return WC_ERR_ARG;
     // blocks of 32 sixteens of rows, or fewer where that makes no more blocks than compute units; every XCD the same number
     if ((ceil_div(a->rows, 16 * kRowTiles4) + 16) * ceil_div(a->m, 16) + kCus > max_blocks(1024)) return WC_ERR_ARG;
     Linear4Args g{};
@@ -102,6 +106,9 @@ wc_status wc_quantize4(const void *w, uint64_t w_stride, uint64_t rows, uint32_t
     if (!w || !aligned(w, 2) || (rows > 1 && w_stride < cols) || !q || !aligned(q, 16) || !scales || !aligned(scales, 2) ||
         !aligned(zeros, 2) || ceil_div(rows * (cols / 8), 256) > max_blocks(256))
         return WC_ERR_ARG;
+    const Rows from = rows_of(w, w_stride, cols, rows), to = line(q, rows * cols / 2), s = line(scales, 2 * rows * (cols / group)),
+               z = line(zeros, 2 * rows * (cols / group));
+    if (!apart(from, to, s, z) || !apart(to, s, z) || !apart(s, z)) return WC_ERR_ARG;
     const Quantize4Args g{static_cast<const uint16_t *>(w), w_stride, static_cast<uint8_t *>(q), static_cast<uint16_t *>(scales),
                           static_cast<uint16_t *>(zeros), rows, cols};
     if (type == WC_T_BF16) launch_quantize4<WC_T_BF16>(g, group, stream);

@@ -358,6 +358,9 @@ wc_status wc_grouped_linear(const wc_grouped *a, void *d_scratch, uint64_t scrat
     const uint64_t need = wc_grouped_linear_scratch(a->m, a->experts, a->rows, a->cols);
     if (scratch_bytes < need) return WC_ERR_CAPACITY;
     if (need && (!d_scratch || !aligned(d_scratch, 16))) return WC_ERR_ARG;
+    if (!apart(rows_of(a->y, a->y_stride, a->rows, a->m), experts_of(a->w, a->w_expert, a->w_row, a->cols, a->rows, a->experts),
+               line(a->ends, 8 * a->experts)))
+        return WC_ERR_ARG;
     GroupedArgs g{};
     g.x = static_cast<const uint16_t *>(a->x);
     g.w = static_cast<const uint16_t *>(a->w);
@@ -401,6 +404,15 @@ wc_status wc_grouped_linear_backward(const wc_grouped_grad *a, void *d_scratch, 
     const uint64_t need = wc_grouped_linear_backward_scratch(a->m, a->experts, a->rows, a->cols);
     if (scratch_bytes < need) return WC_ERR_CAPACITY;
     if (need && (!d_scratch || !aligned(d_scratch, 16))) return WC_ERR_ARG;
+    // the gradient of x is written while w and the other results' inputs are still to be read, that of w after w
+    const Rows ends = line(a->ends, 8 * a->experts), dw = line(a->grad_w, 2ull * a->experts * a->rows * a->cols);
+    if (a->m && a->grad_x &&
+        !apart(rows_of(a->grad_x, a->grad_x_stride, a->cols, a->m), ends, dw,
+               experts_of(a->w, a->w_expert, a->w_row, a->cols, a->rows, a->experts),
+               rows_of(a->grad_w ? a->x : nullptr, a->x_stride, a->cols, a->m)))
+        return WC_ERR_ARG;
+    if (!apart(dw, ends, rows_of(a->grad, a->grad_stride, a->rows, a->m), rows_of(a->x, a->x_stride, a->cols, a->m)))
+        return WC_ERR_ARG;
     if (!(a->grad_x && a->m) && !a->grad_w) return WC_OK;
     if (a->grad_x && a->m) {
         GroupedArgs g{};
@@ -469,6 +481,9 @@ wc_status wc_linear_cross_entropy(const wc_linear_loss *a, void *d_scratch, uint
     const uint64_t need = wc_linear_cross_entropy_scratch(a->m, a->vocab, a->cols);
     if (scratch_bytes < need) return WC_ERR_CAPACITY;
     if (!d_scratch || !aligned(d_scratch, 256)) return WC_ERR_ARG;
+    const Rows hidden = rows_of(a->hidden, a->hidden_stride, a->cols, a->m), tokens = line(a->tokens, 8 * a->m);
+    const Rows weight = rows_of(a->weight, a->weight_stride, a->cols, a->vocab), lse = line(a->lse, 4 * a->m);
+    if (!apart(line(a->loss, 4 * a->m), lse, hidden, weight, tokens) || !apart(lse, hidden, weight, tokens)) return WC_ERR_ARG;
     const uint64_t most = a->m < kLossSlice ? a->m : kLossSlice;
     for (uint64_t r = 0; r < a->m; r += most) {
         LossArgs g{};
@@ -514,6 +529,13 @@ wc_status wc_linear_cross_entropy_backward(const wc_linear_loss_grad *a, void *d
     const LossGradPlan p = loss_grad_plan(a->m, a->vocab, a->cols, terms);
     if (scratch_bytes < wc_linear_cross_entropy_backward_scratch(a->m, a->vocab, a->cols)) return WC_ERR_CAPACITY;
     if (!d_scratch || !aligned(d_scratch, 256)) return WC_ERR_ARG;
+    const Rows hidden = rows_of(a->hidden, a->hidden_stride, a->cols, a->m), tokens = line(a->tokens, 8 * a->m);
+    const Rows weight = rows_of(a->weight, a->weight_stride, a->cols, a->vocab), lse = line(a->lse, 4 * a->m);
+    const Rows gl = line(a->grad_loss, 4 * a->m), gz = line(a->grad_lse, 4 * a->m);
+    const Rows dw = line(a->grad_weight, 2ull * a->vocab * a->cols);
+    if (!apart(rows_of(a->grad_hidden, a->grad_hidden_stride, a->cols, a->m), dw, hidden, weight, tokens, lse, gl, gz) ||
+        !apart(dw, hidden, weight, tokens, lse, gl, gz))
+        return WC_ERR_ARG;
     if (!a->grad_hidden && !a->grad_weight) return WC_OK;
     char *s = static_cast<char *>(d_scratch);
     LossGradArgs g{};

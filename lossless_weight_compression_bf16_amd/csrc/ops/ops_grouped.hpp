@@ -379,33 +379,34 @@ __device__ __forceinline__ void few_rows(const uint16_t *w, uint32_t pitch, uint
         for (int m = 0; m < 2; m++) sum[m][t] = acc[m][0][t];
 }
 
-// 32 rows of weights (n of them in all) from n0 on against `count` <= 32 rows of
+// 32 rows of weights (n of them in all) from n0 on against `count` <= 16 kTiles rows of
 // x, columns of all k.  kSplit: the block's four waves share the columns, and
 // f(t, sums) is called by the wave t with the sums of 16 rows of x; otherwise the rows
 // are the wave's own, and it calls f for every t.  sums[m]: the lane's four
 // of weights' rows first[m] + 4 gr on, against row 16 t + i of x.
-template <int T, bool kSplit, class F>
+template <int T, bool kSplit, int kTiles, class F>
 __device__ __forceinline__ void few_product(const uint16_t *w, uint32_t pitch, uint32_t n, uint32_t n0, uint32_t k,
                                             const uint16_t *x, uint64_t x_stride, uint32_t count, Strip (*strips)[2], F f)
 {
+    static_assert(kTiles == 1 || kTiles == 2, "one sixteen of rows of x or two");
     const uint32_t wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
     const uint32_t most = n < 16 ? 0 : n - 16, first[2] = {min(n0, most), min(n0 + 16, most)};
     uint32_t c0 = 0, c1 = k;
     if (kSplit) wave_quarter(k, kStripCols, wave, c0, c1);
     f32x4 sum[2][2];
-    const uint32_t tiles = (count + 15) / 16;
-    if (tiles <= 1) few_rows<T, 1>(w, pitch, n, first, x, x_stride, count, c0, c1, strips[wave], sum);
-    else few_rows<T, 2>(w, pitch, n, first, x, x_stride, count, c0, c1, strips[wave], sum);
+    const uint32_t tiles = kTiles == 1 ? 1 : (count + 15) / 16;
+    if (tiles == 1) few_rows<T, 1>(w, pitch, n, first, x, x_stride, count, c0, c1, strips[wave], sum);
+    else few_rows<T, kTiles>(w, pitch, n, first, x, x_stride, count, c0, c1, strips[wave], sum);
     if constexpr (!kSplit) {
 #pragma unroll
-        for (uint32_t t = 0; t < 2; t++)
+        for (uint32_t t = 0; t < kTiles; t++)
             if (t < tiles) f(t, first, sum[0][t], sum[1][t]);
     } else {
         f32x4(*part)[4][64] = reinterpret_cast<f32x4(*)[4][64]>(&strips[0][0]);  // [4], when the strips are done
         static_assert(sizeof(Strip) * 8 >= 4 * 4 * 64 * 16, "the waves' sums fit into the strips");
         __syncthreads();
 #pragma unroll
-        for (uint32_t t = 0; t < 2; t++)
+        for (uint32_t t = 0; t < kTiles; t++)
             if (t < tiles) {
                 part[wave][2 * t][lane] = sum[0][t];
                 part[wave][2 * t + 1][lane] = sum[1][t];
@@ -486,7 +487,7 @@ __global__ __launch_bounds__(256, 2) void k_grouped_few(GroupedArgs g)
                 if (n < g.n) one_product<T>(w, g.w_row, g.n, n, g.k, x, [&](uint32_t r, float v) { y[r] = Type<T>::from_f32(v); });
             }
         } else if (kSplit || n0 < g.n) {
-            few_product<T, kSplit>(w, g.w_row, g.n, n0, g.k, x, g.x_stride, count, strips,
+            few_product<T, kSplit, 2>(w, g.w_row, g.n, n0, g.k, x, g.x_stride, count, strips,
                                    [&](uint32_t t, const uint32_t(&first)[2], f32x4 v0, f32x4 v1) {
                                        const uint32_t r = 16 * t + i;
                                        if (r >= count) return;

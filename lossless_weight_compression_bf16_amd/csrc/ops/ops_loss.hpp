@@ -138,12 +138,14 @@ __global__ __launch_bounds__(256, tile_blocks(BM, BN)) void k_loss(LossArgs g)
         });
 }
 
-// The same for up to 32 rows: 32 columns of z for a block (128 without kSplit).
+constexpr uint32_t kLossFew = 16;  // rows, at most, of k_loss_few and k_loss_grad_few
+
+// The same for up to kLossFew rows: 32 columns of z for a block (128 without kSplit).
 template <int T, bool kSplit>
 __global__ __launch_bounds__(256, 2) void k_loss_few(LossArgs g)
 {
     __shared__ Strip strips[4][2];
-    __shared__ float2 stats[4][32];
+    __shared__ float2 stats[4][kLossFew];
     const uint32_t wave = threadIdx.x >> 6, lane = threadIdx.x & 63, i = lane & 15, gr = lane >> 4;
     const uint32_t n0 = kSplit ? 32 * blockIdx.x : 128 * blockIdx.x + 32 * wave;
     constexpr uint32_t kShares = kSplit ? 1 : 4;  // waves with statistics of the same row
@@ -163,7 +165,7 @@ __global__ __launch_bounds__(256, 2) void k_loss_few(LossArgs g)
         }
         if (lane == 0) stats[wave][0] = float2{s.most, s.sum};
     } else if (kSplit || n0 < g.vocab) {
-        few_product<T, kSplit>(g.w, g.w_row, g.vocab, n0, g.k, g.h, g.h_stride, g.m, strips,
+        few_product<T, kSplit, 1>(g.w, g.w_row, g.vocab, n0, g.k, g.h, g.h_stride, g.m, strips,
                                [&](uint32_t t, const uint32_t(&first)[2], f32x4 v0, f32x4 v1) {
                                    const uint32_t row = 16 * t + i;
                                    const int64_t token = row < g.m ? g.tokens[row] : -1;
@@ -191,7 +193,7 @@ __global__ __launch_bounds__(256, 2) void k_loss_few(LossArgs g)
                                    s.join(__shfl_xor(s.most, 32, 64), __shfl_xor(s.sum, 32, 64));
                                    if (gr == 0) stats[kSplit ? 0 : wave][row] = float2{s.most, s.sum};
                                });
-    } else if (lane < 32) {
+    } else if (lane < kLossFew) {
         stats[wave][lane] = float2{-kInf, 0.f};
     }
     __syncthreads();
@@ -340,7 +342,7 @@ __global__ __launch_bounds__(256, tile_blocks(BM, BN)) void k_loss_grad(LossGrad
         });
 }
 
-// The same for up to 32 rows.
+// The same for up to kLossFew rows.
 template <int T, bool kSplit>
 __global__ __launch_bounds__(256, 2) void k_loss_grad_few(LossGradArgs g)
 {
@@ -350,7 +352,7 @@ __global__ __launch_bounds__(256, 2) void k_loss_grad_few(LossGradArgs g)
     if (!kSplit && n0 >= g.width) return;
     float unscale;
     const float scale = loss_scale<T>(g.most, unscale);
-    few_product<T, kSplit>(g.w + (uint64_t)g.v0 * g.w_row, g.w_row, g.width, n0, g.k, g.h, g.h_stride, g.m, strips,
+    few_product<T, kSplit, 1>(g.w + (uint64_t)g.v0 * g.w_row, g.w_row, g.width, n0, g.k, g.h, g.h_stride, g.m, strips,
                            [&](uint32_t t, const uint32_t(&first)[2], f32x4 v0, f32x4 v1) {
                                const uint32_t row = 16 * t + i;
                                if (row >= g.m) return;

@@ -206,7 +206,7 @@ bool valid_loss(uint64_t m, uint32_t vocab, uint32_t cols)
 
 // us by k_loss_few and by tiles: 12 and 16 rows of a vocabulary of 50257 x 768 20 and 25 (32 rows 26 and 25), of 128256 x
 // 4096 156 to 160 and 160 (32 rows 212 and 160)
-bool loss_few(uint64_t m) { return m <= 16; }
+bool loss_few(uint64_t m) { return m <= kLossFew; }
 TileSize loss_tile(uint64_t m, uint32_t vocab, uint32_t k)
 {
     if (flat(m, (uint64_t)vocab * k)) return kFlat;

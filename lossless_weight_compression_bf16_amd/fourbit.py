@@ -113,7 +113,8 @@ def quantize4(w: torch.Tensor, group: int = 64, zeros: bool = False, stream=None
     columns of a row, steps of a seventh of the largest size around 0, or
     with `zeros` of a fifteenth of the range, to which 0 belongs.  Each
     weight goes to the nearest step.  A group with a NaN or an infinity gets
-    a scale that says so."""
+    a scale that says so.  There is no backward pass: weights that require a
+    gradient raise unless gradients are switched off."""
     _ops.check_tensor(w, "w")
     if w.dtype not in _ops.HALVES or w.dim() != 2:
         raise TypeError("w must be a 2-D tensor of a 16-bit float type")
@@ -121,6 +122,10 @@ def quantize4(w: torch.Tensor, group: int = 64, zeros: bool = False, stream=None
     if group not in GROUPS or not cols or cols % group or cols > 1 << 20 or not 1 <= rows <= 1 << 24:
         raise ValueError(f"groups of 32, 64 or 128 columns, whole ones, at most 2^20 columns and 2^24 rows: got {rows} x {cols} in "
                          f"groups of {group}")
+    if torch.is_grad_enabled() and w.requires_grad:
+        _ops.no_backward("quantize4")
+    if _ops.forward_mode():
+        _ops.no_tangents("quantize4", w)
     dev = w.device
 
     def call(raw):

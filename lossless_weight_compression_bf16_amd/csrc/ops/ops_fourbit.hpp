@@ -312,7 +312,8 @@ __global__ __launch_bounds__(256) void k_quantize4(Quantize4Args g)
         hi = fmaxf(hi, __shfl_xor(hi, o, 64));
         bad |= __shfl_xor((int)bad, o, 64) != 0;
     }
-    const float step = bad ? nan32() : g.zeros ? (hi - lo) / 15.f : fmaxf(hi, -lo) / 7.f;
+    const float range = hi - lo;  // of finite numbers it may be past the largest, its fifteenth is not
+    const float step = bad ? nan32() : !g.zeros ? fmaxf(hi, -lo) / 7.f : range < kInf ? range / 15.f : hi / 15.f - lo / 15.f;
     const uint16_t scale = Ty::from_f32(step);
     const float s = Ty::to_f32(scale);
     float zero = 8.f;

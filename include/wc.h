@@ -619,8 +619,10 @@ wc_status wc_linear_cross_entropy_backward(const wc_linear_loss_grad *a, void *d
  *   w_rk = scales_rg (q_rk - zeros_rg),   y = x w^T,
  * q in 0 .. 15, two in a byte (the even column in the low half).  Products of
  * x with whole numbers are exact, their sums over a group, and those of
- * the scaled groups, are fp32, and y is rounded once; an infinity in x makes its row of y NaN.  32 rows of x meet the weights
- * at a time (16 where there are no more): meant for few. */
+ * the scaled groups, are fp32, and y is rounded once.  The sums of a group are those of (16 + q) x and of
+ * (16 + zero) x, whose difference is what is scaled: an infinity in x makes its row of y NaN, and so may finite x where a group's
+ * sum of 31 |x| (or of (16 + |zero|) |x|) passes fp32's range, in BF16 from 2^128 / (32 group) on, 8.3e34 for
+ * groups of 128.  32 rows of x meet the weights at a time (16 where there are no more): meant for few. */
 typedef struct {
     const void *x;          /* m x cols, rows x_stride elements apart, 16-byte aligned rows */
     uint64_t x_stride;      /* a multiple of 8 */

@@ -72,7 +72,9 @@ def _good(x, w) -> bool:
 def linear4(x: torch.Tensor, w: Weights4, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """x w^T, m x rows in the type of x (BF16 or FP16): products of x with
     whole numbers, summed in fp32 over a group, then scaled and summed in fp32
-    and rounded once.  An infinity in a row of x makes its row of y NaN.
+    and rounded once.  An infinity in a row of x makes its row of y NaN, and
+    so may BF16 numbers past 2^128 / (32 group), 8.3e34 for groups of 128,
+    whose sums of (16 + q) x over a group pass fp32's range.
 
     Meant for few rows, where reading the weights is the time; 32 rows of x
     meet them at a time (16 of up to 16).  There is no backward pass: tensors

@@ -74,8 +74,12 @@ uint64_t tiles_expected(uint64_t m, uint32_t experts, uint64_t tile)  // with th
 // 64 to 70), of 8 of 2048 x 4096 32 to 41 and 28 to 35; 65 to 128 rows of each of 8 of 14336 x 4096 340 to 250 and 180 to 203.
 bool flat(uint64_t rows, uint64_t weights) { return rows <= 64 && weights > 1ull << 26; }
 
-// The tiles of y of m rows with n columns each, from k, or of dx (across), whose tiles of 64 rows have 128 columns and are more: both
-// gradients of 602 rows, dealt at random to 16 experts of 2304 x 768, 43 us, and 48.5 by tiles of 128.
+// The tiles of y of m rows with n columns each, from k, or of dx (across), whose tiles of 64 rows have 128 columns and are more
+// where k is over 1024.  us by them and by tiles of 128, 64 rows of each expert, dx of 2048 columns from k = 768, 1032, 1536 and 4096:
+// one expert 12.4, 13.5, 13.4 and 15.9, and 11.0, 13.0, 13.7 and 19.9; 4 experts 12.9, 15.3, 16.7 and 28.6, and 12.8, 17.9, 18.9 and
+// 28.2; 16 experts 14.9, 27.5, 30.5 and 63, and 16.7, 28.8, 33.5 and 63.  Over 1 to 16 experts, 9 to 64 rows and 768 or 2048
+// columns they take 4% less on average from k over 1024 (6% more to 20% less), up to there
+// 1% less (15% more to 23% less).
 TileSize grouped_size(uint64_t m, uint32_t experts, uint32_t n, uint32_t k, bool across)
 {
     const uint64_t hit = m < experts ? m : experts, rows = ceil_div(m, hit);
@@ -94,14 +98,17 @@ uint64_t grouped_part(TileSize size, uint64_t m, uint32_t experts, uint32_t n, u
     return few && k >= 16 * kTileK ? 4 * bm * bn * slots : 0;
 }
 
-// Few rows of each expert, whose weights are few or short: no tile, but more and smaller blocks.  us by
-// k_grouped_few and by tiles of 64: one row of 1024 x 2048 11 and 15, of each of 8 and 16 such experts 11.8 and 15.7, 23 and 17.6;
-// one row of 14336 x 4096 41 and 25, of each of 2 and 8 of 2048 x 7168 18 and 20.5, 55 and 45; of 64 of 768 x 768 16 and 20,
-// 8 rows of each 17 and 19.
+// Few rows of each expert, whose weights are few: no tile, but more and smaller blocks.  us by
+// k_grouped_few and by tiles.  k over 1024: one row of 1024 x 2048 11 and 15, of each of 8 and 16 such experts 11.8 and 15.7,
+// 23 and 17.6; one row of 14336 x 4096 41 and 25, of each of 2 and 8 of 2048 x 7168 18 and 20.5, 55 and 45.  k up to 1024, 8 rows
+// (one row) of each of 32 experts of 2048 x 512 14.7 and 15.9 (14.3 and 15.8), of 2048 x 1024 24 and 29.5 (26 and 29), of 4096 x 1024
+// 53 and 45 (56 and 45); of 64 of 4096 x 256 28 and 37 (35 and 36), of 8192 x 256 55 and 50 (68 and 47); of 256 of 768 x 256 25 and 30
+// (30 and 29), of 2048 x 256 63 and 54 (77 and 52), of 2048 x 768 149 and 135 (139 and 129).  From 2^26 weights on the
+// tiles are of 64 rows past the caches; up to there few rows gain by 14 to 21% on average, one by 2%.
 bool grouped_few(uint64_t m, uint32_t experts, uint32_t n, uint32_t k)
 {
     const uint64_t hit = m < experts ? m : experts;
-    return m <= 8 * hit && (k <= 1024 || hit * n * k < 1ull << 25);
+    return m <= 8 * hit && hit * n * k <= (k <= 1024 ? 1ull << 26 : (1ull << 25) - 1);
 }
 
 TilePlan grouped_dw_plan(uint64_t m, uint32_t experts, uint32_t n, uint32_t k)

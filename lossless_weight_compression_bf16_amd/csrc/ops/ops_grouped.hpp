@@ -61,6 +61,12 @@ __device__ __forceinline__ void check_ends(const int64_t *ends, uint32_t experts
         if (ends[e] > (int64_t)m || ends[e] < (e ? ends[e - 1] : 0)) report(err, WC_EF_BAD_INDEX);
 }
 
+// That look alone, where there are no rows.
+__global__ __launch_bounds__(256) void k_grouped_ends(const int64_t *ends, uint32_t experts, uint32_t *err)
+{
+    check_ends(ends, experts, 0, err);
+}
+
 __device__ __forceinline__ uint32_t wave_upto(uint32_t v)  // the sum of lanes 0 .. this one
 {
     v += lanes_moved<0x111, 0xF>(v, 0u);

@@ -183,6 +183,15 @@ wc_status launch_grouped_linear(GroupedArgs g, hipStream_t stream)
     return launched();
 }
 
+// No rows: all there is to do is to look at the ends, if they are to be looked at.
+wc_status launch_ends(const int64_t *ends, uint32_t experts, uint32_t *err, hipStream_t stream)
+{
+    if (!err) return WC_OK;
+    if (!ends || !aligned(ends, 8)) return WC_ERR_ARG;
+    hipLaunchKernelGGL(k_grouped_ends, dim3(1), dim3(256), 0, stream, ends, experts, err);
+    return launched();
+}
+
 template <int T>
 void launch_grouped_dw(GroupedDwArgs g, const TilePlan &p, hipStream_t stream)
 {
@@ -357,7 +366,7 @@ wc_status wc_grouped_linear(const wc_grouped *a, void *d_scratch, uint64_t scrat
     if (!a || (a->type != WC_T_BF16 && a->type != WC_T_FP16) || !valid_grouped(a->m, a->experts, a->rows, a->cols))
         return WC_ERR_ARG;
     if (d_err && !aligned(d_err, 4)) return WC_ERR_ARG;
-    if (a->m == 0) return WC_OK;
+    if (a->m == 0) return launch_ends(a->ends, a->experts, d_err, stream);
     if (!rows16(a->x, a->x_stride, a->cols) || !rows16(a->w, a->w_row, a->cols) || a->w_expert % 8 ||
         !rows16(a->y, a->y_stride, a->rows) || !a->ends || !aligned(a->ends, 8))
         return WC_ERR_ARG;
@@ -420,7 +429,8 @@ wc_status wc_grouped_linear_backward(const wc_grouped_grad *a, void *d_scratch, 
         return WC_ERR_ARG;
     if (!apart(dw, ends, rows_of(a->grad, a->grad_stride, a->rows, a->m), rows_of(a->x, a->x_stride, a->cols, a->m)))
         return WC_ERR_ARG;
-    if (!(a->grad_x && a->m) && !a->grad_w) return WC_OK;
+    if (!a->m && !a->grad_w) return launch_ends(a->ends, a->experts, d_err, stream);
+    if (!a->grad_x && !a->grad_w) return WC_OK;
     if (a->grad_x && a->m) {
         GroupedArgs g{};
         g.x = static_cast<const uint16_t *>(a->grad);

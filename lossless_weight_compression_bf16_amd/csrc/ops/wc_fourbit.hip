@@ -24,8 +24,9 @@ void launch_linear4(Linear4Args g, hipStream_t stream)
 {
     const uint64_t tiles = ceil_div(g.rows, 16), turns = ceil_div(g.m, 16 * NT), slices = ceil_div(g.cols, SLICE);
     const uint32_t waves = (uint32_t)(slices < WAVES ? slices : WAVES);
-    // a block for each compute unit: its LDS has room for one
-    const uint64_t blocks = turns < kCus ? kCus / turns : 1;
+    // a block for each compute unit, whose LDS has room for one, and as many for each XCD, which has 32 units (14336 x 4096, groups
+    // of 64: 65 rows, 85 blocks a turn are 33 on two XCDs, 75 us, 80 are 30 at most, 44; 129 rows 119 and 64, 224 rows 161 and 91)
+    const uint64_t each = turns < kCus ? kCus / turns : 1, blocks = each < 8 ? each : each / 8 * 8;
     g.row_tiles = (uint32_t)ceil_div(tiles, blocks);
     if (g.row_tiles > kRowTiles4) g.row_tiles = kRowTiles4;
     g.row_blocks = (uint32_t)ceil_div(tiles, g.row_tiles);

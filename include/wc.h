@@ -173,7 +173,8 @@ typedef struct {
 } wc_gemm;
 
 /* Library version (major * 10000 + minor * 100 + patch). */
-int wc_version(void);
+#define WC_VERSION 10500 /* 1.5.0: the loss's gradients whole, or rounded */
+int wc_version(void);  /* WC_VERSION of the library */
 
 /* Human-readable name of a status code. */
 const char *wc_status_string(wc_status s);

@@ -29,8 +29,6 @@ using namespace wc;
 
 namespace {
 
-constexpr int kVersion = 10400;  // 1.4.0: grouped products, loss from hidden states, 4-bit weights (csrc/ops)
-
 bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
 uint64_t chunk_capacity(uint64_t len) { return 128 + 2 * (len + (len & 1)); }
@@ -370,7 +368,7 @@ void launch_gemm_any(uint32_t mt, uint32_t pp, const SegTable &st, uint64_t chun
 
 extern "C" {
 
-int wc_version(void) { return kVersion; }
+int wc_version(void) { return WC_VERSION; }
 
 const char *wc_status_string(wc_status s)
 {

@@ -15,11 +15,14 @@
 // once by a product with ones, and being where the group's sum begins.  So a weight takes 1 to 1.5 vector
 // instructions, and s and z meet it in fp32.  With an infinity in x the result is
 // NaN, also where every weight is finite, and so it may be where a group's sum of 31 |x| passes fp32's range.
-// Measured: 1 row and 4096 x 4096, groups of 64: 7.5 us in the kernel, of which the weights' 8.9 MB take
+// Measured: 1 row and 4096 x 4096, groups of 64: 7.4 us in the kernel, of which the weights' 8.9 MB take
 // 1.4 at the rate of a copy and the rest is one launch and one way through memory, LDS and a
-// barrier; 1 row and 128256 x 4096, 67 us, 4.2 TB/s; 61 rows and
-// 14336 x 4096, groups of 128, 27 us, where the vector instructions take 11 and
-// LDS 6 of them: the 61 rows are two times 32, and the weights are unpacked for each.
+// barrier; 1 row and 128256 x 4096, 63 us, 4.5 TB/s: a barrier of 16 waves and a joining of their sums for every sixteen of rows, while
+// the next two are on their way; 61 rows and 14336 x 4096, groups of 128, 29 us, of which vector instructions take 11 and
+// LDS 6: the rest is the same barrier, twice for each sixteen (4096 columns are two passes of eight waves) and all of it twice, as
+// 61 rows are two times 32.  More rows are more such turns: 2048 rows 712 us, where the products alone need 172.
+// k_quantize4: 4096 x 4096 15 us, 128256 x 4096 422 to 453 us, 3.0 TB/s of reading and writing where a copy reaches
+// 6.5: a thread has one load of 16 bytes on its way, then eight divisions.  Weights are made once.
 #pragma once
 
 #include "ops_common.hpp"

@@ -10,9 +10,10 @@
 // itself (every wave adds up the experts' tiles by lane moves).
 //
 // What bounds them, and what they take: few rows, reading the weights once (122 rows of 8 experts of 14336 x 4096, by
-// tiles of 64: 147 us, 6.4 TB/s; one row of each of 8 of 1024 x 2048, by k_grouped_few: 11 us, one way through
-// memory); many, the matrix cores at the clock that their power leaves (16384 rows of 8 of 14336 x 4096: dx 1520 us, dW
-// 1550 us, 1.25 PFLOP/s); in between, tiles that are not full (32768 rows of 256 of 2048 x 7168: 1870 us, 4.3 TB/s).
+// tiles of 64: 147 us, 6.4 TB/s); one row of each, waits that follow each other (8 of 1024 x 2048, by k_grouped_few: 11.8 us, of
+// which 4.7 at the rate of reading: two trips to memory for the ends, then four for 512 columns of a wave's eight rows, at most two of them
+// on their way at once, by one wave on a SIMD); many, the matrix cores at the clock that their power leaves (16384 rows of 8 of 14336 x 4096:
+// dx 1520 us, dW 1550 us, 1.25 PFLOP/s); in between, tiles that are not full (32768 rows of 256 of 2048 x 7168: 1890 us, 4.3 TB/s).
 #pragma once
 
 #include "ops_common.hpp"

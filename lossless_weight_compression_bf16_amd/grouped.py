@@ -106,7 +106,9 @@ def grouped_linear(x: torch.Tensor, w: torch.Tensor, ends: torch.Tensor, out: to
     device, which never have to come to the host.  rows and cols are
     multiples of 8.  Rows behind the last expert's are not read: their y is
     zero, or in a given `out` what it was.  x and w can be differentiated,
-    once; captured into a graph only while autograd holds no other graph of them.  With check (which waits for the GPU) ends that go back, or past
+    once; captured into a graph only while autograd holds no other graph of
+    them, which is looked at where they are leaves, not for leaves that they are
+    made from.  With check (which waits for the GPU) ends that go back, or past
     the rows, raise; without, y is undefined."""
     if out is not None or not _good(x, w, ends):
         _check(x, w, ends, out)

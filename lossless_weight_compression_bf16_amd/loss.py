@@ -83,7 +83,8 @@ def linear_cross_entropy(hidden: torch.Tensor, weight: torch.Tensor, tokens: tor
     stands for no token (loss 0, whatever the row holds).  hidden and weight
     can be differentiated, once, through loss and lse (a penalty on the
     size of the logits is a function of lse); captured into a graph only
-    while autograd holds no other graph of them.  `rounded` is the gradients':
+    while autograd holds no other graph of them, which is looked at where they
+    are leaves, not for leaves that they are made from.  `rounded` is the gradients':
     see linear_cross_entropy_backward.  With check (which waits for
     the GPU) a token out of range raises; without, its loss is NaN."""
     if not _good(hidden, weight, tokens):

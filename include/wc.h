@@ -589,7 +589,7 @@ wc_status wc_linear_cross_entropy(const wc_linear_loss *a, void *d_scratch, uint
  * two numbers of `type` (16 bits of it in BF16, 22 in FP16), or with `rounded` as
  * one, in half the time of both products; their sums are fp32, and each
  * result is rounded once.  G is
- * made for a piece of the vocabulary at a time, at most 2^27 numbers.  A row
+ * made for a piece of the vocabulary at a time, at most 2^27 numbers, or 256 columns.  A row
  * without a part (both gradients 0, or lse -inf) has none, whatever its
  * hidden values are.  Either result may be NULL. */
 typedef struct {

@@ -209,7 +209,7 @@ void launch_grouped_dw(GroupedDwArgs g, const TilePlan &p, hipStream_t stream)
 
 constexpr uint64_t kLossMaxRows = 1ull << 19;
 constexpr uint32_t kLossSlice = 1u << 15;  // rows of one set of launches of the forward pass
-// G of a piece of the vocabulary, all terms of it: at most 2^27 numbers, 256 MiB, what the last cache holds.  ms with pieces of 2^25,
+// G of a piece of the vocabulary, all terms of it: at most 2^27 numbers, 256 MiB, what the last cache holds, or 256 columns.  ms with pieces of 2^25,
 // 2^26, 2^27, 2^28 and 2^30: 4096 rows, 128256 x 4096, 16.4, 16.2, 16.3, 16.5 and 16.6 (rounded 10.3, 9.7, 9.8, 9.9 and 9.9); 16384
 // rows, 32000 x 2048, 12.4, 10.1, 9.3, 9.0 and 8.9; 65536 rows, 16384 x 1024, whose pieces are of 256 to 8192 columns
 // and whose sums of dH are read and written for each, 24.4, 16.1, 12.6, 11.1 and 10.3: what more scratch would give, and many rows pay.
